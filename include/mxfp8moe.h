@@ -387,6 +387,50 @@ int nvfp4_grouped_mlp_fwd(const void* x_sorted, int64_t R, int64_t H, int64_t F,
                           const uint8_t* w2_q, const uint8_t* w2_sf, const float* w2_amax, float h_amax, void* y,
                           void* workspace, size_t workspace_bytes, void* stream, void* const* stage_events);
 
+/*
+ * Decode: the same layer and plain linears for a few tokens (T <= 64).  Only the weights are low
+ * precision: x (bf16) and the intermediate h (fp32) are not quantized, sums are fp32, and the result
+ * is rounded once, to bf16.  (The activations enter the tensor cores as short sums of E4M3 or E2M1
+ * numbers: bf16 to within 2^-17 of a 32-value block's largest magnitude beside MXFP8 weights and h to
+ * within 2^-12 of its own; both to within 2^-14 of a 16-value block's largest magnitude beside NVFP4
+ * weights.)  Results do not depend on timing.  A token with a non-finite x gives non-finite values in
+ * its own row only; weights must be finite.
+ *
+ * moe_decode_fwd -- a whole MoE layer, from the router's choices to the combined output:
+ *     out[t] = sum_j gate[t,j] W2[e] ( silu(W1[e, 0:F] x_t) * (W1[e, F:2F] x_t) ),  e = experts[t,j]
+ *   x        (device) bf16 [T, H].     experts (device) int32 [T, k].  A negative id is a choice that
+ *            was dropped: it contributes nothing whatever its gate holds; a token without any choice
+ *            gives a row of zeros.  An id >= E is skipped too and reported (MXFP8_ERR_INVALID_ARG).
+ *            A token may list an expert more than once (the weights add).
+ *   gates    (device) float [T, k] or NULL for 1.
+ *   w1_q, w1_sf, w2_q, w2_sf           as for grouped_mlp_fwd (the same buffers).
+ *   out      (device) bf16 [T, H], fully overwritten; must not overlap x.
+ *   workspace (device) moe_decode_workspace_size(T, k, H, F, E) bytes, 256-byte aligned; its first
+ *            4 bytes are the error word (mxfp8_check_device_error).  Nothing in it needs to be
+ *            initialised or kept.  Not shared by two calls in flight.
+ *   Requirements: 0 <= T <= 64, 1 <= k <= 32, 1 <= E <= 1024, H % 128 == 0, F % 128 == 0 (otherwise
+ *   MXFP8_ERR_UNSUPPORTED: larger batches go through moe_permute and grouped_mlp_fwd_tokens).  x, out
+ *   and weights 16-byte aligned, experts and gates 4-byte aligned.  Two kernels.
+ * nvfp4_moe_decode_fwd -- the same from the weights of nvfp4_grouped_mlp_fwd; no h_amax is needed.
+ * mxfp8_matvec, nvfp4_matvec -- y[t] = W x_t for T <= 64 rows of x (device) bf16 [T, K] and W [N, K] as
+ *   mxfp8_quantize (row-wise) or nvfp4_quantize write it with MXFP8_SF_MMA; y (device) bf16 [T, N],
+ *   fully overwritten, must not overlap x.  K % 128 == 0, N % 128 == 0.  workspace (device) holds the
+ *   error word: matvec_workspace_size() bytes, 16-byte aligned.  One kernel.
+ */
+size_t moe_decode_workspace_size(int64_t T, int k, int64_t H, int64_t F, int E);
+int moe_decode_fwd(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, const int32_t* experts,
+                   const float* gates, const uint8_t* w1_q, const uint8_t* w1_sf, const uint8_t* w2_q,
+                   const uint8_t* w2_sf, void* out, void* workspace, size_t workspace_bytes, void* stream);
+int nvfp4_moe_decode_fwd(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, const int32_t* experts,
+                         const float* gates, const uint8_t* w1_q, const uint8_t* w1_sf, const float* w1_amax,
+                         const uint8_t* w2_q, const uint8_t* w2_sf, const float* w2_amax, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+size_t matvec_workspace_size(void);
+int mxfp8_matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf, void* y,
+                 void* workspace, size_t workspace_bytes, void* stream);
+int nvfp4_matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf,
+                 const float* w_amax, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
 /* mxfp8_mma_peak -- measurement aid, with no counterpart on the pages: the rate of the
  * block-scaled tensor-core instruction this library's GEMMs are built on, on the device at hand
  * (the roofline their TFLOP/s are reported against).  Launches one cluster of two CTAs per pair

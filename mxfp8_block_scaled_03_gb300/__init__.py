@@ -15,6 +15,9 @@ approaches, items 1-3):
   moe_permute / grouped_mlp_fwd_tokens / moe_combine
                      the MoE layer around it: device sort of the router's choices by expert,
                      the forward gathering token rows itself, and the per-token sum of outputs.
+  moe_decode_fwd, nvfp4_moe_decode_fwd, mxfp8_matvec, nvfp4_matvec
+                     the whole layer, and a linear, for a few tokens (decode steps), from the
+                     same weights.
 """
 from __future__ import annotations
 
@@ -34,7 +37,8 @@ __all__ = [
     "grouped_mlp_saved_bytes", "grouped_mlp_fwd_train", "grouped_mlp_bwd_workspace_size", "grouped_mlp_bwd",
     "grouped_mlp_fwd_tokens_train", "grouped_mlp_bwd_tokens", "mxfp8_status_string", "mxfp8_abi_version",
     "mxfp8_mma_peak", "grouped_mlp_bwd_workspace_layout", "nvfp4_sf_bytes", "nvfp4_quantize", "nvfp4_grouped_mlp_workspace_size",
-    "nvfp4_grouped_mlp_workspace_layout", "nvfp4_grouped_mlp_fwd",
+    "nvfp4_grouped_mlp_workspace_layout", "nvfp4_grouped_mlp_fwd", "moe_decode_workspace_size", "moe_decode_fwd",
+    "nvfp4_moe_decode_fwd", "matvec_workspace_size", "mxfp8_matvec", "nvfp4_matvec",
 ]
 
 ROWWISE = 1
@@ -131,6 +135,18 @@ def lib() -> ctypes.CDLL:
             L.nvfp4_grouped_mlp_fwd.argtypes = [P, i64, i64, i64, i32, P, P, P, P, P, P, P, P, f32, P, P, sz, P, P]
             L.mxfp8_mma_peak.restype = i32
             L.mxfp8_mma_peak.argtypes = [i64, i32, P, P, P]
+            L.moe_decode_workspace_size.restype = sz
+            L.moe_decode_workspace_size.argtypes = [i64, i32, i64, i64, i32]
+            L.moe_decode_fwd.restype = i32
+            L.moe_decode_fwd.argtypes = [P, i64, i64, i64, i32, i32, P, P, P, P, P, P, P, P, sz, P]
+            L.nvfp4_moe_decode_fwd.restype = i32
+            L.nvfp4_moe_decode_fwd.argtypes = [P, i64, i64, i64, i32, i32, P, P, P, P, P, P, P, P, P, P, sz, P]
+            L.matvec_workspace_size.restype = sz
+            L.matvec_workspace_size.argtypes = []
+            L.mxfp8_matvec.restype = i32
+            L.mxfp8_matvec.argtypes = [P, i64, i64, i64, P, P, P, P, sz, P]
+            L.nvfp4_matvec.restype = i32
+            L.nvfp4_matvec.argtypes = [P, i64, i64, i64, P, P, P, P, P, sz, P]
             _lib = L
     return _lib
 
@@ -531,6 +547,109 @@ def nvfp4_grouped_mlp_fwd(x_sorted, split_sizes, gates, w1, w2, h_amax: float, y
                                        float(h_amax), _ptr(y), _ptr(workspace), workspace.numel(), _stream(stream),
                                        ev), "nvfp4_grouped_mlp_fwd")
     return y
+
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _require_tensor(t, dtype, name: str, shape=None, numel=None):
+    """A contiguous CUDA tensor of this dtype (and shape, or at least numel elements)."""
+    _require(t.is_cuda and t.is_contiguous() and t.dtype == dtype, f"{name}: a contiguous CUDA tensor of {dtype}")
+    _require(shape is None or tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    _require(numel is None or t.numel() >= numel, f"{name}: {t.numel()} elements, expected {numel}")
+
+
+def moe_decode_workspace_size(T: int, k: int, H: int, F: int, E: int) -> int:
+    return int(lib().moe_decode_workspace_size(T, k, H, F, E))
+
+
+def _moe_decode(name, nv, x, experts, gates, w1, w2, out, workspace, stream):
+    import torch
+    u8 = torch.uint8
+    _require(x.dim() == 2 and experts.dim() == 2, f"{name}: x [T, H] and experts [T, k]")
+    T, H = x.shape
+    k = int(experts.shape[1])
+    per = 2 if nv else 1                       # values per code byte
+    F = int(w2[0].shape[1]) * per
+    _require(H > 0 and F > 0 and w2[0].shape[0] % H == 0, f"{name}: W2 codes [E*H, F]")
+    E = int(w2[0].shape[0]) // H
+    _require_tensor(x, torch.bfloat16, "x")
+    _require_tensor(experts, torch.int32, "experts", (T, k))
+    if gates is not None:
+        _require_tensor(gates, torch.float32, "gates", (T, k))
+    sf_bytes = nvfp4_sf_bytes if nv else (lambda M, K, layout: mxfp8_sf_bytes(M, K, ROWWISE, layout))
+    for w, rows, cols, n in ((w1, E * 2 * F, H, "W1"), (w2, E * H, F, "W2")):
+        _require_tensor(w[0], u8, f"{n} codes", (rows, cols // per))
+        _require_tensor(w[1], u8, f"{n} scales", numel=sf_bytes(rows, cols, SF_MMA))
+        if nv:
+            _require_tensor(w[2], torch.float32, f"{n} amax", numel=1)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _require_tensor(out, torch.bfloat16, "out", (T, H))
+    if workspace is None:
+        workspace = torch.empty(max(256, moe_decode_workspace_size(T, k, H, F, E)), dtype=u8, device=x.device)
+    w1, w2 = ([_ptr(t) for t in w[:3 if nv else 2]] for w in (w1, w2))
+    st = getattr(lib(), name)(_ptr(x), T, H, F, E, k, _ptr(experts), _ptr(gates), *w1, *w2, _ptr(out),
+                              _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, name)
+    return out
+
+
+def moe_decode_fwd(x, experts, gates, w1_q, w1_sf, w2_q, w2_sf, out=None, workspace=None, stream=None):
+    """A whole MoE layer for a few tokens (T <= 64): out[t] = sum_j gates[t, j] * expert(experts[t, j])(x_t).
+
+    x bf16 [T, H]; experts int32 [T, k] (negative: a dropped choice); gates float32 [T, k] or None;
+    weights as for grouped_mlp_fwd.  The activations are not quantized.  Returns out bf16 [T, H].
+    `workspace` (uint8 CUDA tensor, moe_decode_workspace_size bytes) is allocated here when not given."""
+    return _moe_decode("moe_decode_fwd", False, x, experts, gates, (w1_q, w1_sf), (w2_q, w2_sf), out, workspace, stream)
+
+
+def nvfp4_moe_decode_fwd(x, experts, gates, w1, w2, out=None, workspace=None, stream=None):
+    """moe_decode_fwd from NVFP4 weights: w1 = (codes, scale codes in SF_MMA layout, amax) as for
+    nvfp4_grouped_mlp_fwd, w2 likewise."""
+    return _moe_decode("nvfp4_moe_decode_fwd", True, x, experts, gates, w1, w2, out, workspace, stream)
+
+
+def matvec_workspace_size() -> int:
+    return int(lib().matvec_workspace_size())
+
+
+def _matvec(name, nv, x, w, out, workspace, stream):
+    import torch
+    _require(x.dim() == 2 and w[0].dim() == 2, f"{name}: x [T, K] and codes [N, ...]")
+    T, K = x.shape
+    N = int(w[0].shape[0])
+    _require_tensor(x, torch.bfloat16, "x")
+    _require_tensor(w[0], torch.uint8, "codes", (N, K // 2 if nv else K))
+    _require_tensor(w[1], torch.uint8, "scales",
+                    numel=nvfp4_sf_bytes(N, K, SF_MMA) if nv else mxfp8_sf_bytes(N, K, ROWWISE, SF_MMA))
+    if nv:
+        _require_tensor(w[2], torch.float32, "amax", numel=1)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _require_tensor(out, torch.bfloat16, "out", (T, N))
+    if workspace is None:
+        workspace = torch.empty(matvec_workspace_size(), dtype=torch.uint8, device=x.device)
+    st = getattr(lib(), name)(_ptr(x), T, K, N, *[_ptr(t) for t in w], _ptr(out), _ptr(workspace), workspace.numel(),
+                              _stream(stream))
+    _check(st, name)
+    return out
+
+
+def mxfp8_matvec(x, w_q, w_sf, out=None, workspace=None, stream=None):
+    """y = x W^T for a few rows of x (bf16 [T, K], T <= 64) from W quantized by mxfp8_quantize (row-wise,
+    SF_MMA).  x is not quantized.  Returns bf16 [T, N]."""
+    return _matvec("mxfp8_matvec", False, x, (w_q, w_sf), out, workspace, stream)
+
+
+def nvfp4_matvec(x, w, out=None, workspace=None, stream=None):
+    """y = x W^T for a few rows of x (bf16 [T, K], T <= 64) from 4-bit weights: w = (codes, scale codes,
+    amax) as nvfp4_quantize writes them with SF_MMA.  Returns bf16 [T, N]."""
+    return _matvec("nvfp4_matvec", True, x, tuple(w[:3]), out, workspace, stream)
 
 
 def mxfp8_mma_peak(iters: int, workspace, fmt: int = 0, stream=None) -> int:
