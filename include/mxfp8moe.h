@@ -410,12 +410,13 @@ int nvfp4_grouped_mlp_fwd(const void* x_sorted, int64_t R, int64_t H, int64_t F,
  *            initialised or kept.  Not shared by two calls in flight.
  *   Requirements: 0 <= T <= 64, 1 <= k <= 32, 1 <= E <= 1024, H % 128 == 0, F % 128 == 0 (otherwise
  *   MXFP8_ERR_UNSUPPORTED: larger batches go through moe_permute and grouped_mlp_fwd_tokens).  x, out
- *   and weights 16-byte aligned, experts and gates 4-byte aligned.  Two kernels.
+ *   and weights 16-byte aligned, experts and gates 4-byte aligned.
  * nvfp4_moe_decode_fwd -- the same from the weights of nvfp4_grouped_mlp_fwd; no h_amax is needed.
  * mxfp8_matvec, nvfp4_matvec -- y[t] = W x_t for T <= 64 rows of x (device) bf16 [T, K] and W [N, K] as
  *   mxfp8_quantize (row-wise) or nvfp4_quantize write it with MXFP8_SF_MMA; y (device) bf16 [T, N],
- *   fully overwritten, must not overlap x.  K % 128 == 0, N % 128 == 0.  workspace (device) holds the
- *   error word: matvec_workspace_size() bytes, 16-byte aligned.  One kernel.
+ *   fully overwritten, must not overlap x.  K % 128 == 0, N % 128 == 0.  workspace (device):
+ *   matvec_workspace_size(T, K) bytes (grows with T and K), 256-byte aligned, its first 4 bytes the
+ *   error word.
  */
 size_t moe_decode_workspace_size(int64_t T, int k, int64_t H, int64_t F, int E);
 int moe_decode_fwd(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, const int32_t* experts,
@@ -425,7 +426,7 @@ int nvfp4_moe_decode_fwd(const void* x, int64_t T, int64_t H, int64_t F, int E, 
                          const float* gates, const uint8_t* w1_q, const uint8_t* w1_sf, const float* w1_amax,
                          const uint8_t* w2_q, const uint8_t* w2_sf, const float* w2_amax, void* out, void* workspace,
                          size_t workspace_bytes, void* stream);
-size_t matvec_workspace_size(void);
+size_t matvec_workspace_size(int64_t T, int64_t K);
 int mxfp8_matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf, void* y,
                  void* workspace, size_t workspace_bytes, void* stream);
 int nvfp4_matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf,

@@ -142,7 +142,7 @@ def lib() -> ctypes.CDLL:
             L.nvfp4_moe_decode_fwd.restype = i32
             L.nvfp4_moe_decode_fwd.argtypes = [P, i64, i64, i64, i32, i32, P, P, P, P, P, P, P, P, P, P, sz, P]
             L.matvec_workspace_size.restype = sz
-            L.matvec_workspace_size.argtypes = []
+            L.matvec_workspace_size.argtypes = [i64, i64]
             L.mxfp8_matvec.restype = i32
             L.mxfp8_matvec.argtypes = [P, i64, i64, i64, P, P, P, P, sz, P]
             L.nvfp4_matvec.restype = i32
@@ -549,16 +549,25 @@ def nvfp4_grouped_mlp_fwd(x_sorted, split_sizes, gates, w1, w2, h_amax: float, y
     return y
 
 
-def _require(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _need(t, dtype, shape, name: str):
+    """A contiguous CUDA tensor of this dtype and shape (an int: at least so many elements).  These calls
+    are as short as the kernels behind them, so the message is put together only when it is needed."""
+    if t.dtype == dtype and t.is_cuda and t.is_contiguous() and \
+            (t.numel() >= shape if isinstance(shape, int) else t.shape == shape):
+        return t.data_ptr()
+    want = f"at least {shape} elements" if isinstance(shape, int) else f"shape {tuple(shape)}"
+    raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, {want}; got {t.dtype}, {tuple(t.shape)}")
 
 
-def _require_tensor(t, dtype, name: str, shape=None, numel=None):
-    """A contiguous CUDA tensor of this dtype (and shape, or at least numel elements)."""
-    _require(t.is_cuda and t.is_contiguous() and t.dtype == dtype, f"{name}: a contiguous CUDA tensor of {dtype}")
-    _require(shape is None or tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    _require(numel is None or t.numel() >= numel, f"{name}: {t.numel()} elements, expected {numel}")
+def _stream_of(t, stream) -> int:
+    """The given stream, or the current stream of the tensor's device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else int(stream.cuda_stream)
+
+
+def _sf_mma_bytes(nv: bool, M: int, K: int) -> int:
+    """Bytes of a row-wise SF_MMA scale array (mxfp8_sf_bytes, nvfp4_sf_bytes)."""
+    return (M + 127) // 128 * ((K + 255) // 256 * 4 if nv else (K // 32 + 3) // 4) * 512
 
 
 def moe_decode_workspace_size(T: int, k: int, H: int, F: int, E: int) -> int:
@@ -567,34 +576,32 @@ def moe_decode_workspace_size(T: int, k: int, H: int, F: int, E: int) -> int:
 
 def _moe_decode(name, nv, x, experts, gates, w1, w2, out, workspace, stream):
     import torch
-    u8 = torch.uint8
-    _require(x.dim() == 2 and experts.dim() == 2, f"{name}: x [T, H] and experts [T, k]")
+    u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
     T, H = x.shape
-    k = int(experts.shape[1])
+    T2, k = experts.shape
     per = 2 if nv else 1                       # values per code byte
-    F = int(w2[0].shape[1]) * per
-    _require(H > 0 and F > 0 and w2[0].shape[0] % H == 0, f"{name}: W2 codes [E*H, F]")
-    E = int(w2[0].shape[0]) // H
-    _require_tensor(x, torch.bfloat16, "x")
-    _require_tensor(experts, torch.int32, "experts", (T, k))
-    if gates is not None:
-        _require_tensor(gates, torch.float32, "gates", (T, k))
-    sf_bytes = nvfp4_sf_bytes if nv else (lambda M, K, layout: mxfp8_sf_bytes(M, K, ROWWISE, layout))
-    for w, rows, cols, n in ((w1, E * 2 * F, H, "W1"), (w2, E * H, F, "W2")):
-        _require_tensor(w[0], u8, f"{n} codes", (rows, cols // per))
-        _require_tensor(w[1], u8, f"{n} scales", numel=sf_bytes(rows, cols, SF_MMA))
-        if nv:
-            _require_tensor(w[2], torch.float32, f"{n} amax", numel=1)
+    M2, F = w2[0].shape
+    F *= per
+    E = M2 // H if H else 0
+    px, pe = _need(x, bf16, (T, H), "x"), _need(experts, torch.int32, (T, k), "experts")
+    pg = None if gates is None else _need(gates, f32, (T, k), "gates")
+    p1, s1 = _need(w1[0], u8, (E * 2 * F, H // per), "W1 codes"), _need(w1[1], u8, _sf_mma_bytes(nv, E * 2 * F, H), "W1 scales")
+    p2, s2 = _need(w2[0], u8, (E * H, F // per), "W2 codes"), _need(w2[1], u8, _sf_mma_bytes(nv, E * H, F), "W2 scales")
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    else:
-        _require_tensor(out, torch.bfloat16, "out", (T, H))
+        out = torch.empty((T, H), dtype=bf16, device=x.device)
+    po = _need(out, bf16, (T, H), "out")
     if workspace is None:
         workspace = torch.empty(max(256, moe_decode_workspace_size(T, k, H, F, E)), dtype=u8, device=x.device)
-    w1, w2 = ([_ptr(t) for t in w[:3 if nv else 2]] for w in (w1, w2))
-    st = getattr(lib(), name)(_ptr(x), T, H, F, E, k, _ptr(experts), _ptr(gates), *w1, *w2, _ptr(out),
-                              _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(st, name)
+    pw = _need(workspace, u8, 256, "workspace")
+    if nv:
+        st = lib().nvfp4_moe_decode_fwd(px, T, H, F, E, k, pe, pg, p1, s1, _need(w1[2], f32, 1, "W1 amax"), p2, s2,
+                                        _need(w2[2], f32, 1, "W2 amax"), po, pw, workspace.numel(),
+                                        _stream_of(x, stream))
+    else:
+        st = lib().moe_decode_fwd(px, T, H, F, E, k, pe, pg, p1, s1, p2, s2, po, pw, workspace.numel(),
+                                  _stream_of(x, stream))
+    if st != OK:
+        raise MXFP8Error(st, name)
     return out
 
 
@@ -613,30 +620,31 @@ def nvfp4_moe_decode_fwd(x, experts, gates, w1, w2, out=None, workspace=None, st
     return _moe_decode("nvfp4_moe_decode_fwd", True, x, experts, gates, w1, w2, out, workspace, stream)
 
 
-def matvec_workspace_size() -> int:
-    return int(lib().matvec_workspace_size())
+def matvec_workspace_size(T: int = 64, K: int = 16384) -> int:
+    """Bytes of a workspace for mxfp8_matvec / nvfp4_matvec calls of up to T rows of up to K values."""
+    return int(lib().matvec_workspace_size(T, K))
 
 
 def _matvec(name, nv, x, w, out, workspace, stream):
     import torch
-    _require(x.dim() == 2 and w[0].dim() == 2, f"{name}: x [T, K] and codes [N, ...]")
+    u8, bf16 = torch.uint8, torch.bfloat16
     T, K = x.shape
-    N = int(w[0].shape[0])
-    _require_tensor(x, torch.bfloat16, "x")
-    _require_tensor(w[0], torch.uint8, "codes", (N, K // 2 if nv else K))
-    _require_tensor(w[1], torch.uint8, "scales",
-                    numel=nvfp4_sf_bytes(N, K, SF_MMA) if nv else mxfp8_sf_bytes(N, K, ROWWISE, SF_MMA))
-    if nv:
-        _require_tensor(w[2], torch.float32, "amax", numel=1)
+    N = w[0].shape[0]
+    px = _need(x, bf16, (T, K), "x")
+    pq, ps = _need(w[0], u8, (N, K // 2 if nv else K), "codes"), _need(w[1], u8, _sf_mma_bytes(nv, N, K), "scales")
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
-    else:
-        _require_tensor(out, torch.bfloat16, "out", (T, N))
+        out = torch.empty((T, N), dtype=bf16, device=x.device)
+    po = _need(out, bf16, (T, N), "out")
     if workspace is None:
-        workspace = torch.empty(matvec_workspace_size(), dtype=torch.uint8, device=x.device)
-    st = getattr(lib(), name)(_ptr(x), T, K, N, *[_ptr(t) for t in w], _ptr(out), _ptr(workspace), workspace.numel(),
-                              _stream(stream))
-    _check(st, name)
+        workspace = torch.empty(max(256, matvec_workspace_size(T, K)), dtype=u8, device=x.device)
+    pw = _need(workspace, u8, 256, "workspace")
+    if nv:
+        st = lib().nvfp4_matvec(px, T, K, N, pq, ps, _need(w[2], torch.float32, 1, "amax"), po, pw, workspace.numel(),
+                                _stream_of(x, stream))
+    else:
+        st = lib().mxfp8_matvec(px, T, K, N, pq, ps, po, pw, workspace.numel(), _stream_of(x, stream))
+    if st != OK:
+        raise MXFP8Error(st, name)
     return out
 
 
@@ -649,7 +657,7 @@ def mxfp8_matvec(x, w_q, w_sf, out=None, workspace=None, stream=None):
 def nvfp4_matvec(x, w, out=None, workspace=None, stream=None):
     """y = x W^T for a few rows of x (bf16 [T, K], T <= 64) from 4-bit weights: w = (codes, scale codes,
     amax) as nvfp4_quantize writes them with SF_MMA.  Returns bf16 [T, N]."""
-    return _matvec("nvfp4_matvec", True, x, tuple(w[:3]), out, workspace, stream)
+    return _matvec("nvfp4_matvec", True, x, w, out, workspace, stream)
 
 
 def mxfp8_mma_peak(iters: int, workspace, fmt: int = 0, stream=None) -> int:

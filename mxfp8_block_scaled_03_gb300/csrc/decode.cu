@@ -21,20 +21,19 @@
 // What bounds it: reading the weights once (a token's flops per weight byte are far below the tensor
 // cores').  So the weights are the M operand: TMA brings 128 rows x 128 code bytes per K step and
 // their scale atoms, the MMA reads both as stored, and no instruction is spent per weight.  The
-// tokens are the N operand, converted by four warps while the weights travel.
+// tokens are the N operand: k_split_x writes the columns of x, GATE_UP's epilogue those of h.
 //
-// Split: one CTA takes a range of K steps of one 128-row tile; a cluster of up to 8 CTAs shares the
-// tile and adds its partial sums through distributed shared memory in a fixed order (no atomics:
-// results do not depend on timing).  Two CTAs share an SM so that one's start and end are hidden
-// behind the other's copies.
-//   k_decode<GATE_UP>  cluster = (gate, up) x K ranges of 128 columns of F of one active expert:
-//                      h = gate silu(g) u, fp32 rows [token-expert pair, F]
-//   k_decode<DOWN>     cluster = K ranges of 128 rows of H; K runs over all active experts' F one
-//                      after the other with one column group per token (zero where the token did
-//                      not choose the expert), so the accumulator itself sums a token's experts
-//   k_decode<LINEAR>   cluster = K ranges of 128 rows of W
-// DOWN is launched programmatically dependent on GATE_UP: its weight copies start while GATE_UP's
-// last CTAs run; only its conversion warps wait for h.
+//   k_split_x          x -> columns, and the bookkeeping of the call
+//   k_decode<GATE_UP>  units: 128 columns of F of one chosen expert (and up to 16 or 32 of its tokens); gate
+//                      and up rows are alternate K steps on two accumulators; h = gate silu(g) u
+//   k_decode<DOWN>     units: 128 rows of H; K runs over all chosen experts' F one after the other, with one
+//                      column group per token (zero where the token did not choose the expert), so the
+//                      accumulator itself sums a token's experts
+//   k_decode<LINEAR>   units: 128 rows of W
+// The kernels are launched programmatically dependent: a kernel's weight copies start while the one
+// before it runs, and only what reads its results waits.  Two CTAs share an SM (one alone reaches 60-87%
+// of the copy bandwidth: its single MMA thread spends 0.3-0.5 us a K step of 16 KB).
+// Measured (4096 -> 114688, one token): MXFP8 76.0 us, 6.38 TB/s (94% of the copy rate); NVFP4 47.4 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -51,20 +50,22 @@
 namespace mx {
 namespace {
 
-constexpr int DEC_THREADS = 192;             // warp 0 copies, warp 1 MMA, warps 2-5 conversion + epilogue
-constexpr int DEC_CONV_WARPS = 4;
+constexpr int DEC_THREADS = 256;             // warp 0 copies, warp 1 MMA, warps 2-3 scales, warps 4-7 epilogue
+constexpr int DEC_SCALE_WARPS = 2;
+constexpr int DEC_FIRST_EPI_WARP = 4;
 constexpr int DEC_A_STAGE = 128 * 128;       // 128 weight rows x 128 code bytes
 constexpr int DEC_MAX_TOKENS = 64;           // tokens of one call
-constexpr int DEC_CHUNK = 32;                // most tokens of one accumulator (bits of an expert's token mask)
+constexpr int DEC_CHUNK = 32;                // DOWN, LINEAR: most tokens of one accumulator
 constexpr int DEC_MAX_K = 32;                // choices per token
-constexpr int DEC_MAX_CLUSTER = 8;
-constexpr int DEC_MAX_A = 8, DEC_MAX_B = 4;  // ring depths
-// Two CTAs per SM: half of 228 KB each, less 1 KB the system keeps per CTA.
-constexpr int DEC_SMEM = 113 * 1024;
+constexpr int DEC_MAX_STAGES = 12;
+constexpr int DEC_MIN_STEPS = 4;             // K steps that make a CTA worth having (2 and 8 measured the same)
+// Half of 228 KB less the 1 KB the system keeps per CTA, so that a kernel's CTAs fit beside those of the
+// kernel before it; the whole SM where that leaves fewer than four stages.
+constexpr int DEC_SMEM_HALF = 113 * 1024, DEC_SMEM_FULL = 226 * 1024;
 constexpr uint32_t DEC_TMEM_COLS = 256;      // two CTAs per SM share 512
-// TMEM columns: the accumulator (up to 160), then two sets of scales of A and of B, used in turn.
-constexpr uint32_t DEC_SFA_COL = 160, DEC_SFB_COL = 192;
-constexpr uint32_t DEC_BAR_CONV = 1;         // hardware barrier of the conversion warps
+// TMEM columns: accumulators (at most 160), then as many sets of scales of A and B as fit, used in turn
+// (at least two): a step's scales may be written while the MMAs of that many steps less one are pending.
+constexpr int SPLIT_THREADS = 1024;          // at most
 
 enum DecMode { DEC_GATE_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
 enum DecFmt { DEC_MX = 0, DEC_NV = 1 };
@@ -72,46 +73,67 @@ enum DecFmt { DEC_MX = 0, DEC_NV = 1 };
 // Columns per token: E4M3 pieces of a bf16 (2) or fp32 (3) value, or base-8 digits (5).
 constexpr int dec_pieces(int fmt, int mode) { return fmt == DEC_NV ? 5 : mode == DEC_DOWN ? 3 : 2; }
 constexpr int dec_step_values(int fmt) { return fmt == DEC_NV ? 256 : 128; }
-constexpr int dec_atoms(int fmt) { return fmt == DEC_NV ? 4 : 1; }   // scale atoms per 128 rows and step
+constexpr int dec_atoms(int fmt) { return fmt == DEC_NV ? 4 : 1; }          // scale atoms per 128 rows and step
+constexpr int dec_exp_bytes(int fmt) { return fmt == DEC_NV ? 16 : 4; }     // blocks of one row and step
+// GATE_UP: most tokens of one unit (an expert with more gives several units); two accumulators of at
+// most 80 columns share the TMEM that DOWN and LINEAR use for one of 160.
+constexpr int dec_group(int fmt) { return fmt == DEC_NV ? 16 : 32; }
 
-// Shared memory of one CTA (byte offsets from a 1024-byte boundary).
+// Shared memory of one CTA (byte offsets from a 1024-byte boundary); the weight ring is at 0.
 struct DecLayout {
-  int na, nb;                        // stages of the weight ring and of the activation ring
+  int stages, smem;
   int b_stage, sfb_stage;
-  int b, sfa, sfb, bars, misc;       // the weight ring is at 0
+  int b, sfa, sfb, bars, misc;
+  int n_max;             // most columns of one accumulator (GATE_UP: the second one starts there)
+  int sf_col, sf_cols, sf_sets;   // TMEM: first column of the scale sets, columns per set, sets
+};
+
+// Activations as columns of the MMA.  Row r * P + q of `codes` holds piece q of row r (a token of x, a
+// token-expert pair of h): 128 code bytes per K step.  P rows of zeros follow them.
+struct DecOperand {
+  uint8_t* codes;   // [(rows + 1) * P][steps * 128]
+  uint8_t* exps;    // [rows][steps][4 | 16]: exponent + 127 of every 32 | 16 values (255: not finite)
+  int* top;         // [T] largest exponent of the token's row, or of all its rows of h (NVFP4)
 };
 
 struct DecParams {
   DecLayout L;
-  const uint16_t* x;      // GATE_UP, LINEAR: bf16 [T, K]
-  float* h;               // GATE_UP out, DOWN in: [T * k, F]
-  float* hmax;            // NVFP4: largest |h| of every 32 columns, [T * k, F / 32]
+  DecOperand in;          // GATE_UP, LINEAR: x;  DOWN: h
+  DecOperand h;           // GATE_UP: where h goes
+  int h_steps;            // GATE_UP: K steps of h
   const uint8_t* w_sf;
   const float* w_amax;    // NVFP4
   const int32_t* experts; // [T, k]
   const float* gates;     // [T, k] or NULL
   uint16_t* out;          // DOWN: [T, H], LINEAR: [T, N]
   uint32_t* err;
+  float* part;            // partial sums: part_slot floats per CTA
+  int part_slot;
+  int* counters;          // [units][4] of units shared by several CTAs: how many are done with a quarter of the rows
   int T, k, E;
   int K;                  // contraction length of one weight row
   int steps;              // its K steps
   int kt;                 // its scale atoms per 128-row tile
   int tiles;              // 128-row tiles (of F, H or N)
   int F;
-  int cs;                 // CTAs per cluster
-  int per_chunk;          // tokens per chunk (blockIdx.y)
+  int max_active;         // most list entries (see the routing)
+  int zero_row;           // row of the operand that is zeros
+  int chunks, per_chunk;  // DOWN, LINEAR: token chunks, tokens per chunk
   uint64_t timeout_ns, drain_ns;
 };
 
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void conv_barrier() {
-  asm volatile("bar.sync %0, %1;" ::"r"(DEC_BAR_CONV), "r"(DEC_CONV_WARPS * 32) : "memory");
+// Wait for the grids this one depends on; what they wrote may then be read, by bulk copies too.
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("fence.proxy.async.global;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// One lane of the (converged) warp.  The compiler knows that a branch on it holds one thread, and issues
+// copies and MMAs there directly; behind `lane == 0` it wraps each of them in a loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void tc_copy_sf(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
@@ -147,147 +169,209 @@ __device__ __forceinline__ bool dec_warp_wait(uint64_t* bar, uint32_t parity, vo
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
-// floor(log2) of a block's largest magnitude from its float bits, kept where the scales used below
-// stay representable (blocks under 2^-100 are treated as if their largest value were 2^-100).
+// floor(log2) of a block's largest magnitude from its float bits (128: not finite), kept where the
+// scales used below stay representable: blocks under 2^-100 count as 2^-100.
 __device__ __forceinline__ int block_exponent(uint32_t abs_bits) {
   return max(static_cast<int>(abs_bits >> 23) - 127, -100);
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-
-template <int N>
-__device__ __forceinline__ uint32_t abs_max_bits(const float (&v)[N]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
+// Multiplier that takes a block's largest magnitude into [128, 256) (MXFP8) or [2, 4) (NVFP4).
+template <int FMT>
+__device__ __forceinline__ float block_multiplier(int eb) {
+  return pow2f((FMT == DEC_NV ? 1 : 7) - min(eb, 127));
+}
+// One step of the decomposition: the next piece of a pair of scaled values, and what is left of them
+// for the following piece.  MXFP8: the leading 4 bits of the significand, or (last) all of it, rounded
+// by the conversion; NVFP4: the nearest integer (adding and subtracting 1.5 * 2^23 rounds to it).
+template <int FMT, bool LAST>
+__device__ __forceinline__ uint64_t next_piece(uint64_t& r) {
+  if constexpr (FMT == DEC_MX) {
+    if constexpr (LAST) return r;
+    const uint64_t top = r & 0xFFF00000FFF00000ull;
+    r = f2_mul(f2_fma(top, f2_pack(-1.0f, -1.0f), r), f2_pack(16.0f, 16.0f));
+    return top;
+  } else {
+    const uint64_t n = f2_add(f2_add(r, f2_pack(12582912.0f, 12582912.0f)), f2_pack(-12582912.0f, -12582912.0f));
+    if constexpr (!LAST) r = f2_fma(n, f2_pack(-8.0f, -8.0f), f2_mul(r, f2_pack(8.0f, 8.0f)));
+    return n;
+  }
 }
 
-// Eight values of a 32-value block (four lanes hold the block) -> P E4M3 pieces: 8 code bytes in
-// row p * tp + c of the step's activation tile and, from the block's first lane, the scale bytes.
-// g: which eight of the step's 128 values.  Pieces 0..P-2 are cut (the residual is exact), the last
-// is rounded to nearest even.
-template <int P>
-__device__ __forceinline__ void put_pieces_mx(const float (&v)[8], uint8_t* sB, uint8_t* sSF, int c, int tp, int g) {
-  uint32_t m = abs_max_bits(v);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  if (c < 0) return;
-  const bool finite = m < 0x7F800000u;
-  const int eb = block_exponent(m);
-  const float inv = pow2f(7 - min(eb, 127));   // largest magnitude in [128, 256)
-  const uint64_t inv2 = f2_pack(inv, inv), sixteen = f2_pack(16.0f, 16.0f), minus1 = f2_pack(-1.0f, -1.0f);
-  uint64_t r[4];
+// x (bf16 [T, K]) -> columns.  One CTA per token; a thread takes 8 values (MXFP8, four threads a block)
+// or 16 (NVFP4, one block) at a time, 8 code bytes either way.  It also prepares the call's bookkeeping:
+// the error word, the range check of the experts' ids, the row exponents of h and the counters.
+// Latency-bound (a token is a few KB): what matters is that the weight kernel's copies start meanwhile.
+struct SplitParams {
+  const uint16_t* x;
+  DecOperand o;
+  uint32_t* err;
+  const int32_t* experts;
+  int* h_top;
+  int* counters;
+  uint4* zero_row[2];     // the rows of zeros behind the columns of x and of h
+  int zero_n[2];
+  int T, K, steps, n_ids, E, n_top, n_counters;
+};
+template <int FMT>
+__global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) {
+  constexpr int P = dec_pieces(FMT, DEC_LINEAR), EB = dec_exp_bytes(FMT);
+  constexpr int VALS = FMT == DEC_NV ? 16 : 8;   // 16 groups per step
+  __shared__ int s_top;
+  pdl_wait();
+  const int t = blockIdx.x, tid = threadIdx.x;
+  if (t == 0 && tid == 0) *p.err = 0;
+  if (tid == 0) s_top = -128;
+  __syncthreads();
+  pdl_launch_dependents();   // everything before this call in the stream is complete
+  if (t == 0) {
+    for (int i = tid; i < p.n_ids; i += blockDim.x)
+      if (__ldg(p.experts + i) >= p.E) atomicOr(p.err, ERR_EXPERT_RANGE);
+    for (int z = 0; z < 2; ++z)
+      for (int i = tid; i < p.zero_n[z]; i += blockDim.x) p.zero_row[z][i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  for (int i = t * blockDim.x + tid; i < p.n_top; i += p.T * blockDim.x) p.h_top[i] = -128;
+  for (int i = t * blockDim.x + tid; i < p.n_counters; i += p.T * blockDim.x) p.counters[i] = 0;
+
+  int top = -128;
+  const int groups = p.K / VALS;
+  for (int g0 = 0; g0 < groups; g0 += blockDim.x) {
+    const int gi = g0 + tid;
+    const bool in = gi < groups;   // K % 128 == 0: whole blocks, and the four threads of one agree
+    const int step = gi >> 4, g = gi & 15;
+    uint4 w[VALS / 8];
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), inv2);
+    for (int i = 0; i < VALS / 8; ++i) {
+      w[i] = in ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.K + gi * VALS) + i)
+                : make_uint4(0u, 0u, 0u, 0u);
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                               __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
+    }
+    m = max(m & 0xFFFFu, m >> 16) << 16;
+    if constexpr (FMT == DEC_MX) {
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    }
+    if (!in) continue;
+    const int eb = block_exponent(m);
+    top = max(top, eb);
+    if (FMT == DEC_NV || (g & 3) == 0)
+      p.o.exps[(static_cast<int64_t>(t) * p.steps + step) * EB + (FMT == DEC_NV ? g : g >> 2)] =
+          static_cast<uint8_t>(eb + 127);
+    const float inv = block_multiplier<FMT>(eb);
+    const uint64_t inv2 = f2_pack(inv, inv);
+    uint64_t r[VALS / 2];
 #pragma unroll
-  for (int q = 0; q < P; ++q) {
-    uint32_t code[4];
+    for (int i = 0; i < VALS / 8; ++i) {
+      r[4 * i] = f2_mul(f2_pack(bf16_lo(w[i].x), bf16_hi(w[i].x)), inv2);
+      r[4 * i + 1] = f2_mul(f2_pack(bf16_lo(w[i].y), bf16_hi(w[i].y)), inv2);
+      r[4 * i + 2] = f2_mul(f2_pack(bf16_lo(w[i].z), bf16_hi(w[i].z)), inv2);
+      r[4 * i + 3] = f2_mul(f2_pack(bf16_lo(w[i].w), bf16_hi(w[i].w)), inv2);
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (q + 1 < P) {
-        const uint64_t top = r[i] & 0xFFF00000FFF00000ull;   // sign, exponent, 3 bits after the leading one
-        code[i] = e4m3x2_f2(top);
-        r[i] = f2_mul(f2_fma(top, minus1, r[i]), sixteen);
+    for (int q = 0; q < P; ++q) {
+      uint64_t n[VALS / 2];
+#pragma unroll
+      for (int i = 0; i < VALS / 2; ++i) n[i] = q + 1 < P ? next_piece<FMT, false>(r[i]) : next_piece<FMT, true>(r[i]);
+      uint2 code;
+      if constexpr (FMT == DEC_MX) {
+        code.x = e4m3x2_f2(n[0]) | (e4m3x2_f2(n[1]) << 16);
+        code.y = e4m3x2_f2(n[2]) | (e4m3x2_f2(n[3]) << 16);
       } else {
-        code[i] = e4m3x2_f2(r[i]);
+        code.x = e2m1x8(f2_lo(n[0]), f2_hi(n[0]), f2_lo(n[1]), f2_hi(n[1]), f2_lo(n[2]), f2_hi(n[2]), f2_lo(n[3]),
+                        f2_hi(n[3]));
+        code.y = e2m1x8(f2_lo(n[4]), f2_hi(n[4]), f2_lo(n[5]), f2_hi(n[5]), f2_lo(n[6]), f2_hi(n[6]), f2_lo(n[7]),
+                        f2_hi(n[7]));
       }
+      *reinterpret_cast<uint2*>(p.o.codes + (static_cast<int64_t>(t) * P + q) * p.steps * 128 + gi * 8) = code;
     }
-    const int row = q * tp + c;
-    *reinterpret_cast<uint2*>(sB + row * 128 + (((g >> 1) ^ (row & 7)) << 4) + ((g & 1) << 3)) =
-        make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
-    if ((g & 3) == 0)   // 0xFF: NaN, the column of a token with a non-finite value
-      sSF[(row >> 7) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (g >> 2)] =
-          finite ? static_cast<uint8_t>(eb + 120 - 4 * q) : static_cast<uint8_t>(0xFF);
+  }
+  if constexpr (FMT == DEC_NV) {
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((tid & 31) == 0) atomicMax(&s_top, top);
+    __syncthreads();
+    if (tid == 0) p.o.top[t] = s_top;
   }
 }
 
-// One 16-value block -> P base-8 digits as E2M1: 8 code bytes in row p * tp + c, and the block's UE4M3
-// scale 2^(8 + e_block - e_token) (the same for every digit).  j: which of the step's 16 blocks.
-template <int P>
-__device__ __forceinline__ void put_pieces_nv(const float (&v)[16], int e_tok, uint8_t* sB, uint8_t* sSF, int nat,
-                                              int c, int tp, int j) {
-  const uint32_t m = abs_max_bits(v);
-  const bool finite = m < 0x7F800000u;
-  // blocks more than 2^17 below the token's largest value share the smallest scale
-  const int eb = max(block_exponent(m), e_tok - 17);
-  const float inv = pow2f(1 - min(eb, 127));   // largest magnitude in [2, 4)
-  const uint64_t inv2 = f2_pack(inv, inv), eight = f2_pack(8.0f, 8.0f), minus8 = f2_pack(-8.0f, -8.0f);
-  // adding and subtracting 1.5 * 2^23 rounds to the nearest integer
-  const uint64_t big = f2_pack(12582912.0f, 12582912.0f), minus_big = f2_pack(-12582912.0f, -12582912.0f);
-  uint64_t r[8];
+// The scale words of one token and K step for its P columns, from its blocks' exponents.
+//   MXFP8  word of piece q: UE8M0 2^(e - 7 - 4 q) per block.
+//   NVFP4  one word per MMA, the same for all digits: UE4M3 2^(8 + e - top) per block (0 below 2^-9, which
+//          drops values under 2^-17 of the token's largest).
+// Blocks that are not finite get a NaN scale.
+__device__ __forceinline__ uint32_t mx_scales(uint32_t e4, int q) {
+  const uint32_t nan = __vcmpeq4(e4, 0xFFFFFFFFu);
+  return __vsub4(e4, 0x07070707u + 0x04040404u * static_cast<uint32_t>(q)) | nan;
+}
+__device__ __forceinline__ uint32_t nv_scales(uint32_t e4, int top) {
+  // u = e - top + 18 - 127 >= 0, four bytes at once: 2^(u - 10) is 0, 1, 2, 4 (subnormal) for u = 0 .. 3 and
+  // (u - 3) << 3 above
+  const uint32_t u = __vsubus4(e4, static_cast<uint32_t>(top + 109) * 0x01010101u);
+  const uint32_t sub = u & __vcmpleu4(u, 0x03030303u);
+  const uint32_t code = (__vsubus4(u, 0x03030303u) << 3) + sub + (__vcmpeq4(sub, 0x03030303u) & 0x01010101u);
+  const uint32_t nan = __vcmpeq4(e4, 0xFFFFFFFFu);
+  return (code & ~nan) | (nan & 0x7F7F7F7Fu);
+}
+
+// Position of set bit n (from 0) of m; 64 when m has no more than n bits set.
+__device__ __forceinline__ int nth_set_bit(uint64_t m, int n) {
+  int base = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), inv2);
-  const int d = eb - e_tok + 8;   // -9 .. 8
-  const uint32_t sc = !finite ? 0x7Fu : d >= -6 ? static_cast<uint32_t>(d + 7) << 3 : 1u << (d + 9);
-#pragma unroll
-  for (int q = 0; q < P; ++q) {
-    uint64_t n[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      n[i] = f2_add(f2_add(r[i], big), minus_big);
-      if (q + 1 < P) r[i] = f2_fma(n[i], minus8, f2_mul(r[i], eight));
+  for (int s = 32; s >= 1; s >>= 1) {
+    const int c = __popcll(m & ((1ull << s) - 1ull));
+    if (n >= c) {
+      n -= c;
+      m >>= s;
+      base += s;
     }
-    const int row = q * tp + c;
-    uint2 w;
-    w.x = e2m1x8(f2_lo(n[0]), f2_hi(n[0]), f2_lo(n[1]), f2_hi(n[1]), f2_lo(n[2]), f2_hi(n[2]), f2_lo(n[3]), f2_hi(n[3]));
-    w.y = e2m1x8(f2_lo(n[4]), f2_hi(n[4]), f2_lo(n[5]), f2_hi(n[5]), f2_lo(n[6]), f2_hi(n[6]), f2_lo(n[7]), f2_hi(n[7]));
-    *reinterpret_cast<uint2*>(sB + row * 128 + (((j >> 1) ^ (row & 7)) << 4) + ((j & 1) << 3)) = w;
-    sSF[((j >> 2) * nat + (row >> 7)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (j & 3)] =
-        static_cast<uint8_t>(sc);
   }
+  return (m & 1ull) != 0 && n == 0 ? base : 64;
 }
+__device__ __forceinline__ int bits_below(uint64_t m, int t) { return __popcll(m & ((1ull << t) - 1ull)); }
 
-__device__ __forceinline__ void unpack8(const uint4 w, float* v) {
-  v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-  v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
-}
-
+// The K steps of all units (128-row tiles, GATE_UP: tile x expert) form one sequence; a CTA runs through
+// a piece of it, whole units or one part of one.  Where several CTAs share a unit, each warp of an epilogue
+// that finishes its 32 rows last sums the parts, in their order (the result does not depend on which it is).
 template <int FMT, int MODE>
-__global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant__ CUtensorMap tm, const DecParams p) {
+__global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant__ CUtensorMap tm_w,
+                                                        const __grid_constant__ CUtensorMap tm_x, const DecParams p) {
   constexpr int P = dec_pieces(FMT, MODE);
-  constexpr int KSTEP = dec_step_values(FMT);
-  constexpr int ATOMS = dec_atoms(FMT);
+  constexpr int ATOMS = dec_atoms(FMT), EB = dec_exp_bytes(FMT);
+  constexpr int ACCS = MODE == DEC_GATE_UP ? 2 : 1;
+  constexpr int GROUP = dec_group(FMT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const DecLayout& L = p.L;
-  uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + L.bars);
-  uint64_t* empty_a = full_a + DEC_MAX_A;
-  uint64_t* full_b = empty_a + DEC_MAX_A;
-  uint64_t* empty_b = full_b + DEC_MAX_B;
-  uint64_t* done = empty_b + DEC_MAX_B;
-  uint64_t* drained = done + 1;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);   // the copies landed and the columns' scales are in place
+  uint64_t* empty = full + DEC_MAX_STAGES;                        // the MMAs have read the stage
+  uint64_t* acc_full = empty + DEC_MAX_STAGES;                    // a run's part of a unit is complete in TMEM
+  uint64_t* acc_empty = acc_full + 1;                             // the epilogue has read it
+  uint64_t* drained = acc_empty + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_nact = reinterpret_cast<int*>(tmem_holder + 2);
-  int* s_tok = reinterpret_cast<int*>(smem + L.misc);            // GATE_UP: token of each column
-  float* s_gate = reinterpret_cast<float*>(s_tok + DEC_CHUNK);   // GATE_UP: its routing weight
-  int* s_emax = reinterpret_cast<int*>(s_gate + DEC_CHUNK);      // NVFP4: exponent of each column's scale
-  uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_emax + DEC_CHUNK);   // [E] tokens that chose the expert
-  int* s_act_e = reinterpret_cast<int*>(s_mask + p.E);           // active experts: id, tokens, first row of h
-  const int nact_max = min(p.E, p.per_chunk * p.k);
-  uint32_t* s_act_m = reinterpret_cast<uint32_t*>(s_act_e + nact_max);
-  int* s_act_off = reinterpret_cast<int*>(s_act_m + nact_max);
+  int* s_row = reinterpret_cast<int*>(smem + L.misc);             // [32] operand row behind each token column
+  uint32_t* s_dirty = reinterpret_cast<uint32_t*>(s_row + 32);    // [stages] DOWN: columns of the stage that are not zero
+  uint32_t* s_fill = s_dirty + 16;                                // [stages] columns of the first steps
+  uint64_t* s_mask = reinterpret_cast<uint64_t*>(s_fill + 16);    // [E] tokens that chose the expert
+  // chosen experts (GATE_UP: and groups of their tokens): tokens, id + 1024 * group, first row of h
+  uint64_t* s_act_m = s_mask + p.E;
+  int* s_act_e = reinterpret_cast<int*>(s_act_m + p.max_active);
+  int* s_act_off = s_act_e + p.max_active;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = static_cast<int>(cluster_cta_rank());
-  const int cluster = blockIdx.x / p.cs;
-  const int t0 = blockIdx.y * p.per_chunk;
+  const int chunk = static_cast<int>(blockIdx.x) % p.chunks;   // the chunks' CTAs run side by side
+  const int t0 = chunk * p.per_chunk;
   const int tc = min(p.per_chunk, p.T - t0);
-  const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
 
-  // The error word starts at 0 here; a wait can run out only after the work below, in any CTA.
-  if (MODE != DEC_DOWN && first_cta && tid == 0) *p.err = 0;
-  if constexpr (MODE == DEC_GATE_UP) pdl_launch_dependents();
+  if (MODE == DEC_GATE_UP && tid == 0) pdl_launch_dependents();
   if (tid == 0) {
-    for (int s = 0; s < DEC_MAX_A; ++s) {
-      mbar_init(&full_a[s], 1);
-      mbar_init(&empty_a[s], 1);
+    for (int s = 0; s < L.stages; ++s) {
+      mbar_init(&full[s], 2);
+      mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < DEC_MAX_B; ++s) {
-      mbar_init(&full_b[s], DEC_CONV_WARPS / L.nb);
-      mbar_init(&empty_b[s], 1);
-    }
-    mbar_init(done, 1);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 4);
     mbar_init(drained, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -297,46 +381,39 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     tmem_alloc(tmem_holder, DEC_TMEM_COLS);
     tmem_relinquish();
   }
-  if (warp >= 2) {   // unused columns hold zero codes, never stale bytes
-    for (int i = tid - 64; i < (L.nb * (L.b_stage + L.sfb_stage)) / 16; i += DEC_CONV_WARPS * 32) {
-      const int off = i * 16;
-      *reinterpret_cast<uint4*>(off < L.nb * L.b_stage ? smem + L.b + off : smem + L.sfb + (off - L.nb * L.b_stage)) =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
-    fence_proxy_async_smem();
-  }
 
-  // ---- routing: which tokens of the chunk chose which expert, and the list of chosen experts ----
+  // ---- routing: which tokens chose which expert, and the list of chosen experts ----
   int nact = 1;
   if constexpr (MODE != DEC_LINEAR) {
     for (int e = tid; e < p.E; e += DEC_THREADS) s_mask[e] = 0;
     __syncthreads();
-    for (int i = tid; i < tc * p.k; i += DEC_THREADS) {
-      const int e = __ldg(p.experts + static_cast<int64_t>(t0) * p.k + i);
-      if (e >= 0 && e < p.E) atomicOr(&s_mask[e], 1u << (i / p.k));
+    for (int i = tid; i < p.T * p.k; i += DEC_THREADS) {
+      const int e = __ldg(p.experts + i);
+      if (e >= 0 && e < p.E) atomicOr(reinterpret_cast<unsigned long long*>(&s_mask[e]), 1ull << (i / p.k));
     }
-    if (MODE == DEC_GATE_UP && first_cta)
-      for (int i = tid; i < p.T * p.k; i += DEC_THREADS)
-        if (__ldg(p.experts + i) >= p.E) atomicOr(p.err, ERR_EXPERT_RANGE);
     __syncthreads();
     if (warp == 0) {
-      int n = 0, rows = t0 * p.k;
+      const uint64_t mine = tc == 64 ? ~0ull : ((1ull << tc) - 1ull) << t0;
+      int n = 0, rows = 0;
       for (int base = 0; base < p.E; base += 32) {
-        const uint32_t m = base + lane < p.E ? s_mask[base + lane] : 0u;
-        const uint32_t act = __ballot_sync(0xFFFFFFFFu, m != 0);
-        int incl = __popc(m);
+        const uint64_t m = base + lane < p.E ? s_mask[base + lane] : 0ull;
+        const int pop = __popcll(m);
+        const int entries = MODE == DEC_GATE_UP ? (pop + GROUP - 1) / GROUP : (m & mine) != 0 ? 1 : 0;
+        if (__ballot_sync(0xFFFFFFFFu, pop != 0) == 0) continue;
+        int incl = pop | (entries << 16);   // two running sums in one word: rows < 2^12, entries < 2^12
         for (int d = 1; d < 32; d <<= 1) {
           const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
           if (lane >= d) incl += o;
         }
-        if (m != 0) {
-          const int pos = n + __popc(act & ((1u << lane) - 1u));
-          s_act_e[pos] = base + lane;
-          s_act_m[pos] = m;
-          s_act_off[pos] = rows + incl - __popc(m);
+        const int pos = n + (incl >> 16) - entries, off = rows + (incl & 0xFFFF) - pop;
+        for (int g = 0; g < entries; ++g) {
+          s_act_e[pos + g] = base + lane + 1024 * g;
+          s_act_m[pos + g] = m;
+          s_act_off[pos + g] = off;
         }
-        n += __popc(act);
-        rows += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        const int last = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        n += last >> 16;
+        rows += last & 0xFFFF;
       }
       if (lane == 0) *s_nact = n;
     }
@@ -347,283 +424,505 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   const uint32_t tmem = *tmem_holder;
   if constexpr (MODE != DEC_LINEAR) nact = *s_nact;
 
-  // ---- this CTA's tile and K range ----
-  int a0 = 0, tile = cluster;
-  if constexpr (MODE == DEC_GATE_UP) {
-    a0 = cluster / p.tiles;
-    tile = cluster - a0 * p.tiles;
-    if (a0 >= nact) {   // fewer experts were chosen than could be: the whole cluster leaves
-      if (warp == 1) tmem_dealloc(tmem, DEC_TMEM_COLS);
-      return;
+  // ---- this CTA's run of K steps ----
+  const int su = MODE == DEC_GATE_UP ? 2 * p.steps : MODE == DEC_DOWN ? nact * p.steps : p.steps;   // per unit
+  const int units = MODE == DEC_GATE_UP ? nact * p.tiles : p.tiles;
+  // More units than CTAs: whole units, the same number for every CTA (so that some CTAs may have none: it is
+  // the memory, not the number of SMs, that has to be filled).  Fewer: as many CTAs as fit for each unit.
+  const int slots = static_cast<int>(gridDim.x) / p.chunks, cta = static_cast<int>(blockIdx.x) / p.chunks;
+  const int per_cta = (units + slots - 1) / slots;
+  const int per_unit = units == 0 || units > slots ? 1 : max(1, min(slots / units, su / DEC_MIN_STEPS));
+  int s_begin = 0, n_steps = 0;
+  if (per_unit == 1) {
+    s_begin = min(cta * per_cta, units) * su;
+    n_steps = min((cta + 1) * per_cta, units) * su - s_begin;
+  } else if (cta < units * per_unit) {
+    const int u = cta / per_unit, o = cta - u * per_unit;
+    s_begin = u * su + su * o / per_unit;
+    n_steps = u * su + su * (o + 1) / per_unit - s_begin;
+  }
+  // DOWN without a single choice: no steps, and every output is zero
+  const bool nothing = MODE == DEC_DOWN && nact == 0;
+
+  // Columns of a unit's MMA: how many tokens, and which row of the operand is behind token column c in a
+  // step of list entry a (-1: zeros).
+  auto columns = [&](int a) {
+    if constexpr (MODE == DEC_GATE_UP)
+      return min(GROUP, __popcll(s_act_m[a]) - (s_act_e[a] >> 10) * GROUP);
+    else
+      return tc;
+  };
+  auto token = [&](int c, int a) { return nth_set_bit(s_act_m[a], (s_act_e[a] >> 10) * GROUP + c); };   // GATE_UP
+  auto source_row = [&](int c, int a) -> int {
+    if constexpr (MODE == DEC_GATE_UP) return c < columns(a) ? token(c, a) : -1;
+    if constexpr (MODE == DEC_LINEAR) return c < tc ? t0 + c : -1;
+    if (c >= tc || !((s_act_m[a] >> (t0 + c)) & 1ull)) return -1;
+    return s_act_off[a] + bits_below(s_act_m[a], t0 + c);
+  };
+  auto mma_columns = [&](int a) { return (P * columns(a) + 15) & ~15; };
+  // Place in the sequence: list entry, 128-row tile, K step, accumulator.  Divisions only to start with.
+  struct Place {
+    int a, tile, f, acc;
+  };
+  auto place_of = [&](int s) {
+    Place q{0, 0, 0, 0};
+    if (s >= units * su) return q;
+    const int u = s / su, r = s - u * su;
+    if constexpr (MODE == DEC_GATE_UP) {
+      q.a = u / p.tiles;
+      q.tile = u - q.a * p.tiles;
+      q.f = r >> 1;
+      q.acc = r & 1;
+    } else {
+      q.a = MODE == DEC_DOWN ? r / p.steps : 0;
+      q.tile = u;
+      q.f = r - q.a * p.steps;
     }
-  }
-  int ncol = tc;          // token columns
-  uint32_t mask0 = 0;
-  if constexpr (MODE == DEC_GATE_UP) {
-    mask0 = s_act_m[a0];
-    ncol = __popc(mask0);
-  }
-  const int tp = (ncol + 7) & ~7;
-  const int n_mma = (P * tp + 15) & ~15;
-  const int nat = (n_mma + 127) >> 7;    // scale atoms of B per MMA
-  const int ns = MODE == DEC_GATE_UP ? p.cs >> 1 : p.cs;
-  const int si = MODE == DEC_GATE_UP ? rank >> 1 : rank;
-  const int total = MODE == DEC_DOWN ? nact * p.steps : p.steps;
-  const int s_begin = static_cast<int>(static_cast<int64_t>(total) * si / ns);
-  const int n_steps = static_cast<int>(static_cast<int64_t>(total) * (si + 1) / ns) - s_begin;
+    return q;
+  };
+  auto advance = [&](Place& q) {
+    if constexpr (MODE == DEC_GATE_UP) {
+      q.acc ^= 1;
+      if (q.acc != 0 || ++q.f < p.steps) return;
+      q.f = 0;
+      if (++q.tile < p.tiles) return;
+      q.tile = 0;
+      ++q.a;
+    } else {
+      if (++q.f < p.steps) return;
+      q.f = 0;
+      if (MODE == DEC_DOWN && ++q.a < nact) return;
+      q.a = 0;
+      ++q.tile;
+    }
+  };
+  // Stage of the ring, and the parity of its current use.
+  struct Ring {
+    int slot;
+    uint32_t phase;
+  };
+  auto next_stage = [&](Ring& r) {
+    if (++r.slot == L.stages) {
+      r.slot = 0;
+      r.phase ^= 1u;
+    }
+  };
 
   if (warp == 0) {
-    // ---------------- weight copies (lane 0) ----------------
-    if (lane == 0) {
-      int a = MODE == DEC_DOWN && p.steps > 0 ? s_begin / p.steps : a0;
-      int f = s_begin - (MODE == DEC_DOWN ? a * p.steps : 0);
-      int issued = 0;
-      for (int i = 0; i < n_steps; ++i) {
-        const int slot = i % L.na;
-        if (i >= L.na && !dec_wait(&empty_a[slot], ((i / L.na) - 1) & 1, abort_flag, p, ERR_TIMEOUT_PRODUCER)) break;
-        int64_t row = static_cast<int64_t>(tile) * 128;
-        if constexpr (MODE == DEC_GATE_UP)
-          row += static_cast<int64_t>(s_act_e[a]) * 2 * p.F + static_cast<int64_t>(rank & 1) * p.F;
-        if constexpr (MODE == DEC_DOWN) row += static_cast<int64_t>(s_act_e[a]) * p.tiles * 128;
-        mbar_arrive_expect_tx(&full_a[slot], DEC_A_STAGE + ATOMS * 512);
-        tma_load_2d(smem + slot * DEC_A_STAGE, &tm, &full_a[slot], f * 128, static_cast<int32_t>(row));
-        bulk_load(smem + L.sfa + slot * ATOMS * 512,
-                  p.w_sf + ((row >> 7) * p.kt + static_cast<int64_t>(f) * ATOMS) * 512, ATOMS * 512, &full_a[slot]);
-        ++issued;
-        if (++f == p.steps) {
-          f = 0;
-          ++a;
+    // ---------------- copies: one lane issues them, all lanes look up the columns' rows ----------------
+    // Token columns to copy into a stage.  DOWN: those of the step's expert, and zeros where an earlier
+    // step of the stage left another expert's token (at first: anything).
+    const uint32_t all_columns = tc >= 32 ? 0xFFFFFFFFu : (1u << tc) - 1u;
+    auto step_columns = [&](int a, int slot) -> uint32_t {
+      if constexpr (MODE != DEC_DOWN) {
+        const int n = columns(a);
+        return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+      } else {
+        const uint32_t mine = static_cast<uint32_t>(s_act_m[a] >> t0) & all_columns;
+        const uint32_t cols = mine | s_dirty[slot];
+        s_dirty[slot] = mine;
+        return cols;
+      }
+    };
+    auto copy_weights = [&](const Place& q, int slot, uint32_t cols) {
+      int row = q.tile * 128;
+      if constexpr (MODE == DEC_GATE_UP) row += (s_act_e[q.a] & 1023) * 2 * p.F + q.acc * p.F;
+      if constexpr (MODE == DEC_DOWN) row += (s_act_e[q.a] & 1023) * p.tiles * 128;
+      mbar_arrive_expect_tx(&full[slot], DEC_A_STAGE + ATOMS * 512 +
+                                             (MODE == DEC_LINEAR ? p.per_chunk : __popc(cols)) * P * 128);
+      tma_load_2d(smem + slot * DEC_A_STAGE, &tm_w, &full[slot], q.f * 128, row);
+      bulk_load(smem + L.sfa + slot * ATOMS * 512,
+                p.w_sf + (static_cast<int64_t>(row >> 7) * p.kt + q.f * ATOMS) * 512, ATOMS * 512, &full[slot]);
+    };
+    int entry = -1;
+    auto set_rows = [&](int a) {   // the whole warp
+      if (MODE == DEC_LINEAR || a == entry) return;
+      entry = a;
+      __syncwarp();
+      if (lane < columns(a)) {
+        const int r = source_row(lane, a);
+        s_row[lane] = r < 0 ? p.zero_row : r;
+      }
+      __syncwarp();
+    };
+    auto copy_columns = [&](const Place& q, int slot, uint32_t cols) {
+      uint8_t* dst = smem + L.b + slot * L.b_stage;
+      if constexpr (MODE == DEC_LINEAR) {   // a box is a chunk's columns
+        tma_load_2d(dst, &tm_x, &full[slot], q.f * 128, t0 * P);
+      } else {                              // a box is a token's columns
+        for (; cols != 0; cols &= cols - 1u) {
+          const int c = __ffs(cols) - 1;
+          tma_load_2d(dst + c * (P * 128), &tm_x, &full[slot], q.f * 128, s_row[c] * P);
         }
       }
-      // every copy must have landed before the CTA may exit or its stages are reused
-      for (int i = max(0, issued - L.na); i < issued; ++i)
-        if (!mbar_wait_bounded(&full_a[i % L.na], (i / L.na) & 1, nullptr, p.drain_ns))
-          atomicOr(p.err, ERR_TIMEOUT_DRAIN);
+    };
+    // fill the ring with weights before waiting for the activations the previous kernel writes
+    const int fill = min(n_steps, L.stages);
+    int issued = 0;
+    Place q = place_of(s_begin);
+    if (elect_one()) {
+      Place w = q;
+      for (int i = 0; i < fill; ++i, advance(w)) {
+        s_dirty[i] = all_columns;
+        s_fill[i] = step_columns(w.a, i);
+        copy_weights(w, i, s_fill[i]);
+      }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---------------- scale copies and MMAs (lane 0) ----------------
-    if (lane == 0) {
-      const uint32_t idesc = FMT == DEC_NV ? idesc_nvf4(128, n_mma) : idesc_mxf8_e4m3(128, n_mma);
-      bool ok = true, any = false;
-      for (int i = 0; i < n_steps; ++i) {
-        const int slot = i % L.na, bs = i % L.nb;
-        if (!dec_wait(&full_a[slot], (i / L.na) & 1, abort_flag, p, ERR_TIMEOUT_MMA) ||
-            !dec_wait(&full_b[bs], (i / L.nb) & 1, abort_flag, p, ERR_TIMEOUT_MMA) ||
-            // the scale columns about to be overwritten were last read by step i - 2's MMAs
-            (i >= 2 && !dec_wait(&empty_a[(i - 2) % L.na], ((i - 2) / L.na) & 1, abort_flag, p, ERR_TIMEOUT_MMA))) {
-          ok = false;
+    pdl_wait();
+    for (; issued < fill; ++issued, advance(q)) {
+      set_rows(q.a);
+      if (elect_one()) copy_columns(q, issued, s_fill[issued]);
+    }
+    Ring r{0, 0};
+    for (; issued < n_steps; ++issued, advance(q), next_stage(r)) {
+      set_rows(q.a);
+      bool ok = true;
+      if (elect_one()) {
+        ok = dec_wait(&empty[r.slot], r.phase, abort_flag, p, ERR_TIMEOUT_PRODUCER);
+        if (ok) {
+          const uint32_t cols = step_columns(q.a, r.slot);
+          copy_weights(q, r.slot, cols);
+          copy_columns(q, r.slot, cols);
+        }
+      }
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+    }
+    __syncwarp();
+    // every copy must have landed before the CTA may exit; after a timeout elsewhere the barriers may lack
+    // their other arrival, and one full drain wait is enough for all the copies
+    if (lane == 0)
+      for (int i = max(0, issued - L.stages); i < issued; ++i)
+        if (!mbar_wait_bounded(&full[i % L.stages], (i / L.stages) & 1, nullptr, p.drain_ns)) {
+          atomicOr(p.err, ERR_TIMEOUT_DRAIN);
           break;
         }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- scale copies and MMAs (one lane) ----------------
+    if (elect_one()) {
+      // descriptors of stage 0: addresses are in units of 16 bytes in their low bits
+      const uint64_t desc_a = sdesc_kmajor_sw128(smem_u32(smem)), desc_b = sdesc_kmajor_sw128(smem_u32(smem + L.b));
+      const uint64_t desc_sfa = sdesc_sf_atom(smem_u32(smem + L.sfa)), desc_sfb = sdesc_sf_atom(smem_u32(smem + L.sfb));
+      bool ok = true, any = false;
+      Ring r{0, 0}, before{0, 0};   // the stage of step i and that of step i - sf_sets
+      int set = 0;
+      int i = 0;
+      for (int seg = 0; ok && i < n_steps; ++seg) {
+        const int u = (s_begin + i) / su, i_end = min(n_steps, (u + 1) * su - s_begin);
+        const int n_mma = mma_columns(MODE == DEC_GATE_UP ? u / p.tiles : 0), nat = (n_mma + 127) >> 7;
+        const uint32_t idesc = FMT == DEC_NV ? idesc_nvf4(128, n_mma) : idesc_mxf8_e4m3(128, n_mma);
+        uint32_t started = 0;   // accumulators that hold something
+        if (seg > 0 && !dec_wait(acc_empty, (seg - 1) & 1, abort_flag, p, ERR_TIMEOUT_MMA)) break;
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + slot * DEC_A_STAGE), sb = smem_u32(smem + L.b + bs * L.b_stage);
-        const uint32_t sfa = smem_u32(smem + L.sfa + slot * ATOMS * 512);
-        const uint32_t sfb = smem_u32(smem + L.sfb + bs * L.sfb_stage);
-        const uint32_t t_sfa = tmem + DEC_SFA_COL + (i & 1) * 16, t_sfb = tmem + DEC_SFB_COL + (i & 1) * 32;
+        for (; i < i_end; ++i, next_stage(r)) {
+          const int slot = r.slot;
+          if (!dec_wait(&full[slot], r.phase, abort_flag, p, ERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          // the scale columns about to be overwritten were last read by step i - sf_sets's MMAs (known to
+          // be over when that step used this stage)
+          if (i >= L.sf_sets && L.sf_sets < L.stages) {
+            if (!dec_wait(&empty[before.slot], before.phase, abort_flag, p, ERR_TIMEOUT_MMA)) {
+              ok = false;
+              break;
+            }
+            next_stage(before);
+          }
+          tc_fence_after();
+          const uint64_t da = desc_a + slot * (DEC_A_STAGE >> 4), db = desc_b + slot * (L.b_stage >> 4);
+          const uint64_t dsa = desc_sfa + slot * (ATOMS * 32), dsb = desc_sfb + slot * (L.sfb_stage >> 4);
+          const uint32_t t_sfa = tmem + L.sf_col + set * L.sf_cols, t_sfb = t_sfa + 4 * ATOMS;
+          if (++set == L.sf_sets) set = 0;
+          const int acc = MODE == DEC_GATE_UP ? (s_begin + i - u * su) & 1 : 0;
+          const uint32_t d = tmem + acc * L.n_max;
 #pragma unroll
-        for (int m = 0; m < ATOMS; ++m) {
-          tc_copy_sf(t_sfa + 4 * m, sdesc_sf_atom(sfa + 512 * m));
-          for (int j = 0; j < nat; ++j)
-            tc_copy_sf(t_sfb + 8 * m + 4 * j, sdesc_sf_atom(sfb + 512 * (m * nat + j)));
-        }
+          for (int m = 0; m < ATOMS; ++m) {
+            tc_copy_sf(t_sfa + 4 * m, dsa + 32 * m);
+            for (int j = 0; j < nat; ++j)
+              tc_copy_sf(t_sfb + 4 * (m * nat + j), dsb + 32 * (m * nat + j));
+          }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (FMT == DEC_NV)
-            tc_mma_nvf4(tmem, sdesc_kmajor_sw128(sa + 32 * k), sdesc_kmajor_sw128(sb + 32 * k), idesc, t_sfa + 4 * k,
-                        t_sfb + 8 * k, (i | k) != 0 ? 1u : 0u);
-          else
-            tc_mma_mxf8(tmem, sdesc_kmajor_sw128(sa + 32 * k), sdesc_kmajor_sw128(sb + 32 * k),
-                        idesc_with_sf_id(idesc, k), t_sfa, t_sfb, (i | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t add = ((started >> acc) & 1u) | (k != 0 ? 1u : 0u);
+            if constexpr (FMT == DEC_NV)
+              tc_mma_nvf4(d, da + 2 * k, db + 2 * k, idesc, t_sfa + 4 * k, t_sfb + 4 * nat * k, add);
+            else
+              tc_mma_mxf8(d, da + 2 * k, db + 2 * k, idesc_with_sf_id(idesc, k), t_sfa, t_sfb, add);
+          }
+          started |= 1u << acc;
+          tc_commit(&empty[slot]);
+          any = true;
         }
-        tc_commit(&empty_a[slot]);
-        tc_commit(&empty_b[bs]);
-        any = true;
+        if (ok) tc_commit(acc_full);
       }
-      if (ok && any) tc_commit(done);
-      else if (ok) mbar_arrive(done);
       if (any) {
         tc_commit(drained);
         if (!mbar_wait_bounded(drained, 0, nullptr, p.drain_ns)) atomicOr(p.err, ERR_TIMEOUT_DRAIN);
       }
     }
     __syncwarp();
-  } else {
-    // ---------------- activations -> columns of the MMA ----------------
-    const int cw = warp - 2, ct = tid - 64;
-    if constexpr (MODE == DEC_DOWN) pdl_wait();   // h is GATE_UP's
-    if constexpr (MODE == DEC_GATE_UP) {
-      if (ct < ncol) {
-        uint32_t m = mask0;
-        for (int i = 0; i < ct; ++i) m &= m - 1u;
-        const int t = __ffs(m) - 1;
-        s_tok[ct] = t;
-        // a token that lists the expert more than once: the weights add
-        float w = 0.0f;
-        for (int j = 0; j < p.k; ++j) {
-          const int64_t q = static_cast<int64_t>(t0 + t) * p.k + j;
-          if (__ldg(p.experts + q) == s_act_e[a0]) w += p.gates != nullptr ? __ldg(p.gates + q) : 1.0f;
-        }
-        s_gate[ct] = w;
-      }
-      conv_barrier();
-    }
-    // row of x (or of h, -1 where the token did not choose expert a) behind column c
-    auto src_row = [&](int c, int a) -> int64_t {
-      if constexpr (MODE == DEC_GATE_UP) return t0 + s_tok[c];
-      if constexpr (MODE == DEC_LINEAR) return t0 + c;
-      const uint32_t m = s_act_m[a];
-      return (m >> c) & 1u ? s_act_off[a] + __popc(m & ((1u << c) - 1u)) : -1;
+  } else if (warp < DEC_FIRST_EPI_WARP) {
+    // ---------------- the columns' scales: warp cw takes steps cw, cw + 2, ...; lane = token column ----------------
+    // Fewer warps than stages: when a warp waits for a slot's last use, the use before that one is known
+    // to be over, as a wait by parity requires.
+    const int cw = warp - 2;
+    pdl_wait();
+    // MXFP8, and NVFP4 with more than eight tokens: lane = token column, all its words; NVFP4 with up to
+    // eight: lane = (word, token), one of the token's four words.
+    const bool spread = FMT == DEC_NV && tc <= 8 && MODE != DEC_GATE_UP;
+    struct Scales {
+      uint32_t e[ATOMS];
+      int c, row, top, n, nat;   // token column and its operand row (-1: zero), columns, atoms per MMA
     };
-    if constexpr (FMT == DEC_NV) {
-      // exponent of each column's largest magnitude over this CTA's K range: one scale per column
-      // and CTA (the ranges' partial sums are added after scaling)
-      for (int c = cw; c < ncol; c += DEC_CONV_WARPS) {
-        uint32_t m = 0;
-        if constexpr (MODE == DEC_DOWN) {
-          const int tiles32 = p.F / 32;
-          for (int s = s_begin; s < s_begin + n_steps;) {
-            const int a = s / p.steps, f = s - a * p.steps;
-            const int nf = min(p.steps - f, s_begin + n_steps - s);
-            const int64_t r = src_row(c, a);
-            if (r >= 0)
-              for (int i = f * 8 + lane; i < min((f + nf) * 8, tiles32); i += 32)
-                m = max(m, __float_as_uint(p.hmax[r * tiles32 + i]));
-            s += nf;
-          }
-        } else {
-          const uint16_t* xr = p.x + src_row(c, 0) * p.K;
-          const int k1 = min((s_begin + n_steps) * KSTEP, p.K);
-          for (int k = s_begin * KSTEP + lane * 8; k < k1; k += 256) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(xr + k));
-            const uint32_t q = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                        __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-            m = max(m, max(q & 0xFFFFu, q >> 16) << 16);
-          }
-        }
-        m = __reduce_max_sync(0xFFFFFFFFu, m);
-        if (lane == 0) s_emax[c] = block_exponent(m);
-      }
+    int top = 0;
+    if (FMT == DEC_NV && MODE != DEC_GATE_UP) {
+      const int c = spread ? lane & 7 : lane;
+      if (c < tc) top = p.in.top[t0 + c];   // one reference per token for all its experts: they share the accumulator
     }
-    if constexpr (FMT == DEC_NV) conv_barrier();   // s_emax
-
-    const int group = cw % L.nb, sub = cw / L.nb, nsub = DEC_CONV_WARPS / L.nb;   // ring slot = group
-    const int g = lane & 15;
-    for (int i = group; i < n_steps; i += L.nb) {
-      if (i >= L.nb &&
-          !dec_warp_wait(&empty_b[group], ((i / L.nb) - 1) & 1, abort_flag, p, ERR_TIMEOUT_SF, lane))
-        break;
-      uint8_t* sB = smem + L.b + group * L.b_stage;
-      uint8_t* sSF = smem + L.sfb + group * L.sfb_stage;
-      const int s = s_begin + i;
-      const int a = MODE == DEC_DOWN ? s / p.steps : a0;
-      const int f = MODE == DEC_DOWN ? s - a * p.steps : s;
-      for (int c0 = 2 * sub; c0 < ncol; c0 += 2 * nsub) {
-        const int c = c0 + (lane >> 4);
-        const int64_t r = c < ncol ? src_row(c, a) : -1;
-        if constexpr (FMT == DEC_MX) {
-          float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          if (r >= 0) {
-            const int64_t o = r * p.K + f * KSTEP + g * 8;
-            if constexpr (MODE == DEC_DOWN) {
-              const float4 u0 = *reinterpret_cast<const float4*>(p.h + o);
-              const float4 u1 = *reinterpret_cast<const float4*>(p.h + o + 4);
-              v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
-              v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
-            } else {
-              unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + o)), v);
-            }
-          }
-          put_pieces_mx<P>(v, sB, sSF, c < ncol ? c : -1, tp, g);
+    int entry = -1;
+    Scales cur{}, next{};
+    auto load = [&](const Place& q, Scales& v) {
+      if (q.a != entry) {
+        entry = q.a;
+        v.c = spread ? lane & 7 : lane;
+        v.row = source_row(v.c, q.a);
+        v.n = columns(q.a);
+        v.nat = (mma_columns(q.a) + 127) >> 7;
+        if (FMT == DEC_NV && MODE == DEC_GATE_UP && v.row >= 0) top = p.in.top[v.row];
+        v.top = top;
+      }
+      if (v.row < 0) return;
+      const uint8_t* src = p.in.exps + (static_cast<int64_t>(v.row) * p.steps + q.f) * EB;
+      if constexpr (FMT == DEC_NV) {
+        if (spread) {
+          v.e[0] = (q.f * 4 + (lane >> 3)) * 64 < p.K ? *reinterpret_cast<const uint32_t*>(src + (lane >> 3) * 4) : 0u;
         } else {
-          float v[16];
+          const uint4 w = *reinterpret_cast<const uint4*>(src);
+          v.e[0] = w.x; v.e[1] = w.y; v.e[2] = w.z; v.e[3] = w.w;
 #pragma unroll
-          for (int q = 0; q < 16; ++q) v[q] = 0.0f;
-          const int kk = f * KSTEP + g * 16;
-          if (r >= 0 && kk < p.K) {
-            const int64_t o = r * p.K + kk;
-            if constexpr (MODE == DEC_DOWN) {
+          for (int m = 0; m < 4; ++m)   // blocks past the row's end
+            if ((q.f * 4 + m) * 64 >= p.K) v.e[m] = 0;
+        }
+      } else {
+        v.e[0] = *reinterpret_cast<const uint32_t*>(src);
+      }
+    };
+    // word of atom m for column col
+    auto word = [&](uint8_t* sf, int nat, int m, int col) {
+      return reinterpret_cast<uint32_t*>(sf + (m * nat + (col >> 7)) * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4);
+    };
+    Place q = place_of(s_begin + cw);
+    if (cw < n_steps) load(q, cur);
+    int slot = cw;
+    uint32_t phase = 1;   // parity of the slot's previous use
+    for (int i = cw; i < n_steps; i += DEC_SCALE_WARPS) {
+      next = cur;
+      if (i + DEC_SCALE_WARPS < n_steps) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float4 u = *reinterpret_cast<const float4*>(p.h + o + 4 * q);
-                v[4 * q] = u.x; v[4 * q + 1] = u.y; v[4 * q + 2] = u.z; v[4 * q + 3] = u.w;
-              }
-            } else {
-              unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + o)), v);
-              unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + o + 8)), v + 8);
-            }
+        for (int z = 0; z < DEC_SCALE_WARPS; ++z) advance(q);
+        load(q, next);
+      }
+      uint32_t w[ATOMS];   // a zero column: 2^-127 (MXFP8) or 0
+      if constexpr (FMT == DEC_NV) {
+        const uint32_t live = cur.row >= 0 ? 0xFFFFFFFFu : 0u;
+        w[0] = nv_scales(cur.e[0], cur.top) & live;
+        if (!spread)
+#pragma unroll
+          for (int m = 1; m < 4; ++m) w[m] = nv_scales(cur.e[m], cur.top) & live;
+      }
+      if (i >= L.stages && !dec_warp_wait(&empty[slot], phase, abort_flag, p, ERR_TIMEOUT_SF, lane)) break;
+      uint8_t* sf = smem + L.sfb + slot * L.sfb_stage;
+      if (cur.c < cur.n) {
+#pragma unroll
+        for (int d = 0; d < P; ++d) {
+          const int col = cur.c * P + d;
+          if constexpr (FMT == DEC_MX) {
+            *word(sf, 1, 0, col) = cur.row >= 0 ? mx_scales(cur.e[0], d) : 0u;
+          } else if (spread) {
+            *word(sf, 1, lane >> 3, col) = w[0];
+          } else {
+            uint32_t* dst = word(sf, cur.nat, 0, col);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) dst[m * cur.nat * 128] = w[m];
           }
-          if (c < ncol) put_pieces_nv<P>(v, s_emax[c], sB, sSF, nat, c, tp, g);
         }
       }
       fence_proxy_async_smem();   // the tensor core reads these bytes through the async proxy
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full_b[group]);
+      if (lane == 0) mbar_arrive(&full[slot]);
+      cur = next;
+      slot += DEC_SCALE_WARPS;
+      if (slot >= L.stages) {
+        slot -= L.stages;
+        phase ^= 1u;
+      }
     }
+  } else {
+    // ---------------- epilogue ----------------
+    pdl_wait();
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    float alpha = 1.0f;
+    if constexpr (FMT == DEC_NV) alpha = 1.0f / nv_encode_scale(__ldg(p.w_amax));
 
-    // ---------------- accumulator -> this CTA's partial sums [column][128 rows] ----------------
-    if (dec_warp_wait(done, 0, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane)) {
-      tc_fence_after();
-      const int quarter = warp & 3, row = quarter * 32 + lane;
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      float* part = reinterpret_cast<float*>(smem);   // the weight ring: all its copies have been consumed
-      float alpha = 1.0f;
-      if constexpr (FMT == DEC_NV) alpha = 1.0f / nv_encode_scale(__ldg(p.w_amax));
-      for (int c0 = 0; c0 < ncol; c0 += 8) {
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (n_steps > 0) {
-          uint32_t d[P][8];
+    // y (DOWN, LINEAR) or h (GATE_UP) of token column c and this thread's row of the tile
+    auto put_out = [&](int c, int tile, float v) {
+      p.out[static_cast<int64_t>(t0 + c) * p.tiles * 128 + tile * 128 + row] =
+          static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+    };
+    auto put_h = [&](int c, int t, int a, int tile, float gate, float gs, float us) {
+      const float hv = gate * (gs / (1.0f + expf(-gs))) * us;
+      // h -> columns of DOWN: a block is the warp's 32 rows (MXFP8) or one half of them (NVFP4)
+      constexpr int PH = dec_pieces(FMT, DEC_DOWN);
+      const int64_t hr = s_act_off[a] + (s_act_e[a] >> 10) * GROUP + c;
+      const int k = tile * 128 + row;   // value of h
+      uint32_t m = __float_as_uint(hv) & 0x7FFFFFFFu;
+      if constexpr (FMT == DEC_MX) {
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+      } else {
 #pragma unroll
-          for (int q = 0; q < P; ++q) tmem_ld_32x32b_x8(t_row + q * tp + c0, d[q]);
+        for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+      }
+      const int eb = block_exponent(m);
+      if ((lane & (FMT == DEC_NV ? 15 : 31)) == 0)
+        p.h.exps[hr * p.h_steps * EB + (FMT == DEC_NV ? k >> 4 : k >> 5)] = static_cast<uint8_t>(eb + 127);
+      const float inv = block_multiplier<FMT>(eb);
+      uint64_t r = f2_pack(hv * inv, 0.0f);
+      uint8_t* dst = p.h.codes + hr * PH * p.h_steps * 128 + (FMT == DEC_NV ? k >> 1 : k);
+#pragma unroll
+      for (int q = 0; q < PH; ++q, dst += p.h_steps * 128) {
+        const uint64_t n = q + 1 < PH ? next_piece<FMT, false>(r) : next_piece<FMT, true>(r);
+        if constexpr (FMT == DEC_MX) {
+          *dst = static_cast<uint8_t>(e4m3x2_f2(n) & 0xFFu);
+        } else {
+          const float other = __shfl_down_sync(0xFFFFFFFFu, f2_lo(n), 1);
+          const uint32_t code = e2m1x8(f2_lo(n), other, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f) & 0xFFu;
+          if ((lane & 1) == 0) *dst = static_cast<uint8_t>(code);
+        }
+      }
+      if constexpr (FMT == DEC_NV) {
+        const int top = __reduce_max_sync(0xFFFFFFFFu, eb);
+        if (lane == 0) atomicMax(p.h.top + t, top);
+      }
+    };
+
+    if (nothing && cta < p.tiles)
+      for (int tile = cta; tile < p.tiles; tile += static_cast<int>(gridDim.x) / p.chunks)
+        for (int c = 0; c < tc; ++c) put_out(c, tile, 0.0f);
+
+    int i = 0, top = 0;
+    for (int seg = 0; i < n_steps; ++seg) {
+      const int u = (s_begin + i) / su, r0 = s_begin + i - u * su;
+      const int i_end = min(n_steps, (u + 1) * su - s_begin), r1 = r0 + i_end - i;
+      const int a = MODE == DEC_GATE_UP ? u / p.tiles : 0, tile = MODE == DEC_GATE_UP ? u - a * p.tiles : u;
+      const int nc = columns(a);
+      // lane c: token and routing weight of token column c (a token that lists the expert twice adds its
+      // weights), and the exponent its scales refer to
+      float gate = 0.0f;
+      int tok = lane < tc ? t0 + lane : 0;
+      if constexpr (MODE == DEC_GATE_UP) {
+        if (lane < nc) {
+          tok = token(lane, a);
+          for (int q = 0; q < p.k; ++q)
+            if (__ldg(p.experts + tok * p.k + q) == (s_act_e[a] & 1023))
+              gate += p.gates != nullptr ? __ldg(p.gates + tok * p.k + q) : 1.0f;
+        }
+      }
+      if (FMT == DEC_NV && (MODE == DEC_GATE_UP || seg == 0)) top = lane < nc ? p.in.top[tok] : 0;
+      // the parts of the CTAs that share the unit
+      const bool whole = per_unit == 1;
+      auto part_of = [&](int o) {
+        return p.part + static_cast<int64_t>((u * per_unit + o) * p.chunks + chunk) * p.part_slot + row;
+      };
+
+      if (!dec_warp_wait(acc_full, seg & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane)) break;
+      tc_fence_after();
+      const bool has[2] = {MODE != DEC_GATE_UP || r1 - r0 > 1 || (r0 & 1) == 0, r1 - r0 > 1 || (r0 & 1) == 1};
+      for (int c0 = 0; c0 < nc; c0 += 8) {
+        float v[ACCS][8];
+#pragma unroll
+        for (int b = 0; b < ACCS; ++b) {
+          uint32_t d[8 * P];
+#pragma unroll
+          for (int q = 0; q < P; ++q) tmem_ld_32x32b_x8(t_row + b * L.n_max + c0 * P + q * 8, d + q * 8);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            v[j] = __uint_as_float(d[P - 1][j]);
+            float x = __uint_as_float(d[j * P + P - 1]);
 #pragma unroll
             for (int q = P - 2; q >= 0; --q)   // smallest first; a digit's place is 1/8 of the one before
-              v[j] = FMT == DEC_NV ? fmaf(v[j], 0.125f, __uint_as_float(d[q][j])) : v[j] + __uint_as_float(d[q][j]);
+              x = FMT == DEC_NV ? fmaf(x, 0.125f, __uint_as_float(d[j * P + q])) : x + __uint_as_float(d[j * P + q]);
+            if constexpr (FMT == DEC_NV) x = ldexpf(x * alpha, __shfl_sync(0xFFFFFFFFu, top, c0 + j) - 9);
+            v[b][j] = has[b] ? x : 0.0f;
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c0 + j < ncol)
-            part[(c0 + j) * 128 + row] =
-                FMT == DEC_NV ? ldexpf(v[j] * alpha, s_emax[c0 + j] - 9) : v[j];
+        for (int j = 0; j < 8; ++j) {
+          const int c = c0 + j;
+          if (c >= nc) break;
+          if (!whole) {
+#pragma unroll
+            for (int b = 0; b < ACCS; ++b) part_of(cta - u * per_unit)[(b * nc + c) * 128] = v[b][j];
+          } else if constexpr (MODE == DEC_GATE_UP) {
+            put_h(c, __shfl_sync(0xFFFFFFFFu, tok, c), a, tile, __shfl_sync(0xFFFFFFFFu, gate, c), v[0][j],
+                  v[ACCS - 1][j]);
+          } else {
+            put_out(c, tile, v[0][j]);
+          }
+        }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      if (!whole) {
+        int before = 0;
+        if (lane == 0) {
+          __threadfence();
+          before = atomicAdd(p.counters + (static_cast<int64_t>(chunk) * units + u) * 4 + quarter, 1);
+          __threadfence();
+        }
+        if (__shfl_sync(0xFFFFFFFFu, before, 0) == per_unit - 1) {
+          // 4 tokens x 4 parts of loads in flight; added in the order of the parts
+          constexpr int TB = 4, OB = 4;
+          for (int c0 = 0; c0 < nc; c0 += TB) {
+            float v[TB][ACCS] = {};
+            for (int o0 = 0; o0 < per_unit; o0 += OB) {
+              float x[OB][TB][ACCS];
+#pragma unroll
+              for (int o = 0; o < OB; ++o) {
+                const float* src = part_of(min(o0 + o, per_unit - 1));
+#pragma unroll
+                for (int j = 0; j < TB; ++j)
+#pragma unroll
+                  for (int b = 0; b < ACCS; ++b)
+                    x[o][j][b] = o0 + o < per_unit && c0 + j < nc ? __ldcg(src + (b * nc + c0 + j) * 128) : 0.0f;
+              }
+#pragma unroll
+              for (int o = 0; o < OB; ++o)
+#pragma unroll
+                for (int j = 0; j < TB; ++j)
+#pragma unroll
+                  for (int b = 0; b < ACCS; ++b) v[j][b] += x[o][j][b];
+            }
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+              if (c0 + j >= nc) break;
+              if constexpr (MODE == DEC_GATE_UP)
+                put_h(c0 + j, __shfl_sync(0xFFFFFFFFu, tok, c0 + j), a, tile, __shfl_sync(0xFFFFFFFFu, gate, c0 + j),
+                      v[j][0], v[j][ACCS - 1]);
+              else
+                put_out(c0 + j, tile, v[j][0]);
+            }
+          }
+        }
+      }
+      i = i_end;
     }
   }
   tc_fence_before();
-  __syncwarp();
-  cluster_sync_all();
-
-  // ---------------- sum over the cluster's K ranges, finish columns rank, rank + cs, ... ----------------
-  if (warp >= 2) {
-    const int row = (warp & 3) * 32 + lane;
-    const float* part = reinterpret_cast<const float*>(smem);
-    for (int c = rank; c < ncol; c += p.cs) {
-      const float* mine = part + c * 128 + row;
-      if constexpr (MODE == DEC_GATE_UP) {
-        float gs = 0.0f, us = 0.0f;
-        for (int q = 0; q < ns; ++q) {
-          gs += ld_cluster_f32(map_to_cta(mine, 2 * q));
-          us += ld_cluster_f32(map_to_cta(mine, 2 * q + 1));
-        }
-        const float hv = s_gate[c] * (gs / (1.0f + expf(-gs))) * us;
-        const int64_t hr = s_act_off[a0] + c;
-        p.h[hr * p.F + tile * 128 + row] = hv;
-        if constexpr (FMT == DEC_NV) {
-          const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(hv) & 0x7FFFFFFFu);
-          if (lane == 0) p.hmax[hr * (p.F / 32) + tile * 4 + (warp & 3)] = __uint_as_float(m);
-        }
-      } else {
-        float v = 0.0f;
-        for (int q = 0; q < ns; ++q) v += ld_cluster_f32(map_to_cta(mine, q));
-        p.out[static_cast<int64_t>(t0 + c) * p.tiles * 128 + tile * 128 + row] =
-            static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
-      }
-    }
-  }
-  __syncwarp();
-  cluster_sync_all();   // no CTA leaves while another reads its partial sums
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, DEC_TMEM_COLS);
@@ -643,8 +942,8 @@ uint64_t dec_wait_ns() {
   return (end != nullptr && *end == 0 && n > 0) ? static_cast<uint64_t>(n) : kDecWaitNs;
 }
 
-// 2-D byte matrix [rows, cols] (row pitch = cols) in boxes of 128 rows x 128 bytes, 128-byte swizzle.
-bool make_weight_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
+// 2-D byte matrix [rows, cols] (row pitch = cols) in boxes of box_rows rows x 128 bytes, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   static std::atomic<void*> entry{nullptr};
   void* fn = entry.load(std::memory_order_acquire);
   if (fn == nullptr) {
@@ -656,7 +955,7 @@ bool make_weight_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t c
   }
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols};
-  const cuuint32_t box[2] = {128, 128}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
              m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -665,99 +964,171 @@ bool make_weight_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t c
 
 constexpr int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
-// Shared memory for chunks of `tokens` tokens; false when fewer than 3 weight stages fit.
-bool dec_layout(int fmt, int mode, int tokens, int E, int nact, DecLayout* out) {
-  const int n = round_up(dec_pieces(fmt, mode) * round_up(tokens, 8), 16);
+// Shared memory for units of `tokens` token columns: half an SM with at least four stages, else a whole one.
+bool dec_layout(int fmt, int mode, int tokens, int E, int max_active, DecLayout* out) {
+  const int n = round_up(dec_pieces(fmt, mode) * tokens, 16);
   DecLayout L{};
   L.b_stage = n * 128;
   L.sfb_stage = dec_atoms(fmt) * ((n + 127) / 128) * 512;
-  // four activation stages (one per conversion warp) unless they would take the weights' room
-  L.nb = 4 * (L.b_stage + L.sfb_stage) <= 40 * 1024 ? 4 : 2;
-  const int misc = 3 * DEC_CHUNK * 4 + (mode == DEC_LINEAR ? 0 : E * 4 + nact * 12);
-  const int fixed = L.nb * (L.b_stage + L.sfb_stage) + 256 + round_up(misc, 16);
-  const int sfa = dec_atoms(fmt) * 512;
-  L.na = std::min(DEC_MAX_A, (DEC_SMEM - 1024 - fixed) / (DEC_A_STAGE + sfa));
-  if (L.na < 3) return false;
-  L.b = L.na * DEC_A_STAGE;
-  L.sfb = L.b + L.nb * L.b_stage;
-  L.sfa = L.sfb + L.nb * L.sfb_stage;
-  L.bars = L.sfa + L.na * sfa;
-  L.misc = L.bars + 256;
+  const int sfa = dec_atoms(fmt) * 512, bars = 384;
+  const int fixed = 1024 + bars + 256 + (mode == DEC_LINEAR ? 0 : round_up(E * 8 + max_active * 16, 16));
+  const int stage = DEC_A_STAGE + sfa + L.b_stage + L.sfb_stage;
+  L.n_max = n;
+  L.sf_col = round_up((mode == DEC_GATE_UP ? 2 : 1) * n, 4);
+  L.sf_cols = 4 * dec_atoms(fmt) * (1 + (n + 127) / 128);
+  L.smem = DEC_SMEM_HALF;
+  if ((L.smem - fixed) / stage < 4) L.smem = DEC_SMEM_FULL;
+  L.stages = std::min(DEC_MAX_STAGES, (L.smem - fixed) / stage);
+  L.sf_sets = std::min(L.stages, (static_cast<int>(DEC_TMEM_COLS) - L.sf_col) / L.sf_cols);
+  if (L.stages < 3 || L.sf_sets < 2) return false;
+  L.b = L.stages * DEC_A_STAGE;
+  L.sfb = L.b + L.stages * L.b_stage;
+  L.sfa = L.sfb + L.stages * L.sfb_stage;
+  L.bars = L.sfa + L.stages * sfa;
+  L.misc = L.bars + bars;
   *out = L;
   return true;
 }
+static_assert(2 * DEC_MAX_STAGES * 8 + 3 * 8 + 16 <= 384, "barriers and flags");
 
-// Per-device set-up of one kernel instance: dynamic shared memory, and the carve-out that lets two
-// CTAs share an SM.
+// Per-device set-up of one kernel instance (dynamic shared memory, and the carve-out that lets two CTAs
+// share an SM); returns the number of SMs, 0 on failure.
 template <int FMT, int MODE>
-bool dec_setup() {
+int dec_setup() {
   constexpr int kMaxDevices = 64;
-  static std::atomic<bool> done[kMaxDevices] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-  if (done[dev]) return true;
-  if (cudaFuncSetAttribute(k_decode<FMT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, DEC_SMEM) != cudaSuccess ||
+  static std::atomic<int> sms[kMaxDevices] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  if ((n = sms[dev].load()) > 0) return n;
+  if (cudaFuncSetAttribute(k_decode<FMT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, DEC_SMEM_FULL) !=
+          cudaSuccess ||
       cudaFuncSetAttribute(k_decode<FMT, MODE>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-    return false;
-  done[dev] = true;
-  return true;
+                           cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  sms[dev].store(n);
+  return n;
 }
+
+// Launch configuration: may start while the kernel before it in the stream ends (the kernels wait for
+// that one themselves).
+struct DecLaunch {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg;
+  DecLaunch(int grid, int threads, int smem, cudaStream_t stream) : cfg{} {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
 
 template <int FMT, int MODE>
-bool dec_launch(const CUtensorMap& tm, const DecParams& p, int clusters, int chunks, bool dependent,
-                cudaStream_t stream) {
-  if (!dec_setup<FMT, MODE>()) return false;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters) * p.cs, static_cast<unsigned>(chunks), 1);
-  cfg.blockDim = dim3(DEC_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = DEC_SMEM;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_decode<FMT, MODE>, tm, p) == cudaSuccess;
-}
-
-// CTAs that share one 128-row tile's K steps: as many (1, 2, 4, 8) as keep at least `min_steps` steps
-// each while the grid has fewer than two CTAs per SM on average.
-int dec_split(int64_t tiles, int64_t steps, int max_split, int min_steps) {
-  int ns = 1;
-  while (2 * ns <= max_split && tiles * ns < 2 * 304 && steps >= static_cast<int64_t>(2 * ns) * min_steps) ns *= 2;
-  return ns;
-}
-
-// Chunks of equal size (at most DEC_CHUNK tokens, fewer where their shared memory does not fit).
-bool dec_chunks(int fmt, int mode, int T, int k, int E, DecLayout* L, int* per_chunk, int* chunks) {
-  for (int cap = DEC_CHUNK; cap >= 8; cap -= 8) {
-    *chunks = (T + cap - 1) / cap;
-    *per_chunk = (T + *chunks - 1) / *chunks;
-    if (dec_layout(fmt, mode, *per_chunk, E, std::min(E, *per_chunk * k), L)) return true;
-  }
-  return false;
+bool dec_launch(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const DecParams& p, int ctas, cudaStream_t stream) {
+  DecLaunch l(ctas, DEC_THREADS, p.L.smem, stream);
+  return cudaLaunchKernelEx(&l.cfg, k_decode<FMT, MODE>, tm_w, tm_x, p) == cudaSuccess;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 constexpr size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-struct DecWs {
-  size_t h, hmax, total;
+// Columns of `rows` rows of K values in `pieces` pieces each, from byte `at` of a workspace.
+struct DecOperandLayout {
+  size_t codes, exps, top, end;
+  int64_t code_rows, steps;
+  int pieces;
 };
-bool dec_ws_layout(int64_t T, int k, int64_t H, int64_t F, int E, DecWs* out) {
-  if (T < 0 || T > DEC_MAX_TOKENS || k < 1 || k > DEC_MAX_K || E < 1 || E > 1024 || H <= 0 || F <= 0 || F > INT32_MAX)
+DecOperandLayout dec_operand(int fmt, int pieces, size_t at, int64_t rows, int64_t K) {
+  DecOperandLayout o{};
+  o.pieces = pieces;
+  o.steps = (K + dec_step_values(fmt) - 1) / dec_step_values(fmt);
+  o.code_rows = (rows + 1) * pieces;
+  o.codes = at;
+  o.exps = align256(o.codes + static_cast<size_t>(o.code_rows) * o.steps * 128);
+  o.top = align256(o.exps + static_cast<size_t>(rows) * o.steps * dec_exp_bytes(fmt));
+  o.end = align256(o.top + DEC_MAX_TOKENS * sizeof(int));
+  return o;
+}
+DecOperand dec_pointers(uint8_t* base, const DecOperandLayout& o) {
+  return {base + o.codes, base + o.exps, reinterpret_cast<int*>(base + o.top)};
+}
+
+// Workspace sizes do not depend on the device: room for the parts of at most this many CTAs.
+constexpr int DEC_MAX_CTAS = 320;
+
+// Workspace: error word (256 bytes), columns of x, columns of h, counters, parts.
+struct DecWs {
+  DecOperandLayout x, h;
+  size_t counters, part, end;
+  int64_t n_up, n_down;   // counters of the two kernels
+  int max_active;
+};
+bool dec_ws_layout(int fmt, int64_t T, int k, int64_t H, int64_t F, int E, DecWs* out) {
+  if (T < 0 || T > DEC_MAX_TOKENS || k < 1 || k > DEC_MAX_K || E < 1 || E > 1024 || H <= 0 || F <= 0 ||
+      H > INT32_MAX || F > INT32_MAX)
     return false;
   DecWs w{};
-  w.h = 256;
-  w.hmax = align256(w.h + static_cast<size_t>(T) * k * F * sizeof(float));
-  w.total = align256(w.hmax + static_cast<size_t>(T) * k * ((F + 31) / 32) * sizeof(float));
+  w.max_active = static_cast<int>(std::min<int64_t>(E, T * k) + T * k / dec_group(fmt));
+  w.x = dec_operand(fmt, dec_pieces(fmt, DEC_GATE_UP), 256, T, H);
+  w.h = dec_operand(fmt, dec_pieces(fmt, DEC_DOWN), w.x.end, T * k, F);
+  w.n_up = 4 * w.max_active * ((F + 127) / 128);
+  w.n_down = 4 * ((T + DEC_CHUNK - 1) / DEC_CHUNK) * ((H + 127) / 128);
+  w.counters = w.h.end;
+  w.part = align256(w.counters + static_cast<size_t>(w.n_up + w.n_down) * sizeof(int));
+  const int64_t tokens = std::min<int64_t>(T, DEC_CHUNK), up = std::min<int64_t>(T, dec_group(fmt));
+  w.end = w.part + static_cast<size_t>(DEC_MAX_CTAS) * std::max(tokens, 2 * up) * 128 * sizeof(float);
   *out = w;
   return true;
+}
+
+// Linear: error word, columns of x, counters, parts.
+struct LinWs {
+  DecOperandLayout x;
+  size_t counters, part, end;
+  int64_t n_counters;
+};
+LinWs lin_ws_layout(int fmt, int64_t T, int64_t K, int64_t N) {
+  LinWs w{};
+  w.x = dec_operand(fmt, dec_pieces(fmt, DEC_LINEAR), 256, T, K);
+  w.n_counters = 4 * ((T + DEC_CHUNK - 1) / DEC_CHUNK) * ((N + 127) / 128);
+  w.part = w.x.end;
+  // the counters come last: their number depends on N
+  w.counters = w.part + static_cast<size_t>(DEC_MAX_CTAS) * std::min<int64_t>(T, DEC_CHUNK) * 128 * sizeof(float);
+  w.end = w.counters + static_cast<size_t>(w.n_counters) * sizeof(int);
+  return w;
+}
+constexpr int64_t LIN_WS_ROWS = 1 << 20;   // rows of W a workspace of matvec_workspace_size() serves
+
+// The first kernel of a call (see k_split_x); `experts` and the h operand only for the MoE layer.
+template <int FMT>
+bool split_launch(const void* x, const DecParams& p, const DecOperandLayout& xl, const DecOperandLayout* hl,
+                  int n_counters, cudaStream_t stream) {
+  SplitParams q{};
+  q.x = static_cast<const uint16_t*>(x);
+  q.o = p.in;
+  q.err = p.err;
+  q.counters = p.counters;
+  q.n_counters = n_counters;
+  q.T = p.T;
+  q.K = p.K;
+  q.steps = p.steps;
+  q.zero_row[0] = reinterpret_cast<uint4*>(p.in.codes + (xl.code_rows - xl.pieces) * xl.steps * 128);
+  q.zero_n[0] = static_cast<int>(xl.steps * 8 * xl.pieces);
+  if (hl != nullptr) {
+    q.experts = p.experts;
+    q.n_ids = p.T * p.k;
+    q.E = p.E;
+    q.h_top = p.h.top;
+    q.n_top = p.T;
+    q.zero_row[1] = reinterpret_cast<uint4*>(p.h.codes + (hl->code_rows - hl->pieces) * hl->steps * 128);
+    q.zero_n[1] = static_cast<int>(hl->steps * 8 * hl->pieces);
+  }
+  DecLaunch l(p.T, std::min(SPLIT_THREADS, round_up(p.K / (FMT == DEC_NV ? 16 : 8), 32)), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, k_split_x<FMT>, q) == cudaSuccess;
 }
 
 template <int FMT>
@@ -770,9 +1141,9 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
   if (static_cast<int64_t>(E) * 2 * F > INT32_MAX || static_cast<int64_t>(E) * H > INT32_MAX)
     return MXFP8_ERR_UNSUPPORTED;
   DecWs ws;
-  if (!dec_ws_layout(T, k, H, F, E, &ws)) return MXFP8_ERR_UNSUPPORTED;
-  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < ws.total)
-    return workspace == nullptr ? MXFP8_ERR_INVALID_ARG : MXFP8_ERR_WORKSPACE;
+  if (!dec_ws_layout(FMT, T, k, H, F, E, &ws)) return MXFP8_ERR_UNSUPPORTED;
+  if (workspace == nullptr) return MXFP8_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < ws.end) return MXFP8_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0)
     return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
@@ -783,55 +1154,70 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
       (reinterpret_cast<uintptr_t>(gates) & 3u) != 0)
     return MXFP8_ERR_INVALID_ARG;
   if (FMT == DEC_NV && (w1_amax == nullptr || w2_amax == nullptr)) return MXFP8_ERR_INVALID_ARG;
+  // steps of all units, as the kernels count them
+  const int64_t act = ws.max_active, up_units = act * (F / 128);
+  if (up_units * 2 * ws.x.steps > INT32_MAX || act * ws.h.steps * (H / 128) > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
 
-  const int bytes_per_2 = FMT == DEC_NV ? 1 : 2;   // code bytes of two values
-  CUtensorMap m1, m2;
-  if (!make_weight_map(&m1, w1_q, static_cast<uint64_t>(E) * 2 * F, static_cast<uint64_t>(H) * bytes_per_2 / 2) ||
-      !make_weight_map(&m2, w2_q, static_cast<uint64_t>(E) * H, static_cast<uint64_t>(F) * bytes_per_2 / 2))
-    return MXFP8_ERR_CUDA;
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  const int ks = dec_step_values(FMT);
+  const uint64_t code_div = FMT == DEC_NV ? 2 : 1;   // values per code byte
+  CUtensorMap m1, m2, mx, mh;
+  if (!make_map(&m1, w1_q, static_cast<uint64_t>(E) * 2 * F, H / code_div, 128) ||
+      !make_map(&m2, w2_q, static_cast<uint64_t>(E) * H, F / code_div, 128) ||
+      !make_map(&mx, w + ws.x.codes, ws.x.code_rows, ws.x.steps * 128, ws.x.pieces) ||
+      !make_map(&mh, w + ws.h.codes, ws.h.code_rows, ws.h.steps * 128, ws.h.pieces))
+    return MXFP8_ERR_CUDA;
+  const int sms = std::min(dec_setup<FMT, DEC_GATE_UP>(), dec_setup<FMT, DEC_DOWN>());
+  if (sms <= 0 || 2 * sms > DEC_MAX_CTAS) return MXFP8_ERR_CUDA;
+
   DecParams p{};
-  p.x = static_cast<const uint16_t*>(x);
-  p.h = reinterpret_cast<float*>(w + ws.h);
-  p.hmax = reinterpret_cast<float*>(w + ws.hmax);
+  p.in = dec_pointers(w, ws.x);
+  p.h = dec_pointers(w, ws.h);
+  p.h_steps = static_cast<int>(ws.h.steps);
   p.experts = experts;
   p.gates = gates;
   p.out = static_cast<uint16_t*>(out);
   p.err = reinterpret_cast<uint32_t*>(w);
+  p.part = reinterpret_cast<float*>(w + ws.part);
+  p.counters = reinterpret_cast<int*>(w + ws.counters);
   p.T = static_cast<int>(T);
   p.k = k;
   p.E = E;
   p.F = static_cast<int>(F);
+  p.max_active = ws.max_active;
   p.timeout_ns = dec_wait_ns();
   p.drain_ns = kDecWaitNs;
-  int chunks = 0;
-  // one chunking for both kernels: DOWN (more columns per token) has the tighter layout
-  if (!dec_chunks(FMT, DEC_DOWN, p.T, k, E, &p.L, &p.per_chunk, &chunks)) return MXFP8_ERR_UNSUPPORTED;
-  const DecLayout down = p.L;
-  const int nact = std::min(E, p.per_chunk * k);
-  if (!dec_layout(FMT, DEC_GATE_UP, p.per_chunk, E, nact, &p.L)) return MXFP8_ERR_UNSUPPORTED;
 
+  const int group = std::min(p.T, dec_group(FMT));
+  if (!dec_layout(FMT, DEC_GATE_UP, group, E, p.max_active, &p.L)) return MXFP8_ERR_UNSUPPORTED;
+  p.part_slot = 2 * group * 128;
   p.w_sf = w1_sf;
   p.w_amax = w1_amax;
   p.K = static_cast<int>(H);
-  p.steps = static_cast<int>((H + ks - 1) / ks);
+  p.steps = static_cast<int>(ws.x.steps);
   p.kt = p.steps * dec_atoms(FMT);
   p.tiles = static_cast<int>(F / 128);
-  const int64_t clusters = static_cast<int64_t>(nact) * p.tiles;
-  p.cs = 2 * dec_split(2 * clusters * chunks, p.steps, DEC_MAX_CLUSTER / 2, 2);
-  if (clusters * p.cs > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
-  if (!dec_launch<FMT, DEC_GATE_UP>(m1, p, static_cast<int>(clusters), chunks, false, s)) return MXFP8_ERR_CUDA;
+  p.chunks = 1;
+  p.per_chunk = p.T;
+  const DecParams up = p;
 
-  p.L = down;
+  p.chunks = (p.T + DEC_CHUNK - 1) / DEC_CHUNK;
+  p.per_chunk = (p.T + p.chunks - 1) / p.chunks;
+  if (!dec_layout(FMT, DEC_DOWN, p.per_chunk, E, p.max_active, &p.L)) return MXFP8_ERR_UNSUPPORTED;
+  p.part_slot = p.per_chunk * 128;
+  p.counters += ws.n_up;
+  p.in = p.h;
   p.w_sf = w2_sf;
   p.w_amax = w2_amax;
   p.K = static_cast<int>(F);
-  p.steps = static_cast<int>((F + ks - 1) / ks);
+  p.steps = p.h_steps;
   p.kt = p.steps * dec_atoms(FMT);
   p.tiles = static_cast<int>(H / 128);
-  p.cs = dec_split(static_cast<int64_t>(p.tiles) * chunks, static_cast<int64_t>(nact) * p.steps, DEC_MAX_CLUSTER, 2);
-  if (!dec_launch<FMT, DEC_DOWN>(m2, p, p.tiles, chunks, true, s)) return MXFP8_ERR_CUDA;
+  p.zero_row = p.T * k;
+
+  if (!split_launch<FMT>(x, up, ws.x, &ws.h, static_cast<int>(ws.n_up + ws.n_down), s) ||
+      !dec_launch<FMT, DEC_GATE_UP>(m1, mx, up, (up.L.smem == DEC_SMEM_HALF ? 2 : 1) * sms, s) ||
+      !dec_launch<FMT, DEC_DOWN>(m2, mh, p, (p.L.smem == DEC_SMEM_HALF ? 2 : 1) * sms / p.chunks * p.chunks, s))
+    return MXFP8_ERR_CUDA;
   return MXFP8_OK;
 }
 
@@ -839,10 +1225,12 @@ template <int FMT>
 int matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf,
            const float* w_amax, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   if (T < 0 || K <= 0 || N < 0) return MXFP8_ERR_INVALID_ARG;
-  if (T > DEC_MAX_TOKENS || K % 128 != 0 || N % 128 != 0 || K > INT32_MAX || N > INT32_MAX)
+  if (T > DEC_MAX_TOKENS || K % 128 != 0 || N % 128 != 0 || K > INT32_MAX || N > LIN_WS_ROWS)
     return MXFP8_ERR_UNSUPPORTED;
-  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return MXFP8_ERR_INVALID_ARG;
-  if (workspace_bytes < matvec_workspace_size()) return MXFP8_ERR_WORKSPACE;
+  const LinWs ws = lin_ws_layout(FMT, T, K, N);
+  if (N / 128 * ws.x.steps > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
+  if (workspace == nullptr) return MXFP8_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < ws.end) return MXFP8_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0 || N == 0)
     return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
@@ -850,28 +1238,39 @@ int matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, c
   for (const void* q : ptrs)
     if (q == nullptr || !aligned16(q)) return MXFP8_ERR_INVALID_ARG;
   if (FMT == DEC_NV && w_amax == nullptr) return MXFP8_ERR_INVALID_ARG;
-  CUtensorMap m;
-  if (!make_weight_map(&m, w_q, static_cast<uint64_t>(N), static_cast<uint64_t>(K) / (FMT == DEC_NV ? 2 : 1)))
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  CUtensorMap m, mx;
+  const int chunks = static_cast<int>((T + DEC_CHUNK - 1) / DEC_CHUNK), per_chunk = static_cast<int>((T + chunks - 1) / chunks);
+  if (!make_map(&m, w_q, static_cast<uint64_t>(N), static_cast<uint64_t>(K) / (FMT == DEC_NV ? 2 : 1), 128) ||
+      !make_map(&mx, w + ws.x.codes, ws.x.code_rows, ws.x.steps * 128, per_chunk * ws.x.pieces))
     return MXFP8_ERR_CUDA;
-  const int ks = dec_step_values(FMT);
+  const int sms = dec_setup<FMT, DEC_LINEAR>();
+  if (sms <= 0 || 2 * sms > DEC_MAX_CTAS) return MXFP8_ERR_CUDA;
   DecParams p{};
-  p.x = static_cast<const uint16_t*>(x);
+  p.in = dec_pointers(w, ws.x);
   p.w_sf = w_sf;
   p.w_amax = w_amax;
   p.out = static_cast<uint16_t*>(y);
-  p.err = static_cast<uint32_t*>(workspace);
+  p.err = reinterpret_cast<uint32_t*>(w);
+  p.part = reinterpret_cast<float*>(w + ws.part);
+  p.counters = reinterpret_cast<int*>(w + ws.counters);
   p.T = static_cast<int>(T);
   p.k = 1;
   p.K = static_cast<int>(K);
-  p.steps = static_cast<int>((K + ks - 1) / ks);
+  p.steps = static_cast<int>(ws.x.steps);
   p.kt = p.steps * dec_atoms(FMT);
   p.tiles = static_cast<int>(N / 128);
   p.timeout_ns = dec_wait_ns();
   p.drain_ns = kDecWaitNs;
-  int chunks = 0;
-  if (!dec_chunks(FMT, DEC_LINEAR, p.T, 1, 0, &p.L, &p.per_chunk, &chunks)) return MXFP8_ERR_UNSUPPORTED;
-  p.cs = dec_split(static_cast<int64_t>(p.tiles) * chunks, p.steps, DEC_MAX_CLUSTER, 2);
-  return dec_launch<FMT, DEC_LINEAR>(m, p, p.tiles, chunks, false, s) ? MXFP8_OK : MXFP8_ERR_CUDA;
+  p.chunks = chunks;
+  p.per_chunk = per_chunk;
+  p.part_slot = p.per_chunk * 128;
+  if (!dec_layout(FMT, DEC_LINEAR, p.per_chunk, 0, 0, &p.L)) return MXFP8_ERR_UNSUPPORTED;
+  const int ctas = p.L.smem == DEC_SMEM_HALF ? 2 * sms : sms;
+  if (!split_launch<FMT>(x, p, ws.x, nullptr, static_cast<int>(ws.n_counters), s) ||
+      !dec_launch<FMT, DEC_LINEAR>(m, mx, p, ctas / p.chunks * p.chunks, s))
+    return MXFP8_ERR_CUDA;
+  return MXFP8_OK;
 }
 
 }  // namespace
@@ -882,8 +1281,9 @@ using namespace mx;
 extern "C" {
 
 size_t moe_decode_workspace_size(int64_t T, int k, int64_t H, int64_t F, int E) {
-  DecWs w;
-  return dec_ws_layout(T, k, H, F, E, &w) ? w.total : 0;
+  DecWs mx, nv;   // enough for either weight format
+  if (!dec_ws_layout(DEC_MX, T, k, H, F, E, &mx) || !dec_ws_layout(DEC_NV, T, k, H, F, E, &nv)) return 0;
+  return std::max(mx.end, nv.end);
 }
 
 int moe_decode_fwd(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, const int32_t* experts,
@@ -901,7 +1301,10 @@ int nvfp4_moe_decode_fwd(const void* x, int64_t T, int64_t H, int64_t F, int E, 
                             workspace, workspace_bytes, stream);
 }
 
-size_t matvec_workspace_size(void) { return 256; }
+size_t matvec_workspace_size(int64_t T, int64_t K) {
+  if (T < 0 || T > DEC_MAX_TOKENS || K <= 0 || K > INT32_MAX) return 0;
+  return std::max(lin_ws_layout(DEC_MX, T, K, LIN_WS_ROWS).end, lin_ws_layout(DEC_NV, T, K, LIN_WS_ROWS).end);
+}
 
 int mxfp8_matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf, void* y,
                  void* workspace, size_t workspace_bytes, void* stream) {
