@@ -432,6 +432,43 @@ int mxfp8_matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* 
 int nvfp4_matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf,
                  const float* w_amax, void* y, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The junction between two blocks (for example around the MoE layer): RMS norm of a block's output,
+ * its gate, the scaled residual, and the RMS norm in front of the next block, in one pass.
+ *     yh = y / rms(y), z = yh * w_post   (post_norm 0: z = y);     rms(v) = sqrt(mean(v^2) + eps)
+ *     res_out = res_scale * res + gate * z
+ *     n = res_out / rms(res_out) * w_pre          (from res_out before its rounding)
+ * residual_norm_fwd
+ *   y       (device) bf16 [T, H], the block's output.
+ *   res     (device) [T, H] residual stream, res_out the same type (res_out may be res):
+ *           res_dtype RESIDUAL_BF16 or RESIDUAL_F32.
+ *   w_post, w_pre (device) float [H], or NULL for 1 (w_post only with post_norm 1).
+ *   gate    (device) float: gate_kind RESIDUAL_GATE_CHANNEL [H], RESIDUAL_GATE_TOKEN [T],
+ *           RESIDUAL_GATE_NONE NULL.
+ *   n       (device, out) bf16 [T, H], the next block's input.
+ *   stats   (device, out) float [2, T]: 1 / rms(y) (1 without the post-norm) and 1 / rms(res_out).
+ * residual_norm_bwd -- gradients of all inputs, from the gradients of n and of res_out:
+ *   dn      bf16 [T, H].   dres_out [T, H] in the residual's type, or NULL for 0 (may be dres).
+ *   y, res_out, stats, w_post, gate, w_pre, res_scale   as the forward had or wrote them.
+ *   dy      bf16 [T, H] out.   dres [T, H] out in the residual's type.
+ *   dw_post, dgate, dw_pre   float out, shaped like the weights, or NULL to skip (and where the weight
+ *           is NULL).
+ *   workspace  residual_norm_bwd_workspace_size(T, H) bytes, 16-byte aligned (unused for few rows).
+ * Sums are fp32 in an order that depends on T, H and the device only.  Requirements: H % 8 == 0,
+ * H <= 8192; 16-byte aligned pointers (token gates and stats 4-byte).  T == 0 is a no-op (the
+ * backward's weight gradients are zeros).  No device-side errors.
+ */
+enum { RESIDUAL_BF16 = 0, RESIDUAL_F32 = 1 };
+enum { RESIDUAL_GATE_NONE = 0, RESIDUAL_GATE_CHANNEL = 1, RESIDUAL_GATE_TOKEN = 2 };
+int residual_norm_fwd(const void* y, const void* res, const float* w_post, const float* gate, const float* w_pre,
+                      int64_t T, int64_t H, int res_dtype, int gate_kind, int post_norm, float res_scale, float eps,
+                      void* res_out, void* n, float* stats, void* stream);
+size_t residual_norm_bwd_workspace_size(int64_t T, int64_t H);
+int residual_norm_bwd(const void* dn, const void* dres_out, const void* y, const void* res_out, const float* stats,
+                      const float* w_post, const float* gate, const float* w_pre, int64_t T, int64_t H, int res_dtype,
+                      int gate_kind, int post_norm, float res_scale, void* dy, void* dres, float* dw_post,
+                      float* dgate, float* dw_pre, void* workspace, size_t workspace_bytes, void* stream);
+
 /* mxfp8_mma_peak -- measurement aid, with no counterpart on the pages: the rate of the
  * block-scaled tensor-core instruction this library's GEMMs are built on, on the device at hand
  * (the roofline their TFLOP/s are reported against).  Launches one cluster of two CTAs per pair

@@ -18,6 +18,8 @@ approaches, items 1-3):
   moe_decode_fwd, nvfp4_moe_decode_fwd, mxfp8_matvec, nvfp4_matvec
                      the whole layer, and a linear, for a few tokens (decode steps), from the
                      same weights.
+  residual_norm_fwd / residual_norm_bwd
+                     the norms behind and before a block with its gate and the scaled residual.
 """
 from __future__ import annotations
 
@@ -39,6 +41,7 @@ __all__ = [
     "mxfp8_mma_peak", "grouped_mlp_bwd_workspace_layout", "nvfp4_sf_bytes", "nvfp4_quantize", "nvfp4_grouped_mlp_workspace_size",
     "nvfp4_grouped_mlp_workspace_layout", "nvfp4_grouped_mlp_fwd", "moe_decode_workspace_size", "moe_decode_fwd",
     "nvfp4_moe_decode_fwd", "matvec_workspace_size", "mxfp8_matvec", "nvfp4_matvec",
+    "residual_norm_fwd", "residual_norm_bwd", "residual_norm_bwd_workspace_size",
 ]
 
 ROWWISE = 1
@@ -147,6 +150,12 @@ def lib() -> ctypes.CDLL:
             L.mxfp8_matvec.argtypes = [P, i64, i64, i64, P, P, P, P, sz, P]
             L.nvfp4_matvec.restype = i32
             L.nvfp4_matvec.argtypes = [P, i64, i64, i64, P, P, P, P, P, sz, P]
+            L.residual_norm_fwd.restype = i32
+            L.residual_norm_fwd.argtypes = [P, P, P, P, P, i64, i64, i32, i32, i32, f32, f32, P, P, P, P]
+            L.residual_norm_bwd_workspace_size.restype = sz
+            L.residual_norm_bwd_workspace_size.argtypes = [i64, i64]
+            L.residual_norm_bwd.restype = i32
+            L.residual_norm_bwd.argtypes = [P, P, P, P, P, P, P, P, i64, i64, i32, i32, i32, f32, P, P, P, P, P, P, sz, P]
             _lib = L
     return _lib
 
@@ -658,6 +667,76 @@ def nvfp4_matvec(x, w, out=None, workspace=None, stream=None):
     """y = x W^T for a few rows of x (bf16 [T, K], T <= 64) from 4-bit weights: w = (codes, scale codes,
     amax) as nvfp4_quantize writes them with SF_MMA.  Returns bf16 [T, N]."""
     return _matvec("nvfp4_matvec", True, x, w, out, workspace, stream)
+
+
+def _norm_args(y, res_like, w_post, gate, w_pre, post_norm):
+    """(T, H, residual dtype, its code, gate kind, gate pointer, w_post pointer, w_pre pointer)."""
+    import torch
+    f32 = torch.float32
+    T, H = y.shape
+    rt = res_like.dtype
+    if rt is not torch.bfloat16 and rt is not f32:
+        raise ValueError(f"residual: expected bfloat16 or float32, got {rt}")
+    kind, pg = 0, None
+    if gate is not None:
+        kind = 1 if gate.dim() == 1 else 2     # [H]: per channel; [T, 1]: per token
+        pg = _need(gate, f32, (H,) if kind == 1 else (T, 1), "gate")
+    return (T, H, rt, 0 if rt is torch.bfloat16 else 1, kind, pg,
+            None if w_post is None else _need(w_post, f32, (H,), "w_post"),
+            None if w_pre is None else _need(w_pre, f32, (H,), "w_pre"))
+
+
+def residual_norm_fwd(y, res, w_post=None, gate=None, w_pre=None, res_scale: float = 1.0, post_norm: bool = True,
+                      eps: float = 1e-6, out=None, stream=None):
+    """res_out = res_scale * res + gate * rms_norm(y) * w_post;  n = rms_norm(res_out) * w_pre.
+
+    y bf16 [T, H]; res bf16 or float32 [T, H]; w_post, w_pre float32 [H] or None; gate float32 [H] (per
+    channel), [T, 1] (per token) or None; post_norm False: no norm of y.  Returns (res_out, n bf16, stats
+    float32 [2, T]); `out` may pass the three (res_out may be res)."""
+    import torch
+    bf16 = torch.bfloat16
+    T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res, w_post, gate, w_pre, post_norm)
+    py, pr = _need(y, bf16, (T, H), "y"), _need(res, rt, (T, H), "res")
+    if out is None:
+        out = (torch.empty_like(res), torch.empty_like(y), torch.empty((2, T), dtype=torch.float32, device=y.device))
+    st = lib().residual_norm_fwd(py, pr, pa, pg, pb, T, H, code, kind, 1 if post_norm else 0, res_scale, eps,
+                                 _need(out[0], rt, (T, H), "res_out"), _need(out[1], bf16, (T, H), "n"),
+                                 _need(out[2], torch.float32, (2, T), "stats"), _stream_of(y, stream))
+    if st != OK:
+        raise MXFP8Error(st, "residual_norm_fwd")
+    return tuple(out)
+
+
+def residual_norm_bwd_workspace_size(T: int, H: int) -> int:
+    return int(lib().residual_norm_bwd_workspace_size(T, H))
+
+
+def residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post=None, gate=None, w_pre=None, res_scale: float = 1.0,
+                      post_norm: bool = True, workspace=None, stream=None):
+    """Gradients of residual_norm_fwd from those of n (bf16 [T, H]) and of res_out (residual's type, or None
+    for 0); y, res_out, stats as the forward read or wrote them.  Returns (dy bf16, dres, dw_post, dgate,
+    dw_pre), the last three float32 shaped like the weights (None where the weight is None)."""
+    import torch
+    bf16, f32 = torch.bfloat16, torch.float32
+    T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res_out, w_post, gate, w_pre, post_norm)
+    pn, py, pr = _need(dn, bf16, (T, H), "dn"), _need(y, bf16, (T, H), "y"), _need(res_out, rt, (T, H), "res_out")
+    pd = None if dres_out is None else _need(dres_out, rt, (T, H), "dres_out")
+    dy, dres = torch.empty_like(y), torch.empty_like(res_out)
+    dgate = torch.empty_like(gate) if kind == 2 else None
+    cols = (w_post is not None) + (kind == 1) + (w_pre is not None)
+    cols = list(torch.empty((cols, H), dtype=f32, device=y.device).unbind(0)) if cols else []
+    dw_post = cols.pop() if w_post is not None else None
+    dgate = cols.pop() if kind == 1 else dgate
+    dw_pre = cols.pop() if w_pre is not None else None
+    if workspace is None:
+        workspace = torch.empty(max(16, residual_norm_bwd_workspace_size(T, H)), dtype=torch.uint8, device=y.device)
+    st = lib().residual_norm_bwd(pn, pd, py, pr, _need(stats, f32, (2, T), "stats"), pa, pg, pb, T, H, code, kind,
+                                 1 if post_norm else 0, res_scale, dy.data_ptr(), dres.data_ptr(), _ptr(dw_post),
+                                 _ptr(dgate), _ptr(dw_pre), workspace.data_ptr(), workspace.numel(),
+                                 _stream_of(y, stream))
+    if st != OK:
+        raise MXFP8Error(st, "residual_norm_bwd")
+    return dy, dres, dw_post, dgate, dw_pre
 
 
 def mxfp8_mma_peak(iters: int, workspace, fmt: int = 0, stream=None) -> int:
