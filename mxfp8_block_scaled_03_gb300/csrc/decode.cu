@@ -1,6 +1,6 @@
-// decode.cu -- the expert MLP and plain linears for a few tokens (decode steps): a whole MoE layer
-// in two kernels, and y = x W^T for a few rows of x, from the MXFP8 and NVFP4 weights the grouped
-// GEMMs use (same codes, same tensor-core scale layout).
+// decode.cu -- the expert MLP and plain linears for a few tokens (decode steps): a whole MoE layer and
+// y = x W^T for a few rows of x, from the MXFP8 and NVFP4 weights the grouped GEMMs use (same codes, same
+// tensor-core scale layout).
 //
 //   moe_decode_fwd, nvfp4_moe_decode_fwd   out[t] = sum_j gate[t,j] W2[e] (silu(W1g[e] x_t) * (W1u[e] x_t))
 //   mxfp8_matvec, nvfp4_matvec             y[t] = W x_t
@@ -21,19 +21,17 @@
 // What bounds it: reading the weights once (a token's flops per weight byte are far below the tensor
 // cores').  So the weights are the M operand: TMA brings 128 rows x 128 code bytes per K step and
 // their scale atoms, the MMA reads both as stored, and no instruction is spent per weight.  The
-// tokens are the N operand: k_split_x writes the columns of x, GATE_UP's epilogue those of h.
-//
-//   k_split_x          x -> columns, and the bookkeeping of the call
-//   k_decode<GATE_UP>  units: 128 columns of F of one chosen expert (and up to 16 or 32 of its tokens); gate
-//                      and up rows are alternate K steps on two accumulators; h = gate silu(g) u
-//   k_decode<DOWN>     units: 128 rows of H; K runs over all chosen experts' F one after the other, with one
-//                      column group per token (zero where the token did not choose the expert), so the
-//                      accumulator itself sums a token's experts
-//   k_decode<LINEAR>   units: 128 rows of W
+// tokens are the N operand.  A (token, expert) pair is a row of activations; pairs are numbered expert after
+// expert, so that an expert's columns are one box of the copy.
+//   k_split_x        x -> columns (by token, or by pair for the MoE layer), and the bookkeeping of the call
+//   k_decode<UP>     units: 128 columns of F of one chosen expert (and up to 16 or 32 of its tokens); gate
+//                    and up rows are alternate K steps on two accumulators; h = gate silu(g) u -> columns
+//   k_decode<DOWN>   units: 128 rows of H of one chosen expert; a row of partial results per pair
+//   k_sum_rows       adds a token's pairs
+//   k_decode<LINEAR> units: 128 rows of W
 // The kernels are launched programmatically dependent: a kernel's weight copies start while the one
 // before it runs, and only what reads its results waits.  Two CTAs share an SM (one alone reaches 60-87%
 // of the copy bandwidth: its single MMA thread spends 0.3-0.5 us a K step of 16 KB).
-// Measured (4096 -> 114688, one token): MXFP8 76.0 us, 6.38 TB/s (94% of the copy rate); NVFP4 47.4 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -55,59 +53,59 @@ constexpr int DEC_SCALE_WARPS = 2;
 constexpr int DEC_FIRST_EPI_WARP = 4;
 constexpr int DEC_A_STAGE = 128 * 128;       // 128 weight rows x 128 code bytes
 constexpr int DEC_MAX_TOKENS = 64;           // tokens of one call
-constexpr int DEC_CHUNK = 32;                // DOWN, LINEAR: most tokens of one accumulator
+constexpr int DEC_CHUNK = 32;                // LINEAR: most tokens of one accumulator
 constexpr int DEC_MAX_K = 32;                // choices per token
 constexpr int DEC_MAX_STAGES = 12;
 constexpr int DEC_MIN_STEPS = 4;             // K steps that make a CTA worth having (2 and 8 measured the same)
 // Half of 228 KB less the 1 KB the system keeps per CTA, so that a kernel's CTAs fit beside those of the
-// kernel before it; the whole SM where that leaves fewer than four stages.
+// kernel before it; the whole SM where that leaves fewer than three stages.
 constexpr int DEC_SMEM_HALF = 113 * 1024, DEC_SMEM_FULL = 226 * 1024;
 constexpr uint32_t DEC_TMEM_COLS = 256;      // two CTAs per SM share 512
 // TMEM columns: accumulators (at most 160), then as many sets of scales of A and B as fit, used in turn
 // (at least two): a step's scales may be written while the MMAs of that many steps less one are pending.
 constexpr int SPLIT_THREADS = 1024;          // at most
 
-enum DecMode { DEC_GATE_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
+enum DecMode { DEC_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
 enum DecFmt { DEC_MX = 0, DEC_NV = 1 };
 
-// Columns per token: E4M3 pieces of a bf16 (2) or fp32 (3) value, or base-8 digits (5).
+// Columns per activation row: E4M3 pieces of a bf16 (2) or fp32 (3) value, or base-8 digits (5).
 constexpr int dec_pieces(int fmt, int mode) { return fmt == DEC_NV ? 5 : mode == DEC_DOWN ? 3 : 2; }
 constexpr int dec_step_values(int fmt) { return fmt == DEC_NV ? 256 : 128; }
 constexpr int dec_atoms(int fmt) { return fmt == DEC_NV ? 4 : 1; }          // scale atoms per 128 rows and step
 constexpr int dec_exp_bytes(int fmt) { return fmt == DEC_NV ? 16 : 4; }     // blocks of one row and step
-// GATE_UP: most tokens of one unit (an expert with more gives several units); two accumulators of at
-// most 80 columns share the TMEM that DOWN and LINEAR use for one of 160.
-constexpr int dec_group(int fmt) { return fmt == DEC_NV ? 16 : 32; }
+// Most rows of a unit.  MoE: two accumulators of at most 80 columns share the TMEM that LINEAR uses for one of
+// 160 (an expert with more tokens gives several units, which read its weights side by side, from L2).
+constexpr int dec_group(int fmt, int mode) { return mode == DEC_LINEAR ? DEC_CHUNK : fmt == DEC_NV ? 16 : 32; }
 
 // Shared memory of one CTA (byte offsets from a 1024-byte boundary); the weight ring is at 0.
 struct DecLayout {
   int stages, smem;
   int b_stage, sfb_stage;
   int b, sfa, sfb, bars, misc;
-  int n_max;             // most columns of one accumulator (GATE_UP: the second one starts there)
+  int n_max;             // most columns of one accumulator (UP: the second one starts there)
   int sf_col, sf_cols, sf_sets;   // TMEM: first column of the scale sets, columns per set, sets
 };
 
-// Activations as columns of the MMA.  Row r * P + q of `codes` holds piece q of row r (a token of x, a
-// token-expert pair of h): 128 code bytes per K step.  P rows of zeros follow them.
+// Activations as columns of the MMA.  Row r * P + q of `codes` holds piece q of row r: 128 code bytes per K step.
 struct DecOperand {
-  uint8_t* codes;   // [(rows + 1) * P][steps * 128]
+  uint8_t* codes;   // [rows * P][steps * 128]
   uint8_t* exps;    // [rows][steps][4 | 16]: exponent + 127 of every 32 | 16 values (255: not finite)
-  int* top;         // [T] largest exponent of the token's row, or of all its rows of h (NVFP4)
+  int* top;         // [rows] largest exponent of the row (NVFP4)
 };
 
 struct DecParams {
   DecLayout L;
-  DecOperand in;          // GATE_UP, LINEAR: x;  DOWN: h
-  DecOperand h;           // GATE_UP: where h goes
-  int h_steps;            // GATE_UP: K steps of h
+  DecOperand in;          // UP, LINEAR: x;  DOWN: h
+  DecOperand h;           // UP: where h goes
+  int h_steps;            // UP: K steps of h
   const uint8_t* w_sf;
   const float* w_amax;    // NVFP4
   const int32_t* experts; // [T, k]
-  const float* gates;     // [T, k] or NULL
-  uint16_t* out;          // DOWN: [T, H], LINEAR: [T, N]
+  const float* gate;      // UP: [pairs] routing weights
+  uint16_t* out;          // LINEAR: [T, N]
+  float* y;               // DOWN: [pairs, H]
   uint32_t* err;
-  float* part;            // partial sums: part_slot floats per CTA
+  float* part;            // partial sums: part_slot floats per CTA, MoE twice
   int part_slot;
   int* counters;          // [units][4] of units shared by several CTAs: how many are done with a quarter of the rows
   int T, k, E;
@@ -115,10 +113,9 @@ struct DecParams {
   int steps;              // its K steps
   int kt;                 // its scale atoms per 128-row tile
   int tiles;              // 128-row tiles (of F, H or N)
-  int F;
   int max_active;         // most list entries (see the routing)
-  int zero_row;           // row of the operand that is zeros
-  int chunks, per_chunk;  // DOWN, LINEAR: token chunks, tokens per chunk
+  int chunks, per_chunk;  // LINEAR: token chunks, tokens per chunk
+  int box_rows;           // activation rows in a box of columns
   uint64_t timeout_ns, drain_ns;
 };
 
@@ -128,6 +125,7 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
+__device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // One lane of the (converged) warp.  The compiler knows that a branch on it holds one thread, and issues
 // copies and MMAs there directly; behind `lane == 0` it wraps each of them in a loop over the lanes.
 __device__ __forceinline__ bool elect_one() {
@@ -197,40 +195,94 @@ __device__ __forceinline__ uint64_t next_piece(uint64_t& r) {
   }
 }
 
-// x (bf16 [T, K]) -> columns.  One CTA per token; a thread takes 8 values (MXFP8, four threads a block)
-// or 16 (NVFP4, one block) at a time, 8 code bytes either way.  It also prepares the call's bookkeeping:
-// the error word, the range check of the experts' ids, the row exponents of h and the counters.
+// The code bytes of the next piece of eight (MXFP8) or sixteen (NVFP4) scaled values.
+template <int FMT, bool LAST>
+__device__ __forceinline__ uint2 next_codes(uint64_t (&r)[FMT == DEC_NV ? 8 : 4]) {
+  constexpr int N = FMT == DEC_NV ? 8 : 4;
+  uint64_t n[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) n[i] = next_piece<FMT, LAST>(r[i]);
+  uint2 code;
+  if constexpr (FMT == DEC_MX) {
+    code.x = e4m3x2_f2(n[0]) | (e4m3x2_f2(n[1]) << 16);
+    code.y = e4m3x2_f2(n[2]) | (e4m3x2_f2(n[3]) << 16);
+  } else {
+    code.x = e2m1x8(f2_lo(n[0]), f2_hi(n[0]), f2_lo(n[1]), f2_hi(n[1]), f2_lo(n[2]), f2_hi(n[2]), f2_lo(n[3]),
+                    f2_hi(n[3]));
+    code.y = e2m1x8(f2_lo(n[4]), f2_hi(n[4]), f2_lo(n[5]), f2_hi(n[5]), f2_lo(n[6]), f2_hi(n[6]), f2_lo(n[7]),
+                    f2_hi(n[7]));
+  }
+  return code;
+}
+
+// x (bf16 [T, K]) -> columns; a thread takes 8 values (MXFP8, four threads a block) or 16 (NVFP4, one block)
+// at a time, 8 code bytes either way.  It also prepares the call's bookkeeping: the error word, the range
+// check of the experts' ids, the row exponents of h and the counters.
+//   BY_PAIR  one CTA per choice (t, j), which finds the choice's pair as the weight kernels' routing numbers
+//            them, writes its token's columns there and the pair's routing weight (a token that lists an expert
+//            more than once is one pair with the sum of the weights); a choice that is dropped or repeats an
+//            earlier one has none.
+//   else     one CTA per token.
 // Latency-bound (a token is a few KB): what matters is that the weight kernel's copies start meanwhile.
 struct SplitParams {
   const uint16_t* x;
   DecOperand o;
   uint32_t* err;
   const int32_t* experts;
+  const float* gates;
+  float* gate;            // [pairs]
+  int* row_of;            // [T, k] pair of every choice (-1: none)
   int* h_top;
   int* counters;
-  uint4* zero_row[2];     // the rows of zeros behind the columns of x and of h
-  int zero_n[2];
-  int T, K, steps, n_ids, E, n_top, n_counters;
+  int T, K, steps, n_ids, E, k, n_top, n_counters;
 };
-template <int FMT>
+template <int FMT, bool BY_PAIR>
 __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) {
   constexpr int P = dec_pieces(FMT, DEC_LINEAR), EB = dec_exp_bytes(FMT);
   constexpr int VALS = FMT == DEC_NV ? 16 : 8;   // 16 groups per step
-  __shared__ int s_top;
+  __shared__ int s_top, s_row;
   pdl_wait();
-  const int t = blockIdx.x, tid = threadIdx.x;
-  if (t == 0 && tid == 0) *p.err = 0;
-  if (tid == 0) s_top = -128;
+  const int b = blockIdx.x, t = BY_PAIR ? b / p.k : b, tid = threadIdx.x;
+  if (b == 0 && tid == 0) *p.err = 0;
+  if (tid == 0) {
+    s_top = -128;
+    s_row = 0;
+  }
   __syncthreads();
   pdl_launch_dependents();   // everything before this call in the stream is complete
-  if (t == 0) {
+  if (b == 0)
     for (int i = tid; i < p.n_ids; i += blockDim.x)
       if (__ldg(p.experts + i) >= p.E) atomicOr(p.err, ERR_EXPERT_RANGE);
-    for (int z = 0; z < 2; ++z)
-      for (int i = tid; i < p.zero_n[z]; i += blockDim.x) p.zero_row[z][i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = b * blockDim.x + tid; i < p.n_top; i += gridDim.x * blockDim.x) p.h_top[i] = -128;
+  for (int i = b * blockDim.x + tid; i < p.n_counters; i += gridDim.x * blockDim.x) p.counters[i] = 0;
+
+  int dst = t;   // row of the operand
+  if constexpr (BY_PAIR) {
+    // pairs of lower experts, and of this expert with lower tokens
+    const int e = __ldg(p.experts + b);
+    bool none = e < 0 || e >= p.E;
+    for (int j = t * p.k; j < b; ++j) none |= __ldg(p.experts + j) == e;
+    int below = 0;
+    if (!none)
+      for (int i = tid; i < p.n_ids; i += blockDim.x) {
+        const int o = __ldg(p.experts + i), ot = i / p.k;
+        bool first = o >= 0 && (o < e || (o == e && ot < t));
+        for (int j = ot * p.k; first && j < i; ++j) first = __ldg(p.experts + j) != o;
+        below += first ? 1 : 0;
+      }
+    below = __reduce_add_sync(0xFFFFFFFFu, below);
+    if ((tid & 31) == 0 && below != 0) atomicAdd(&s_row, below);
+    __syncthreads();
+    dst = s_row;
+    if (tid == 0) {
+      p.row_of[b] = none ? -1 : dst;
+      float g = 0.0f;
+      for (int j = b; !none && j < (t + 1) * p.k; ++j)
+        if (__ldg(p.experts + j) == e) g += p.gates != nullptr ? __ldg(p.gates + j) : 1.0f;
+      if (!none) p.gate[dst] = g;
+    }
+    if (none) return;
   }
-  for (int i = t * blockDim.x + tid; i < p.n_top; i += p.T * blockDim.x) p.h_top[i] = -128;
-  for (int i = t * blockDim.x + tid; i < p.n_counters; i += p.T * blockDim.x) p.counters[i] = 0;
 
   int top = -128;
   const int groups = p.K / VALS;
@@ -256,10 +308,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
     const int eb = block_exponent(m);
     top = max(top, eb);
     if (FMT == DEC_NV || (g & 3) == 0)
-      p.o.exps[(static_cast<int64_t>(t) * p.steps + step) * EB + (FMT == DEC_NV ? g : g >> 2)] =
+      p.o.exps[(static_cast<int64_t>(dst) * p.steps + step) * EB + (FMT == DEC_NV ? g : g >> 2)] =
           static_cast<uint8_t>(eb + 127);
-    const float inv = block_multiplier<FMT>(eb);
-    const uint64_t inv2 = f2_pack(inv, inv);
+    const uint64_t inv2 = f2_pack(block_multiplier<FMT>(eb), block_multiplier<FMT>(eb));
     uint64_t r[VALS / 2];
 #pragma unroll
     for (int i = 0; i < VALS / 8; ++i) {
@@ -270,34 +321,22 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
     }
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-      uint64_t n[VALS / 2];
-#pragma unroll
-      for (int i = 0; i < VALS / 2; ++i) n[i] = q + 1 < P ? next_piece<FMT, false>(r[i]) : next_piece<FMT, true>(r[i]);
-      uint2 code;
-      if constexpr (FMT == DEC_MX) {
-        code.x = e4m3x2_f2(n[0]) | (e4m3x2_f2(n[1]) << 16);
-        code.y = e4m3x2_f2(n[2]) | (e4m3x2_f2(n[3]) << 16);
-      } else {
-        code.x = e2m1x8(f2_lo(n[0]), f2_hi(n[0]), f2_lo(n[1]), f2_hi(n[1]), f2_lo(n[2]), f2_hi(n[2]), f2_lo(n[3]),
-                        f2_hi(n[3]));
-        code.y = e2m1x8(f2_lo(n[4]), f2_hi(n[4]), f2_lo(n[5]), f2_hi(n[5]), f2_lo(n[6]), f2_hi(n[6]), f2_lo(n[7]),
-                        f2_hi(n[7]));
-      }
-      *reinterpret_cast<uint2*>(p.o.codes + (static_cast<int64_t>(t) * P + q) * p.steps * 128 + gi * 8) = code;
+      const uint2 code = q + 1 < P ? next_codes<FMT, false>(r) : next_codes<FMT, true>(r);
+      *reinterpret_cast<uint2*>(p.o.codes + (static_cast<int64_t>(dst) * P + q) * p.steps * 128 + gi * 8) = code;
     }
   }
   if constexpr (FMT == DEC_NV) {
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if ((tid & 31) == 0) atomicMax(&s_top, top);
     __syncthreads();
-    if (tid == 0) p.o.top[t] = s_top;
+    if (tid == 0) p.o.top[dst] = s_top;
   }
 }
 
-// The scale words of one token and K step for its P columns, from its blocks' exponents.
+// The scale words of one activation row and K step for its P columns, from its blocks' exponents.
 //   MXFP8  word of piece q: UE8M0 2^(e - 7 - 4 q) per block.
 //   NVFP4  one word per MMA, the same for all digits: UE4M3 2^(8 + e - top) per block (0 below 2^-9, which
-//          drops values under 2^-17 of the token's largest).
+//          drops values under 2^-17 of the row's largest).
 // Blocks that are not finite get a NaN scale.
 __device__ __forceinline__ uint32_t mx_scales(uint32_t e4, int q) {
   const uint32_t nan = __vcmpeq4(e4, 0xFFFFFFFFu);
@@ -313,58 +352,39 @@ __device__ __forceinline__ uint32_t nv_scales(uint32_t e4, int top) {
   return (code & ~nan) | (nan & 0x7F7F7F7Fu);
 }
 
-// Position of set bit n (from 0) of m; 64 when m has no more than n bits set.
-__device__ __forceinline__ int nth_set_bit(uint64_t m, int n) {
-  int base = 0;
-#pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) {
-    const int c = __popcll(m & ((1ull << s) - 1ull));
-    if (n >= c) {
-      n -= c;
-      m >>= s;
-      base += s;
-    }
-  }
-  return (m & 1ull) != 0 && n == 0 ? base : 64;
-}
-__device__ __forceinline__ int bits_below(uint64_t m, int t) { return __popcll(m & ((1ull << t) - 1ull)); }
-
-// The K steps of all units (128-row tiles, GATE_UP: tile x expert) form one sequence; a CTA runs through
-// a piece of it, whole units or one part of one.  Where several CTAs share a unit, each warp of an epilogue
-// that finishes its 32 rows last sums the parts, in their order (the result does not depend on which it is).
+// The K steps of all units (128-row tiles; MoE: of a chosen expert, for a group of its tokens) form one
+// sequence; a CTA runs through a part of one unit and then through whole ones.  Where several CTAs share a
+// unit, whoever finishes last sums the parts, in their order (the result does not depend on who it is).
 template <int FMT, int MODE>
 __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant__ CUtensorMap tm_w,
-                                                        const __grid_constant__ CUtensorMap tm_x, const DecParams p) {
+                                                           const __grid_constant__ CUtensorMap tm_x, const DecParams p) {
   constexpr int P = dec_pieces(FMT, MODE);
   constexpr int ATOMS = dec_atoms(FMT), EB = dec_exp_bytes(FMT);
-  constexpr int ACCS = MODE == DEC_GATE_UP ? 2 : 1;
-  constexpr int GROUP = dec_group(FMT);
+  constexpr bool UP = MODE == DEC_UP, MOE = MODE != DEC_LINEAR;
+  constexpr int ACCS = UP ? 2 : 1;
+  constexpr int GROUP = dec_group(FMT, MODE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const DecLayout& L = p.L;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);   // the copies landed and the columns' scales are in place
   uint64_t* empty = full + DEC_MAX_STAGES;                        // the MMAs have read the stage
-  uint64_t* acc_full = empty + DEC_MAX_STAGES;                    // a run's part of a unit is complete in TMEM
+  uint64_t* acc_full = empty + DEC_MAX_STAGES;                    // this CTA's part of a unit is complete in TMEM
   uint64_t* acc_empty = acc_full + 1;                             // the epilogue has read it
   uint64_t* drained = acc_empty + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_nact = reinterpret_cast<int*>(tmem_holder + 2);
-  int* s_row = reinterpret_cast<int*>(smem + L.misc);             // [32] operand row behind each token column
-  uint32_t* s_dirty = reinterpret_cast<uint32_t*>(s_row + 32);    // [stages] DOWN: columns of the stage that are not zero
-  uint32_t* s_fill = s_dirty + 16;                                // [stages] columns of the first steps
-  uint64_t* s_mask = reinterpret_cast<uint64_t*>(s_fill + 16);    // [E] tokens that chose the expert
-  // chosen experts (GATE_UP: and groups of their tokens): tokens, id + 1024 * group, first row of h
-  uint64_t* s_act_m = s_mask + p.E;
-  int* s_act_e = reinterpret_cast<int*>(s_act_m + p.max_active);
-  int* s_act_off = s_act_e + p.max_active;
+  int* s_last = s_nact + 1;
+  // MoE: tokens that chose the expert [E]; then the list of groups of tokens: expert, first pair, pairs
+  uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + L.misc);
+  int* s_act_e = reinterpret_cast<int*>(s_mask + p.E);
+  int* s_act_row = s_act_e + p.max_active;
+  int* s_act_n = s_act_row + p.max_active;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int chunk = static_cast<int>(blockIdx.x) % p.chunks;   // the chunks' CTAs run side by side
-  const int t0 = chunk * p.per_chunk;
-  const int tc = min(p.per_chunk, p.T - t0);
+  const int chunk = static_cast<int>(blockIdx.x) % p.chunks;   // LINEAR: the chunks' CTAs run side by side
 
-  if (MODE == DEC_GATE_UP && tid == 0) pdl_launch_dependents();
+  if (MOE && tid == 0) pdl_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < L.stages; ++s) {
       mbar_init(&full[s], 2);
@@ -383,8 +403,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   }
 
   // ---- routing: which tokens chose which expert, and the list of chosen experts ----
-  int nact = 1;
-  if constexpr (MODE != DEC_LINEAR) {
+  if constexpr (MOE) {
     for (int e = tid; e < p.E; e += DEC_THREADS) s_mask[e] = 0;
     __syncthreads();
     for (int i = tid; i < p.T * p.k; i += DEC_THREADS) {
@@ -393,23 +412,21 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     }
     __syncthreads();
     if (warp == 0) {
-      const uint64_t mine = tc == 64 ? ~0ull : ((1ull << tc) - 1ull) << t0;
       int n = 0, rows = 0;
       for (int base = 0; base < p.E; base += 32) {
-        const uint64_t m = base + lane < p.E ? s_mask[base + lane] : 0ull;
-        const int pop = __popcll(m);
-        const int entries = MODE == DEC_GATE_UP ? (pop + GROUP - 1) / GROUP : (m & mine) != 0 ? 1 : 0;
+        const int pop = base + lane < p.E ? __popcll(s_mask[base + lane]) : 0;
+        const int groups = (pop + GROUP - 1) / GROUP;
         if (__ballot_sync(0xFFFFFFFFu, pop != 0) == 0) continue;
-        int incl = pop | (entries << 16);   // two running sums in one word: rows < 2^12, entries < 2^12
+        int incl = pop | (groups << 16);   // two running sums in one word: pairs and groups are below 2^12
         for (int d = 1; d < 32; d <<= 1) {
           const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
           if (lane >= d) incl += o;
         }
-        const int pos = n + (incl >> 16) - entries, off = rows + (incl & 0xFFFF) - pop;
-        for (int g = 0; g < entries; ++g) {
-          s_act_e[pos + g] = base + lane + 1024 * g;
-          s_act_m[pos + g] = m;
-          s_act_off[pos + g] = off;
+        const int pos = n + (incl >> 16) - groups, row = rows + (incl & 0xFFFF) - pop;
+        for (int g = 0; g < groups; ++g) {
+          s_act_e[pos + g] = base + lane;
+          s_act_row[pos + g] = row + g * GROUP;
+          s_act_n[pos + g] = min(GROUP, pop - g * GROUP);
         }
         const int last = __shfl_sync(0xFFFFFFFFu, incl, 31);
         n += last >> 16;
@@ -422,79 +439,53 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  if constexpr (MODE != DEC_LINEAR) nact = *s_nact;
 
-  // ---- this CTA's run of K steps ----
-  const int su = MODE == DEC_GATE_UP ? 2 * p.steps : MODE == DEC_DOWN ? nact * p.steps : p.steps;   // per unit
-  const int units = MODE == DEC_GATE_UP ? nact * p.tiles : p.tiles;
-  // More units than CTAs: whole units, the same number for every CTA (so that some CTAs may have none: it is
-  // the memory, not the number of SMs, that has to be filled).  Fewer: as many CTAs as fit for each unit.
+  // ---- this CTA's piece of the sequence ----
+  const int su = UP ? 2 * p.steps : p.steps;                    // steps of a unit
+  const int units = MOE ? *s_nact * p.tiles : p.tiles;
+  // Every CTA takes the same number of whole units; the units left over are shared, each by as many CTAs as fit
+  // (and find DEC_MIN_STEPS steps).  The share comes first, so that adding its parts up is hidden.
   const int slots = static_cast<int>(gridDim.x) / p.chunks, cta = static_cast<int>(blockIdx.x) / p.chunks;
-  const int per_cta = (units + slots - 1) / slots;
-  const int per_unit = units == 0 || units > slots ? 1 : max(1, min(slots / units, su / DEC_MIN_STEPS));
-  int s_begin = 0, n_steps = 0;
-  if (per_unit == 1) {
-    s_begin = min(cta * per_cta, units) * su;
-    n_steps = min((cta + 1) * per_cta, units) * su - s_begin;
-  } else if (cta < units * per_unit) {
+  const int whole = units / slots, shared = units - whole * slots;
+  const int per_unit = shared == 0 ? 1 : max(1, min(slots / shared, su / DEC_MIN_STEPS));   // CTAs of a shared unit
+  int s_share = 0, n_share = 0;        // this CTA's steps of its share, and
+  const int s_whole = cta * whole * su, n_whole = whole * su;   // of its whole units
+  if (cta < shared * per_unit) {
     const int u = cta / per_unit, o = cta - u * per_unit;
-    s_begin = u * su + su * o / per_unit;
-    n_steps = u * su + su * (o + 1) / per_unit - s_begin;
+    s_share = (slots * whole + u) * su + su * o / per_unit;
+    n_share = (slots * whole + u) * su + su * (o + 1) / per_unit - s_share;
   }
-  // DOWN without a single choice: no steps, and every output is zero
-  const bool nothing = MODE == DEC_DOWN && nact == 0;
-
-  // Columns of a unit's MMA: how many tokens, and which row of the operand is behind token column c in a
-  // step of list entry a (-1: zeros).
-  auto columns = [&](int a) {
-    if constexpr (MODE == DEC_GATE_UP)
-      return min(GROUP, __popcll(s_act_m[a]) - (s_act_e[a] >> 10) * GROUP);
-    else
-      return tc;
-  };
-  auto token = [&](int c, int a) { return nth_set_bit(s_act_m[a], (s_act_e[a] >> 10) * GROUP + c); };   // GATE_UP
-  auto source_row = [&](int c, int a) -> int {
-    if constexpr (MODE == DEC_GATE_UP) return c < columns(a) ? token(c, a) : -1;
-    if constexpr (MODE == DEC_LINEAR) return c < tc ? t0 + c : -1;
-    if (c >= tc || !((s_act_m[a] >> (t0 + c)) & 1ull)) return -1;
-    return s_act_off[a] + bits_below(s_act_m[a], t0 + c);
-  };
-  auto mma_columns = [&](int a) { return (P * columns(a) + 15) & ~15; };
+  const int n_steps = n_share + n_whole;
+  // Activation rows of list entry a (LINEAR: of the chunk), and the columns of its MMA.
+  auto rows_of = [&](int a) { return MOE ? s_act_n[a] : min(p.per_chunk, p.T - chunk * p.per_chunk); };
+  auto first_row = [&](int a) { return MOE ? s_act_row[a] : chunk * p.per_chunk; };
+  auto mma_columns = [&](int a) { return (P * rows_of(a) + 15) & ~15; };
   // Place in the sequence: list entry, 128-row tile, K step, accumulator.  Divisions only to start with.
   struct Place {
     int a, tile, f, acc;
   };
-  auto place_of = [&](int s) {
+  auto place_of = [&](int i) {   // of this CTA's step i
     Place q{0, 0, 0, 0};
-    if (s >= units * su) return q;
+    if (i >= n_steps) return q;
+    const int s = i < n_share ? s_share + i : s_whole + i - n_share;
     const int u = s / su, r = s - u * su;
-    if constexpr (MODE == DEC_GATE_UP) {
-      q.a = u / p.tiles;
-      q.tile = u - q.a * p.tiles;
-      q.f = r >> 1;
-      q.acc = r & 1;
-    } else {
-      q.a = MODE == DEC_DOWN ? r / p.steps : 0;
-      q.tile = u;
-      q.f = r - q.a * p.steps;
-    }
+    q.a = u / p.tiles;
+    q.tile = u - q.a * p.tiles;
+    q.f = UP ? r >> 1 : r;
+    q.acc = UP ? r & 1 : 0;
     return q;
   };
-  auto advance = [&](Place& q) {
-    if constexpr (MODE == DEC_GATE_UP) {
-      q.acc ^= 1;
-      if (q.acc != 0 || ++q.f < p.steps) return;
-      q.f = 0;
-      if (++q.tile < p.tiles) return;
-      q.tile = 0;
-      ++q.a;
-    } else {
-      if (++q.f < p.steps) return;
-      q.f = 0;
-      if (MODE == DEC_DOWN && ++q.a < nact) return;
-      q.a = 0;
-      ++q.tile;
+  auto advance = [&](Place& q, int i) {   // from step i to the next
+    if (i + 1 == n_share) {
+      q = place_of(n_share);
+      return;
     }
+    if constexpr (UP) q.acc ^= 1;
+    if (q.acc != 0 || ++q.f < p.steps) return;
+    q.f = 0;
+    if (++q.tile < p.tiles) return;
+    q.tile = 0;
+    ++q.a;
   };
   // Stage of the ring, and the parity of its current use.
   struct Ring {
@@ -509,94 +500,41 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   };
 
   if (warp == 0) {
-    // ---------------- copies: one lane issues them, all lanes look up the columns' rows ----------------
-    // Token columns to copy into a stage.  DOWN: those of the step's expert, and zeros where an earlier
-    // step of the stage left another expert's token (at first: anything).
-    const uint32_t all_columns = tc >= 32 ? 0xFFFFFFFFu : (1u << tc) - 1u;
-    auto step_columns = [&](int a, int slot) -> uint32_t {
-      if constexpr (MODE != DEC_DOWN) {
-        const int n = columns(a);
-        return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
-      } else {
-        const uint32_t mine = static_cast<uint32_t>(s_act_m[a] >> t0) & all_columns;
-        const uint32_t cols = mine | s_dirty[slot];
-        s_dirty[slot] = mine;
-        return cols;
-      }
-    };
-    auto copy_weights = [&](const Place& q, int slot, uint32_t cols) {
-      int row = q.tile * 128;
-      if constexpr (MODE == DEC_GATE_UP) row += (s_act_e[q.a] & 1023) * 2 * p.F + q.acc * p.F;
-      if constexpr (MODE == DEC_DOWN) row += (s_act_e[q.a] & 1023) * p.tiles * 128;
-      mbar_arrive_expect_tx(&full[slot], DEC_A_STAGE + ATOMS * 512 +
-                                             (MODE == DEC_LINEAR ? p.per_chunk : __popc(cols)) * P * 128);
-      tma_load_2d(smem + slot * DEC_A_STAGE, &tm_w, &full[slot], q.f * 128, row);
-      bulk_load(smem + L.sfa + slot * ATOMS * 512,
-                p.w_sf + (static_cast<int64_t>(row >> 7) * p.kt + q.f * ATOMS) * 512, ATOMS * 512, &full[slot]);
-    };
-    int entry = -1;
-    auto set_rows = [&](int a) {   // the whole warp
-      if (MODE == DEC_LINEAR || a == entry) return;
-      entry = a;
-      __syncwarp();
-      if (lane < columns(a)) {
-        const int r = source_row(lane, a);
-        s_row[lane] = r < 0 ? p.zero_row : r;
-      }
-      __syncwarp();
-    };
-    auto copy_columns = [&](const Place& q, int slot, uint32_t cols) {
-      uint8_t* dst = smem + L.b + slot * L.b_stage;
-      if constexpr (MODE == DEC_LINEAR) {   // a box is a chunk's columns
-        tma_load_2d(dst, &tm_x, &full[slot], q.f * 128, t0 * P);
-      } else {                              // a box is a token's columns
-        for (; cols != 0; cols &= cols - 1u) {
-          const int c = __ffs(cols) - 1;
-          tma_load_2d(dst + c * (P * 128), &tm_x, &full[slot], q.f * 128, s_row[c] * P);
-        }
-      }
-    };
-    // fill the ring with weights before waiting for the activations the previous kernel writes
-    const int fill = min(n_steps, L.stages);
+    // ---------------- copies (one lane) ----------------
     int issued = 0;
-    Place q = place_of(s_begin);
     if (elect_one()) {
-      Place w = q;
-      for (int i = 0; i < fill; ++i, advance(w)) {
-        s_dirty[i] = all_columns;
-        s_fill[i] = step_columns(w.a, i);
-        copy_weights(w, i, s_fill[i]);
+      auto copy_weights = [&](const Place& q, int slot) {
+        int row = q.tile * 128;
+        if constexpr (MOE) row += (s_act_e[q.a] * ACCS + q.acc) * (p.tiles * 128);
+        mbar_arrive_expect_tx(&full[slot], DEC_A_STAGE + ATOMS * 512 + p.box_rows * P * 128);
+        tma_load_2d(smem + slot * DEC_A_STAGE, &tm_w, &full[slot], q.f * 128, row);
+        bulk_load(smem + L.sfa + slot * ATOMS * 512,
+                  p.w_sf + (static_cast<int64_t>(row >> 7) * p.kt + q.f * ATOMS) * 512, ATOMS * 512, &full[slot]);
+      };
+      // the unit's columns and whatever follows them: a box has a fixed height
+      auto copy_columns = [&](const Place& q, int slot) {
+        tma_load_2d(smem + L.b + slot * L.b_stage, &tm_x, &full[slot], q.f * 128, first_row(q.a) * P);
+      };
+      // fill the ring with weights before waiting for the activations the previous kernel writes
+      const int fill = min(n_steps, L.stages);
+      Place q = place_of(0), w = q;
+      for (int i = 0; i < fill; advance(w, i), ++i) copy_weights(w, i);
+      pdl_wait();
+      for (; issued < fill; advance(q, issued), ++issued) copy_columns(q, issued);
+      Ring r{0, 0};
+      for (; issued < n_steps; advance(q, issued), ++issued, next_stage(r)) {
+        if (!dec_wait(&empty[r.slot], r.phase, abort_flag, p, ERR_TIMEOUT_PRODUCER)) break;
+        copy_weights(q, r.slot);
+        copy_columns(q, r.slot);
       }
-    }
-    __syncwarp();
-    pdl_wait();
-    for (; issued < fill; ++issued, advance(q)) {
-      set_rows(q.a);
-      if (elect_one()) copy_columns(q, issued, s_fill[issued]);
-    }
-    Ring r{0, 0};
-    for (; issued < n_steps; ++issued, advance(q), next_stage(r)) {
-      set_rows(q.a);
-      bool ok = true;
-      if (elect_one()) {
-        ok = dec_wait(&empty[r.slot], r.phase, abort_flag, p, ERR_TIMEOUT_PRODUCER);
-        if (ok) {
-          const uint32_t cols = step_columns(q.a, r.slot);
-          copy_weights(q, r.slot, cols);
-          copy_columns(q, r.slot, cols);
-        }
-      }
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-    }
-    __syncwarp();
-    // every copy must have landed before the CTA may exit; after a timeout elsewhere the barriers may lack
-    // their other arrival, and one full drain wait is enough for all the copies
-    if (lane == 0)
+      // every copy must have landed before the CTA may exit; after a timeout elsewhere the barriers may lack
+      // their other arrival, and one full drain wait is enough for all the copies
       for (int i = max(0, issued - L.stages); i < issued; ++i)
         if (!mbar_wait_bounded(&full[i % L.stages], (i / L.stages) & 1, nullptr, p.drain_ns)) {
           atomicOr(p.err, ERR_TIMEOUT_DRAIN);
           break;
         }
+    }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- scale copies and MMAs (one lane) ----------------
@@ -606,16 +544,16 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       const uint64_t desc_sfa = sdesc_sf_atom(smem_u32(smem + L.sfa)), desc_sfb = sdesc_sf_atom(smem_u32(smem + L.sfb));
       bool ok = true, any = false;
       Ring r{0, 0}, before{0, 0};   // the stage of step i and that of step i - sf_sets
-      int set = 0;
-      int i = 0;
+      int i = 0, set = 0;
+      Place q = place_of(0);
       for (int seg = 0; ok && i < n_steps; ++seg) {
-        const int u = (s_begin + i) / su, i_end = min(n_steps, (u + 1) * su - s_begin);
-        const int n_mma = mma_columns(MODE == DEC_GATE_UP ? u / p.tiles : 0), nat = (n_mma + 127) >> 7;
+        const int a = q.a, tile = q.tile;
+        const int n_mma = mma_columns(a), nat = (n_mma + 127) >> 7;
         const uint32_t idesc = FMT == DEC_NV ? idesc_nvf4(128, n_mma) : idesc_mxf8_e4m3(128, n_mma);
         uint32_t started = 0;   // accumulators that hold something
         if (seg > 0 && !dec_wait(acc_empty, (seg - 1) & 1, abort_flag, p, ERR_TIMEOUT_MMA)) break;
         tc_fence_after();
-        for (; i < i_end; ++i, next_stage(r)) {
+        for (; i < n_steps && q.a == a && q.tile == tile; advance(q, i), ++i, next_stage(r)) {
           const int slot = r.slot;
           if (!dec_wait(&full[slot], r.phase, abort_flag, p, ERR_TIMEOUT_MMA)) {
             ok = false;
@@ -635,23 +573,21 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
           const uint64_t dsa = desc_sfa + slot * (ATOMS * 32), dsb = desc_sfb + slot * (L.sfb_stage >> 4);
           const uint32_t t_sfa = tmem + L.sf_col + set * L.sf_cols, t_sfb = t_sfa + 4 * ATOMS;
           if (++set == L.sf_sets) set = 0;
-          const int acc = MODE == DEC_GATE_UP ? (s_begin + i - u * su) & 1 : 0;
-          const uint32_t d = tmem + acc * L.n_max;
+          const uint32_t d = tmem + q.acc * L.n_max;
 #pragma unroll
           for (int m = 0; m < ATOMS; ++m) {
             tc_copy_sf(t_sfa + 4 * m, dsa + 32 * m);
-            for (int j = 0; j < nat; ++j)
-              tc_copy_sf(t_sfb + 4 * (m * nat + j), dsb + 32 * (m * nat + j));
+            for (int j = 0; j < nat; ++j) tc_copy_sf(t_sfb + 4 * (m * nat + j), dsb + 32 * (m * nat + j));
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t add = ((started >> acc) & 1u) | (k != 0 ? 1u : 0u);
+            const uint32_t add = ((started >> q.acc) & 1u) | (k != 0 ? 1u : 0u);
             if constexpr (FMT == DEC_NV)
               tc_mma_nvf4(d, da + 2 * k, db + 2 * k, idesc, t_sfa + 4 * k, t_sfb + 4 * nat * k, add);
             else
               tc_mma_mxf8(d, da + 2 * k, db + 2 * k, idesc_with_sf_id(idesc, k), t_sfa, t_sfb, add);
           }
-          started |= 1u << acc;
+          started |= 1u << q.acc;
           tc_commit(&empty[slot]);
           any = true;
         }
@@ -664,39 +600,33 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     }
     __syncwarp();
   } else if (warp < DEC_FIRST_EPI_WARP) {
-    // ---------------- the columns' scales: warp cw takes steps cw, cw + 2, ...; lane = token column ----------------
+    // ---------------- the columns' scales: warp cw takes steps cw, cw + 2, ... ----------------
     // Fewer warps than stages: when a warp waits for a slot's last use, the use before that one is known
     // to be over, as a wait by parity requires.
     const int cw = warp - 2;
     pdl_wait();
-    // MXFP8, and NVFP4 with more than eight tokens: lane = token column, all its words; NVFP4 with up to
-    // eight: lane = (word, token), one of the token's four words.
-    const bool spread = FMT == DEC_NV && tc <= 8 && MODE != DEC_GATE_UP;
+    // MXFP8, and NVFP4 with more than eight rows: lane = row, all its words; NVFP4 with up to eight:
+    // lane = (word, row), one of the row's four words.
     struct Scales {
       uint32_t e[ATOMS];
-      int c, row, top, n, nat;   // token column and its operand row (-1: zero), columns, atoms per MMA
+      int c, top, n, nat;   // row of the unit (lanes past the last: none) and its reference, rows, atoms per MMA
+      bool spread;
     };
-    int top = 0;
-    if (FMT == DEC_NV && MODE != DEC_GATE_UP) {
-      const int c = spread ? lane & 7 : lane;
-      if (c < tc) top = p.in.top[t0 + c];   // one reference per token for all its experts: they share the accumulator
-    }
-    int entry = -1;
+    int entry = -1, row = 0;
     Scales cur{}, next{};
     auto load = [&](const Place& q, Scales& v) {
       if (q.a != entry) {
         entry = q.a;
-        v.c = spread ? lane & 7 : lane;
-        v.row = source_row(v.c, q.a);
-        v.n = columns(q.a);
+        v.n = rows_of(q.a);
         v.nat = (mma_columns(q.a) + 127) >> 7;
-        if (FMT == DEC_NV && MODE == DEC_GATE_UP && v.row >= 0) top = p.in.top[v.row];
-        v.top = top;
+        v.spread = FMT == DEC_NV && v.n <= 8;
+        v.c = v.spread ? lane & 7 : lane;
+        row = first_row(q.a) + min(v.c, v.n - 1);
+        if constexpr (FMT == DEC_NV) v.top = p.in.top[row];
       }
-      if (v.row < 0) return;
-      const uint8_t* src = p.in.exps + (static_cast<int64_t>(v.row) * p.steps + q.f) * EB;
+      const uint8_t* src = p.in.exps + (static_cast<int64_t>(row) * p.steps + q.f) * EB;
       if constexpr (FMT == DEC_NV) {
-        if (spread) {
+        if (v.spread) {
           v.e[0] = (q.f * 4 + (lane >> 3)) * 64 < p.K ? *reinterpret_cast<const uint32_t*>(src + (lane >> 3) * 4) : 0u;
         } else {
           const uint4 w = *reinterpret_cast<const uint4*>(src);
@@ -713,7 +643,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     auto word = [&](uint8_t* sf, int nat, int m, int col) {
       return reinterpret_cast<uint32_t*>(sf + (m * nat + (col >> 7)) * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4);
     };
-    Place q = place_of(s_begin + cw);
+    Place q = place_of(cw);
     if (cw < n_steps) load(q, cur);
     int slot = cw;
     uint32_t phase = 1;   // parity of the slot's previous use
@@ -721,16 +651,15 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       next = cur;
       if (i + DEC_SCALE_WARPS < n_steps) {
 #pragma unroll
-        for (int z = 0; z < DEC_SCALE_WARPS; ++z) advance(q);
+        for (int z = 0; z < DEC_SCALE_WARPS; ++z) advance(q, i + z);
         load(q, next);
       }
-      uint32_t w[ATOMS];   // a zero column: 2^-127 (MXFP8) or 0
+      uint32_t w[ATOMS];
       if constexpr (FMT == DEC_NV) {
-        const uint32_t live = cur.row >= 0 ? 0xFFFFFFFFu : 0u;
-        w[0] = nv_scales(cur.e[0], cur.top) & live;
-        if (!spread)
+        w[0] = nv_scales(cur.e[0], cur.top);
+        if (!cur.spread)
 #pragma unroll
-          for (int m = 1; m < 4; ++m) w[m] = nv_scales(cur.e[m], cur.top) & live;
+          for (int m = 1; m < 4; ++m) w[m] = nv_scales(cur.e[m], cur.top);
       }
       if (i >= L.stages && !dec_warp_wait(&empty[slot], phase, abort_flag, p, ERR_TIMEOUT_SF, lane)) break;
       uint8_t* sf = smem + L.sfb + slot * L.sfb_stage;
@@ -739,8 +668,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         for (int d = 0; d < P; ++d) {
           const int col = cur.c * P + d;
           if constexpr (FMT == DEC_MX) {
-            *word(sf, 1, 0, col) = cur.row >= 0 ? mx_scales(cur.e[0], d) : 0u;
-          } else if (spread) {
+            *word(sf, 1, 0, col) = mx_scales(cur.e[0], d);
+          } else if (cur.spread) {
             *word(sf, 1, lane >> 3, col) = w[0];
           } else {
             uint32_t* dst = word(sf, cur.nat, 0, col);
@@ -766,159 +695,166 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     float alpha = 1.0f;
     if constexpr (FMT == DEC_NV) alpha = 1.0f / nv_encode_scale(__ldg(p.w_amax));
-
-    // y (DOWN, LINEAR) or h (GATE_UP) of token column c and this thread's row of the tile
-    auto put_out = [&](int c, int tile, float v) {
-      p.out[static_cast<int64_t>(t0 + c) * p.tiles * 128 + tile * 128 + row] =
-          static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
-    };
-    auto put_h = [&](int c, int t, int a, int tile, float gate, float gs, float us) {
-      const float hv = gate * (gs / (1.0f + expf(-gs))) * us;
-      // h -> columns of DOWN: a block is the warp's 32 rows (MXFP8) or one half of them (NVFP4)
-      constexpr int PH = dec_pieces(FMT, DEC_DOWN);
-      const int64_t hr = s_act_off[a] + (s_act_e[a] >> 10) * GROUP + c;
-      const int k = tile * 128 + row;   // value of h
-      uint32_t m = __float_as_uint(hv) & 0x7FFFFFFFu;
-      if constexpr (FMT == DEC_MX) {
-        m = __reduce_max_sync(0xFFFFFFFFu, m);
-      } else {
-#pragma unroll
-        for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-      }
-      const int eb = block_exponent(m);
-      if ((lane & (FMT == DEC_NV ? 15 : 31)) == 0)
-        p.h.exps[hr * p.h_steps * EB + (FMT == DEC_NV ? k >> 4 : k >> 5)] = static_cast<uint8_t>(eb + 127);
-      const float inv = block_multiplier<FMT>(eb);
-      uint64_t r = f2_pack(hv * inv, 0.0f);
-      uint8_t* dst = p.h.codes + hr * PH * p.h_steps * 128 + (FMT == DEC_NV ? k >> 1 : k);
-#pragma unroll
-      for (int q = 0; q < PH; ++q, dst += p.h_steps * 128) {
-        const uint64_t n = q + 1 < PH ? next_piece<FMT, false>(r) : next_piece<FMT, true>(r);
-        if constexpr (FMT == DEC_MX) {
-          *dst = static_cast<uint8_t>(e4m3x2_f2(n) & 0xFFu);
-        } else {
-          const float other = __shfl_down_sync(0xFFFFFFFFu, f2_lo(n), 1);
-          const uint32_t code = e2m1x8(f2_lo(n), other, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f) & 0xFFu;
-          if ((lane & 1) == 0) *dst = static_cast<uint8_t>(code);
-        }
-      }
-      if constexpr (FMT == DEC_NV) {
-        const int top = __reduce_max_sync(0xFFFFFFFFu, eb);
-        if (lane == 0) atomicMax(p.h.top + t, top);
-      }
-    };
-
-    if (nothing && cta < p.tiles)
-      for (int tile = cta; tile < p.tiles; tile += static_cast<int>(gridDim.x) / p.chunks)
-        for (int c = 0; c < tc; ++c) put_out(c, tile, 0.0f);
-
-    int i = 0, top = 0;
+    int i = 0;
+    Place q = place_of(0);
     for (int seg = 0; i < n_steps; ++seg) {
-      const int u = (s_begin + i) / su, r0 = s_begin + i - u * su;
-      const int i_end = min(n_steps, (u + 1) * su - s_begin), r1 = r0 + i_end - i;
-      const int a = MODE == DEC_GATE_UP ? u / p.tiles : 0, tile = MODE == DEC_GATE_UP ? u - a * p.tiles : u;
-      const int nc = columns(a);
-      // lane c: token and routing weight of token column c (a token that lists the expert twice adds its
-      // weights), and the exponent its scales refer to
-      float gate = 0.0f;
-      int tok = lane < tc ? t0 + lane : 0;
-      if constexpr (MODE == DEC_GATE_UP) {
-        if (lane < nc) {
-          tok = token(lane, a);
-          for (int q = 0; q < p.k; ++q)
-            if (__ldg(p.experts + tok * p.k + q) == (s_act_e[a] & 1023))
-              gate += p.gates != nullptr ? __ldg(p.gates + tok * p.k + q) : 1.0f;
-        }
-      }
-      if (FMT == DEC_NV && (MODE == DEC_GATE_UP || seg == 0)) top = lane < nc ? p.in.top[tok] : 0;
-      // the parts of the CTAs that share the unit
-      const bool whole = per_unit == 1;
+      const bool share = i < n_share && per_unit > 1;
+      const int r0 = q.f * ACCS + q.acc, r1 = i < n_share ? r0 + n_share : su;   // the part's steps of the unit
+      const int u = share ? cta / per_unit : 0;                                    // which shared unit
+      const int n = rows_of(q.a), row0 = first_row(q.a), tile = q.tile;
+      float unscale = 1.0f;   // lane c: of row c's sums
+      if constexpr (FMT == DEC_NV) unscale = ldexpf(alpha, p.in.top[row0 + min(lane, n - 1)] - 9);
+      // y of activation row c and this thread's weight row
+      auto put = [&](int c, float v) {
+        const int64_t o = static_cast<int64_t>(row0 + c) * (p.tiles * 128) + tile * 128 + row;
+        if constexpr (MODE == DEC_DOWN) p.y[o] = v;
+        else p.out[o] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+      };
+      // part o of the unit: [accumulator][activation row][128 weight rows], in the place of the CTA that has it
+      // (whole units of UP pass through a second place: the first may still be read by another CTA)
       auto part_of = [&](int o) {
-        return p.part + static_cast<int64_t>((u * per_unit + o) * p.chunks + chunk) * p.part_slot + row;
+        const int c = share ? u * per_unit + o : slots + cta;
+        return p.part + static_cast<int64_t>(c * p.chunks + chunk) * p.part_slot;
       };
 
       if (!dec_warp_wait(acc_full, seg & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane)) break;
       tc_fence_after();
-      const bool has[2] = {MODE != DEC_GATE_UP || r1 - r0 > 1 || (r0 & 1) == 0, r1 - r0 > 1 || (r0 & 1) == 1};
-      for (int c0 = 0; c0 < nc; c0 += 8) {
-        float v[ACCS][8];
+      float* mine = part_of(share ? cta - u * per_unit : 0) + row;
+      const int parts = share ? per_unit : 1;
+      const bool has[2] = {!UP || r1 - r0 > 1 || (r0 & 1) == 0, r1 - r0 > 1 || (r0 & 1) == 1};
+#pragma unroll 1
+      for (int c0 = 0; c0 < n; c0 += 8) {
 #pragma unroll
         for (int b = 0; b < ACCS; ++b) {
           uint32_t d[8 * P];
 #pragma unroll
-          for (int q = 0; q < P; ++q) tmem_ld_32x32b_x8(t_row + b * L.n_max + c0 * P + q * 8, d + q * 8);
+          for (int z = 0; z < P; ++z) tmem_ld_32x32b_x8(t_row + b * L.n_max + c0 * P + z * 8, d + z * 8);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float x = __uint_as_float(d[j * P + P - 1]);
 #pragma unroll
-            for (int q = P - 2; q >= 0; --q)   // smallest first; a digit's place is 1/8 of the one before
-              x = FMT == DEC_NV ? fmaf(x, 0.125f, __uint_as_float(d[j * P + q])) : x + __uint_as_float(d[j * P + q]);
-            if constexpr (FMT == DEC_NV) x = ldexpf(x * alpha, __shfl_sync(0xFFFFFFFFu, top, c0 + j) - 9);
-            v[b][j] = has[b] ? x : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = c0 + j;
-          if (c >= nc) break;
-          if (!whole) {
-#pragma unroll
-            for (int b = 0; b < ACCS; ++b) part_of(cta - u * per_unit)[(b * nc + c) * 128] = v[b][j];
-          } else if constexpr (MODE == DEC_GATE_UP) {
-            put_h(c, __shfl_sync(0xFFFFFFFFu, tok, c), a, tile, __shfl_sync(0xFFFFFFFFu, gate, c), v[0][j],
-                  v[ACCS - 1][j]);
-          } else {
-            put_out(c, tile, v[0][j]);
+            for (int z = P - 2; z >= 0; --z)   // smallest first; a digit's place is 1/8 of the one before
+              x = FMT == DEC_NV ? fmaf(x, 0.125f, __uint_as_float(d[j * P + z])) : x + __uint_as_float(d[j * P + z]);
+            if constexpr (FMT == DEC_NV) x *= __shfl_sync(0xFFFFFFFFu, unscale, c0 + j);
+            if (c0 + j >= n) continue;
+            if (!UP && !share) put(c0 + j, x);
+            else mine[(b * n + c0 + j) * 128] = has[b] ? x : 0.0f;
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
-      if (!whole) {
-        int before = 0;
-        if (lane == 0) {
-          __threadfence();
-          before = atomicAdd(p.counters + (static_cast<int64_t>(chunk) * units + u) * 4 + quarter, 1);
-          __threadfence();
-        }
-        if (__shfl_sync(0xFFFFFFFFu, before, 0) == per_unit - 1) {
-          // 4 tokens x 4 parts of loads in flight; added in the order of the parts
-          constexpr int TB = 4, OB = 4;
-          for (int c0 = 0; c0 < nc; c0 += TB) {
-            float v[TB][ACCS] = {};
-            for (int o0 = 0; o0 < per_unit; o0 += OB) {
-              float x[OB][TB][ACCS];
+      if (lane == 0) mbar_arrive(acc_empty);   // the next unit's MMAs may begin
+      int* counter = p.counters + (chunk * shared + u) * 4;
+
+      if constexpr (!UP) {
+        // Each warp for its 32 weight rows: the last of the unit's parts adds them all up, in order.
+        if (share) {
+          int before = 0;
+          if (lane == 0) {
+            __threadfence();
+            before = atomicAdd(counter + quarter, 1);
+            __threadfence();
+          }
+          if (__shfl_sync(0xFFFFFFFFu, before, 0) == parts - 1) {
+            constexpr int TB = 4, OB = 4;   // 4 rows x 4 parts of loads in flight
+#pragma unroll 1
+            for (int c0 = 0; c0 < n; c0 += TB) {
+              float sum[TB] = {};
+#pragma unroll 1
+              for (int o0 = 0; o0 < parts; o0 += OB) {
+                float x[OB][TB];
 #pragma unroll
-              for (int o = 0; o < OB; ++o) {
-                const float* src = part_of(min(o0 + o, per_unit - 1));
+                for (int o = 0; o < OB; ++o) {
+                  const float* src = part_of(min(o0 + o, parts - 1)) + row;
 #pragma unroll
-                for (int j = 0; j < TB; ++j)
+                  for (int j = 0; j < TB; ++j)
+                    x[o][j] = o0 + o < parts && c0 + j < n ? __ldcg(src + (c0 + j) * 128) : 0.0f;
+                }
 #pragma unroll
-                  for (int b = 0; b < ACCS; ++b)
-                    x[o][j][b] = o0 + o < per_unit && c0 + j < nc ? __ldcg(src + (b * nc + c0 + j) * 128) : 0.0f;
+                for (int o = 0; o < OB; ++o)
+#pragma unroll
+                  for (int j = 0; j < TB; ++j) sum[j] += x[o][j];
               }
 #pragma unroll
-              for (int o = 0; o < OB; ++o)
-#pragma unroll
-                for (int j = 0; j < TB; ++j)
-#pragma unroll
-                  for (int b = 0; b < ACCS; ++b) v[j][b] += x[o][j][b];
-            }
-#pragma unroll
-            for (int j = 0; j < TB; ++j) {
-              if (c0 + j >= nc) break;
-              if constexpr (MODE == DEC_GATE_UP)
-                put_h(c0 + j, __shfl_sync(0xFFFFFFFFu, tok, c0 + j), a, tile, __shfl_sync(0xFFFFFFFFu, gate, c0 + j),
-                      v[j][0], v[j][ACCS - 1]);
-              else
-                put_out(c0 + j, tile, v[j][0]);
+              for (int j = 0; j < TB; ++j)
+                if (c0 + j < n) put(c0 + j, sum[j]);
             }
           }
         }
+      } else {
+        // h from the gate and up sums, as columns of DOWN: a thread takes 8 (MXFP8) or 16 (NVFP4) values of one
+        // activation row, the same way as k_split_x.
+        epi_barrier();   // the other warps' rows are written
+        bool last = true;
+        if (share) {
+          if (tid == DEC_FIRST_EPI_WARP * 32) {
+            __threadfence();
+            *s_last = atomicAdd(counter, 1) == parts - 1 ? 1 : 0;
+            __threadfence();
+          }
+          epi_barrier();
+          last = *s_last != 0;
+        }
+        constexpr int PH = dec_pieces(FMT, DEC_DOWN);
+        constexpr int VALS = FMT == DEC_NV ? 16 : 8, PER_ROW = 128 / VALS;
+        const int g = (tid & 127) % PER_ROW, k0 = tile * 128 + g * VALS;   // values k0 .. of h
+        const int64_t pitch = static_cast<int64_t>(p.h_steps) * 128;
+#pragma unroll 1
+        for (int cb = 0; last && cb < n; cb += 128 / PER_ROW) {
+          const int c = cb + (tid & 127) / PER_ROW;
+          const bool live = c < n;
+          const int64_t hr = row0 + min(c, n - 1);
+          const float gate = p.gate[hr];
+          float h[VALS];
+          {
+            float gs[VALS] = {}, us[VALS] = {};
+#pragma unroll 1
+            for (int o = 0; o < parts; ++o) {
+              const float* src = part_of(o) + min(c, n - 1) * 128 + g * VALS;
+#pragma unroll
+              for (int z = 0; z < VALS; z += 4) {
+                const float4 a = __ldcg(reinterpret_cast<const float4*>(src + z));
+                const float4 b = __ldcg(reinterpret_cast<const float4*>(src + n * 128 + z));
+                gs[z] += a.x; gs[z + 1] += a.y; gs[z + 2] += a.z; gs[z + 3] += a.w;
+                us[z] += b.x; us[z + 1] += b.y; us[z + 2] += b.z; us[z + 3] += b.w;
+              }
+            }
+#pragma unroll
+            for (int z = 0; z < VALS; ++z) h[z] = gate * (gs[z] / (1.0f + expf(-gs[z]))) * us[z];
+          }
+          uint32_t m = 0;
+#pragma unroll
+          for (int z = 0; z < VALS; ++z) m = max(m, __float_as_uint(h[z]) & 0x7FFFFFFFu);
+          if constexpr (FMT == DEC_MX) {   // four threads a block
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          }
+          const int eb = block_exponent(m);
+          if (live && (FMT == DEC_NV || (g & 3) == 0))
+            p.h.exps[hr * p.h_steps * EB + (FMT == DEC_NV ? k0 >> 4 : k0 >> 5)] = static_cast<uint8_t>(eb + 127);
+          const uint64_t inv2 = f2_pack(block_multiplier<FMT>(eb), block_multiplier<FMT>(eb));
+          uint64_t r[VALS / 2];
+#pragma unroll
+          for (int z = 0; z < VALS / 2; ++z) r[z] = f2_mul(f2_pack(h[2 * z], h[2 * z + 1]), inv2);
+          uint8_t* dst = p.h.codes + hr * PH * pitch + (FMT == DEC_NV ? k0 >> 1 : k0);
+#pragma unroll
+          for (int d = 0; d < PH; ++d) {
+            const uint2 code = d + 1 < PH ? next_codes<FMT, false>(r) : next_codes<FMT, true>(r);
+            if (live) *reinterpret_cast<uint2*>(dst + d * pitch) = code;
+          }
+          if constexpr (FMT == DEC_NV) {   // eight threads a row
+            int t = live ? eb : -128;
+#pragma unroll
+            for (int d = 4; d >= 1; d >>= 1) t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, d));
+            if (live && g == 0) atomicMax(p.h.top + hr, t);
+          }
+        }
+        epi_barrier();   // all have read the parts before the next unit overwrites them
       }
-      i = i_end;
+      i += r1 - r0;
+      q = place_of(i);
     }
   }
   tc_fence_before();
@@ -927,6 +863,25 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     tc_fence_after();
     tmem_dealloc(tmem, DEC_TMEM_COLS);
   }
+}
+
+// out[t] = sum of the pairs' rows y[row_of[t, j]], j in order (-1: none).  Four columns per thread.
+__global__ void __launch_bounds__(256) k_sum_rows(const float* y, const int* row_of, int k, int H, uint16_t* out) {
+  pdl_wait();
+  const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (c >= H) return;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int r = row_of[t * k + j];
+    if (r < 0) continue;
+    const float4 x = *reinterpret_cast<const float4*>(y + static_cast<int64_t>(r) * H + c);
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  *reinterpret_cast<uint2*>(out + static_cast<int64_t>(t) * H + c) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 // ---- host side -------------------------------------------------------------------------------
@@ -964,20 +919,20 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
 
 constexpr int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
-// Shared memory for units of `tokens` token columns: half an SM with at least four stages, else a whole one.
-bool dec_layout(int fmt, int mode, int tokens, int E, int max_active, DecLayout* out) {
-  const int n = round_up(dec_pieces(fmt, mode) * tokens, 16);
+// Shared memory for units of `rows` activation rows: half an SM with at least three stages, else a whole one.
+bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* out) {
+  const int n = round_up(dec_pieces(fmt, mode) * rows, 16);
   DecLayout L{};
   L.b_stage = n * 128;
   L.sfb_stage = dec_atoms(fmt) * ((n + 127) / 128) * 512;
-  const int sfa = dec_atoms(fmt) * 512, bars = 384;
-  const int fixed = 1024 + bars + 256 + (mode == DEC_LINEAR ? 0 : round_up(E * 8 + max_active * 16, 16));
-  const int stage = DEC_A_STAGE + sfa + L.b_stage + L.sfb_stage;
   L.n_max = n;
-  L.sf_col = round_up((mode == DEC_GATE_UP ? 2 : 1) * n, 4);
+  L.sf_col = (mode == DEC_UP ? 2 : 1) * n;
   L.sf_cols = 4 * dec_atoms(fmt) * (1 + (n + 127) / 128);
+  const int sfa = dec_atoms(fmt) * 512, bars = 384;
+  const int fixed = 1024 + bars + (mode == DEC_LINEAR ? 0 : round_up(E * 8 + max_active * 12, 16));
+  const int stage = DEC_A_STAGE + sfa + L.b_stage + L.sfb_stage;
   L.smem = DEC_SMEM_HALF;
-  if ((L.smem - fixed) / stage < 4) L.smem = DEC_SMEM_FULL;
+  if ((L.smem - fixed) / stage < 3) L.smem = DEC_SMEM_FULL;
   L.stages = std::min(DEC_MAX_STAGES, (L.smem - fixed) / stage);
   L.sf_sets = std::min(L.stages, (static_cast<int>(DEC_TMEM_COLS) - L.sf_col) / L.sf_cols);
   if (L.stages < 3 || L.sf_sets < 2) return false;
@@ -990,6 +945,9 @@ bool dec_layout(int fmt, int mode, int tokens, int E, int max_active, DecLayout*
   return true;
 }
 static_assert(2 * DEC_MAX_STAGES * 8 + 3 * 8 + 16 <= 384, "barriers and flags");
+static_assert(dec_group(DEC_MX, DEC_DOWN) * 3 <= 160 && dec_group(DEC_MX, DEC_UP) * 2 * 2 <= 160 &&
+                  dec_group(DEC_NV, DEC_UP) * 5 * 2 <= 160 && DEC_CHUNK * 5 <= 160,
+              "accumulators");
 
 // Per-device set-up of one kernel instance (dynamic shared memory, and the carve-out that lets two CTAs
 // share an SM); returns the number of SMs, 0 on failure.
@@ -1028,8 +986,9 @@ struct DecLaunch {
 };
 
 template <int FMT, int MODE>
-bool dec_launch(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const DecParams& p, int ctas, cudaStream_t stream) {
-  DecLaunch l(ctas, DEC_THREADS, p.L.smem, stream);
+bool dec_launch(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const DecParams& p, int sms, cudaStream_t stream) {
+  const int ctas = p.L.smem == DEC_SMEM_HALF ? 2 * sms : sms;
+  DecLaunch l(ctas / p.chunks * p.chunks, DEC_THREADS, p.L.smem, stream);
   return cudaLaunchKernelEx(&l.cfg, k_decode<FMT, MODE>, tm_w, tm_x, p) == cudaSuccess;
 }
 
@@ -1046,11 +1005,11 @@ DecOperandLayout dec_operand(int fmt, int pieces, size_t at, int64_t rows, int64
   DecOperandLayout o{};
   o.pieces = pieces;
   o.steps = (K + dec_step_values(fmt) - 1) / dec_step_values(fmt);
-  o.code_rows = (rows + 1) * pieces;
+  o.code_rows = rows * pieces;
   o.codes = at;
   o.exps = align256(o.codes + static_cast<size_t>(o.code_rows) * o.steps * 128);
   o.top = align256(o.exps + static_cast<size_t>(rows) * o.steps * dec_exp_bytes(fmt));
-  o.end = align256(o.top + DEC_MAX_TOKENS * sizeof(int));
+  o.end = align256(o.top + static_cast<size_t>(rows) * sizeof(int));
   return o;
 }
 DecOperand dec_pointers(uint8_t* base, const DecOperandLayout& o) {
@@ -1060,10 +1019,11 @@ DecOperand dec_pointers(uint8_t* base, const DecOperandLayout& o) {
 // Workspace sizes do not depend on the device: room for the parts of at most this many CTAs.
 constexpr int DEC_MAX_CTAS = 320;
 
-// Workspace: error word (256 bytes), columns of x, columns of h, counters, parts.
+// Workspace of the MoE layer: error word (256 bytes), columns of x and of h, rows of y, routing weights and
+// numbers of the pairs, counters, parts.
 struct DecWs {
   DecOperandLayout x, h;
-  size_t counters, part, end;
+  size_t y, gate, row_of, counters, part, end;
   int64_t n_up, n_down;   // counters of the two kernels
   int max_active;
 };
@@ -1072,63 +1032,45 @@ bool dec_ws_layout(int fmt, int64_t T, int k, int64_t H, int64_t F, int E, DecWs
       H > INT32_MAX || F > INT32_MAX)
     return false;
   DecWs w{};
-  w.max_active = static_cast<int>(std::min<int64_t>(E, T * k) + T * k / dec_group(fmt));
-  w.x = dec_operand(fmt, dec_pieces(fmt, DEC_GATE_UP), 256, T, H);
-  w.h = dec_operand(fmt, dec_pieces(fmt, DEC_DOWN), w.x.end, T * k, F);
-  w.n_up = 4 * w.max_active * ((F + 127) / 128);
-  w.n_down = 4 * ((T + DEC_CHUNK - 1) / DEC_CHUNK) * ((H + 127) / 128);
-  w.counters = w.h.end;
+  const int64_t pairs = T * k;
+  const int group = dec_group(fmt, DEC_UP);
+  w.max_active = static_cast<int>(std::min<int64_t>(E, pairs) + pairs / group);
+  w.x = dec_operand(fmt, dec_pieces(fmt, DEC_UP), 256, pairs, H);
+  w.h = dec_operand(fmt, dec_pieces(fmt, DEC_DOWN), w.x.end, pairs, F);
+  // only units that are shared use counters, and those are fewer than the CTAs
+  w.n_up = 4 * std::min<int64_t>(w.max_active * ((F + 127) / 128), DEC_MAX_CTAS);
+  w.n_down = 4 * std::min<int64_t>(w.max_active * ((H + 127) / 128), DEC_MAX_CTAS);
+  w.y = w.h.end;
+  w.gate = align256(w.y + static_cast<size_t>(pairs) * H * sizeof(float));
+  w.row_of = align256(w.gate + static_cast<size_t>(pairs) * sizeof(float));
+  w.counters = align256(w.row_of + static_cast<size_t>(pairs) * sizeof(int));
   w.part = align256(w.counters + static_cast<size_t>(w.n_up + w.n_down) * sizeof(int));
-  const int64_t tokens = std::min<int64_t>(T, DEC_CHUNK), up = std::min<int64_t>(T, dec_group(fmt));
-  w.end = w.part + static_cast<size_t>(DEC_MAX_CTAS) * std::max(tokens, 2 * up) * 128 * sizeof(float);
+  w.end = w.part + static_cast<size_t>(2 * DEC_MAX_CTAS) * 2 * std::min<int64_t>(T, group) * 128 * sizeof(float);
   *out = w;
   return true;
 }
 
-// Linear: error word, columns of x, counters, parts.
+// Workspace of a linear: error word, columns of x, counters, parts.
 struct LinWs {
   DecOperandLayout x;
   size_t counters, part, end;
   int64_t n_counters;
 };
-LinWs lin_ws_layout(int fmt, int64_t T, int64_t K, int64_t N) {
+LinWs lin_ws_layout(int fmt, int64_t T, int64_t K) {
   LinWs w{};
   w.x = dec_operand(fmt, dec_pieces(fmt, DEC_LINEAR), 256, T, K);
-  w.n_counters = 4 * ((T + DEC_CHUNK - 1) / DEC_CHUNK) * ((N + 127) / 128);
-  w.part = w.x.end;
-  // the counters come last: their number depends on N
-  w.counters = w.part + static_cast<size_t>(DEC_MAX_CTAS) * std::min<int64_t>(T, DEC_CHUNK) * 128 * sizeof(float);
-  w.end = w.counters + static_cast<size_t>(w.n_counters) * sizeof(int);
+  w.n_counters = 4 * DEC_MAX_CTAS;   // chunks * units that are shared: fewer than the CTAs
+  w.counters = w.x.end;
+  w.part = align256(w.counters + static_cast<size_t>(w.n_counters) * sizeof(int));
+  w.end = w.part + static_cast<size_t>(DEC_MAX_CTAS) * std::min<int64_t>(T, DEC_CHUNK) * 128 * sizeof(float);
   return w;
 }
-constexpr int64_t LIN_WS_ROWS = 1 << 20;   // rows of W a workspace of matvec_workspace_size() serves
 
-// The first kernel of a call (see k_split_x); `experts` and the h operand only for the MoE layer.
-template <int FMT>
-bool split_launch(const void* x, const DecParams& p, const DecOperandLayout& xl, const DecOperandLayout* hl,
-                  int n_counters, cudaStream_t stream) {
-  SplitParams q{};
-  q.x = static_cast<const uint16_t*>(x);
-  q.o = p.in;
-  q.err = p.err;
-  q.counters = p.counters;
-  q.n_counters = n_counters;
-  q.T = p.T;
-  q.K = p.K;
-  q.steps = p.steps;
-  q.zero_row[0] = reinterpret_cast<uint4*>(p.in.codes + (xl.code_rows - xl.pieces) * xl.steps * 128);
-  q.zero_n[0] = static_cast<int>(xl.steps * 8 * xl.pieces);
-  if (hl != nullptr) {
-    q.experts = p.experts;
-    q.n_ids = p.T * p.k;
-    q.E = p.E;
-    q.h_top = p.h.top;
-    q.n_top = p.T;
-    q.zero_row[1] = reinterpret_cast<uint4*>(p.h.codes + (hl->code_rows - hl->pieces) * hl->steps * 128);
-    q.zero_n[1] = static_cast<int>(hl->steps * 8 * hl->pieces);
-  }
-  DecLaunch l(p.T, std::min(SPLIT_THREADS, round_up(p.K / (FMT == DEC_NV ? 16 : 8), 32)), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, k_split_x<FMT>, q) == cudaSuccess;
+// The first kernel of a call (see k_split_x).
+template <int FMT, bool BY_PAIR>
+bool split_launch(const SplitParams& q, cudaStream_t stream) {
+  DecLaunch l(BY_PAIR ? q.T * q.k : q.T, std::min(SPLIT_THREADS, round_up(q.K / (FMT == DEC_NV ? 16 : 8), 32)), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, k_split_x<FMT, BY_PAIR>, q) == cudaSuccess;
 }
 
 template <int FMT>
@@ -1155,79 +1097,94 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
     return MXFP8_ERR_INVALID_ARG;
   if (FMT == DEC_NV && (w1_amax == nullptr || w2_amax == nullptr)) return MXFP8_ERR_INVALID_ARG;
   // steps of all units, as the kernels count them
-  const int64_t act = ws.max_active, up_units = act * (F / 128);
-  if (up_units * 2 * ws.x.steps > INT32_MAX || act * ws.h.steps * (H / 128) > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
+  const int64_t act = ws.max_active;
+  if (act * (F / 128) * 2 * ws.x.steps > INT32_MAX || act * (H / 128) * ws.h.steps > INT32_MAX)
+    return MXFP8_ERR_UNSUPPORTED;
 
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  const uint64_t code_div = FMT == DEC_NV ? 2 : 1;   // values per code byte
+  const uint64_t per_byte = FMT == DEC_NV ? 2 : 1;   // values per code byte
+  const int group = std::min(static_cast<int>(T), dec_group(FMT, DEC_UP));
   CUtensorMap m1, m2, mx, mh;
-  if (!make_map(&m1, w1_q, static_cast<uint64_t>(E) * 2 * F, H / code_div, 128) ||
-      !make_map(&m2, w2_q, static_cast<uint64_t>(E) * H, F / code_div, 128) ||
-      !make_map(&mx, w + ws.x.codes, ws.x.code_rows, ws.x.steps * 128, ws.x.pieces) ||
-      !make_map(&mh, w + ws.h.codes, ws.h.code_rows, ws.h.steps * 128, ws.h.pieces))
+  if (!make_map(&m1, w1_q, static_cast<uint64_t>(E) * 2 * F, H / per_byte, 128) ||
+      !make_map(&m2, w2_q, static_cast<uint64_t>(E) * H, F / per_byte, 128) ||
+      !make_map(&mx, w + ws.x.codes, ws.x.code_rows, ws.x.steps * 128, ws.x.pieces * group) ||
+      !make_map(&mh, w + ws.h.codes, ws.h.code_rows, ws.h.steps * 128, ws.h.pieces * group))
     return MXFP8_ERR_CUDA;
-  const int sms = std::min(dec_setup<FMT, DEC_GATE_UP>(), dec_setup<FMT, DEC_DOWN>());
+  const int sms = std::min(dec_setup<FMT, DEC_UP>(), dec_setup<FMT, DEC_DOWN>());
   if (sms <= 0 || 2 * sms > DEC_MAX_CTAS) return MXFP8_ERR_CUDA;
 
-  DecParams p{};
-  p.in = dec_pointers(w, ws.x);
-  p.h = dec_pointers(w, ws.h);
-  p.h_steps = static_cast<int>(ws.h.steps);
-  p.experts = experts;
-  p.gates = gates;
-  p.out = static_cast<uint16_t*>(out);
-  p.err = reinterpret_cast<uint32_t*>(w);
-  p.part = reinterpret_cast<float*>(w + ws.part);
-  p.counters = reinterpret_cast<int*>(w + ws.counters);
-  p.T = static_cast<int>(T);
-  p.k = k;
-  p.E = E;
-  p.F = static_cast<int>(F);
-  p.max_active = ws.max_active;
-  p.timeout_ns = dec_wait_ns();
-  p.drain_ns = kDecWaitNs;
+  DecParams up{};
+  up.in = dec_pointers(w, ws.x);
+  up.h = dec_pointers(w, ws.h);
+  up.h_steps = static_cast<int>(ws.h.steps);
+  up.experts = experts;
+  up.gate = reinterpret_cast<float*>(w + ws.gate);
+  up.y = reinterpret_cast<float*>(w + ws.y);
+  up.err = reinterpret_cast<uint32_t*>(w);
+  up.part = reinterpret_cast<float*>(w + ws.part);
+  up.part_slot = 2 * group * 128;
+  up.counters = reinterpret_cast<int*>(w + ws.counters);
+  up.T = static_cast<int>(T);
+  up.k = k;
+  up.E = E;
+  up.max_active = ws.max_active;
+  up.chunks = 1;
+  up.box_rows = group;
+  up.timeout_ns = dec_wait_ns();
+  up.drain_ns = kDecWaitNs;
+  DecParams down = up;
+  up.w_sf = w1_sf;
+  up.w_amax = w1_amax;
+  up.K = static_cast<int>(H);
+  up.steps = static_cast<int>(ws.x.steps);
+  up.kt = up.steps * dec_atoms(FMT);
+  up.tiles = static_cast<int>(F / 128);
+  down.in = up.h;
+  down.counters += ws.n_up;
+  down.w_sf = w2_sf;
+  down.w_amax = w2_amax;
+  down.K = static_cast<int>(F);
+  down.steps = up.h_steps;
+  down.kt = down.steps * dec_atoms(FMT);
+  down.tiles = static_cast<int>(H / 128);
+  if (!dec_layout(FMT, DEC_UP, group, E, ws.max_active, &up.L) ||
+      !dec_layout(FMT, DEC_DOWN, group, E, ws.max_active, &down.L))
+    return MXFP8_ERR_UNSUPPORTED;
 
-  const int group = std::min(p.T, dec_group(FMT));
-  if (!dec_layout(FMT, DEC_GATE_UP, group, E, p.max_active, &p.L)) return MXFP8_ERR_UNSUPPORTED;
-  p.part_slot = 2 * group * 128;
-  p.w_sf = w1_sf;
-  p.w_amax = w1_amax;
-  p.K = static_cast<int>(H);
-  p.steps = static_cast<int>(ws.x.steps);
-  p.kt = p.steps * dec_atoms(FMT);
-  p.tiles = static_cast<int>(F / 128);
-  p.chunks = 1;
-  p.per_chunk = p.T;
-  const DecParams up = p;
-
-  p.chunks = (p.T + DEC_CHUNK - 1) / DEC_CHUNK;
-  p.per_chunk = (p.T + p.chunks - 1) / p.chunks;
-  if (!dec_layout(FMT, DEC_DOWN, p.per_chunk, E, p.max_active, &p.L)) return MXFP8_ERR_UNSUPPORTED;
-  p.part_slot = p.per_chunk * 128;
-  p.counters += ws.n_up;
-  p.in = p.h;
-  p.w_sf = w2_sf;
-  p.w_amax = w2_amax;
-  p.K = static_cast<int>(F);
-  p.steps = p.h_steps;
-  p.kt = p.steps * dec_atoms(FMT);
-  p.tiles = static_cast<int>(H / 128);
-  p.zero_row = p.T * k;
-
-  if (!split_launch<FMT>(x, up, ws.x, &ws.h, static_cast<int>(ws.n_up + ws.n_down), s) ||
-      !dec_launch<FMT, DEC_GATE_UP>(m1, mx, up, (up.L.smem == DEC_SMEM_HALF ? 2 : 1) * sms, s) ||
-      !dec_launch<FMT, DEC_DOWN>(m2, mh, p, (p.L.smem == DEC_SMEM_HALF ? 2 : 1) * sms / p.chunks * p.chunks, s))
-    return MXFP8_ERR_CUDA;
-  return MXFP8_OK;
+  SplitParams q{};
+  q.x = static_cast<const uint16_t*>(x);
+  q.o = up.in;
+  q.err = up.err;
+  q.experts = experts;
+  q.gates = gates;
+  q.gate = const_cast<float*>(up.gate);
+  q.row_of = reinterpret_cast<int*>(w + ws.row_of);
+  q.h_top = up.h.top;
+  q.counters = up.counters;
+  q.T = up.T;
+  q.K = up.K;
+  q.steps = up.steps;
+  q.n_ids = up.T * k;
+  q.E = E;
+  q.k = k;
+  q.n_top = FMT == DEC_NV ? up.T * k : 0;
+  q.n_counters = static_cast<int>(ws.n_up + ws.n_down);
+  DecLaunch sum(up.T, 256, 0, s);
+  sum.cfg.gridDim.y = static_cast<unsigned>((H / 4 + 255) / 256);
+  const bool ok = split_launch<FMT, true>(q, s) && dec_launch<FMT, DEC_UP>(m1, mx, up, sms, s) &&
+                  dec_launch<FMT, DEC_DOWN>(m2, mh, down, sms, s) &&
+                  cudaLaunchKernelEx(&sum.cfg, k_sum_rows, static_cast<const float*>(down.y),
+                                     static_cast<const int*>(q.row_of), k, static_cast<int>(H),
+                                     static_cast<uint16_t*>(out)) == cudaSuccess;
+  return ok ? MXFP8_OK : MXFP8_ERR_CUDA;
 }
 
 template <int FMT>
 int matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf,
            const float* w_amax, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   if (T < 0 || K <= 0 || N < 0) return MXFP8_ERR_INVALID_ARG;
-  if (T > DEC_MAX_TOKENS || K % 128 != 0 || N % 128 != 0 || K > INT32_MAX || N > LIN_WS_ROWS)
-    return MXFP8_ERR_UNSUPPORTED;
-  const LinWs ws = lin_ws_layout(FMT, T, K, N);
+  if (T > DEC_MAX_TOKENS || K % 128 != 0 || N % 128 != 0 || K > INT32_MAX || N > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
+  const LinWs ws = lin_ws_layout(FMT, T, K);
   if (N / 128 * ws.x.steps > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
   if (workspace == nullptr) return MXFP8_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < ws.end) return MXFP8_ERR_WORKSPACE;
@@ -1239,38 +1196,42 @@ int matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, c
     if (q == nullptr || !aligned16(q)) return MXFP8_ERR_INVALID_ARG;
   if (FMT == DEC_NV && w_amax == nullptr) return MXFP8_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(workspace);
+  DecParams p{};
+  p.chunks = static_cast<int>((T + DEC_CHUNK - 1) / DEC_CHUNK);
+  p.per_chunk = static_cast<int>((T + p.chunks - 1) / p.chunks);
+  p.box_rows = p.per_chunk;
   CUtensorMap m, mx;
-  const int chunks = static_cast<int>((T + DEC_CHUNK - 1) / DEC_CHUNK), per_chunk = static_cast<int>((T + chunks - 1) / chunks);
   if (!make_map(&m, w_q, static_cast<uint64_t>(N), static_cast<uint64_t>(K) / (FMT == DEC_NV ? 2 : 1), 128) ||
-      !make_map(&mx, w + ws.x.codes, ws.x.code_rows, ws.x.steps * 128, per_chunk * ws.x.pieces))
+      !make_map(&mx, w + ws.x.codes, ws.x.code_rows, ws.x.steps * 128, ws.x.pieces * p.box_rows))
     return MXFP8_ERR_CUDA;
   const int sms = dec_setup<FMT, DEC_LINEAR>();
   if (sms <= 0 || 2 * sms > DEC_MAX_CTAS) return MXFP8_ERR_CUDA;
-  DecParams p{};
   p.in = dec_pointers(w, ws.x);
   p.w_sf = w_sf;
   p.w_amax = w_amax;
   p.out = static_cast<uint16_t*>(y);
   p.err = reinterpret_cast<uint32_t*>(w);
   p.part = reinterpret_cast<float*>(w + ws.part);
+  p.part_slot = p.per_chunk * 128;
   p.counters = reinterpret_cast<int*>(w + ws.counters);
   p.T = static_cast<int>(T);
-  p.k = 1;
   p.K = static_cast<int>(K);
   p.steps = static_cast<int>(ws.x.steps);
   p.kt = p.steps * dec_atoms(FMT);
   p.tiles = static_cast<int>(N / 128);
   p.timeout_ns = dec_wait_ns();
   p.drain_ns = kDecWaitNs;
-  p.chunks = chunks;
-  p.per_chunk = per_chunk;
-  p.part_slot = p.per_chunk * 128;
   if (!dec_layout(FMT, DEC_LINEAR, p.per_chunk, 0, 0, &p.L)) return MXFP8_ERR_UNSUPPORTED;
-  const int ctas = p.L.smem == DEC_SMEM_HALF ? 2 * sms : sms;
-  if (!split_launch<FMT>(x, p, ws.x, nullptr, static_cast<int>(ws.n_counters), s) ||
-      !dec_launch<FMT, DEC_LINEAR>(m, mx, p, ctas / p.chunks * p.chunks, s))
-    return MXFP8_ERR_CUDA;
-  return MXFP8_OK;
+  SplitParams q{};
+  q.x = static_cast<const uint16_t*>(x);
+  q.o = p.in;
+  q.err = p.err;
+  q.counters = p.counters;
+  q.n_counters = static_cast<int>(ws.n_counters);
+  q.T = p.T;
+  q.K = p.K;
+  q.steps = p.steps;
+  return split_launch<FMT, false>(q, s) && dec_launch<FMT, DEC_LINEAR>(m, mx, p, sms, s) ? MXFP8_OK : MXFP8_ERR_CUDA;
 }
 
 }  // namespace
@@ -1303,7 +1264,7 @@ int nvfp4_moe_decode_fwd(const void* x, int64_t T, int64_t H, int64_t F, int E, 
 
 size_t matvec_workspace_size(int64_t T, int64_t K) {
   if (T < 0 || T > DEC_MAX_TOKENS || K <= 0 || K > INT32_MAX) return 0;
-  return std::max(lin_ws_layout(DEC_MX, T, K, LIN_WS_ROWS).end, lin_ws_layout(DEC_NV, T, K, LIN_WS_ROWS).end);
+  return std::max(lin_ws_layout(DEC_MX, T, K).end, lin_ws_layout(DEC_NV, T, K).end);
 }
 
 int mxfp8_matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, const uint8_t* w_sf, void* y,
