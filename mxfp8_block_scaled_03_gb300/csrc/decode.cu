@@ -241,33 +241,45 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
   constexpr int P = dec_pieces(FMT, DEC_LINEAR), EB = dec_exp_bytes(FMT);
   constexpr int VALS = FMT == DEC_NV ? 16 : 8;   // 16 groups per step
   __shared__ int s_top, s_row;
+  __shared__ int s_ids[BY_PAIR ? DEC_MAX_TOKENS * DEC_MAX_K : 1];
   pdl_wait();
   const int b = blockIdx.x, t = BY_PAIR ? b / p.k : b, tid = threadIdx.x;
-  if (b == 0 && tid == 0) *p.err = 0;
   if (tid == 0) {
     s_top = -128;
     s_row = 0;
   }
-  __syncthreads();
   pdl_launch_dependents();   // everything before this call in the stream is complete
-  if (b == 0)
-    for (int i = tid; i < p.n_ids; i += blockDim.x)
-      if (__ldg(p.experts + i) >= p.E) atomicOr(p.err, ERR_EXPERT_RANGE);
+  // this thread's first values: on their way while the pair is looked up
+  const int groups = p.K / VALS;
+  uint4 ahead[VALS / 8];
+#pragma unroll
+  for (int i = 0; i < VALS / 8; ++i)
+    ahead[i] = tid < groups ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.K + tid * VALS) + i)
+                            : make_uint4(0u, 0u, 0u, 0u);
+  int bad = 0;
+  if constexpr (BY_PAIR)
+    for (int i = tid; i < p.n_ids; i += blockDim.x) {
+      const int e = __ldg(p.experts + i);
+      s_ids[i] = e;
+      bad |= e >= p.E ? 1 : 0;
+    }
+  bad = __syncthreads_or(bad);
+  if (b == 0 && tid == 0) *p.err = bad ? ERR_EXPERT_RANGE : 0u;
   for (int i = b * blockDim.x + tid; i < p.n_top; i += gridDim.x * blockDim.x) p.h_top[i] = -128;
   for (int i = b * blockDim.x + tid; i < p.n_counters; i += gridDim.x * blockDim.x) p.counters[i] = 0;
 
   int dst = t;   // row of the operand
   if constexpr (BY_PAIR) {
     // pairs of lower experts, and of this expert with lower tokens
-    const int e = __ldg(p.experts + b);
+    const int e = s_ids[b];
     bool none = e < 0 || e >= p.E;
-    for (int j = t * p.k; j < b; ++j) none |= __ldg(p.experts + j) == e;
+    for (int j = t * p.k; j < b; ++j) none |= s_ids[j] == e;
     int below = 0;
     if (!none)
       for (int i = tid; i < p.n_ids; i += blockDim.x) {
-        const int o = __ldg(p.experts + i), ot = i / p.k;
+        const int o = s_ids[i], ot = i / p.k;
         bool first = o >= 0 && (o < e || (o == e && ot < t));
-        for (int j = ot * p.k; first && j < i; ++j) first = __ldg(p.experts + j) != o;
+        for (int j = ot * p.k; first && j < i; ++j) first = s_ids[j] != o;
         below += first ? 1 : 0;
       }
     below = __reduce_add_sync(0xFFFFFFFFu, below);
@@ -278,14 +290,13 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
       p.row_of[b] = none ? -1 : dst;
       float g = 0.0f;
       for (int j = b; !none && j < (t + 1) * p.k; ++j)
-        if (__ldg(p.experts + j) == e) g += p.gates != nullptr ? __ldg(p.gates + j) : 1.0f;
+        if (s_ids[j] == e) g += p.gates != nullptr ? __ldg(p.gates + j) : 1.0f;
       if (!none) p.gate[dst] = g;
     }
     if (none) return;
   }
 
   int top = -128;
-  const int groups = p.K / VALS;
   for (int g0 = 0; g0 < groups; g0 += blockDim.x) {
     const int gi = g0 + tid;
     const bool in = gi < groups;   // K % 128 == 0: whole blocks, and the four threads of one agree
@@ -294,8 +305,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < VALS / 8; ++i) {
-      w[i] = in ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.K + gi * VALS) + i)
-                : make_uint4(0u, 0u, 0u, 0u);
+      w[i] = g0 == 0 ? ahead[i]
+             : in    ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.K + gi * VALS) + i)
+                     : make_uint4(0u, 0u, 0u, 0u);
       m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
                                __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
     }
@@ -370,8 +382,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   uint64_t* empty = full + DEC_MAX_STAGES;                        // the MMAs have read the stage
   uint64_t* acc_full = empty + DEC_MAX_STAGES;                    // this CTA's part of a unit is complete in TMEM
   uint64_t* acc_empty = acc_full + 1;                             // the epilogue has read it
-  uint64_t* drained = acc_empty + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t* drained = acc_empty + 1;                              // [3] MMA warp, scale warps: nothing in flight
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_nact = reinterpret_cast<int*>(tmem_holder + 2);
   int* s_last = s_nact + 1;
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 4);
-    mbar_init(drained, 1);
+    for (int s = 0; s < 3; ++s) mbar_init(&drained[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -541,9 +553,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     if (elect_one()) {
       // descriptors of stage 0: addresses are in units of 16 bytes in their low bits
       const uint64_t desc_a = sdesc_kmajor_sw128(smem_u32(smem)), desc_b = sdesc_kmajor_sw128(smem_u32(smem + L.b));
-      const uint64_t desc_sfa = sdesc_sf_atom(smem_u32(smem + L.sfa)), desc_sfb = sdesc_sf_atom(smem_u32(smem + L.sfb));
+      const uint64_t desc_sfa = sdesc_sf_atom(smem_u32(smem + L.sfa));
       bool ok = true, any = false;
-      Ring r{0, 0}, before{0, 0};   // the stage of step i and that of step i - sf_sets
+      Ring r{0, 0};
       int i = 0, set = 0;
       Place q = place_of(0);
       for (int seg = 0; ok && i < n_steps; ++seg) {
@@ -559,26 +571,14 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
             ok = false;
             break;
           }
-          // the scale columns about to be overwritten were last read by step i - sf_sets's MMAs (known to
-          // be over when that step used this stage)
-          if (i >= L.sf_sets && L.sf_sets < L.stages) {
-            if (!dec_wait(&empty[before.slot], before.phase, abort_flag, p, ERR_TIMEOUT_MMA)) {
-              ok = false;
-              break;
-            }
-            next_stage(before);
-          }
           tc_fence_after();
           const uint64_t da = desc_a + slot * (DEC_A_STAGE >> 4), db = desc_b + slot * (L.b_stage >> 4);
-          const uint64_t dsa = desc_sfa + slot * (ATOMS * 32), dsb = desc_sfb + slot * (L.sfb_stage >> 4);
+          const uint64_t dsa = desc_sfa + slot * (ATOMS * 32);
           const uint32_t t_sfa = tmem + L.sf_col + set * L.sf_cols, t_sfb = t_sfa + 4 * ATOMS;
           if (++set == L.sf_sets) set = 0;
           const uint32_t d = tmem + q.acc * L.n_max;
 #pragma unroll
-          for (int m = 0; m < ATOMS; ++m) {
-            tc_copy_sf(t_sfa + 4 * m, dsa + 32 * m);
-            for (int j = 0; j < nat; ++j) tc_copy_sf(t_sfb + 4 * (m * nat + j), dsb + 32 * (m * nat + j));
-          }
+          for (int m = 0; m < ATOMS; ++m) tc_copy_sf(t_sfa + 4 * m, dsa + 32 * m);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t add = ((started >> q.acc) & 1u) | (k != 0 ? 1u : 0u);
@@ -601,10 +601,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     __syncwarp();
   } else if (warp < DEC_FIRST_EPI_WARP) {
     // ---------------- the columns' scales: warp cw takes steps cw, cw + 2, ... ----------------
-    // Fewer warps than stages: when a warp waits for a slot's last use, the use before that one is known
-    // to be over, as a wait by parity requires.
+    // It writes them to shared memory, has them copied to the step's set in TMEM (here, not by the MMA thread,
+    // whose time per step is what limits a CTA), and the copies' completion counts on `full`.
+    // The set (and the stage) must have been read by step i - sf_sets.  Fewer warps than stages: when a warp
+    // waits for that step, the use of its stage before it is known to be over, as a wait by parity requires.
     const int cw = warp - 2;
-    pdl_wait();
     // MXFP8, and NVFP4 with more than eight rows: lane = row, all its words; NVFP4 with up to eight:
     // lane = (word, row), one of the row's four words.
     struct Scales {
@@ -644,9 +645,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       return reinterpret_cast<uint32_t*>(sf + (m * nat + (col >> 7)) * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4);
     };
     Place q = place_of(cw);
+    pdl_wait();
     if (cw < n_steps) load(q, cur);
-    int slot = cw;
-    uint32_t phase = 1;   // parity of the slot's previous use
+    int slot = cw, set = cw % L.sf_sets;
+    Ring read{cw >= L.sf_sets ? cw - L.sf_sets : 0, 0};   // stage of step i - sf_sets
+    const uint64_t desc_sfb = sdesc_sf_atom(smem_u32(smem + L.sfb));
     for (int i = cw; i < n_steps; i += DEC_SCALE_WARPS) {
       next = cur;
       if (i + DEC_SCALE_WARPS < n_steps) {
@@ -661,7 +664,13 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
 #pragma unroll
           for (int m = 1; m < 4; ++m) w[m] = nv_scales(cur.e[m], cur.top);
       }
-      if (i >= L.stages && !dec_warp_wait(&empty[slot], phase, abort_flag, p, ERR_TIMEOUT_SF, lane)) break;
+      if (i >= L.sf_sets) {
+        if (!dec_warp_wait(&empty[read.slot], read.phase, abort_flag, p, ERR_TIMEOUT_SF, lane)) break;
+        next_stage(read);
+        next_stage(read);
+      } else if (i + DEC_SCALE_WARPS >= L.sf_sets) {
+        read = Ring{i + DEC_SCALE_WARPS - L.sf_sets, 0};   // of the next step of this warp
+      }
       uint8_t* sf = smem + L.sfb + slot * L.sfb_stage;
       if (cur.c < cur.n) {
 #pragma unroll
@@ -680,14 +689,22 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       }
       fence_proxy_async_smem();   // the tensor core reads these bytes through the async proxy
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[slot]);
-      cur = next;
-      slot += DEC_SCALE_WARPS;
-      if (slot >= L.stages) {
-        slot -= L.stages;
-        phase ^= 1u;
+      if (elect_one()) {
+        const uint64_t dsb = desc_sfb + slot * (L.sfb_stage >> 4);
+        const uint32_t t_sfb = tmem + L.sf_col + set * L.sf_cols + 4 * ATOMS;
+        for (int m = 0; m < ATOMS * cur.nat; ++m) tc_copy_sf(t_sfb + 4 * m, dsb + 32 * m);
+        tc_commit(&full[slot]);
       }
+      __syncwarp();
+      cur = next;
+      slot = slot + DEC_SCALE_WARPS < L.stages ? slot + DEC_SCALE_WARPS : slot + DEC_SCALE_WARPS - L.stages;
+      set = (set + DEC_SCALE_WARPS) % L.sf_sets;
     }
+    if (cw < n_steps && elect_one()) {
+      tc_commit(&drained[1 + cw]);
+      if (!mbar_wait_bounded(&drained[1 + cw], 0, nullptr, p.drain_ns)) atomicOr(p.err, ERR_TIMEOUT_DRAIN);
+    }
+    __syncwarp();
   } else {
     // ---------------- epilogue ----------------
     pdl_wait();
@@ -944,7 +961,7 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
   *out = L;
   return true;
 }
-static_assert(2 * DEC_MAX_STAGES * 8 + 3 * 8 + 16 <= 384, "barriers and flags");
+static_assert(2 * DEC_MAX_STAGES * 8 + 5 * 8 + 16 <= 384, "barriers and flags");
 static_assert(dec_group(DEC_MX, DEC_DOWN) * 3 <= 160 && dec_group(DEC_MX, DEC_UP) * 2 * 2 <= 160 &&
                   dec_group(DEC_NV, DEC_UP) * 5 * 2 <= 160 && DEC_CHUNK * 5 <= 160,
               "accumulators");
@@ -1039,7 +1056,7 @@ bool dec_ws_layout(int fmt, int64_t T, int k, int64_t H, int64_t F, int E, DecWs
   w.h = dec_operand(fmt, dec_pieces(fmt, DEC_DOWN), w.x.end, pairs, F);
   // only units that are shared use counters, and those are fewer than the CTAs
   w.n_up = 4 * std::min<int64_t>(w.max_active * ((F + 127) / 128), DEC_MAX_CTAS);
-  w.n_down = 4 * std::min<int64_t>(w.max_active * ((H + 127) / 128), DEC_MAX_CTAS);
+  w.n_down = 4 * std::min<int64_t>(std::max<int64_t>(w.max_active, 1) * ((H + 127) / 128), DEC_MAX_CTAS);
   w.y = w.h.end;
   w.gate = align256(w.y + static_cast<size_t>(pairs) * H * sizeof(float));
   w.row_of = align256(w.gate + static_cast<size_t>(pairs) * sizeof(float));
@@ -1169,14 +1186,15 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
   q.k = k;
   q.n_top = FMT == DEC_NV ? up.T * k : 0;
   q.n_counters = static_cast<int>(ws.n_up + ws.n_down);
+  if (!split_launch<FMT, true>(q, s) || !dec_launch<FMT, DEC_UP>(m1, mx, up, sms, s) ||
+      !dec_launch<FMT, DEC_DOWN>(m2, mh, down, sms, s))
+    return MXFP8_ERR_CUDA;
   DecLaunch sum(up.T, 256, 0, s);
   sum.cfg.gridDim.y = static_cast<unsigned>((H / 4 + 255) / 256);
-  const bool ok = split_launch<FMT, true>(q, s) && dec_launch<FMT, DEC_UP>(m1, mx, up, sms, s) &&
-                  dec_launch<FMT, DEC_DOWN>(m2, mh, down, sms, s) &&
-                  cudaLaunchKernelEx(&sum.cfg, k_sum_rows, static_cast<const float*>(down.y),
-                                     static_cast<const int*>(q.row_of), k, static_cast<int>(H),
-                                     static_cast<uint16_t*>(out)) == cudaSuccess;
-  return ok ? MXFP8_OK : MXFP8_ERR_CUDA;
+  return cudaLaunchKernelEx(&sum.cfg, k_sum_rows, static_cast<const float*>(down.y), static_cast<const int*>(q.row_of), k,
+                            static_cast<int>(H), static_cast<uint16_t*>(out)) == cudaSuccess
+             ? MXFP8_OK
+             : MXFP8_ERR_CUDA;
 }
 
 template <int FMT>
