@@ -721,18 +721,14 @@ def residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post=None, gate=None, w
     T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res_out, w_post, gate, w_pre, post_norm)
     pn, py, pr = _need(dn, bf16, (T, H), "dn"), _need(y, bf16, (T, H), "y"), _need(res_out, rt, (T, H), "res_out")
     pd = None if dres_out is None else _need(dres_out, rt, (T, H), "dres_out")
-    dy, dres = torch.empty_like(y), torch.empty_like(res_out)
-    dgate = torch.empty_like(gate) if kind == 2 else None
-    cols = (w_post is not None) + (kind == 1) + (w_pre is not None)
-    cols = list(torch.empty((cols, H), dtype=f32, device=y.device).unbind(0)) if cols else []
-    dw_post = cols.pop() if w_post is not None else None
-    dgate = cols.pop() if kind == 1 else dgate
-    dw_pre = cols.pop() if w_pre is not None else None
+    like = torch.empty_like
+    dy, dres = like(y), like(res_out)
+    dw_post, dgate, dw_pre = (None if w is None else like(w) for w in (w_post, gate, w_pre))
     if workspace is None:
         workspace = torch.empty(max(16, residual_norm_bwd_workspace_size(T, H)), dtype=torch.uint8, device=y.device)
     st = lib().residual_norm_bwd(pn, pd, py, pr, _need(stats, f32, (2, T), "stats"), pa, pg, pb, T, H, code, kind,
                                  1 if post_norm else 0, res_scale, dy.data_ptr(), dres.data_ptr(), _ptr(dw_post),
-                                 _ptr(dgate), _ptr(dw_pre), workspace.data_ptr(), workspace.numel(),
+                                 _ptr(dgate), _ptr(dw_pre), _need(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
                                  _stream_of(y, stream))
     if st != OK:
         raise MXFP8Error(st, "residual_norm_bwd")

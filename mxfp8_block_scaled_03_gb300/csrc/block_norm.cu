@@ -31,12 +31,6 @@
 namespace mx {
 namespace {
 
-#ifndef NVB
-#define NVB 512
-#endif
-#ifndef NVMAX
-#define NVMAX 256
-#endif
 constexpr int BN_THREADS = 512;          // most threads of a CTA
 constexpr int BN_MAX_H = 8192;           // two vectors of 8 values per thread
 constexpr int BN_MAX_STAGES = 4;
@@ -187,16 +181,17 @@ struct Lane {
   __device__ __forceinline__ uint4* block(int stage, int v, int i) const {
     return ring + ((stage * V + v) * PIECES + i) * blockDim.x;
   }
-  __device__ __forceinline__ void copy(const uint16_t* row, int stage, int v, int i) const {
+  // from array[o ..], o being where the row starts
+  __device__ __forceinline__ void copy(const uint16_t* array, int64_t o, int stage, int v, int i) const {
     const int j = t + v * tpr;
-    if (j < nv) cp_async16(block(stage, v, i) + threadIdx.x, row + j * 8);
+    if (j < nv) cp_async16(block(stage, v, i) + threadIdx.x, array + o + j * 8);
   }
-  __device__ __forceinline__ void copy(const float* row, int stage, int v, int i) const {
+  __device__ __forceinline__ void copy(const float* array, int64_t o, int stage, int v, int i) const {
     const int lane = threadIdx.x & 31;
     uint4* dst = block(stage, v, i) + (threadIdx.x - lane) * 2;
     const int j = (t - lane + v * tpr) * 2 + lane;   // in units of four floats
-    if (j < 2 * nv) cp_async16(dst + lane, row + j * 4);
-    if (j + 32 < 2 * nv) cp_async16(dst + 32 + lane, row + (j + 32) * 4);
+    if (j < 2 * nv) cp_async16(dst + lane, array + o + j * 4);
+    if (j + 32 < 2 * nv) cp_async16(dst + 32 + lane, array + o + (j + 32) * 4);
   }
   __device__ __forceinline__ void read(int stage, int v, int i, Vec8& out, uint16_t) const {
     unpack(block(stage, v, i) + threadIdx.x, out, 0, uint16_t{});
@@ -224,12 +219,13 @@ __global__ void __launch_bounds__(BN_THREADS, V == 1 ? 2 : 1) k_residual_norm_fw
   for (int v = 0; v < V; ++v) in[v] = me.t + v * p.tpr < p.nv;
 
   auto fetch = [&](int64_t row, int stage) {
-    __syncwarp();   // the warp has read what the stage held
+    if (RP == 2) __syncwarp();   // the warp has read what the stage held
     if (row < p.T) {
+      const int64_t o = row * p.H;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        me.copy(y + row * p.H, stage, v, 0);
-        me.copy(res + row * p.H, stage, v, 1);
+        me.copy(y, o, stage, v, 0);
+        me.copy(res, o, stage, v, 1);
       }
     }
     cp_async_commit();
@@ -258,7 +254,7 @@ __global__ void __launch_bounds__(BN_THREADS, V == 1 ? 2 : 1) k_residual_norm_fw
     const float tg = next_tg;
     if (tgate != nullptr && row + step < p.T) next_tg = __ldg(tgate + row + step);
     cp_async_wait(p.stages - 1);
-    __syncwarp();
+    if (RP == 2) __syncwarp();
     Vec8 z[V], r[V];
     uint64_t ss = 0;
 #pragma unroll
@@ -323,14 +319,15 @@ __global__ void __launch_bounds__(BN_THREADS, 1) k_residual_norm_bwd(const NormP
   for (int v = 0; v < V; ++v) in[v] = me.t + v * p.tpr < p.nv;
 
   auto fetch = [&](int64_t row, int stage) {
-    __syncwarp();   // the warp has read what the stage held
+    if (RP == 2) __syncwarp();   // the warp has read what the stage held
     if (row < p.T) {
+      const int64_t o = row * p.H;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        me.copy(dn + row * p.H, stage, v, 0);
-        me.copy(y + row * p.H, stage, v, 1);
-        me.copy(res + row * p.H, stage, v, 2);
-        if (dro != nullptr) me.copy(dro + row * p.H, stage, v, 2 + RP);
+        me.copy(dn, o, stage, v, 0);
+        me.copy(y, o, stage, v, 1);
+        me.copy(res, o, stage, v, 2);
+        if (dro != nullptr) me.copy(dro, o, stage, v, 2 + RP);
       }
     }
     cp_async_commit();
@@ -426,7 +423,7 @@ __global__ void __launch_bounds__(BN_THREADS, 1) k_residual_norm_bwd(const NormP
     }
     if (++stage == p.stages) stage = 0;
     cp_async_wait(p.stages - 2);
-    __syncwarp();
+    if (RP == 2) __syncwarp();
     const bool more = row + step < p.T;
     float2 sums;
     if (V == 1) {
@@ -517,7 +514,9 @@ struct NormShape {
 NormShape norm_shape(int H, int pieces, bool bwd, size_t least) {
   NormShape s{};
   const int nv = H / 8;
-  s.v = nv <= (bwd ? NVB : NVMAX) ? 1 : 2;
+  // two vectors per thread beyond 2048 columns: fewer warps to exchange sums with (forward, 4096 columns: 101 ->
+  // 87 us); the backward's registers hold only one (4096 columns: 145 against 278 us)
+  s.v = nv <= (bwd ? BN_THREADS : BN_THREADS / 2) ? 1 : 2;
   s.tpr = ((nv + s.v - 1) / s.v + 31) / 32 * 32;
   s.groups = std::max(1, BN_THREADS / s.tpr);
   if (s.tpr > 32) s.groups = std::min(s.groups, 15);   // one hardware barrier per group
