@@ -734,7 +734,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         return p.part + static_cast<int64_t>(c * p.chunks + chunk) * p.part_slot;
       };
 
-      if (!dec_warp_wait(acc_full, seg & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane)) break;
+      // one outcome for the four warps: they meet at barriers below
+      if (!group_and(1, 128, dec_warp_wait(acc_full, seg & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane))) break;
       tc_fence_after();
       float* mine = part_of(share ? cta - u * per_unit : 0) + row;
       const int parts = share ? per_unit : 1;
@@ -1096,7 +1097,8 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
                const uint8_t* w2_q, const uint8_t* w2_sf, const float* w2_amax, void* out, void* workspace,
                size_t workspace_bytes, void* stream) {
   if (T < 0 || E < 1 || E > 1024 || k < 1 || H <= 0 || F <= 0) return MXFP8_ERR_INVALID_ARG;
-  if (T > DEC_MAX_TOKENS || k > DEC_MAX_K || H % 128 != 0 || F % 128 != 0) return MXFP8_ERR_UNSUPPORTED;
+  if (T > DEC_MAX_TOKENS || k > DEC_MAX_K || H % 128 != 0 || F % 128 != 0 || H > INT32_MAX || F > INT32_MAX)
+    return MXFP8_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(E) * 2 * F > INT32_MAX || static_cast<int64_t>(E) * H > INT32_MAX)
     return MXFP8_ERR_UNSUPPORTED;
   DecWs ws;
