@@ -53,14 +53,13 @@ constexpr int DEC_SCALE_WARPS = 2;
 constexpr int DEC_FIRST_EPI_WARP = 4;
 constexpr int DEC_A_STAGE = 128 * 128;       // 128 weight rows x 128 code bytes
 constexpr int DEC_MAX_TOKENS = 64;           // tokens of one call
-constexpr int DEC_CHUNK = 32;                // LINEAR: most tokens of one accumulator
 constexpr int DEC_MAX_K = 32;                // choices per token
 constexpr int DEC_MAX_STAGES = 12;
 constexpr int DEC_MIN_STEPS = 4;             // K steps that make a CTA worth having (2 and 8 measured the same)
 // Half of 228 KB less the 1 KB the system keeps per CTA, so that a kernel's CTAs fit beside those of the
 // kernel before it; the whole SM where that leaves fewer than three stages.
 constexpr int DEC_SMEM_HALF = 113 * 1024, DEC_SMEM_FULL = 226 * 1024;
-constexpr uint32_t DEC_TMEM_COLS = 256;      // two CTAs per SM share 512
+constexpr uint32_t DEC_TMEM_HALF = 256, DEC_TMEM_FULL = 512;   // likewise
 // TMEM columns: accumulators (at most 160), then as many sets of scales of A and B as fit, used in turn
 // (at least two): a step's scales may be written while the MMAs of that many steps less one are pending.
 constexpr int SPLIT_THREADS = 1024;          // at most
@@ -73,9 +72,12 @@ constexpr int dec_pieces(int fmt, int mode) { return fmt == DEC_NV ? 5 : mode ==
 constexpr int dec_step_values(int fmt) { return fmt == DEC_NV ? 256 : 128; }
 constexpr int dec_atoms(int fmt) { return fmt == DEC_NV ? 4 : 1; }          // scale atoms per 128 rows and step
 constexpr int dec_exp_bytes(int fmt) { return fmt == DEC_NV ? 16 : 4; }     // blocks of one row and step
-// Most rows of a unit.  MoE: two accumulators of at most 80 columns share the TMEM that LINEAR uses for one of
-// 160 (an expert with more tokens gives several units, which read its weights side by side, from L2).
-constexpr int dec_group(int fmt, int mode) { return mode == DEC_LINEAR ? DEC_CHUNK : fmt == DEC_NV ? 16 : 32; }
+// Most rows of a unit.  LINEAR: one accumulator of at most 128 (MXFP8) or 160 (NVFP4) columns; more tokens come
+// in two chunks.  MoE: two accumulators of at most 80 (an expert with more tokens gives several units).  Units of
+// the same weights read them side by side, from L2.
+constexpr int dec_group(int fmt, int mode) {
+  return fmt == DEC_NV ? (mode == DEC_LINEAR ? 32 : 16) : (mode == DEC_LINEAR ? 64 : 32);
+}
 
 // Shared memory of one CTA (byte offsets from a 1024-byte boundary); the weight ring is at 0.
 struct DecLayout {
@@ -84,6 +86,7 @@ struct DecLayout {
   int b, sfa, sfb, bars, misc;
   int n_max;             // most columns of one accumulator (UP: the second one starts there)
   int sf_col, sf_cols, sf_sets;   // TMEM: first column of the scale sets, columns per set, sets
+  uint32_t tmem_cols;
 };
 
 // Activations as columns of the MMA.  Row r * P + q of `codes` holds piece q of row r: 128 code bytes per K step.
@@ -125,7 +128,6 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
-__device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // One lane of the (converged) warp.  The compiler knows that a branch on it holds one thread, and issues
 // copies and MMAs there directly; behind `lane == 0` it wraps each of them in a loop over the lanes.
 __device__ __forceinline__ bool elect_one() {
@@ -150,6 +152,16 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
+}
+
+// Four values' E2M1 codes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1x4_f2(uint64_t v, uint64_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "mov.b32 %0, {a, b, a, b};\n\t}"
+      : "=r"(r)
+      : "f"(f2_lo(v)), "f"(f2_hi(v)), "f"(f2_lo(w)), "f"(f2_hi(w)));
+  return r & 0xFFFFu;
 }
 
 // One thread waits; on a timeout it records the bit and raises the CTA's abort flag.
@@ -193,6 +205,16 @@ __device__ __forceinline__ uint64_t next_piece(uint64_t& r) {
     if constexpr (!LAST) r = f2_fma(n, f2_pack(-8.0f, -8.0f), f2_mul(r, f2_pack(8.0f, 8.0f)));
     return n;
   }
+}
+
+// Sum over a value's columns, smallest piece first; a digit's place is 1/8 of the one before.
+template <int FMT, int P>
+__device__ __forceinline__ float sum_pieces(const uint32_t* d) {
+  float x = __uint_as_float(d[P - 1]);
+#pragma unroll
+  for (int z = P - 2; z >= 0; --z)
+    x = FMT == DEC_NV ? fmaf(x, 0.125f, __uint_as_float(d[z])) : x + __uint_as_float(d[z]);
+  return x;
 }
 
 // The code bytes of the next piece of eight (MXFP8) or sixteen (NVFP4) scaled values.
@@ -374,7 +396,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   constexpr int ATOMS = dec_atoms(FMT), EB = dec_exp_bytes(FMT);
   constexpr bool UP = MODE == DEC_UP, MOE = MODE != DEC_LINEAR;
   constexpr int ACCS = UP ? 2 : 1;
-  constexpr int GROUP = dec_group(FMT, MODE);
+  constexpr int GROUP = dec_group(FMT, MODE), ROWS = (GROUP + 31) / 32;   // ROWS: of a unit, per lane of a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const DecLayout& L = p.L;
@@ -386,7 +408,6 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_nact = reinterpret_cast<int*>(tmem_holder + 2);
-  int* s_last = s_nact + 1;
   // MoE: tokens that chose the expert [E]; then the list of groups of tokens: expert, first pair, pairs
   uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + L.misc);
   int* s_act_e = reinterpret_cast<int*>(s_mask + p.E);
@@ -410,7 +431,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, DEC_TMEM_COLS);
+    tmem_alloc(tmem_holder, L.tmem_cols);
     tmem_relinquish();
   }
 
@@ -456,7 +477,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   const int su = UP ? 2 * p.steps : p.steps;                    // steps of a unit
   const int units = MOE ? *s_nact * p.tiles : p.tiles;
   // Every CTA takes the same number of whole units; the units left over are shared, each by as many CTAs as fit
-  // (and find DEC_MIN_STEPS steps).  The share comes first, so that adding its parts up is hidden.
+  // (and find DEC_MIN_STEPS steps).  The share comes first, so that adding its parts up is hidden.  (Dealing the
+  // left-over steps out evenly, with two parts of units in a CTA, measured 5-15% slower: more sums of parts.)
   const int slots = static_cast<int>(gridDim.x) / p.chunks, cta = static_cast<int>(blockIdx.x) / p.chunks;
   const int whole = units / slots, shared = units - whole * slots;
   const int per_unit = shared == 0 ? 1 : max(1, min(slots / shared, su / DEC_MIN_STEPS));   // CTAs of a shared unit
@@ -606,10 +628,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     // The set (and the stage) must have been read by step i - sf_sets.  Fewer warps than stages: when a warp
     // waits for that step, the use of its stage before it is known to be over, as a wait by parity requires.
     const int cw = warp - 2;
-    // MXFP8, and NVFP4 with more than eight rows: lane = row, all its words; NVFP4 with up to eight:
-    // lane = (word, row), one of the row's four words.
+    // MXFP8 (ROWS rows a lane), and NVFP4 with more than eight rows: lane = row, all its words; NVFP4 with up
+    // to eight: lane = (word, row), one of the row's four words.
+    static_assert(FMT == DEC_MX || ROWS == 1, "one row a lane");
     struct Scales {
-      uint32_t e[ATOMS];
+      uint32_t e[ATOMS * ROWS];
       int c, top, n, nat;   // row of the unit (lanes past the last: none) and its reference, rows, atoms per MMA
       bool spread;
     };
@@ -637,7 +660,12 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
             if ((q.f * 4 + m) * 64 >= p.K) v.e[m] = 0;
         }
       } else {
-        v.e[0] = *reinterpret_cast<const uint32_t*>(src);
+#pragma unroll
+        for (int z = 0; z < ROWS; ++z)
+          if (z * 32 < v.n) {
+            const int more = min(v.c + z * 32, v.n - 1) - min(v.c, v.n - 1);
+            v.e[z] = *reinterpret_cast<const uint32_t*>(src + static_cast<int64_t>(more) * p.steps * EB);
+          }
       }
     };
     // word of atom m for column col
@@ -672,12 +700,14 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         read = Ring{i + DEC_SCALE_WARPS - L.sf_sets, 0};   // of the next step of this warp
       }
       uint8_t* sf = smem + L.sfb + slot * L.sfb_stage;
-      if (cur.c < cur.n) {
+#pragma unroll
+      for (int z = 0; z < ROWS; ++z) {
+        if (cur.c + z * 32 >= cur.n) break;
 #pragma unroll
         for (int d = 0; d < P; ++d) {
-          const int col = cur.c * P + d;
+          const int col = (cur.c + z * 32) * P + d;
           if constexpr (FMT == DEC_MX) {
-            *word(sf, 1, 0, col) = mx_scales(cur.e[0], d);
+            *word(sf, 1, 0, col) = mx_scales(cur.e[z], d);
           } else if (cur.spread) {
             *word(sf, 1, lane >> 3, col) = w[0];
           } else {
@@ -717,7 +747,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     for (int seg = 0; i < n_steps; ++seg) {
       const bool share = i < n_share && per_unit > 1;
       const int r0 = q.f * ACCS + q.acc, r1 = i < n_share ? r0 + n_share : su;   // the part's steps of the unit
-      const int u = share ? cta / per_unit : 0;                                    // which shared unit
+      const int u = share ? cta / per_unit : 0, parts = share ? per_unit : 1;      // which shared unit
       const int n = rows_of(q.a), row0 = first_row(q.a), tile = q.tile;
       float unscale = 1.0f;   // lane c: of row c's sums
       if constexpr (FMT == DEC_NV) unscale = ldexpf(alpha, p.in.top[row0 + min(lane, n - 1)] - 9);
@@ -734,142 +764,165 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         return p.part + static_cast<int64_t>(c * p.chunks + chunk) * p.part_slot;
       };
 
-      // one outcome for the four warps: they meet at barriers below
-      if (!group_and(1, 128, dec_warp_wait(acc_full, seg & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane))) break;
+      if (!dec_warp_wait(acc_full, seg & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane)) break;
       tc_fence_after();
       float* mine = part_of(share ? cta - u * per_unit : 0) + row;
-      const int parts = share ? per_unit : 1;
-      const bool has[2] = {!UP || r1 - r0 > 1 || (r0 & 1) == 0, r1 - r0 > 1 || (r0 & 1) == 1};
+      int* counter = p.counters + (chunk * shared + u) * 4 + quarter;   // each warp for its 32 weight rows
+      // A part of a unit is in memory; true in the warp that finds all the others there too.
+      auto last_part = [&]() {
+        int before = 0;
+        if (lane == 0) {
+          __threadfence();
+          before = atomicAdd(counter, 1);
+          __threadfence();
+        }
+        __syncwarp();
+        return __shfl_sync(0xFFFFFFFFu, before, 0) == parts - 1;
+      };
+      auto release = [&]() {   // the next unit's MMAs may begin
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+      };
+      if constexpr (!UP) {
 #pragma unroll 1
-      for (int c0 = 0; c0 < n; c0 += 8) {
-#pragma unroll
-        for (int b = 0; b < ACCS; ++b) {
+        for (int c0 = 0; c0 < n; c0 += 8) {
           uint32_t d[8 * P];
 #pragma unroll
-          for (int z = 0; z < P; ++z) tmem_ld_32x32b_x8(t_row + b * L.n_max + c0 * P + z * 8, d + z * 8);
+          for (int z = 0; z < P; ++z) tmem_ld_32x32b_x8(t_row + c0 * P + z * 8, d + z * 8);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            float x = __uint_as_float(d[j * P + P - 1]);
-#pragma unroll
-            for (int z = P - 2; z >= 0; --z)   // smallest first; a digit's place is 1/8 of the one before
-              x = FMT == DEC_NV ? fmaf(x, 0.125f, __uint_as_float(d[j * P + z])) : x + __uint_as_float(d[j * P + z]);
+            float x = sum_pieces<FMT, P>(d + j * P);
             if constexpr (FMT == DEC_NV) x *= __shfl_sync(0xFFFFFFFFu, unscale, c0 + j);
             if (c0 + j >= n) continue;
-            if (!UP && !share) put(c0 + j, x);
-            else mine[(b * n + c0 + j) * 128] = has[b] ? x : 0.0f;
+            if (share) mine[(c0 + j) * 128] = x;
+            else put(c0 + j, x);
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);   // the next unit's MMAs may begin
-      int* counter = p.counters + (chunk * shared + u) * 4;
-
-      if constexpr (!UP) {
-        // Each warp for its 32 weight rows: the last of the unit's parts adds them all up, in order.
-        if (share) {
-          int before = 0;
-          if (lane == 0) {
-            __threadfence();
-            before = atomicAdd(counter + quarter, 1);
-            __threadfence();
-          }
-          if (__shfl_sync(0xFFFFFFFFu, before, 0) == parts - 1) {
-            constexpr int TB = 4, OB = 4;   // 4 rows x 4 parts of loads in flight
+        release();
+        // whoever is last adds the parts up, in order
+        if (share && last_part()) {
+          constexpr int TB = 4, OB = 4;   // 4 rows x 4 parts of loads in flight
 #pragma unroll 1
-            for (int c0 = 0; c0 < n; c0 += TB) {
-              float sum[TB] = {};
+          for (int c0 = 0; c0 < n; c0 += TB) {
+            float sum[TB] = {};
 #pragma unroll 1
-              for (int o0 = 0; o0 < parts; o0 += OB) {
-                float x[OB][TB];
+            for (int o0 = 0; o0 < parts; o0 += OB) {
+              float x[OB][TB];
 #pragma unroll
-                for (int o = 0; o < OB; ++o) {
-                  const float* src = part_of(min(o0 + o, parts - 1)) + row;
+              for (int o = 0; o < OB; ++o) {
+                const float* src = part_of(min(o0 + o, parts - 1)) + row;
 #pragma unroll
-                  for (int j = 0; j < TB; ++j)
-                    x[o][j] = o0 + o < parts && c0 + j < n ? __ldcg(src + (c0 + j) * 128) : 0.0f;
-                }
-#pragma unroll
-                for (int o = 0; o < OB; ++o)
-#pragma unroll
-                  for (int j = 0; j < TB; ++j) sum[j] += x[o][j];
+                for (int j = 0; j < TB; ++j)
+                  x[o][j] = o0 + o < parts && c0 + j < n ? __ldcg(src + (c0 + j) * 128) : 0.0f;
               }
 #pragma unroll
-              for (int j = 0; j < TB; ++j)
-                if (c0 + j < n) put(c0 + j, sum[j]);
+              for (int o = 0; o < OB; ++o)
+#pragma unroll
+                for (int j = 0; j < TB; ++j) sum[j] += x[o][j];
             }
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+              if (c0 + j < n) put(c0 + j, sum[j]);
           }
         }
       } else {
-        // h from the gate and up sums, as columns of DOWN: a thread takes 8 (MXFP8) or 16 (NVFP4) values of one
-        // activation row, the same way as k_split_x.
-        epi_barrier();   // the other warps' rows are written
-        bool last = true;
-        if (share) {
-          if (tid == DEC_FIRST_EPI_WARP * 32) {
-            __threadfence();
-            *s_last = atomicAdd(counter, 1) == parts - 1 ? 1 : 0;
-            __threadfence();
-          }
-          epi_barrier();
-          last = *s_last != 0;
-        }
-        constexpr int PH = dec_pieces(FMT, DEC_DOWN);
-        constexpr int VALS = FMT == DEC_NV ? 16 : 8, PER_ROW = 128 / VALS;
-        const int g = (tid & 127) % PER_ROW, k0 = tile * 128 + g * VALS;   // values k0 .. of h
+        // h from the gate and up sums, as columns of DOWN.  A lane has one weight row; four lanes transpose their
+        // values of four activation rows, and each converts four values of one of them (a block is 16 or 32 lanes
+        // wide).  Sums that are parts, and those of many rows while more units follow, go through memory first,
+        // which frees the accumulators early.  Short straight code: its first pass is fetched instruction by
+        // instruction behind the weights' stream.
+        constexpr int PH = dec_pieces(FMT, DEC_DOWN), LD = (4 * P + 7) / 8;
+        const bool has[2] = {r1 - r0 > 1 || (r0 & 1) == 0, r1 - r0 > 1 || (r0 & 1) == 1};
+        const bool staged = share || (n > 4 && i + r1 - r0 < n_steps);
+        const float gates = p.gate[row0 + min(lane, n - 1)];
         const int64_t pitch = static_cast<int64_t>(p.h_steps) * 128;
+        const int k0 = tile * 128 + quarter * 32 + (lane & ~3);   // of this lane's four values
 #pragma unroll 1
-        for (int cb = 0; last && cb < n; cb += 128 / PER_ROW) {
-          const int c = cb + (tid & 127) / PER_ROW;
-          const bool live = c < n;
-          const int64_t hr = row0 + min(c, n - 1);
-          const float gate = p.gate[hr];
-          float h[VALS];
-          {
-            float gs[VALS] = {}, us[VALS] = {};
+        for (int phase = staged ? 0 : 1; phase < 2; ++phase) {
+          if (phase == 1 && share && !last_part()) break;
 #pragma unroll 1
-            for (int o = 0; o < parts; ++o) {
-              const float* src = part_of(o) + min(c, n - 1) * 128 + g * VALS;
+          for (int c0 = 0; c0 < n; c0 += 4) {
+            float v[2][4];   // [accumulator][row]
+            if (phase == 0 || !staged) {
+              uint32_t d[2][8 * LD];
 #pragma unroll
-              for (int z = 0; z < VALS; z += 4) {
-                const float4 a = __ldcg(reinterpret_cast<const float4*>(src + z));
-                const float4 b = __ldcg(reinterpret_cast<const float4*>(src + n * 128 + z));
-                gs[z] += a.x; gs[z + 1] += a.y; gs[z + 2] += a.z; gs[z + 3] += a.w;
-                us[z] += b.x; us[z + 1] += b.y; us[z + 2] += b.z; us[z + 3] += b.w;
+              for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int z = 0; z < LD; ++z) tmem_ld_32x32b_x8(t_row + b * L.n_max + c0 * P + z * 8, d[b] + z * 8);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float scale = FMT == DEC_NV ? __shfl_sync(0xFFFFFFFFu, unscale, (c0 + j) & 31) : 1.0f;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) v[b][j] = has[b] ? sum_pieces<FMT, P>(d[b] + j * P) * scale : 0.0f;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[0][j] = v[1][j] = 0.0f;
+#pragma unroll 2
+              for (int o = 0; o < parts; ++o) {
+                const float* src = part_of(o) + row;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) v[b][j] += __ldcg(src + (b * n + min(c0 + j, n - 1)) * 128);
               }
             }
+            if (phase == 0) {
 #pragma unroll
-            for (int z = 0; z < VALS; ++z) h[z] = gate * (gs[z] / (1.0f + expf(-gs[z]))) * us[z];
+              for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (c0 + j < n) mine[(b * n + c0 + j) * 128] = v[b][j];
+              continue;
+            }
+            float h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              h[j] = __shfl_sync(0xFFFFFFFFu, gates, (c0 + j) & 31) * __fdividef(v[0][j], 1.0f + expf(-v[0][j])) * v[1][j];
+            // transpose: lane l of four keeps row c0 + l, values k0 .. k0 + 3
+#pragma unroll
+            for (int z = 1; z < 4; z *= 2) {
+              const bool up = (lane & z) != 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if ((j & z) == 0) {
+                  const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? h[j] : h[j | z], z);
+                  h[j] = up ? other : h[j];
+                  h[j | z] = up ? h[j | z] : other;
+                }
+            }
+            const int c = c0 + (lane & 3);
+            const bool live = c < n;
+            const int64_t hr = row0 + min(c, n - 1);
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int z = 4; z < (FMT == DEC_NV ? 16 : 32); z *= 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, z));
+            const int eb = block_exponent(m);
+            if (live && (lane & (FMT == DEC_NV ? 12 : 28)) == 0)
+              p.h.exps[hr * p.h_steps * EB + (FMT == DEC_NV ? k0 >> 4 : k0 >> 5)] = static_cast<uint8_t>(eb + 127);
+            if constexpr (FMT == DEC_NV) {
+              const int t = max(eb, __shfl_xor_sync(0xFFFFFFFFu, eb, 16));
+              if (live && (lane & 28) == 0) atomicMax(p.h.top + hr, t);
+            }
+            const uint64_t inv2 = f2_pack(block_multiplier<FMT>(eb), block_multiplier<FMT>(eb));
+            uint64_t ra = f2_mul(f2_pack(h[0], h[1]), inv2), rb = f2_mul(f2_pack(h[2], h[3]), inv2);
+            uint8_t* dst = p.h.codes + hr * PH * pitch + (FMT == DEC_NV ? k0 >> 1 : k0);
+#pragma unroll
+            for (int d = 0; d < PH; ++d, dst += pitch) {
+              const uint64_t a = d + 1 < PH ? next_piece<FMT, false>(ra) : next_piece<FMT, true>(ra);
+              const uint64_t b = d + 1 < PH ? next_piece<FMT, false>(rb) : next_piece<FMT, true>(rb);
+              if (!live) continue;
+              if constexpr (FMT == DEC_NV) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(e2m1x4_f2(a, b));
+              else *reinterpret_cast<uint32_t*>(dst) = e4m3x2_f2(a) | (e4m3x2_f2(b) << 16);
+            }
           }
-          uint32_t m = 0;
-#pragma unroll
-          for (int z = 0; z < VALS; ++z) m = max(m, __float_as_uint(h[z]) & 0x7FFFFFFFu);
-          if constexpr (FMT == DEC_MX) {   // four threads a block
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-          }
-          const int eb = block_exponent(m);
-          if (live && (FMT == DEC_NV || (g & 3) == 0))
-            p.h.exps[hr * p.h_steps * EB + (FMT == DEC_NV ? k0 >> 4 : k0 >> 5)] = static_cast<uint8_t>(eb + 127);
-          const uint64_t inv2 = f2_pack(block_multiplier<FMT>(eb), block_multiplier<FMT>(eb));
-          uint64_t r[VALS / 2];
-#pragma unroll
-          for (int z = 0; z < VALS / 2; ++z) r[z] = f2_mul(f2_pack(h[2 * z], h[2 * z + 1]), inv2);
-          uint8_t* dst = p.h.codes + hr * PH * pitch + (FMT == DEC_NV ? k0 >> 1 : k0);
-#pragma unroll
-          for (int d = 0; d < PH; ++d) {
-            const uint2 code = d + 1 < PH ? next_codes<FMT, false>(r) : next_codes<FMT, true>(r);
-            if (live) *reinterpret_cast<uint2*>(dst + d * pitch) = code;
-          }
-          if constexpr (FMT == DEC_NV) {   // eight threads a row
-            int t = live ? eb : -128;
-#pragma unroll
-            for (int d = 4; d >= 1; d >>= 1) t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, d));
-            if (live && g == 0) atomicMax(p.h.top + hr, t);
-          }
+          if (phase == 0 || !staged) release();
         }
-        epi_barrier();   // all have read the parts before the next unit overwrites them
       }
       i += r1 - r0;
       q = place_of(i);
@@ -879,7 +932,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, DEC_TMEM_COLS);
+    tmem_dealloc(tmem, L.tmem_cols);
   }
 }
 
@@ -952,7 +1005,8 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
   L.smem = DEC_SMEM_HALF;
   if ((L.smem - fixed) / stage < 3) L.smem = DEC_SMEM_FULL;
   L.stages = std::min(DEC_MAX_STAGES, (L.smem - fixed) / stage);
-  L.sf_sets = std::min(L.stages, (static_cast<int>(DEC_TMEM_COLS) - L.sf_col) / L.sf_cols);
+  L.tmem_cols = L.smem == DEC_SMEM_HALF ? DEC_TMEM_HALF : DEC_TMEM_FULL;
+  L.sf_sets = std::min(L.stages, (static_cast<int>(L.tmem_cols) - L.sf_col) / L.sf_cols);
   if (L.stages < 3 || L.sf_sets < 2) return false;
   L.b = L.stages * DEC_A_STAGE;
   L.sfb = L.b + L.stages * L.b_stage;
@@ -964,7 +1018,8 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
 }
 static_assert(2 * DEC_MAX_STAGES * 8 + 5 * 8 + 16 <= 384, "barriers and flags");
 static_assert(dec_group(DEC_MX, DEC_DOWN) * 3 <= 160 && dec_group(DEC_MX, DEC_UP) * 2 * 2 <= 160 &&
-                  dec_group(DEC_NV, DEC_UP) * 5 * 2 <= 160 && DEC_CHUNK * 5 <= 160,
+                  dec_group(DEC_NV, DEC_UP) * 5 * 2 <= 160 && dec_group(DEC_NV, DEC_LINEAR) * 5 <= 160 &&
+                  dec_group(DEC_MX, DEC_LINEAR) * 2 <= 128,
               "accumulators");
 
 // Per-device set-up of one kernel instance (dynamic shared memory, and the carve-out that lets two CTAs
@@ -1080,7 +1135,7 @@ LinWs lin_ws_layout(int fmt, int64_t T, int64_t K) {
   w.n_counters = 4 * DEC_MAX_CTAS;   // chunks * units that are shared: fewer than the CTAs
   w.counters = w.x.end;
   w.part = align256(w.counters + static_cast<size_t>(w.n_counters) * sizeof(int));
-  w.end = w.part + static_cast<size_t>(DEC_MAX_CTAS) * std::min<int64_t>(T, DEC_CHUNK) * 128 * sizeof(float);
+  w.end = w.part + static_cast<size_t>(DEC_MAX_CTAS) * std::min<int64_t>(T, dec_group(fmt, DEC_LINEAR)) * 128 * sizeof(float);
   return w;
 }
 
@@ -1217,7 +1272,7 @@ int matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, c
   if (FMT == DEC_NV && w_amax == nullptr) return MXFP8_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   DecParams p{};
-  p.chunks = static_cast<int>((T + DEC_CHUNK - 1) / DEC_CHUNK);
+  p.chunks = static_cast<int>((T + dec_group(FMT, DEC_LINEAR) - 1) / dec_group(FMT, DEC_LINEAR));
   p.per_chunk = static_cast<int>((T + p.chunks - 1) / p.chunks);
   p.box_rows = p.per_chunk;
   CUtensorMap m, mx;
