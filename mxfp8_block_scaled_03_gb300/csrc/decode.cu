@@ -372,18 +372,19 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
 //   NVFP4  one word per MMA, the same for all digits: UE4M3 2^(8 + e - top) per block (0 below 2^-9, which
 //          drops values under 2^-17 of the row's largest).
 // Blocks that are not finite get a NaN scale.
+// (Plain arithmetic: the byte-wise intrinsics are chains of instructions, 0.4 us a step for a warp alone.)
 __device__ __forceinline__ uint32_t mx_scales(uint32_t e4, int q) {
-  const uint32_t nan = __vcmpeq4(e4, 0xFFFFFFFFu);
-  return __vsub4(e4, 0x07070707u + 0x04040404u * static_cast<uint32_t>(q)) | nan;
+  const uint32_t ones = ((e4 & 0x7F7F7F7Fu) + 0x01010101u) & e4 & 0x80808080u;   // the top bit of a byte of ones
+  return (e4 - (0x07070707u + 0x04040404u * static_cast<uint32_t>(q))) | ((ones >> 7) * 0xFFu);   // e4 >= 27: no borrow
 }
 __device__ __forceinline__ uint32_t nv_scales(uint32_t e4, int top) {
-  // u = e - top + 18 - 127 >= 0, four bytes at once: 2^(u - 10) is 0, 1, 2, 4 (subnormal) for u = 0 .. 3 and
-  // (u - 3) << 3 above
-  const uint32_t u = __vsubus4(e4, static_cast<uint32_t>(top + 109) * 0x01010101u);
-  const uint32_t sub = u & __vcmpleu4(u, 0x03030303u);
-  const uint32_t code = (__vsubus4(u, 0x03030303u) << 3) + sub + (__vcmpeq4(sub, 0x03030303u) & 0x01010101u);
-  const uint32_t nan = __vcmpeq4(e4, 0xFFFFFFFFu);
-  return (code & ~nan) | (nan & 0x7F7F7F7Fu);
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = static_cast<int>((e4 >> (8 * i)) & 0xFFu);
+    v[i] = __uint_as_float(e == 255 ? 0x7FC00000u : static_cast<uint32_t>(max(e - top + 8, 0)) << 23);
+  }
+  return e4m3x2_f2(f2_pack(v[0], v[1])) | (e4m3x2_f2(f2_pack(v[2], v[3])) << 16);
 }
 
 // The K steps of all units (128-row tiles; MoE: of a chosen expert, for a group of its tokens) form one
@@ -631,12 +632,15 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     // MXFP8 (ROWS rows a lane), and NVFP4 with more than eight rows: lane = row, all its words; NVFP4 with up
     // to eight: lane = (word, row), one of the row's four words.
     static_assert(FMT == DEC_MX || ROWS == 1, "one row a lane");
+    // One warp does all of a step, so the code between two steps is kept short, and nothing touches a loaded value
+    // before the step it is for.
     struct Scales {
       uint32_t e[ATOMS * ROWS];
-      int c, top, n, nat;   // row of the unit (lanes past the last: none) and its reference, rows, atoms per MMA
+      int c, top, n, nat, f;   // row of the unit (lanes past the last: none) and its reference, rows, atoms per MMA
       bool spread;
     };
-    int entry = -1, row = 0;
+    int entry = -1;
+    const uint8_t* src = nullptr;   // of this lane's row
     Scales cur{}, next{};
     auto load = [&](const Place& q, Scales& v) {
       if (q.a != entry) {
@@ -645,37 +649,35 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         v.nat = (mma_columns(q.a) + 127) >> 7;
         v.spread = FMT == DEC_NV && v.n <= 8;
         v.c = v.spread ? lane & 7 : lane;
-        row = first_row(q.a) + min(v.c, v.n - 1);
+        const int row = first_row(q.a) + min(v.c, v.n - 1);
         if constexpr (FMT == DEC_NV) v.top = p.in.top[row];
+        src = p.in.exps + static_cast<int64_t>(row) * p.steps * EB + (v.spread ? (lane >> 3) * 4 : 0);
       }
-      const uint8_t* src = p.in.exps + (static_cast<int64_t>(row) * p.steps + q.f) * EB;
+      v.f = q.f;
+      const uint8_t* at = src + q.f * EB;
       if constexpr (FMT == DEC_NV) {
         if (v.spread) {
-          v.e[0] = (q.f * 4 + (lane >> 3)) * 64 < p.K ? *reinterpret_cast<const uint32_t*>(src + (lane >> 3) * 4) : 0u;
+          v.e[0] = *reinterpret_cast<const uint32_t*>(at);
         } else {
-          const uint4 w = *reinterpret_cast<const uint4*>(src);
+          const uint4 w = *reinterpret_cast<const uint4*>(at);
           v.e[0] = w.x; v.e[1] = w.y; v.e[2] = w.z; v.e[3] = w.w;
-#pragma unroll
-          for (int m = 0; m < 4; ++m)   // blocks past the row's end
-            if ((q.f * 4 + m) * 64 >= p.K) v.e[m] = 0;
         }
       } else {
 #pragma unroll
         for (int z = 0; z < ROWS; ++z)
           if (z * 32 < v.n) {
             const int more = min(v.c + z * 32, v.n - 1) - min(v.c, v.n - 1);
-            v.e[z] = *reinterpret_cast<const uint32_t*>(src + static_cast<int64_t>(more) * p.steps * EB);
+            v.e[z] = *reinterpret_cast<const uint32_t*>(at + static_cast<int64_t>(more) * p.steps * EB);
           }
       }
     };
-    // word of atom m for column col
-    auto word = [&](uint8_t* sf, int nat, int m, int col) {
-      return reinterpret_cast<uint32_t*>(sf + (m * nat + (col >> 7)) * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4);
-    };
+    // place of a column's word of the first atom, from the start of the step's scales
+    auto word = [](int col) { return (col >> 7) * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4; };
     Place q = place_of(cw);
     pdl_wait();
     if (cw < n_steps) load(q, cur);
     int slot = cw, set = cw % L.sf_sets;
+    const int set_next = DEC_SCALE_WARPS % L.sf_sets;
     Ring read{cw >= L.sf_sets ? cw - L.sf_sets : 0, 0};   // stage of step i - sf_sets
     const uint64_t desc_sfb = sdesc_sf_atom(smem_u32(smem + L.sfb));
     for (int i = cw; i < n_steps; i += DEC_SCALE_WARPS) {
@@ -685,12 +687,16 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         for (int z = 0; z < DEC_SCALE_WARPS; ++z) advance(q, i + z);
         load(q, next);
       }
-      uint32_t w[ATOMS];
+      uint32_t w[ATOMS * ROWS];
       if constexpr (FMT == DEC_NV) {
-        w[0] = nv_scales(cur.e[0], cur.top);
+        // words past the row's end count as zeros
+        w[0] = nv_scales((cur.f * 4 + (cur.spread ? lane >> 3 : 0)) * 64 < p.K ? cur.e[0] : 0u, cur.top);
         if (!cur.spread)
 #pragma unroll
-          for (int m = 1; m < 4; ++m) w[m] = nv_scales(cur.e[m], cur.top);
+          for (int m = 1; m < 4; ++m) w[m] = nv_scales((cur.f * 4 + m) * 64 < p.K ? cur.e[m] : 0u, cur.top);
+      } else {
+#pragma unroll
+        for (int z = 0; z < ROWS; ++z) w[z] = cur.e[z];
       }
       if (i >= L.sf_sets) {
         if (!dec_warp_wait(&empty[read.slot], read.phase, abort_flag, p, ERR_TIMEOUT_SF, lane)) break;
@@ -705,15 +711,14 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         if (cur.c + z * 32 >= cur.n) break;
 #pragma unroll
         for (int d = 0; d < P; ++d) {
-          const int col = (cur.c + z * 32) * P + d;
+          uint8_t* dst = sf + word((cur.c + z * 32) * P + d);
           if constexpr (FMT == DEC_MX) {
-            *word(sf, 1, 0, col) = mx_scales(cur.e[z], d);
+            *reinterpret_cast<uint32_t*>(dst) = mx_scales(w[z], d);
           } else if (cur.spread) {
-            *word(sf, 1, lane >> 3, col) = w[0];
+            *reinterpret_cast<uint32_t*>(dst + (lane >> 3) * 512) = w[0];
           } else {
-            uint32_t* dst = word(sf, cur.nat, 0, col);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) dst[m * cur.nat * 128] = w[m];
+            for (int m = 0; m < 4; ++m) *reinterpret_cast<uint32_t*>(dst + m * cur.nat * 512) = w[m];
           }
         }
       }
@@ -728,7 +733,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       __syncwarp();
       cur = next;
       slot = slot + DEC_SCALE_WARPS < L.stages ? slot + DEC_SCALE_WARPS : slot + DEC_SCALE_WARPS - L.stages;
-      set = (set + DEC_SCALE_WARPS) % L.sf_sets;
+      set += set_next;
+      if (set >= L.sf_sets) set -= L.sf_sets;
     }
     if (cw < n_steps && elect_one()) {
       tc_commit(&drained[1 + cw]);
