@@ -49,7 +49,7 @@ namespace mx {
 namespace {
 
 constexpr int DEC_THREADS = 256;             // warp 0 copies, warp 1 MMA, warps 2-3 scales, warps 4-7 epilogue
-constexpr int DEC_SCALE_WARPS = 2;
+constexpr int DEC_SCALE_WARPS = 2;           // they take turns
 constexpr int DEC_FIRST_EPI_WARP = 4;
 constexpr int DEC_A_STAGE = 128 * 128;       // 128 weight rows x 128 code bytes
 constexpr int DEC_MAX_TOKENS = 64;           // tokens of one call
@@ -174,6 +174,7 @@ __device__ __forceinline__ bool dec_wait(uint64_t* bar, uint32_t parity, volatil
 }
 __device__ __forceinline__ bool dec_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, const DecParams& p,
                                               uint32_t err_bit, int lane) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;   // mostly: one instruction for the warp
   int ok = 1;
   if (lane == 0) ok = dec_wait(bar, parity, abort, p, err_bit) ? 1 : 0;
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
@@ -683,8 +684,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     for (int i = cw; i < n_steps; i += DEC_SCALE_WARPS) {
       next = cur;
       if (i + DEC_SCALE_WARPS < n_steps) {
-#pragma unroll
-        for (int z = 0; z < DEC_SCALE_WARPS; ++z) advance(q, i + z);
+        // two steps on: mostly one along K of the same accumulator (UP), or two
+        if (q.f + 2 / ACCS < p.steps && (i >= n_share || i + 2 < n_share)) q.f += 2 / ACCS;
+        else advance(q, i), advance(q, i + 1);
         load(q, next);
       }
       uint32_t w[ATOMS * ROWS];
