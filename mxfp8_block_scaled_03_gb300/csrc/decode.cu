@@ -60,7 +60,7 @@ constexpr int DEC_MIN_STEPS = 4;             // K steps that make a CTA worth ha
 // kernel before it; the whole SM where that leaves fewer than three stages.
 constexpr int DEC_SMEM_HALF = 113 * 1024, DEC_SMEM_FULL = 226 * 1024;
 constexpr uint32_t DEC_TMEM_HALF = 256, DEC_TMEM_FULL = 512;   // likewise
-// TMEM columns: accumulators (at most 160), then as many sets of scales of A and B as fit, used in turn
+// TMEM columns: accumulators (at most 160, twice where they fit), then as many sets of scales of A and B as fit, used in turn
 // (at least two): a step's scales may be written while the MMAs of that many steps less one are pending.
 constexpr int SPLIT_THREADS = 1024;          // at most
 
@@ -85,6 +85,7 @@ struct DecLayout {
   int b_stage, sfb_stage;
   int b, sfa, sfb, bars, misc;
   int n_max;             // most columns of one accumulator (UP: the second one starts there)
+  int acc_two;           // 1: two buffers of accumulators, for alternate units
   int sf_col, sf_cols, sf_sets;   // TMEM: first column of the scale sets, columns per set, sets
   uint32_t tmem_cols;
 };
@@ -404,9 +405,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   const DecLayout& L = p.L;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);   // the copies landed and the columns' scales are in place
   uint64_t* empty = full + DEC_MAX_STAGES;                        // the MMAs have read the stage
-  uint64_t* acc_full = empty + DEC_MAX_STAGES;                    // this CTA's part of a unit is complete in TMEM
-  uint64_t* acc_empty = acc_full + 1;                             // the epilogue has read it
-  uint64_t* drained = acc_empty + 1;                              // [3] MMA warp, scale warps: nothing in flight
+  uint64_t* acc_full = empty + DEC_MAX_STAGES;                    // [2] this CTA's part of a unit is complete in TMEM
+  uint64_t* acc_empty = acc_full + 2;                             // [2] the epilogue has read it
+  uint64_t* drained = acc_empty + 2;                              // [3] MMA warp, scale warps: nothing in flight
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_nact = reinterpret_cast<int*>(tmem_holder + 2);
@@ -425,8 +426,10 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       mbar_init(&full[s], 2);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 4);
+    }
     for (int s = 0; s < 3; ++s) mbar_init(&drained[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -587,7 +590,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         const int n_mma = mma_columns(a), nat = (n_mma + 127) >> 7;
         const uint32_t idesc = FMT == DEC_NV ? idesc_nvf4(128, n_mma) : idesc_mxf8_e4m3(128, n_mma);
         uint32_t started = 0;   // accumulators that hold something
-        if (seg > 0 && !dec_wait(acc_empty, (seg - 1) & 1, abort_flag, p, ERR_TIMEOUT_MMA)) break;
+        const int buf = seg & L.acc_two;
+        if (seg > L.acc_two && !dec_wait(&acc_empty[buf], ((seg >> L.acc_two) - 1) & 1, abort_flag, p, ERR_TIMEOUT_MMA)) break;
         tc_fence_after();
         for (; i < n_steps && q.a == a && q.tile == tile; advance(q, i), ++i, next_stage(r)) {
           const int slot = r.slot;
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
           const uint64_t dsa = desc_sfa + slot * (ATOMS * 32);
           const uint32_t t_sfa = tmem + L.sf_col + set * L.sf_cols, t_sfb = t_sfa + 4 * ATOMS;
           if (++set == L.sf_sets) set = 0;
-          const uint32_t d = tmem + q.acc * L.n_max;
+          const uint32_t d = tmem + (buf * ACCS + q.acc) * L.n_max;
 #pragma unroll
           for (int m = 0; m < ATOMS; ++m) tc_copy_sf(t_sfa + 4 * m, dsa + 32 * m);
 #pragma unroll
@@ -615,7 +619,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
           tc_commit(&empty[slot]);
           any = true;
         }
-        if (ok) tc_commit(acc_full);
+        if (ok) tc_commit(&acc_full[buf]);
       }
       if (any) {
         tc_commit(drained);
@@ -747,7 +751,6 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     // ---------------- epilogue ----------------
     pdl_wait();
     const int quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     float alpha = 1.0f;
     if constexpr (FMT == DEC_NV) alpha = 1.0f / nv_encode_scale(__ldg(p.w_amax));
     int i = 0;
@@ -772,7 +775,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         return p.part + static_cast<int64_t>(c * p.chunks + chunk) * p.part_slot;
       };
 
-      if (!dec_warp_wait(acc_full, seg & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane)) break;
+      const int buf = seg & L.acc_two;
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * ACCS * L.n_max;
+      if (!dec_warp_wait(&acc_full[buf], (seg >> L.acc_two) & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane)) break;
       tc_fence_after();
       float* mine = part_of(share ? cta - u * per_unit : 0) + row;
       int* counter = p.counters + (chunk * shared + u) * 4 + quarter;   // each warp for its 32 weight rows
@@ -790,7 +795,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       auto release = [&]() {   // the next unit's MMAs may begin
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
       };
       if constexpr (!UP) {
 #pragma unroll 1
@@ -1005,7 +1010,6 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
   L.b_stage = n * 128;
   L.sfb_stage = dec_atoms(fmt) * ((n + 127) / 128) * 512;
   L.n_max = n;
-  L.sf_col = (mode == DEC_UP ? 2 : 1) * n;
   L.sf_cols = 4 * dec_atoms(fmt) * (1 + (n + 127) / 128);
   const int sfa = dec_atoms(fmt) * 512, bars = 384;
   const int fixed = 1024 + bars + (mode == DEC_LINEAR ? 0 : round_up(E * 8 + max_active * 12, 16));
@@ -1014,7 +1018,13 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
   if ((L.smem - fixed) / stage < 3) L.smem = DEC_SMEM_FULL;
   L.stages = std::min(DEC_MAX_STAGES, (L.smem - fixed) / stage);
   L.tmem_cols = L.smem == DEC_SMEM_HALF ? DEC_TMEM_HALF : DEC_TMEM_FULL;
-  L.sf_sets = std::min(L.stages, (static_cast<int>(L.tmem_cols) - L.sf_col) / L.sf_cols);
+  // two buffers of accumulators where that leaves three sets of scales
+  for (L.acc_two = 1; L.acc_two >= 0; --L.acc_two) {
+    L.sf_col = (mode == DEC_UP ? 2 : 1) * n << L.acc_two;
+    L.sf_sets = std::min(L.stages, (static_cast<int>(L.tmem_cols) - L.sf_col) / L.sf_cols);
+    if (L.sf_sets >= 3) break;
+  }
+  L.acc_two = std::max(L.acc_two, 0);
   if (L.stages < 3 || L.sf_sets < 2) return false;
   L.b = L.stages * DEC_A_STAGE;
   L.sfb = L.b + L.stages * L.b_stage;
@@ -1024,7 +1034,7 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
   *out = L;
   return true;
 }
-static_assert(2 * DEC_MAX_STAGES * 8 + 5 * 8 + 16 <= 384, "barriers and flags");
+static_assert(2 * DEC_MAX_STAGES * 8 + 7 * 8 + 16 <= 384, "barriers and flags");
 static_assert(dec_group(DEC_MX, DEC_DOWN) * 3 <= 160 && dec_group(DEC_MX, DEC_UP) * 2 * 2 <= 160 &&
                   dec_group(DEC_NV, DEC_UP) * 5 * 2 <= 160 && dec_group(DEC_NV, DEC_LINEAR) * 5 <= 160 &&
                   dec_group(DEC_MX, DEC_LINEAR) * 2 <= 128,
