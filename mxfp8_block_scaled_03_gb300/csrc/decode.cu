@@ -487,36 +487,29 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   const int slots = static_cast<int>(gridDim.x) / p.chunks, cta = static_cast<int>(blockIdx.x) / p.chunks;
   const int whole = units / slots, shared = units - whole * slots;
   const int per_unit = shared == 0 ? 1 : max(1, min(slots / shared, su / DEC_MIN_STEPS));   // CTAs of a shared unit
-  int s_share = 0, n_share = 0;        // this CTA's steps of its share, and
-  const int s_whole = cta * whole * su, n_whole = whole * su;   // of its whole units
+  // Place in the sequence: list entry, 128-row tile, K step, accumulator.  Divisions only here.
+  struct Place {
+    int a, tile, f, acc;
+  };
+  auto unit_at = [&](int u) { return Place{u / p.tiles, u % p.tiles, 0, 0}; };
+  const Place first_whole = unit_at(cta * whole);
+  Place first = first_whole;
+  int n_share = 0;   // this CTA's steps of its share
   if (cta < shared * per_unit) {
-    const int u = cta / per_unit, o = cta - u * per_unit;
-    s_share = (slots * whole + u) * su + su * o / per_unit;
-    n_share = (slots * whole + u) * su + su * (o + 1) / per_unit - s_share;
+    const int u = cta / per_unit, o = cta - u * per_unit, r = su * o / per_unit;
+    n_share = su * (o + 1) / per_unit - r;
+    first = unit_at(slots * whole + u);
+    first.f = UP ? r >> 1 : r;
+    first.acc = UP ? r & 1 : 0;
   }
-  const int n_steps = n_share + n_whole;
+  const int n_steps = n_share + whole * su;
   // Activation rows of list entry a (LINEAR: of the chunk), and the columns of its MMA.
   auto rows_of = [&](int a) { return MOE ? s_act_n[a] : min(p.per_chunk, p.T - chunk * p.per_chunk); };
   auto first_row = [&](int a) { return MOE ? s_act_row[a] : chunk * p.per_chunk; };
   auto mma_columns = [&](int a) { return (P * rows_of(a) + 15) & ~15; };
-  // Place in the sequence: list entry, 128-row tile, K step, accumulator.  Divisions only to start with.
-  struct Place {
-    int a, tile, f, acc;
-  };
-  auto place_of = [&](int i) {   // of this CTA's step i
-    Place q{0, 0, 0, 0};
-    if (i >= n_steps) return q;
-    const int s = i < n_share ? s_share + i : s_whole + i - n_share;
-    const int u = s / su, r = s - u * su;
-    q.a = u / p.tiles;
-    q.tile = u - q.a * p.tiles;
-    q.f = UP ? r >> 1 : r;
-    q.acc = UP ? r & 1 : 0;
-    return q;
-  };
   auto advance = [&](Place& q, int i) {   // from step i to the next
     if (i + 1 == n_share) {
-      q = place_of(n_share);
+      q = first_whole;
       return;
     }
     if constexpr (UP) q.acc ^= 1;
@@ -556,7 +549,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       };
       // fill the ring with weights before waiting for the activations the previous kernel writes
       const int fill = min(n_steps, L.stages);
-      Place q = place_of(0), w = q;
+      Place q = first, w = q;
       for (int i = 0; i < fill; advance(w, i), ++i) copy_weights(w, i);
       pdl_wait();
       for (; issued < fill; advance(q, issued), ++issued) copy_columns(q, issued);
@@ -584,7 +577,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       bool ok = true, any = false;
       Ring r{0, 0};
       int i = 0, set = 0;
-      Place q = place_of(0);
+      Place q = first;
       for (int seg = 0; ok && i < n_steps; ++seg) {
         const int a = q.a, tile = q.tile;
         const int n_mma = mma_columns(a), nat = (n_mma + 127) >> 7;
@@ -678,7 +671,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     };
     // place of a column's word of the first atom, from the start of the step's scales
     auto word = [](int col) { return (col >> 7) * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4; };
-    Place q = place_of(cw);
+    Place q = first;
+    if (cw != 0) advance(q, 0);
     pdl_wait();
     if (cw < n_steps) load(q, cur);
     int slot = cw, set = cw % L.sf_sets;
@@ -754,7 +748,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     float alpha = 1.0f;
     if constexpr (FMT == DEC_NV) alpha = 1.0f / nv_encode_scale(__ldg(p.w_amax));
     int i = 0;
-    Place q = place_of(0);
+    Place q = first;
     for (int seg = 0; i < n_steps; ++seg) {
       const bool share = i < n_share && per_unit > 1;
       const int r0 = q.f * ACCS + q.acc, r1 = i < n_share ? r0 + n_share : su;   // the part's steps of the unit
@@ -938,7 +932,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         }
       }
       i += r1 - r0;
-      q = place_of(i);
+      q.f = p.steps - 1;   // on from the last step of what was done
+      q.acc = ACCS - 1;
+      advance(q, i - 1);
     }
   }
   tc_fence_before();
@@ -1125,7 +1121,7 @@ bool dec_ws_layout(int fmt, int64_t T, int k, int64_t H, int64_t F, int E, DecWs
   DecWs w{};
   const int64_t pairs = T * k;
   const int group = dec_group(fmt, DEC_UP);
-  w.max_active = static_cast<int>(std::min<int64_t>(E, pairs) + pairs / group);
+  w.max_active = static_cast<int>(std::min<int64_t>(E, pairs) + (T > group ? pairs / group : 0));
   w.x = dec_operand(fmt, dec_pieces(fmt, DEC_UP), 256, pairs, H);
   w.h = dec_operand(fmt, dec_pieces(fmt, DEC_DOWN), w.x.end, pairs, F);
   // only units that are shared use counters, and those are fewer than the CTAs
@@ -1190,7 +1186,8 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
   if (FMT == DEC_NV && (w1_amax == nullptr || w2_amax == nullptr)) return MXFP8_ERR_INVALID_ARG;
   // steps of all units, as the kernels count them
   const int64_t act = ws.max_active;
-  if (act * (F / 128) * 2 * ws.x.steps > INT32_MAX || act * (H / 128) * ws.h.steps > INT32_MAX)
+  if (std::max<int64_t>(act * (F / 128), DEC_MAX_CTAS) * 2 * ws.x.steps > INT32_MAX ||
+      std::max<int64_t>(act * (H / 128), DEC_MAX_CTAS) * ws.h.steps > INT32_MAX)
     return MXFP8_ERR_UNSUPPORTED;
 
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -1278,7 +1275,7 @@ int matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, c
   if (T < 0 || K <= 0 || N < 0) return MXFP8_ERR_INVALID_ARG;
   if (T > DEC_MAX_TOKENS || K % 128 != 0 || N % 128 != 0 || K > INT32_MAX || N > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
   const LinWs ws = lin_ws_layout(FMT, T, K);
-  if (N / 128 * ws.x.steps > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
+  if (std::max<int64_t>(N / 128, DEC_MAX_CTAS) * ws.x.steps > INT32_MAX) return MXFP8_ERR_UNSUPPORTED;
   if (workspace == nullptr) return MXFP8_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < ws.end) return MXFP8_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -251,3 +251,32 @@ def test_waits_that_run_out_are_reported(mx):
     code = "from tests.test_gpu_decode_edges import timeout_child; timeout_child()"
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
+
+
+@FORMATS
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 128), (2, 14336, 640), (3, 4352, 1024), (4, 8192, 4096), (1, 2048, 9600),
+                                   (9, 4096, 1152), (33, 2048, 384)])
+def test_units_shared_by_several_ctas(mx, fmt, T, K, N):
+    """Few tiles and long rows: every tile's sum is put together from the parts of several CTAs."""
+    w, wv = D.weight(mx, fmt, N, K, seed=T)
+    x = D.activations(T, K, seed=K)
+    y = D.matvec(mx, fmt, x, w)
+    ref, S = x.double() @ wv.t(), D.block_max(x.double(), 32 if fmt == "mxfp8" else 16) @ wv.abs().t()
+    D.check(y, ref, 2.0 ** -8 * ref.abs() + 2.0 ** -12 * S + 1e-30)
+
+
+@FORMATS
+@pytest.mark.parametrize("T,k,E,H,F", [(1, 2, 16, 4096, 2048), (2, 3, 4, 2048, 1152), (4, 1, 8, 8192, 384),
+                                       (3, 8, 32, 2048, 640)])
+def test_experts_shared_by_several_ctas(mx, fmt, T, k, E, H, F):
+    w1, v1 = D.weight(mx, fmt, E * 2 * F, H, seed=1)
+    w2, v2 = D.weight(mx, fmt, E * H, F, seed=2)
+    x = D.activations(T, H, seed=3)
+    rng = np.random.default_rng(T)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[0, 0] = -1 if T > 1 else ids[0, 0]      # fewer experts than there may be
+    ids, gates = G.to_dev(ids), G.to_dev(rng.random((T, k), dtype=np.float32))
+    y = D.moe(mx, fmt, x, ids, gates, w1, w2)
+    ref, bound = D.moe_ref(fmt, x, ids, gates, v1, v2, E, H, F)
+    D.check(y, ref, bound)
+    assert all((D.moe(mx, fmt, x, ids, gates, w1, w2) == y).all() for _ in range(3))
