@@ -129,6 +129,28 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
+// Copies of weights: read once, so first to leave the L2 (activations, workspace and instructions stay).
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void tma_load_weights(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4}], "
+      "[%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load_weights(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                                  uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
 // One lane of the (converged) warp.  The compiler knows that a branch on it holds one thread, and issues
 // copies and MMAs there directly; behind `lane == 0` it wraps each of them in a loop over the lanes.
 __device__ __forceinline__ bool elect_one() {
@@ -535,13 +557,14 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     // ---------------- copies (one lane) ----------------
     int issued = 0;
     if (elect_one()) {
+      const uint64_t policy = evict_first();
       auto copy_weights = [&](const Place& q, int slot) {
         int row = q.tile * 128;
         if constexpr (MOE) row += (s_act_e[q.a] * ACCS + q.acc) * (p.tiles * 128);
         mbar_arrive_expect_tx(&full[slot], DEC_A_STAGE + ATOMS * 512 + p.box_rows * P * 128);
-        tma_load_2d(smem + slot * DEC_A_STAGE, &tm_w, &full[slot], q.f * 128, row);
-        bulk_load(smem + L.sfa + slot * ATOMS * 512,
-                  p.w_sf + (static_cast<int64_t>(row >> 7) * p.kt + q.f * ATOMS) * 512, ATOMS * 512, &full[slot]);
+        tma_load_weights(smem + slot * DEC_A_STAGE, &tm_w, &full[slot], q.f * 128, row, policy);
+        bulk_load_weights(smem + L.sfa + slot * ATOMS * 512,
+                  p.w_sf + (static_cast<int64_t>(row >> 7) * p.kt + q.f * ATOMS) * 512, ATOMS * 512, &full[slot], policy);
       };
       // the unit's columns and whatever follows them: a box has a fixed height
       auto copy_columns = [&](const Place& q, int slot) {
