@@ -30,8 +30,21 @@
 //   k_sum_rows       adds a token's pairs
 //   k_decode<LINEAR> units: 128 rows of W
 // The kernels are launched programmatically dependent: a kernel's weight copies start while the one
-// before it runs, and only what reads its results waits.  Two CTAs share an SM (one alone reaches 60-87%
-// of the copy bandwidth: its single MMA thread spends 0.3-0.5 us a K step of 16 KB).
+// before it runs, and only what reads its results waits.  Weights are copied evict-first, so that everything
+// else stays in L2 (NVFP4, 64 experts 2048x1408, 64 tokens: 69 us, 77 without).
+// Two CTAs share an SM.  A CTA is bound by its own instructions, 0.2-0.45 us a K step of 16 KB (the MMA thread,
+// and the two warps that turn exponents into scales), an SM draws a step from memory in 0.35 us, and a kernel's
+// first and last microseconds have one CTA's latencies: one CTA per SM with twice the stages measured the
+// same to 3% for 1 to 16 tokens, but 170 us against 142 (MoE, NVFP4, 8 experts 4096x14336, 64 tokens) and 34
+// against 27 (linear, MXFP8, 61x4096->28672).
+// Measured (replayed graph, every call on other weights; share of the 6.77 TB/s a copy reaches):
+//   MoE 8 experts 4096x14336, k 2    MXFP8  1 token 66.7 us (81%), 16 226 (95%), 64 235 (91%)
+//                                    NVFP4  1 token 42.0 us (70%), 16 130 (90%), 64 142 (82%)
+//   MoE 64 experts 2048x1408, k 8    MXFP8  1 token 24.6 us (43%), 8 68.3 (82%), 64 104.5 (81%)
+//                                    NVFP4  1 token 20.3 us (28%), 8 45.7 (67%), 64 69.3 (66%)
+//   linear 4096->28672               MXFP8  1 token 22.6 us (79%), 61 27.0 (68%)
+//                                    NVFP4  1 token 15.0 us (65%), 61 26.0 (40%)
+//   linear 1x4096->4096              MXFP8  9.0 us, NVFP4 8.2: launch, columns, first weights, parts, one after the other
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -55,13 +68,16 @@ constexpr int DEC_A_STAGE = 128 * 128;       // 128 weight rows x 128 code bytes
 constexpr int DEC_MAX_TOKENS = 64;           // tokens of one call
 constexpr int DEC_MAX_K = 32;                // choices per token
 constexpr int DEC_MAX_STAGES = 12;
-constexpr int DEC_MIN_STEPS = 4;             // K steps that make a CTA worth having (2 and 8 measured the same)
+// K values that make a CTA worth having in a shared unit: 4 steps of NVFP4, 8 of MXFP8.  Measured, 1x4096->4096 and one
+// token on 64 experts 2048x1408: NVFP4 8.2 and 20.3 us (half: 8.5, 21.3; twice: 8.9, 21.1), MXFP8 9.0 and 24.6 us
+// (half: 9.3, 25.9).
+constexpr int DEC_MIN_VALUES = 1024;
 // Half of 228 KB less the 1 KB the system keeps per CTA, so that a kernel's CTAs fit beside those of the
 // kernel before it; the whole SM where that leaves fewer than three stages.
 constexpr int DEC_SMEM_HALF = 113 * 1024, DEC_SMEM_FULL = 226 * 1024;
 constexpr uint32_t DEC_TMEM_HALF = 256, DEC_TMEM_FULL = 512;   // likewise
-// TMEM columns: accumulators (at most 160, twice where they fit), then as many sets of scales of A and B as fit, used in turn
-// (at least two): a step's scales may be written while the MMAs of that many steps less one are pending.
+// TMEM columns: accumulators (at most 160, twice where they fit), then as many sets of scales of A and B as fit, used in
+// turn (at least two): a step's scales may be written while the MMAs of that many steps less one are pending.
 constexpr int SPLIT_THREADS = 1024;          // at most
 
 enum DecMode { DEC_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
@@ -73,8 +89,8 @@ constexpr int dec_step_values(int fmt) { return fmt == DEC_NV ? 256 : 128; }
 constexpr int dec_atoms(int fmt) { return fmt == DEC_NV ? 4 : 1; }          // scale atoms per 128 rows and step
 constexpr int dec_exp_bytes(int fmt) { return fmt == DEC_NV ? 16 : 4; }     // blocks of one row and step
 // Most rows of a unit.  LINEAR: one accumulator of at most 128 (MXFP8) or 160 (NVFP4) columns; more tokens come
-// in two chunks.  MoE: two accumulators of at most 80 (an expert with more tokens gives several units).  Units of
-// the same weights read them side by side, from L2.
+// in two chunks (MXFP8, 61x4096->28672: 28.7 us in one, 30.6 in two).  MoE: two accumulators of at most 80 (an
+// expert with more tokens gives several units).  Units of the same weights read them side by side, from L2.
 constexpr int dec_group(int fmt, int mode) {
   return fmt == DEC_NV ? (mode == DEC_LINEAR ? 32 : 16) : (mode == DEC_LINEAR ? 64 : 32);
 }
@@ -109,7 +125,7 @@ struct DecParams {
   uint16_t* out;          // LINEAR: [T, N]
   float* y;               // DOWN: [pairs, H]
   uint32_t* err;
-  float* part;            // partial sums: part_slot floats per CTA, MoE twice
+  float* part;            // partial sums: part_slot floats per CTA
   int part_slot;
   int* counters;          // [units][4] of units shared by several CTAs: how many are done with a quarter of the rows
   int T, k, E;
@@ -300,8 +316,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
   uint4 ahead[VALS / 8];
 #pragma unroll
   for (int i = 0; i < VALS / 8; ++i)
-    ahead[i] = tid < groups ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.K + tid * VALS) + i)
-                            : make_uint4(0u, 0u, 0u, 0u);
+    ahead[i] = tid < groups
+                   ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.K + tid * VALS) + i)
+                   : make_uint4(0u, 0u, 0u, 0u);
   int bad = 0;
   if constexpr (BY_PAIR)
     for (int i = tid; i < p.n_ids; i += blockDim.x) {
@@ -420,12 +437,12 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   constexpr int P = dec_pieces(FMT, MODE);
   constexpr int ATOMS = dec_atoms(FMT), EB = dec_exp_bytes(FMT);
   constexpr bool UP = MODE == DEC_UP, MOE = MODE != DEC_LINEAR;
-  constexpr int ACCS = UP ? 2 : 1;
+  constexpr int ACCS = UP ? 2 : 1, MIN_STEPS = DEC_MIN_VALUES / dec_step_values(FMT);
   constexpr int GROUP = dec_group(FMT, MODE), ROWS = (GROUP + 31) / 32;   // ROWS: of a unit, per lane of a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const DecLayout& L = p.L;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);   // the copies landed and the columns' scales are in place
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);   // the copies landed, the columns' scales are in place
   uint64_t* empty = full + DEC_MAX_STAGES;                        // the MMAs have read the stage
   uint64_t* acc_full = empty + DEC_MAX_STAGES;                    // [2] this CTA's part of a unit is complete in TMEM
   uint64_t* acc_empty = acc_full + 2;                             // [2] the epilogue has read it
@@ -504,11 +521,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   const int su = UP ? 2 * p.steps : p.steps;                    // steps of a unit
   const int units = MOE ? *s_nact * p.tiles : p.tiles;
   // Every CTA takes the same number of whole units; the units left over are shared, each by as many CTAs as fit
-  // (and find DEC_MIN_STEPS steps).  The share comes first, so that adding its parts up is hidden.  (Dealing the
+  // (and find MIN_STEPS steps).  The share comes first, so that adding its parts up is hidden.  (Dealing the
   // left-over steps out evenly, with two parts of units in a CTA, measured 5-15% slower: more sums of parts.)
   const int slots = static_cast<int>(gridDim.x) / p.chunks, cta = static_cast<int>(blockIdx.x) / p.chunks;
   const int whole = units / slots, shared = units - whole * slots;
-  const int per_unit = shared == 0 ? 1 : max(1, min(slots / shared, su / DEC_MIN_STEPS));   // CTAs of a shared unit
+  const int per_unit = shared == 0 ? 1 : max(1, min(slots / shared, su / MIN_STEPS));   // CTAs of a shared unit
   // Place in the sequence: list entry, 128-row tile, K step, accumulator.  Divisions only here.
   struct Place {
     int a, tile, f, acc;
@@ -564,7 +581,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         mbar_arrive_expect_tx(&full[slot], DEC_A_STAGE + ATOMS * 512 + p.box_rows * P * 128);
         tma_load_weights(smem + slot * DEC_A_STAGE, &tm_w, &full[slot], q.f * 128, row, policy);
         bulk_load_weights(smem + L.sfa + slot * ATOMS * 512,
-                  p.w_sf + (static_cast<int64_t>(row >> 7) * p.kt + q.f * ATOMS) * 512, ATOMS * 512, &full[slot], policy);
+                          p.w_sf + (static_cast<int64_t>(row >> 7) * p.kt + q.f * ATOMS) * 512, ATOMS * 512,
+                          &full[slot], policy);
       };
       // the unit's columns and whatever follows them: a box has a fixed height
       auto copy_columns = [&](const Place& q, int slot) {
@@ -607,7 +625,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         const uint32_t idesc = FMT == DEC_NV ? idesc_nvf4(128, n_mma) : idesc_mxf8_e4m3(128, n_mma);
         uint32_t started = 0;   // accumulators that hold something
         const int buf = seg & L.acc_two;
-        if (seg > L.acc_two && !dec_wait(&acc_empty[buf], ((seg >> L.acc_two) - 1) & 1, abort_flag, p, ERR_TIMEOUT_MMA)) break;
+        if (seg > L.acc_two &&
+            !dec_wait(&acc_empty[buf], ((seg >> L.acc_two) - 1) & 1, abort_flag, p, ERR_TIMEOUT_MMA))
+          break;
         tc_fence_after();
         for (; i < n_steps && q.a == a && q.tile == tile; advance(q, i), ++i, next_stage(r)) {
           const int slot = r.slot;
@@ -775,7 +795,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     for (int seg = 0; i < n_steps; ++seg) {
       const bool share = i < n_share && per_unit > 1;
       const int r0 = q.f * ACCS + q.acc, r1 = i < n_share ? r0 + n_share : su;   // the part's steps of the unit
-      const int u = share ? cta / per_unit : 0, parts = share ? per_unit : 1;      // which shared unit
+      const int u = cta / per_unit, parts = per_unit;   // if shared: which unit, how many parts
       const int n = rows_of(q.a), row0 = first_row(q.a), tile = q.tile;
       float unscale = 1.0f;   // lane c: of row c's sums
       if constexpr (FMT == DEC_NV) unscale = ldexpf(alpha, p.in.top[row0 + min(lane, n - 1)] - 9);
@@ -786,17 +806,15 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
         else p.out[o] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
       };
       // part o of the unit: [accumulator][activation row][128 weight rows], in the place of the CTA that has it
-      // (whole units of UP pass through a second place: the first may still be read by another CTA)
       auto part_of = [&](int o) {
-        const int c = share ? u * per_unit + o : slots + cta;
-        return p.part + static_cast<int64_t>(c * p.chunks + chunk) * p.part_slot;
+        return p.part + static_cast<int64_t>((u * per_unit + o) * p.chunks + chunk) * p.part_slot;
       };
 
       const int buf = seg & L.acc_two;
       const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * ACCS * L.n_max;
       if (!dec_warp_wait(&acc_full[buf], (seg >> L.acc_two) & 1, abort_flag, p, ERR_TIMEOUT_EPILOGUE, lane)) break;
       tc_fence_after();
-      float* mine = part_of(share ? cta - u * per_unit : 0) + row;
+      float* mine = part_of(cta - u * per_unit) + row;
       int* counter = p.counters + (chunk * shared + u) * 4 + quarter;   // each warp for its 32 weight rows
       // A part of a unit is in memory; true in the warp that finds all the others there too.
       auto last_part = [&]() {
@@ -860,22 +878,20 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       } else {
         // h from the gate and up sums, as columns of DOWN.  A lane has one weight row; four lanes transpose their
         // values of four activation rows, and each converts four values of one of them (a block is 16 or 32 lanes
-        // wide).  Sums that are parts, and those of many rows while more units follow, go through memory first,
-        // which frees the accumulators early.  Short straight code: its first pass is fetched instruction by
-        // instruction behind the weights' stream.
+        // wide).  (Passing the sums of whole units through memory as well, to free the accumulators earlier, measured
+        // the same.)  Short straight code: its first pass is fetched line by line behind the weights' stream.
         constexpr int PH = dec_pieces(FMT, DEC_DOWN), LD = (4 * P + 7) / 8;
         const bool has[2] = {r1 - r0 > 1 || (r0 & 1) == 0, r1 - r0 > 1 || (r0 & 1) == 1};
-        const bool staged = share || (n > 4 && i + r1 - r0 < n_steps);
         const float gates = p.gate[row0 + min(lane, n - 1)];
         const int64_t pitch = static_cast<int64_t>(p.h_steps) * 128;
         const int k0 = tile * 128 + quarter * 32 + (lane & ~3);   // of this lane's four values
 #pragma unroll 1
-        for (int phase = staged ? 0 : 1; phase < 2; ++phase) {
+        for (int phase = share ? 0 : 1; phase < 2; ++phase) {
           if (phase == 1 && share && !last_part()) break;
 #pragma unroll 1
           for (int c0 = 0; c0 < n; c0 += 4) {
             float v[2][4];   // [accumulator][row]
-            if (phase == 0 || !staged) {
+            if (phase == 0 || !share) {
               uint32_t d[2][8 * LD];
 #pragma unroll
               for (int b = 0; b < 2; ++b)
@@ -911,7 +927,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
             float h[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              h[j] = __shfl_sync(0xFFFFFFFFu, gates, (c0 + j) & 31) * __fdividef(v[0][j], 1.0f + expf(-v[0][j])) * v[1][j];
+              h[j] = __shfl_sync(0xFFFFFFFFu, gates, (c0 + j) & 31) * __fdividef(v[0][j], 1.0f + expf(-v[0][j])) *
+                     v[1][j];
             // transpose: lane l of four keeps row c0 + l, values k0 .. k0 + 3
 #pragma unroll
             for (int z = 1; z < 4; z *= 2) {
@@ -951,7 +968,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
               else *reinterpret_cast<uint32_t*>(dst) = e4m3x2_f2(a) | (e4m3x2_f2(b) << 16);
             }
           }
-          if (phase == 0 || !staged) release();
+          if (phase == 0 || !share) release();
         }
       }
       i += r1 - r0;
@@ -1037,7 +1054,8 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
   if ((L.smem - fixed) / stage < 3) L.smem = DEC_SMEM_FULL;
   L.stages = std::min(DEC_MAX_STAGES, (L.smem - fixed) / stage);
   L.tmem_cols = L.smem == DEC_SMEM_HALF ? DEC_TMEM_HALF : DEC_TMEM_FULL;
-  // two buffers of accumulators where that leaves three sets of scales
+  // Two buffers of accumulators, where that leaves three sets of scales: the next unit's MMAs start while one is read
+  // (NVFP4, 61x4096->28672: 26.0 us with, 28.1 without; fewer sets would hold up every step instead).
   for (L.acc_two = 1; L.acc_two >= 0; --L.acc_two) {
     L.sf_col = (mode == DEC_UP ? 2 : 1) * n << L.acc_two;
     L.sf_sets = std::min(L.stages, (static_cast<int>(L.tmem_cols) - L.sf_col) / L.sf_cols);
@@ -1155,7 +1173,7 @@ bool dec_ws_layout(int fmt, int64_t T, int k, int64_t H, int64_t F, int E, DecWs
   w.row_of = align256(w.gate + static_cast<size_t>(pairs) * sizeof(float));
   w.counters = align256(w.row_of + static_cast<size_t>(pairs) * sizeof(int));
   w.part = align256(w.counters + static_cast<size_t>(w.n_up + w.n_down) * sizeof(int));
-  w.end = w.part + static_cast<size_t>(2 * DEC_MAX_CTAS) * 2 * std::min<int64_t>(T, group) * 128 * sizeof(float);
+  w.end = w.part + static_cast<size_t>(DEC_MAX_CTAS) * 2 * std::min<int64_t>(T, group) * 128 * sizeof(float);
   *out = w;
   return true;
 }
