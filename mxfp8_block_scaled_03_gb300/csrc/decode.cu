@@ -61,9 +61,6 @@
 namespace mx {
 namespace {
 
-constexpr int DEC_THREADS = 256;             // warp 0 copies, warp 1 MMA, warps 2-3 scales, warps 4-7 epilogue
-constexpr int DEC_SCALE_WARPS = 2;           // they take turns
-constexpr int DEC_FIRST_EPI_WARP = 4;
 constexpr int DEC_A_STAGE = 128 * 128;       // 128 weight rows x 128 code bytes
 constexpr int DEC_MAX_TOKENS = 64;           // tokens of one call
 constexpr int DEC_MAX_K = 32;                // choices per token
@@ -82,6 +79,11 @@ constexpr int SPLIT_THREADS = 1024;          // at most
 
 enum DecMode { DEC_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
 enum DecFmt { DEC_MX = 0, DEC_NV = 1 };
+
+// Warp 0 copies, warp 1 issues MMAs, then come the warps that write the columns' scales (they take turns), and four
+// for the epilogue.
+constexpr int dec_scale_warps(int mode) { return mode == DEC_LINEAR ? 3 : 2; }
+constexpr int dec_threads(int mode) { return 32 * (2 + dec_scale_warps(mode) + 4); }
 
 // Columns per activation row: E4M3 pieces of a bf16 (2) or fp32 (3) value, or base-8 digits (5).
 constexpr int dec_pieces(int fmt, int mode) { return fmt == DEC_NV ? 5 : mode == DEC_DOWN ? 3 : 2; }
@@ -432,12 +434,13 @@ __device__ __forceinline__ uint32_t nv_scales(uint32_t e4, int top) {
 // sequence; a CTA runs through a part of one unit and then through whole ones.  Where several CTAs share a
 // unit, whoever finishes last sums the parts, in their order (the result does not depend on who it is).
 template <int FMT, int MODE>
-__global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant__ CUtensorMap tm_w,
+__global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_constant__ CUtensorMap tm_w,
                                                            const __grid_constant__ CUtensorMap tm_x, const DecParams p) {
   constexpr int P = dec_pieces(FMT, MODE);
   constexpr int ATOMS = dec_atoms(FMT), EB = dec_exp_bytes(FMT);
   constexpr bool UP = MODE == DEC_UP, MOE = MODE != DEC_LINEAR;
   constexpr int ACCS = UP ? 2 : 1, MIN_STEPS = DEC_MIN_VALUES / dec_step_values(FMT);
+  constexpr int THREADS = dec_threads(MODE), SCALE_WARPS = dec_scale_warps(MODE), FIRST_EPI_WARP = 2 + SCALE_WARPS;
   constexpr int GROUP = dec_group(FMT, MODE), ROWS = (GROUP + 31) / 32;   // ROWS: of a unit, per lane of a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -446,8 +449,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
   uint64_t* empty = full + DEC_MAX_STAGES;                        // the MMAs have read the stage
   uint64_t* acc_full = empty + DEC_MAX_STAGES;                    // [2] this CTA's part of a unit is complete in TMEM
   uint64_t* acc_empty = acc_full + 2;                             // [2] the epilogue has read it
-  uint64_t* drained = acc_empty + 2;                              // [3] MMA warp, scale warps: nothing in flight
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 3);
+  uint64_t* drained = acc_empty + 2;                              // [4] MMA warp, scale warps: nothing in flight
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_nact = reinterpret_cast<int*>(tmem_holder + 2);
   // MoE: tokens that chose the expert [E]; then the list of groups of tokens: expert, first pair, pairs
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], 4);
     }
-    for (int s = 0; s < 3; ++s) mbar_init(&drained[s], 1);
+    for (int s = 0; s < 1 + SCALE_WARPS; ++s) mbar_init(&drained[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -481,9 +484,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
 
   // ---- routing: which tokens chose which expert, and the list of chosen experts ----
   if constexpr (MOE) {
-    for (int e = tid; e < p.E; e += DEC_THREADS) s_mask[e] = 0;
+    for (int e = tid; e < p.E; e += THREADS) s_mask[e] = 0;
     __syncthreads();
-    for (int i = tid; i < p.T * p.k; i += DEC_THREADS) {
+    for (int i = tid; i < p.T * p.k; i += THREADS) {
       const int e = __ldg(p.experts + i);
       if (e >= 0 && e < p.E) atomicOr(reinterpret_cast<unsigned long long*>(&s_mask[e]), 1ull << (i / p.k));
     }
@@ -663,8 +666,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       }
     }
     __syncwarp();
-  } else if (warp < DEC_FIRST_EPI_WARP) {
-    // ---------------- the columns' scales: warp cw takes steps cw, cw + 2, ... ----------------
+  } else if (warp < FIRST_EPI_WARP) {
+    // ---------------- the columns' scales: warp cw takes every SCALE_WARPS-th step, from cw ----------------
     // It writes them to shared memory, has them copied to the step's set in TMEM (here, not by the MMA thread,
     // whose time per step is what limits a CTA), and the copies' completion counts on `full`.
     // The set (and the stage) must have been read by step i - sf_sets.  Fewer warps than stages: when a warp
@@ -715,19 +718,25 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
     // place of a column's word of the first atom, from the start of the step's scales
     auto word = [](int col) { return (col >> 7) * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4; };
     Place q = first;
-    if (cw != 0) advance(q, 0);
+#pragma unroll 1
+    for (int z = 0; z < cw; ++z) advance(q, z);
     pdl_wait();
     if (cw < n_steps) load(q, cur);
     int slot = cw, set = cw % L.sf_sets;
-    const int set_next = DEC_SCALE_WARPS % L.sf_sets;
+    const int set_next = SCALE_WARPS % L.sf_sets;
     Ring read{cw >= L.sf_sets ? cw - L.sf_sets : 0, 0};   // stage of step i - sf_sets
     const uint64_t desc_sfb = sdesc_sf_atom(smem_u32(smem + L.sfb));
-    for (int i = cw; i < n_steps; i += DEC_SCALE_WARPS) {
+    for (int i = cw; i < n_steps; i += SCALE_WARPS) {
       next = cur;
-      if (i + DEC_SCALE_WARPS < n_steps) {
-        // two steps on: mostly one along K of the same accumulator (UP), or two
-        if (q.f + 2 / ACCS < p.steps && (i >= n_share || i + 2 < n_share)) q.f += 2 / ACCS;
-        else advance(q, i), advance(q, i + 1);
+      if (i + SCALE_WARPS < n_steps) {
+        // mostly on along K, for the same accumulator
+        static_assert(SCALE_WARPS % ACCS == 0, "same accumulator");
+        if (q.f + SCALE_WARPS / ACCS < p.steps && (i >= n_share || i + SCALE_WARPS < n_share)) {
+          q.f += SCALE_WARPS / ACCS;
+        } else {
+#pragma unroll 1
+          for (int z = 0; z < SCALE_WARPS; ++z) advance(q, i + z);
+        }
         load(q, next);
       }
       uint32_t w[ATOMS * ROWS];
@@ -743,10 +752,10 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       }
       if (i >= L.sf_sets) {
         if (!dec_warp_wait(&empty[read.slot], read.phase, abort_flag, p, ERR_TIMEOUT_SF, lane)) break;
-        next_stage(read);
-        next_stage(read);
-      } else if (i + DEC_SCALE_WARPS >= L.sf_sets) {
-        read = Ring{i + DEC_SCALE_WARPS - L.sf_sets, 0};   // of the next step of this warp
+#pragma unroll
+        for (int z = 0; z < SCALE_WARPS; ++z) next_stage(read);
+      } else if (i + SCALE_WARPS >= L.sf_sets) {
+        read = Ring{i + SCALE_WARPS - L.sf_sets, 0};   // of the next step of this warp
       }
       uint8_t* sf = smem + L.sfb + slot * L.sfb_stage;
 #pragma unroll
@@ -775,7 +784,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_decode(const __grid_constant
       }
       __syncwarp();
       cur = next;
-      slot = slot + DEC_SCALE_WARPS < L.stages ? slot + DEC_SCALE_WARPS : slot + DEC_SCALE_WARPS - L.stages;
+      slot = slot + SCALE_WARPS < L.stages ? slot + SCALE_WARPS : slot + SCALE_WARPS - L.stages;
       set += set_next;
       if (set >= L.sf_sets) set -= L.sf_sets;
     }
@@ -1071,7 +1080,7 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
   *out = L;
   return true;
 }
-static_assert(2 * DEC_MAX_STAGES * 8 + 7 * 8 + 16 <= 384, "barriers and flags");
+static_assert(2 * DEC_MAX_STAGES * 8 + 8 * 8 + 16 <= 384, "barriers and flags");
 static_assert(dec_group(DEC_MX, DEC_DOWN) * 3 <= 160 && dec_group(DEC_MX, DEC_UP) * 2 * 2 <= 160 &&
                   dec_group(DEC_NV, DEC_UP) * 5 * 2 <= 160 && dec_group(DEC_NV, DEC_LINEAR) * 5 <= 160 &&
                   dec_group(DEC_MX, DEC_LINEAR) * 2 <= 128,
@@ -1116,7 +1125,7 @@ struct DecLaunch {
 template <int FMT, int MODE>
 bool dec_launch(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const DecParams& p, int sms, cudaStream_t stream) {
   const int ctas = p.L.smem == DEC_SMEM_HALF ? 2 * sms : sms;
-  DecLaunch l(ctas / p.chunks * p.chunks, DEC_THREADS, p.L.smem, stream);
+  DecLaunch l(ctas / p.chunks * p.chunks, dec_threads(MODE), p.L.smem, stream);
   return cudaLaunchKernelEx(&l.cfg, k_decode<FMT, MODE>, tm_w, tm_x, p) == cudaSuccess;
 }
 
