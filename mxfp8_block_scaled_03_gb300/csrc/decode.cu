@@ -843,13 +843,14 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
       };
       if constexpr (!UP) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < n; c0 += 8) {
-          uint32_t d[8 * P];
+        for (int c0 = 0; c0 < n; c0 += 4) {
+          constexpr int LD = (4 * P + 7) / 8;
+          uint32_t d[8 * LD];
 #pragma unroll
-          for (int z = 0; z < P; ++z) tmem_ld_32x32b_x8(t_row + c0 * P + z * 8, d + z * 8);
+          for (int z = 0; z < LD; ++z) tmem_ld_32x32b_x8(t_row + c0 * P + z * 8, d + z * 8);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             float x = sum_pieces<FMT, P>(d + j * P);
             if constexpr (FMT == DEC_NV) x *= __shfl_sync(0xFFFFFFFFu, unscale, c0 + j);
             if (c0 + j >= n) continue;
@@ -860,7 +861,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
         release();
         // whoever is last adds the parts up, in order
         if (share && last_part()) {
-          constexpr int TB = 4, OB = 4;   // 4 rows x 4 parts of loads in flight
+          constexpr int TB = 4, OB = 2;   // 4 rows x 2 parts of loads in flight
 #pragma unroll 1
           for (int c0 = 0; c0 < n; c0 += TB) {
             float sum[TB] = {};
