@@ -484,11 +484,13 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
 
   // ---- routing: which tokens chose which expert, and the list of chosen experts ----
   if constexpr (MOE) {
-    for (int e = tid; e < p.E; e += THREADS) s_mask[e] = 0;
+    const int ids = p.T * p.k;
+    int e = tid < ids ? __ldg(p.experts + tid) : -1;   // on its way meanwhile
+    for (int z = tid; z < p.E; z += THREADS) s_mask[z] = 0;
     __syncthreads();
-    for (int i = tid; i < p.T * p.k; i += THREADS) {
-      const int e = __ldg(p.experts + i);
-      if (e >= 0 && e < p.E) atomicOr(reinterpret_cast<unsigned long long*>(&s_mask[e]), 1ull << (i / p.k));
+    for (int i = tid; i < ids; i += THREADS, e = i < ids ? __ldg(p.experts + i) : -1) {
+      const int t = i / p.k;
+      if (e >= 0 && e < p.E) atomicOr(reinterpret_cast<uint32_t*>(&s_mask[e]) + (t >> 5), 1u << (t & 31));
     }
     __syncthreads();
     if (warp == 0) {
