@@ -568,10 +568,11 @@ def _need(t, dtype, shape, name: str):
     raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, {want}; got {t.dtype}, {tuple(t.shape)}")
 
 
-def _stream_of(t, stream) -> int:
-    """The given stream, or the current stream of the tensor's device."""
+def _stream_of(t) -> int:
+    """The current stream of the tensor's device.  A call with a stream of its own makes that one current first, so
+    that what the call allocates belongs to it."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else int(stream.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _sf_mma_bytes(nv: bool, M: int, K: int) -> int:
@@ -585,6 +586,9 @@ def moe_decode_workspace_size(T: int, k: int, H: int, F: int, E: int) -> int:
 
 def _moe_decode(name, nv, x, experts, gates, w1, w2, out, workspace, stream):
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _moe_decode(name, nv, x, experts, gates, w1, w2, out, workspace, None)
     u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
     T, H = x.shape
     T2, k = experts.shape
@@ -605,10 +609,10 @@ def _moe_decode(name, nv, x, experts, gates, w1, w2, out, workspace, stream):
     if nv:
         st = lib().nvfp4_moe_decode_fwd(px, T, H, F, E, k, pe, pg, p1, s1, _need(w1[2], f32, 1, "W1 amax"), p2, s2,
                                         _need(w2[2], f32, 1, "W2 amax"), po, pw, workspace.numel(),
-                                        _stream_of(x, stream))
+                                        _stream_of(x))
     else:
         st = lib().moe_decode_fwd(px, T, H, F, E, k, pe, pg, p1, s1, p2, s2, po, pw, workspace.numel(),
-                                  _stream_of(x, stream))
+                                  _stream_of(x))
     if st != OK:
         raise MXFP8Error(st, name)
     return out
@@ -636,6 +640,9 @@ def matvec_workspace_size(T: int = 64, K: int = 16384) -> int:
 
 def _matvec(name, nv, x, w, out, workspace, stream):
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _matvec(name, nv, x, w, out, workspace, None)
     u8, bf16 = torch.uint8, torch.bfloat16
     T, K = x.shape
     N = w[0].shape[0]
@@ -649,9 +656,9 @@ def _matvec(name, nv, x, w, out, workspace, stream):
     pw = _need(workspace, u8, 256, "workspace")
     if nv:
         st = lib().nvfp4_matvec(px, T, K, N, pq, ps, _need(w[2], torch.float32, 1, "amax"), po, pw, workspace.numel(),
-                                _stream_of(x, stream))
+                                _stream_of(x))
     else:
-        st = lib().mxfp8_matvec(px, T, K, N, pq, ps, po, pw, workspace.numel(), _stream_of(x, stream))
+        st = lib().mxfp8_matvec(px, T, K, N, pq, ps, po, pw, workspace.numel(), _stream_of(x))
     if st != OK:
         raise MXFP8Error(st, name)
     return out
@@ -694,6 +701,9 @@ def residual_norm_fwd(y, res, w_post=None, gate=None, w_pre=None, res_scale: flo
     channel), [T, 1] (per token) or None; post_norm False: no norm of y.  Returns (res_out, n bf16, stats
     float32 [2, T]); `out` may pass the three (res_out may be res)."""
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return residual_norm_fwd(y, res, w_post, gate, w_pre, res_scale, post_norm, eps, out)
     bf16 = torch.bfloat16
     T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res, w_post, gate, w_pre, post_norm)
     py, pr = _need(y, bf16, (T, H), "y"), _need(res, rt, (T, H), "res")
@@ -701,7 +711,7 @@ def residual_norm_fwd(y, res, w_post=None, gate=None, w_pre=None, res_scale: flo
         out = (torch.empty_like(res), torch.empty_like(y), torch.empty((2, T), dtype=torch.float32, device=y.device))
     st = lib().residual_norm_fwd(py, pr, pa, pg, pb, T, H, code, kind, 1 if post_norm else 0, res_scale, eps,
                                  _need(out[0], rt, (T, H), "res_out"), _need(out[1], bf16, (T, H), "n"),
-                                 _need(out[2], torch.float32, (2, T), "stats"), _stream_of(y, stream))
+                                 _need(out[2], torch.float32, (2, T), "stats"), _stream_of(y))
     if st != OK:
         raise MXFP8Error(st, "residual_norm_fwd")
     return tuple(out)
@@ -717,6 +727,9 @@ def residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post=None, gate=None, w
     for 0); y, res_out, stats as the forward read or wrote them.  Returns (dy bf16, dres, dw_post, dgate,
     dw_pre), the last three float32 shaped like the weights (None where the weight is None)."""
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post, gate, w_pre, res_scale, post_norm, workspace)
     bf16, f32 = torch.bfloat16, torch.float32
     T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res_out, w_post, gate, w_pre, post_norm)
     pn, py, pr = _need(dn, bf16, (T, H), "dn"), _need(y, bf16, (T, H), "y"), _need(res_out, rt, (T, H), "res_out")
@@ -729,7 +742,7 @@ def residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post=None, gate=None, w
     st = lib().residual_norm_bwd(pn, pd, py, pr, _need(stats, f32, (2, T), "stats"), pa, pg, pb, T, H, code, kind,
                                  1 if post_norm else 0, res_scale, dy.data_ptr(), dres.data_ptr(), _ptr(dw_post),
                                  _ptr(dgate), _ptr(dw_pre), _need(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
-                                 _stream_of(y, stream))
+                                 _stream_of(y))
     if st != OK:
         raise MXFP8Error(st, "residual_norm_bwd")
     return dy, dres, dw_post, dgate, dw_pre

@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
       const uint64_t desc_a = sdesc_kmajor_sw128(smem_u32(smem)), desc_b = sdesc_kmajor_sw128(smem_u32(smem + L.b));
       const uint64_t desc_sfa = sdesc_sf_atom(smem_u32(smem + L.sfa));
       bool ok = true, any = false;
+      pdl_wait();   // the columns come after it anyway: the limits of the waits start here
       Ring r{0, 0};
       int i = 0, set = 0;
       Place q = first;

@@ -280,3 +280,52 @@ def test_experts_shared_by_several_ctas(mx, fmt, T, k, E, H, F):
     ref, bound = D.moe_ref(fmt, x, ids, gates, v1, v2, E, H, F)
     D.check(y, ref, bound)
     assert all((D.moe(mx, fmt, x, ids, gates, w1, w2) == y).all() for _ in range(3))
+
+
+@FORMATS
+def test_weights_past_four_gigabytes(mx, fmt):
+    """The last expert of a layer of more than 2^32 weight bytes gives, bit for bit, what it gives alone."""
+    import torch
+    E, H, F = (40, 4096, 14336) if fmt == "mxfp8" else (80, 4096, 14336)
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def rnd(M, K):
+        q = torch.randint(0, 120, (M, K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+        n = mx.mxfp8_sf_bytes(M, K, mx.ROWWISE, mx.SF_MMA) if fmt == "mxfp8" else mx.nvfp4_sf_bytes(M, K, mx.SF_MMA)
+        sf = torch.randint(*((110, 118) if fmt == "mxfp8" else (0x20, 0x30)), (n,), dtype=torch.uint8, device="cuda",
+                           generator=gen)
+        return (q, sf) if fmt == "mxfp8" else (q, sf, torch.full((1,), 0.125, device="cuda"))
+
+    def last(w):   # of E equal shares
+        return tuple(t if t.numel() == 1 else t[t.shape[0] // E * (E - 1):] for t in w)
+    w1, w2 = rnd(E * 2 * F, H), rnd(E * H, F)
+    assert w1[0].numel() > 2 ** 32
+    x = D.activations(2, H, seed=2)
+    ids, alone = (torch.full((2, 1), e, dtype=torch.int32, device="cuda") for e in (E - 1, 0))
+    y = D.moe(mx, fmt, x, ids, None, w1, w2)
+    assert torch.isfinite(y.float()).all() and y.any()
+    assert torch.equal(y.view(torch.int16), D.moe(mx, fmt, x, alone, None, last(w1), last(w2)).view(torch.int16))
+
+
+@FORMATS
+def test_a_stream_of_its_own(mx, fmt):
+    """stream=: the kernels run there, and what the call allocates belongs to that stream."""
+    import torch
+    w, _ = D.weight(mx, fmt, 256, 512, seed=1)
+    x = D.activations(3, 512, seed=2)
+    r, v = torch.randn_like(x), torch.ones(512, device="cuda")
+    y, (ro, n, st) = D.matvec(mx, fmt, x, w), mx.residual_norm_fwd(x, r, w_pre=v)
+    grads = mx.residual_norm_bwd(n, None, x, ro, st, w_pre=v)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                       # the current stream is busy
+    z = D.matvec(mx, fmt, x, w, stream=side)
+    out = mx.residual_norm_fwd(x, r, w_pre=v, stream=side)
+    more = mx.residual_norm_bwd(n, None, x, ro, st, w_pre=v, stream=side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query(), "ran on the current stream"
+    torch.cuda.synchronize()
+    for a, b in zip((y, ro, n, st, *grads), (z, *out, *more)):
+        assert (a is None and b is None) or torch.equal(a, b)
