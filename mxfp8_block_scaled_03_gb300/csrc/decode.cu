@@ -577,38 +577,54 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
 
   if (warp == 0) {
     // ---------------- copies (one lane) ----------------
-    int issued = 0;
     if (elect_one()) {
       const uint64_t policy = evict_first();
-      auto copy_weights = [&](const Place& q, int slot) {
-        int row = q.tile * 128;
-        if constexpr (MOE) row += (s_act_e[q.a] * ACCS + q.acc) * (p.tiles * 128);
-        mbar_arrive_expect_tx(&full[slot], DEC_A_STAGE + ATOMS * 512 + p.box_rows * P * 128);
-        tma_load_weights(smem + slot * DEC_A_STAGE, &tm_w, &full[slot], q.f * 128, row, policy);
-        bulk_load_weights(smem + L.sfa + slot * ATOMS * 512,
-                          p.w_sf + (static_cast<int64_t>(row >> 7) * p.kt + q.f * ATOMS) * 512, ATOMS * 512,
-                          &full[slot], policy);
-      };
-      // the unit's columns and whatever follows them: a box has a fixed height
-      auto copy_columns = [&](const Place& q, int slot) {
-        tma_load_2d(smem + L.b + slot * L.b_stage, &tm_x, &full[slot], q.f * 128, first_row(q.a) * P);
-      };
-      // fill the ring with weights before waiting for the activations the previous kernel writes
+      // of the unit at hand: its first weight row and scale atoms per accumulator, and its first column
+      int unit_a = -1, unit_tile = -1, row[ACCS], column = 0;
+      const uint8_t* sf[ACCS];
+      // First the ring is filled with weights, before waiting for the activations the previous kernel writes; then
+      // come those stages' columns, and all that is left.
       const int fill = min(n_steps, L.stages);
-      Place q = first, w = q;
-      for (int i = 0; i < fill; advance(w, i), ++i) copy_weights(w, i);
-      pdl_wait();
-      for (; issued < fill; advance(q, issued), ++issued) copy_columns(q, issued);
+      int issued = 0;
       Ring r{0, 0};
-      for (; issued < n_steps; advance(q, issued), ++issued, next_stage(r)) {
-        if (!dec_wait(&empty[r.slot], r.phase, abort_flag, p, ERR_TIMEOUT_PRODUCER)) break;
-        copy_weights(q, r.slot);
-        copy_columns(q, r.slot);
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass == 1) pdl_wait();
+        const int end = pass == 0 ? fill : n_steps;
+        Place q = first;
+        r = Ring{0, 0};
+#pragma unroll 1
+        for (issued = 0; issued < end; advance(q, issued), ++issued, next_stage(r)) {
+          const bool refill = issued >= fill;
+          if (refill && !dec_wait(&empty[r.slot], r.phase ^ 1u, abort_flag, p, ERR_TIMEOUT_PRODUCER)) break;
+          if (q.tile != unit_tile || q.a != unit_a) {
+            unit_a = q.a;
+            unit_tile = q.tile;
+            column = first_row(q.a) * P;
+#pragma unroll
+            for (int c = 0; c < ACCS; ++c) {
+              row[c] = q.tile * 128;
+              if constexpr (MOE) row[c] += (s_act_e[q.a] * ACCS + c) * (p.tiles * 128);
+              sf[c] = p.w_sf + static_cast<int64_t>(row[c] >> 7) * p.kt * 512;
+            }
+          }
+          const bool up = UP && q.acc != 0;
+          if (pass == 0 || refill) {
+            mbar_arrive_expect_tx(&full[r.slot], DEC_A_STAGE + ATOMS * 512 + p.box_rows * P * 128);
+            tma_load_weights(smem + r.slot * DEC_A_STAGE, &tm_w, &full[r.slot], q.f * 128, up ? row[ACCS - 1] : row[0],
+                             policy);
+            bulk_load_weights(smem + L.sfa + r.slot * ATOMS * 512, (up ? sf[ACCS - 1] : sf[0]) + q.f * ATOMS * 512,
+                              ATOMS * 512, &full[r.slot], policy);
+          }
+          // the unit's columns and whatever follows them: a box has a fixed height
+          if (pass == 1) tma_load_2d(smem + L.b + r.slot * L.b_stage, &tm_x, &full[r.slot], q.f * 128, column);
+        }
       }
       // every copy must have landed before the CTA may exit; after a timeout elsewhere the barriers may lack
       // their other arrival, and one full drain wait is enough for all the copies
-      for (int i = max(0, issued - L.stages); i < issued; ++i)
-        if (!mbar_wait_bounded(&full[i % L.stages], (i / L.stages) & 1, nullptr, p.drain_ns)) {
+      Ring e = issued < L.stages ? Ring{0, 0} : Ring{r.slot, r.phase ^ 1u};
+      for (int z = min(issued, L.stages); z > 0; --z, next_stage(e))
+        if (!mbar_wait_bounded(&full[e.slot], e.phase, nullptr, p.drain_ns)) {
           atomicOr(p.err, ERR_TIMEOUT_DRAIN);
           break;
         }
