@@ -31,20 +31,20 @@
 //   k_decode<LINEAR> units: 128 rows of W
 // The kernels are launched programmatically dependent: a kernel's weight copies start while the one
 // before it runs, and only what reads its results waits.  Weights are copied evict-first, so that everything
-// else stays in L2 (NVFP4, 64 experts 2048x1408, 64 tokens: 69 us, 77 without).
-// Two CTAs share an SM.  A CTA is bound by its own instructions, 0.2-0.45 us a K step of 16 KB (the MMA thread,
-// and the two warps that turn exponents into scales), an SM draws a step from memory in 0.35 us, and a kernel's
-// first and last microseconds have one CTA's latencies: one CTA per SM with twice the stages measured the
-// same to 3% for 1 to 16 tokens, but 170 us against 142 (MoE, NVFP4, 8 experts 4096x14336, 64 tokens) and 34
-// against 27 (linear, MXFP8, 61x4096->28672).
+// else stays in L2 (NVFP4, 64 experts 2048x1408, 64 tokens: 68 us, 74 without).
+// Two CTAs share an SM.  A CTA is bound by its own instructions, 0.2-0.4 us a K step of 16 KB (the MMA thread,
+// and the warps that turn exponents into scales), an SM draws a step from memory in 0.35 us, and a kernel's
+// first and last microseconds have one CTA's latencies.  One CTA per SM with twice the stages: 165 us against 142
+// (MoE, NVFP4, 8 experts 4096x14336, 64 tokens), 33 against 27.5 (linear, MXFP8, 61x4096->28672), within 3%
+// for 1 to 16 tokens (dec_layout says where it is used all the same).
 // Measured (replayed graph, every call on other weights; share of the 6.77 TB/s a copy reaches):
-//   MoE 8 experts 4096x14336, k 2    MXFP8  1 token 66.7 us (81%), 16 226 (95%), 64 235 (91%)
-//                                    NVFP4  1 token 42.0 us (70%), 16 130 (90%), 64 142 (82%)
-//   MoE 64 experts 2048x1408, k 8    MXFP8  1 token 24.6 us (43%), 8 68.3 (82%), 64 104.5 (81%)
-//                                    NVFP4  1 token 20.3 us (28%), 8 45.7 (67%), 64 69.3 (66%)
-//   linear 4096->28672               MXFP8  1 token 22.6 us (79%), 61 27.0 (68%)
-//                                    NVFP4  1 token 15.0 us (65%), 61 26.0 (40%)
-//   linear 1x4096->4096              MXFP8  9.0 us, NVFP4 8.2: launch, columns, first weights, parts, one after the other
+//   MoE 8 experts 4096x14336, k 2    MXFP8  1 token 67.0 us (80%), 16 224 (96%), 64 230 (94%)
+//                                    NVFP4  1 token 42.3 us (69%), 16 129 (91%), 64 142 (82%)
+//   MoE 64 experts 2048x1408, k 8    MXFP8  1 token 24.4 us (43%), 8 66.7 (84%), 64 101.9 (83%)
+//                                    NVFP4  1 token 19.5 us (29%), 8 45.0 (68%), 64 68.4 (67%)
+//   linear 4096->28672               MXFP8  1 token 22.6 us (79%), 61 27.3 (68%)
+//                                    NVFP4  1 token 14.7 us (66%), 61 21.5 (48%)
+//   linear 1x4096->4096              MXFP8  9.0 us, NVFP4 8.0: launch, columns, first weights, parts, in a row
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -66,8 +66,8 @@ constexpr int DEC_MAX_TOKENS = 64;           // tokens of one call
 constexpr int DEC_MAX_K = 32;                // choices per token
 constexpr int DEC_MAX_STAGES = 12;
 // K values that make a CTA worth having in a shared unit: 4 steps of NVFP4, 8 of MXFP8.  Measured, 1x4096->4096 and one
-// token on 64 experts 2048x1408: NVFP4 8.2 and 20.3 us (half: 8.5, 21.3; twice: 8.9, 21.1), MXFP8 9.0 and 24.6 us
-// (half: 9.3, 25.9).
+// token on 64 experts 2048x1408: NVFP4 8.0 and 19.5 us (half: 8.8, 20.9; twice: 8.4, 20.2), MXFP8 9.0 and 24.4 us
+// (half: 9.7, 25.8; twice: 10.1, 25.4).
 constexpr int DEC_MIN_VALUES = 1024;
 // Half of 228 KB less the 1 KB the system keeps per CTA, so that a kernel's CTAs fit beside those of the
 // kernel before it; the whole SM where that leaves fewer than three stages.
@@ -81,7 +81,8 @@ enum DecMode { DEC_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
 enum DecFmt { DEC_MX = 0, DEC_NV = 1 };
 
 // Warp 0 copies, warp 1 issues MMAs, then come the warps that write the columns' scales (they take turns), and four
-// for the epilogue.
+// for the epilogue.  Linears have three for the scales (NVFP4, 61x4096->28672: 21.5 us, 25.5 with two; elsewhere the
+// same); UP needs an even number, and its registers leave room for two.
 constexpr int dec_scale_warps(int mode) { return mode == DEC_LINEAR ? 3 : 2; }
 constexpr int dec_threads(int mode) { return 32 * (2 + dec_scale_warps(mode) + 4); }
 
@@ -90,12 +91,10 @@ constexpr int dec_pieces(int fmt, int mode) { return fmt == DEC_NV ? 5 : mode ==
 constexpr int dec_step_values(int fmt) { return fmt == DEC_NV ? 256 : 128; }
 constexpr int dec_atoms(int fmt) { return fmt == DEC_NV ? 4 : 1; }          // scale atoms per 128 rows and step
 constexpr int dec_exp_bytes(int fmt) { return fmt == DEC_NV ? 16 : 4; }     // blocks of one row and step
-// Most rows of a unit.  LINEAR: one accumulator of at most 128 (MXFP8) or 160 (NVFP4) columns; more tokens come
-// in two chunks (MXFP8, 61x4096->28672: 28.7 us in one, 30.6 in two).  MoE: two accumulators of at most 80 (an
-// expert with more tokens gives several units).  Units of the same weights read them side by side, from L2.
-constexpr int dec_group(int fmt, int mode) {
-  return fmt == DEC_NV ? (mode == DEC_LINEAR ? 32 : 16) : (mode == DEC_LINEAR ? 64 : 32);
-}
+// Most rows of a unit.  LINEAR: one accumulator of at most 64 (MXFP8) or 160 (NVFP4) columns; more tokens come in two
+// chunks (one chunk of 64 measured the same with MXFP8).  MoE: two accumulators of at most 80 (an expert with more
+// tokens gives several units).  Units of the same weights read them side by side, from L2.
+constexpr int dec_group(int fmt, int mode) { return fmt == DEC_NV && mode != DEC_LINEAR ? 16 : 32; }
 
 // Shared memory of one CTA (byte offsets from a 1024-byte boundary); the weight ring is at 0.
 struct DecLayout {
@@ -441,7 +440,8 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
   constexpr bool UP = MODE == DEC_UP, MOE = MODE != DEC_LINEAR;
   constexpr int ACCS = UP ? 2 : 1, MIN_STEPS = DEC_MIN_VALUES / dec_step_values(FMT);
   constexpr int THREADS = dec_threads(MODE), SCALE_WARPS = dec_scale_warps(MODE), FIRST_EPI_WARP = 2 + SCALE_WARPS;
-  constexpr int GROUP = dec_group(FMT, MODE), ROWS = (GROUP + 31) / 32;   // ROWS: of a unit, per lane of a warp
+  constexpr int GROUP = dec_group(FMT, MODE);
+  static_assert(GROUP <= 32, "a lane per row");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const DecLayout& L = p.L;
@@ -692,13 +692,12 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
     // The set (and the stage) must have been read by step i - sf_sets.  Fewer warps than stages: when a warp
     // waits for that step, the use of its stage before it is known to be over, as a wait by parity requires.
     const int cw = warp - 2;
-    // MXFP8 (ROWS rows a lane), and NVFP4 with more than eight rows: lane = row, all its words; NVFP4 with up
-    // to eight: lane = (word, row), one of the row's four words.
-    static_assert(FMT == DEC_MX || ROWS == 1, "one row a lane");
+    // MXFP8, and NVFP4 with more than eight rows: lane = row, all its words; NVFP4 with up to eight:
+    // lane = (word, row), one of the row's four words.
     // One warp does all of a step, so the code between two steps is kept short, and nothing touches a loaded value
     // before the step it is for.
     struct Scales {
-      uint32_t e[ATOMS * ROWS];
+      uint32_t e[ATOMS];
       int c, top, n, nat, f;   // row of the unit (lanes past the last: none) and its reference, rows, atoms per MMA
       bool spread;
     };
@@ -726,12 +725,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
           v.e[0] = w.x; v.e[1] = w.y; v.e[2] = w.z; v.e[3] = w.w;
         }
       } else {
-#pragma unroll
-        for (int z = 0; z < ROWS; ++z)
-          if (z * 32 < v.n) {
-            const int more = min(v.c + z * 32, v.n - 1) - min(v.c, v.n - 1);
-            v.e[z] = *reinterpret_cast<const uint32_t*>(at + static_cast<int64_t>(more) * p.steps * EB);
-          }
+        v.e[0] = *reinterpret_cast<const uint32_t*>(at);
       }
     };
     // place of a column's word of the first atom, from the start of the step's scales
@@ -758,7 +752,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
         }
         load(q, next);
       }
-      uint32_t w[ATOMS * ROWS];
+      uint32_t w[ATOMS];
       if constexpr (FMT == DEC_NV) {
         // words past the row's end count as zeros
         w[0] = nv_scales((cur.f * 4 + (cur.spread ? lane >> 3 : 0)) * 64 < p.K ? cur.e[0] : 0u, cur.top);
@@ -766,8 +760,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
 #pragma unroll
           for (int m = 1; m < 4; ++m) w[m] = nv_scales((cur.f * 4 + m) * 64 < p.K ? cur.e[m] : 0u, cur.top);
       } else {
-#pragma unroll
-        for (int z = 0; z < ROWS; ++z) w[z] = cur.e[z];
+        w[0] = cur.e[0];
       }
       if (i >= L.sf_sets) {
         if (!dec_warp_wait(&empty[read.slot], read.phase, abort_flag, p, ERR_TIMEOUT_SF, lane)) break;
@@ -777,14 +770,12 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
         read = Ring{i + SCALE_WARPS - L.sf_sets, 0};   // of the next step of this warp
       }
       uint8_t* sf = smem + L.sfb + slot * L.sfb_stage;
-#pragma unroll
-      for (int z = 0; z < ROWS; ++z) {
-        if (cur.c + z * 32 >= cur.n) break;
+      if (cur.c < cur.n) {
 #pragma unroll
         for (int d = 0; d < P; ++d) {
-          uint8_t* dst = sf + word((cur.c + z * 32) * P + d);
+          uint8_t* dst = sf + word(cur.c * P + d);
           if constexpr (FMT == DEC_MX) {
-            *reinterpret_cast<uint32_t*>(dst) = mx_scales(w[z], d);
+            *reinterpret_cast<uint32_t*>(dst) = mx_scales(w[0], d);
           } else if (cur.spread) {
             *reinterpret_cast<uint32_t*>(dst + (lane >> 3) * 512) = w[0];
           } else {
@@ -1068,8 +1059,10 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
 
 constexpr int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
-// Shared memory for units of `rows` activation rows: half an SM with at least three stages, else a whole one.
-bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* out) {
+// Shared memory for units of `rows` activation rows: half an SM where that holds three stages, else a whole one.
+// MXFP8 experts with units for all CTAs take a whole one too (`many`): 64 experts 2048x1408, 64 tokens 101 us against
+// 104, 8 experts 4096x14336, 64 tokens 231 against 235.  Elsewhere two CTAs are better, as said at the top.
+bool dec_layout(int fmt, int mode, int rows, int E, int max_active, bool many, DecLayout* out) {
   const int n = round_up(dec_pieces(fmt, mode) * rows, 16);
   DecLayout L{};
   L.b_stage = n * 128;
@@ -1080,11 +1073,11 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
   const int fixed = 1024 + bars + (mode == DEC_LINEAR ? 0 : round_up(E * 8 + max_active * 12, 16));
   const int stage = DEC_A_STAGE + sfa + L.b_stage + L.sfb_stage;
   L.smem = DEC_SMEM_HALF;
-  if ((L.smem - fixed) / stage < 3) L.smem = DEC_SMEM_FULL;
+  if ((L.smem - fixed) / stage < 3 || (fmt == DEC_MX && many)) L.smem = DEC_SMEM_FULL;
   L.stages = std::min(DEC_MAX_STAGES, (L.smem - fixed) / stage);
   L.tmem_cols = L.smem == DEC_SMEM_HALF ? DEC_TMEM_HALF : DEC_TMEM_FULL;
   // Two buffers of accumulators, where that leaves three sets of scales: the next unit's MMAs start while one is read
-  // (NVFP4, 61x4096->28672: 26.0 us with, 28.1 without; fewer sets would hold up every step instead).
+  // (NVFP4, 61x4096->28672: 21.5 us with, 24.8 without; fewer sets would hold up every step instead).
   for (L.acc_two = 1; L.acc_two >= 0; --L.acc_two) {
     L.sf_col = (mode == DEC_UP ? 2 : 1) * n << L.acc_two;
     L.sf_sets = std::min(L.stages, (static_cast<int>(L.tmem_cols) - L.sf_col) / L.sf_cols);
@@ -1102,8 +1095,7 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, DecLayout* o
 }
 static_assert(2 * DEC_MAX_STAGES * 8 + 8 * 8 + 16 <= 384, "barriers and flags");
 static_assert(dec_group(DEC_MX, DEC_DOWN) * 3 <= 160 && dec_group(DEC_MX, DEC_UP) * 2 * 2 <= 160 &&
-                  dec_group(DEC_NV, DEC_UP) * 5 * 2 <= 160 && dec_group(DEC_NV, DEC_LINEAR) * 5 <= 160 &&
-                  dec_group(DEC_MX, DEC_LINEAR) * 2 <= 128,
+                  dec_group(DEC_NV, DEC_UP) * 5 * 2 <= 160 && dec_group(DEC_NV, DEC_LINEAR) * 5 <= 160,
               "accumulators");
 
 // Per-device set-up of one kernel instance (dynamic shared memory, and the carve-out that lets two CTAs
@@ -1306,8 +1298,8 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
   down.steps = up.h_steps;
   down.kt = down.steps * dec_atoms(FMT);
   down.tiles = static_cast<int>(H / 128);
-  if (!dec_layout(FMT, DEC_UP, group, E, ws.max_active, &up.L) ||
-      !dec_layout(FMT, DEC_DOWN, group, E, ws.max_active, &down.L))
+  if (!dec_layout(FMT, DEC_UP, group, E, ws.max_active, act * up.tiles >= 2 * sms, &up.L) ||
+      !dec_layout(FMT, DEC_DOWN, group, E, ws.max_active, act * down.tiles >= 2 * sms, &down.L))
     return MXFP8_ERR_UNSUPPORTED;
 
   SplitParams q{};
@@ -1381,7 +1373,7 @@ int matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, c
   p.tiles = static_cast<int>(N / 128);
   p.timeout_ns = dec_wait_ns();
   p.drain_ns = kDecWaitNs;
-  if (!dec_layout(FMT, DEC_LINEAR, p.per_chunk, 0, 0, &p.L)) return MXFP8_ERR_UNSUPPORTED;
+  if (!dec_layout(FMT, DEC_LINEAR, p.per_chunk, 0, 0, false, &p.L)) return MXFP8_ERR_UNSUPPORTED;
   SplitParams q{};
   q.x = static_cast<const uint16_t*>(x);
   q.o = p.in;
