@@ -602,7 +602,9 @@ def _moe_decode(name, nv, x, experts, gates, w1, w2, out, workspace, stream):
     p2, s2 = _need(w2[0], u8, (E * H, F // per), "W2 codes"), _need(w2[1], u8, _sf_mma_bytes(nv, E * H, F), "W2 scales")
     if out is None:
         out = torch.empty((T, H), dtype=bf16, device=x.device)
-    po = _need(out, bf16, (T, H), "out")
+        po = out.data_ptr()
+    else:
+        po = _need(out, bf16, (T, H), "out")
     if workspace is None:
         workspace = torch.empty(max(256, moe_decode_workspace_size(T, k, H, F, E)), dtype=u8, device=x.device)
     pw = _need(workspace, u8, 256, "workspace")
@@ -650,7 +652,9 @@ def _matvec(name, nv, x, w, out, workspace, stream):
     pq, ps = _need(w[0], u8, (N, K // 2 if nv else K), "codes"), _need(w[1], u8, _sf_mma_bytes(nv, N, K), "scales")
     if out is None:
         out = torch.empty((T, N), dtype=bf16, device=x.device)
-    po = _need(out, bf16, (T, N), "out")
+        po = out.data_ptr()
+    else:
+        po = _need(out, bf16, (T, N), "out")
     if workspace is None:
         workspace = torch.empty(max(256, matvec_workspace_size(T, K)), dtype=u8, device=x.device)
     pw = _need(workspace, u8, 256, "workspace")
@@ -708,13 +712,17 @@ def residual_norm_fwd(y, res, w_post=None, gate=None, w_pre=None, res_scale: flo
     T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res, w_post, gate, w_pre, post_norm)
     py, pr = _need(y, bf16, (T, H), "y"), _need(res, rt, (T, H), "res")
     if out is None:
-        out = (torch.empty_like(res), torch.empty_like(y), torch.empty((2, T), dtype=torch.float32, device=y.device))
-    st = lib().residual_norm_fwd(py, pr, pa, pg, pb, T, H, code, kind, 1 if post_norm else 0, res_scale, eps,
-                                 _need(out[0], rt, (T, H), "res_out"), _need(out[1], bf16, (T, H), "n"),
-                                 _need(out[2], torch.float32, (2, T), "stats"), _stream_of(y))
+        res_out, n, stats = torch.empty_like(res), torch.empty_like(y), torch.empty((2, T), dtype=torch.float32, device=y.device)
+        po, pn, ps = res_out.data_ptr(), n.data_ptr(), stats.data_ptr()
+    else:
+        res_out, n, stats = out
+        po, pn = _need(res_out, rt, (T, H), "res_out"), _need(n, bf16, (T, H), "n")
+        ps = _need(stats, torch.float32, (2, T), "stats")
+    st = lib().residual_norm_fwd(py, pr, pa, pg, pb, T, H, code, kind, 1 if post_norm else 0, res_scale, eps, po, pn, ps,
+                                 _stream_of(y))
     if st != OK:
         raise MXFP8Error(st, "residual_norm_fwd")
-    return tuple(out)
+    return res_out, n, stats
 
 
 def residual_norm_bwd_workspace_size(T: int, H: int) -> int:
