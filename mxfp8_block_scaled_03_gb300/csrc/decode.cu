@@ -869,36 +869,40 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
           }
         }
         release();
-        // whoever is last adds the parts up, in order
+        // Whoever is last adds the parts up, in order.  Eight lanes take the warp's 32 weight rows of an activation row,
+        // four at a time, with eight parts on their way: this is a chain of trips to the L2.
         if (share && last_part()) {
-          constexpr int TB = 4, OB = 2;   // 4 rows x 2 parts of loads in flight
+          constexpr int OB = 8;
+          const int r4 = quarter * 32 + (lane & 7) * 4;
 #pragma unroll 1
-          for (int c0 = 0; c0 < n; c0 += TB) {
-            float sum[TB] = {};
+          for (int c = lane >> 3; c < n; c += 4) {
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
             for (int o0 = 0; o0 < parts; o0 += OB) {
-              float x[OB][TB];
-#pragma unroll
-              for (int o = 0; o < OB; ++o) {
-                const float* src = part_of(min(o0 + o, parts - 1)) + row;
-#pragma unroll
-                for (int j = 0; j < TB; ++j)
-                  x[o][j] = o0 + o < parts && c0 + j < n ? __ldcg(src + (c0 + j) * 128) : 0.0f;
-              }
+              float4 x[OB];
 #pragma unroll
               for (int o = 0; o < OB; ++o)
+                x[o] = o0 + o < parts ? __ldcg(reinterpret_cast<const float4*>(part_of(o0 + o) + c * 128 + r4))
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                for (int j = 0; j < TB; ++j) sum[j] += x[o][j];
+              for (int o = 0; o < OB; ++o) {
+                sum.x += x[o].x;
+                sum.y += x[o].y;
+                sum.z += x[o].z;
+                sum.w += x[o].w;
+              }
             }
-#pragma unroll
-            for (int j = 0; j < TB; ++j)
-              if (c0 + j < n) put(c0 + j, sum[j]);
+            const int64_t at = static_cast<int64_t>(row0 + c) * (p.tiles * 128) + tile * 128 + r4;
+            if constexpr (MODE == DEC_DOWN)
+              *reinterpret_cast<float4*>(p.y + at) = sum;
+            else
+              *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
           }
         }
       } else {
-        // h from the gate and up sums, as columns of DOWN.  A lane has one weight row; four lanes transpose their
-        // values of four activation rows, and each converts four values of one of them (a block is 16 or 32 lanes
-        // wide).  (Passing the sums of whole units through memory as well, to free the accumulators earlier, measured
+        // h from the gate and up sums, as columns of DOWN.  In the accumulators a lane has one weight row; four lanes
+        // transpose their values of four activation rows, and each converts four values of one of them (a block is 16
+        // or 32 lanes wide).  (Passing the sums of whole units through memory as well, to free the accumulators earlier, measured
         // the same.)  Short straight code: its first pass is fetched line by line behind the weights' stream.
         constexpr int PH = dec_pieces(FMT, DEC_DOWN), LD = (4 * P + 7) / 8;
         const bool has[2] = {r1 - r0 > 1 || (r0 & 1) == 0, r1 - r0 > 1 || (r0 & 1) == 1};
@@ -924,46 +928,51 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
 #pragma unroll
                 for (int b = 0; b < 2; ++b) v[b][j] = has[b] ? sum_pieces<FMT, P>(d[b] + j * P) * scale : 0.0f;
               }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[0][j] = v[1][j] = 0.0f;
-#pragma unroll 2
-              for (int o = 0; o < parts; ++o) {
-                const float* src = part_of(o) + row;
+              if (phase == 0) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) v[b][j] += __ldcg(src + (b * n + min(c0 + j, n - 1)) * 128);
+                  for (int j = 0; j < 4; ++j)
+                    if (c0 + j < n) mine[(b * n + c0 + j) * 128] = v[b][j];
+                continue;
               }
-            }
-            if (phase == 0) {
+              // lane l of four keeps row c0 + l, values k0 .. k0 + 3
 #pragma unroll
-              for (int b = 0; b < 2; ++b)
+              for (int z = 1; z < 4; z *= 2) {
+                const bool up = (lane & z) != 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (c0 + j < n) mine[(b * n + c0 + j) * 128] = v[b][j];
-              continue;
-            }
-            float h[4];
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              h[j] = __shfl_sync(0xFFFFFFFFu, gates, (c0 + j) & 31) * __fdividef(v[0][j], 1.0f + expf(-v[0][j])) *
-                     v[1][j];
-            // transpose: lane l of four keeps row c0 + l, values k0 .. k0 + 3
+                  for (int j = 0; j < 4; ++j)
+                    if ((j & z) == 0) {
+                      const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[b][j] : v[b][j | z], z);
+                      v[b][j] = up ? other : v[b][j];
+                      v[b][j | z] = up ? v[b][j | z] : other;
+                    }
+              }
+            } else {   // the parts, in order
 #pragma unroll
-            for (int z = 1; z < 4; z *= 2) {
-              const bool up = (lane & z) != 0;
+              for (int j = 0; j < 4; ++j) v[0][j] = v[1][j] = 0.0f;
+#pragma unroll 4
+              for (int o = 0; o < parts; ++o) {
+                const float* src = part_of(o) + min(c0 + (lane & 3), n - 1) * 128 + quarter * 32 + (lane & ~3);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if ((j & z) == 0) {
-                  const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? h[j] : h[j | z], z);
-                  h[j] = up ? other : h[j];
-                  h[j | z] = up ? h[j | z] : other;
+                for (int b = 0; b < 2; ++b) {
+                  const float4 x = __ldcg(reinterpret_cast<const float4*>(src + b * n * 128));
+                  v[b][0] += x.x;
+                  v[b][1] += x.y;
+                  v[b][2] += x.z;
+                  v[b][3] += x.w;
                 }
+              }
             }
             const int c = c0 + (lane & 3);
             const bool live = c < n;
             const int64_t hr = row0 + min(c, n - 1);
+            const float gate = __shfl_sync(0xFFFFFFFFu, gates, c & 31);
+            float h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = gate * __fdividef(v[0][j], 1.0f + expf(-v[0][j])) * v[1][j];
             uint32_t m = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);
