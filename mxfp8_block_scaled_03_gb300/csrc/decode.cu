@@ -69,6 +69,9 @@ constexpr int DEC_MAX_STAGES = 12;
 // token on 64 experts 2048x1408: NVFP4 8.0 and 19.5 us (half: 8.8, 20.9; twice: 8.4, 20.2), MXFP8 9.0 and 24.4 us
 // (half: 9.7, 25.8; twice: 10.1, 25.4).
 constexpr int DEC_MIN_VALUES = 1024;
+// Most CTAs of a shared unit: their parts are read in one go (linear 3x14336->4096, MXFP8: 15.1 us, with 9 parts 15.3;
+// 19x11136->2304: 13.4 and 14.6; the other way 1x14336->1024, whose K would do for 14: 9.8 and 9.0).
+constexpr int DEC_MAX_PARTS = 8;
 // Half of 228 KB less the 1 KB the system keeps per CTA, so that a kernel's CTAs fit beside those of the
 // kernel before it; the whole SM where that leaves fewer than three stages.
 constexpr int DEC_SMEM_HALF = 113 * 1024, DEC_SMEM_FULL = 226 * 1024;
@@ -530,7 +533,8 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
   // left-over steps out evenly, with two parts of units in a CTA, measured 5-15% slower: more sums of parts.)
   const int slots = static_cast<int>(gridDim.x) / p.chunks, cta = static_cast<int>(blockIdx.x) / p.chunks;
   const int whole = units / slots, shared = units - whole * slots;
-  const int per_unit = shared == 0 ? 1 : max(1, min(slots / shared, su / MIN_STEPS));   // CTAs of a shared unit
+  // CTAs of a shared unit
+  const int per_unit = shared == 0 ? 1 : max(1, min(DEC_MAX_PARTS, min(slots / shared, su / MIN_STEPS)));
   // Place in the sequence: list entry, 128-row tile, K step, accumulator.  Divisions only here.
   struct Place {
     int a, tile, f, acc;
@@ -870,27 +874,22 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
         }
         release();
         // Whoever is last adds the parts up, in order.  Eight lanes take the warp's 32 weight rows of an activation row,
-        // four at a time, with eight parts on their way: this is a chain of trips to the L2.
+        // four at a time, with all parts on their way: this is a chain of trips to the L2.
         if (share && last_part()) {
-          constexpr int OB = 8;
           const int r4 = quarter * 32 + (lane & 7) * 4;
 #pragma unroll 1
           for (int c = lane >> 3; c < n; c += 4) {
-            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-            for (int o0 = 0; o0 < parts; o0 += OB) {
-              float4 x[OB];
+            float4 x[DEC_MAX_PARTS], sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-              for (int o = 0; o < OB; ++o)
-                x[o] = o0 + o < parts ? __ldcg(reinterpret_cast<const float4*>(part_of(o0 + o) + c * 128 + r4))
-                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int o = 0; o < DEC_MAX_PARTS; ++o)
+              x[o] = o < parts ? __ldcg(reinterpret_cast<const float4*>(part_of(o) + c * 128 + r4))
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-              for (int o = 0; o < OB; ++o) {
-                sum.x += x[o].x;
-                sum.y += x[o].y;
-                sum.z += x[o].z;
-                sum.w += x[o].w;
-              }
+            for (int o = 0; o < DEC_MAX_PARTS; ++o) {
+              sum.x += x[o].x;
+              sum.y += x[o].y;
+              sum.z += x[o].z;
+              sum.w += x[o].w;
             }
             const int64_t at = static_cast<int64_t>(row0 + c) * (p.tiles * 128) + tile * 128 + r4;
             if constexpr (MODE == DEC_DOWN)
