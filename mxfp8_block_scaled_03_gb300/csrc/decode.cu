@@ -38,13 +38,13 @@
 // (MoE, NVFP4, 8 experts 4096x14336, 64 tokens), 33 against 27.5 (linear, MXFP8, 61x4096->28672), within 3%
 // for 1 to 16 tokens (dec_layout says where it is used all the same).
 // Measured (replayed graph, every call on other weights; share of the 6.77 TB/s a copy reaches):
-//   MoE 8 experts 4096x14336, k 2    MXFP8  1 token 67.0 us (80%), 16 224 (96%), 64 230 (94%)
-//                                    NVFP4  1 token 42.3 us (69%), 16 129 (91%), 64 142 (82%)
-//   MoE 64 experts 2048x1408, k 8    MXFP8  1 token 24.4 us (43%), 8 66.7 (84%), 64 101.9 (83%)
-//                                    NVFP4  1 token 19.5 us (29%), 8 45.0 (68%), 64 68.4 (67%)
-//   linear 4096->28672               MXFP8  1 token 22.6 us (79%), 61 27.3 (68%)
-//                                    NVFP4  1 token 14.7 us (66%), 61 21.5 (48%)
-//   linear 1x4096->4096              MXFP8  9.0 us, NVFP4 8.0: launch, columns, first weights, parts, in a row
+//   MoE 8 experts 4096x14336, k 2    MXFP8  1 token 66.5 us (81%), 16 224 (96%), 64 229 (94%)
+//                                    NVFP4  1 token 42.1 us (70%), 16 129 (91%), 64 142 (82%)
+//   MoE 64 experts 2048x1408, k 8    MXFP8  1 token 24.1 us (44%), 8 66.5 (84%), 64 101.5 (83%)
+//                                    NVFP4  1 token 19.6 us (29%), 8 45.0 (68%), 64 68.0 (68%)
+//   linear 4096->28672               MXFP8  1 token 22.6 us (79%), 61 27.1 (68%)
+//                                    NVFP4  1 token 14.6 us (67%), 61 21.6 (48%)
+//   linear 1x4096->4096              MXFP8  8.5 us, NVFP4 7.5: launch, columns, first weights, parts, in a row
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -65,9 +65,9 @@ constexpr int DEC_A_STAGE = 128 * 128;       // 128 weight rows x 128 code bytes
 constexpr int DEC_MAX_TOKENS = 64;           // tokens of one call
 constexpr int DEC_MAX_K = 32;                // choices per token
 constexpr int DEC_MAX_STAGES = 12;
-// K values that make a CTA worth having in a shared unit: 4 steps of NVFP4, 8 of MXFP8.  Measured, 1x4096->4096 and one
-// token on 64 experts 2048x1408: NVFP4 8.0 and 19.5 us (half: 8.8, 20.9; twice: 8.4, 20.2), MXFP8 9.0 and 24.4 us
-// (half: 9.7, 25.8; twice: 10.1, 25.4).
+// K values that make a CTA worth having in a shared unit: 4 steps of NVFP4, 8 of MXFP8.  Half as many cost 0.7 us
+// (1x4096->4096) and 1.4 us (one token on 64 experts 2048x1408) more in either format, twice as many 0.4 and 0.7 us
+// (NVFP4), 1.0 and 1.0 us (MXFP8).
 constexpr int DEC_MIN_VALUES = 1024;
 // Most CTAs of a shared unit: their parts are read in one go (linear 3x14336->4096, MXFP8: 15.1 us, with 9 parts 15.3;
 // 19x11136->2304: 13.4 and 14.6; the other way 1x14336->1024, whose K would do for 14: 9.8 and 9.0).
