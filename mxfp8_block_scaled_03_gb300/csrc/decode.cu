@@ -14,7 +14,8 @@
 //          largest lose bits below 2^-17 of it.
 //   NVFP4  a block's values, scaled to |v| < 4, are written in base 8 with digits -4..4 (E2M1 holds
 //          these integers): v = d0 + d1/8 + ... + d4/4096, an error of at most 2^-14 of the block's
-//          largest value.
+//          largest value.  Its scale is relative to the row's largest block and reaches 2^-17 of it; a smaller block
+//          of x is written under that scale, in its lower digits, with an error of at most 2^-31 of the row's largest.
 // Accumulation is fp32 in TMEM; the columns of one token are added in fp32 and the result is
 // rounded once, to bf16.
 //
@@ -79,6 +80,8 @@ constexpr uint32_t DEC_TMEM_HALF = 256, DEC_TMEM_FULL = 512;   // likewise
 // TMEM columns: accumulators (at most 160, twice where they fit), then as many sets of scales of A and B as fit, used in
 // turn (at least two): a step's scales may be written while the MMAs of that many steps less one are pending.
 constexpr int SPLIT_THREADS = 1024;          // at most
+// Binades from a row's largest NVFP4 block scale, 2^8, to the smallest number of UE4M3, 2^-9.
+constexpr int NV_SPAN = 17;
 
 enum DecMode { DEC_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
 enum DecFmt { DEC_MX = 0, DEC_NV = 1 };
@@ -363,29 +366,45 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
     if (none) return;
   }
 
-  int top = -128;
+  // bf16 values of this thread's group gi, and their largest magnitude's bits
+  auto load = [&](int g0, uint4 (&w)[VALS / 8]) {
+    const int gi = g0 + tid;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < VALS / 8; ++i) {
+      w[i] = g0 == 0 ? ahead[i]
+             : gi < groups ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.K + gi * VALS) + i)
+                           : make_uint4(0u, 0u, 0u, 0u);
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                               __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
+    }
+    return max(m & 0xFFFFu, m >> 16) << 16;
+  };
+  // NVFP4: the row's largest exponent comes first, since the blocks' scales reach NV_SPAN binades below it; a smaller
+  // block is written under the smallest scale, in its lower digits.
+  int lowest = -128;
+  if constexpr (FMT == DEC_NV) {
+    int top = -128;
+    uint4 w[VALS / 8];
+    for (int g0 = 0; g0 < groups; g0 += blockDim.x) top = max(top, block_exponent(load(g0, w)));
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((tid & 31) == 0) atomicMax(&s_top, top);
+    __syncthreads();
+    lowest = s_top - NV_SPAN;
+    if (tid == 0) p.o.top[dst] = s_top;
+  }
   for (int g0 = 0; g0 < groups; g0 += blockDim.x) {
     const int gi = g0 + tid;
     const bool in = gi < groups;   // K % 128 == 0: whole blocks, and the four threads of one agree
     const int step = gi >> 4, g = gi & 15;
     uint4 w[VALS / 8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < VALS / 8; ++i) {
-      w[i] = g0 == 0 ? ahead[i]
-             : in    ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.K + gi * VALS) + i)
-                     : make_uint4(0u, 0u, 0u, 0u);
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
-                               __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
-    }
-    m = max(m & 0xFFFFu, m >> 16) << 16;
+    uint32_t m = load(g0, w);
     if constexpr (FMT == DEC_MX) {
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     }
     if (!in) continue;
-    const int eb = block_exponent(m);
-    top = max(top, eb);
+    const int eb = max(block_exponent(m), lowest);
     if (FMT == DEC_NV || (g & 3) == 0)
       p.o.exps[(static_cast<int64_t>(dst) * p.steps + step) * EB + (FMT == DEC_NV ? g : g >> 2)] =
           static_cast<uint8_t>(eb + 127);
@@ -403,12 +422,6 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
       const uint2 code = q + 1 < P ? next_codes<FMT, false>(r) : next_codes<FMT, true>(r);
       *reinterpret_cast<uint2*>(p.o.codes + (static_cast<int64_t>(dst) * P + q) * p.steps * 128 + gi * 8) = code;
     }
-  }
-  if constexpr (FMT == DEC_NV) {
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if ((tid & 31) == 0) atomicMax(&s_top, top);
-    __syncthreads();
-    if (tid == 0) p.o.top[dst] = s_top;
   }
 }
 
