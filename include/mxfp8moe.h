@@ -390,10 +390,13 @@ int nvfp4_grouped_mlp_fwd(const void* x_sorted, int64_t R, int64_t H, int64_t F,
 /*
  * Decode: the same layer and plain linears for a few tokens (T <= 64).  Only the weights are low
  * precision: x (bf16) and the intermediate h (fp32) are not quantized, sums are fp32, and the result
- * is rounded once, to bf16.  (The activations enter the tensor cores as short sums of E4M3 or E2M1
- * numbers: bf16 to within 2^-17 of a 32-value block's largest magnitude beside MXFP8 weights and h to
- * within 2^-12 of its own; both to within 2^-14 of a 16-value block's largest magnitude beside NVFP4
- * weights.)  Results do not depend on timing.  A token with a non-finite x gives non-finite values in
+ * is rounded once, to bf16.  The activations enter the tensor cores as short sums of E4M3 or E2M1
+ * numbers, off by at most
+ *   MXFP8 weights  x: 2^-17 of the largest magnitude of its block of 32;  h: 2^-12 of its own;
+ *   NVFP4 weights  x and h: 2^-14 of the largest magnitude of the block of 16 plus 2^-31 of the row's
+ *                  (a block more than 2^17 below the row's largest keeps fewer digits, one 2^31 below none).
+ * Blocks whose largest magnitude is below 2^-100 are written as if it were 2^-100.  Results do not
+ * depend on timing.  A token with a non-finite x gives non-finite values in
  * its own row only; weights must be finite.
  *
  * moe_decode_fwd -- a whole MoE layer, from the router's choices to the combined output:

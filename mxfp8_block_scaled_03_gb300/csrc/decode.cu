@@ -15,7 +15,7 @@
 //   NVFP4  a block's values, scaled to |v| < 4, are written in base 8 with digits -4..4 (E2M1 holds
 //          these integers): v = d0 + d1/8 + ... + d4/4096, an error of at most 2^-14 of the block's
 //          largest value.  Its scale is relative to the row's largest block and reaches 2^-17 of it; a smaller block
-//          of x is written under that scale, in its lower digits, with an error of at most 2^-31 of the row's largest.
+//          is written under that scale, in its lower digits, with an error of at most 2^-31 of the row's largest more.
 // Accumulation is fp32 in TMEM; the columns of one token are added in fp32 and the result is
 // rounded once, to bf16.
 //
@@ -27,6 +27,7 @@
 //   k_split_x        x -> columns (by token, or by pair for the MoE layer), and the bookkeeping of the call
 //   k_decode<UP>     units: 128 columns of F of one chosen expert (and up to 16 or 32 of its tokens); gate
 //                    and up rows are alternate K steps on two accumulators; h = gate silu(g) u -> columns
+//   k_lift_low_blocks  NVFP4: small blocks of h under the smallest scale
 //   k_decode<DOWN>   units: 128 rows of H of one chosen expert; a row of partial results per pair
 //   k_sum_rows       adds a token's pairs
 //   k_decode<LINEAR> units: 128 rows of W
@@ -82,6 +83,7 @@ constexpr uint32_t DEC_TMEM_HALF = 256, DEC_TMEM_FULL = 512;   // likewise
 constexpr int SPLIT_THREADS = 1024;          // at most
 // Binades from a row's largest NVFP4 block scale, 2^8, to the smallest number of UE4M3, 2^-9.
 constexpr int NV_SPAN = 17;
+constexpr int LIFT_THREADS = 128;
 
 enum DecMode { DEC_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
 enum DecFmt { DEC_MX = 0, DEC_NV = 1 };
@@ -118,6 +120,7 @@ struct DecOperand {
   uint8_t* codes;   // [rows * P][steps * 128]
   uint8_t* exps;    // [rows][steps][4 | 16]: exponent + 127 of every 32 | 16 values (255: not finite)
   int* top;         // [rows] largest exponent of the row (NVFP4)
+  int* low;         // [rows] smallest exponent of the row's blocks but those of zeros (NVFP4, h)
 };
 
 struct DecParams {
@@ -301,7 +304,7 @@ struct SplitParams {
   const float* gates;
   float* gate;            // [pairs]
   int* row_of;            // [T, k] pair of every choice (-1: none)
-  int* h_top;
+  int *h_top, *h_low;
   int* counters;
   int T, K, steps, n_ids, E, k, n_top, n_counters;
 };
@@ -335,7 +338,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
     }
   bad = __syncthreads_or(bad);
   if (b == 0 && tid == 0) *p.err = bad ? ERR_EXPERT_RANGE : 0u;
-  for (int i = b * blockDim.x + tid; i < p.n_top; i += gridDim.x * blockDim.x) p.h_top[i] = -128;
+  for (int i = b * blockDim.x + tid; i < p.n_top; i += gridDim.x * blockDim.x) {
+    p.h_top[i] = -128;
+    p.h_low[i] = 128;
+  }
   for (int i = b * blockDim.x + tid; i < p.n_counters; i += gridDim.x * blockDim.x) p.counters[i] = 0;
 
   int dst = t;   // row of the operand
@@ -427,8 +433,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_split_x(const SplitParams p) 
 
 // The scale words of one activation row and K step for its P columns, from its blocks' exponents.
 //   MXFP8  word of piece q: UE8M0 2^(e - 7 - 4 q) per block.
-//   NVFP4  one word per MMA, the same for all digits: UE4M3 2^(8 + e - top) per block (0 below 2^-9, which
-//          drops values under 2^-17 of the row's largest).
+//   NVFP4  one word per MMA, the same for all digits: UE4M3 2^(8 + e - top) per block (e >= top - NV_SPAN).
 // Blocks that are not finite get a NaN scale.
 // (Plain arithmetic: the byte-wise intrinsics are chains of instructions, 0.4 us a step for a warp alone.)
 __device__ __forceinline__ uint32_t mx_scales(uint32_t e4, int q) {
@@ -994,8 +999,13 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
             if (live && (lane & (FMT == DEC_NV ? 12 : 28)) == 0)
               p.h.exps[hr * p.h_steps * EB + (FMT == DEC_NV ? k0 >> 4 : k0 >> 5)] = static_cast<uint8_t>(eb + 127);
             if constexpr (FMT == DEC_NV) {
+              const int lo = m == 0u ? 128 : eb;
               const int t = max(eb, __shfl_xor_sync(0xFFFFFFFFu, eb, 16));
-              if (live && (lane & 28) == 0) atomicMax(p.h.top + hr, t);
+              const int l = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 16));
+              if (live && (lane & 28) == 0) {
+                atomicMax(p.h.top + hr, t);
+                atomicMin(p.h.low + hr, l);
+              }
             }
             const uint64_t inv2 = f2_pack(block_multiplier<FMT>(eb), block_multiplier<FMT>(eb));
             uint64_t ra = f2_mul(f2_pack(h[0], h[1]), inv2), rb = f2_mul(f2_pack(h[2], h[3]), inv2);
@@ -1023,6 +1033,62 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L.tmem_cols);
+  }
+}
+
+// h of the pairs (NVFP4, `blocks` blocks a row), between UP and DOWN: the row's largest exponent is known only now.
+// Blocks more than NV_SPAN binades below it are written again under the smallest scale, as k_split_x does with x:
+// the five digits as one integer, divided by the power of two between the scales, rounded to nearest.  Seldom needed
+// (a row with values 2^17 apart), and only such a row is read.
+// The launch costs a call 0 to 1.4 us: one token on 64 experts 2048x1408 19.3 -> 20.3, 64 tokens 68.3 -> 69.8, 8 experts
+// 4096x14336 142.9 -> 144.7.  Left to UP's last warp per expert, which needs a fence and a count after every unit: 20.4,
+// 76.0 and 149.2 us.
+__global__ void __launch_bounds__(LIFT_THREADS) k_lift_low_blocks(const DecOperand h, int steps, int blocks) {
+  constexpr int P = dec_pieces(DEC_NV, DEC_DOWN);
+  pdl_launch_dependents();
+  pdl_wait();
+  const int row = blockIdx.x;
+  const int lowest = h.top[row] - NV_SPAN;
+  if (h.low[row] >= lowest) return;
+  const int64_t pitch = static_cast<int64_t>(steps) * 128;
+  uint8_t* exps = h.exps + static_cast<int64_t>(row) * steps * dec_exp_bytes(DEC_NV);
+  uint8_t* codes = h.codes + static_cast<int64_t>(row) * P * pitch;
+  for (int b = threadIdx.x; b < blocks; b += LIFT_THREADS) {
+    const int shift = lowest + 127 - static_cast<int>(exps[b]);
+    if (shift <= 0) continue;
+    uint2 in[P], out[P];
+#pragma unroll
+    for (int d = 0; d < P; ++d) {
+      in[d] = *reinterpret_cast<const uint2*>(codes + d * pitch + b * 8);
+      out[d] = make_uint2(0u, 0u);
+    }
+#pragma unroll 1
+    for (int z = 0; z < 64; z += 4) {   // one value: bits z % 32 of either word
+      const bool hi = z >= 32;
+      const int at = z & 31;
+      int v = 0;
+#pragma unroll
+      for (int d = 0; d < P; ++d) {
+        const uint32_t c = ((hi ? in[d].y : in[d].x) >> at) & 15u;
+        const int m = (c & 7u) < 4u ? static_cast<int>(c & 7u) >> 1 : static_cast<int>(c & 7u) - 2;   // 0 1 2 3 4
+        v = v * 8 + ((c & 8u) != 0u ? -m : m);
+      }
+      // |v| < 2^15: to nearest, halves away from zero
+      const int a = shift > 16 ? 0 : (abs(v) + (1 << (shift - 1))) >> shift;
+      v = v < 0 ? -a : a;
+#pragma unroll
+      for (int d = P - 1; d >= 0; --d) {
+        const int digit = d == 0 ? v : ((v + 4) & 7) - 4;
+        v = (v - digit) >> 3;
+        const uint32_t m = static_cast<uint32_t>(abs(digit));
+        const uint32_t c = (m < 3u ? m * 2u : m + 2u) | (digit < 0 ? 8u : 0u);
+        if (hi) out[d].y |= c << at;
+        else out[d].x |= c << at;
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < P; ++d) *reinterpret_cast<uint2*>(codes + d * pitch + b * 8) = out[d];
+    exps[b] = static_cast<uint8_t>(lowest + 127);
   }
 }
 
@@ -1167,7 +1233,7 @@ constexpr size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(25
 
 // Columns of `rows` rows of K values in `pieces` pieces each, from byte `at` of a workspace.
 struct DecOperandLayout {
-  size_t codes, exps, top, end;
+  size_t codes, exps, top, low, end;
   int64_t code_rows, steps;
   int pieces;
 };
@@ -1179,11 +1245,12 @@ DecOperandLayout dec_operand(int fmt, int pieces, size_t at, int64_t rows, int64
   o.codes = at;
   o.exps = align256(o.codes + static_cast<size_t>(o.code_rows) * o.steps * 128);
   o.top = align256(o.exps + static_cast<size_t>(rows) * o.steps * dec_exp_bytes(fmt));
-  o.end = align256(o.top + static_cast<size_t>(rows) * sizeof(int));
+  o.low = align256(o.top + static_cast<size_t>(rows) * sizeof(int));
+  o.end = align256(o.low + static_cast<size_t>(rows) * sizeof(int));
   return o;
 }
 DecOperand dec_pointers(uint8_t* base, const DecOperandLayout& o) {
-  return {base + o.codes, base + o.exps, reinterpret_cast<int*>(base + o.top)};
+  return {base + o.codes, base + o.exps, reinterpret_cast<int*>(base + o.top), reinterpret_cast<int*>(base + o.low)};
 }
 
 // Workspace sizes do not depend on the device: room for the parts of at most this many CTAs.
@@ -1332,6 +1399,7 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
   q.gate = const_cast<float*>(up.gate);
   q.row_of = reinterpret_cast<int*>(w + ws.row_of);
   q.h_top = up.h.top;
+  q.h_low = up.h.low;
   q.counters = up.counters;
   q.T = up.T;
   q.K = up.K;
@@ -1341,9 +1409,13 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
   q.k = k;
   q.n_top = FMT == DEC_NV ? up.T * k : 0;
   q.n_counters = static_cast<int>(ws.n_up + ws.n_down);
-  if (!split_launch<FMT, true>(q, s) || !dec_launch<FMT, DEC_UP>(m1, mx, up, sms, s) ||
-      !dec_launch<FMT, DEC_DOWN>(m2, mh, down, sms, s))
-    return MXFP8_ERR_CUDA;
+  if (!split_launch<FMT, true>(q, s) || !dec_launch<FMT, DEC_UP>(m1, mx, up, sms, s)) return MXFP8_ERR_CUDA;
+  if constexpr (FMT == DEC_NV) {
+    DecLaunch lift(up.T * k, LIFT_THREADS, 0, s);
+    if (cudaLaunchKernelEx(&lift.cfg, k_lift_low_blocks, up.h, up.h_steps, down.K / 16) != cudaSuccess)
+      return MXFP8_ERR_CUDA;
+  }
+  if (!dec_launch<FMT, DEC_DOWN>(m2, mh, down, sms, s)) return MXFP8_ERR_CUDA;
   DecLaunch sum(up.T, 256, 0, s);
   sum.cfg.gridDim.y = static_cast<unsigned>((H / 4 + 255) / 256);
   return cudaLaunchKernelEx(&sum.cfg, k_sum_rows, static_cast<const float*>(down.y), static_cast<const int*>(q.row_of), k,

@@ -96,3 +96,41 @@ def test_layer_on_tokens_with_a_large_channel(mx, fmt):
     x[:, 64:96] = 0
     ref, bound = D.moe_ref(fmt, x, ids, None, v1, v2, E, H, F)
     D.check(y, ref, bound)
+
+
+@FORMATS
+@pytest.mark.parametrize("T,k,E,H,F", [(1, 1, 2, 256, 384), (7, 2, 3, 256, 1152), (20, 1, 1, 128, 640),
+                                       (3, 2, 4, 4096, 512), (33, 2, 4, 256, 2048), (2, 2, 2, 512, 14336)])
+@pytest.mark.parametrize("size", [1.0, 8.0, 64.0])
+def test_layer_beside_a_large_channel(mx, fmt, T, k, E, H, F, size):
+    """A channel of h far above the others (its gate and up rows follow the signs of a token), and zeros in W2's
+    columns there."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(T * 64 + F)
+    x = torch.randn((T, H), generator=gen, device="cuda")
+    sign = torch.sign(x[0]) + (x[0] == 0)
+    for t in range(1, T, 2):                             # half of the tokens: signs that agree by 3/4
+        keep = torch.rand((H,), generator=gen, device="cuda") < 0.75
+        x[t] = torch.where(keep, x[t].abs() * sign, x[t])
+    x = x.bfloat16()
+    w1 = 0.02 * torch.randn((E, 2, F, H), generator=gen, device="cuda")
+    w2 = 0.02 * torch.randn((E, H, F), generator=gen, device="cuda")
+    blk = F // 64 * 32
+    w1[:, :, blk + 7] = 0.02 * size * sign
+    w2[:, :, blk:blk + 32] = 0
+    w1, v1 = quantized(mx, fmt, w1.view(-1, H).bfloat16())
+    w2, v2 = quantized(mx, fmt, w2.view(-1, F).bfloat16())
+    ids = torch.rand((T, E), generator=gen, device="cuda").argsort(1)[:, :k].int().contiguous()
+    gates = 0.25 + torch.rand((T, k), generator=gen, device="cuda")
+    y = D.moe(mx, fmt, x, ids, gates, w1, w2)
+    ref, bound = D.moe_ref(fmt, x, ids, gates, v1, v2, E, H, F)
+    if fmt == "nvfp4":
+        for t in range(T):
+            for j in range(k):
+                e = int(ids[t, j])
+                g, u = (x[t].double() @ v1[(2 * e + b) * F:(2 * e + b + 1) * F].t() for b in (0, 1))
+                top = float((g / (1 + torch.exp(-g)) * u).abs().max() * gates[t, j])
+                bound[t] += 2.0 ** -31 * top * v2[e * H:(e + 1) * H].abs().sum(1)
+    D.check(y, ref, bound)
+    again = D.moe(mx, fmt, x, ids, gates, w1, w2)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16)), "not reproducible"
