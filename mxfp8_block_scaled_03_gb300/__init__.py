@@ -558,21 +558,26 @@ def nvfp4_grouped_mlp_fwd(x_sorted, split_sizes, gates, w1, w2, h_amax: float, y
     return y
 
 
-def _need(t, dtype, shape, name: str):
-    """A contiguous CUDA tensor of this dtype and shape (an int: at least so many elements).  These calls
+def _place(t, name: str):
+    """(device, its current stream) of a call: the device of its first tensor.  The library launches on the current
+    device, so it has to be that one.  A call with a stream of its own makes that stream and its device current
+    first, so that what the call allocates belongs to it."""
+    from torch import _C
+    dev = t.get_device()                       # -1: not on a GPU
+    if dev < 0 or dev != _C._cuda_getDevice():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device (or the stream's); got {t.device}")
+    return dev, _C._cuda_getCurrentRawStream(dev)
+
+
+def _need(t, dtype, shape, name: str, dev: int):
+    """A contiguous tensor of this device, dtype and shape (an int: at least so many elements).  These calls
     are as short as the kernels behind them, so the message is put together only when it is needed."""
-    if t.dtype == dtype and t.is_cuda and t.is_contiguous() and \
+    if t.dtype == dtype and t.get_device() == dev and t.is_contiguous() and \
             (t.numel() >= shape if isinstance(shape, int) else t.shape == shape):
         return t.data_ptr()
     want = f"at least {shape} elements" if isinstance(shape, int) else f"shape {tuple(shape)}"
-    raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, {want}; got {t.dtype}, {tuple(t.shape)}")
-
-
-def _stream_of(t) -> int:
-    """The current stream of the tensor's device.  A call with a stream of its own makes that one current first, so
-    that what the call allocates belongs to it."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    raise ValueError(f"{name}: expected a contiguous tensor of {dtype}, {want}, on cuda:{dev}; "
+                     f"got {t.dtype}, {tuple(t.shape)}, {t.device}")
 
 
 def _sf_mma_bytes(nv: bool, M: int, K: int) -> int:
@@ -590,31 +595,32 @@ def _moe_decode(name, nv, x, experts, gates, w1, w2, out, workspace, stream):
         with torch.cuda.stream(stream):
             return _moe_decode(name, nv, x, experts, gates, w1, w2, out, workspace, None)
     u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
+    dev, current = _place(x, "x")
     T, H = x.shape
     T2, k = experts.shape
     per = 2 if nv else 1                       # values per code byte
     M2, F = w2[0].shape
     F *= per
     E = M2 // H if H else 0
-    px, pe = _need(x, bf16, (T, H), "x"), _need(experts, torch.int32, (T, k), "experts")
-    pg = None if gates is None else _need(gates, f32, (T, k), "gates")
-    p1, s1 = _need(w1[0], u8, (E * 2 * F, H // per), "W1 codes"), _need(w1[1], u8, _sf_mma_bytes(nv, E * 2 * F, H), "W1 scales")
-    p2, s2 = _need(w2[0], u8, (E * H, F // per), "W2 codes"), _need(w2[1], u8, _sf_mma_bytes(nv, E * H, F), "W2 scales")
+    px, pe = _need(x, bf16, (T, H), "x", dev), _need(experts, torch.int32, (T, k), "experts", dev)
+    pg = None if gates is None else _need(gates, f32, (T, k), "gates", dev)
+    p1 = _need(w1[0], u8, (E * 2 * F, H // per), "W1 codes", dev)
+    s1 = _need(w1[1], u8, _sf_mma_bytes(nv, E * 2 * F, H), "W1 scales", dev)
+    p2 = _need(w2[0], u8, (E * H, F // per), "W2 codes", dev)
+    s2 = _need(w2[1], u8, _sf_mma_bytes(nv, E * H, F), "W2 scales", dev)
     if out is None:
         out = torch.empty((T, H), dtype=bf16, device=x.device)
         po = out.data_ptr()
     else:
-        po = _need(out, bf16, (T, H), "out")
+        po = _need(out, bf16, (T, H), "out", dev)
     if workspace is None:
         workspace = torch.empty(max(256, moe_decode_workspace_size(T, k, H, F, E)), dtype=u8, device=x.device)
-    pw = _need(workspace, u8, 256, "workspace")
+    pw = _need(workspace, u8, 256, "workspace", dev)
     if nv:
-        st = lib().nvfp4_moe_decode_fwd(px, T, H, F, E, k, pe, pg, p1, s1, _need(w1[2], f32, 1, "W1 amax"), p2, s2,
-                                        _need(w2[2], f32, 1, "W2 amax"), po, pw, workspace.numel(),
-                                        _stream_of(x))
+        st = lib().nvfp4_moe_decode_fwd(px, T, H, F, E, k, pe, pg, p1, s1, _need(w1[2], f32, 1, "W1 amax", dev), p2, s2,
+                                        _need(w2[2], f32, 1, "W2 amax", dev), po, pw, workspace.numel(), current)
     else:
-        st = lib().moe_decode_fwd(px, T, H, F, E, k, pe, pg, p1, s1, p2, s2, po, pw, workspace.numel(),
-                                  _stream_of(x))
+        st = lib().moe_decode_fwd(px, T, H, F, E, k, pe, pg, p1, s1, p2, s2, po, pw, workspace.numel(), current)
     if st != OK:
         raise MXFP8Error(st, name)
     return out
@@ -646,23 +652,24 @@ def _matvec(name, nv, x, w, out, workspace, stream):
         with torch.cuda.stream(stream):
             return _matvec(name, nv, x, w, out, workspace, None)
     u8, bf16 = torch.uint8, torch.bfloat16
+    dev, current = _place(x, "x")
     T, K = x.shape
     N = w[0].shape[0]
-    px = _need(x, bf16, (T, K), "x")
-    pq, ps = _need(w[0], u8, (N, K // 2 if nv else K), "codes"), _need(w[1], u8, _sf_mma_bytes(nv, N, K), "scales")
+    px, pq = _need(x, bf16, (T, K), "x", dev), _need(w[0], u8, (N, K // 2 if nv else K), "codes", dev)
+    ps = _need(w[1], u8, _sf_mma_bytes(nv, N, K), "scales", dev)
     if out is None:
         out = torch.empty((T, N), dtype=bf16, device=x.device)
         po = out.data_ptr()
     else:
-        po = _need(out, bf16, (T, N), "out")
+        po = _need(out, bf16, (T, N), "out", dev)
     if workspace is None:
         workspace = torch.empty(max(256, matvec_workspace_size(T, K)), dtype=u8, device=x.device)
-    pw = _need(workspace, u8, 256, "workspace")
+    pw = _need(workspace, u8, 256, "workspace", dev)
     if nv:
-        st = lib().nvfp4_matvec(px, T, K, N, pq, ps, _need(w[2], torch.float32, 1, "amax"), po, pw, workspace.numel(),
-                                _stream_of(x))
+        st = lib().nvfp4_matvec(px, T, K, N, pq, ps, _need(w[2], torch.float32, 1, "amax", dev), po, pw,
+                                workspace.numel(), current)
     else:
-        st = lib().mxfp8_matvec(px, T, K, N, pq, ps, po, pw, workspace.numel(), _stream_of(x))
+        st = lib().mxfp8_matvec(px, T, K, N, pq, ps, po, pw, workspace.numel(), current)
     if st != OK:
         raise MXFP8Error(st, name)
     return out
@@ -681,9 +688,10 @@ def nvfp4_matvec(x, w, out=None, workspace=None, stream=None):
 
 
 def _norm_args(y, res_like, w_post, gate, w_pre, post_norm):
-    """(T, H, residual dtype, its code, gate kind, gate pointer, w_post pointer, w_pre pointer)."""
+    """(device, stream, T, H, residual dtype, its code, gate kind, gate pointer, w_post pointer, w_pre pointer)."""
     import torch
     f32 = torch.float32
+    dev, current = _place(y, "y")
     T, H = y.shape
     rt = res_like.dtype
     if rt is not torch.bfloat16 and rt is not f32:
@@ -691,10 +699,10 @@ def _norm_args(y, res_like, w_post, gate, w_pre, post_norm):
     kind, pg = 0, None
     if gate is not None:
         kind = 1 if gate.dim() == 1 else 2     # [H]: per channel; [T, 1]: per token
-        pg = _need(gate, f32, (H,) if kind == 1 else (T, 1), "gate")
-    return (T, H, rt, 0 if rt is torch.bfloat16 else 1, kind, pg,
-            None if w_post is None else _need(w_post, f32, (H,), "w_post"),
-            None if w_pre is None else _need(w_pre, f32, (H,), "w_pre"))
+        pg = _need(gate, f32, (H,) if kind == 1 else (T, 1), "gate", dev)
+    return (dev, current, T, H, rt, 0 if rt is torch.bfloat16 else 1, kind, pg,
+            None if w_post is None else _need(w_post, f32, (H,), "w_post", dev),
+            None if w_pre is None else _need(w_pre, f32, (H,), "w_pre", dev))
 
 
 def residual_norm_fwd(y, res, w_post=None, gate=None, w_pre=None, res_scale: float = 1.0, post_norm: bool = True,
@@ -709,17 +717,17 @@ def residual_norm_fwd(y, res, w_post=None, gate=None, w_pre=None, res_scale: flo
         with torch.cuda.stream(stream):
             return residual_norm_fwd(y, res, w_post, gate, w_pre, res_scale, post_norm, eps, out)
     bf16 = torch.bfloat16
-    T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res, w_post, gate, w_pre, post_norm)
-    py, pr = _need(y, bf16, (T, H), "y"), _need(res, rt, (T, H), "res")
+    dev, current, T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res, w_post, gate, w_pre, post_norm)
+    py, pr = _need(y, bf16, (T, H), "y", dev), _need(res, rt, (T, H), "res", dev)
     if out is None:
         res_out, n, stats = torch.empty_like(res), torch.empty_like(y), torch.empty((2, T), dtype=torch.float32, device=y.device)
         po, pn, ps = res_out.data_ptr(), n.data_ptr(), stats.data_ptr()
     else:
         res_out, n, stats = out
-        po, pn = _need(res_out, rt, (T, H), "res_out"), _need(n, bf16, (T, H), "n")
-        ps = _need(stats, torch.float32, (2, T), "stats")
-    st = lib().residual_norm_fwd(py, pr, pa, pg, pb, T, H, code, kind, 1 if post_norm else 0, res_scale, eps, po, pn, ps,
-                                 _stream_of(y))
+        po, pn = _need(res_out, rt, (T, H), "res_out", dev), _need(n, bf16, (T, H), "n", dev)
+        ps = _need(stats, torch.float32, (2, T), "stats", dev)
+    st = lib().residual_norm_fwd(py, pr, pa, pg, pb, T, H, code, kind, 1 if post_norm else 0, res_scale, eps, po, pn,
+                                 ps, current)
     if st != OK:
         raise MXFP8Error(st, "residual_norm_fwd")
     return res_out, n, stats
@@ -739,18 +747,19 @@ def residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post=None, gate=None, w
         with torch.cuda.stream(stream):
             return residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post, gate, w_pre, res_scale, post_norm, workspace)
     bf16, f32 = torch.bfloat16, torch.float32
-    T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res_out, w_post, gate, w_pre, post_norm)
-    pn, py, pr = _need(dn, bf16, (T, H), "dn"), _need(y, bf16, (T, H), "y"), _need(res_out, rt, (T, H), "res_out")
-    pd = None if dres_out is None else _need(dres_out, rt, (T, H), "dres_out")
+    dev, current, T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res_out, w_post, gate, w_pre, post_norm)
+    pn, py = _need(dn, bf16, (T, H), "dn", dev), _need(y, bf16, (T, H), "y", dev)
+    pr = _need(res_out, rt, (T, H), "res_out", dev)
+    pd = None if dres_out is None else _need(dres_out, rt, (T, H), "dres_out", dev)
     like = torch.empty_like
     dy, dres = like(y), like(res_out)
     dw_post, dgate, dw_pre = (None if w is None else like(w) for w in (w_post, gate, w_pre))
     if workspace is None:
         workspace = torch.empty(max(16, residual_norm_bwd_workspace_size(T, H)), dtype=torch.uint8, device=y.device)
-    st = lib().residual_norm_bwd(pn, pd, py, pr, _need(stats, f32, (2, T), "stats"), pa, pg, pb, T, H, code, kind,
+    st = lib().residual_norm_bwd(pn, pd, py, pr, _need(stats, f32, (2, T), "stats", dev), pa, pg, pb, T, H, code, kind,
                                  1 if post_norm else 0, res_scale, dy.data_ptr(), dres.data_ptr(), _ptr(dw_post),
-                                 _ptr(dgate), _ptr(dw_pre), _need(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
-                                 _stream_of(y))
+                                 _ptr(dgate), _ptr(dw_pre), _need(workspace, torch.uint8, 0, "workspace", dev),
+                                 workspace.numel(), current)
     if st != OK:
         raise MXFP8Error(st, "residual_norm_bwd")
     return dy, dres, dw_post, dgate, dw_pre
