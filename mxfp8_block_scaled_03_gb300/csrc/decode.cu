@@ -786,6 +786,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
       }
       if (i >= L.sf_sets) {
         if (!dec_warp_wait(&empty[read.slot], read.phase, abort_flag, p, ERR_TIMEOUT_SF, lane)) break;
+        tc_fence_after();   // the copies to the set below come after the MMAs that read it
 #pragma unroll
         for (int z = 0; z < SCALE_WARPS; ++z) next_stage(read);
       } else if (i + SCALE_WARPS >= L.sf_sets) {
