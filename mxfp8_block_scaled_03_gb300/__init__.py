@@ -687,7 +687,7 @@ def nvfp4_matvec(x, w, out=None, workspace=None, stream=None):
     return _matvec("nvfp4_matvec", True, x, w, out, workspace, stream)
 
 
-def _norm_args(y, res_like, w_post, gate, w_pre, post_norm):
+def _norm_args(y, res_like, w_post, gate, w_pre):
     """(device, stream, T, H, residual dtype, its code, gate kind, gate pointer, w_post pointer, w_pre pointer)."""
     import torch
     f32 = torch.float32
@@ -717,7 +717,7 @@ def residual_norm_fwd(y, res, w_post=None, gate=None, w_pre=None, res_scale: flo
         with torch.cuda.stream(stream):
             return residual_norm_fwd(y, res, w_post, gate, w_pre, res_scale, post_norm, eps, out)
     bf16 = torch.bfloat16
-    dev, current, T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res, w_post, gate, w_pre, post_norm)
+    dev, current, T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res, w_post, gate, w_pre)
     py, pr = _need(y, bf16, (T, H), "y", dev), _need(res, rt, (T, H), "res", dev)
     if out is None:
         res_out, n, stats = torch.empty_like(res), torch.empty_like(y), torch.empty((2, T), dtype=torch.float32, device=y.device)
@@ -747,7 +747,7 @@ def residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post=None, gate=None, w
         with torch.cuda.stream(stream):
             return residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post, gate, w_pre, res_scale, post_norm, workspace)
     bf16, f32 = torch.bfloat16, torch.float32
-    dev, current, T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res_out, w_post, gate, w_pre, post_norm)
+    dev, current, T, H, rt, code, kind, pg, pa, pb = _norm_args(y, res_out, w_post, gate, w_pre)
     pn, py = _need(dn, bf16, (T, H), "dn", dev), _need(y, bf16, (T, H), "y", dev)
     pr = _need(res_out, rt, (T, H), "res_out", dev)
     pd = None if dres_out is None else _need(dres_out, rt, (T, H), "dres_out", dev)

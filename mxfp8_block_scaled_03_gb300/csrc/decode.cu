@@ -836,7 +836,6 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
     Place q = first;
     for (int seg = 0; i < n_steps; ++seg) {
       const bool share = i < n_share && per_unit > 1;
-      const int r0 = q.f * ACCS + q.acc, r1 = i < n_share ? r0 + n_share : su;   // the part's steps of the unit
       const int u = cta / per_unit, parts = per_unit;   // if shared: which unit, how many parts
       const int n = rows_of(q.a), row0 = first_row(q.a), tile = q.tile;
       float unscale = 1.0f;   // lane c: of row c's sums
@@ -923,7 +922,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
         // or 32 lanes wide).  (Passing the sums of whole units through memory as well, to free the accumulators earlier, measured
         // the same.)  Short straight code: its first pass is fetched line by line behind the weights' stream.
         constexpr int PH = dec_pieces(FMT, DEC_DOWN), LD = (4 * P + 7) / 8;
-        const bool has[2] = {r1 - r0 > 1 || (r0 & 1) == 0, r1 - r0 > 1 || (r0 & 1) == 1};
+        static_assert(MIN_STEPS >= 2, "a part of a unit holds steps of both accumulators");
         const float gates = p.gate[row0 + min(lane, n - 1)];
         const int64_t pitch = static_cast<int64_t>(p.h_steps) * 128;
         const int k0 = tile * 128 + quarter * 32 + (lane & ~3);   // of this lane's four values
@@ -944,7 +943,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
               for (int j = 0; j < 4; ++j) {
                 const float scale = FMT == DEC_NV ? __shfl_sync(0xFFFFFFFFu, unscale, (c0 + j) & 31) : 1.0f;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) v[b][j] = has[b] ? sum_pieces<FMT, P>(d[b] + j * P) * scale : 0.0f;
+                for (int b = 0; b < 2; ++b) v[b][j] = sum_pieces<FMT, P>(d[b] + j * P) * scale;
               }
               if (phase == 0) {
 #pragma unroll
@@ -1023,7 +1022,7 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
           if (phase == 0 || !share) release();
         }
       }
-      i += r1 - r0;
+      i += i < n_share ? n_share : su;
       q.f = p.steps - 1;   // on from the last step of what was done
       q.acc = ACCS - 1;
       advance(q, i - 1);
