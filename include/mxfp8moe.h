@@ -396,8 +396,8 @@ int nvfp4_grouped_mlp_fwd(const void* x_sorted, int64_t R, int64_t H, int64_t F,
  *   NVFP4 weights  x and h: 2^-14 of the largest magnitude of the block of 16 plus 2^-31 of the row's
  *                  (a block more than 2^17 below the row's largest keeps fewer digits, one 2^31 below none).
  * Blocks whose largest magnitude is below 2^-100 are written as if it were 2^-100.  Results do not
- * depend on timing.  A token with a non-finite x gives non-finite values in
- * its own row only; weights must be finite.
+ * depend on timing.  A token with a non-finite x gives non-finite values in its own row only; weights
+ * must be finite.
  *
  * moe_decode_fwd -- a whole MoE layer, from the router's choices to the combined output:
  *     out[t] = sum_j gate[t,j] W2[e] ( silu(W1[e, 0:F] x_t) * (W1[e, F:2F] x_t) ),  e = experts[t,j]
@@ -411,13 +411,16 @@ int nvfp4_grouped_mlp_fwd(const void* x_sorted, int64_t R, int64_t H, int64_t F,
  *   workspace (device) moe_decode_workspace_size(T, k, H, F, E) bytes, 256-byte aligned; its first
  *            4 bytes are the error word (mxfp8_check_device_error).  Nothing in it needs to be
  *            initialised or kept.  Not shared by two calls in flight.
- *   Requirements: 0 <= T <= 64, 1 <= k <= 32, 1 <= E <= 1024, H % 128 == 0, F % 128 == 0 (otherwise
+ *   Requirements: T >= 0, k >= 1, H > 0, F > 0, 1 <= E <= 1024 (otherwise MXFP8_ERR_INVALID_ARG);
+ *   T <= 64, k <= 32, H % 128 == 0, F % 128 == 0, fewer than 2^31 weight rows (otherwise
  *   MXFP8_ERR_UNSUPPORTED: larger batches go through moe_permute and grouped_mlp_fwd_tokens).  x, out
  *   and weights 16-byte aligned, experts and gates 4-byte aligned.
  * nvfp4_moe_decode_fwd -- the same from the weights of nvfp4_grouped_mlp_fwd; no h_amax is needed.
  * mxfp8_matvec, nvfp4_matvec -- y[t] = W x_t for T <= 64 rows of x (device) bf16 [T, K] and W [N, K] as
  *   mxfp8_quantize (row-wise) or nvfp4_quantize write it with MXFP8_SF_MMA; y (device) bf16 [T, N],
- *   fully overwritten, must not overlap x.  K % 128 == 0, N % 128 == 0.  workspace (device):
+ *   fully overwritten, must not overlap x.  T >= 0, K > 0, N >= 0 (otherwise MXFP8_ERR_INVALID_ARG);
+ *   T <= 64, K % 128 == 0, N % 128 == 0 (otherwise MXFP8_ERR_UNSUPPORTED: a narrower W, a router's for
+ *   fewer than 128 experts, is filled up with rows of zeros).  workspace (device):
  *   matvec_workspace_size(T, K) bytes (grows with T and K), 256-byte aligned, its first 4 bytes the
  *   error word.
  */

@@ -630,14 +630,18 @@ def moe_decode_fwd(x, experts, gates, w1_q, w1_sf, w2_q, w2_sf, out=None, worksp
     """A whole MoE layer for a few tokens (T <= 64): out[t] = sum_j gates[t, j] * expert(experts[t, j])(x_t).
 
     x bf16 [T, H]; experts int32 [T, k] (negative: a dropped choice); gates float32 [T, k] or None;
-    weights as for grouped_mlp_fwd.  The activations are not quantized.  Returns out bf16 [T, H].
-    `workspace` (uint8 CUDA tensor, moe_decode_workspace_size bytes) is allocated here when not given."""
+    weights as for grouped_mlp_fwd.  The activations are not rounded to 8 bits: x is off by at most 2^-17 of its
+    block's largest value, the intermediate by 2^-12.  Returns out bf16 [T, H].
+    `workspace` (uint8 CUDA tensor, moe_decode_workspace_size bytes) is allocated here when not given, and its
+    error word is lost with it: to learn of an id >= E, which is skipped, or of a wait that ran out, pass one and
+    ask mxfp8_check_device_error."""
     return _moe_decode("moe_decode_fwd", False, x, experts, gates, (w1_q, w1_sf), (w2_q, w2_sf), out, workspace, stream)
 
 
 def nvfp4_moe_decode_fwd(x, experts, gates, w1, w2, out=None, workspace=None, stream=None):
     """moe_decode_fwd from NVFP4 weights: w1 = (codes, scale codes in SF_MMA layout, amax) as for
-    nvfp4_grouped_mlp_fwd, w2 likewise."""
+    nvfp4_grouped_mlp_fwd, w2 likewise.  x and the intermediate are off by at most 2^-14 of their block's largest
+    value plus 2^-31 of the row's."""
     return _moe_decode("nvfp4_moe_decode_fwd", True, x, experts, gates, w1, w2, out, workspace, stream)
 
 
@@ -677,13 +681,15 @@ def _matvec(name, nv, x, w, out, workspace, stream):
 
 def mxfp8_matvec(x, w_q, w_sf, out=None, workspace=None, stream=None):
     """y = x W^T for a few rows of x (bf16 [T, K], T <= 64) from W quantized by mxfp8_quantize (row-wise,
-    SF_MMA).  x is not quantized.  Returns bf16 [T, N]."""
+    SF_MMA).  x is not rounded to 8 bits (off by at most 2^-17 of a block's largest value).  Returns bf16 [T, N].
+    `workspace` (matvec_workspace_size bytes) and its error word as for moe_decode_fwd."""
     return _matvec("mxfp8_matvec", False, x, (w_q, w_sf), out, workspace, stream)
 
 
 def nvfp4_matvec(x, w, out=None, workspace=None, stream=None):
     """y = x W^T for a few rows of x (bf16 [T, K], T <= 64) from 4-bit weights: w = (codes, scale codes,
-    amax) as nvfp4_quantize writes them with SF_MMA.  Returns bf16 [T, N]."""
+    amax) as nvfp4_quantize writes them with SF_MMA.  x is off by at most 2^-14 of a block's largest value plus
+    2^-31 of the row's.  Returns bf16 [T, N].  `workspace` (matvec_workspace_size bytes) as for moe_decode_fwd."""
     return _matvec("nvfp4_matvec", True, x, w, out, workspace, stream)
 
 
