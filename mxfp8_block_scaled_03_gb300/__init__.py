@@ -562,11 +562,11 @@ def _place(t, name: str):
     """(device, its current stream) of a call: the device of its first tensor.  The library launches on the current
     device, so it has to be that one.  A call with a stream of its own makes that stream and its device current
     first, so that what the call allocates belongs to it."""
-    from torch import _C
+    import torch
     dev = t.get_device()                       # -1: not on a GPU
-    if dev < 0 or dev != _C._cuda_getDevice():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: expected a tensor on the current CUDA device (or the stream's); got {t.device}")
-    return dev, _C._cuda_getCurrentRawStream(dev)
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _need(t, dtype, shape, name: str, dev: int):
