@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(BN_THREADS, 1) k_residual_norm_bwd(const NormP
     return s1;
   };
   // The second half of a row and the first half of the next run between two barriers, so that a row costs
-  // one exchange between its warps instead of two (16384 x 4096, bf16: 164 -> 145 us).  With two vectors per
-  // thread the registers do not hold both (202 -> 282 us): there the halves follow each other.
+  // one exchange between its warps instead of two (16384 x 4096, bf16, column sums included: 162 -> 150 us).  With two
+  // vectors per thread the registers do not hold both (8192 x 8192: 190 -> 272 us): there the halves follow each other.
   const uint64_t scale = f2_splat(p.res_scale);
   Scalars cur = scalars(first), next = scalars(first + step);
   cp_async_wait(p.stages - 2);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(BN_THREADS, 1) k_residual_norm_bwd(const NormP
 
 // Adds the CTAs' column sums part[.][k][c].  A CTA takes 32 columns of one k; its warps take equal shares of the
 // CTAs, added in order: five trips to the L2 at once instead of 19 in turn (16384 x 4096, the backward as a whole:
-// 150 us, with 8 warps 152; 1531 x 2048: 16.6 and 18.3).
+// 150 us, with 8 warps 152; 1531 x 2048: 16.4 and 18.2).
 __global__ void __launch_bounds__(COLS_THREADS) k_norm_columns(const NormParams p, int ctas) {
   __shared__ float s[COLS_THREADS / 32][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -515,8 +515,9 @@ struct NormShape {
 NormShape norm_shape(int H, int pieces, bool bwd, size_t least) {
   NormShape s{};
   const int nv = H / 8;
-  // two vectors per thread beyond 2048 columns: fewer warps to exchange sums with (forward, 4096 columns: 101 ->
-  // 87 us); the backward's registers hold only one (4096 columns: 145 against 278 us)
+  // two vectors per thread beyond 2048 columns: fewer warps to exchange sums with (forward, 16384 x 4096: 101 ->
+  // 91 us); the backward's registers hold only one (150 against 174 us), so beyond 4096 columns, where it needs two, it
+  // runs at 50 to 63% of the copy (13000 x 5120: 238 us, 8192 x 8192: 190)
   s.v = nv <= (bwd ? BN_THREADS : BN_THREADS / 2) ? 1 : 2;
   s.tpr = ((nv + s.v - 1) / s.v + 31) / 32 * 32;
   s.groups = std::max(1, BN_THREADS / s.tpr);

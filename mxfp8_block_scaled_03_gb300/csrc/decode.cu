@@ -33,19 +33,20 @@
 //   k_decode<LINEAR> units: 128 rows of W
 // The kernels are launched programmatically dependent: a kernel's weight copies start while the one
 // before it runs, and only what reads its results waits.  Weights are copied evict-first, so that everything
-// else stays in L2 (NVFP4, 64 experts 2048x1408, 64 tokens: 68 us, 74 without).
+// else stays in L2 (NVFP4, 64 experts 2048x1408, 64 tokens: 69 us, 75 without).
 // Two CTAs share an SM.  A CTA is bound by its own instructions, 0.2-0.4 us a K step of 16 KB (the MMA thread,
 // and the warps that turn exponents into scales), an SM draws a step from memory in 0.35 us, and a kernel's
-// first and last microseconds have one CTA's latencies.  One CTA per SM with twice the stages: 165 us against 142
-// (MoE, NVFP4, 8 experts 4096x14336, 64 tokens), 33 against 27.5 (linear, MXFP8, 61x4096->28672), within 3%
+// first and last microseconds have one CTA's latencies.  One CTA per SM with twice the stages: 200 us against 158
+// (MoE, NVFP4, 8 experts 4096x14336, 64 tokens), 28.2 against 26.5 (linear, MXFP8, 61x4096->28672), within 6%
 // for 1 to 16 tokens (dec_layout says where it is used all the same).
 // Measured (replayed graph, every call on other weights; share of the 6.77 TB/s a copy reaches):
-//   MoE 8 experts 4096x14336, k 2    MXFP8  1 token 66.5 us (81%), 16 224 (96%), 64 229 (94%)
-//                                    NVFP4  1 token 42.1 us (70%), 16 129 (91%), 64 142 (82%)
-//   MoE 64 experts 2048x1408, k 8    MXFP8  1 token 24.1 us (44%), 8 66.5 (84%), 64 101.5 (83%)
-//                                    NVFP4  1 token 19.6 us (29%), 8 45.0 (68%), 64 68.0 (68%)
-//   linear 4096->28672               MXFP8  1 token 22.6 us (79%), 61 27.1 (68%)
-//                                    NVFP4  1 token 14.6 us (67%), 61 21.6 (48%)
+//   MoE 8 experts 4096x14336, k 2    MXFP8  1 token 67.1 us (80%), 16 224 (96%), 64 229 (94%)
+//                                    NVFP4  1 token 42.5 us (69%), 16 130 (90%), 64 144 to 159 (74 to 82%: by how the
+//                                           tokens fall into groups of 16)
+//   MoE 64 experts 2048x1408, k 8    MXFP8  1 token 24.1 us (44%), 8 67.1 (84%), 64 101.6 (83%)
+//                                    NVFP4  1 token 20.7 us (28%), 8 45.7 (67%), 64 69.9 (66%)
+//   linear 4096->28672               MXFP8  1 token 22.7 us (79%), 61 27.3 (68%)
+//                                    NVFP4  1 token 14.7 us (67%), 61 21.5 (48%)
 //   linear 1x4096->4096              MXFP8  8.5 us, NVFP4 7.5: launch, columns, first weights, parts, in a row
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -89,7 +90,7 @@ enum DecMode { DEC_UP = 0, DEC_DOWN = 1, DEC_LINEAR = 2 };
 enum DecFmt { DEC_MX = 0, DEC_NV = 1 };
 
 // Warp 0 copies, warp 1 issues MMAs, then come the warps that write the columns' scales (they take turns), and four
-// for the epilogue.  Linears have three for the scales (NVFP4, 61x4096->28672: 21.5 us, 25.5 with two; elsewhere the
+// for the epilogue.  Linears have three for the scales (NVFP4, 61x4096->28672: 21.7 us, 25.8 with two; elsewhere the
 // same); UP needs an even number, and its registers leave room for two.
 constexpr int dec_scale_warps(int mode) { return mode == DEC_LINEAR ? 3 : 2; }
 constexpr int dec_threads(int mode) { return 32 * (2 + dec_scale_warps(mode) + 4); }
@@ -547,8 +548,9 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
   const int su = UP ? 2 * p.steps : p.steps;                    // steps of a unit
   const int units = MOE ? *s_nact * p.tiles : p.tiles;
   // Every CTA takes the same number of whole units; the units left over are shared, each by as many CTAs as fit
-  // (and find MIN_STEPS steps).  The share comes first, so that adding its parts up is hidden.  (Dealing the
-  // left-over steps out evenly, with two parts of units in a CTA, measured 5-15% slower: more sums of parts.)
+  // (and find MIN_STEPS steps).  The share comes first, so that adding its parts up is hidden.  per_unit is rounded
+  // down: 224 units and no whole ones leave 80 of 304 CTAs without work.  (Dealing the left-over steps out evenly, with
+  // two parts of units in a CTA, measured 5-15% slower while parts were added one by one; not measured again since.)
   const int slots = static_cast<int>(gridDim.x) / p.chunks, cta = static_cast<int>(blockIdx.x) / p.chunks;
   const int whole = units / slots, shared = units - whole * slots;
   // CTAs of a shared unit
@@ -989,7 +991,8 @@ __global__ void __launch_bounds__(dec_threads(MODE), 2) k_decode(const __grid_co
             const float gate = __shfl_sync(0xFFFFFFFFu, gates, c & 31);
             float h[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = gate * __fdividef(v[0][j], 1.0f + expf(-v[0][j])) * v[1][j];
+            for (int j = 0; j < 4; ++j)   // __fdividef: 2 ulp of 32 bits, far below what the pieces of h keep
+              h[j] = gate * __fdividef(v[0][j], 1.0f + expf(-v[0][j])) * v[1][j];
             uint32_t m = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);
@@ -1164,7 +1167,7 @@ bool dec_layout(int fmt, int mode, int rows, int E, int max_active, bool many, D
   L.stages = std::min(DEC_MAX_STAGES, (L.smem - fixed) / stage);
   L.tmem_cols = L.smem == DEC_SMEM_HALF ? DEC_TMEM_HALF : DEC_TMEM_FULL;
   // Two buffers of accumulators, where that leaves three sets of scales: the next unit's MMAs start while one is read
-  // (NVFP4, 61x4096->28672: 21.5 us with, 24.8 without; fewer sets would hold up every step instead).
+  // (NVFP4, 61x4096->28672: 21.7 us with, 25.1 without; fewer sets would hold up every step instead).
   for (L.acc_two = 1; L.acc_two >= 0; --L.acc_two) {
     L.sf_col = (mode == DEC_UP ? 2 : 1) * n << L.acc_two;
     L.sf_sets = std::min(L.stages, (static_cast<int>(L.tmem_cols) - L.sf_col) / L.sf_cols);
