@@ -397,7 +397,8 @@ int nvfp4_grouped_mlp_fwd(const void* x_sorted, int64_t R, int64_t H, int64_t F,
  *                  (a block more than 2^17 below the row's largest keeps fewer digits, one 2^31 below none).
  * Blocks whose largest magnitude is below 2^-100 are written as if it were 2^-100.  Results do not
  * depend on timing.  A token with a non-finite x gives non-finite values in its own row only; weights
- * must be finite.
+ * must be finite.  The kernels run on the current device, to which all pointers and the stream
+ * have to belong (for the junction below too).
  *
  * moe_decode_fwd -- a whole MoE layer, from the router's choices to the combined output:
  *     out[t] = sum_j gate[t,j] W2[e] ( silu(W1[e, 0:F] x_t) * (W1[e, F:2F] x_t) ),  e = experts[t,j]
