@@ -123,7 +123,7 @@ int grouped_mlp_fwd(const void* x_sorted, int64_t R, int64_t H, int64_t F, int E
 /*
  * Dispatch and combine around the grouped MLP (page section "Dense vs. MoE scaling": each token
  * uses a few of the experts; item 1: GroupedLinear runs on tokens gathered per expert).  The
- * router (a small GEMM + top-k) is not part of this library: its choices arrive as expert ids.
+ * router's choices arrive as expert ids (moe_route_fwd makes them from its logits).
  *
  * moe_permute -- stable sort of the router's (token, slot) choices by expert, on the device.
  *   experts      (device) int32 [T, k]: expert of slot j of token t, in [0, E).
@@ -475,6 +475,88 @@ int residual_norm_bwd(const void* dn, const void* dres_out, const void* y, const
                       const float* w_post, const float* gate, const float* w_pre, int64_t T, int64_t H, int res_dtype,
                       int gate_kind, int post_norm, float res_scale, void* dy, void* dres, float* dw_post,
                       float* dgate, float* dw_pre, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The router's decisions, and their gradient.  With logits l [T, E] (the router's linear is the
+ * caller's), of N tokens that take part (token_mask set, some logit above -inf):
+ *     lse_t = log sum_e exp(l_te),  p_te = exp(l_te - lse_t)
+ *     choices of t: its k largest logits above -inf, the lower expert first among equals
+ *     gates_tj = p of choice j, with normalize divided by the sum over the token's choices
+ *     counts_e = choices of expert e,  prob_sum_e = sum_t p_te
+ *     losses[0] = E sum_e counts_e / (N k) * prob_sum_e / N        (balance: 1 if all are equal)
+ *     losses[1] = sum_t lse_t^2 / N                                (the logits' scale)
+ * moe_route_fwd
+ *   logits     (device) [T, E], logits_dtype MOE_LOGITS_BF16 or MOE_LOGITS_F32.  A logit of -inf closes
+ *              an expert to a token.  A token with a NaN or +inf logit takes part without choices and
+ *              makes lse, prob_sum and losses[1] NaN.
+ *   token_mask (device) bytes [T], 0: the token takes no part whatever its logits hold; or NULL.
+ *   experts    (device, out) int32 [T, k], gates (device, out) float [T, k], largest first.  Where there
+ *              is no choice (the token takes no part, or fewer than k experts are open) the gate is 0 and
+ *              the id -1 (spread 0: a dropped choice of moe_decode_fwd) or (t*k + j) % E (spread 1: every
+ *              slot has a row, as moe_permute and the grouped calls need it; its gate of 0 makes the row
+ *              zeros).
+ *   lse        (device, out) float [T]; -inf where the token takes no part.
+ *   counts     (device, out) int32 [E + 1]: choices per expert, then N.
+ *   prob_sum   (device, out) float [E].   losses (device, out) float [2].
+ *   workspace  moe_route_workspace_size(T, E, k) bytes, 16-byte aligned (unused for few tokens).
+ * moe_route_bwd -- the logits' gradient (counts are constants):
+ *   logits, experts, gates, lse, counts, normalize   as the forward had or wrote them; counts may be sums
+ *              over several batches (all E + 1 of them: the losses' gradient is then that of the whole).
+ *   dgates     (device) float gradient of the gates: [T, k], or with row_of_slot (moe_permute) [T*k] in the
+ *              sorted rows' order, as grouped_mlp_bwd writes it; or NULL for 0.  Slots of gate 0 pass
+ *              nothing on, whatever their place holds, nor do row ids outside [0, T*k).
+ *   dprob_sum  (device) float [E] gradient of prob_sum, or NULL for 0.
+ *   dlosses    (device) float [2] gradient of losses, or NULL for 0.
+ *   dlogits    (device, out) [T, E] in the logits' type; 0 where the token takes no part.
+ * Sums are fp32 in an order that depends on T, E and the device only.  Requirements: T >= 0,
+ * 1 <= E <= 1024, 1 <= k <= E, T*k < 2^31 (otherwise MXFP8_ERR_INVALID_ARG); k <= 32 (otherwise
+ * MXFP8_ERR_UNSUPPORTED); pointers aligned to their elements.  No device-side errors.
+ */
+enum { MOE_LOGITS_BF16 = 0, MOE_LOGITS_F32 = 1 };
+size_t moe_route_workspace_size(int64_t T, int E, int k);
+int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k, const uint8_t* token_mask,
+                  int normalize, int spread, int32_t* experts, float* gates, float* lse, int32_t* counts,
+                  float* prob_sum, float* losses, void* workspace, size_t workspace_bytes, void* stream);
+int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k, const int32_t* experts,
+                  const float* gates, const float* lse, const int32_t* counts, const float* dgates,
+                  const int32_t* row_of_slot, const float* dprob_sum, const float* dlosses, int normalize,
+                  void* dlogits, void* stream);
+
+/*
+ * Softmax cross entropy of a linear layer over a large vocabulary, without the logits in memory:
+ *     z_tv = x_t . w_v (fp32),  lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_{t, targets_t}
+ * linear_cross_entropy_fwd
+ *   x        (device) bf16 [T, H].     w (device) bf16 [V, H].
+ *   targets  (device) [T], int32 (wide_targets 0) or int64 (1).  A negative target is a row that takes no
+ *            part (padding, a prompt): its loss is 0.  One >= V makes the loss NaN and is reported
+ *            (MXFP8_ERR_INVALID_ARG from mxfp8_check_device_error).
+ *   loss, lse (device, out) float [T]; lse is written for every row.
+ *   workspace linear_cross_entropy_workspace_size(T, H, V) bytes, 256-byte aligned; its first 4 bytes
+ *            are the error word.  Nothing in it needs to be initialised or kept.  Not shared by two
+ *            calls in flight.
+ * linear_cross_entropy_bwd -- gradients of x and w from those of loss and lse:
+ *     dz_tv = (dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = targets_t]  (rounded to bf16)
+ *     dx_t = sum_v dz_tv w_v,  dw_v = sum_t dz_tv x_t
+ *   dloss    (device) float [T].       dlse (device) float [T], or NULL for 0 (a loss on the logits' scale).
+ *   x, w, targets, lse                 as the forward had or wrote them.
+ *   dx       (device, out) bf16 [T, H].   dw (device, out) bf16 [V, H].  Both are fully overwritten.  A row
+ *            without a target (negative or >= V) passes nothing on, whatever its x, lse, dloss and dlse hold;
+ *            its dx is 0.
+ *   workspace linear_cross_entropy_bwd_workspace_size(T, H, V) bytes, as above (packed rows, one piece of
+ *            dz of at most 2^27 elements where T is up to 65536, parts of dx).
+ * Results do not depend on timing.  Requirements: T >= 0, H > 0, V > 0 (otherwise
+ * MXFP8_ERR_INVALID_ARG); H % 8 == 0, H <= 2^20, T <= 2^24, V <= 2^28, fewer than 2^30 tiles of 128 x 128
+ * logits (otherwise MXFP8_ERR_UNSUPPORTED); x, w, dx, dw 16-byte aligned, the others to their elements.
+ * T == 0: dw is zeros.
+ */
+size_t linear_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V);
+int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, int wide_targets, int64_t T, int64_t H,
+                             int64_t V, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream);
+size_t linear_cross_entropy_bwd_workspace_size(int64_t T, int64_t H, int64_t V);
+int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* x, const void* w, const void* targets,
+                             int wide_targets, const float* lse, int64_t T, int64_t H, int64_t V, void* dx, void* dw,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* mxfp8_mma_peak -- measurement aid, with no counterpart on the pages: the rate of the
  * block-scaled tensor-core instruction this library's GEMMs are built on, on the device at hand

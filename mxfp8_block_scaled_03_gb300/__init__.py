@@ -20,6 +20,10 @@ approaches, items 1-3):
                      same weights.
   residual_norm_fwd / residual_norm_bwd
                      the norms behind and before a block with its gate and the scaled residual.
+  moe_route_fwd / moe_route_bwd
+                     the router's choices, weights, counts per expert and losses from its logits.
+  linear_cross_entropy_fwd / linear_cross_entropy_bwd
+                     the loss of a linear layer over a large vocabulary, without its logits in memory.
 """
 from __future__ import annotations
 
@@ -42,6 +46,8 @@ __all__ = [
     "nvfp4_grouped_mlp_workspace_layout", "nvfp4_grouped_mlp_fwd", "moe_decode_workspace_size", "moe_decode_fwd",
     "nvfp4_moe_decode_fwd", "matvec_workspace_size", "mxfp8_matvec", "nvfp4_matvec",
     "residual_norm_fwd", "residual_norm_bwd", "residual_norm_bwd_workspace_size",
+    "moe_route_workspace_size", "moe_route_fwd", "moe_route_bwd", "linear_cross_entropy_workspace_size",
+    "linear_cross_entropy_fwd", "linear_cross_entropy_bwd_workspace_size", "linear_cross_entropy_bwd",
 ]
 
 ROWWISE = 1
@@ -156,6 +162,20 @@ def lib() -> ctypes.CDLL:
             L.residual_norm_bwd_workspace_size.argtypes = [i64, i64]
             L.residual_norm_bwd.restype = i32
             L.residual_norm_bwd.argtypes = [P, P, P, P, P, P, P, P, i64, i64, i32, i32, i32, f32, P, P, P, P, P, P, sz, P]
+            L.moe_route_workspace_size.restype = sz
+            L.moe_route_workspace_size.argtypes = [i64, i32, i32]
+            L.moe_route_fwd.restype = i32
+            L.moe_route_fwd.argtypes = [P, i32, i64, i32, i32, P, i32, i32, P, P, P, P, P, P, P, sz, P]
+            L.moe_route_bwd.restype = i32
+            L.moe_route_bwd.argtypes = [P, i32, i64, i32, i32, P, P, P, P, P, P, P, P, i32, P, P]
+            L.linear_cross_entropy_workspace_size.restype = sz
+            L.linear_cross_entropy_workspace_size.argtypes = [i64, i64, i64]
+            L.linear_cross_entropy_fwd.restype = i32
+            L.linear_cross_entropy_fwd.argtypes = [P, P, P, i32, i64, i64, i64, P, P, P, sz, P]
+            L.linear_cross_entropy_bwd_workspace_size.restype = sz
+            L.linear_cross_entropy_bwd_workspace_size.argtypes = [i64, i64, i64]
+            L.linear_cross_entropy_bwd.restype = i32
+            L.linear_cross_entropy_bwd.argtypes = [P, P, P, P, P, i32, P, i64, i64, i64, P, P, P, sz, P]
             _lib = L
     return _lib
 
@@ -769,6 +789,166 @@ def residual_norm_bwd(dn, dres_out, y, res_out, stats, w_post=None, gate=None, w
     if st != OK:
         raise MXFP8Error(st, "residual_norm_bwd")
     return dy, dres, dw_post, dgate, dw_pre
+
+
+def moe_route_workspace_size(T: int, E: int, k: int) -> int:
+    return int(lib().moe_route_workspace_size(T, E, k))
+
+
+def _logits(logits, name: str, dev: int):
+    """(T, E, code of the type, pointer) of a router's logits."""
+    import torch
+    if logits.dtype is not torch.bfloat16 and logits.dtype is not torch.float32 or logits.dim() != 2:
+        raise ValueError(f"{name}: expected bfloat16 or float32 [T, E], got {logits.dtype}, {tuple(logits.shape)}")
+    T, E = logits.shape
+    return T, E, 0 if logits.dtype is torch.bfloat16 else 1, _need(logits, logits.dtype, (T, E), name, dev)
+
+
+def moe_route_fwd(logits, k: int, token_mask=None, normalize: bool = True, spread: bool = False, out=None,
+                  workspace=None, stream=None):
+    """A router's decisions from its logits [T, E] (bf16 or float32): each token's k largest, their softmax weights
+    (with `normalize` over the chosen alone), the counts, and the two losses.
+
+    token_mask bool or uint8 [T]: tokens at 0 take no part.  A logit of -inf closes an expert.  Slots without a
+    choice have gate 0 and id -1, or with `spread` (t * k + j) % E: moe_decode_fwd takes the former, moe_permute
+    needs the latter.  Returns (experts int32 [T, k], gates float32 [T, k], lse float32 [T], counts int32 [E + 1]: choices
+    per expert and tokens that take part, prob_sum float32 [E], losses float32 [2]: balance and mean of lse^2); `out` may
+    pass the six.  `workspace`: uint8 CUDA tensor, moe_route_workspace_size bytes."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_route_fwd(logits, k, token_mask, normalize, spread, out, workspace)
+    f32, i32 = torch.float32, torch.int32
+    dev, current = _place(logits, "logits")
+    T, E, code, pl = _logits(logits, "logits", dev)
+    pm = None
+    if token_mask is not None:
+        if token_mask.dtype is not torch.bool and token_mask.dtype is not torch.uint8:
+            raise ValueError(f"token_mask: expected bool or uint8, got {token_mask.dtype}")
+        pm = _need(token_mask, token_mask.dtype, (T,), "token_mask", dev)
+    kinds = ((i32, (T, k)), (f32, (T, k)), (f32, (T,)), (i32, (E + 1,)), (f32, (E,)), (f32, (2,)))
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=dtype, device=logits.device) for dtype, shape in kinds)
+        ptrs = [t.data_ptr() for t in out]
+    else:
+        names = ("experts", "gates", "lse", "counts", "prob_sum", "losses")
+        ptrs = [_need(t, dtype, shape, name, dev) for t, (dtype, shape), name in zip(out, kinds, names)]
+    if workspace is None:
+        workspace = torch.empty(max(16, moe_route_workspace_size(T, E, k)), dtype=torch.uint8, device=logits.device)
+    st = lib().moe_route_fwd(pl, code, T, E, k, pm, 1 if normalize else 0, 1 if spread else 0, *ptrs,
+                             _need(workspace, torch.uint8, 0, "workspace", dev), workspace.numel(), current)
+    if st != OK:
+        raise MXFP8Error(st, "moe_route_fwd")
+    return tuple(out)
+
+
+def moe_route_bwd(logits, experts, gates, lse, counts, dgates=None, dlosses=None, row_of_slot=None, dprob_sum=None,
+                  normalize: bool = True, out=None, stream=None):
+    """The gradient of moe_route_fwd's logits (in their type) from those of the gates (float32 [T, k]; with row_of_slot
+    from moe_permute [T * k] in sorted-row order, as grouped_mlp_bwd gives it), of the losses (float32 [2]) and of
+    prob_sum (float32 [E]); None: 0.  logits, experts, gates, lse, counts, normalize as the forward had or wrote
+    them; counts may be the sum over several batches."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_route_bwd(logits, experts, gates, lse, counts, dgates, dlosses, row_of_slot, dprob_sum, normalize,
+                                 out)
+    f32, i32 = torch.float32, torch.int32
+    dev, current = _place(logits, "logits")
+    T, E, code, pl = _logits(logits, "logits", dev)
+    k = experts.shape[1]
+    if row_of_slot is not None and dgates is None:
+        raise ValueError("row_of_slot without dgates")
+    args = (_need(experts, i32, (T, k), "experts", dev), _need(gates, f32, (T, k), "gates", dev),
+            _need(lse, f32, (T,), "lse", dev), _need(counts, i32, (E + 1,), "counts", dev),
+            None if dgates is None else _need(dgates, f32, (T, k) if row_of_slot is None else (T * k,), "dgates", dev),
+            None if row_of_slot is None else _need(row_of_slot, i32, (T, k), "row_of_slot", dev),
+            None if dprob_sum is None else _need(dprob_sum, f32, (E,), "dprob_sum", dev),
+            None if dlosses is None else _need(dlosses, f32, (2,), "dlosses", dev))
+    if out is None:
+        out = torch.empty_like(logits)
+        po = out.data_ptr()
+    else:
+        po = _need(out, logits.dtype, (T, E), "out", dev)
+    st = lib().moe_route_bwd(pl, code, T, E, k, *args, 1 if normalize else 0, po, current)
+    if st != OK:
+        raise MXFP8Error(st, "moe_route_bwd")
+    return out
+
+
+def linear_cross_entropy_workspace_size(T: int, H: int, V: int) -> int:
+    return int(lib().linear_cross_entropy_workspace_size(T, H, V))
+
+
+def linear_cross_entropy_bwd_workspace_size(T: int, H: int, V: int) -> int:
+    return int(lib().linear_cross_entropy_bwd_workspace_size(T, H, V))
+
+
+def _lce_args(x, w, targets):
+    """(device, stream, T, H, V, x pointer, w pointer, targets pointer, 1 for int64 targets)."""
+    import torch
+    dev, current = _place(x, "x")
+    T, H = x.shape
+    V = w.shape[0]
+    if targets.dtype is not torch.int32 and targets.dtype is not torch.int64:
+        raise ValueError(f"targets: expected int32 or int64, got {targets.dtype}")
+    return (dev, current, T, H, V, _need(x, torch.bfloat16, (T, H), "x", dev),
+            _need(w, torch.bfloat16, (V, H), "w", dev), _need(targets, targets.dtype, (T,), "targets", dev),
+            1 if targets.dtype is torch.int64 else 0)
+
+
+def linear_cross_entropy_fwd(x, w, targets, out=None, workspace=None, stream=None):
+    """Cross entropy of softmax(x W^T) against targets, without the logits in memory.
+
+    x bf16 [T, H]; w bf16 [V, H]; targets int32 or int64 [T], negative: the row takes no part (its loss is 0).  Returns
+    (loss float32 [T], lse float32 [T]); `out` may pass the two.  `workspace` (uint8 CUDA tensor,
+    linear_cross_entropy_workspace_size bytes) is allocated here when not given, and its error word is lost with it: a
+    target >= V then shows as a NaN loss only."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_cross_entropy_fwd(x, w, targets, out, workspace)
+    f32, u8 = torch.float32, torch.uint8
+    dev, current, T, H, V, px, pw, pt, wide = _lce_args(x, w, targets)
+    if out is None:
+        out = (torch.empty(T, dtype=f32, device=x.device), torch.empty(T, dtype=f32, device=x.device))
+        ptrs = [t.data_ptr() for t in out]
+    else:
+        ptrs = [_need(t, f32, (T,), name, dev) for t, name in zip(out, ("loss", "lse"))]
+    if workspace is None:
+        workspace = torch.empty(max(256, linear_cross_entropy_workspace_size(T, H, V)), dtype=u8, device=x.device)
+    st = lib().linear_cross_entropy_fwd(px, pw, pt, wide, T, H, V, *ptrs, _need(workspace, u8, 256, "workspace", dev),
+                                        workspace.numel(), current)
+    if st != OK:
+        raise MXFP8Error(st, "linear_cross_entropy_fwd")
+    return tuple(out)
+
+
+def linear_cross_entropy_bwd(dloss, x, w, targets, lse, dlse=None, out=None, workspace=None, stream=None):
+    """Gradients of linear_cross_entropy_fwd from those of loss (float32 [T]) and of lse (float32 [T], or None for 0);
+    x, w, targets, lse as the forward had or wrote them.  Rows without a target pass nothing on, whatever they hold.
+    Returns (dx bf16 [T, H], dw bf16 [V, H]); `out` may pass the two.  `workspace`:
+    linear_cross_entropy_bwd_workspace_size bytes, as for the forward."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_cross_entropy_bwd(dloss, x, w, targets, lse, dlse, out, workspace)
+    f32, u8 = torch.float32, torch.uint8
+    dev, current, T, H, V, px, pw, pt, wide = _lce_args(x, w, targets)
+    pd, ps = _need(dloss, f32, (T,), "dloss", dev), _need(lse, f32, (T,), "lse", dev)
+    pe = None if dlse is None else _need(dlse, f32, (T,), "dlse", dev)
+    if out is None:
+        out = torch.empty_like(x), torch.empty_like(w)
+        ptrs = [t.data_ptr() for t in out]
+    else:
+        ptrs = [_need(out[0], torch.bfloat16, (T, H), "dx", dev), _need(out[1], torch.bfloat16, (V, H), "dw", dev)]
+    if workspace is None:
+        workspace = torch.empty(max(256, linear_cross_entropy_bwd_workspace_size(T, H, V)), dtype=u8, device=x.device)
+    st = lib().linear_cross_entropy_bwd(pd, pe, px, pw, pt, wide, ps, T, H, V, *ptrs,
+                                        _need(workspace, u8, 256, "workspace", dev), workspace.numel(), current)
+    if st != OK:
+        raise MXFP8Error(st, "linear_cross_entropy_bwd")
+    return tuple(out)
 
 
 def mxfp8_mma_peak(iters: int, workspace, fmt: int = 0, stream=None) -> int:

@@ -323,7 +323,7 @@ int mxfp8_check_device_error(const void* workspace, void* stream, uint32_t* flag
   if (flags) *flags = w;
   if (w & ERR_TIMEOUT_MASK) return MXFP8_ERR_DEVICE_TIMEOUT;
   if (w & (ERR_SPLIT_SUM | ERR_SPLIT_NEGATIVE)) return MXFP8_ERR_SPLIT_MISMATCH;
-  if (w & (ERR_EXPERT_RANGE | ERR_TOKEN_RANGE)) return MXFP8_ERR_INVALID_ARG;
+  if (w & (ERR_EXPERT_RANGE | ERR_TOKEN_RANGE | ERR_TARGET_RANGE)) return MXFP8_ERR_INVALID_ARG;
   return MXFP8_OK;
 }
 

@@ -1,0 +1,957 @@
+// cross_entropy.cu -- softmax cross entropy of a linear layer over a large vocabulary, and its gradient, without the
+// logits in memory.
+//
+// For a row x_t with target y_t and the vocabulary's rows w_v (all bf16), z_tv = x_t . w_v in 32 bits:
+//   lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_{t, y_t}
+// and for gradients dloss_t and dlse_t:
+//   dz_tv = (dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = y_t]
+//   dx_t = sum_v dz_tv w_v,   dw_v = sum_t dz_tv x_t
+// A row with a negative target takes no part: loss 0, no gradient, whatever its x holds.
+//
+// What bounds it: the tensor cores (forward 2 T H V operations, backward 6 T H V: the logits again, then the two
+// products), and for few rows the bytes of w.  One GEMM kernel, k_ce_gemm, does all four products on tcgen05 with
+// bf16 operands and fp32 accumulators in TMEM; its modes differ in the operands' layout and in the epilogue:
+//   CE_LSE  x w^T      -> per row and column tile: the largest logit and the sum of exponentials; the target's logit
+//   CE_DZ   x w^T      -> dz of one piece of the vocabulary, bf16, in the workspace
+//   CE_DW   dz^T x     -> dw of the piece            (both operands contract over their rows: M- and N-major tiles)
+//   CE_DX   dz w       -> dx, in fp32 parts where the vocabulary has several pieces or is split over CTAs
+// The backward first packs the rows that take part, so that padding costs nothing and nothing it holds can reach
+// dw (0 * NaN).  dz is rounded to bf16 (by at most 2^-8 of its value): it is the operand of two products whose results
+// are rounded to bf16 as well.  It lives for one piece of the vocabulary only, of at most CE_DZ_ELEMS elements.
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "mx_device.cuh"
+#include "mx_internal.h"
+#include "mxfp8moe.h"
+
+namespace mx {
+namespace {
+
+constexpr int CE_BK = 64;                          // K per stage: 64 bf16 = one 128-byte swizzle row
+constexpr int CE_HALF = 128;                       // rows of A and of B that a CTA stages
+constexpr int CE_STAGES = 6;
+constexpr int CE_OP_BYTES = CE_HALF * CE_BK * 2;   // 16 KB per operand
+constexpr int CE_STAGE_BYTES = 2 * CE_OP_BYTES;
+constexpr int CE_THREADS = 384;
+constexpr int CE_WARP_PRODUCER = 0;
+constexpr int CE_WARP_MMA = 1;
+constexpr int CE_EPI_WARP0 = 4;
+constexpr int CE_EPI_WARPS = 8;
+constexpr uint32_t CE_BAR_EPI = 1;                 // hardware barrier of the epilogue warps
+constexpr int CE_BUF_BYTES = 2048;                 // a warp's staging tile: 32 rows x 32 bf16; two per warp
+constexpr int CE_EPI_BYTES = CE_EPI_WARPS * 2 * CE_BUF_BYTES;
+constexpr int CE_DATA_BYTES = CE_STAGES * CE_STAGE_BYTES;
+constexpr int CE_BAR_OFFSET = CE_DATA_BYTES + CE_EPI_BYTES;
+constexpr int CE_SMEM_BYTES = CE_BAR_OFFSET + (2 * CE_STAGES + 5) * 8 + 8 + 1024;
+static_assert(CE_SMEM_BYTES <= 232448, "shared memory budget");
+constexpr int64_t CE_DZ_ELEMS = int64_t(1) << 27;  // most elements of dz at a time (256 MB)
+constexpr int64_t CE_MIN_PIECE = 2048;             // vocabulary entries of a piece, whatever the rows
+constexpr uint64_t CE_WAIT_NS = 2000000000ull;     // 2 s per individual wait
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+enum { CE_LSE = 0, CE_DZ = 1, CE_DW = 2, CE_DX = 3 };
+
+struct CeMeta {
+  uint32_t error;
+  int32_t n;          // rows that take part (backward)
+  int32_t reserved[62];
+};
+static_assert(sizeof(CeMeta) == 256, "header");
+
+struct CeParams {
+  CeMeta* meta;
+  const int32_t* row_map;      // backward: row of packed row i, then the rows that take no part
+  int rows;                    // CE_LSE: T
+  int V, v0, vcols;            // vocabulary; first entry and entries of this piece
+  int H;
+  int group_m;                 // row tiles that share a column tile before the next one is taken
+  int splits, split_steps;     // CE_DX: K steps of each share of the piece
+  const void* targets;
+  int wide_targets;
+  const float* lse;
+  const float* dloss;
+  const float* dlse;
+  float2* part;                // CE_LSE: [2 * column tiles][pitch] (largest logit, sum) in base 2
+  float* zy;                   // CE_LSE: the target's logit
+  int64_t pitch;
+  float* acc;                  // CE_DX: [splits][pitch][H] fp32, or NULL: dx is written directly
+  int acc_add;
+  int d_rows, d_cols;          // CE_DZ, CE_DW: extent of the map that is stored to
+  uint16_t* dx;
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ int64_t ce_target(const CeParams& p, int64_t row) {
+  return p.wide_targets ? __ldg(static_cast<const long long*>(p.targets) + row)
+                        : static_cast<int64_t>(__ldg(static_cast<const int32_t*>(p.targets) + row));
+}
+
+// Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B, K-major unless the M / N major bits are set.
+__host__ __device__ constexpr uint32_t ce_idesc(uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) |
+         ((M >> 4) << 24);
+}
+// Shared memory descriptor of an M- or N-major operand in 128-byte swizzle: boxes of 64 elements x 64 rows of K
+// (8 KB apart: leading byte offset), groups of 8 rows of K 1024 bytes apart (stride byte offset).
+__device__ __forceinline__ uint64_t ce_sdesc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192 >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+template <int CG>
+__device__ __forceinline__ void ce_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+
+struct CeUnits {
+  int nm, nn, splits, steps;   // row tiles, column tiles, shares of K, K steps in all
+  int total;
+};
+template <int MODE, int CG>
+__device__ __forceinline__ CeUnits ce_units(const CeParams& p) {
+  constexpr int TILE = CE_HALF * CG;
+  auto up = [](int a, int b) { return (a + b - 1) / b; };
+  CeUnits c;
+  c.splits = 1;
+  if (MODE == CE_LSE) {
+    c.nm = up(p.rows, TILE);
+    c.nn = up(p.V, TILE);
+    c.steps = up(p.H, CE_BK);
+  } else if (MODE == CE_DZ) {
+    c.nm = up(p.meta->n, TILE);
+    c.nn = up(p.vcols, TILE);
+    c.steps = up(p.H, CE_BK);
+  } else if (MODE == CE_DW) {
+    c.nm = up(p.vcols, TILE);
+    c.nn = up(p.H, TILE);
+    c.steps = up(p.meta->n, CE_BK);
+  } else {
+    c.nm = up(p.meta->n, TILE);
+    c.nn = up(p.H, TILE);
+    c.steps = up(p.vcols, CE_BK);
+    c.splits = p.splits;
+  }
+  c.total = c.nm * c.nn * c.splits;
+  return c;
+}
+struct CeTile {
+  int m, n, split, k0, steps;  // row tile, column tile, share, first K step and their number
+};
+// Unit u: shares outermost, then groups of group_m row tiles, in each the row tiles of one column tile after another.
+template <int MODE>
+__device__ __forceinline__ CeTile ce_tile(int u, const CeUnits& c, const CeParams& p) {
+  CeTile t;
+  const int per = c.nm * c.nn;
+  t.split = MODE == CE_DX ? u / per : 0;
+  const int w0 = u - t.split * per;
+  const int g = w0 / (p.group_m * c.nn);
+  const int in_g = min(p.group_m, c.nm - g * p.group_m);
+  const int w = w0 - g * p.group_m * c.nn;
+  t.n = w / in_g;
+  t.m = g * p.group_m + (w - t.n * in_g);
+  t.k0 = MODE == CE_DX ? t.split * p.split_steps : 0;
+  t.steps = MODE == CE_DX ? min(p.split_steps, c.steps - t.k0) : c.steps;
+  return t;
+}
+
+// Bounded wait of one thread; a wait that runs out is reported and raises the abort flag of this CTA (and of its peer).
+template <int CG>
+__device__ __forceinline__ bool ce_wait(uint64_t* bar, uint32_t parity, bool cluster_scope, volatile int* abort,
+                                        uint32_t peer_abort, const CeParams& p, uint32_t err_bit) {
+  if (CG == 2 && cluster_scope ? mbar_wait_cluster_bounded(bar, parity, abort, p.timeout_ns)
+                               : mbar_wait_bounded(bar, parity, abort, p.timeout_ns))
+    return true;
+  atomicOr(&p.meta->error, err_bit);
+  *abort = 1;
+  if (CG == 2) st_remote_u32(peer_abort, 1u);
+  return false;
+}
+
+// CG = 1: a CTA computes tiles of 128 x 128.  CG = 2: a CTA pair computes tiles of 256 x 256, each CTA with 128 rows
+// of A and of B in its shared memory and 128 rows of the result in its TMEM.  Either way a stage is 32 KB per CTA and
+// the accumulators are double-buffered, so that an epilogue runs beside the next tile's products.
+template <int MODE, int CG>
+__global__ void __launch_bounds__(CE_THREADS, 1)
+    k_ce_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ CUtensorMap tmD, const CeParams p) {
+  constexpr bool A_MN = MODE == CE_DW, B_MN = MODE == CE_DW || MODE == CE_DX;
+  constexpr int TILE = CE_HALF * CG;
+  constexpr int NH = TILE / 2;                      // columns of an epilogue warp
+  constexpr uint32_t TMEM_COLS = 2 * TILE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + CE_BAR_OFFSET);
+  uint64_t* empty = full + CE_STAGES;
+  uint64_t* acc_full = empty + CE_STAGES;           // [2]
+  uint64_t* acc_empty = acc_full + 2;               // [2]
+  uint64_t* drained = acc_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0u;
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < CE_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], CG * CE_EPI_WARPS);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == CE_WARP_MMA) {
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(tmem_holder, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_holder, TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();                  // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const CeUnits units = ce_units<MODE, CG>(p);
+  const int first = CG == 2 ? static_cast<int>(cluster_index()) : static_cast<int>(blockIdx.x);
+  const int stride = CG == 2 ? static_cast<int>(cluster_count()) : static_cast<int>(gridDim.x);
+  const uint32_t peer_abort = CG == 2 ? map_to_cta(const_cast<int*>(abort_flag), rank ^ 1u) : 0u;
+  uint32_t prod_issued = 0;
+
+  if (warp == CE_WARP_PRODUCER) {
+    // ---------------- tile copies (every CTA its own; one lane) ----------------
+    if (lane == 0) {
+      const uint32_t leader_full = CG == 2 ? map_to_cta(full, 0) : 0u;
+      uint32_t issued_parity = 0;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = first; ok && u < units.total; u += stride) {
+        const CeTile t = ce_tile<MODE>(u, units, p);
+        const int a0 = t.m * TILE + CE_HALF * static_cast<int>(rank);
+        const int b0 = t.n * TILE + CE_HALF * static_cast<int>(rank);
+        for (int s = 0; s < t.steps; ++s) {
+          if (!ce_wait<CG>(&empty[stage], phase ^ 1u, false, abort_flag, peer_abort, p, ERR_TIMEOUT_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sA = smem + stage * CE_STAGE_BYTES;
+          uint8_t* sB = sA + CE_OP_BYTES;
+          const int k = (t.k0 + s) * CE_BK;
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+            if constexpr (CG == 2) tma_load_2d_pair(dst, map, leader_full + stage * 8, x, y);
+            else tma_load_2d(dst, map, &full[stage], x, y);
+          };
+          if (A_MN) {
+            load(sA, &tmA, a0, k);
+            load(sA + CE_OP_BYTES / 2, &tmA, a0 + 64, k);
+          } else {
+            load(sA, &tmA, k, a0);
+          }
+          // B rows: the vocabulary from v0 (logits), or K rows of it (dx)
+          if (B_MN) {
+            const int ky = MODE == CE_DX ? p.v0 + k : k;
+            load(sB, &tmB, b0, ky);
+            load(sB + CE_OP_BYTES / 2, &tmB, b0 + 64, ky);
+          } else {
+            load(sB, &tmB, k, p.v0 + b0);
+          }
+          if (leader) mbar_arrive_expect_tx(&full[stage], CG * CE_STAGE_BYTES);
+          prod_issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == CE_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Copies land before the CTA exits: the leader waits for its stages (their barriers count both CTAs' copies);
+      // the second CTA's wait for the leader is the pair's closing barriers below.
+      if (leader)
+        for (int s = 0; s < CE_STAGES; ++s)
+          if ((prod_issued >> s) & 1u)
+            if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
+              atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+    }
+    __syncwarp();
+  } else if (warp == CE_WARP_MMA && leader) {
+    // ---------------- MMA issuer (one lane of the leader) ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = ce_idesc(TILE, TILE, A_MN, B_MN);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool issued = false, ok = true;
+      for (int u = first; ok && u < units.total; u += stride) {
+        const CeTile t = ce_tile<MODE>(u, units, p);
+        if (t.steps == 0) continue;                 // no rows: the epilogue writes zeros without the accumulator
+        if (!ce_wait<CG>(&acc_empty[buf], acc_phase ^ 1u, true, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA)) break;
+        tc_fence_after();
+        for (int s = 0; s < t.steps; ++s) {
+          if (!ce_wait<CG>(&full[stage], phase, false, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + stage * CE_STAGE_BYTES), b0 = a0 + CE_OP_BYTES;
+#pragma unroll
+          for (int k = 0; k < CE_BK / 16; ++k) {
+            const uint64_t da = A_MN ? ce_sdesc_mn(a0 + 2048 * k) : sdesc_kmajor_sw128(a0 + 32 * k);
+            const uint64_t db = B_MN ? ce_sdesc_mn(b0 + 2048 * k) : sdesc_kmajor_sw128(b0 + 32 * k);
+            ce_mma<CG>(tmem + buf * TILE, da, db, idesc, (s | k) != 0 ? 1u : 0u);
+          }
+          if constexpr (CG == 2) tc_commit_pair_both(&empty[stage]);
+          else tc_commit(&empty[stage]);
+          issued = true;
+          if (++stage == CE_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if constexpr (CG == 2) tc_commit_pair_both(&acc_full[buf]);
+        else tc_commit(&acc_full[buf]);
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1u;
+      }
+      if (issued) {
+        if constexpr (CG == 2) tc_commit_pair_local(drained);
+        else tc_commit(drained);
+        if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= CE_EPI_WARP0) {
+    // ---------------- epilogue (every CTA its 128 rows) ----------------
+    const int quarter = warp & 3;
+    const int half = (warp - CE_EPI_WARP0) >> 2;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + NH * half;
+    uint8_t* wbuf = smem + CE_DATA_BYTES + (warp - CE_EPI_WARP0) * 2 * CE_BUF_BYTES;
+    const int n_rows = MODE == CE_LSE ? p.rows : MODE == CE_DW ? 0 : p.meta->n;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    for (int u = first; u < units.total; u += stride) {
+      const CeTile t = ce_tile<MODE>(u, units, p);
+      const int row0 = t.m * TILE + CE_HALF * static_cast<int>(rank) + quarter * 32;
+      const int row = row0 + lane;
+      const int col0 = t.n * TILE + NH * half;
+      // what the row needs besides its logits, before the wait
+      int y = -1;                                   // the target's column; outside every tile without one
+      float rate = 0.0f, hot = 0.0f, lse2 = 0.0f;
+      int src = 0;
+      if (MODE == CE_LSE && row < n_rows) {
+        const int64_t target = ce_target(p, row);
+        y = target < p.V ? static_cast<int>(max(target, int64_t(-1))) : -1;
+      }
+      if ((MODE == CE_DZ || MODE == CE_DX) && row < n_rows) src = __ldg(p.row_map + row);
+      if (MODE == CE_DZ && row < n_rows) {
+        y = static_cast<int>(ce_target(p, src)) - p.v0;
+        hot = __ldg(p.dloss + src);
+        rate = hot + (p.dlse != nullptr ? __ldg(p.dlse + src) : 0.0f);
+        lse2 = __ldg(p.lse + src) * LOG2E;
+      }
+      if (t.steps > 0) {
+        bool got = true;
+        if (warp == CE_EPI_WARP0 && lane == 0)
+          got = ce_wait<CG>(&acc_full[buf], acc_phase, false, abort_flag, peer_abort, p, ERR_TIMEOUT_EPILOGUE);
+        if (!group_and(CE_BAR_EPI, CE_EPI_WARPS * 32, got)) break;
+        tc_fence_after();
+      }
+      float m = -INFINITY, sum = 0.0f;              // CE_LSE, in base 2
+#pragma unroll 1
+      for (int c = 0; c < NH; c += 32) {
+        uint32_t v[32];
+        if (t.steps > 0) {
+          tmem_ld_32x32b_x32(t_row + buf * TILE + c, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+        if (c + 32 >= NH && t.steps > 0) {          // all of this warp's columns have been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 2) mbar_arrive_remote(map_to_cta(&acc_empty[buf], 0));
+            else mbar_arrive(&acc_empty[buf]);
+          }
+        }
+        const int col = col0 + c;
+        if constexpr (MODE == CE_LSE) {
+          if (y >= col && y < col + 32) {
+            const int at = y - col;
+            float zy = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i == at) zy = __uint_as_float(v[i]);
+            p.zy[row] = zy;
+          }
+          if (col + 32 > p.V) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col + i >= p.V) v[i] = 0xFF800000u;   // -inf
+          }
+          float top = __uint_as_float(v[0]);
+#pragma unroll
+          for (int i = 1; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+          const float m_new = fmaxf(m, top * LOG2E);
+          const float base = m_new == -INFINITY ? 0.0f : m_new;
+          float add = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) add += ex2(fmaf(__uint_as_float(v[i]), LOG2E, -base));
+          sum = sum * ex2(m - base) + add;
+          m = m_new;
+        } else if constexpr (MODE == CE_DZ || MODE == CE_DW) {
+          if constexpr (MODE == CE_DZ) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float d = rate * ex2(fmaf(__uint_as_float(v[i]), LOG2E, -lse2));
+              if (y == col + i) d -= hot;
+              v[i] = row < n_rows && col + i < p.vcols ? __float_as_uint(d) : 0u;
+            }
+          }
+          uint8_t* out = wbuf + ((c >> 5) & 1) * CE_BUF_BYTES;
+          if (lane == 0) bulk_wait_read_le1();      // the store that last used this buffer has read it
+          __syncwarp();
+          // row `lane`: four 16-byte chunks, 64B swizzle (chunk j of row i at j ^ ((i >> 1) & 3))
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 o;
+            o.x = pack_bf16x2(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
+            o.y = pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
+            o.z = pack_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
+            o.w = pack_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
+            *reinterpret_cast<uint4*>(out + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) = o;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.d_rows && col < p.d_cols) tma_store_2d(&tmD, out, col, row0);   // clipped at the edges
+            bulk_commit_group();
+          }
+        } else if (row < n_rows) {                  // CE_DX
+          if (p.acc == nullptr) {
+            uint16_t* dst = p.dx + static_cast<int64_t>(src) * p.H + col;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              if (col + j < p.H) {
+                uint4 o;
+                o.x = pack_bf16x2(__uint_as_float(v[j + 0]), __uint_as_float(v[j + 1]));
+                o.y = pack_bf16x2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                o.z = pack_bf16x2(__uint_as_float(v[j + 4]), __uint_as_float(v[j + 5]));
+                o.w = pack_bf16x2(__uint_as_float(v[j + 6]), __uint_as_float(v[j + 7]));
+                *reinterpret_cast<uint4*>(dst + j) = o;
+              }
+          } else {
+            float* dst = p.acc + (t.split * p.pitch + row) * p.H + col;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              if (col + j < p.H) {
+                if (p.acc_add) {
+                  const float4 a = *reinterpret_cast<const float4*>(dst + j);
+                  const float4 b = *reinterpret_cast<const float4*>(dst + j + 4);
+                  const float old[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) v[j + i] = __float_as_uint(__uint_as_float(v[j + i]) + old[i]);
+                }
+                st_global_32B(dst + j, make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]),
+                              make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]));
+              }
+          }
+        }
+      }
+      if (MODE == CE_LSE && row < n_rows) p.part[(2 * t.n + half) * p.pitch + row] = make_float2(m, sum);
+      if (t.steps > 0) {
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1u;
+      }
+    }
+    if ((MODE == CE_DZ || MODE == CE_DW) && lane == 0) bulk_wait_all();   // stores complete before exit
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) {
+    cluster_sync_all();   // all pair MMAs are done and no remote arrive targets an exited CTA
+    // After an abort the second CTA's copies may still be in flight towards the leader's barriers: they depend on
+    // nothing but memory and get a fixed 200 us to land before either CTA exits.
+    if (!leader && warp == CE_WARP_PRODUCER && lane == 0 && prod_issued != 0 && *abort_flag) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 200000ull) {
+      }
+    }
+    cluster_sync_all();
+  }
+  if (warp == CE_WARP_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    if constexpr (CG == 2) tmem_dealloc_pair(tmem, TMEM_COLS);
+    else tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the parts of each row: 256 threads take `width` rows (a power of two up to 32), 256 / width shares of the parts.
+__global__ void __launch_bounds__(256) k_ce_merge(const CeParams p, int parts, int width, float* loss, float* lse) {
+  __shared__ float2 s[256];
+  const int r = threadIdx.x % width, share = threadIdx.x / width, shares = 256 / width;
+  const int row = blockIdx.x * width + r;
+  float m = -INFINITY, sum = 0.0f;
+  auto join = [&](float2 o) {
+    const float m_new = fmaxf(m, o.x);
+    const float base = m_new == -INFINITY ? 0.0f : m_new;
+    sum = sum * ex2(m - base) + o.y * ex2(o.x - base);
+    m = m_new;
+  };
+  if (row < p.rows) {
+#pragma unroll 4
+    for (int i = share; i < parts; i += shares) join(__ldcs(p.part + i * p.pitch + row));
+  }
+  s[threadIdx.x] = make_float2(m, sum);
+  for (int o = shares / 2; o > 0; o >>= 1) {
+    __syncthreads();
+    if (share < o) {
+      join(s[threadIdx.x + o * width]);
+      s[threadIdx.x] = make_float2(m, sum);
+    }
+  }
+  if (share == 0 && row < p.rows) {
+    const float total = (m + log2f(sum)) * LN2;
+    lse[row] = total;
+    const int64_t y = ce_target(p, row);
+    float l = 0.0f;
+    if (y >= p.V) {
+      l = NAN;
+      atomicOr(&p.meta->error, ERR_TARGET_RANGE);
+    } else if (y >= 0) {
+      l = total - p.zy[row];
+    }
+    loss[row] = l;
+  }
+}
+
+// row_map: the rows that take part in order, then the others in order; their number.  One CTA.
+__global__ void __launch_bounds__(1024) k_ce_rows(const CeParams p, int64_t T, int32_t* row_map) {
+  __shared__ int s_warp[32];
+  __shared__ int s_bad;
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  const int per = static_cast<int>((T + 1023) / 1024);
+  const int64_t t0 = static_cast<int64_t>(threadIdx.x) * per, t1 = min(T, t0 + per);
+  int mine = 0;
+  for (int64_t t = t0; t < t1; ++t) {
+    const int64_t y = ce_target(p, t);
+    mine += y >= 0 && y < p.V;
+    if (y >= p.V) s_bad = 1;
+  }
+  int scan = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if ((threadIdx.x & 31) >= o) scan += a;
+  }
+  if ((threadIdx.x & 31) == 31) s_warp[threadIdx.x >> 5] = scan;
+  __syncthreads();
+  int before = scan - mine, n = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < static_cast<int>(threadIdx.x >> 5)) before += s_warp[w];
+    n += s_warp[w];
+  }
+  int64_t other = n + t0 - before;            // rows before t0 that take no part come first
+  for (int64_t t = t0; t < t1; ++t) {
+    const int64_t y = ce_target(p, t);
+    if (y >= 0 && y < p.V) row_map[before++] = static_cast<int32_t>(t);
+    else row_map[other++] = static_cast<int32_t>(t);
+  }
+  if (threadIdx.x == 0) {
+    p.meta->n = n;
+    p.meta->error = s_bad ? ERR_TARGET_RANGE : 0u;
+  }
+}
+
+// Packed rows: xp[i] = x[row_map[i]] for i < n, zeros up to T_pad; dx of the rows that take no part is zero.
+__global__ void __launch_bounds__(256) k_ce_pack(const CeParams p, const uint4* x, int64_t T, int64_t t_pad, uint4* xp) {
+  const int n = p.meta->n;
+  const int per_row = p.H / 8;
+  for (int64_t i = blockIdx.x; i < t_pad; i += gridDim.x) {
+    const int src = i < T ? p.row_map[i] : 0;
+    for (int c = threadIdx.x; c < per_row; c += 256) {
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      xp[i * per_row + c] = i < n ? __ldcs(x + static_cast<int64_t>(src) * per_row + c) : zero;
+      if (i >= n && i < T) reinterpret_cast<uint4*>(p.dx)[static_cast<int64_t>(src) * per_row + c] = zero;
+    }
+  }
+}
+
+// dx of the packed rows from their fp32 parts, added in order.
+__global__ void __launch_bounds__(256) k_ce_dx(const CeParams p) {
+  const int n = p.meta->n;
+  const int per_row = p.H / 8;
+  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
+    const int src = p.row_map[i];
+    for (int c = threadIdx.x; c < per_row; c += 256) {
+      float v[8] = {};
+      for (int s = 0; s < p.splits; ++s) {
+        const float4* a = reinterpret_cast<const float4*>(p.acc + (s * p.pitch + i) * p.H) + 2 * c;
+        const float4 lo = __ldcs(a), hi = __ldcs(a + 1);
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+      }
+      uint4 o;
+      o.x = pack_bf16x2(v[0], v[1]);
+      o.y = pack_bf16x2(v[2], v[3]);
+      o.z = pack_bf16x2(v[4], v[5]);
+      o.w = pack_bf16x2(v[6], v[7]);
+      reinterpret_cast<uint4*>(p.dx)[static_cast<int64_t>(src) * per_row + c] = o;
+    }
+  }
+}
+
+// ---- host side -------------------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 ce_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* q = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(q);
+  });
+  return fn;
+}
+// bf16 [rows, cols] with `pitch` elements per row, boxes of box_cols x box_rows.
+bool ce_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch, int box_cols, int box_rows) {
+  auto enc = ce_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool ce_kmajor(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
+  return ce_map(m, base, rows, cols, pitch, CE_BK, CE_HALF);
+}
+bool ce_mnmajor(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
+  return ce_map(m, base, rows, cols, pitch, 64, CE_BK);
+}
+bool ce_store(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
+  return ce_map(m, base, rows, cols, pitch, 32, 32);
+}
+
+struct CeDevice {
+  int sms = 0;
+  int pairs = 0;               // CTA pairs that run at the same time (0: none)
+};
+
+template <int MODE, int CG>
+cudaLaunchConfig_t ce_config(int units, cudaLaunchAttribute* attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  if (CG == 2) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  cfg.gridDim = dim3(CG * units, 1, 1);
+  cfg.blockDim = dim3(CE_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = CE_SMEM_BYTES;
+  cfg.stream = stream;
+  return cfg;
+}
+template <int MODE, int CG>
+bool ce_prepare() {
+  return cudaFuncSetAttribute(k_ce_gemm<MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, CE_SMEM_BYTES) ==
+         cudaSuccess;
+}
+bool ce_device(CeDevice* out) {
+  static CeDevice info[64];
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  CeDevice& d = info[dev];
+  if (d.sms == 0) {
+    int sms = 0, pairs = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return false;
+    if (!ce_prepare<CE_LSE, 1>() || !ce_prepare<CE_DZ, 1>() || !ce_prepare<CE_DW, 1>() || !ce_prepare<CE_DX, 1>() ||
+        !ce_prepare<CE_LSE, 2>() || !ce_prepare<CE_DZ, 2>() || !ce_prepare<CE_DW, 2>() || !ce_prepare<CE_DX, 2>())
+      return false;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = ce_config<CE_LSE, 2>(64, attr, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&pairs, k_ce_gemm<CE_LSE, 2>, &cfg) != cudaSuccess) {
+      cudaGetLastError();   // clear: single CTAs are used instead
+      pairs = 0;
+    }
+    d.pairs = pairs;
+    d.sms = sms;
+  }
+  *out = d;
+  return true;
+}
+
+template <int MODE>
+cudaError_t ce_launch(bool pair, int64_t units, const CeDevice& dev, const CUtensorMap& a, const CUtensorMap& b,
+                      const CUtensorMap& d, const CeParams& p, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  if (pair) {
+    cudaLaunchConfig_t cfg = ce_config<MODE, 2>(static_cast<int>(std::min<int64_t>(units, dev.pairs)), attr, stream);
+    return cudaLaunchKernelEx(&cfg, k_ce_gemm<MODE, 2>, a, b, d, p);
+  }
+  cudaLaunchConfig_t cfg = ce_config<MODE, 1>(static_cast<int>(std::min<int64_t>(units, dev.sms)), attr, stream);
+  return cudaLaunchKernelEx(&cfg, k_ce_gemm<MODE, 1>, a, b, d, p);
+}
+
+constexpr int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+// Pairs compute tiles of 256 x 256 where those keep all pairs busy, single CTAs tiles of 128 x 128 otherwise.
+bool use_pair(const CeDevice& dev, int64_t m, int64_t n) { return dev.pairs > 0 && up(m, 256) * up(n, 256) >= dev.pairs; }
+
+// Row tiles of a group: as many as keep their rows of A (of `bytes` each) within 48 MB of the L2.
+int group_of(int64_t row_bytes, bool pair, int64_t most) {
+  const int64_t g = (int64_t(48) << 20) / (row_bytes * (pair ? 256 : 128));
+  return static_cast<int>(std::max<int64_t>(1, std::min(g, most)));
+}
+
+uint64_t ce_wait_ns() {
+  const char* v = getenv("MXFP8MOE_WAIT_LIMIT_NS");
+  if (v == nullptr || *v == 0) return CE_WAIT_NS;
+  char* end = nullptr;
+  const unsigned long long n = strtoull(v, &end, 10);
+  return (end != nullptr && *end == 0 && n > 0) ? static_cast<uint64_t>(n) : CE_WAIT_NS;
+}
+
+bool ce_sizes_ok(int64_t T, int64_t H, int64_t V) { return T >= 0 && H > 0 && V > 0; }
+bool ce_sizes_supported(int64_t T, int64_t H, int64_t V) {
+  return H % 8 == 0 && T <= (int64_t(1) << 24) && H <= (int64_t(1) << 20) && V <= (int64_t(1) << 28) &&
+         up(T, 128) * up(V, 128) <= INT32_MAX / 2;
+}
+bool ce_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct CeFwdWs {
+  size_t part, zy, total;
+  int64_t pitch, parts;
+};
+CeFwdWs ce_fwd_ws(int64_t T, int64_t V) {
+  CeFwdWs w{};
+  w.pitch = up(T, 32) * 32;
+  w.parts = 2 * up(V, 128);
+  w.part = sizeof(CeMeta);
+  w.zy = up256(w.part + static_cast<size_t>(w.parts) * w.pitch * sizeof(float2));
+  w.total = up256(w.zy + static_cast<size_t>(w.pitch) * sizeof(float));
+  return w;
+}
+
+// Backward workspace: header, row map, packed x [t_pad, H], dz of one piece [t_pad, piece], fp32 parts of dx.
+struct CeBwdWs {
+  size_t row_map, xp, dz, acc, total;
+  int64_t t_pad, piece, pieces;
+  int splits;
+};
+constexpr int CE_MAX_SPLITS = 16;
+CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
+  CeBwdWs w{};
+  w.t_pad = up(T, 256) * 256;
+  const int64_t most = std::max(CE_MIN_PIECE, CE_DZ_ELEMS / std::max<int64_t>(w.t_pad, 256) / 256 * 256);
+  w.pieces = up(V, most);
+  w.piece = up(up(V, w.pieces), 256) * 256;
+  w.pieces = up(V, w.piece);
+  // dx has few tiles where there are few rows: K is shared out so that about 152 CTAs have work
+  const int64_t tiles = up(T, 128) * up(H, 128);
+  w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({CE_MAX_SPLITS, 152 / std::max<int64_t>(tiles, 1),
+                                                                      up(w.piece, 8 * CE_BK)})));
+  w.row_map = sizeof(CeMeta);
+  w.xp = up256(w.row_map + static_cast<size_t>(w.t_pad) * 4);
+  w.dz = up256(w.xp + static_cast<size_t>(w.t_pad) * H * 2);
+  w.acc = up256(w.dz + static_cast<size_t>(w.t_pad) * w.piece * 2);
+  w.total = up256(w.acc + (w.pieces > 1 || w.splits > 1 ? static_cast<size_t>(w.splits) * w.t_pad * H * 4 : 0));
+  return w;
+}
+
+}  // namespace
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" {
+
+size_t linear_cross_entropy_workspace_size(int64_t T, int64_t H, int64_t V) {
+  if (!ce_sizes_ok(T, H, V) || !ce_sizes_supported(T, H, V)) return 0;
+  return ce_fwd_ws(T, V).total;
+}
+
+int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, int wide_targets, int64_t T, int64_t H,
+                             int64_t V, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (!ce_sizes_ok(T, H, V) || wide_targets < 0 || wide_targets > 1) return MXFP8_ERR_INVALID_ARG;
+  if (!ce_sizes_supported(T, H, V)) return MXFP8_ERR_UNSUPPORTED;
+  if (workspace == nullptr) return MXFP8_ERR_INVALID_ARG;
+  const CeFwdWs ws = ce_fwd_ws(T, V);
+  if (!ce_aligned(workspace, 256) || workspace_bytes < ws.total) return MXFP8_ERR_WORKSPACE;
+  if (T > 0) {
+    if (x == nullptr || w == nullptr || targets == nullptr || loss == nullptr || lse == nullptr)
+      return MXFP8_ERR_INVALID_ARG;
+    if (!ce_aligned(x, 16) || !ce_aligned(w, 16) || !ce_aligned(targets, wide_targets ? 8 : 4) || !ce_aligned(loss, 4) ||
+        !ce_aligned(lse, 4))
+      return MXFP8_ERR_INVALID_ARG;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  if (cudaMemsetAsync(workspace, 0, sizeof(CeMeta), st) != cudaSuccess) return MXFP8_ERR_CUDA;
+  if (T == 0) return MXFP8_OK;
+  CeDevice dev;
+  if (!ce_device(&dev)) return MXFP8_ERR_CUDA;
+  const bool pair = use_pair(dev, T, V);
+  const int64_t tile = pair ? 256 : 128;
+  CeParams p{};
+  p.meta = reinterpret_cast<CeMeta*>(base);
+  p.rows = static_cast<int>(T);
+  p.V = p.vcols = static_cast<int>(V);
+  p.H = static_cast<int>(H);
+  p.group_m = group_of(H * 2, pair, up(T, tile));
+  p.splits = 1;
+  p.targets = targets;
+  p.wide_targets = wide_targets;
+  p.part = reinterpret_cast<float2*>(base + ws.part);
+  p.zy = reinterpret_cast<float*>(base + ws.zy);
+  p.pitch = ws.pitch;
+  p.timeout_ns = ce_wait_ns();
+  CUtensorMap a, b;
+  if (!ce_kmajor(&a, x, T, H, H) || !ce_kmajor(&b, w, V, H, H)) return MXFP8_ERR_CUDA;
+  if (ce_launch<CE_LSE>(pair, up(T, tile) * up(V, tile), dev, a, b, a, p, st) != cudaSuccess) return MXFP8_ERR_CUDA;
+  int width = 32;
+  while (width > 1 && width / 2 >= T) width /= 2;
+  k_ce_merge<<<static_cast<unsigned>(up(T, width)), 256, 0, st>>>(p, static_cast<int>(2 * up(V, tile)), width, loss, lse);
+  return cudaGetLastError() == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
+}
+
+size_t linear_cross_entropy_bwd_workspace_size(int64_t T, int64_t H, int64_t V) {
+  if (!ce_sizes_ok(T, H, V) || !ce_sizes_supported(T, H, V)) return 0;
+  return ce_bwd_ws(T, H, V).total;
+}
+
+int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* x, const void* w, const void* targets,
+                             int wide_targets, const float* lse, int64_t T, int64_t H, int64_t V, void* dx, void* dw,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (!ce_sizes_ok(T, H, V) || wide_targets < 0 || wide_targets > 1) return MXFP8_ERR_INVALID_ARG;
+  if (!ce_sizes_supported(T, H, V)) return MXFP8_ERR_UNSUPPORTED;
+  if (workspace == nullptr || dw == nullptr || !ce_aligned(dw, 16)) return MXFP8_ERR_INVALID_ARG;
+  const CeBwdWs ws = ce_bwd_ws(T, H, V);
+  if (!ce_aligned(workspace, 256) || workspace_bytes < ws.total) return MXFP8_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {   // sums over no rows
+    return cudaMemsetAsync(workspace, 0, sizeof(CeMeta), st) == cudaSuccess &&
+                   cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * H * 2, st) == cudaSuccess
+               ? MXFP8_OK
+               : MXFP8_ERR_CUDA;
+  }
+  for (const void* q : {x, w, static_cast<const void*>(dx)})
+    if (q == nullptr || !ce_aligned(q, 16)) return MXFP8_ERR_INVALID_ARG;
+  if (targets == nullptr || !ce_aligned(targets, wide_targets ? 8 : 4)) return MXFP8_ERR_INVALID_ARG;
+  if (dloss == nullptr || lse == nullptr || !ce_aligned(dloss, 4) || !ce_aligned(lse, 4) || !ce_aligned(dlse, 4))
+    return MXFP8_ERR_INVALID_ARG;
+  CeDevice dev;
+  if (!ce_device(&dev)) return MXFP8_ERR_CUDA;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  uint16_t* xp = reinterpret_cast<uint16_t*>(base + ws.xp);
+  uint16_t* dz = reinterpret_cast<uint16_t*>(base + ws.dz);
+  CeParams p{};
+  p.meta = reinterpret_cast<CeMeta*>(base);
+  p.row_map = reinterpret_cast<int32_t*>(base + ws.row_map);
+  p.V = static_cast<int>(V);
+  p.H = static_cast<int>(H);
+  p.targets = targets;
+  p.wide_targets = wide_targets;
+  p.lse = lse;
+  p.dloss = dloss;
+  p.dlse = dlse;
+  p.pitch = ws.t_pad;
+  p.acc = ws.pieces > 1 || ws.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
+  p.dx = static_cast<uint16_t*>(dx);
+  p.timeout_ns = ce_wait_ns();
+  k_ce_rows<<<1, 1024, 0, st>>>(p, T, const_cast<int32_t*>(p.row_map));
+  const unsigned rows_grid = static_cast<unsigned>(std::min<int64_t>(ws.t_pad, 8 * dev.sms));
+  k_ce_pack<<<rows_grid, 256, 0, st>>>(p, static_cast<const uint4*>(x), T, ws.t_pad, reinterpret_cast<uint4*>(xp));
+  if (cudaGetLastError() != cudaSuccess) return MXFP8_ERR_CUDA;
+  CUtensorMap x_k, x_mn, w_k, w_mn, dz_k, dz_mn, dz_st;
+  if (!ce_kmajor(&x_k, xp, ws.t_pad, H, H) || !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) ||
+      !ce_mnmajor(&w_mn, w, V, H, H) || !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece) ||
+      !ce_mnmajor(&dz_mn, dz, ws.t_pad, ws.piece, ws.piece) || !ce_store(&dz_st, dz, ws.t_pad, ws.piece, ws.piece))
+    return MXFP8_ERR_CUDA;
+  for (int64_t i = 0; i < ws.pieces; ++i) {
+    const int64_t v0 = i * ws.piece, cols = std::min(ws.piece, V - v0);
+    p.v0 = static_cast<int>(v0);
+    p.vcols = static_cast<int>(cols);
+    p.splits = 1;
+    p.acc_add = i > 0;
+    const bool dz_pair = use_pair(dev, T, cols), dw_pair = use_pair(dev, cols, H), dx_pair = use_pair(dev, T, H);
+    const int64_t zt = dz_pair ? 256 : 128, wt = dw_pair ? 256 : 128, xt = dx_pair ? 256 : 128;
+    p.group_m = group_of(H * 2, dz_pair, up(T, zt));
+    p.d_rows = static_cast<int>(ws.t_pad);
+    p.d_cols = static_cast<int>(ws.piece);
+    if (ce_launch<CE_DZ>(dz_pair, up(T, zt) * up(cols, zt), dev, x_k, w_k, dz_st, p, st) != cudaSuccess)
+      return MXFP8_ERR_CUDA;
+    CUtensorMap dw_st;
+    if (!ce_store(&dw_st, static_cast<uint16_t*>(dw) + v0 * H, cols, H, H)) return MXFP8_ERR_CUDA;
+    p.group_m = 1;
+    p.d_rows = static_cast<int>(cols);
+    p.d_cols = static_cast<int>(H);
+    if (ce_launch<CE_DW>(dw_pair, up(cols, wt) * up(H, wt), dev, dz_mn, x_mn, dw_st, p, st) != cudaSuccess)
+      return MXFP8_ERR_CUDA;
+    p.group_m = 1;
+    p.split_steps = static_cast<int>(up(up(ws.piece, CE_BK), ws.splits));
+    p.splits = static_cast<int>(up(up(cols, CE_BK), p.split_steps));
+    if (ce_launch<CE_DX>(dx_pair, up(T, xt) * up(H, xt) * p.splits, dev, dz_k, w_mn, dz_st, p, st) != cudaSuccess)
+      return MXFP8_ERR_CUDA;
+  }
+  if (p.acc != nullptr) {
+    // every share of the first piece was written; a shorter last piece may have filled fewer of them
+    p.splits = static_cast<int>(up(up(std::min(ws.piece, V), CE_BK), up(up(ws.piece, CE_BK), ws.splits)));
+    k_ce_dx<<<rows_grid, 256, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return MXFP8_ERR_CUDA;
+  }
+  return MXFP8_OK;
+}
+
+}  // extern "C"

@@ -12,6 +12,7 @@ enum : uint32_t {
   ERR_SPLIT_NEGATIVE = 1u << 1,   // a negative split size
   ERR_EXPERT_RANGE = 1u << 2,     // an expert id outside [0, E) given to the permute
   ERR_TOKEN_RANGE = 1u << 3,      // a token id outside [0, T) in token_of_row
+  ERR_TARGET_RANGE = 1u << 4,     // a target >= V given to the cross entropy
   ERR_TIMEOUT_PRODUCER = 1u << 8, // TMA producer gave up waiting for a free stage
   ERR_TIMEOUT_MMA = 1u << 9,      // MMA issuer gave up waiting for data or a free accumulator
   ERR_TIMEOUT_EPILOGUE = 1u << 10,// epilogue gave up waiting for an accumulator
