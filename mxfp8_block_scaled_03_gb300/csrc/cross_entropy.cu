@@ -26,6 +26,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "mx_device.cuh"
 #include "mx_internal.h"
@@ -51,6 +52,9 @@ constexpr int CE_DATA_BYTES = CE_STAGES * CE_STAGE_BYTES;
 constexpr int CE_BAR_OFFSET = CE_DATA_BYTES + CE_EPI_BYTES;
 constexpr int CE_SMEM_BYTES = CE_BAR_OFFSET + (2 * CE_STAGES + 5) * 8 + 8 + 1024;
 static_assert(CE_SMEM_BYTES <= 232448, "shared memory budget");
+constexpr int CE_CHUNK = 16;                       // CE_LSE: K steps that the tensor core sums before fp32 adds take over
+constexpr uint32_t CE_REGS_LOW = 56, CE_REGS_HIGH = 224;   // CE_LSE: warps 0-3, epilogue warps
+static_assert(128 * CE_REGS_LOW + 256 * CE_REGS_HIGH == CE_THREADS * 168, "register split must equal the launch pool");
 constexpr int64_t CE_DZ_ELEMS = int64_t(1) << 27;  // most elements of dz at a time (256 MB)
 constexpr int64_t CE_MIN_PIECE = 2048;             // vocabulary entries of a piece, whatever the rows
 constexpr uint64_t CE_WAIT_NS = 2000000000ull;     // 2 s per individual wait
@@ -84,6 +88,8 @@ struct CeParams {
   int64_t pitch;
   float* acc;                  // CE_DX: [splits][pitch][H] fp32, or NULL: dx is written directly
   int acc_add;
+  uint16_t* dz;                // few rows, CE_DZ: [NT][dz_pitch]
+  int64_t dz_pitch;
   int d_rows, d_cols;          // CE_DZ, CE_DW: extent of the map that is stored to
   uint16_t* dx;
   uint64_t timeout_ns;
@@ -129,6 +135,25 @@ __device__ __forceinline__ void ce_mma(uint32_t d_tmem, uint64_t a, uint64_t b, 
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
         "r"(accumulate)
         : "memory");
+}
+
+template <uint32_t N>
+__device__ __forceinline__ void ce_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void ce_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 16 consecutive TMEM columns of this warp's 32 lanes.
+__device__ __forceinline__ void ce_tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
 struct CeUnits {
@@ -206,6 +231,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
   constexpr int TILE = CE_HALF * CG;
   constexpr int NH = TILE / 2;                      // columns of an epilogue warp
   constexpr uint32_t TMEM_COLS = 2 * TILE;
+  constexpr int CHUNK = MODE == CE_LSE ? CE_CHUNK : 1 << 30;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + CE_BAR_OFFSET);
@@ -255,109 +281,119 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
   const uint32_t peer_abort = CG == 2 ? map_to_cta(const_cast<int*>(abort_flag), rank ^ 1u) : 0u;
   uint32_t prod_issued = 0;
 
-  if (warp == CE_WARP_PRODUCER) {
-    // ---------------- tile copies (every CTA its own; one lane) ----------------
-    if (lane == 0) {
-      const uint32_t leader_full = CG == 2 ? map_to_cta(full, 0) : 0u;
-      uint32_t issued_parity = 0;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = first; ok && u < units.total; u += stride) {
-        const CeTile t = ce_tile<MODE>(u, units, p);
-        const int a0 = t.m * TILE + CE_HALF * static_cast<int>(rank);
-        const int b0 = t.n * TILE + CE_HALF * static_cast<int>(rank);
-        for (int s = 0; s < t.steps; ++s) {
-          if (!ce_wait<CG>(&empty[stage], phase ^ 1u, false, abort_flag, peer_abort, p, ERR_TIMEOUT_PRODUCER)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sA = smem + stage * CE_STAGE_BYTES;
-          uint8_t* sB = sA + CE_OP_BYTES;
-          const int k = (t.k0 + s) * CE_BK;
-          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
-            if constexpr (CG == 2) tma_load_2d_pair(dst, map, leader_full + stage * 8, x, y);
-            else tma_load_2d(dst, map, &full[stage], x, y);
-          };
-          if (A_MN) {
-            load(sA, &tmA, a0, k);
-            load(sA + CE_OP_BYTES / 2, &tmA, a0 + 64, k);
-          } else {
-            load(sA, &tmA, k, a0);
-          }
-          // B rows: the vocabulary from v0 (logits), or K rows of it (dx)
-          if (B_MN) {
-            const int ky = MODE == CE_DX ? p.v0 + k : k;
-            load(sB, &tmB, b0, ky);
-            load(sB + CE_OP_BYTES / 2, &tmB, b0 + 64, ky);
-          } else {
-            load(sB, &tmB, k, p.v0 + b0);
-          }
-          if (leader) mbar_arrive_expect_tx(&full[stage], CG * CE_STAGE_BYTES);
-          prod_issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == CE_STAGES) {
-            stage = 0;
-            phase ^= 1u;
+  if (warp < CE_EPI_WARP0) {
+    if constexpr (MODE == CE_LSE) ce_regs_dec<CE_REGS_LOW>();
+    if (warp == CE_WARP_PRODUCER) {
+      // ---------------- tile copies (every CTA its own; one lane) ----------------
+      if (lane == 0) {
+        const uint32_t leader_full = CG == 2 ? map_to_cta(full, 0) : 0u;
+        uint32_t issued_parity = 0;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = first; ok && u < units.total; u += stride) {
+          const CeTile t = ce_tile<MODE>(u, units, p);
+          const int a0 = t.m * TILE + CE_HALF * static_cast<int>(rank);
+          const int b0 = t.n * TILE + CE_HALF * static_cast<int>(rank);
+          for (int s = 0; s < t.steps; ++s) {
+            if (!ce_wait<CG>(&empty[stage], phase ^ 1u, false, abort_flag, peer_abort, p, ERR_TIMEOUT_PRODUCER)) {
+              ok = false;
+              break;
+            }
+            uint8_t* sA = smem + stage * CE_STAGE_BYTES;
+            uint8_t* sB = sA + CE_OP_BYTES;
+            const int k = (t.k0 + s) * CE_BK;
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+              if constexpr (CG == 2) tma_load_2d_pair(dst, map, leader_full + stage * 8, x, y);
+              else tma_load_2d(dst, map, &full[stage], x, y);
+            };
+            if (A_MN) {
+              load(sA, &tmA, a0, k);
+              load(sA + CE_OP_BYTES / 2, &tmA, a0 + 64, k);
+            } else {
+              load(sA, &tmA, k, a0);
+            }
+            // B rows: the vocabulary from v0 (logits), or K rows of it (dx)
+            if (B_MN) {
+              const int ky = MODE == CE_DX ? p.v0 + k : k;
+              load(sB, &tmB, b0, ky);
+              load(sB + CE_OP_BYTES / 2, &tmB, b0 + 64, ky);
+            } else {
+              load(sB, &tmB, k, p.v0 + b0);
+            }
+            if (leader) mbar_arrive_expect_tx(&full[stage], CG * CE_STAGE_BYTES);
+            prod_issued |= 1u << stage;
+            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == CE_STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
+        // Copies land before the CTA exits: the leader waits for its stages (their barriers count both CTAs' copies);
+        // the second CTA's wait for the leader is the pair's closing barriers below.
+        if (leader)
+          for (int s = 0; s < CE_STAGES; ++s)
+            if ((prod_issued >> s) & 1u)
+              if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
+                atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
       }
-      // Copies land before the CTA exits: the leader waits for its stages (their barriers count both CTAs' copies);
-      // the second CTA's wait for the leader is the pair's closing barriers below.
-      if (leader)
-        for (int s = 0; s < CE_STAGES; ++s)
-          if ((prod_issued >> s) & 1u)
-            if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
-              atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
-    }
-    __syncwarp();
-  } else if (warp == CE_WARP_MMA && leader) {
-    // ---------------- MMA issuer (one lane of the leader) ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc = ce_idesc(TILE, TILE, A_MN, B_MN);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool issued = false, ok = true;
-      for (int u = first; ok && u < units.total; u += stride) {
-        const CeTile t = ce_tile<MODE>(u, units, p);
-        if (t.steps == 0) continue;                 // no rows: the epilogue writes zeros without the accumulator
-        if (!ce_wait<CG>(&acc_empty[buf], acc_phase ^ 1u, true, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA)) break;
-        tc_fence_after();
-        for (int s = 0; s < t.steps; ++s) {
-          if (!ce_wait<CG>(&full[stage], phase, false, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + stage * CE_STAGE_BYTES), b0 = a0 + CE_OP_BYTES;
+      __syncwarp();
+    } else if (warp == CE_WARP_MMA && leader) {
+      // ---------------- MMA issuer (one lane of the leader) ----------------
+      if (lane == 0) {
+        constexpr uint32_t idesc = ce_idesc(TILE, TILE, A_MN, B_MN);
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool issued = false, ok = true;
+        for (int u = first; ok && u < units.total; u += stride) {
+          const CeTile t = ce_tile<MODE>(u, units, p);
+          if (t.steps == 0) continue;                 // no rows: the epilogue writes zeros without the accumulator
+          for (int s = 0; s < t.steps; ++s) {
+            if (s % CHUNK == 0) {
+              if (!ce_wait<CG>(&acc_empty[buf], acc_phase ^ 1u, true, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            if (!ce_wait<CG>(&full[stage], phase, false, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(smem + stage * CE_STAGE_BYTES), b0 = a0 + CE_OP_BYTES;
 #pragma unroll
-          for (int k = 0; k < CE_BK / 16; ++k) {
-            const uint64_t da = A_MN ? ce_sdesc_mn(a0 + 2048 * k) : sdesc_kmajor_sw128(a0 + 32 * k);
-            const uint64_t db = B_MN ? ce_sdesc_mn(b0 + 2048 * k) : sdesc_kmajor_sw128(b0 + 32 * k);
-            ce_mma<CG>(tmem + buf * TILE, da, db, idesc, (s | k) != 0 ? 1u : 0u);
-          }
-          if constexpr (CG == 2) tc_commit_pair_both(&empty[stage]);
-          else tc_commit(&empty[stage]);
-          issued = true;
-          if (++stage == CE_STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            for (int k = 0; k < CE_BK / 16; ++k) {
+              const uint64_t da = A_MN ? ce_sdesc_mn(a0 + 2048 * k) : sdesc_kmajor_sw128(a0 + 32 * k);
+              const uint64_t db = B_MN ? ce_sdesc_mn(b0 + 2048 * k) : sdesc_kmajor_sw128(b0 + 32 * k);
+              ce_mma<CG>(tmem + buf * TILE, da, db, idesc, (s % CHUNK | k) != 0 ? 1u : 0u);
+            }
+            if constexpr (CG == 2) tc_commit_pair_both(&empty[stage]);
+            else tc_commit(&empty[stage]);
+            issued = true;
+            if (++stage == CE_STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if ((s + 1) % CHUNK == 0 || s + 1 == t.steps) {
+              if constexpr (CG == 2) tc_commit_pair_both(&acc_full[buf]);
+              else tc_commit(&acc_full[buf]);
+              buf ^= 1;
+              if (buf == 0) acc_phase ^= 1u;
+            }
           }
         }
-        if (!ok) break;
-        if constexpr (CG == 2) tc_commit_pair_both(&acc_full[buf]);
-        else tc_commit(&acc_full[buf]);
-        buf ^= 1;
-        if (buf == 0) acc_phase ^= 1u;
+        if (issued) {
+          if constexpr (CG == 2) tc_commit_pair_local(drained);
+          else tc_commit(drained);
+          if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+        }
       }
-      if (issued) {
-        if constexpr (CG == 2) tc_commit_pair_local(drained);
-        else tc_commit(drained);
-        if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
-      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= CE_EPI_WARP0) {
+  } else {
+    if constexpr (MODE == CE_LSE) ce_regs_inc<CE_REGS_HIGH>();
     // ---------------- epilogue (every CTA its 128 rows) ----------------
     const int quarter = warp & 3;
     const int half = (warp - CE_EPI_WARP0) >> 2;
@@ -386,14 +422,73 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
         rate = hot + (p.dlse != nullptr ? __ldg(p.dlse + src) : 0.0f);
         lse2 = __ldg(p.lse + src) * LOG2E;
       }
-      if (t.steps > 0) {
+      auto wait_acc = [&]() {
         bool got = true;
         if (warp == CE_EPI_WARP0 && lane == 0)
           got = ce_wait<CG>(&acc_full[buf], acc_phase, false, abort_flag, peer_abort, p, ERR_TIMEOUT_EPILOGUE);
-        if (!group_and(CE_BAR_EPI, CE_EPI_WARPS * 32, got)) break;
+        got = group_and(CE_BAR_EPI, CE_EPI_WARPS * 32, got);
         tc_fence_after();
+        return got;
+      };
+      auto release_acc = [&]() {                    // all of this warp's columns have been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) mbar_arrive_remote(map_to_cta(&acc_empty[buf], 0));
+          else mbar_arrive(&acc_empty[buf]);
+        }
+      };
+      auto next_acc = [&]() {
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1u;
+      };
+      if constexpr (MODE == CE_LSE) {
+        // The tensor core cuts its sums off instead of rounding them, always towards zero: H = 4096 in one sum left loss
+        // off by 2.8e-6 of its norm, an fp32 product by 0.6e-6.  So it sums CE_CHUNK steps at a time, and these are added
+        // here, rounded: 0.6e-6 with 16 steps (1269 us for 8192 x 4096 x 32000), 1.4e-6 with 32 (1256), 0.3e-6 with 8 (1293).
+        float z[NH];
+        bool ok = true;
+        for (int s = 0; ok && s < t.steps; s += CE_CHUNK) {
+          ok = wait_acc();
+          if (ok) {
+#pragma unroll
+            for (int c = 0; c < NH; c += 32) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(t_row + buf * TILE + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[c + i] = s == 0 ? __uint_as_float(v[i]) : z[c + i] + __uint_as_float(v[i]);
+            }
+            release_acc();
+            next_acc();
+          }
+        }
+        if (!ok) break;
+        if (y >= col0 && y < col0 + NH) {
+          const int at = y - col0;
+          float zy = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NH; ++i)
+            if (i == at) zy = z[i];
+          p.zy[row] = zy;
+        }
+        if (col0 + NH > p.V) {
+#pragma unroll
+          for (int i = 0; i < NH; ++i)
+            if (col0 + i >= p.V) z[i] = -INFINITY;
+        }
+        float top = z[0];
+#pragma unroll
+        for (int i = 1; i < NH; ++i) top = fmaxf(top, z[i]);
+        const float m = top * LOG2E;                // in base 2
+        const float base = m == -INFINITY ? 0.0f : m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) sum += ex2(fmaf(z[i], LOG2E, -base));
+        if (row < n_rows) p.part[(2 * t.n + half) * p.pitch + row] = make_float2(m, sum);
+        continue;
       }
-      float m = -INFINITY, sum = 0.0f;              // CE_LSE, in base 2
+      if (t.steps > 0 && !wait_acc()) break;
 #pragma unroll 1
       for (int c = 0; c < NH; c += 32) {
         uint32_t v[32];
@@ -404,40 +499,9 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0u;
         }
-        if (c + 32 >= NH && t.steps > 0) {          // all of this warp's columns have been read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 2) mbar_arrive_remote(map_to_cta(&acc_empty[buf], 0));
-            else mbar_arrive(&acc_empty[buf]);
-          }
-        }
+        if (c + 32 >= NH && t.steps > 0) release_acc();
         const int col = col0 + c;
-        if constexpr (MODE == CE_LSE) {
-          if (y >= col && y < col + 32) {
-            const int at = y - col;
-            float zy = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i == at) zy = __uint_as_float(v[i]);
-            p.zy[row] = zy;
-          }
-          if (col + 32 > p.V) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (col + i >= p.V) v[i] = 0xFF800000u;   // -inf
-          }
-          float top = __uint_as_float(v[0]);
-#pragma unroll
-          for (int i = 1; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-          const float m_new = fmaxf(m, top * LOG2E);
-          const float base = m_new == -INFINITY ? 0.0f : m_new;
-          float add = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) add += ex2(fmaf(__uint_as_float(v[i]), LOG2E, -base));
-          sum = sum * ex2(m - base) + add;
-          m = m_new;
-        } else if constexpr (MODE == CE_DZ || MODE == CE_DW) {
+        if constexpr (MODE == CE_DZ || MODE == CE_DW) {
           if constexpr (MODE == CE_DZ) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -496,11 +560,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
           }
         }
       }
-      if (MODE == CE_LSE && row < n_rows) p.part[(2 * t.n + half) * p.pitch + row] = make_float2(m, sum);
-      if (t.steps > 0) {
-        buf ^= 1;
-        if (buf == 0) acc_phase ^= 1u;
-      }
+      if (t.steps > 0) next_acc();
     }
     if ((MODE == CE_DZ || MODE == CE_DW) && lane == 0) bulk_wait_all();   // stores complete before exit
   }
@@ -526,10 +586,304 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
   }
 }
 
-// Joins the parts of each row: 256 threads take `width` rows (a power of two up to 32), 256 / width shares of the parts.
-__global__ void __launch_bounds__(256) k_ce_merge(const CeParams p, int parts, int width, float* loss, float* lse) {
-  __shared__ float2 s[256];
-  const int r = threadIdx.x % width, share = threadIdx.x / width, shares = 256 / width;
+// ---- few rows -------------------------------------------------------------------------------
+// Up to CE_FEW rows: the weights are the M operand (128 rows of w, or 128 columns for dx), the rows the N operand
+// (NT of them), so that nothing is spent on rows that are not there and a CTA's stages hold little but weights.  Bound:
+// the bytes of w.  Two CTAs per SM keep twice the copies in flight.
+//   CE_LSE  z^T = w x^T: a thread has one vocabulary entry and all rows; it carries every row's running maximum and sum
+//           over all its tiles, and lanes are joined once, at the end
+//   CE_DZ   the same product, dz written packed row by packed row
+//   CE_DX   dx^T = w^T dz^T over a share of the vocabulary: fp32 parts
+constexpr int CE_FEW = 64;
+constexpr int CE_FEW_BUFS = 4;                     // accumulators of NT columns
+template <int NT>
+struct FewShape {
+  static constexpr int EPI_WARPS = NT == 64 ? 8 : 4;        // 64 rows' maxima and sums need two threads per entry
+  static constexpr int COLS = NT / (EPI_WARPS / 4);
+  static constexpr int PER_SM = NT == 64 ? 1 : 2;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int B_BYTES = NT * CE_BK * 2;
+  static constexpr int STAGE_BYTES = CE_OP_BYTES + B_BYTES;
+  static constexpr int STAGES = NT == 64 ? 9 : NT == 32 ? 5 : 6;
+  static constexpr int PARAM_OFFSET = STAGES * STAGE_BYTES;             // [NT] float4 (CE_DZ), [EPI_WARPS][COLS] float2 (CE_LSE)
+  static constexpr int BAR_OFFSET = PARAM_OFFSET + EPI_WARPS * COLS * 16;
+  static constexpr int SMEM_BYTES = BAR_OFFSET + (2 * STAGES + 2 * CE_FEW_BUFS + 1) * 8 + 8 + 1024;
+  static_assert(SMEM_BYTES <= (PER_SM == 2 ? 115712 : 232448), "shared memory budget");
+  static_assert(PER_SM * CE_FEW_BUFS * NT <= 512, "TMEM budget");
+};
+
+template <int MODE, int NT>
+__global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
+    k_ce_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const CeParams p) {
+  using S = FewShape<NT>;
+  constexpr bool A_MN = MODE == CE_DX;
+  constexpr int CHUNK = MODE == CE_LSE ? CE_CHUNK : 1 << 30;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BAR_OFFSET);
+  uint64_t* empty = full + S::STAGES;
+  uint64_t* acc_full = empty + S::STAGES;
+  uint64_t* acc_empty = acc_full + CE_FEW_BUFS;
+  uint64_t* drained = acc_empty + CE_FEW_BUFS;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < CE_FEW_BUFS; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], S::EPI_WARPS);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, CE_FEW_BUFS * NT);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  // units: 128 vocabulary entries each, or (share of the piece, 128 columns of dx)
+  const int tiles = MODE == CE_DX ? (p.H + 127) / 128 : (p.vcols + 127) / 128;
+  const int k_steps = MODE == CE_DX ? (p.vcols + CE_BK - 1) / CE_BK : (p.H + CE_BK - 1) / CE_BK;
+  const int total = MODE == CE_DX ? tiles * p.splits : tiles;
+  auto k_begin = [&](int u) { return MODE == CE_DX ? u / tiles * p.split_steps : 0; };
+  auto k_end = [&](int u) { return MODE == CE_DX ? min(k_steps, (u / tiles + 1) * p.split_steps) : k_steps; };
+
+  if (warp == 0) {
+    // ---------------- tile copies (one lane) ----------------
+    if (lane == 0) {
+      uint32_t issued = 0, issued_parity = 0;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const int m0 = (MODE == CE_DX ? u % tiles : u) * 128;
+        const int k1 = k_end(u);
+        for (int ks = k_begin(u); ks < k1; ++ks) {
+          if (!ce_wait<1>(&empty[stage], phase ^ 1u, false, abort_flag, 0u, p, ERR_TIMEOUT_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sA = smem + stage * S::STAGE_BYTES;
+          mbar_arrive_expect_tx(&full[stage], S::STAGE_BYTES);
+          if (A_MN) {
+            tma_load_2d(sA, &tmA, &full[stage], m0, p.v0 + ks * CE_BK);
+            tma_load_2d(sA + CE_OP_BYTES / 2, &tmA, &full[stage], m0 + 64, p.v0 + ks * CE_BK);
+          } else {
+            tma_load_2d(sA, &tmA, &full[stage], ks * CE_BK, p.v0 + m0);
+          }
+          tma_load_2d(sA + CE_OP_BYTES, &tmB, &full[stage], ks * CE_BK, 0);
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == S::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      for (int s = 0; s < S::STAGES; ++s)           // copies land before the CTA exits
+        if ((issued >> s) & 1u)
+          if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
+            atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (one lane) ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = ce_idesc(128, NT, A_MN, false);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool issued = false, ok = true;
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const int steps = k_end(u) - k_begin(u);
+        for (int s = 0; s < steps; ++s) {
+          if (s % CHUNK == 0) {
+            if (!ce_wait<1>(&acc_empty[buf], acc_phase ^ 1u, false, abort_flag, 0u, p, ERR_TIMEOUT_MMA)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (!ce_wait<1>(&full[stage], phase, false, abort_flag, 0u, p, ERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + stage * S::STAGE_BYTES), b0 = a0 + CE_OP_BYTES;
+#pragma unroll
+          for (int k = 0; k < CE_BK / 16; ++k)
+            ce_mma<1>(tmem + buf * NT, A_MN ? ce_sdesc_mn(a0 + 2048 * k) : sdesc_kmajor_sw128(a0 + 32 * k),
+                      sdesc_kmajor_sw128(b0 + 32 * k), idesc, (s % CHUNK | k) != 0 ? 1u : 0u);
+          tc_commit(&empty[stage]);
+          issued = true;
+          if (++stage == S::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if ((s + 1) % CHUNK == 0 || s + 1 == steps) {
+            tc_commit(&acc_full[buf]);
+            if (++buf == CE_FEW_BUFS) {
+              buf = 0;
+              acc_phase ^= 1u;
+            }
+          }
+        }
+      }
+      if (issued) {
+        tc_commit(drained);
+        if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue ----------------
+    const int quarter = warp & 3;
+    const int c0 = (warp - 2) / 4 * S::COLS;        // first row (column of the accumulator) of this warp
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+    const int n_rows = MODE == CE_LSE ? p.rows : p.meta->n;
+    // CE_DZ: what each row needs; CE_LSE: its target (other rows: no target, rate 0)
+    float4* s_row = reinterpret_cast<float4*>(smem + S::PARAM_OFFSET);
+    if (MODE != CE_DX) {
+      const int i = static_cast<int>(threadIdx.x) - 64;
+      if (i < NT) {
+        float4 r = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
+        if (i < n_rows) {
+          const int src = MODE == CE_DZ ? __ldg(p.row_map + i) : i;
+          const int64_t target = ce_target(p, src);
+          if (target >= 0 && target < p.V) r.w = __int_as_float(static_cast<int>(target) - p.v0);
+          if (MODE == CE_DZ) {
+            r.z = __ldg(p.dloss + src);
+            r.x = r.z + (p.dlse != nullptr ? __ldg(p.dlse + src) : 0.0f);
+            r.y = __ldg(p.lse + src) * LOG2E;
+          }
+        }
+        s_row[i] = r;
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(CE_BAR_EPI), "r"(S::EPI_WARPS * 32) : "memory");
+    }
+    // CE_LSE, base 2: below every logit, and finite, so that a first logit replaces it without a case of its own
+    float m[S::COLS], sum[S::COLS];
+    if (MODE == CE_LSE) {
+#pragma unroll
+      for (int j = 0; j < S::COLS; ++j) {
+        m[j] = -3e38f;
+        sum[j] = 0.0f;
+      }
+    }
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+      const int steps = k_end(u) - k_begin(u);
+      float z[S::COLS];
+      for (int s = 0; s < steps; s += CHUNK < steps ? CHUNK : steps) {
+        int got = 1;
+        if (lane == 0) got = ce_wait<1>(&acc_full[buf], acc_phase, false, abort_flag, 0u, p, ERR_TIMEOUT_EPILOGUE) ? 1 : 0;
+        ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[S::COLS];
+        if constexpr (S::COLS == 16) ce_tmem_ld16(t_row + buf * NT, v);
+        else tmem_ld_32x32b_x32(t_row + buf * NT, v);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        if (++buf == CE_FEW_BUFS) {
+          buf = 0;
+          acc_phase ^= 1u;
+        }
+#pragma unroll
+        for (int j = 0; j < S::COLS; ++j) z[j] = s == 0 ? __uint_as_float(v[j]) : z[j] + __uint_as_float(v[j]);
+      }
+      if (!ok) break;
+      if constexpr (MODE == CE_LSE) {
+        const int v = u * 128 + quarter * 32 + lane;
+        if (v < p.V) {
+#pragma unroll
+          for (int j = 0; j < S::COLS; ++j) {
+            if (__float_as_int(s_row[c0 + j].w) == v) p.zy[c0 + j] = z[j];
+            const float d = fmaf(z[j], LOG2E, -m[j]);
+            const float e = ex2(-fabsf(d));
+            sum[j] = d > 0.0f ? fmaf(sum[j], e, 1.0f) : sum[j] + e;
+            m[j] = fmaxf(m[j], z[j] * LOG2E);
+          }
+        }
+      } else if constexpr (MODE == CE_DZ) {
+        const int v = u * 128 + quarter * 32 + lane;
+        uint16_t* dst = p.dz + static_cast<int64_t>(c0) * p.dz_pitch + v;
+#pragma unroll
+        for (int j = 0; j < S::COLS; ++j) {
+          const float4 r = s_row[c0 + j];
+          float d = r.x * ex2(fmaf(z[j], LOG2E, -r.y));
+          if (__float_as_int(r.w) == v) d -= r.z;
+          dst[j * p.dz_pitch] = c0 + j < n_rows && v < p.vcols ? __bfloat16_as_ushort(__float2bfloat16_rn(d)) : 0;
+        }
+      } else {
+        const int h = u % tiles * 128 + quarter * 32 + lane;
+        float* dst = p.acc + (static_cast<int64_t>(u / tiles) * p.pitch + c0) * p.H + h;
+        if (h < p.H) {
+#pragma unroll
+          for (int j = 0; j < S::COLS; ++j)
+            if (c0 + j < n_rows) {
+              float* q = dst + static_cast<int64_t>(j) * p.H;
+              *q = p.acc_add ? *q + z[j] : z[j];
+            }
+        }
+      }
+    }
+    if constexpr (MODE == CE_LSE) {
+      // join the warp's lanes, then the quarters
+      float2* s_part = reinterpret_cast<float2*>(smem + S::PARAM_OFFSET);
+      asm volatile("bar.sync %0, %1;" ::"r"(CE_BAR_EPI), "r"(S::EPI_WARPS * 32) : "memory");   // s_row has been read
+#pragma unroll
+      for (int j = 0; j < S::COLS; ++j) {
+        float top = m[j];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        float t = sum[j] * ex2(m[j] - top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+        if (lane == 0) s_part[quarter * NT + c0 + j] = make_float2(top, t);
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(CE_BAR_EPI), "r"(S::EPI_WARPS * 32) : "memory");
+      const int i = static_cast<int>(threadIdx.x) - 64;
+      if (i < n_rows && i < NT) {
+        float2 a = s_part[i];
+        for (int q = 1; q < 4; ++q) {
+          const float2 b = s_part[q * NT + i];
+          const float top = fmaxf(a.x, b.x);
+          a = make_float2(top, a.y * ex2(a.x - top) + b.y * ex2(b.x - top));
+        }
+        p.part[blockIdx.x * p.pitch + i] = a;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, CE_FEW_BUFS * NT);
+  }
+}
+
+// Joins the parts of each row: the CTA takes `width` rows (a power of two up to 32), its threads equal shares of the
+// parts.
+constexpr int CE_MERGE_THREADS = 512;
+__global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p, int parts, int width, float* loss, float* lse) {
+  __shared__ float2 s[CE_MERGE_THREADS];
+  const int r = threadIdx.x % width, share = threadIdx.x / width, shares = CE_MERGE_THREADS / width;
   const int row = blockIdx.x * width + r;
   float m = -INFINITY, sum = 0.0f;
   auto join = [&](float2 o) {
@@ -667,8 +1021,8 @@ bool ce_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_
              CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool ce_kmajor(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
-  return ce_map(m, base, rows, cols, pitch, CE_BK, CE_HALF);
+bool ce_kmajor(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch, int box = CE_HALF) {
+  return ce_map(m, base, rows, cols, pitch, CE_BK, box);
 }
 bool ce_mnmajor(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
   return ce_map(m, base, rows, cols, pitch, 64, CE_BK);
@@ -699,6 +1053,14 @@ cudaLaunchConfig_t ce_config(int units, cudaLaunchAttribute* attr, cudaStream_t 
   cfg.stream = stream;
   return cfg;
 }
+template <int MODE>
+bool ce_prepare_few() {
+  auto set = [](auto kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  return set(k_ce_few<MODE, 16>, FewShape<16>::SMEM_BYTES) && set(k_ce_few<MODE, 32>, FewShape<32>::SMEM_BYTES) &&
+         set(k_ce_few<MODE, 64>, FewShape<64>::SMEM_BYTES);
+}
 template <int MODE, int CG>
 bool ce_prepare() {
   return cudaFuncSetAttribute(k_ce_gemm<MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, CE_SMEM_BYTES) ==
@@ -715,7 +1077,7 @@ bool ce_device(CeDevice* out) {
     int sms = 0, pairs = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return false;
     if (!ce_prepare<CE_LSE, 1>() || !ce_prepare<CE_DZ, 1>() || !ce_prepare<CE_DW, 1>() || !ce_prepare<CE_DX, 1>() ||
-        !ce_prepare<CE_LSE, 2>() || !ce_prepare<CE_DZ, 2>() || !ce_prepare<CE_DW, 2>() || !ce_prepare<CE_DX, 2>())
+        !ce_prepare_few<CE_LSE>() || !ce_prepare_few<CE_DZ>() || !ce_prepare_few<CE_DX>() || !ce_prepare<CE_LSE, 2>() || !ce_prepare<CE_DZ, 2>() || !ce_prepare<CE_DW, 2>() || !ce_prepare<CE_DX, 2>())
       return false;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = ce_config<CE_LSE, 2>(64, attr, nullptr);
@@ -740,6 +1102,23 @@ cudaError_t ce_launch(bool pair, int64_t units, const CeDevice& dev, const CUten
   }
   cudaLaunchConfig_t cfg = ce_config<MODE, 1>(static_cast<int>(std::min<int64_t>(units, dev.sms)), attr, stream);
   return cudaLaunchKernelEx(&cfg, k_ce_gemm<MODE, 1>, a, b, d, p);
+}
+
+int few_rows(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }   // NT of up to CE_FEW rows
+template <int MODE>
+cudaError_t ce_launch_few(int64_t T, int64_t units, const CeDevice& dev, const CUtensorMap& a, const CUtensorMap& b,
+                          const CeParams& p, cudaStream_t stream, int* ctas = nullptr) {
+  auto go = [&](auto nt, auto kernel) {
+    using S = FewShape<decltype(nt)::value>;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, S::PER_SM * dev.sms));
+    if (ctas != nullptr) *ctas = static_cast<int>(grid);
+    kernel<<<grid, S::THREADS, S::SMEM_BYTES, stream>>>(a, b, p);
+    return cudaGetLastError();
+  };
+  const int nt = few_rows(T);
+  if (nt == 16) return go(std::integral_constant<int, 16>{}, k_ce_few<MODE, 16>);
+  if (nt == 32) return go(std::integral_constant<int, 32>{}, k_ce_few<MODE, 32>);
+  return go(std::integral_constant<int, 64>{}, k_ce_few<MODE, 64>);
 }
 
 constexpr int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -788,24 +1167,31 @@ struct CeBwdWs {
   size_t row_map, xp, dz, acc, total;
   int64_t t_pad, piece, pieces;
   int splits;
+  bool few;
 };
 constexpr int CE_MAX_SPLITS = 16;
 CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   CeBwdWs w{};
-  w.t_pad = up(T, 256) * 256;
+  w.few = T <= CE_FEW;
+  w.t_pad = w.few ? few_rows(T) : up(T, 256) * 256;
   const int64_t most = std::max(CE_MIN_PIECE, CE_DZ_ELEMS / std::max<int64_t>(w.t_pad, 256) / 256 * 256);
   w.pieces = up(V, most);
   w.piece = up(up(V, w.pieces), 256) * 256;
   w.pieces = up(V, w.piece);
   // dx has few tiles where there are few rows: K is shared out so that about 152 CTAs have work
+  // (few rows: two CTAs per SM of up to 32 rows)
   const int64_t tiles = up(T, 128) * up(H, 128);
-  w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({CE_MAX_SPLITS, 152 / std::max<int64_t>(tiles, 1),
+  if (w.few)
+    w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((w.t_pad < 64 ? 304 : 152) / tiles,
+                                                                       up(w.piece, 4 * CE_BK))));
+  else
+    w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({CE_MAX_SPLITS, 152 / std::max<int64_t>(tiles, 1),
                                                                       up(w.piece, 8 * CE_BK)})));
   w.row_map = sizeof(CeMeta);
   w.xp = up256(w.row_map + static_cast<size_t>(w.t_pad) * 4);
   w.dz = up256(w.xp + static_cast<size_t>(w.t_pad) * H * 2);
   w.acc = up256(w.dz + static_cast<size_t>(w.t_pad) * w.piece * 2);
-  w.total = up256(w.acc + (w.pieces > 1 || w.splits > 1 ? static_cast<size_t>(w.splits) * w.t_pad * H * 4 : 0));
+  w.total = up256(w.acc + (w.few || w.pieces > 1 || w.splits > 1 ? static_cast<size_t>(w.splits) * w.t_pad * H * 4 : 0));
   return w;
 }
 
@@ -842,7 +1228,8 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   if (T == 0) return MXFP8_OK;
   CeDevice dev;
   if (!ce_device(&dev)) return MXFP8_ERR_CUDA;
-  const bool pair = use_pair(dev, T, V);
+  const bool few = T <= CE_FEW;
+  const bool pair = !few && use_pair(dev, T, V);
   const int64_t tile = pair ? 256 : 128;
   CeParams p{};
   p.meta = reinterpret_cast<CeMeta*>(base);
@@ -858,11 +1245,14 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   p.pitch = ws.pitch;
   p.timeout_ns = ce_wait_ns();
   CUtensorMap a, b;
-  if (!ce_kmajor(&a, x, T, H, H) || !ce_kmajor(&b, w, V, H, H)) return MXFP8_ERR_CUDA;
-  if (ce_launch<CE_LSE>(pair, up(T, tile) * up(V, tile), dev, a, b, a, p, st) != cudaSuccess) return MXFP8_ERR_CUDA;
+  if (!ce_kmajor(&a, x, T, H, H, few ? few_rows(T) : CE_HALF) || !ce_kmajor(&b, w, V, H, H)) return MXFP8_ERR_CUDA;
+  int parts = static_cast<int>(2 * up(V, tile));
+  const cudaError_t e = few ? ce_launch_few<CE_LSE>(T, up(V, 128), dev, b, a, p, st, &parts)
+                            : ce_launch<CE_LSE>(pair, up(T, tile) * up(V, tile), dev, a, b, a, p, st);
+  if (e != cudaSuccess) return MXFP8_ERR_CUDA;
   int width = 32;
   while (width > 1 && width / 2 >= T) width /= 2;
-  k_ce_merge<<<static_cast<unsigned>(up(T, width)), 256, 0, st>>>(p, static_cast<int>(2 * up(V, tile)), width, loss, lse);
+  k_ce_merge<<<static_cast<unsigned>(up(T, width)), CE_MERGE_THREADS, 0, st>>>(p, parts, width, loss, lse);
   return cudaGetLastError() == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
 }
 
@@ -907,7 +1297,7 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.dloss = dloss;
   p.dlse = dlse;
   p.pitch = ws.t_pad;
-  p.acc = ws.pieces > 1 || ws.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
+  p.acc = ws.few || ws.pieces > 1 || ws.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
   p.dx = static_cast<uint16_t*>(dx);
   p.timeout_ns = ce_wait_ns();
   k_ce_rows<<<1, 1024, 0, st>>>(p, T, const_cast<int32_t*>(p.row_map));
@@ -915,8 +1305,11 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   k_ce_pack<<<rows_grid, 256, 0, st>>>(p, static_cast<const uint4*>(x), T, ws.t_pad, reinterpret_cast<uint4*>(xp));
   if (cudaGetLastError() != cudaSuccess) return MXFP8_ERR_CUDA;
   CUtensorMap x_k, x_mn, w_k, w_mn, dz_k, dz_mn, dz_st;
-  if (!ce_kmajor(&x_k, xp, ws.t_pad, H, H) || !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) ||
-      !ce_mnmajor(&w_mn, w, V, H, H) || !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece) ||
+  const int box = ws.few ? static_cast<int>(ws.t_pad) : CE_HALF;
+  p.dz = dz;
+  p.dz_pitch = ws.piece;
+  if (!ce_kmajor(&x_k, xp, ws.t_pad, H, H, box) || !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) ||
+      !ce_mnmajor(&w_mn, w, V, H, H) || !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece, box) ||
       !ce_mnmajor(&dz_mn, dz, ws.t_pad, ws.piece, ws.piece) || !ce_store(&dz_st, dz, ws.t_pad, ws.piece, ws.piece))
     return MXFP8_ERR_CUDA;
   for (int64_t i = 0; i < ws.pieces; ++i) {
@@ -930,7 +1323,8 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     p.group_m = group_of(H * 2, dz_pair, up(T, zt));
     p.d_rows = static_cast<int>(ws.t_pad);
     p.d_cols = static_cast<int>(ws.piece);
-    if (ce_launch<CE_DZ>(dz_pair, up(T, zt) * up(cols, zt), dev, x_k, w_k, dz_st, p, st) != cudaSuccess)
+    if ((ws.few ? ce_launch_few<CE_DZ>(T, up(cols, 128), dev, w_k, x_k, p, st)
+                : ce_launch<CE_DZ>(dz_pair, up(T, zt) * up(cols, zt), dev, x_k, w_k, dz_st, p, st)) != cudaSuccess)
       return MXFP8_ERR_CUDA;
     CUtensorMap dw_st;
     if (!ce_store(&dw_st, static_cast<uint16_t*>(dw) + v0 * H, cols, H, H)) return MXFP8_ERR_CUDA;
@@ -942,7 +1336,9 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     p.group_m = 1;
     p.split_steps = static_cast<int>(up(up(ws.piece, CE_BK), ws.splits));
     p.splits = static_cast<int>(up(up(cols, CE_BK), p.split_steps));
-    if (ce_launch<CE_DX>(dx_pair, up(T, xt) * up(H, xt) * p.splits, dev, dz_k, w_mn, dz_st, p, st) != cudaSuccess)
+    if ((ws.few ? ce_launch_few<CE_DX>(T, up(H, 128) * p.splits, dev, w_mn, dz_k, p, st)
+                : ce_launch<CE_DX>(dx_pair, up(T, xt) * up(H, xt) * p.splits, dev, dz_k, w_mn, dz_st, p, st)) !=
+        cudaSuccess)
       return MXFP8_ERR_CUDA;
   }
   if (p.acc != nullptr) {
