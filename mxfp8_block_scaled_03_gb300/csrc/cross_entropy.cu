@@ -48,10 +48,11 @@ constexpr int CE_EPI_WARPS = 8;
 constexpr uint32_t CE_BAR_EPI = 1;                 // hardware barrier of the epilogue warps
 constexpr int CE_BUF_BYTES = 2048;                 // a warp's staging tile: 32 rows x 32 bf16; two per warp
 constexpr int CE_EPI_BYTES = CE_EPI_WARPS * 2 * CE_BUF_BYTES;
-constexpr int CE_DATA_BYTES = CE_STAGES * CE_STAGE_BYTES;
-constexpr int CE_BAR_OFFSET = CE_DATA_BYTES + CE_EPI_BYTES;
-constexpr int CE_SMEM_BYTES = CE_BAR_OFFSET + (2 * CE_STAGES + 5) * 8 + 8 + 1024;
-static_assert(CE_SMEM_BYTES <= 232448, "shared memory budget");
+constexpr int ce_smem_bytes(int stages) {
+  return stages * CE_STAGE_BYTES + CE_EPI_BYTES + (2 * stages + 5) * 8 + 8 + 1024;
+}
+constexpr int CE_SHORT = 2;                        // stages where K is one step (dw of few rows): two CTAs per SM
+static_assert(ce_smem_bytes(CE_STAGES) <= 232448 && ce_smem_bytes(CE_SHORT) <= 115712, "shared memory budget");
 constexpr int CE_CHUNK = 16;                       // CE_LSE: K steps that the tensor core sums before fp32 adds take over
 constexpr uint32_t CE_REGS_LOW = 56, CE_REGS_HIGH = 224;   // CE_LSE: warps 0-3, epilogue warps
 static_assert(128 * CE_REGS_LOW + 256 * CE_REGS_HIGH == CE_THREADS * 168, "register split must equal the launch pool");
@@ -66,7 +67,8 @@ enum { CE_LSE = 0, CE_DZ = 1, CE_DW = 2, CE_DX = 3 };
 struct CeMeta {
   uint32_t error;
   int32_t n;          // rows that take part (backward)
-  int32_t reserved[62];
+  int32_t splits;     // shares of the vocabulary in dx
+  int32_t reserved[61];
 };
 static_assert(sizeof(CeMeta) == 256, "header");
 
@@ -77,7 +79,8 @@ struct CeParams {
   int V, v0, vcols;            // vocabulary; first entry and entries of this piece
   int H;
   int group_m;                 // row tiles that share a column tile before the next one is taken
-  int splits, split_steps;     // CE_DX: K steps of each share of the piece
+  int few_splits;              // few rows, CE_DX: shares of the piece
+  int piece_steps;             // CE_DX: K steps of a whole piece, dealt out to meta->splits shares
   const void* targets;
   int wide_targets;
   const float* lse;
@@ -92,6 +95,7 @@ struct CeParams {
   int64_t dz_pitch;
   int d_rows, d_cols;          // CE_DZ, CE_DW: extent of the map that is stored to
   uint16_t* dx;
+  uint32_t* status;            // forward: an error word per CTA, joined by k_ce_merge; backward: NULL, meta->error
   uint64_t timeout_ns;
 };
 
@@ -100,6 +104,14 @@ __device__ __forceinline__ float ex2(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+__device__ __forceinline__ void ce_report(const CeParams& p, uint32_t bits) {
+  atomicOr(p.status != nullptr ? p.status + blockIdx.x : &p.meta->error, bits);
+}
+// Programmatic dependent launches: every kernel of a call lets the next one start its set-up at once, and waits for
+// the one before it (and so for all of them) before it touches what that one reads or writes.  dw needs nothing of dx,
+// the kernel before it, and runs beside its end: dx lets it start once dz is complete, and dw waits for dx when it is done.
+__device__ __forceinline__ void ce_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void ce_wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ int64_t ce_target(const CeParams& p, int64_t row) {
   return p.wide_targets ? __ldg(static_cast<const long long*>(p.targets) + row)
                         : static_cast<int64_t>(__ldg(static_cast<const int32_t*>(p.targets) + row));
@@ -156,8 +168,16 @@ __device__ __forceinline__ void ce_tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
+template <int MODE>
+__device__ __forceinline__ void ce_start() {
+  if (MODE == CE_DX) ce_wait_before();
+  ce_dependents();
+  if (MODE == CE_DZ) ce_wait_before();
+}
+
 struct CeUnits {
-  int nm, nn, splits, steps;   // row tiles, column tiles, shares of K, K steps in all
+  int nm, nn, steps;           // row tiles, column tiles, K steps in all
+  int split_steps;             // CE_DX: K steps of a share
   int total;
 };
 template <int MODE, int CG>
@@ -165,7 +185,7 @@ __device__ __forceinline__ CeUnits ce_units(const CeParams& p) {
   constexpr int TILE = CE_HALF * CG;
   auto up = [](int a, int b) { return (a + b - 1) / b; };
   CeUnits c;
-  c.splits = 1;
+  int splits = 1;
   if (MODE == CE_LSE) {
     c.nm = up(p.rows, TILE);
     c.nn = up(p.V, TILE);
@@ -182,9 +202,13 @@ __device__ __forceinline__ CeUnits ce_units(const CeParams& p) {
     c.nm = up(p.meta->n, TILE);
     c.nn = up(p.H, TILE);
     c.steps = up(p.vcols, CE_BK);
-    c.splits = p.splits;
   }
-  c.total = c.nm * c.nn * c.splits;
+  c.split_steps = c.steps;
+  if (MODE == CE_DX) {
+    c.split_steps = up(p.piece_steps, p.meta->splits);
+    splits = up(c.steps, c.split_steps);
+  }
+  c.total = c.nm * c.nn * splits;
   return c;
 }
 struct CeTile {
@@ -202,8 +226,8 @@ __device__ __forceinline__ CeTile ce_tile(int u, const CeUnits& c, const CeParam
   const int w = w0 - g * p.group_m * c.nn;
   t.n = w / in_g;
   t.m = g * p.group_m + (w - t.n * in_g);
-  t.k0 = MODE == CE_DX ? t.split * p.split_steps : 0;
-  t.steps = MODE == CE_DX ? min(p.split_steps, c.steps - t.k0) : c.steps;
+  t.k0 = MODE == CE_DX ? t.split * c.split_steps : 0;
+  t.steps = MODE == CE_DX ? min(c.split_steps, c.steps - t.k0) : c.steps;
   return t;
 }
 
@@ -214,7 +238,7 @@ __device__ __forceinline__ bool ce_wait(uint64_t* bar, uint32_t parity, bool clu
   if (CG == 2 && cluster_scope ? mbar_wait_cluster_bounded(bar, parity, abort, p.timeout_ns)
                                : mbar_wait_bounded(bar, parity, abort, p.timeout_ns))
     return true;
-  atomicOr(&p.meta->error, err_bit);
+  ce_report(p, err_bit);
   *abort = 1;
   if (CG == 2) st_remote_u32(peer_abort, 1u);
   return false;
@@ -223,8 +247,8 @@ __device__ __forceinline__ bool ce_wait(uint64_t* bar, uint32_t parity, bool clu
 // CG = 1: a CTA computes tiles of 128 x 128.  CG = 2: a CTA pair computes tiles of 256 x 256, each CTA with 128 rows
 // of A and of B in its shared memory and 128 rows of the result in its TMEM.  Either way a stage is 32 KB per CTA and
 // the accumulators are double-buffered, so that an epilogue runs beside the next tile's products.
-template <int MODE, int CG>
-__global__ void __launch_bounds__(CE_THREADS, 1)
+template <int MODE, int CG, int STAGES>
+__global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
     k_ce_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmD, const CeParams p) {
   constexpr bool A_MN = MODE == CE_DW, B_MN = MODE == CE_DW || MODE == CE_DX;
@@ -234,9 +258,9 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
   constexpr int CHUNK = MODE == CE_LSE ? CE_CHUNK : 1 << 30;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + CE_BAR_OFFSET);
-  uint64_t* empty = full + CE_STAGES;
-  uint64_t* acc_full = empty + CE_STAGES;           // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * CE_STAGE_BYTES + CE_EPI_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;           // [2]
   uint64_t* acc_empty = acc_full + 2;               // [2]
   uint64_t* drained = acc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
@@ -248,7 +272,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
   const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < CE_STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -258,6 +282,10 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
+    if (p.status != nullptr) {                      // (the forward's first kernel: nothing else writes these yet)
+      p.status[blockIdx.x] = 0u;
+      if (blockIdx.x == 0) p.meta->error = 0u;
+    }
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -275,6 +303,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
   if (CG == 2) cluster_sync_all();                  // the peer's barriers exist before anything arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  ce_start<MODE>();
   const CeUnits units = ce_units<MODE, CG>(p);
   const int first = CG == 2 ? static_cast<int>(cluster_index()) : static_cast<int>(blockIdx.x);
   const int stride = CG == 2 ? static_cast<int>(cluster_count()) : static_cast<int>(gridDim.x);
@@ -324,7 +353,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
             if (leader) mbar_arrive_expect_tx(&full[stage], CG * CE_STAGE_BYTES);
             prod_issued |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-            if (++stage == CE_STAGES) {
+            if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
             }
@@ -333,10 +362,10 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
         // Copies land before the CTA exits: the leader waits for its stages (their barriers count both CTAs' copies);
         // the second CTA's wait for the leader is the pair's closing barriers below.
         if (leader)
-          for (int s = 0; s < CE_STAGES; ++s)
+          for (int s = 0; s < STAGES; ++s)
             if ((prod_issued >> s) & 1u)
               if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
-                atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+                ce_report(p, ERR_TIMEOUT_DRAIN);
       }
       __syncwarp();
     } else if (warp == CE_WARP_MMA && leader) {
@@ -372,7 +401,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
             if constexpr (CG == 2) tc_commit_pair_both(&empty[stage]);
             else tc_commit(&empty[stage]);
             issued = true;
-            if (++stage == CE_STAGES) {
+            if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
             }
@@ -387,7 +416,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
         if (issued) {
           if constexpr (CG == 2) tc_commit_pair_local(drained);
           else tc_commit(drained);
-          if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+          if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
         }
       }
       __syncwarp();
@@ -398,7 +427,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
     const int quarter = warp & 3;
     const int half = (warp - CE_EPI_WARP0) >> 2;
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + NH * half;
-    uint8_t* wbuf = smem + CE_DATA_BYTES + (warp - CE_EPI_WARP0) * 2 * CE_BUF_BYTES;
+    uint8_t* wbuf = smem + STAGES * CE_STAGE_BYTES + (warp - CE_EPI_WARP0) * 2 * CE_BUF_BYTES;
     const int n_rows = MODE == CE_LSE ? p.rows : MODE == CE_DW ? 0 : p.meta->n;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -565,6 +594,7 @@ __global__ void __launch_bounds__(CE_THREADS, 1)
     if ((MODE == CE_DZ || MODE == CE_DW) && lane == 0) bulk_wait_all();   // stores complete before exit
   }
 
+  if (MODE == CE_DW) ce_wait_before();
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) {
@@ -641,6 +671,10 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
+    if (p.status != nullptr) {                      // (the forward's first kernel: nothing else writes these yet)
+      p.status[blockIdx.x] = 0u;
+      if (blockIdx.x == 0) p.meta->error = 0u;
+    }
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -652,18 +686,37 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  // (the copying thread waits later, see there)
+  if (threadIdx.x != 0) ce_start<MODE>();
   // units: 128 vocabulary entries each, or (share of the piece, 128 columns of dx)
   const int tiles = MODE == CE_DX ? (p.H + 127) / 128 : (p.vcols + 127) / 128;
   const int k_steps = MODE == CE_DX ? (p.vcols + CE_BK - 1) / CE_BK : (p.H + CE_BK - 1) / CE_BK;
-  const int total = MODE == CE_DX ? tiles * p.splits : tiles;
-  auto k_begin = [&](int u) { return MODE == CE_DX ? u / tiles * p.split_steps : 0; };
-  auto k_end = [&](int u) { return MODE == CE_DX ? min(k_steps, (u / tiles + 1) * p.split_steps) : k_steps; };
+  const int split_steps = MODE == CE_DX ? (p.piece_steps + p.few_splits - 1) / p.few_splits : k_steps;
+  const int total = MODE == CE_DX ? tiles * ((k_steps + split_steps - 1) / split_steps) : tiles;
+  auto k_begin = [&](int u) { return MODE == CE_DX ? u / tiles * split_steps : 0; };
+  auto k_end = [&](int u) { return MODE == CE_DX ? min(k_steps, (u / tiles + 1) * split_steps) : k_steps; };
 
   if (warp == 0) {
     // ---------------- tile copies (one lane) ----------------
     if (lane == 0) {
+      // The weights' copies of the first stages need nothing of the kernel before (row packing, dz): they are on their
+      // way while it ends.
+      const int k_first = k_begin(blockIdx.x);
+      const int early = MODE == CE_LSE ? 0 : min(S::STAGES, k_end(blockIdx.x) - k_first);
+      auto load_w = [&](int stage, int m0, int ks) {
+        uint8_t* sA = smem + stage * S::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full[stage], S::STAGE_BYTES);
+        if (A_MN) {
+          tma_load_2d(sA, &tmA, &full[stage], m0, p.v0 + ks * CE_BK);
+          tma_load_2d(sA + CE_OP_BYTES / 2, &tmA, &full[stage], m0 + 64, p.v0 + ks * CE_BK);
+        } else {
+          tma_load_2d(sA, &tmA, &full[stage], ks * CE_BK, p.v0 + m0);
+        }
+      };
+      for (int s = 0; s < early; ++s) load_w(s, (MODE == CE_DX ? blockIdx.x % tiles : blockIdx.x) * 128, k_first + s);
+      ce_start<MODE>();
       uint32_t issued = 0, issued_parity = 0;
-      int stage = 0;
+      int stage = 0, ahead = early;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
@@ -674,15 +727,9 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
             ok = false;
             break;
           }
-          uint8_t* sA = smem + stage * S::STAGE_BYTES;
-          mbar_arrive_expect_tx(&full[stage], S::STAGE_BYTES);
-          if (A_MN) {
-            tma_load_2d(sA, &tmA, &full[stage], m0, p.v0 + ks * CE_BK);
-            tma_load_2d(sA + CE_OP_BYTES / 2, &tmA, &full[stage], m0 + 64, p.v0 + ks * CE_BK);
-          } else {
-            tma_load_2d(sA, &tmA, &full[stage], ks * CE_BK, p.v0 + m0);
-          }
-          tma_load_2d(sA + CE_OP_BYTES, &tmB, &full[stage], ks * CE_BK, 0);
+          if (ahead > 0) --ahead;
+          else load_w(stage, m0, ks);
+          tma_load_2d(smem + stage * S::STAGE_BYTES + CE_OP_BYTES, &tmB, &full[stage], ks * CE_BK, 0);
           issued |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == S::STAGES) {
@@ -694,7 +741,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
       for (int s = 0; s < S::STAGES; ++s)           // copies land before the CTA exits
         if ((issued >> s) & 1u)
           if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
-            atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+            ce_report(p, ERR_TIMEOUT_DRAIN);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -741,7 +788,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
       }
       if (issued) {
         tc_commit(drained);
-        if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) atomicOr(&p.meta->error, ERR_TIMEOUT_DRAIN);
+        if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
       }
     }
     __syncwarp();
@@ -881,7 +928,8 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
 // Joins the parts of each row: the CTA takes `width` rows (a power of two up to 32), its threads equal shares of the
 // parts.
 constexpr int CE_MERGE_THREADS = 512;
-__global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p, int parts, int width, float* loss, float* lse) {
+__global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p, int parts, int width, int statuses, float* loss,
+                                                               float* lse) {
   __shared__ float2 s[CE_MERGE_THREADS];
   const int r = threadIdx.x % width, share = threadIdx.x / width, shares = CE_MERGE_THREADS / width;
   const int row = blockIdx.x * width + r;
@@ -892,8 +940,14 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
     sum = sum * ex2(m - base) + o.y * ex2(o.x - base);
     m = m_new;
   };
+  ce_wait_before();
+  if (blockIdx.x == 0) {
+    uint32_t bits = 0;
+    for (int i = threadIdx.x; i < statuses; i += CE_MERGE_THREADS) bits |= p.status[i];
+    if (bits != 0) atomicOr(&p.meta->error, bits);
+  }
   if (row < p.rows) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = share; i < parts; i += shares) join(__ldcs(p.part + i * p.pitch + row));
   }
   s[threadIdx.x] = make_float2(m, sum);
@@ -919,16 +973,57 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
   }
 }
 
+// Shares of the vocabulary in dx, from the rows that take part: as many as deal the K steps out evenly to `workers` CTAs
+// (or pairs), a share's fixed cost counted as CE_SHARE_STEPS steps.
+constexpr int CE_SHARE_STEPS = 8;
+__device__ __forceinline__ int ce_splits(int units, int steps, int workers, int most) {   // a whole warp; most <= 32
+  const int s = 1 + (threadIdx.x & 31);
+  const int64_t waves = (static_cast<int64_t>(units) * s + workers - 1) / workers;
+  const int64_t c = waves * ((steps + s - 1) / s + CE_SHARE_STEPS);
+  const uint32_t cost = s <= most && s <= steps && c < INT_MAX ? static_cast<uint32_t>(c) : INT_MAX;
+  const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, cost);
+  return __ffs(__ballot_sync(0xFFFFFFFFu, cost == least));
+}
+struct CePack {
+  const uint4* x;
+  uint4* xp;
+  int32_t* row_map;
+  int T, t_pad;
+  int dx_tile, dx_workers, dx_most;   // ce_splits; few rows: dx_most shares (dx_workers 0)
+};
+__device__ __forceinline__ void ce_put_meta(const CeParams& p, const CePack& q, int n, bool bad) {   // warp 0
+  int splits = q.dx_most;
+  if (q.dx_workers > 0) {
+    const int units = (n + q.dx_tile - 1) / q.dx_tile * ((p.H + q.dx_tile - 1) / q.dx_tile);
+    splits = ce_splits(units, p.piece_steps, q.dx_workers, q.dx_most);
+  }
+  if (threadIdx.x == 0) {
+    p.meta->n = n;
+    p.meta->error = bad ? ERR_TARGET_RANGE : 0u;
+    p.meta->splits = splits;
+  }
+}
+// xp[i] = x[src] for i < n, zeros up to t_pad; dx of a row that takes no part is zero.
+__device__ __forceinline__ void ce_pack_row(const CeParams& p, const CePack& q, int i, int src, int n) {
+  const int64_t per_row = p.H / 8;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int c = threadIdx.x; c < per_row; c += blockDim.x) {
+    if (i < q.t_pad) q.xp[i * per_row + c] = i < n ? __ldcs(q.x + src * per_row + c) : zero;
+    if (i >= n && i < q.T) reinterpret_cast<uint4*>(p.dx)[src * per_row + c] = zero;
+  }
+}
+
 // row_map: the rows that take part in order, then the others in order; their number.  One CTA.
-__global__ void __launch_bounds__(1024) k_ce_rows(const CeParams p, int64_t T, int32_t* row_map) {
+__global__ void __launch_bounds__(1024) k_ce_rows(const CeParams p, const CePack q) {
   __shared__ int s_warp[32];
   __shared__ int s_bad;
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
-  const int per = static_cast<int>((T + 1023) / 1024);
-  const int64_t t0 = static_cast<int64_t>(threadIdx.x) * per, t1 = min(T, t0 + per);
+  ce_dependents();
+  const int per = (q.T + 1023) / 1024;
+  const int t0 = min(q.T, static_cast<int>(threadIdx.x) * per), t1 = min(q.T, t0 + per);
   int mine = 0;
-  for (int64_t t = t0; t < t1; ++t) {
+  for (int t = t0; t < t1; ++t) {
     const int64_t y = ce_target(p, t);
     mine += y >= 0 && y < p.V;
     if (y >= p.V) s_bad = 1;
@@ -945,53 +1040,101 @@ __global__ void __launch_bounds__(1024) k_ce_rows(const CeParams p, int64_t T, i
     if (w < static_cast<int>(threadIdx.x >> 5)) before += s_warp[w];
     n += s_warp[w];
   }
-  int64_t other = n + t0 - before;            // rows before t0 that take no part come first
-  for (int64_t t = t0; t < t1; ++t) {
+  int other = n + t0 - before;                // rows before t0 that take no part come first
+  for (int t = t0; t < t1; ++t) {
     const int64_t y = ce_target(p, t);
-    if (y >= 0 && y < p.V) row_map[before++] = static_cast<int32_t>(t);
-    else row_map[other++] = static_cast<int32_t>(t);
+    if (y >= 0 && y < p.V) q.row_map[before++] = t;
+    else q.row_map[other++] = t;
   }
-  if (threadIdx.x == 0) {
-    p.meta->n = n;
-    p.meta->error = s_bad ? ERR_TARGET_RANGE : 0u;
+  if (threadIdx.x < 32) ce_put_meta(p, q, n, s_bad != 0);
+}
+__global__ void __launch_bounds__(256) k_ce_pack(const CeParams p, const CePack q) {
+  ce_dependents();
+  ce_wait_before();
+  const int n = p.meta->n;
+  for (int i = blockIdx.x; i < max(q.t_pad, q.T); i += gridDim.x) ce_pack_row(p, q, i, i < q.T ? q.row_map[i] : 0, n);
+}
+// Both for up to CE_PREP_ROWS rows: every CTA makes the map for itself, the first one writes it.
+constexpr int CE_PREP_ROWS = 1024;
+__global__ void __launch_bounds__(256) k_ce_prep(const CeParams p, const CePack q) {
+  __shared__ int s_map[CE_PREP_ROWS];
+  __shared__ int s_warp[8];
+  __shared__ int s_bad;
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  ce_dependents();
+  const int t0 = 4 * threadIdx.x;
+  bool in[4];
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t y = t0 + j < q.T ? ce_target(p, t0 + j) : -1;
+    in[j] = y >= 0 && y < p.V;
+    mine += in[j];
+    if (y >= p.V) s_bad = 1;
   }
+  int scan = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if ((threadIdx.x & 31) >= o) scan += a;
+  }
+  if ((threadIdx.x & 31) == 31) s_warp[threadIdx.x >> 5] = scan;
+  __syncthreads();
+  int before = scan - mine, n = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < static_cast<int>(threadIdx.x >> 5)) before += s_warp[w];
+    n += s_warp[w];
+  }
+  int other = n + t0 - before;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (t0 + j < q.T) s_map[in[j] ? before++ : other++] = t0 + j;
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < q.T; i += 256) q.row_map[i] = s_map[i];
+    if (threadIdx.x < 32) ce_put_meta(p, q, n, s_bad != 0);
+  }
+  for (int i = blockIdx.x; i < max(q.t_pad, q.T); i += gridDim.x) ce_pack_row(p, q, i, i < q.T ? s_map[i] : 0, n);
 }
 
-// Packed rows: xp[i] = x[row_map[i]] for i < n, zeros up to T_pad; dx of the rows that take no part is zero.
-__global__ void __launch_bounds__(256) k_ce_pack(const CeParams p, const uint4* x, int64_t T, int64_t t_pad, uint4* xp) {
-  const int n = p.meta->n;
-  const int per_row = p.H / 8;
-  for (int64_t i = blockIdx.x; i < t_pad; i += gridDim.x) {
-    const int src = i < T ? p.row_map[i] : 0;
-    for (int c = threadIdx.x; c < per_row; c += 256) {
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      xp[i * per_row + c] = i < n ? __ldcs(x + static_cast<int64_t>(src) * per_row + c) : zero;
-      if (i >= n && i < T) reinterpret_cast<uint4*>(p.dx)[static_cast<int64_t>(src) * per_row + c] = zero;
+// dx of the packed rows from their fp32 parts, added in a fixed order: a thread has four columns, of eight or more shares
+// every eighth (38 in a row took 7 us for 5 x 1024 values).
+constexpr int CE_DX_THREADS = 256;
+__global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int steps) {
+  __shared__ float4 s_sum[CE_DX_THREADS];
+  ce_wait_before();
+  const int split_steps = (p.piece_steps + p.meta->splits - 1) / p.meta->splits;
+  const int splits = (steps + split_steps - 1) / split_steps;   // of the first piece; a shorter last one has no more
+  const int slices = splits >= 8 ? 8 : 1, width = CE_DX_THREADS / slices;
+  const int slice = threadIdx.x / width, lane = threadIdx.x % width;
+  const int per_row = p.H / 4;
+  const int64_t total = static_cast<int64_t>(p.meta->n) * per_row;
+  for (int64_t e0 = blockIdx.x * int64_t(width); e0 < total; e0 += gridDim.x * int64_t(width)) {
+    const int64_t e = e0 + lane;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float4 o) {
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    };
+    const int64_t i = e / per_row;
+    const int c = static_cast<int>(e - i * per_row);
+    if (e < total) {
+      const float4* a = reinterpret_cast<const float4*>(p.acc) + i * per_row + c;
+#pragma unroll 8
+      for (int s = slice; s < splits; s += slices) add(__ldcs(a + s * p.pitch * per_row));
     }
-  }
-}
-
-// dx of the packed rows from their fp32 parts, added in order.
-__global__ void __launch_bounds__(256) k_ce_dx(const CeParams p) {
-  const int n = p.meta->n;
-  const int per_row = p.H / 8;
-  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
-    const int src = p.row_map[i];
-    for (int c = threadIdx.x; c < per_row; c += 256) {
-      float v[8] = {};
-      for (int s = 0; s < p.splits; ++s) {
-        const float4* a = reinterpret_cast<const float4*>(p.acc + (s * p.pitch + i) * p.H) + 2 * c;
-        const float4 lo = __ldcs(a), hi = __ldcs(a + 1);
-        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
-      }
-      uint4 o;
-      o.x = pack_bf16x2(v[0], v[1]);
-      o.y = pack_bf16x2(v[2], v[3]);
-      o.z = pack_bf16x2(v[4], v[5]);
-      o.w = pack_bf16x2(v[6], v[7]);
-      reinterpret_cast<uint4*>(p.dx)[static_cast<int64_t>(src) * per_row + c] = o;
+    if (slices > 1) {
+      __syncthreads();
+      s_sum[threadIdx.x] = v;
+      __syncthreads();
+      if (slice == 0)
+        for (int q = 1; q < slices; ++q) add(s_sum[q * width + lane]);
     }
+    if (slice == 0 && e < total)
+      reinterpret_cast<uint2*>(p.dx)[static_cast<int64_t>(p.row_map[i]) * per_row + c] =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
 }
 
@@ -1036,22 +1179,35 @@ struct CeDevice {
   int pairs = 0;               // CTA pairs that run at the same time (0: none)
 };
 
-template <int MODE, int CG>
-cudaLaunchConfig_t ce_config(int units, cudaLaunchAttribute* attr, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  if (CG == 2) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+// Launch with programmatic dependence on the kernel before (all but a call's first) and, for pairs, clusters of two.
+template <typename... Params, typename... Args>
+cudaError_t ce_go(void (*kernel)(Params...), int64_t grid, int threads, size_t smem, cudaStream_t stream, bool first,
+                  bool pair, Args... args) {
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (!first) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
   }
-  cfg.gridDim = dim3(CG * units, 1, 1);
-  cfg.blockDim = dim3(CE_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = CE_SMEM_BYTES;
+  if (pair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  return cfg;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <int MODE, int CG, int STAGES>
+bool ce_prepare() {
+  return cudaFuncSetAttribute(k_ce_gemm<MODE, CG, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              ce_smem_bytes(STAGES)) == cudaSuccess;
 }
 template <int MODE>
 bool ce_prepare_few() {
@@ -1060,11 +1216,6 @@ bool ce_prepare_few() {
   };
   return set(k_ce_few<MODE, 16>, FewShape<16>::SMEM_BYTES) && set(k_ce_few<MODE, 32>, FewShape<32>::SMEM_BYTES) &&
          set(k_ce_few<MODE, 64>, FewShape<64>::SMEM_BYTES);
-}
-template <int MODE, int CG>
-bool ce_prepare() {
-  return cudaFuncSetAttribute(k_ce_gemm<MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, CE_SMEM_BYTES) ==
-         cudaSuccess;
 }
 bool ce_device(CeDevice* out) {
   static CeDevice info[64];
@@ -1076,12 +1227,24 @@ bool ce_device(CeDevice* out) {
   if (d.sms == 0) {
     int sms = 0, pairs = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return false;
-    if (!ce_prepare<CE_LSE, 1>() || !ce_prepare<CE_DZ, 1>() || !ce_prepare<CE_DW, 1>() || !ce_prepare<CE_DX, 1>() ||
-        !ce_prepare_few<CE_LSE>() || !ce_prepare_few<CE_DZ>() || !ce_prepare_few<CE_DX>() || !ce_prepare<CE_LSE, 2>() || !ce_prepare<CE_DZ, 2>() || !ce_prepare<CE_DW, 2>() || !ce_prepare<CE_DX, 2>())
+    constexpr int ST = CE_STAGES;
+    if (!ce_prepare<CE_LSE, 1, ST>() || !ce_prepare<CE_DZ, 1, ST>() || !ce_prepare<CE_DW, 1, ST>() ||
+        !ce_prepare<CE_DX, 1, ST>() || !ce_prepare<CE_LSE, 2, ST>() || !ce_prepare<CE_DZ, 2, ST>() ||
+        !ce_prepare<CE_DW, 2, ST>() || !ce_prepare<CE_DX, 2, ST>() || !ce_prepare<CE_DW, 1, CE_SHORT>() ||
+        !ce_prepare_few<CE_LSE>() || !ce_prepare_few<CE_DZ>() || !ce_prepare_few<CE_DX>())
       return false;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = ce_config<CE_LSE, 2>(64, attr, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&pairs, k_ce_gemm<CE_LSE, 2>, &cfg) != cudaSuccess) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(128, 1, 1);
+    cfg.blockDim = dim3(CE_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = ce_smem_bytes(ST);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&pairs, k_ce_gemm<CE_LSE, 2, ST>, &cfg) != cudaSuccess) {
       cudaGetLastError();   // clear: single CTAs are used instead
       pairs = 0;
     }
@@ -1094,14 +1257,11 @@ bool ce_device(CeDevice* out) {
 
 template <int MODE>
 cudaError_t ce_launch(bool pair, int64_t units, const CeDevice& dev, const CUtensorMap& a, const CUtensorMap& b,
-                      const CUtensorMap& d, const CeParams& p, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  if (pair) {
-    cudaLaunchConfig_t cfg = ce_config<MODE, 2>(static_cast<int>(std::min<int64_t>(units, dev.pairs)), attr, stream);
-    return cudaLaunchKernelEx(&cfg, k_ce_gemm<MODE, 2>, a, b, d, p);
-  }
-  cudaLaunchConfig_t cfg = ce_config<MODE, 1>(static_cast<int>(std::min<int64_t>(units, dev.sms)), attr, stream);
-  return cudaLaunchKernelEx(&cfg, k_ce_gemm<MODE, 1>, a, b, d, p);
+                      const CUtensorMap& d, const CeParams& p, cudaStream_t stream, int* ctas = nullptr) {
+  const int64_t grid = pair ? 2 * std::min<int64_t>(units, dev.pairs) : std::min<int64_t>(units, dev.sms);
+  if (ctas != nullptr) *ctas = static_cast<int>(grid);
+  return ce_go(pair ? k_ce_gemm<MODE, 2, CE_STAGES> : k_ce_gemm<MODE, 1, CE_STAGES>, grid, CE_THREADS,
+               ce_smem_bytes(CE_STAGES), stream, MODE == CE_LSE, pair, a, b, d, p);
 }
 
 int few_rows(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }   // NT of up to CE_FEW rows
@@ -1112,8 +1272,7 @@ cudaError_t ce_launch_few(int64_t T, int64_t units, const CeDevice& dev, const C
     using S = FewShape<decltype(nt)::value>;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, S::PER_SM * dev.sms));
     if (ctas != nullptr) *ctas = static_cast<int>(grid);
-    kernel<<<grid, S::THREADS, S::SMEM_BYTES, stream>>>(a, b, p);
-    return cudaGetLastError();
+    return ce_go(kernel, grid, S::THREADS, S::SMEM_BYTES, stream, MODE == CE_LSE, false, a, b, p);
   };
   const int nt = few_rows(T);
   if (nt == 16) return go(std::integral_constant<int, 16>{}, k_ce_few<MODE, 16>);
@@ -1124,8 +1283,14 @@ cudaError_t ce_launch_few(int64_t T, int64_t units, const CeDevice& dev, const C
 constexpr int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// Pairs compute tiles of 256 x 256 where those keep all pairs busy, single CTAs tiles of 128 x 128 otherwise.
-bool use_pair(const CeDevice& dev, int64_t m, int64_t n) { return dev.pairs > 0 && up(m, 256) * up(n, 256) >= dev.pairs; }
+// Pairs compute tiles of 256 x 256, single CTAs tiles of 128 x 128, of which they take two in 1.6 times as long as a CTA of
+// a pair its half tile (their operands are read twice as often).  Whichever is done first.
+bool use_pair(const CeDevice& dev, int64_t m, int64_t n, int64_t splits = 1) {
+  if (dev.pairs <= 0) return false;
+  const int64_t pair = up(up(m, 256) * up(n, 256) * splits, dev.pairs) * 10;
+  const int64_t single = up(up(m, 128) * up(n, 128) * splits, dev.sms) * 8;
+  return pair <= single;
+}
 
 // Row tiles of a group: as many as keep their rows of A (of `bytes` each) within 48 MB of the L2.
 int group_of(int64_t row_bytes, bool pair, int64_t most) {
@@ -1148,15 +1313,17 @@ bool ce_sizes_supported(int64_t T, int64_t H, int64_t V) {
 }
 bool ce_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+constexpr size_t CE_MAX_CTAS = 1024;   // of a launch
 struct CeFwdWs {
-  size_t part, zy, total;
+  size_t status, part, zy, total;
   int64_t pitch, parts;
 };
 CeFwdWs ce_fwd_ws(int64_t T, int64_t V) {
   CeFwdWs w{};
   w.pitch = up(T, 32) * 32;
   w.parts = 2 * up(V, 128);
-  w.part = sizeof(CeMeta);
+  w.status = sizeof(CeMeta);
+  w.part = w.status + CE_MAX_CTAS * sizeof(uint32_t);
   w.zy = up256(w.part + static_cast<size_t>(w.parts) * w.pitch * sizeof(float2));
   w.total = up256(w.zy + static_cast<size_t>(w.pitch) * sizeof(float));
   return w;
@@ -1178,15 +1345,10 @@ CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   w.pieces = up(V, most);
   w.piece = up(up(V, w.pieces), 256) * 256;
   w.pieces = up(V, w.piece);
-  // dx has few tiles where there are few rows: K is shared out so that about 152 CTAs have work
-  // (few rows: two CTAs per SM of up to 32 rows)
+  // dx has few tiles where there are few rows: its K is shared out
   const int64_t tiles = up(T, 128) * up(H, 128);
-  if (w.few)
-    w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((w.t_pad < 64 ? 304 : 152) / tiles,
-                                                                       up(w.piece, 4 * CE_BK))));
-  else
-    w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({CE_MAX_SPLITS, 152 / std::max<int64_t>(tiles, 1),
-                                                                      up(w.piece, 8 * CE_BK)})));
+  const int64_t wanted = w.few ? (w.t_pad < 64 ? 304 : 152) / tiles : tiles >= 8 * 152 ? 1 : CE_MAX_SPLITS;
+  w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(wanted, up(w.piece, 4 * CE_BK))));
   w.row_map = sizeof(CeMeta);
   w.xp = up256(w.row_map + static_cast<size_t>(w.t_pad) * 4);
   w.dz = up256(w.xp + static_cast<size_t>(w.t_pad) * H * 2);
@@ -1224,8 +1386,7 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  if (cudaMemsetAsync(workspace, 0, sizeof(CeMeta), st) != cudaSuccess) return MXFP8_ERR_CUDA;
-  if (T == 0) return MXFP8_OK;
+  if (T == 0) return cudaMemsetAsync(workspace, 0, sizeof(CeMeta), st) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
   CeDevice dev;
   if (!ce_device(&dev)) return MXFP8_ERR_CUDA;
   const bool few = T <= CE_FEW;
@@ -1237,7 +1398,7 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   p.V = p.vcols = static_cast<int>(V);
   p.H = static_cast<int>(H);
   p.group_m = group_of(H * 2, pair, up(T, tile));
-  p.splits = 1;
+  p.status = reinterpret_cast<uint32_t*>(base + ws.status);
   p.targets = targets;
   p.wide_targets = wide_targets;
   p.part = reinterpret_cast<float2*>(base + ws.part);
@@ -1246,14 +1407,18 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   p.timeout_ns = ce_wait_ns();
   CUtensorMap a, b;
   if (!ce_kmajor(&a, x, T, H, H, few ? few_rows(T) : CE_HALF) || !ce_kmajor(&b, w, V, H, H)) return MXFP8_ERR_CUDA;
-  int parts = static_cast<int>(2 * up(V, tile));
-  const cudaError_t e = few ? ce_launch_few<CE_LSE>(T, up(V, 128), dev, b, a, p, st, &parts)
-                            : ce_launch<CE_LSE>(pair, up(T, tile) * up(V, tile), dev, a, b, a, p, st);
+  int ctas = 0;
+  const cudaError_t e = few ? ce_launch_few<CE_LSE>(T, up(V, 128), dev, b, a, p, st, &ctas)
+                            : ce_launch<CE_LSE>(pair, up(T, tile) * up(V, tile), dev, a, b, a, p, st, &ctas);
   if (e != cudaSuccess) return MXFP8_ERR_CUDA;
+  const int parts = few ? ctas : static_cast<int>(2 * up(V, tile));
+  // as many rows per CTA as leave every SM one: 1531 rows of 394 parts took 14.8 us with 32
   int width = 32;
-  while (width > 1 && width / 2 >= T) width /= 2;
-  k_ce_merge<<<static_cast<unsigned>(up(T, width)), CE_MERGE_THREADS, 0, st>>>(p, parts, width, loss, lse);
-  return cudaGetLastError() == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
+  while (width > 1 && up(T, width) < dev.sms) width /= 2;
+  return ce_go(k_ce_merge, up(T, width), CE_MERGE_THREADS, 0, st, false, false, p, parts, width, ctas, loss, lse) ==
+                 cudaSuccess
+             ? MXFP8_OK
+             : MXFP8_ERR_CUDA;
 }
 
 size_t linear_cross_entropy_bwd_workspace_size(int64_t T, int64_t H, int64_t V) {
@@ -1300,10 +1465,25 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.acc = ws.few || ws.pieces > 1 || ws.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
   p.dx = static_cast<uint16_t*>(dx);
   p.timeout_ns = ce_wait_ns();
-  k_ce_rows<<<1, 1024, 0, st>>>(p, T, const_cast<int32_t*>(p.row_map));
-  const unsigned rows_grid = static_cast<unsigned>(std::min<int64_t>(ws.t_pad, 8 * dev.sms));
-  k_ce_pack<<<rows_grid, 256, 0, st>>>(p, static_cast<const uint4*>(x), T, ws.t_pad, reinterpret_cast<uint4*>(xp));
-  if (cudaGetLastError() != cudaSuccess) return MXFP8_ERR_CUDA;
+  const bool dx_pair = !ws.few && use_pair(dev, T, H, ws.splits);
+  p.piece_steps = static_cast<int>(up(ws.piece, CE_BK));
+  p.few_splits = ws.splits;
+  CePack q{};
+  q.x = static_cast<const uint4*>(x);
+  q.xp = reinterpret_cast<uint4*>(xp);
+  q.row_map = reinterpret_cast<int32_t*>(base + ws.row_map);
+  q.T = static_cast<int>(T);
+  q.t_pad = static_cast<int>(ws.t_pad);
+  q.dx_tile = dx_pair ? 256 : 128;
+  q.dx_workers = ws.few ? 0 : dx_pair ? dev.pairs : dev.sms;
+  q.dx_most = ws.splits;
+  const int64_t rows_grid = std::min<int64_t>(std::max(T, ws.t_pad), 8 * dev.sms);
+  if (T <= CE_PREP_ROWS) {
+    if (ce_go(k_ce_prep, rows_grid, 256, 0, st, true, false, p, q) != cudaSuccess) return MXFP8_ERR_CUDA;
+  } else if (ce_go(k_ce_rows, 1, 1024, 0, st, true, false, p, q) != cudaSuccess ||
+             ce_go(k_ce_pack, rows_grid, 256, 0, st, false, false, p, q) != cudaSuccess) {
+    return MXFP8_ERR_CUDA;
+  }
   CUtensorMap x_k, x_mn, w_k, w_mn, dz_k, dz_mn, dz_st;
   const int box = ws.few ? static_cast<int>(ws.t_pad) : CE_HALF;
   p.dz = dz;
@@ -1316,9 +1496,8 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     const int64_t v0 = i * ws.piece, cols = std::min(ws.piece, V - v0);
     p.v0 = static_cast<int>(v0);
     p.vcols = static_cast<int>(cols);
-    p.splits = 1;
     p.acc_add = i > 0;
-    const bool dz_pair = use_pair(dev, T, cols), dw_pair = use_pair(dev, cols, H), dx_pair = use_pair(dev, T, H);
+    const bool dz_pair = use_pair(dev, T, cols), dw_pair = use_pair(dev, cols, H);
     const int64_t zt = dz_pair ? 256 : 128, wt = dw_pair ? 256 : 128, xt = dx_pair ? 256 : 128;
     p.group_m = group_of(H * 2, dz_pair, up(T, zt));
     p.d_rows = static_cast<int>(ws.t_pad);
@@ -1326,27 +1505,26 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     if ((ws.few ? ce_launch_few<CE_DZ>(T, up(cols, 128), dev, w_k, x_k, p, st)
                 : ce_launch<CE_DZ>(dz_pair, up(T, zt) * up(cols, zt), dev, x_k, w_k, dz_st, p, st)) != cudaSuccess)
       return MXFP8_ERR_CUDA;
-    CUtensorMap dw_st;
-    if (!ce_store(&dw_st, static_cast<uint16_t*>(dw) + v0 * H, cols, H, H)) return MXFP8_ERR_CUDA;
     p.group_m = 1;
-    p.d_rows = static_cast<int>(cols);
-    p.d_cols = static_cast<int>(H);
-    if (ce_launch<CE_DW>(dw_pair, up(cols, wt) * up(H, wt), dev, dz_mn, x_mn, dw_st, p, st) != cudaSuccess)
-      return MXFP8_ERR_CUDA;
-    p.group_m = 1;
-    p.split_steps = static_cast<int>(up(up(ws.piece, CE_BK), ws.splits));
-    p.splits = static_cast<int>(up(up(cols, CE_BK), p.split_steps));
-    if ((ws.few ? ce_launch_few<CE_DX>(T, up(H, 128) * p.splits, dev, w_mn, dz_k, p, st)
-                : ce_launch<CE_DX>(dx_pair, up(T, xt) * up(H, xt) * p.splits, dev, dz_k, w_mn, dz_st, p, st)) !=
+    // dx first: few rows leave w in the L2 for it, which dw overwrites
+    if ((ws.few ? ce_launch_few<CE_DX>(T, up(H, 128) * ws.splits, dev, w_mn, dz_k, p, st)
+                : ce_launch<CE_DX>(dx_pair, up(T, xt) * up(H, xt) * ws.splits, dev, dz_k, w_mn, dz_st, p, st)) !=
         cudaSuccess)
       return MXFP8_ERR_CUDA;
+    CUtensorMap dw_st;
+    if (!ce_store(&dw_st, static_cast<uint16_t*>(dw) + v0 * H, cols, H, H)) return MXFP8_ERR_CUDA;
+    p.d_rows = static_cast<int>(cols);
+    p.d_cols = static_cast<int>(H);
+    const cudaError_t e =
+        ws.few ? ce_go(k_ce_gemm<CE_DW, 1, CE_SHORT>, std::min<int64_t>(up(cols, 128) * up(H, 128), 2 * dev.sms),
+                       CE_THREADS, ce_smem_bytes(CE_SHORT), st, false, false, dz_mn, x_mn, dw_st, p)
+               : ce_launch<CE_DW>(dw_pair, up(cols, wt) * up(H, wt), dev, dz_mn, x_mn, dw_st, p, st);
+    if (e != cudaSuccess) return MXFP8_ERR_CUDA;
   }
-  if (p.acc != nullptr) {
-    // every share of the first piece was written; a shorter last piece may have filled fewer of them
-    p.splits = static_cast<int>(up(up(std::min(ws.piece, V), CE_BK), up(up(ws.piece, CE_BK), ws.splits)));
-    k_ce_dx<<<rows_grid, 256, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return MXFP8_ERR_CUDA;
-  }
+  if (p.acc != nullptr &&
+      ce_go(k_ce_dx, std::min<int64_t>(up(T * (H / 4), CE_DX_THREADS / 8), 8 * dev.sms), CE_DX_THREADS, 0, st, false, false, p,
+            static_cast<int>(up(std::min(ws.piece, V), CE_BK))) != cudaSuccess)
+    return MXFP8_ERR_CUDA;
   return MXFP8_OK;
 }
 
