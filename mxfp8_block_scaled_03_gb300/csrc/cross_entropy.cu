@@ -90,6 +90,8 @@ struct CeParams {
   float* zy;                   // CE_LSE: the target's logit
   int64_t pitch;
   float* acc;                  // CE_DX: [splits][pitch][H] fp32, or NULL: dx is written directly
+  float* acc_w;                // CE_DW: [dw_splits][vcols][H] fp32, or NULL: dw is written directly
+  int dw_splits;
   int acc_add;
   uint16_t* dz;                // few rows, CE_DZ: [NT][dz_pitch]
   int64_t dz_pitch;
@@ -177,7 +179,7 @@ __device__ __forceinline__ void ce_start() {
 
 struct CeUnits {
   int nm, nn, steps;           // row tiles, column tiles, K steps in all
-  int split_steps;             // CE_DX: K steps of a share
+  int split_steps;             // CE_DX, CE_DW: K steps of a share
   int total;
 };
 template <int MODE, int CG>
@@ -208,6 +210,10 @@ __device__ __forceinline__ CeUnits ce_units(const CeParams& p) {
     c.split_steps = up(p.piece_steps, p.meta->splits);
     splits = up(c.steps, c.split_steps);
   }
+  if (MODE == CE_DW && p.dw_splits > 1) {           // every share writes its part, one without rows zeros
+    c.split_steps = max(1, up(c.steps, p.dw_splits));
+    splits = p.dw_splits;
+  }
   c.total = c.nm * c.nn * splits;
   return c;
 }
@@ -219,15 +225,16 @@ template <int MODE>
 __device__ __forceinline__ CeTile ce_tile(int u, const CeUnits& c, const CeParams& p) {
   CeTile t;
   const int per = c.nm * c.nn;
-  t.split = MODE == CE_DX ? u / per : 0;
+  constexpr bool SPLIT = MODE == CE_DX || MODE == CE_DW;
+  t.split = SPLIT ? u / per : 0;
   const int w0 = u - t.split * per;
   const int g = w0 / (p.group_m * c.nn);
   const int in_g = min(p.group_m, c.nm - g * p.group_m);
   const int w = w0 - g * p.group_m * c.nn;
   t.n = w / in_g;
   t.m = g * p.group_m + (w - t.n * in_g);
-  t.k0 = MODE == CE_DX ? t.split * c.split_steps : 0;
-  t.steps = MODE == CE_DX ? min(c.split_steps, c.steps - t.k0) : c.steps;
+  t.k0 = SPLIT ? t.split * c.split_steps : 0;
+  t.steps = SPLIT ? max(0, min(c.split_steps, c.steps - t.k0)) : c.steps;
   return t;
 }
 
@@ -538,6 +545,16 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
               if (y == col + i) d -= hot;
               v[i] = row < n_rows && col + i < p.vcols ? __float_as_uint(d) : 0u;
             }
+          }
+          if (MODE == CE_DW && p.acc_w != nullptr) {
+            float* dst = p.acc_w + (static_cast<int64_t>(t.split) * p.vcols + row) * p.H + col;
+            if (row < p.vcols)
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+                if (col + j < p.H)
+                  st_global_32B(dst + j, make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]),
+                                make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]));
+            continue;
           }
           uint8_t* out = wbuf + ((c >> 5) & 1) * CE_BUF_BYTES;
           if (lane == 0) bulk_wait_read_le1();      // the store that last used this buffer has read it
@@ -878,6 +895,15 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
         }
       } else {
         const int h = u % tiles * 128 + quarter * 32 + lane;
+        if (p.acc == nullptr) {
+          if (h < p.H)
+#pragma unroll
+            for (int j = 0; j < S::COLS; ++j)
+              if (c0 + j < n_rows)
+                p.dx[static_cast<int64_t>(__ldg(p.row_map + c0 + j)) * p.H + h] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(z[j]));
+          continue;
+        }
         float* dst = p.acc + (static_cast<int64_t>(u / tiles) * p.pitch + c0) * p.H + h;
         if (h < p.H) {
 #pragma unroll
@@ -1003,98 +1029,59 @@ __device__ __forceinline__ void ce_put_meta(const CeParams& p, const CePack& q, 
     p.meta->splits = splits;
   }
 }
-// xp[i] = x[src] for i < n, zeros up to t_pad; dx of a row that takes no part is zero.
-__device__ __forceinline__ void ce_pack_row(const CeParams& p, const CePack& q, int i, int src, int n) {
+// The rows that take part, packed in order: row_map[i] and xp[i] = x[row_map[i]] for i < n, zeros up to t_pad; dx of the
+// other rows is zero.  Every CTA counts all targets (they are in the L2 after the first) and packs its share of the rows:
+// one CTA that wrote the map for a second kernel took 19 us for 16384 rows, and 15 more for the copy.
+constexpr int CE_PREP_THREADS = 1024;
+__global__ void __launch_bounds__(CE_PREP_THREADS) k_ce_prep(const CeParams p, const CePack q) {
+  __shared__ int s_warp[3][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ce_dependents();
+  const int per = (q.T + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int r0 = min(q.T, static_cast<int>(blockIdx.x) * per), r1 = min(q.T, r0 + per);
+  int all = 0, ahead = 0, bad = 0;
+#pragma unroll 4
+  for (int t = threadIdx.x; t < q.T; t += CE_PREP_THREADS) {
+    const int64_t y = ce_target(p, t);
+    const int in = y >= 0 && y < p.V;
+    all += in;
+    ahead += t < r0 ? in : 0;
+    bad |= y >= p.V;
+  }
+  all = __reduce_add_sync(0xFFFFFFFFu, all);
+  ahead = __reduce_add_sync(0xFFFFFFFFu, ahead);
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if (lane == 0) {
+    s_warp[0][warp] = all;
+    s_warp[1][warp] = ahead;
+    s_warp[2][warp] = bad;
+  }
+  __syncthreads();
+  const int n = __reduce_add_sync(0xFFFFFFFFu, s_warp[0][lane]);
+  int at = __reduce_add_sync(0xFFFFFFFFu, s_warp[1][lane]);
+  bad = __any_sync(0xFFFFFFFFu, s_warp[2][lane]);
+  if (blockIdx.x == 0 && warp == 0) ce_put_meta(p, q, n, bad != 0);
   const int64_t per_row = p.H / 8;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int c = threadIdx.x; c < per_row; c += blockDim.x) {
-    if (i < q.t_pad) q.xp[i * per_row + c] = i < n ? __ldcs(q.x + src * per_row + c) : zero;
-    if (i >= n && i < q.T) reinterpret_cast<uint4*>(p.dx)[src * per_row + c] = zero;
+  // 32 rows at a time: every warp knows which of them take part, and copies its own
+  for (int t0 = r0; t0 < r1; t0 += 32) {
+    const int t = t0 + lane;
+    const int64_t y = t < r1 ? ce_target(p, t) : -1;
+    const uint32_t in = __ballot_sync(0xFFFFFFFFu, y >= 0 && y < p.V);
+    const int rows = min(32, r1 - t0);
+    if (warp < rows) {
+      const bool mine = (in >> warp) & 1u;
+      const int i = at + __popc(in & ((1u << warp) - 1u)), src = t0 + warp;
+      uint4* to = mine ? q.xp + i * per_row : reinterpret_cast<uint4*>(p.dx) + src * per_row;
+      const uint4* from = q.x + src * per_row;
+#pragma unroll 4
+      for (int64_t c = lane; c < per_row; c += 32) to[c] = mine ? __ldcs(from + c) : zero;
+      if (mine && lane == 0) q.row_map[i] = src;
+    }
+    at += __popc(in);
   }
-}
-
-// row_map: the rows that take part in order, then the others in order; their number.  One CTA.
-__global__ void __launch_bounds__(1024) k_ce_rows(const CeParams p, const CePack q) {
-  __shared__ int s_warp[32];
-  __shared__ int s_bad;
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  ce_dependents();
-  const int per = (q.T + 1023) / 1024;
-  const int t0 = min(q.T, static_cast<int>(threadIdx.x) * per), t1 = min(q.T, t0 + per);
-  int mine = 0;
-  for (int t = t0; t < t1; ++t) {
-    const int64_t y = ce_target(p, t);
-    mine += y >= 0 && y < p.V;
-    if (y >= p.V) s_bad = 1;
-  }
-  int scan = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-    if ((threadIdx.x & 31) >= o) scan += a;
-  }
-  if ((threadIdx.x & 31) == 31) s_warp[threadIdx.x >> 5] = scan;
-  __syncthreads();
-  int before = scan - mine, n = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w < static_cast<int>(threadIdx.x >> 5)) before += s_warp[w];
-    n += s_warp[w];
-  }
-  int other = n + t0 - before;                // rows before t0 that take no part come first
-  for (int t = t0; t < t1; ++t) {
-    const int64_t y = ce_target(p, t);
-    if (y >= 0 && y < p.V) q.row_map[before++] = t;
-    else q.row_map[other++] = t;
-  }
-  if (threadIdx.x < 32) ce_put_meta(p, q, n, s_bad != 0);
-}
-__global__ void __launch_bounds__(256) k_ce_pack(const CeParams p, const CePack q) {
-  ce_dependents();
-  ce_wait_before();
-  const int n = p.meta->n;
-  for (int i = blockIdx.x; i < max(q.t_pad, q.T); i += gridDim.x) ce_pack_row(p, q, i, i < q.T ? q.row_map[i] : 0, n);
-}
-// Both for up to CE_PREP_ROWS rows: every CTA makes the map for itself, the first one writes it.
-constexpr int CE_PREP_ROWS = 1024;
-__global__ void __launch_bounds__(256) k_ce_prep(const CeParams p, const CePack q) {
-  __shared__ int s_map[CE_PREP_ROWS];
-  __shared__ int s_warp[8];
-  __shared__ int s_bad;
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  ce_dependents();
-  const int t0 = 4 * threadIdx.x;
-  bool in[4];
-  int mine = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t y = t0 + j < q.T ? ce_target(p, t0 + j) : -1;
-    in[j] = y >= 0 && y < p.V;
-    mine += in[j];
-    if (y >= p.V) s_bad = 1;
-  }
-  int scan = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-    if ((threadIdx.x & 31) >= o) scan += a;
-  }
-  if ((threadIdx.x & 31) == 31) s_warp[threadIdx.x >> 5] = scan;
-  __syncthreads();
-  int before = scan - mine, n = 0;
-  for (int w = 0; w < 8; ++w) {
-    if (w < static_cast<int>(threadIdx.x >> 5)) before += s_warp[w];
-    n += s_warp[w];
-  }
-  int other = n + t0 - before;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (t0 + j < q.T) s_map[in[j] ? before++ : other++] = t0 + j;
-  __syncthreads();
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < q.T; i += 256) q.row_map[i] = s_map[i];
-    if (threadIdx.x < 32) ce_put_meta(p, q, n, s_bad != 0);
-  }
-  for (int i = blockIdx.x; i < max(q.t_pad, q.T); i += gridDim.x) ce_pack_row(p, q, i, i < q.T ? s_map[i] : 0, n);
+  for (int64_t i = n + blockIdx.x * int64_t(32) + warp; i < q.t_pad; i += gridDim.x * int64_t(32))
+    for (int64_t c = lane; c < per_row; c += 32) q.xp[i * per_row + c] = zero;
 }
 
 // dx of the packed rows from their fp32 parts, added in a fixed order: a thread has four columns, of eight or more shares
@@ -1135,6 +1122,25 @@ __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int s
     if (slice == 0 && e < total)
       reinterpret_cast<uint2*>(p.dx)[static_cast<int64_t>(p.row_map[i]) * per_row + c] =
           make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
+}
+
+// dw of a piece from its fp32 parts, added in order: a thread has four columns.
+__global__ void __launch_bounds__(256) k_ce_dw(const CeParams p, uint16_t* dw) {
+  ce_wait_before();
+  const int64_t total = static_cast<int64_t>(p.vcols) * (p.H / 4);
+  const float4* a = reinterpret_cast<const float4*>(p.acc_w);
+  for (int64_t e = blockIdx.x * int64_t(256) + threadIdx.x; e < total; e += gridDim.x * int64_t(256)) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int s = 0; s < p.dw_splits; ++s) {
+      const float4 o = __ldcs(a + s * total + e);
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    }
+    reinterpret_cast<uint2*>(dw)[e] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
 }
 
@@ -1331,9 +1337,9 @@ CeFwdWs ce_fwd_ws(int64_t T, int64_t V) {
 
 // Backward workspace: header, row map, packed x [t_pad, H], dz of one piece [t_pad, piece], fp32 parts of dx.
 struct CeBwdWs {
-  size_t row_map, xp, dz, acc, total;
+  size_t row_map, xp, dz, acc, acc_w, total;
   int64_t t_pad, piece, pieces;
-  int splits;
+  int splits, dw_splits;
   bool few;
 };
 constexpr int CE_MAX_SPLITS = 16;
@@ -1353,7 +1359,12 @@ CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   w.xp = up256(w.row_map + static_cast<size_t>(w.t_pad) * 4);
   w.dz = up256(w.xp + static_cast<size_t>(w.t_pad) * H * 2);
   w.acc = up256(w.dz + static_cast<size_t>(w.t_pad) * w.piece * 2);
-  w.total = up256(w.acc + (w.few || w.pieces > 1 || w.splits > 1 ? static_cast<size_t>(w.splits) * w.t_pad * H * 4 : 0));
+  // dw has few tiles where the vocabulary and H are small: its rows are shared out
+  const int64_t dw_tiles = up(w.piece, 128) * up(H, 128);
+  w.dw_splits = w.few ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({CE_MAX_SPLITS, 152 / dw_tiles,
+                                                                                     up(T, 8 * CE_BK)})));
+  w.acc_w = up256(w.acc + (w.pieces > 1 || w.splits > 1 ? static_cast<size_t>(w.splits) * w.t_pad * H * 4 : 0));
+  w.total = up256(w.acc_w + (w.dw_splits > 1 ? static_cast<size_t>(w.dw_splits) * w.piece * H * 4 : 0));
   return w;
 }
 
@@ -1462,7 +1473,9 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.dloss = dloss;
   p.dlse = dlse;
   p.pitch = ws.t_pad;
-  p.acc = ws.few || ws.pieces > 1 || ws.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
+  p.acc = ws.pieces > 1 || ws.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
+  p.acc_w = ws.dw_splits > 1 ? reinterpret_cast<float*>(base + ws.acc_w) : nullptr;
+  p.dw_splits = ws.dw_splits;
   p.dx = static_cast<uint16_t*>(dx);
   p.timeout_ns = ce_wait_ns();
   const bool dx_pair = !ws.few && use_pair(dev, T, H, ws.splits);
@@ -1477,13 +1490,8 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   q.dx_tile = dx_pair ? 256 : 128;
   q.dx_workers = ws.few ? 0 : dx_pair ? dev.pairs : dev.sms;
   q.dx_most = ws.splits;
-  const int64_t rows_grid = std::min<int64_t>(std::max(T, ws.t_pad), 8 * dev.sms);
-  if (T <= CE_PREP_ROWS) {
-    if (ce_go(k_ce_prep, rows_grid, 256, 0, st, true, false, p, q) != cudaSuccess) return MXFP8_ERR_CUDA;
-  } else if (ce_go(k_ce_rows, 1, 1024, 0, st, true, false, p, q) != cudaSuccess ||
-             ce_go(k_ce_pack, rows_grid, 256, 0, st, false, false, p, q) != cudaSuccess) {
+  if (ce_go(k_ce_prep, std::min<int64_t>(up(T, 32), dev.sms), CE_PREP_THREADS, 0, st, true, false, p, q) != cudaSuccess)
     return MXFP8_ERR_CUDA;
-  }
   CUtensorMap x_k, x_mn, w_k, w_mn, dz_k, dz_mn, dz_st;
   const int box = ws.few ? static_cast<int>(ws.t_pad) : CE_HALF;
   p.dz = dz;
@@ -1497,7 +1505,7 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     p.v0 = static_cast<int>(v0);
     p.vcols = static_cast<int>(cols);
     p.acc_add = i > 0;
-    const bool dz_pair = use_pair(dev, T, cols), dw_pair = use_pair(dev, cols, H);
+    const bool dz_pair = use_pair(dev, T, cols), dw_pair = use_pair(dev, cols, H, ws.dw_splits);
     const int64_t zt = dz_pair ? 256 : 128, wt = dw_pair ? 256 : 128, xt = dx_pair ? 256 : 128;
     p.group_m = group_of(H * 2, dz_pair, up(T, zt));
     p.d_rows = static_cast<int>(ws.t_pad);
@@ -1518,8 +1526,11 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     const cudaError_t e =
         ws.few ? ce_go(k_ce_gemm<CE_DW, 1, CE_SHORT>, std::min<int64_t>(up(cols, 128) * up(H, 128), 2 * dev.sms),
                        CE_THREADS, ce_smem_bytes(CE_SHORT), st, false, false, dz_mn, x_mn, dw_st, p)
-               : ce_launch<CE_DW>(dw_pair, up(cols, wt) * up(H, wt), dev, dz_mn, x_mn, dw_st, p, st);
+               : ce_launch<CE_DW>(dw_pair, up(cols, wt) * up(H, wt) * ws.dw_splits, dev, dz_mn, x_mn, dw_st, p, st);
     if (e != cudaSuccess) return MXFP8_ERR_CUDA;
+    if (p.acc_w != nullptr && ce_go(k_ce_dw, std::min<int64_t>(up(cols * (H / 4), 256), 8 * dev.sms), 256, 0, st, false,
+                                    false, p, static_cast<uint16_t*>(dw) + v0 * H) != cudaSuccess)
+      return MXFP8_ERR_CUDA;
   }
   if (p.acc != nullptr &&
       ce_go(k_ce_dx, std::min<int64_t>(up(T * (H / 4), CE_DX_THREADS / 8), 8 * dev.sms), CE_DX_THREADS, 0, st, false, false, p,
