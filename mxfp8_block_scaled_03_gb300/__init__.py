@@ -826,20 +826,27 @@ def moe_route_fwd(logits, k: int, token_mask=None, normalize: bool = True, sprea
         if token_mask.dtype is not torch.bool and token_mask.dtype is not torch.uint8:
             raise ValueError(f"token_mask: expected bool or uint8, got {token_mask.dtype}")
         pm = _need(token_mask, token_mask.dtype, (T,), "token_mask", dev)
-    kinds = ((i32, (T, k)), (f32, (T, k)), (f32, (T,)), (i32, (E + 1,)), (f32, (E,)), (f32, (2,)))
+    where = logits.device
     if out is None:
-        out = tuple(torch.empty(shape, dtype=dtype, device=logits.device) for dtype, shape in kinds)
-        ptrs = [t.data_ptr() for t in out]
+        empty = torch.empty
+        out = (empty((T, k), dtype=i32, device=where), empty((T, k), dtype=f32, device=where),
+               empty(T, dtype=f32, device=where), empty(E + 1, dtype=i32, device=where),
+               empty(E, dtype=f32, device=where), empty(2, dtype=f32, device=where))
+        experts, gates, lse, counts, prob_sum, losses = out
+        pe, pg, ps = experts.data_ptr(), gates.data_ptr(), lse.data_ptr()
+        pc, pp, po = counts.data_ptr(), prob_sum.data_ptr(), losses.data_ptr()
     else:
-        names = ("experts", "gates", "lse", "counts", "prob_sum", "losses")
-        ptrs = [_need(t, dtype, shape, name, dev) for t, (dtype, shape), name in zip(out, kinds, names)]
+        experts, gates, lse, counts, prob_sum, losses = out
+        pe, pg = _need(experts, i32, (T, k), "experts", dev), _need(gates, f32, (T, k), "gates", dev)
+        ps, pc = _need(lse, f32, (T,), "lse", dev), _need(counts, i32, (E + 1,), "counts", dev)
+        pp, po = _need(prob_sum, f32, (E,), "prob_sum", dev), _need(losses, f32, (2,), "losses", dev)
     if workspace is None:
-        workspace = torch.empty(max(16, moe_route_workspace_size(T, E, k)), dtype=torch.uint8, device=logits.device)
-    st = lib().moe_route_fwd(pl, code, T, E, k, pm, 1 if normalize else 0, 1 if spread else 0, *ptrs,
+        workspace = torch.empty(max(16, moe_route_workspace_size(T, E, k)), dtype=torch.uint8, device=where)
+    st = lib().moe_route_fwd(pl, code, T, E, k, pm, 1 if normalize else 0, 1 if spread else 0, pe, pg, ps, pc, pp, po,
                              _need(workspace, torch.uint8, 0, "workspace", dev), workspace.numel(), current)
     if st != OK:
         raise MXFP8Error(st, "moe_route_fwd")
-    return tuple(out)
+    return experts, gates, lse, counts, prob_sum, losses
 
 
 def moe_route_bwd(logits, experts, gates, lse, counts, dgates=None, dlosses=None, row_of_slot=None, dprob_sum=None,

@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         bool got = true;
         if (warp == CE_EPI_WARP0 && lane == 0)
           got = ce_wait<CG>(&acc_full[buf], acc_phase, false, abort_flag, peer_abort, p, ERR_TIMEOUT_EPILOGUE);
+        __syncwarp();                               // (the barrier counts whole warps, whichever lanes come first)
         got = group_and(CE_BAR_EPI, CE_EPI_WARPS * 32, got);
         tc_fence_after();
         return got;
@@ -833,6 +834,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
         }
         s_row[i] = r;
       }
+      __syncwarp();
       asm volatile("bar.sync %0, %1;" ::"r"(CE_BAR_EPI), "r"(S::EPI_WARPS * 32) : "memory");
     }
     // CE_LSE, base 2: below every logit, and finite, so that a first logit replaces it without a case of its own
@@ -918,6 +920,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
     if constexpr (MODE == CE_LSE) {
       // join the warp's lanes, then the quarters
       float2* s_part = reinterpret_cast<float2*>(smem + S::PARAM_OFFSET);
+      __syncwarp();
       asm volatile("bar.sync %0, %1;" ::"r"(CE_BAR_EPI), "r"(S::EPI_WARPS * 32) : "memory");   // s_row has been read
 #pragma unroll
       for (int j = 0; j < S::COLS; ++j) {
@@ -929,6 +932,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
         if (lane == 0) s_part[quarter * NT + c0 + j] = make_float2(top, t);
       }
+      __syncwarp();
       asm volatile("bar.sync %0, %1;" ::"r"(CE_BAR_EPI), "r"(S::EPI_WARPS * 32) : "memory");
       const int i = static_cast<int>(threadIdx.x) - 64;
       if (i < n_rows && i < NT) {

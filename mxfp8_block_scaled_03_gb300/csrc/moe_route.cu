@@ -27,6 +27,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "mx_device.cuh"
 #include "mx_internal.h"
@@ -35,14 +36,11 @@
 namespace mx {
 namespace {
 
-constexpr int RT_THREADS = 256;
-constexpr int RT_WARPS = RT_THREADS / 32;
 constexpr int RT_MAX_E = 1024;
 constexpr int RT_MAX_K = 32;
 constexpr int RT_MAX_CTAS = 304;
-constexpr int RT_FINAL_THREADS = 1024;
+constexpr int RT_FINAL_THREADS = 512;
 constexpr uint32_t FULL = 0xFFFFFFFFu;
-constexpr uint32_t KEY_MINUS_INF = 0x007FFFFFu;   // route_key(-inf); a key of 0 is no logit at all
 
 struct RouteParams {
   const void* logits;
@@ -55,10 +53,8 @@ struct RouteParams {
   int32_t* counts;        // [E + 1]: choices per expert, tokens that take part
   float* prob_sum;
   float* losses;
-  float* part_p;          // [gridDim.x][E] the CTAs' sums of p
-  int32_t* part_c;        // [gridDim.x][E] and counts
-  float* part_z;          // [gridDim.x]
-  int32_t* part_n;        // [gridDim.x]
+  float2* part;           // [gridDim.x][E + 1] the CTAs' sums of p and counts (integer bits), of lse^2 and of tokens
+  int vec;                // the logits' rows can be read V at a time
   const float* dgates;    // backward
   const int32_t* row_of_slot;
   const float* dprob_sum;
@@ -74,65 +70,161 @@ __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) {
   *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
+// V consecutive logits (V a multiple of 4, aligned).
+template <int V>
+__device__ __forceinline__ void load_logits(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(p + i));
+    v[i] = w.x;
+    v[i + 1] = w.y;
+    v[i + 2] = w.z;
+    v[i + 3] = w.w;
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_logits(const uint16_t* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p + i));
+    v[i] = bf16_lo(w.x);
+    v[i + 1] = bf16_hi(w.x);
+    v[i + 2] = bf16_lo(w.y);
+    v[i + 3] = bf16_hi(w.y);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_logits(float* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int V>
+__device__ __forceinline__ void store_logits(uint16_t* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4)
+    *reinterpret_cast<uint2*>(p + i) = make_uint2(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]));
+}
 
-// Unsigned keys in the order of the floats (-0 counts as +0).
-__device__ __forceinline__ uint32_t route_key(float v) {
+constexpr float LOG2E = 1.4426950408889634f;
+// exp(v - top): the difference first, so that logits of the type's lowest value stay finite.
+__device__ __forceinline__ float exp_below(float v, float top) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((v - top) * LOG2E));
+  return r;
+}
+
+// Candidates: unsigned numbers in the order of the logits (-0 counts as +0) and, among equals, the lowest expert first;
+// no two of a token are equal, and 0 is none.  The order of a float is that of its bits with the sign turned over (all of
+// them if it is negative); below it stands 65535 - expert: 32 bits for bf16, 48 for float.
+__device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
-__device__ __forceinline__ float route_value(uint32_t key) {
-  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+__device__ __forceinline__ float value_of(uint32_t order) {
+  return __uint_as_float(order ^ ((order >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
+constexpr uint32_t ORDER_MINUS_INF = 0x007FFFFFu;
+template <typename S>
+struct Key;
+template <>
+struct Key<float> {
+  using type = unsigned long long;
+  static __device__ __forceinline__ type make(float v, int e) {
+    return (static_cast<type>(order_of(v)) << 32) | (65535u - static_cast<uint32_t>(e));
+  }
+  static __device__ __forceinline__ float value(type c) { return value_of(static_cast<uint32_t>(c >> 32)); }
+  static __device__ __forceinline__ int expert(type c) { return static_cast<int>(65535u - static_cast<uint32_t>(c)); }
+  static __device__ __forceinline__ bool real(type c) { return static_cast<uint32_t>(c >> 32) > ORDER_MINUS_INF; }
+};
+template <>
+struct Key<uint16_t> {
+  using type = uint32_t;
+  static __device__ __forceinline__ type make(float v, int e) {
+    return (order_of(v) & 0xFFFF0000u) | (65535u - static_cast<uint32_t>(e));
+  }
+  static __device__ __forceinline__ float value(type c) {   // (the lower half of a negative value's order is not zero)
+    return __uint_as_float(__float_as_uint(value_of(c)) & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ int expert(type c) { return static_cast<int>(65535u - (c & 0xFFFFu)); }
+  static __device__ __forceinline__ bool real(type c) { return (c >> 16) > (ORDER_MINUS_INF >> 16); }
+};
 
-// Sums and maxima over a group of L lanes, in an order that every lane shares.
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
+// Sorts c[LO .. LO + N) downwards: Batcher's odd-even merge sort, all of its indexes known to the compiler.
+template <typename K>
+__device__ __forceinline__ void swap_down(K& a, K& b) {
+  const K hi = a > b ? a : b;
+  b = a > b ? b : a;
+  a = hi;
+}
+template <int LO, int N, int R, typename K>
+__device__ __forceinline__ void merge_down(K* c) {
+  if constexpr (2 * R < N) {
+    merge_down<LO, N, 2 * R>(c);
+    merge_down<LO + R, N, 2 * R>(c);
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
-  return v;
-}
-template <int L>
-__device__ __forceinline__ bool group_any(bool v) {
-  const uint32_t b = __ballot_sync(FULL, v);
-  return ((b >> ((threadIdx.x & 31) / L * L)) & (L == 32 ? FULL : (1u << (L % 32)) - 1u)) != 0;
-}
-// Largest key of the group and, among equals, the lowest expert.
-template <int L>
-__device__ __forceinline__ void group_best(uint32_t& key, int& e) {
-  if constexpr (L == 32) {
-    const uint32_t top = __reduce_max_sync(FULL, key);
-    e = static_cast<int>(__reduce_min_sync(FULL, key == top ? static_cast<uint32_t>(e) : FULL));
-    key = top;
+    for (int i = LO + R; i + R < LO + N; i += 2 * R) swap_down(c[i], c[i + R]);
   } else {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) {
-      const uint32_t other = __shfl_xor_sync(FULL, key, o);
-      const int oe = __shfl_xor_sync(FULL, e, o);
-      if (other > key || (other == key && oe < e)) {
-        key = other;
-        e = oe;
-      }
-    }
+    swap_down(c[LO], c[LO + R]);
+  }
+}
+template <int LO, int N, typename K>
+__device__ __forceinline__ void sort_down(K* c) {
+  if constexpr (N > 1) {
+    sort_down<LO, N / 2>(c);
+    sort_down<LO + N / 2, N / 2>(c);
+    merge_down<LO, N, 1>(c);
   }
 }
 
-// Sum over the CTA (every thread gets it); s has RT_FINAL_THREADS / 32 entries.
+// The L lanes of a token: part of a warp, or two or four warps, which exchange over shared memory (`s`: 2 x 16 words;
+// two buffers in turn, so that one barrier per exchange is enough).  Every lane gets the same result.
+template <int L>
+struct Group {
+  unsigned long long* s;
+  int turn;
+  __device__ __forceinline__ explicit Group(unsigned long long* scratch) : s(scratch), turn(0) {}
+  template <typename V, typename F>
+  __device__ __forceinline__ V join(V v, F f) {
+#pragma unroll
+    for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(FULL, v, o));
+    if constexpr (L > 32) {
+      unsigned long long* buf = s + 16 * turn;   // a word per warp, whatever its type: groups are not in step
+      turn ^= 1;
+      const int warp = threadIdx.x >> 5, first = threadIdx.x / L * (L / 32);
+      if ((threadIdx.x & 31) == 0) *reinterpret_cast<V*>(buf + warp) = v;
+      __syncwarp();                           // (bar.sync counts whole warps, whichever lanes come first)
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / L), "r"(L) : "memory");
+      v = *reinterpret_cast<const V*>(buf + first);
+#pragma unroll
+      for (int i = 1; i < L / 32; ++i) v = f(v, *reinterpret_cast<const V*>(buf + first + i));
+    }
+    return v;
+  }
+  __device__ __forceinline__ float sum(float v) {
+    return join(v, [](float a, float b) { return a + b; });
+  }
+  __device__ __forceinline__ float max(float v) {
+    return join(v, [](float a, float b) { return fmaxf(a, b); });
+  }
+  template <typename K>
+  __device__ __forceinline__ K best(K v) {
+    return join(v, [](K a, K b) { return a > b ? a : b; });
+  }
+};
+
+// Sum over the CTA (every thread gets it); s has 32 entries.
 template <typename V>
 __device__ __forceinline__ V block_sum(V v, V* s) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  if (lane == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
-  V t = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) t += s[w];
-  return t;
+  v = lane < static_cast<int>(blockDim.x >> 5) ? s[lane] : V(0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
 }
 
 // The losses from the whole sums; `weighted` is this thread's share of sum_e count_e P_e.
@@ -143,148 +235,188 @@ __device__ __forceinline__ void put_losses(const RouteParams& p, float weighted,
   p.losses[1] = z / nf;
 }
 
-// A lane's logits are those of experts l, l + L, ..., l + (V - 1) L.
-template <typename S, int L, int V>
-__global__ void __launch_bounds__(RT_THREADS) k_route_fwd(const RouteParams p) {
-  extern __shared__ float s_dyn[];            // [RT_WARPS][E] sums of p, then [E] counts
-  __shared__ float s_f[RT_FINAL_THREADS / 32];
-  __shared__ int s_i[RT_FINAL_THREADS / 32];
-  constexpr int G = RT_THREADS / L;
+// A token has L lanes with V consecutive experts each.  Its choice j is kept by lane j % L; with more than one choice per
+// lane (MANY, k > L) a lane has room for all it may get.
+template <int L, int V>
+struct RouteShape {
+  static constexpr int THREADS = 512;
+  static constexpr int GROUPS = THREADS / L;
+  static constexpr int WARPS = THREADS / 32;
+  static constexpr int ROWS = L < 32 ? WARPS : GROUPS;                // sums of p that a CTA keeps per expert
+  static constexpr int MOST = L * V < RT_MAX_K ? V : (RT_MAX_K + L - 1) / L;
+};
+// A lane's logits of token t, -inf where there are none.
+template <typename S, int V>
+__device__ __forceinline__ void fetch(const RouteParams& p, int64_t t, int e0, bool on, float* v) {
+  const S* row = static_cast<const S*>(p.logits) + t * p.E + e0;
+  if (p.vec && on && e0 < p.E) {
+    load_logits<V>(row, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = on && e0 + i < p.E ? load_logit(row + i) : -INFINITY;
+  }
+}
+
+template <typename S, int L, int V, bool MANY>
+__global__ void __launch_bounds__(RouteShape<L, V>::THREADS, 2) k_route_fwd(const RouteParams p) {
+  using R = RouteShape<L, V>;
+  using K = typename Key<S>::type;
+  constexpr int SLOTS = MANY ? R::MOST : 1;
+  extern __shared__ float s_dyn[];            // [ROWS][E] sums of p, then [E] counts
+  __shared__ unsigned long long s_x[32];
+  __shared__ float s_f[32];
+  __shared__ int s_i[32];
+  Group<L> lanes(s_x);
   const int l = threadIdx.x % L, group = threadIdx.x / L;
-  const int E = p.E, k = p.k;
-  int* hist = reinterpret_cast<int*>(s_dyn + RT_WARPS * E);
-  for (int e = threadIdx.x; e < E; e += RT_THREADS) hist[e] = 0;
+  const int E = p.E, k = p.k, e0 = l * V;
+  int* hist = reinterpret_cast<int*>(s_dyn + R::ROWS * E);
+  for (int e = threadIdx.x; e < E; e += R::THREADS) hist[e] = 0;
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   float psum[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) psum[i] = 0.0f;
   float zsum = 0.0f;
   int n = 0;
-  const S* logits = static_cast<const S*>(p.logits);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * G; t0 < p.T; t0 += static_cast<int64_t>(gridDim.x) * G) {
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * R::GROUPS; t0 < p.T;
+       t0 += static_cast<int64_t>(gridDim.x) * R::GROUPS) {
     const int64_t t = t0 + group;
     const bool in = t < p.T;
     const bool on = in && (p.mask == nullptr || p.mask[t] != 0);
     float v[V];
+    fetch<S, V>(p, t, e0, on, v);
+    // the largest logit; +inf stands for a NaN or +inf among them: the token's results are NaN
     float top = -INFINITY;
-    bool odd = false;                         // a NaN or +inf: the token's results are NaN
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] = on && l + L * i < E ? load_logit(logits + t * E + l + L * i) : -INFINITY;
-      odd |= !(v[i] < INFINITY);
-      top = fmaxf(top, v[i]);
-    }
-    odd = group_any<L>(odd);
-    top = group_max<L>(top);
-    const bool some = odd || top > -INFINITY;
+    for (int i = 0; i < V; ++i) top = v[i] < INFINITY ? fmaxf(top, v[i]) : INFINITY;
+    top = lanes.max(top);
+    const bool odd = top == INFINITY;
+    const bool some = top > -INFINITY;
+    const float base = some ? top : 0.0f;
     float total = 0.0f;
-    uint32_t key[V];
+    K c[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      key[i] = some && !odd && l + L * i < E ? route_key(v[i]) : 0u;
-      v[i] = some ? expf(v[i] - top) : 0.0f;
+      c[i] = odd || e0 + i >= E ? K(0) : Key<S>::make(v[i], e0 + i);
+      v[i] = exp_below(v[i], base);           // 0 for -inf
       total += v[i];
     }
-    total = group_sum<L>(total);
+    total = lanes.sum(total);
     if (odd) total = NAN;
     const float inv = some ? 1.0f / total : 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) psum[i] += v[i] * inv;
+    for (int i = 0; i < V; ++i) psum[i] = fmaf(v[i], inv, psum[i]);
     const float lse = some ? top + logf(total) : -INFINITY;
     if (in && l == 0) {
-      p.lse[t] = lse;
+      p.lse[t] = odd ? NAN : lse;
       if (some) {
-        zsum += lse * lse;
+        zsum += odd ? NAN : lse * lse;
         ++n;
       }
     }
-    uint32_t mine = 0;                        // lane j keeps choice j
-    int mine_e = 0;
-    for (int j = 0; j < k; ++j) {
-      uint32_t best = 0;
-      int e = 0;
+    // k rounds: every lane offers the best it has left; the one whose offer is taken moves up
+    sort_down<0, V>(c);
+    K mine[SLOTS];
+    float chosen = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == 0 || key[i] > best) {
-          best = key[i];
-          e = l + L * i;
-        }
-      group_best<L>(best, e);
-      if (l == j) {
-        mine = best;
-        mine_e = e;
+    for (int s = 0; s < SLOTS; ++s) {
+      mine[s] = 0;
+#pragma unroll 1
+      for (int r = 0; r < L && s * L + r < k; ++r) {
+        const K best = lanes.best(c[0]);
+        if (l == r) mine[s] = best;
+        const bool taken = best == c[0];
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) c[i] = taken ? c[i + 1] : c[i];
+        if (taken) c[V - 1] = 0;
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e == l + L * i) key[i] = 0u;
+      if (Key<S>::real(mine[s])) chosen += exp_below(Key<S>::value(mine[s]), base);
     }
-    const bool real = mine > KEY_MINUS_INF;
-    float g = real ? expf(route_value(mine) - top) : 0.0f;
-    const float chosen = group_sum<L>(g);
-    g = real ? g / (p.normalize ? chosen : total) : 0.0f;
-    if (in && l < k) {
-      const int64_t slot = t * k + l;
-      p.experts[slot] = real ? mine_e : p.spread ? static_cast<int>(static_cast<uint32_t>(slot) % E) : -1;
-      p.gates[slot] = g;
-      if (real) atomicAdd(&hist[mine_e], 1);
+    chosen = lanes.sum(chosen);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int j = s * L + l;
+      if (in && j < k) {
+        const int64_t slot = t * k + j;
+        const bool real = Key<S>::real(mine[s]);
+        const int e = Key<S>::expert(mine[s]);
+        p.experts[slot] = real ? e : p.spread ? static_cast<int>(static_cast<uint32_t>(slot) % E) : -1;
+        p.gates[slot] = real ? exp_below(Key<S>::value(mine[s]), base) / (p.normalize ? chosen : total) : 0.0f;
+        if (real) atomicAdd(&hist[e], 1);
+      }
     }
   }
-  // the CTA's sums: lanes of a warp with the same experts, then the warps in order
+  // the CTA's sums: lanes of a warp with the same experts, then the rest in order
 #pragma unroll
   for (int i = 0; i < V; ++i) {
 #pragma unroll
     for (int o = L; o < 32; o <<= 1) psum[i] += __shfl_xor_sync(FULL, psum[i], o);
-    if ((threadIdx.x & 31) < L && l + L * i < E) s_dyn[(threadIdx.x >> 5) * E + l + L * i] = psum[i];
+    if ((L >= 32 || (threadIdx.x & 31) < L) && e0 + i < E)
+      s_dyn[(L < 32 ? threadIdx.x >> 5 : group) * E + e0 + i] = psum[i];
   }
   zsum = block_sum(zsum, s_f);
   n = block_sum(n, s_i);
   const bool alone = gridDim.x == 1;
+  float2* part = p.part + static_cast<int64_t>(blockIdx.x) * (E + 1);
   float weighted = 0.0f;
-  for (int e = threadIdx.x; e < E; e += RT_THREADS) {
+  for (int e = threadIdx.x; e < E; e += R::THREADS) {
     float s = 0.0f;
-    for (int w = 0; w < RT_WARPS; ++w) s += s_dyn[w * E + e];
+#pragma unroll
+    for (int w = 0; w < R::ROWS; ++w) s += s_dyn[w * E + e];
     if (alone) {
       p.prob_sum[e] = s;
       p.counts[e] = hist[e];
       weighted += s * static_cast<float>(hist[e]);
     } else {
-      p.part_p[static_cast<int64_t>(blockIdx.x) * E + e] = s;
-      p.part_c[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
+      part[e] = make_float2(s, __int_as_float(hist[e]));
     }
   }
   if (alone) {
     weighted = block_sum(weighted, s_f);
     if (threadIdx.x == 0) put_losses(p, weighted, zsum, n);
   } else if (threadIdx.x == 0) {
-    p.part_z[blockIdx.x] = zsum;
-    p.part_n[blockIdx.x] = n;
+    part[E] = make_float2(zsum, __int_as_float(n));
   }
 }
 
-// Adds the CTAs' sums in a fixed order: thread (e, s) takes CTAs s, s + slices, ...; then a tree over the slices.
+// Adds the CTAs' sums in a fixed order.  A cluster of eight CTAs, each with an eighth of the experts: thread (e, s) takes
+// CTAs s, s + slices, ..., a tree joins the slices, and the first CTA gets the others' shares of the balance loss.  (One CTA
+// for all took 10 us for 64 experts and 50 for 1024.)
+constexpr int RT_FINAL_CTAS = 8;
 __global__ void __launch_bounds__(RT_FINAL_THREADS) k_route_final(const RouteParams p, int ctas) {
   __shared__ float s_p[RT_FINAL_THREADS];
   __shared__ int s_c[RT_FINAL_THREADS];
-  __shared__ float s_f[RT_FINAL_THREADS / 32];
-  __shared__ int s_i[RT_FINAL_THREADS / 32];
+  __shared__ float s_f[32];
+  __shared__ int s_i[32];
+  __shared__ float s_w[RT_FINAL_CTAS];
+  const uint32_t rank = cluster_cta_rank();
+  const int share = (p.E + RT_FINAL_CTAS - 1) / RT_FINAL_CTAS;
   int width = 1;
-  while (width < p.E) width <<= 1;
+  while (width < share) width <<= 1;
   const int slices = RT_FINAL_THREADS / width;
-  const int e = threadIdx.x % width, slice = threadIdx.x / width;
+  const int own = threadIdx.x % width, slice = threadIdx.x / width;
+  const int e = static_cast<int>(rank) * share + own;
+  const bool in = own < share && e < p.E;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  float2 zn = make_float2(0.0f, 0.0f);
+  for (int i = threadIdx.x; rank == 0 && i < ctas; i += RT_FINAL_THREADS) {
+    const float2 o = __ldcg(p.part + static_cast<int64_t>(i) * (p.E + 1) + p.E);
+    zn.x += o.x;
+    zn.y = __int_as_float(__float_as_int(zn.y) + __float_as_int(o.y));
+  }
   float s = 0.0f;
   int c = 0;
-  if (e < p.E) {
-#pragma unroll 4
+  if (in) {
+#pragma unroll 8
     for (int i = slice; i < ctas; i += slices) {
-      s += __ldcg(p.part_p + static_cast<int64_t>(i) * p.E + e);
-      c += __ldcg(p.part_c + static_cast<int64_t>(i) * p.E + e);
+      const float2 o = __ldcg(p.part + static_cast<int64_t>(i) * (p.E + 1) + e);
+      s += o.x;
+      c += __float_as_int(o.y);
     }
   }
   s_p[threadIdx.x] = s;
   s_c[threadIdx.x] = c;
-  const float z = block_sum(threadIdx.x < ctas ? __ldcg(p.part_z + threadIdx.x) : 0.0f, s_f);
-  const int n = block_sum(threadIdx.x < ctas ? __ldcg(p.part_n + threadIdx.x) : 0, s_i);
+  __syncthreads();
   for (int o = slices / 2; o > 0; o >>= 1) {
     if (slice < o) {
       s_p[threadIdx.x] += s_p[threadIdx.x + o * width];
@@ -293,20 +425,73 @@ __global__ void __launch_bounds__(RT_FINAL_THREADS) k_route_final(const RoutePar
     __syncthreads();
   }
   float weighted = 0.0f;
-  if (slice == 0 && e < p.E) {
-    p.prob_sum[e] = s_p[e];
-    p.counts[e] = s_c[e];
-    weighted = s_p[e] * static_cast<float>(s_c[e]);
+  if (slice == 0 && in) {
+    p.prob_sum[e] = s_p[own];
+    p.counts[e] = s_c[own];
+    weighted = s_p[own] * static_cast<float>(s_c[own]);
   }
   weighted = block_sum(weighted, s_f);
-  if (threadIdx.x == 0) put_losses(p, weighted, z, n);
+  if (threadIdx.x == 0) st_remote_u32(map_to_cta(s_w + rank, 0), __float_as_uint(weighted));
+  cluster_sync_all();
+  if (rank == 0) {
+    const float z = block_sum(zn.x, s_f);
+    const int n = block_sum(__float_as_int(zn.y), s_i);
+    if (threadIdx.x == 0) {
+      float all = 0.0f;
+      for (int i = 0; i < RT_FINAL_CTAS; ++i) all += s_w[i];
+      put_losses(p, all, z, n);
+    }
+  }
 }
 
-template <typename S, int L, int V>
-__global__ void __launch_bounds__(RT_THREADS) k_route_bwd(const RouteParams p) {
-  constexpr int G = RT_THREADS / L;
+// What a token's lane reads in the backward: asked for one token ahead.
+template <int V, int SLOTS>
+struct BwdToken {
+  float v[V];
+  float lse;
+  float g[SLOTS], dg[SLOTS];
+  int at[SLOTS];
+};
+
+template <typename S, int L, int V, bool MANY>
+__global__ void __launch_bounds__(RouteShape<L, V>::THREADS, 2) k_route_bwd(const RouteParams p) {
+  using R = RouteShape<L, V>;
+  constexpr int SLOTS = MANY ? R::MOST : 1;
+  __shared__ unsigned long long s_x[32];
+  __shared__ __align__(16) float s_add[MANY ? 1 : R::GROUPS][L * V];
+  Group<L> lanes(s_x);
   const int l = threadIdx.x % L, group = threadIdx.x / L;
-  const int E = p.E, k = p.k;
+  const int E = p.E, k = p.k, e0 = l * V;
+  if (!MANY) {
+    for (int i = threadIdx.x; i < R::GROUPS * L * V; i += R::THREADS) s_add[0][i] = 0.0f;
+    __syncthreads();
+  }
+  const int64_t slots = p.T * k;
+  auto ask = [&](int64_t t) {
+    BwdToken<V, SLOTS> a;
+    const bool in = t < p.T;
+    a.lse = in ? __ldg(p.lse + t) : -INFINITY;
+    fetch<S, V>(p, t, e0, in, a.v);
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+      const int j = q * L + l;
+      a.g[q] = a.dg[q] = 0.0f;
+      a.at[q] = -1;
+      if (in && j < k && p.dgates != nullptr) {
+        const int64_t slot = t * k + j;
+        a.at[q] = __ldg(p.experts + slot);
+        a.g[q] = __ldg(p.gates + slot);
+        int64_t from = slot;
+        if (p.row_of_slot != nullptr) from = __ldg(p.row_of_slot + slot);
+        if (from >= 0 && from < slots) a.dg[q] = __ldg(p.dgates + from);
+      }
+    }
+    return a;
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R::GROUPS;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * R::GROUPS + group;
+  BwdToken<V, SLOTS> next;
+  if (!MANY) next = ask(t);                   // (with many choices per lane there are no registers for it)
   const float n = fmaxf(static_cast<float>(__ldg(p.counts + E)), 1.0f);
   const float db = p.dlosses != nullptr ? __ldg(p.dlosses) : 0.0f;
   const float dz = p.dlosses != nullptr ? __ldg(p.dlosses + 1) : 0.0f;
@@ -314,58 +499,94 @@ __global__ void __launch_bounds__(RT_THREADS) k_route_bwd(const RouteParams p) {
   float c[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = l + L * i;
-    c[i] = e < E ? unit * static_cast<float>(__ldg(p.counts + e)) : 0.0f;
-    if (e < E && p.dprob_sum != nullptr) c[i] += __ldg(p.dprob_sum + e);
+    c[i] = e0 + i < E ? unit * static_cast<float>(__ldg(p.counts + e0 + i)) : 0.0f;
+    if (e0 + i < E && p.dprob_sum != nullptr) c[i] += __ldg(p.dprob_sum + e0 + i);
   }
-  const S* logits = static_cast<const S*>(p.logits);
   S* dlogits = static_cast<S*>(p.dlogits);
-  const int64_t slots = p.T * k;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * G; t0 < p.T; t0 += static_cast<int64_t>(gridDim.x) * G) {
-    const int64_t t = t0 + group;
-    const bool in = t < p.T;
-    const float lse = in ? __ldg(p.lse + t) : -INFINITY;
-    const bool on = !(lse == -INFINITY);      // the forward leaves -inf where a token takes no part
-    float pr[V];
+  for (; t - group < p.T; t += step) {
+    BwdToken<V, SLOTS> a = MANY ? ask(t) : next;
+    if (!MANY) next = ask(t + step);
+    const bool on = !(a.lse == -INFINITY);    // the forward leaves -inf where a token takes no part
+    // a lane's choices: gate_j dg_j, and where it goes; a gate of 0 passes nothing on, whatever its gradient's place holds
+    float gd[SLOTS];
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+      const bool real = on && a.at[q] >= 0 && a.at[q] < E && a.g[q] != 0.0f;
+      if (!real) a.at[q] = -1;
+      gd[q] = real ? a.g[q] * a.dg[q] : 0.0f;
+      s += gd[q];
+    }
+    s = lanes.sum(s);
+    const float lse0 = on ? a.lse : 0.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      pr[i] = on && l + L * i < E ? expf(load_logit(logits + t * E + l + L * i) - lse) : 0.0f;
-      dot += pr[i] * c[i];
+      a.v[i] = on && e0 + i < E ? exp_below(a.v[i], lse0) : 0.0f;   // p
+      dot = fmaf(a.v[i], c[i], dot);
     }
-    dot = group_sum<L>(dot);
-    float gd = 0.0f, g = 0.0f;                // lane j has choice j
-    int at = -1;
-    if (on && l < k && p.dgates != nullptr) {
-      const int64_t slot = t * k + l;
-      const int e = __ldg(p.experts + slot);
-      g = __ldg(p.gates + slot);
-      int64_t from = slot;
-      if (p.row_of_slot != nullptr) from = __ldg(p.row_of_slot + slot);
-      // a gate of 0 passes nothing on, whatever is in its gradient's place
-      if (e >= 0 && e < E && g != 0.0f && from >= 0 && from < slots) {
-        at = e;
-        gd = g * __ldg(p.dgates + from);
+    dot = lanes.sum(dot);
+    const float base = on ? 2.0f * dz / n * a.lse - dot - (p.normalize ? 0.0f : s) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.v[i] *= c[i] + base;
+    if (p.dgates != nullptr) {
+      if constexpr (!MANY) {
+        // The choices' shares go through the token's row of shared memory, which is zero but for them: one store, the
+        // lane's own V values, one store of zero.  Experts that a token lists more than once are joined first.
+        float add = p.normalize ? gd[0] - a.g[0] * s : gd[0];
+        const int mine = a.at[0];
+        bool put = mine >= 0;
+        if (threadIdx.x % L < 32) {           // the choices' lanes are in the group's first warp
+          const uint32_t same = __match_any_sync(FULL, put ? group * RT_MAX_E + mine : -1 - static_cast<int>(threadIdx.x));
+          if (__any_sync(FULL, (same & (same - 1)) != 0)) {
+            float all = 0.0f;
+            for (int r = 0; r < 32; ++r) {    // in the order of the slots
+              const float o = __shfl_sync(FULL, add, r);
+              if ((same >> r) & 1u) all += o;
+            }
+            add = all;
+            put = put && (same & ((1u << (threadIdx.x & 31)) - 1u)) == 0;
+          }
+        }
+        float* row = s_add[group];
+        __syncwarp();
+        if (put) row[mine] = add;
+        if constexpr (L > 32) lanes.sum(0.0f);   // (a barrier of the group)
+        else __syncwarp();
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const float4 o = *reinterpret_cast<const float4*>(row + e0 + i);
+          a.v[i] += o.x;
+          a.v[i + 1] += o.y;
+          a.v[i + 2] += o.z;
+          a.v[i + 3] += o.w;
+        }
+        if constexpr (L > 32) lanes.sum(0.0f);
+        else __syncwarp();
+        if (put) row[mine] = 0.0f;
+      } else {
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) {
+          const float add = p.normalize ? gd[q] - a.g[q] * s : gd[q];
+          for (int r = 0; r < L && q * L + r < k; ++r) {
+            const float o = __shfl_sync(FULL, add, r, L);
+            const int e = __shfl_sync(FULL, a.at[q], r, L) - e0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (e == i) a.v[i] += o;
+          }
+        }
       }
     }
-    const float s = group_sum<L>(gd);
-    const float add = p.normalize ? gd - g * s : gd;
-    const float base = 2.0f * dz / n * lse - dot - (p.normalize ? 0.0f : s);
-    float d[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = on ? pr[i] * (c[i] + base) : 0.0f;
-    if (p.dgates != nullptr)
-      for (int j = 0; j < k; ++j) {
-        const float a = __shfl_sync(FULL, add, j, L);
-        const int e = __shfl_sync(FULL, at, j, L);
+    if (t < p.T) {
+      S* row = dlogits + t * E + e0;
+      if (p.vec) {
+        if (e0 < E) store_logits<V>(row, a.v);
+      } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (e == l + L * i) d[i] += a;
+          if (e0 + i < E) store_logit(row + i, a.v[i]);
       }
-    if (in) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (l + L * i < E) store_logit(dlogits + t * E + l + L * i, d[i]);
     }
   }
 }
@@ -384,12 +605,32 @@ int route_sms() {
   return n;
 }
 
-int lanes_of(int E) { return E <= 4 ? 4 : E <= 8 ? 8 : E <= 16 ? 16 : 32; }
+// Calls f with the lanes and logits per lane of a token: eight logits per lane, so that up to 16 tokens share a warp's
+// rounds and a token of many experts has two or four warps.
+template <typename F>
+auto with_shape(int E, F f) {
+  using std::integral_constant;
+  if (E <= 4) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+  if (E <= 8) return f(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+  if (E <= 16) return f(integral_constant<int, 2>{}, integral_constant<int, 8>{});
+  if (E <= 32) return f(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+  if (E <= 64) return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+  if (E <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+  if (E <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 8>{});
+  if (E <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+  return f(integral_constant<int, 128>{}, integral_constant<int, 8>{});
+}
+int groups_of(int E) {
+  return with_shape(E, [](auto l, auto v) { return RouteShape<decltype(l)::value, decltype(v)::value>::GROUPS; });
+}
 
-// One CTA up to four tokens per group: a second kernel costs more than they do.
+// One CTA up to two tokens per group: a second kernel costs more than they do.  More CTAs take equal numbers of tokens.
 int64_t fwd_ctas(int64_t T, int E) {
-  const int64_t groups = RT_THREADS / lanes_of(E);
-  return T <= 4 * groups ? 1 : std::min<int64_t>((T + groups - 1) / groups, RT_MAX_CTAS);
+  const int64_t passes = (T + groups_of(E) - 1) / groups_of(E);
+  if (passes <= 2) return 1;
+  const int64_t most = RT_MAX_CTAS;
+  const int64_t per = (passes + most - 1) / most;
+  return (passes + per - 1) / per;
 }
 
 bool sizes_ok(int64_t T, int E, int k, int dtype) {
@@ -401,25 +642,26 @@ bool logits_ok(const void* p, int dtype) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_LOGITS_F32 ? 3u : 1u)) == 0;
 }
 
-template <bool BWD, typename S, int L, int V>
-void launch_one(const RouteParams& p, unsigned grid, cudaStream_t st) {
-  if constexpr (BWD)
-    k_route_bwd<S, L, V><<<grid, RT_THREADS, 0, st>>>(p);
-  else
-    k_route_fwd<S, L, V><<<grid, RT_THREADS, (RT_WARPS + 1) * static_cast<size_t>(p.E) * 4, st>>>(p);
-}
-
 template <bool BWD, typename S>
 void launch_route(const RouteParams& p, unsigned grid, cudaStream_t st) {
-  if (p.E <= 4) launch_one<BWD, S, 4, 1>(p, grid, st);
-  else if (p.E <= 8) launch_one<BWD, S, 8, 1>(p, grid, st);
-  else if (p.E <= 16) launch_one<BWD, S, 16, 1>(p, grid, st);
-  else if (p.E <= 32) launch_one<BWD, S, 32, 1>(p, grid, st);
-  else if (p.E <= 64) launch_one<BWD, S, 32, 2>(p, grid, st);
-  else if (p.E <= 128) launch_one<BWD, S, 32, 4>(p, grid, st);
-  else if (p.E <= 256) launch_one<BWD, S, 32, 8>(p, grid, st);
-  else if (p.E <= 512) launch_one<BWD, S, 32, 16>(p, grid, st);
-  else launch_one<BWD, S, 32, 32>(p, grid, st);
+  with_shape(p.E, [&](auto lanes, auto each) {
+    constexpr int L = decltype(lanes)::value, V = decltype(each)::value;
+    using R = RouteShape<L, V>;
+    RouteParams q = p;
+    auto whole = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & (sizeof(S) * 4 - 1)) == 0; };
+    q.vec = p.E % V == 0 && whole(p.logits) && (!BWD || whole(p.dlogits));
+    auto go = [&](auto many) {
+      constexpr bool MANY = decltype(many)::value;
+      if constexpr (BWD)
+        k_route_bwd<S, L, V, MANY><<<grid, R::THREADS, 0, st>>>(q);
+      else
+        k_route_fwd<S, L, V, MANY><<<grid, R::THREADS, (R::ROWS + 1) * static_cast<size_t>(p.E) * 4, st>>>(q);
+    };
+    if constexpr (R::MOST > 1) {
+      if (p.k > L) return go(std::true_type{});
+    }
+    go(std::false_type{});
+  });
 }
 
 }  // namespace
@@ -431,7 +673,7 @@ extern "C" {
 
 size_t moe_route_workspace_size(int64_t T, int E, int k) {
   if (!sizes_ok(T, E, k, MOE_LOGITS_F32) || k > RT_MAX_K) return 0;
-  return static_cast<size_t>(fwd_ctas(T, E)) * (2 * E + 2) * 4;
+  return static_cast<size_t>(fwd_ctas(T, E)) * (E + 1) * sizeof(float2);
 }
 
 int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k, const uint8_t* token_mask,
@@ -466,24 +708,25 @@ int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
   p.counts = counts;
   p.prob_sum = prob_sum;
   p.losses = losses;
-  p.part_p = static_cast<float*>(workspace);
-  p.part_c = reinterpret_cast<int32_t*>(p.part_p + ctas * E);
-  p.part_z = reinterpret_cast<float*>(p.part_c + ctas * E);
-  p.part_n = reinterpret_cast<int32_t*>(p.part_z + ctas);
+  p.part = static_cast<float2*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (logits_dtype == MOE_LOGITS_F32) launch_route<false, float>(p, static_cast<unsigned>(ctas), st);
   else launch_route<false, uint16_t>(p, static_cast<unsigned>(ctas), st);
   if (cudaGetLastError() != cudaSuccess) return MXFP8_ERR_CUDA;
   if (ctas > 1) {
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = RT_FINAL_CTAS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1, 1, 1);
+    cfg.gridDim = dim3(RT_FINAL_CTAS, 1, 1);
     cfg.blockDim = dim3(RT_FINAL_THREADS, 1, 1);
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, k_route_final, p, static_cast<int>(ctas)) != cudaSuccess) return MXFP8_ERR_CUDA;
   }
   return MXFP8_OK;
@@ -521,8 +764,8 @@ int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
   p.dprob_sum = dprob_sum;
   p.dlosses = dlosses;
   p.dlogits = dlogits;
-  const int64_t groups = RT_THREADS / lanes_of(E);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((T + groups - 1) / groups, 8 * sms));
+  const int64_t groups = groups_of(E);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((T + groups - 1) / groups, 2 * sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (logits_dtype == MOE_LOGITS_F32) launch_route<true, float>(p, grid, st);
   else launch_route<true, uint16_t>(p, grid, st);

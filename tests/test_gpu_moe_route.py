@@ -82,7 +82,8 @@ def near(x, ref, bar, name):
 
 SHAPES = [(1, 1, 1), (1, 8, 2), (5, 3, 3), (7, 4, 1), (40, 5, 2), (33, 8, 8), (100, 16, 4), (70, 17, 6), (64, 32, 32),
           (300, 33, 5), (257, 64, 8), (50, 100, 8), (41, 128, 1), (20, 200, 32), (30, 256, 8), (19, 300, 3), (11, 512, 6),
-          (9, 777, 32), (6, 1024, 4), (1500, 60, 6), (3000, 8, 2)]
+          (9, 777, 32), (6, 1024, 4), (1500, 60, 6), (3000, 8, 2), (5000, 4, 3), (2500, 31, 31), (1300, 128, 8), (700, 256, 2),
+          (400, 768, 20)]
 
 
 @pytest.mark.parametrize("T,E,k", SHAPES)
@@ -221,6 +222,30 @@ def test_no_token_takes_part(mx, T, E):
     d = mx.moe_route_bwd(l, experts, gates, lse, counts, dgates=torch.full((T, 2), math.nan, device="cuda"),
                          dlosses=torch.ones(2, device="cuda"))
     assert d.shape == (T, E) and not d.any()
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (8, 6), (64, 5), (300, 4), (1000, 9)])
+def test_an_expert_listed_twice(mx, E, k):
+    """The backward adds the shares of an expert that a token's list names more than once."""
+    import torch
+    T = 37
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn((T, E), generator=gen, device="cuda")
+    _, _, lse, counts, _, _ = mx.moe_route_fwd(logits, k)
+    experts = torch.randint(0, max(1, E // 4), (T, k), generator=gen, device="cuda").int()
+    experts[:, 1] = experts[:, 0]
+    p = torch.exp(logits.double() - lse.double()[:, None])
+    gates = p.gather(1, experts.long()).float()
+    dg = torch.randn((T, k), generator=gen, device="cuda")
+    got = mx.moe_route_bwd(logits, experts, gates, lse, counts, dgates=dg, normalize=False)
+    gd = gates.double() * dg.double()
+    want = -p * gd.sum(1, keepdim=True)
+    mag = p * gd.abs().sum(1, keepdim=True)
+    want.scatter_add_(1, experts.long(), gd)
+    mag.scatter_add_(1, experts.long(), gd.abs())
+    near(got, want, (2.0 ** -15 * mag + 1e-38).cpu(), "dlogits")
+    again = mx.moe_route_bwd(logits, experts, gates, lse, counts, dgates=dg, normalize=False)
+    assert torch.equal(got, again)
 
 
 def test_counts_of_several_batches(mx):
