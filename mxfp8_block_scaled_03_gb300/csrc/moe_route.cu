@@ -39,6 +39,7 @@ namespace {
 constexpr int RT_MAX_E = 1024;
 constexpr int RT_MAX_K = 32;
 constexpr int RT_MAX_CTAS = 304;
+constexpr int RT_CLUSTER = 16;         // CTAs of the forward that join their sums without a second kernel
 constexpr int RT_FINAL_THREADS = 512;
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 
@@ -55,6 +56,7 @@ struct RouteParams {
   float* losses;
   float2* part;           // [gridDim.x][E + 1] the CTAs' sums of p and counts (integer bits), of lse^2 and of tokens
   int vec;                // the logits' rows can be read V at a time
+  int cluster;            // the forward's CTAs are one cluster and join their sums themselves
   const float* dgates;    // backward
   const int32_t* row_of_slot;
   const float* dprob_sum;
@@ -235,6 +237,12 @@ __device__ __forceinline__ void put_losses(const RouteParams& p, float weighted,
   p.losses[1] = z / nf;
 }
 
+__device__ __forceinline__ uint32_t load_remote(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // A token has L lanes with V consecutive experts each.  Its choice j is kept by lane j % L; with more than one choice per
 // lane (MANY, k > L) a lane has room for all it may get.
 template <int L, int V>
@@ -278,13 +286,20 @@ __global__ void __launch_bounds__(RouteShape<L, V>::THREADS, 2) k_route_fwd(cons
   for (int i = 0; i < V; ++i) psum[i] = 0.0f;
   float zsum = 0.0f;
   int n = 0;
+  float ahead[V];                             // the next token's logits
+  auto ask = [&](int64_t t) {
+    const bool on = t < p.T && (p.mask == nullptr || p.mask[t] != 0);
+    fetch<S, V>(p, t, e0, on, ahead);
+  };
+  ask(static_cast<int64_t>(blockIdx.x) * R::GROUPS + group);
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * R::GROUPS; t0 < p.T;
        t0 += static_cast<int64_t>(gridDim.x) * R::GROUPS) {
     const int64_t t = t0 + group;
     const bool in = t < p.T;
-    const bool on = in && (p.mask == nullptr || p.mask[t] != 0);
     float v[V];
-    fetch<S, V>(p, t, e0, on, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = ahead[i];
+    ask(t + static_cast<int64_t>(gridDim.x) * R::GROUPS);
     // the largest logit; +inf stands for a NaN or +inf among them: the token's results are NaN
     float top = -INFINITY;
 #pragma unroll
@@ -356,6 +371,59 @@ __global__ void __launch_bounds__(RouteShape<L, V>::THREADS, 2) k_route_fwd(cons
   }
   zsum = block_sum(zsum, s_f);
   n = block_sum(n, s_i);
+  if (p.cluster) {
+    // every CTA adds up a share of the experts over the cluster, the first one the rest
+    __shared__ float s_w[RT_CLUSTER];
+    __shared__ float s_z;
+    __shared__ int s_n;
+    for (int e = threadIdx.x; e < E; e += R::THREADS) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < R::ROWS; ++w) s += s_dyn[w * E + e];
+      s_dyn[e] = s;
+    }
+    if (threadIdx.x == 0) {
+      s_z = zsum;
+      s_n = n;
+    }
+    cluster_sync_all();
+    const uint32_t rank = cluster_cta_rank();
+    const int share = (E + RT_CLUSTER - 1) / RT_CLUSTER;
+    const int e = static_cast<int>(rank) * share + threadIdx.x;
+    float weighted = 0.0f;
+    if (static_cast<int>(threadIdx.x) < share && e < E) {
+      float s = 0.0f;
+      int c = 0;
+#pragma unroll
+      for (int r = 0; r < RT_CLUSTER; ++r) {
+        s += __uint_as_float(load_remote(map_to_cta(s_dyn + e, r)));
+        c += static_cast<int>(load_remote(map_to_cta(hist + e, r)));
+      }
+      p.prob_sum[e] = s;
+      p.counts[e] = c;
+      weighted = s * static_cast<float>(c);
+    }
+    weighted = block_sum(weighted, s_f);
+    float z = 0.0f;
+    int all = 0;
+    if (rank == 0 && threadIdx.x < RT_CLUSTER) {
+      z = __uint_as_float(load_remote(map_to_cta(&s_z, threadIdx.x)));
+      all = static_cast<int>(load_remote(map_to_cta(&s_n, threadIdx.x)));
+    }
+    if (threadIdx.x == 0) st_remote_u32(map_to_cta(s_w + rank, 0), __float_as_uint(weighted));
+    cluster_sync_all();
+    if (rank == 0 && threadIdx.x < 32) {
+      weighted = threadIdx.x < RT_CLUSTER ? s_w[threadIdx.x] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        z += __shfl_xor_sync(FULL, z, o);
+        all += __shfl_xor_sync(FULL, all, o);
+        weighted += __shfl_xor_sync(FULL, weighted, o);
+      }
+      if (threadIdx.x == 0) put_losses(p, weighted, z, all);
+    }
+    return;
+  }
   const bool alone = gridDim.x == 1;
   float2* part = p.part + static_cast<int64_t>(blockIdx.x) * (E + 1);
   float weighted = 0.0f;
@@ -624,13 +692,20 @@ int groups_of(int E) {
   return with_shape(E, [](auto l, auto v) { return RouteShape<decltype(l)::value, decltype(v)::value>::GROUPS; });
 }
 
-// One CTA up to two tokens per group: a second kernel costs more than they do.  More CTAs take equal numbers of tokens.
-int64_t fwd_ctas(int64_t T, int E) {
+// One CTA up to two passes (a token per group each), a cluster of 16 up to 64 passes; beyond, as many CTAs as give all of
+// them equal passes, and a second kernel for their sums.
+constexpr int RT_CLUSTER_PASSES = 4 * RT_CLUSTER;
+struct FwdGrid {
+  int ctas;
+  bool cluster;
+};
+FwdGrid fwd_grid(int64_t T, int E, bool clusters) {
   const int64_t passes = (T + groups_of(E) - 1) / groups_of(E);
-  if (passes <= 2) return 1;
+  if (passes <= 2) return {1, false};
+  if (clusters && passes <= RT_CLUSTER_PASSES) return {RT_CLUSTER, true};
   const int64_t most = RT_MAX_CTAS;
   const int64_t per = (passes + most - 1) / most;
-  return (passes + per - 1) / per;
+  return {static_cast<int>((passes + per - 1) / per), false};
 }
 
 bool sizes_ok(int64_t T, int E, int k, int dtype) {
@@ -642,9 +717,45 @@ bool logits_ok(const void* p, int dtype) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_LOGITS_F32 ? 3u : 1u)) == 0;
 }
 
+// Whether clusters of 16 of this kernel can run (asked once per device); a cluster launch.
+template <typename F>
+cudaLaunchConfig_t cluster_config(F, size_t smem, int threads, cudaLaunchAttribute* attr, cudaStream_t st) {
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = RT_CLUSTER;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(RT_CLUSTER, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+template <auto KERNEL>
+bool clusters_run(size_t smem, int threads) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices] = {};   // 1: no, 2: yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if (known[dev].load() == 0) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = cluster_config(KERNEL, smem, threads, attr, nullptr);
+    int n = 0;
+    const bool ok =
+        cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();   // clear: a second kernel joins the sums
+    known[dev].store(ok ? 2 : 1);
+  }
+  return known[dev].load() == 2;
+}
+
+// Launches and returns the forward's CTAs that a second kernel has to join (1: none).
 template <bool BWD, typename S>
-void launch_route(const RouteParams& p, unsigned grid, cudaStream_t st) {
-  with_shape(p.E, [&](auto lanes, auto each) {
+int launch_route(const RouteParams& p, unsigned grid, cudaStream_t st) {
+  return with_shape(p.E, [&](auto lanes, auto each) {
     constexpr int L = decltype(lanes)::value, V = decltype(each)::value;
     using R = RouteShape<L, V>;
     RouteParams q = p;
@@ -652,15 +763,30 @@ void launch_route(const RouteParams& p, unsigned grid, cudaStream_t st) {
     q.vec = p.E % V == 0 && whole(p.logits) && (!BWD || whole(p.dlogits));
     auto go = [&](auto many) {
       constexpr bool MANY = decltype(many)::value;
-      if constexpr (BWD)
+      if constexpr (BWD) {
         k_route_bwd<S, L, V, MANY><<<grid, R::THREADS, 0, st>>>(q);
-      else
-        k_route_fwd<S, L, V, MANY><<<grid, R::THREADS, (R::ROWS + 1) * static_cast<size_t>(p.E) * 4, st>>>(q);
+        return 1;
+      } else {
+        constexpr auto kernel = k_route_fwd<S, L, V, MANY>;
+        const size_t smem = (R::ROWS + 1) * static_cast<size_t>(p.E) * 4;
+        FwdGrid g = fwd_grid(p.T, p.E, true);
+        if (g.cluster && !clusters_run<kernel>((R::ROWS + 1) * static_cast<size_t>(L * V) * 4, R::THREADS))
+          g = fwd_grid(p.T, p.E, false);
+        if (g.cluster) {
+          q.cluster = 1;
+          cudaLaunchAttribute attr[1];
+          const cudaLaunchConfig_t cfg = cluster_config(kernel, smem, R::THREADS, attr, st);
+          cudaLaunchKernelEx(&cfg, kernel, q);
+          return 1;
+        }
+        kernel<<<g.ctas, R::THREADS, smem, st>>>(q);
+        return g.ctas;
+      }
     };
     if constexpr (R::MOST > 1) {
       if (p.k > L) return go(std::true_type{});
     }
-    go(std::false_type{});
+    return go(std::false_type{});
   });
 }
 
@@ -673,7 +799,7 @@ extern "C" {
 
 size_t moe_route_workspace_size(int64_t T, int E, int k) {
   if (!sizes_ok(T, E, k, MOE_LOGITS_F32) || k > RT_MAX_K) return 0;
-  return static_cast<size_t>(fwd_ctas(T, E)) * (E + 1) * sizeof(float2);
+  return static_cast<size_t>(fwd_grid(T, E, false).ctas) * (E + 1) * sizeof(float2);
 }
 
 int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k, const uint8_t* token_mask,
@@ -689,8 +815,7 @@ int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
   for (const void* q : {static_cast<const void*>(counts), static_cast<const void*>(prob_sum),
                         static_cast<const void*>(losses)})
     if (q == nullptr || !aligned4(q)) return MXFP8_ERR_INVALID_ARG;
-  const int64_t ctas = fwd_ctas(T, E);
-  if (ctas > 1) {
+  if (fwd_grid(T, E, false).ctas > 1) {
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return MXFP8_ERR_INVALID_ARG;
     if (workspace_bytes < moe_route_workspace_size(T, E, k)) return MXFP8_ERR_WORKSPACE;
   }
@@ -710,8 +835,8 @@ int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
   p.losses = losses;
   p.part = static_cast<float2*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (logits_dtype == MOE_LOGITS_F32) launch_route<false, float>(p, static_cast<unsigned>(ctas), st);
-  else launch_route<false, uint16_t>(p, static_cast<unsigned>(ctas), st);
+  const int ctas = logits_dtype == MOE_LOGITS_F32 ? launch_route<false, float>(p, 0, st)
+                                                  : launch_route<false, uint16_t>(p, 0, st);
   if (cudaGetLastError() != cudaSuccess) return MXFP8_ERR_CUDA;
   if (ctas > 1) {
     cudaLaunchAttribute attr[2];
@@ -727,7 +852,7 @@ int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, k_route_final, p, static_cast<int>(ctas)) != cudaSuccess) return MXFP8_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, k_route_final, p, ctas) != cudaSuccess) return MXFP8_ERR_CUDA;
   }
   return MXFP8_OK;
 }
