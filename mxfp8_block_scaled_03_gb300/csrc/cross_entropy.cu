@@ -75,7 +75,7 @@ static_assert(sizeof(CeMeta) == 256, "header");
 struct CeParams {
   CeMeta* meta;
   const int32_t* row_map;      // backward: row of packed row i, then the rows that take no part
-  int rows;                    // CE_LSE: T
+  int rows;                    // forward, and backward of few rows: T; otherwise 0: meta->n packed rows
   int V, v0, vcols;            // vocabulary; first entry and entries of this piece
   int H;
   int group_m;                 // row tiles that share a column tile before the next one is taken
@@ -97,7 +97,11 @@ struct CeParams {
   int64_t dz_pitch;
   int d_rows, d_cols;          // CE_DZ, CE_DW: extent of the map that is stored to
   uint16_t* dx;
-  uint32_t* status;            // forward: an error word per CTA, joined by k_ce_merge; backward: NULL, meta->error
+  const uint4* x;              // few rows, CE_DZ of the first piece: x, and a copy with zeros for rows that take no part
+  uint4* xp;
+  uint32_t* status;            // a call's first kernel: an error word per CTA; otherwise NULL, meta->error
+  const uint32_t* join;        // the kernel after it: those words, to be added to meta->error
+  int joins;
   uint64_t timeout_ns;
 };
 
@@ -114,6 +118,12 @@ __device__ __forceinline__ void ce_report(const CeParams& p, uint32_t bits) {
 // the kernel before it, and runs beside its end: dx lets it start once dz is complete, and dw waits for dx when it is done.
 __device__ __forceinline__ void ce_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void ce_wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void ce_join(const CeParams& p, int thread, int threads) {
+  uint32_t bits = 0;
+  for (int i = thread; i < p.joins; i += threads) bits |= p.join[i];
+  if (bits != 0) atomicOr(&p.meta->error, bits);
+}
+__device__ __forceinline__ int ce_rows(const CeParams& p) { return p.rows > 0 ? p.rows : p.meta->n; }
 __device__ __forceinline__ int64_t ce_target(const CeParams& p, int64_t row) {
   return p.wide_targets ? __ldg(static_cast<const long long*>(p.targets) + row)
                         : static_cast<int64_t>(__ldg(static_cast<const int32_t*>(p.targets) + row));
@@ -199,7 +209,7 @@ __device__ __forceinline__ CeUnits ce_units(const CeParams& p) {
   } else if (MODE == CE_DW) {
     c.nm = up(p.vcols, TILE);
     c.nn = up(p.H, TILE);
-    c.steps = up(p.meta->n, CE_BK);
+    c.steps = up(ce_rows(p), CE_BK);
   } else {
     c.nm = up(p.meta->n, TILE);
     c.nn = up(p.H, TILE);
@@ -368,11 +378,14 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         }
         // Copies land before the CTA exits: the leader waits for its stages (their barriers count both CTAs' copies);
         // the second CTA's wait for the leader is the pair's closing barriers below.
+        // (After an abort the second CTA may never have copied its half: then one wait is enough for this CTA's.)
         if (leader)
           for (int s = 0; s < STAGES; ++s)
-            if ((prod_issued >> s) & 1u)
-              if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
-                ce_report(p, ERR_TIMEOUT_DRAIN);
+            if (((prod_issued >> s) & 1u) &&
+                !mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS)) {
+              ce_report(p, ERR_TIMEOUT_DRAIN);
+              break;
+            }
       }
       __syncwarp();
     } else if (warp == CE_WARP_MMA && leader) {
@@ -640,7 +653,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
 // the bytes of w.  Two CTAs per SM keep twice the copies in flight.
 //   CE_LSE  z^T = w x^T: a thread has one vocabulary entry and all rows; it carries every row's running maximum and sum
 //           over all its tiles, and lanes are joined once, at the end
-//   CE_DZ   the same product, dz written packed row by packed row
+//   CE_DZ   the same product and dz; rows that take no part are zeros in dz and in a copy of x for dw (no packing)
 //   CE_DX   dx^T = w^T dz^T over a share of the vocabulary: fp32 parts
 constexpr int CE_FEW = 64;
 constexpr int CE_FEW_BUFS = 4;                     // accumulators of NT columns
@@ -666,6 +679,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
   using S = FewShape<NT>;
   constexpr bool A_MN = MODE == CE_DX;
   constexpr int CHUNK = MODE == CE_LSE ? CE_CHUNK : 1 << 30;
+  constexpr int NO_TARGET = INT_MIN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BAR_OFFSET);
@@ -756,6 +770,10 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
           }
         }
       }
+      for (; ahead > 0; --ahead) {                  // (after an abort) the early stages get their other half
+        tma_load_2d(smem + (early - ahead) * S::STAGE_BYTES + CE_OP_BYTES, &tmB, &full[early - ahead], 0, 0);
+        issued |= 1u << (early - ahead);
+      }
       for (int s = 0; s < S::STAGES; ++s)           // copies land before the CTA exits
         if ((issued >> s) & 1u)
           if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
@@ -815,27 +833,38 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
     const int quarter = warp & 3;
     const int c0 = (warp - 2) / 4 * S::COLS;        // first row (column of the accumulator) of this warp
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
-    const int n_rows = MODE == CE_LSE ? p.rows : p.meta->n;
-    // CE_DZ: what each row needs; CE_LSE: its target (other rows: no target, rate 0)
+    const int n_rows = p.rows;
+    // CE_DZ: what each row needs; CE_LSE: its target
     float4* s_row = reinterpret_cast<float4*>(smem + S::PARAM_OFFSET);
     if (MODE != CE_DX) {
       const int i = static_cast<int>(threadIdx.x) - 64;
       if (i < NT) {
-        float4 r = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
+        float4 r = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(NO_TARGET));
         if (i < n_rows) {
-          const int src = MODE == CE_DZ ? __ldg(p.row_map + i) : i;
-          const int64_t target = ce_target(p, src);
-          if (target >= 0 && target < p.V) r.w = __int_as_float(static_cast<int>(target) - p.v0);
-          if (MODE == CE_DZ) {
-            r.z = __ldg(p.dloss + src);
-            r.x = r.z + (p.dlse != nullptr ? __ldg(p.dlse + src) : 0.0f);
-            r.y = __ldg(p.lse + src) * LOG2E;
+          const int64_t target = ce_target(p, i);
+          if (target >= 0 && target < p.V) {
+            r.w = __int_as_float(static_cast<int>(target) - p.v0);
+            if (MODE == CE_DZ) {
+              r.z = __ldg(p.dloss + i);
+              r.x = r.z + (p.dlse != nullptr ? __ldg(p.dlse + i) : 0.0f);
+              r.y = __ldg(p.lse + i) * LOG2E;
+            }
           }
+          if (MODE == CE_DZ && target >= p.V && blockIdx.x == 0) ce_report(p, ERR_TARGET_RANGE);
         }
         s_row[i] = r;
       }
       __syncwarp();
       asm volatile("bar.sync %0, %1;" ::"r"(CE_BAR_EPI), "r"(S::EPI_WARPS * 32) : "memory");
+      if (MODE == CE_DZ && p.xp != nullptr)
+        for (int r = blockIdx.x; r < NT; r += gridDim.x) {
+          const bool in = __float_as_int(s_row[r].w) != NO_TARGET;
+          const int64_t per_row = p.H / 8;
+          for (int64_t c = i; c < per_row; c += S::EPI_WARPS * 32)
+            p.xp[r * per_row + c] = in ? __ldg(p.x + r * per_row + c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    } else if (p.join != nullptr && blockIdx.x == 0) {
+      ce_join(p, static_cast<int>(threadIdx.x) - 64, S::EPI_WARPS * 32);
     }
     // CE_LSE, base 2: below every logit, and finite, so that a first logit replaces it without a case of its own
     float m[S::COLS], sum[S::COLS];
@@ -893,7 +922,8 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
           const float4 r = s_row[c0 + j];
           float d = r.x * ex2(fmaf(z[j], LOG2E, -r.y));
           if (__float_as_int(r.w) == v) d -= r.z;
-          dst[j * p.dz_pitch] = c0 + j < n_rows && v < p.vcols ? __bfloat16_as_ushort(__float2bfloat16_rn(d)) : 0;
+          const bool in = __float_as_int(r.w) != NO_TARGET && v < p.vcols;
+          dst[j * p.dz_pitch] = in ? __bfloat16_as_ushort(__float2bfloat16_rn(d)) : 0;
         }
       } else {
         const int h = u % tiles * 128 + quarter * 32 + lane;
@@ -901,9 +931,11 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
           if (h < p.H)
 #pragma unroll
             for (int j = 0; j < S::COLS; ++j)
-              if (c0 + j < n_rows)
-                p.dx[static_cast<int64_t>(__ldg(p.row_map + c0 + j)) * p.H + h] =
-                    __bfloat16_as_ushort(__float2bfloat16_rn(z[j]));
+              if (c0 + j < n_rows) {
+                const int64_t target = ce_target(p, c0 + j);
+                p.dx[static_cast<int64_t>(c0 + j) * p.H + h] =
+                    target >= 0 && target < p.V ? __bfloat16_as_ushort(__float2bfloat16_rn(z[j])) : 0;
+              }
           continue;
         }
         float* dst = p.acc + (static_cast<int64_t>(u / tiles) * p.pitch + c0) * p.H + h;
@@ -958,8 +990,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
 // Joins the parts of each row: the CTA takes `width` rows (a power of two up to 32), its threads equal shares of the
 // parts.
 constexpr int CE_MERGE_THREADS = 512;
-__global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p, int parts, int width, int statuses, float* loss,
-                                                               float* lse) {
+__global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p, int parts, int width, float* loss, float* lse) {
   __shared__ float2 s[CE_MERGE_THREADS];
   const int r = threadIdx.x % width, share = threadIdx.x / width, shares = CE_MERGE_THREADS / width;
   const int row = blockIdx.x * width + r;
@@ -971,11 +1002,7 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
     m = m_new;
   };
   ce_wait_before();
-  if (blockIdx.x == 0) {
-    uint32_t bits = 0;
-    for (int i = threadIdx.x; i < statuses; i += CE_MERGE_THREADS) bits |= p.status[i];
-    if (bits != 0) atomicOr(&p.meta->error, bits);
-  }
+  if (blockIdx.x == 0) ce_join(p, threadIdx.x, CE_MERGE_THREADS);
   if (row < p.rows) {
 #pragma unroll 8
     for (int i = share; i < parts; i += shares) join(__ldcs(p.part + i * p.pitch + row));
@@ -1019,14 +1046,11 @@ struct CePack {
   uint4* xp;
   int32_t* row_map;
   int T, t_pad;
-  int dx_tile, dx_workers, dx_most;   // ce_splits; few rows: dx_most shares (dx_workers 0)
+  int dx_tile, dx_workers, dx_most;   // ce_splits
 };
 __device__ __forceinline__ void ce_put_meta(const CeParams& p, const CePack& q, int n, bool bad) {   // warp 0
-  int splits = q.dx_most;
-  if (q.dx_workers > 0) {
-    const int units = (n + q.dx_tile - 1) / q.dx_tile * ((p.H + q.dx_tile - 1) / q.dx_tile);
-    splits = ce_splits(units, p.piece_steps, q.dx_workers, q.dx_most);
-  }
+  const int units = (n + q.dx_tile - 1) / q.dx_tile * ((p.H + q.dx_tile - 1) / q.dx_tile);
+  const int splits = ce_splits(units, p.piece_steps, q.dx_workers, q.dx_most);
   if (threadIdx.x == 0) {
     p.meta->n = n;
     p.meta->error = bad ? ERR_TARGET_RANGE : 0u;
@@ -1094,12 +1118,14 @@ constexpr int CE_DX_THREADS = 256;
 __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int steps) {
   __shared__ float4 s_sum[CE_DX_THREADS];
   ce_wait_before();
-  const int split_steps = (p.piece_steps + p.meta->splits - 1) / p.meta->splits;
+  const bool few = p.rows > 0;                // rows as they are, those that take no part among them
+  const int most = few ? p.few_splits : p.meta->splits;
+  const int split_steps = (p.piece_steps + most - 1) / most;
   const int splits = (steps + split_steps - 1) / split_steps;   // of the first piece; a shorter last one has no more
   const int slices = splits >= 8 ? 8 : 1, width = CE_DX_THREADS / slices;
   const int slice = threadIdx.x / width, lane = threadIdx.x % width;
   const int per_row = p.H / 4;
-  const int64_t total = static_cast<int64_t>(p.meta->n) * per_row;
+  const int64_t total = static_cast<int64_t>(ce_rows(p)) * per_row;
   for (int64_t e0 = blockIdx.x * int64_t(width); e0 < total; e0 += gridDim.x * int64_t(width)) {
     const int64_t e = e0 + lane;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1123,9 +1149,14 @@ __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int s
       if (slice == 0)
         for (int q = 1; q < slices; ++q) add(s_sum[q * width + lane]);
     }
-    if (slice == 0 && e < total)
-      reinterpret_cast<uint2*>(p.dx)[static_cast<int64_t>(p.row_map[i]) * per_row + c] =
-          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    if (slice == 0 && e < total) {
+      uint2 o = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (few) {
+        const int64_t target = ce_target(p, i);
+        if (target < 0 || target >= p.V) o = make_uint2(0u, 0u);
+      }
+      reinterpret_cast<uint2*>(p.dx)[(few ? i : static_cast<int64_t>(p.row_map[i])) * per_row + c] = o;
+    }
   }
 }
 
@@ -1277,12 +1308,12 @@ cudaError_t ce_launch(bool pair, int64_t units, const CeDevice& dev, const CUten
 int few_rows(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }   // NT of up to CE_FEW rows
 template <int MODE>
 cudaError_t ce_launch_few(int64_t T, int64_t units, const CeDevice& dev, const CUtensorMap& a, const CUtensorMap& b,
-                          const CeParams& p, cudaStream_t stream, int* ctas = nullptr) {
+                          const CeParams& p, cudaStream_t stream, bool first, int* ctas = nullptr) {
   auto go = [&](auto nt, auto kernel) {
     using S = FewShape<decltype(nt)::value>;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, S::PER_SM * dev.sms));
     if (ctas != nullptr) *ctas = static_cast<int>(grid);
-    return ce_go(kernel, grid, S::THREADS, S::SMEM_BYTES, stream, MODE == CE_LSE, false, a, b, p);
+    return ce_go(kernel, grid, S::THREADS, S::SMEM_BYTES, stream, first, false, a, b, p);
   };
   const int nt = few_rows(T);
   if (nt == 16) return go(std::integral_constant<int, 16>{}, k_ce_few<MODE, 16>);
@@ -1341,7 +1372,7 @@ CeFwdWs ce_fwd_ws(int64_t T, int64_t V) {
 
 // Backward workspace: header, row map, packed x [t_pad, H], dz of one piece [t_pad, piece], fp32 parts of dx.
 struct CeBwdWs {
-  size_t row_map, xp, dz, acc, acc_w, total;
+  size_t status, row_map, xp, dz, acc, acc_w, total;
   int64_t t_pad, piece, pieces;
   int splits, dw_splits;
   bool few;
@@ -1358,8 +1389,9 @@ CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   // dx has few tiles where there are few rows: its K is shared out
   const int64_t tiles = up(T, 128) * up(H, 128);
   const int64_t wanted = w.few ? (w.t_pad < 64 ? 304 : 152) / tiles : tiles >= 8 * 152 ? 1 : CE_MAX_SPLITS;
-  w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(wanted, up(w.piece, 4 * CE_BK))));
-  w.row_map = sizeof(CeMeta);
+  w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(wanted, up(w.piece, 16 * CE_BK))));
+  w.status = sizeof(CeMeta);
+  w.row_map = w.status + CE_MAX_CTAS * sizeof(uint32_t);
   w.xp = up256(w.row_map + static_cast<size_t>(w.t_pad) * 4);
   w.dz = up256(w.xp + static_cast<size_t>(w.t_pad) * H * 2);
   w.acc = up256(w.dz + static_cast<size_t>(w.t_pad) * w.piece * 2);
@@ -1423,14 +1455,16 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   CUtensorMap a, b;
   if (!ce_kmajor(&a, x, T, H, H, few ? few_rows(T) : CE_HALF) || !ce_kmajor(&b, w, V, H, H)) return MXFP8_ERR_CUDA;
   int ctas = 0;
-  const cudaError_t e = few ? ce_launch_few<CE_LSE>(T, up(V, 128), dev, b, a, p, st, &ctas)
+  const cudaError_t e = few ? ce_launch_few<CE_LSE>(T, up(V, 128), dev, b, a, p, st, true, &ctas)
                             : ce_launch<CE_LSE>(pair, up(T, tile) * up(V, tile), dev, a, b, a, p, st, &ctas);
   if (e != cudaSuccess) return MXFP8_ERR_CUDA;
+  p.join = p.status;
+  p.joins = ctas;
   const int parts = few ? ctas : static_cast<int>(2 * up(V, tile));
   // as many rows per CTA as leave every SM one: 1531 rows of 394 parts took 14.8 us with 32
   int width = 32;
   while (width > 1 && up(T, width) < dev.sms) width /= 2;
-  return ce_go(k_ce_merge, up(T, width), CE_MERGE_THREADS, 0, st, false, false, p, parts, width, ctas, loss, lse) ==
+  return ce_go(k_ce_merge, up(T, width), CE_MERGE_THREADS, 0, st, false, false, p, parts, width, loss, lse) ==
                  cudaSuccess
              ? MXFP8_OK
              : MXFP8_ERR_CUDA;
@@ -1485,22 +1519,26 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   const bool dx_pair = !ws.few && use_pair(dev, T, H, ws.splits);
   p.piece_steps = static_cast<int>(up(ws.piece, CE_BK));
   p.few_splits = ws.splits;
-  CePack q{};
-  q.x = static_cast<const uint4*>(x);
-  q.xp = reinterpret_cast<uint4*>(xp);
-  q.row_map = reinterpret_cast<int32_t*>(base + ws.row_map);
-  q.T = static_cast<int>(T);
-  q.t_pad = static_cast<int>(ws.t_pad);
-  q.dx_tile = dx_pair ? 256 : 128;
-  q.dx_workers = ws.few ? 0 : dx_pair ? dev.pairs : dev.sms;
-  q.dx_most = ws.splits;
-  if (ce_go(k_ce_prep, std::min<int64_t>(up(T, 32), dev.sms), CE_PREP_THREADS, 0, st, true, false, p, q) != cudaSuccess)
-    return MXFP8_ERR_CUDA;
+  if (ws.few) {
+    p.rows = static_cast<int>(T);
+  } else {
+    CePack q{};
+    q.x = static_cast<const uint4*>(x);
+    q.xp = reinterpret_cast<uint4*>(xp);
+    q.row_map = reinterpret_cast<int32_t*>(base + ws.row_map);
+    q.T = static_cast<int>(T);
+    q.t_pad = static_cast<int>(ws.t_pad);
+    q.dx_tile = dx_pair ? 256 : 128;
+    q.dx_workers = dx_pair ? dev.pairs : dev.sms;
+    q.dx_most = ws.splits;
+    if (ce_go(k_ce_prep, std::min<int64_t>(up(T, 32), dev.sms), CE_PREP_THREADS, 0, st, true, false, p, q) != cudaSuccess)
+      return MXFP8_ERR_CUDA;
+  }
   CUtensorMap x_k, x_mn, w_k, w_mn, dz_k, dz_mn, dz_st;
   const int box = ws.few ? static_cast<int>(ws.t_pad) : CE_HALF;
   p.dz = dz;
   p.dz_pitch = ws.piece;
-  if (!ce_kmajor(&x_k, xp, ws.t_pad, H, H, box) || !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) ||
+  if (!ce_kmajor(&x_k, ws.few ? x : xp, ws.few ? T : ws.t_pad, H, H, box) || !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) ||
       !ce_mnmajor(&w_mn, w, V, H, H) || !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece, box) ||
       !ce_mnmajor(&dz_mn, dz, ws.t_pad, ws.piece, ws.piece) || !ce_store(&dz_st, dz, ws.t_pad, ws.piece, ws.piece))
     return MXFP8_ERR_CUDA;
@@ -1514,12 +1552,21 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     p.group_m = group_of(H * 2, dz_pair, up(T, zt));
     p.d_rows = static_cast<int>(ws.t_pad);
     p.d_cols = static_cast<int>(ws.piece);
-    if ((ws.few ? ce_launch_few<CE_DZ>(T, up(cols, 128), dev, w_k, x_k, p, st)
-                : ce_launch<CE_DZ>(dz_pair, up(T, zt) * up(cols, zt), dev, x_k, w_k, dz_st, p, st)) != cudaSuccess)
+    if (ws.few) {
+      const bool first = i == 0;
+      CeParams z = p;
+      z.x = static_cast<const uint4*>(x);
+      z.xp = first ? reinterpret_cast<uint4*>(xp) : nullptr;
+      z.status = first ? reinterpret_cast<uint32_t*>(base + ws.status) : nullptr;
+      if (ce_launch_few<CE_DZ>(T, up(cols, 128), dev, w_k, x_k, z, st, first, &p.joins) != cudaSuccess)
+        return MXFP8_ERR_CUDA;
+      p.join = z.status;
+    } else if (ce_launch<CE_DZ>(dz_pair, up(T, zt) * up(cols, zt), dev, x_k, w_k, dz_st, p, st) != cudaSuccess) {
       return MXFP8_ERR_CUDA;
+    }
     p.group_m = 1;
     // dx first: few rows leave w in the L2 for it, which dw overwrites
-    if ((ws.few ? ce_launch_few<CE_DX>(T, up(H, 128) * ws.splits, dev, w_mn, dz_k, p, st)
+    if ((ws.few ? ce_launch_few<CE_DX>(T, up(H, 128) * ws.splits, dev, w_mn, dz_k, p, st, false)
                 : ce_launch<CE_DX>(dx_pair, up(T, xt) * up(H, xt) * ws.splits, dev, dz_k, w_mn, dz_st, p, st)) !=
         cudaSuccess)
       return MXFP8_ERR_CUDA;
