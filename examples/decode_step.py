@@ -4,7 +4,8 @@ A stack of blocks runs one step for T sequences.  Per block:
 
     y        = nvfp4_matvec(o, w_o)                     the attention's output projection (its input o is given)
     r, n     = residual_norm_fwd(y, r, ...)             gate, scaled residual, norm in front of the MoE layer
-    logits   = mxfp8_matvec(n, router)                  routing: softmax over the k largest
+    logits   = mxfp8_matvec(n, router)
+    experts, gates = moe_route_fwd(logits, k)           the k largest, softmax over them
     y        = nvfp4_moe_decode_fwd(n, experts, gates)  the MoE layer
     r, n     = residual_norm_fwd(y, r, ...)             the junction to the next block
 
@@ -75,6 +76,11 @@ class Decoder:
         self.linear_ws = torch.empty(mx.matvec_workspace_size(T, H), dtype=torch.uint8, device=device)
         self.moe_ws = torch.empty(mx.moe_decode_workspace_size(T, k, H, F, E), dtype=torch.uint8, device=device)
         self.choices = [torch.empty((T, k), dtype=torch.int32, device=device) for _ in blocks]
+        # what moe_route_fwd writes beside the choices: weights, lse, counts, sums of the probabilities, losses
+        self.routed = (torch.empty((T, k), device=device), torch.empty(T, device=device),
+                       torch.empty(E + 1, dtype=torch.int32, device=device), torch.empty(E, device=device),
+                       torch.empty(2, device=device))
+        self.route_ws = torch.empty(max(16, mx.moe_route_workspace_size(T, E, k)), dtype=torch.uint8, device=device)
 
     def step(self):
         out = (self.r, self.n, self.stats)
@@ -83,10 +89,8 @@ class Decoder:
             mx.residual_norm_fwd(self.y, self.r, w_post=b.norms[0], w_pre=b.norms[1], res_scale=self.res_scale,
                                  eps=EPS, out=out)
             mx.mxfp8_matvec(self.n, *b.router, out=self.logits, workspace=self.linear_ws)
-            top, experts = self.logits.float().topk(b.k, dim=-1)
-            choices.copy_(experts)
-            mx.nvfp4_moe_decode_fwd(self.n, choices, torch.softmax(top, dim=-1), b.w1, b.w2, out=self.y,
-                                    workspace=self.moe_ws)
+            mx.moe_route_fwd(self.logits, b.k, out=(choices, *self.routed), workspace=self.route_ws)
+            mx.nvfp4_moe_decode_fwd(self.n, choices, self.routed[0], b.w1, b.w2, out=self.y, workspace=self.moe_ws)
             mx.residual_norm_fwd(self.y, self.r, w_post=b.norms[2], gate=b.gate, w_pre=b.norms[3],
                                  res_scale=self.res_scale, eps=EPS, out=out)
 
