@@ -68,7 +68,8 @@ struct CeMeta {
   uint32_t error;
   int32_t n;          // rows that take part (backward)
   int32_t splits;     // shares of the vocabulary in dx
-  int32_t reserved[61];
+  float gain;         // dz is held divided by it
+  int32_t reserved[60];
 };
 static_assert(sizeof(CeMeta) == 256, "header");
 
@@ -92,6 +93,7 @@ struct CeParams {
   float* acc;                  // CE_DX: [splits][pitch][H] fp32, or NULL: dx is written directly
   float* acc_w;                // CE_DW: [dw_splits][vcols][H] fp32, or NULL: dw is written directly
   int dw_splits;
+  int dw_rows;                 // few rows, CE_DW: rows of dz (and of the copies of x)
   int acc_add;
   uint16_t* dz;                // few rows, CE_DZ: [NT][dz_pitch]
   int64_t dz_pitch;
@@ -123,6 +125,28 @@ __device__ __forceinline__ void ce_join(const CeParams& p, int thread, int threa
   for (int i = thread; i < p.joins; i += threads) bits |= p.join[i];
   if (bits != 0) atomicOr(&p.meta->error, bits);
 }
+// dz is held divided by the largest |dloss| (of the finite ones of rows that take part; without any, by the largest
+// |dlse|): where all rows weigh the same, the target's entry is then p - 1, which bf16 holds exactly for p near 0, and not
+// the same weight rounded in every row (by up to 2^-8 and always the same way: 1 / n for a mean).
+struct CeGain {
+  uint32_t loss, lse;   // bits of the largest magnitudes
+  __device__ __forceinline__ CeGain() : loss(0), lse(0) {}
+  static __device__ __forceinline__ uint32_t bits(float v) {
+    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+  }
+  __device__ __forceinline__ void add(const CeParams& p, int64_t row) {
+    loss = max(loss, bits(__ldg(p.dloss + row)));
+    if (p.dlse != nullptr) lse = max(lse, bits(__ldg(p.dlse + row)));
+  }
+  __device__ __forceinline__ void join_warp() {
+    loss = __reduce_max_sync(0xFFFFFFFFu, loss);
+    lse = __reduce_max_sync(0xFFFFFFFFu, lse);
+  }
+  __device__ __forceinline__ float value() const {
+    return loss != 0 ? __uint_as_float(loss) : lse != 0 ? __uint_as_float(lse) : 1.0f;
+  }
+};
 __device__ __forceinline__ int ce_rows(const CeParams& p) { return p.rows > 0 ? p.rows : p.meta->n; }
 __device__ __forceinline__ int64_t ce_target(const CeParams& p, int64_t row) {
   return p.wide_targets ? __ldg(static_cast<const long long*>(p.targets) + row)
@@ -170,7 +194,7 @@ __device__ __forceinline__ void ce_regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// 16 consecutive TMEM columns of this warp's 32 lanes.
+// 16 or 32 consecutive TMEM columns of this warp's 32 lanes.
 __device__ __forceinline__ void ce_tmem_ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -185,6 +209,12 @@ __device__ __forceinline__ void ce_start() {
   if (MODE == CE_DX) ce_wait_before();
   ce_dependents();
   if (MODE == CE_DZ) ce_wait_before();
+}
+
+template <int N>
+__device__ __forceinline__ void ce_tmem_ld(uint32_t taddr, uint32_t* r) {
+  if constexpr (N == 16) ce_tmem_ld16(taddr, r);
+  else tmem_ld_32x32b_x32(taddr, r);
 }
 
 struct CeUnits {
@@ -209,7 +239,7 @@ __device__ __forceinline__ CeUnits ce_units(const CeParams& p) {
   } else if (MODE == CE_DW) {
     c.nm = up(p.vcols, TILE);
     c.nn = up(p.H, TILE);
-    c.steps = up(ce_rows(p), CE_BK);
+    c.steps = up(p.rows > 0 ? p.dw_rows : p.meta->n, CE_BK);
   } else {
     c.nm = up(p.meta->n, TILE);
     c.nn = up(p.H, TILE);
@@ -449,6 +479,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + NH * half;
     uint8_t* wbuf = smem + STAGES * CE_STAGE_BYTES + (warp - CE_EPI_WARP0) * 2 * CE_BUF_BYTES;
     const int n_rows = MODE == CE_LSE ? p.rows : MODE == CE_DW ? 0 : p.meta->n;
+    const float gain = MODE == CE_LSE ? 1.0f : p.meta->gain;
     int buf = 0;
     uint32_t acc_phase = 0;
     for (int u = first; u < units.total; u += stride) {
@@ -467,8 +498,8 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
       if ((MODE == CE_DZ || MODE == CE_DX) && row < n_rows) src = __ldg(p.row_map + row);
       if (MODE == CE_DZ && row < n_rows) {
         y = static_cast<int>(ce_target(p, src)) - p.v0;
-        hot = __ldg(p.dloss + src);
-        rate = hot + (p.dlse != nullptr ? __ldg(p.dlse + src) : 0.0f);
+        hot = __ldg(p.dloss + src) / gain;
+        rate = hot + (p.dlse != nullptr ? __ldg(p.dlse + src) / gain : 0.0f);
         lse2 = __ldg(p.lse + src) * LOG2E;
       }
       auto wait_acc = [&]() {
@@ -570,6 +601,10 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
                                 make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]));
             continue;
           }
+          if (MODE == CE_DW) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * gain);
+          }
           uint8_t* out = wbuf + ((c >> 5) & 1) * CE_BUF_BYTES;
           if (lane == 0) bulk_wait_read_le1();      // the store that last used this buffer has read it
           __syncwarp();
@@ -591,6 +626,8 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
           }
         } else if (row < n_rows) {                  // CE_DX
           if (p.acc == nullptr) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * gain);
             uint16_t* dst = p.dx + static_cast<int64_t>(src) * p.H + col;
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
@@ -655,30 +692,35 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
 //           over all its tiles, and lanes are joined once, at the end
 //   CE_DZ   the same product and dz; rows that take no part are zeros in dz and in a copy of x for dw (no packing)
 //   CE_DX   dx^T = w^T dz^T over a share of the vocabulary: fp32 parts
+// The tensor cores have time to spare here, so dz is held in two bf16 pieces, the second of what the first one leaves (to
+// 2^-16 of it): NT rows of first pieces and NT of second ones, in dx's product as 2 NT columns, in dw's as 2 NT rows of K
+// beside two copies of x.
 constexpr int CE_FEW = 64;
-constexpr int CE_FEW_BUFS = 4;                     // accumulators of NT columns
-template <int NT>
+constexpr int CE_FEW_BUFS = 4;                     // accumulators of NT columns (dx: 2 NT)
+constexpr int CE_FEW_CHUNK = 2;                    // as CE_CHUNK: the epilogue has nothing else to do
+template <int MODE, int NT>
 struct FewShape {
   static constexpr int EPI_WARPS = NT == 64 ? 8 : 4;        // 64 rows' maxima and sums need two threads per entry
   static constexpr int COLS = NT / (EPI_WARPS / 4);
   static constexpr int PER_SM = NT == 64 ? 1 : 2;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr int B_BYTES = NT * CE_BK * 2;
+  static constexpr int NB = MODE == CE_DX ? 2 * NT : NT;    // rows of the N operand
+  static constexpr int B_BYTES = NB * CE_BK * 2;
   static constexpr int STAGE_BYTES = CE_OP_BYTES + B_BYTES;
-  static constexpr int STAGES = NT == 64 ? 9 : NT == 32 ? 5 : 6;
+  static constexpr int STAGES = MODE == CE_DX ? (NT == 64 ? 6 : NT == 32 ? 4 : 5) : (NT == 64 ? 9 : NT == 32 ? 5 : 6);
   static constexpr int PARAM_OFFSET = STAGES * STAGE_BYTES;             // [NT] float4 (CE_DZ), [EPI_WARPS][COLS] float2 (CE_LSE)
   static constexpr int BAR_OFFSET = PARAM_OFFSET + EPI_WARPS * COLS * 16;
   static constexpr int SMEM_BYTES = BAR_OFFSET + (2 * STAGES + 2 * CE_FEW_BUFS + 1) * 8 + 8 + 1024;
   static_assert(SMEM_BYTES <= (PER_SM == 2 ? 115712 : 232448), "shared memory budget");
-  static_assert(PER_SM * CE_FEW_BUFS * NT <= 512, "TMEM budget");
+  static_assert(PER_SM * CE_FEW_BUFS * NB <= 512, "TMEM budget");
 };
 
 template <int MODE, int NT>
-__global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
+__global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT>::PER_SM)
     k_ce_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const CeParams p) {
-  using S = FewShape<NT>;
+  using S = FewShape<MODE, NT>;
   constexpr bool A_MN = MODE == CE_DX;
-  constexpr int CHUNK = MODE == CE_LSE ? CE_CHUNK : 1 << 30;
+  constexpr int CHUNK = MODE == CE_LSE ? CE_FEW_CHUNK : 1 << 30;
   constexpr int NO_TARGET = INT_MIN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -711,7 +753,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, CE_FEW_BUFS * NT);
+    tmem_alloc(tmem_holder, CE_FEW_BUFS * S::NB);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -783,7 +825,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
   } else if (warp == 1) {
     // ---------------- MMA issuer (one lane) ----------------
     if (lane == 0) {
-      constexpr uint32_t idesc = ce_idesc(128, NT, A_MN, false);
+      constexpr uint32_t idesc = ce_idesc(128, S::NB, A_MN, false);
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool issued = false, ok = true;
@@ -805,7 +847,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
           const uint32_t a0 = smem_u32(smem + stage * S::STAGE_BYTES), b0 = a0 + CE_OP_BYTES;
 #pragma unroll
           for (int k = 0; k < CE_BK / 16; ++k)
-            ce_mma<1>(tmem + buf * NT, A_MN ? ce_sdesc_mn(a0 + 2048 * k) : sdesc_kmajor_sw128(a0 + 32 * k),
+            ce_mma<1>(tmem + buf * S::NB, A_MN ? ce_sdesc_mn(a0 + 2048 * k) : sdesc_kmajor_sw128(a0 + 32 * k),
                       sdesc_kmajor_sw128(b0 + 32 * k), idesc, (s % CHUNK | k) != 0 ? 1u : 0u);
           tc_commit(&empty[stage]);
           issued = true;
@@ -836,8 +878,20 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
     const int n_rows = p.rows;
     // CE_DZ: what each row needs; CE_LSE: its target
     float4* s_row = reinterpret_cast<float4*>(smem + S::PARAM_OFFSET);
+    float gain = 1.0f;
+    if (MODE == CE_DX) gain = p.meta->gain;
     if (MODE != CE_DX) {
       const int i = static_cast<int>(threadIdx.x) - 64;
+      if (MODE == CE_DZ) {                          // every warp for itself
+        CeGain g;
+        for (int t = lane; t < n_rows; t += 32) {
+          const int64_t target = ce_target(p, t);
+          if (target >= 0 && target < p.V) g.add(p, t);
+        }
+        g.join_warp();
+        gain = g.value();
+        if (blockIdx.x == 0 && i == 0) p.meta->gain = gain;
+      }
       if (i < NT) {
         float4 r = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(NO_TARGET));
         if (i < n_rows) {
@@ -845,8 +899,8 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
           if (target >= 0 && target < p.V) {
             r.w = __int_as_float(static_cast<int>(target) - p.v0);
             if (MODE == CE_DZ) {
-              r.z = __ldg(p.dloss + i);
-              r.x = r.z + (p.dlse != nullptr ? __ldg(p.dlse + i) : 0.0f);
+              r.z = __ldg(p.dloss + i) / gain;
+              r.x = r.z + (p.dlse != nullptr ? __ldg(p.dlse + i) / gain : 0.0f);
               r.y = __ldg(p.lse + i) * LOG2E;
             }
           }
@@ -860,8 +914,11 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
         for (int r = blockIdx.x; r < NT; r += gridDim.x) {
           const bool in = __float_as_int(s_row[r].w) != NO_TARGET;
           const int64_t per_row = p.H / 8;
-          for (int64_t c = i; c < per_row; c += S::EPI_WARPS * 32)
-            p.xp[r * per_row + c] = in ? __ldg(p.x + r * per_row + c) : make_uint4(0u, 0u, 0u, 0u);
+          for (int64_t c = i; c < per_row; c += S::EPI_WARPS * 32) {
+            const uint4 o = in ? __ldg(p.x + r * per_row + c) : make_uint4(0u, 0u, 0u, 0u);
+            p.xp[r * per_row + c] = o;
+            p.xp[(NT + r) * per_row + c] = o;
+          }
         }
     } else if (p.join != nullptr && blockIdx.x == 0) {
       ce_join(p, static_cast<int>(threadIdx.x) - 64, S::EPI_WARPS * 32);
@@ -888,9 +945,14 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
         if (!ok) break;
         tc_fence_after();
         uint32_t v[S::COLS];
-        if constexpr (S::COLS == 16) ce_tmem_ld16(t_row + buf * NT, v);
-        else tmem_ld_32x32b_x32(t_row + buf * NT, v);
+        ce_tmem_ld<S::COLS>(t_row + buf * S::NB, v);
+        uint32_t lo[MODE == CE_DX ? S::COLS : 1];
+        if constexpr (MODE == CE_DX) ce_tmem_ld<S::COLS>(t_row + buf * S::NB + NT, lo);
         tmem_ld_wait();
+        if constexpr (MODE == CE_DX) {
+#pragma unroll
+          for (int j = 0; j < S::COLS; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(lo[j]));
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[buf]);
@@ -923,7 +985,9 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
           float d = r.x * ex2(fmaf(z[j], LOG2E, -r.y));
           if (__float_as_int(r.w) == v) d -= r.z;
           const bool in = __float_as_int(r.w) != NO_TARGET && v < p.vcols;
-          dst[j * p.dz_pitch] = in ? __bfloat16_as_ushort(__float2bfloat16_rn(d)) : 0;
+          const __nv_bfloat16 hi = __float2bfloat16_rn(d), lo = __float2bfloat16_rn(d - __bfloat162float(hi));
+          dst[j * p.dz_pitch] = in ? __bfloat16_as_ushort(hi) : 0;
+          dst[(NT + j) * p.dz_pitch] = in ? __bfloat16_as_ushort(lo) : 0;
         }
       } else {
         const int h = u % tiles * 128 + quarter * 32 + lane;
@@ -934,7 +998,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
               if (c0 + j < n_rows) {
                 const int64_t target = ce_target(p, c0 + j);
                 p.dx[static_cast<int64_t>(c0 + j) * p.H + h] =
-                    target >= 0 && target < p.V ? __bfloat16_as_ushort(__float2bfloat16_rn(z[j])) : 0;
+                    target >= 0 && target < p.V ? __bfloat16_as_ushort(__float2bfloat16_rn(z[j] * gain)) : 0;
               }
           continue;
         }
@@ -983,7 +1047,7 @@ __global__ void __launch_bounds__(FewShape<NT>::THREADS, FewShape<NT>::PER_SM)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, CE_FEW_BUFS * NT);
+    tmem_dealloc(tmem, CE_FEW_BUFS * S::NB);
   }
 }
 
@@ -1048,13 +1112,14 @@ struct CePack {
   int T, t_pad;
   int dx_tile, dx_workers, dx_most;   // ce_splits
 };
-__device__ __forceinline__ void ce_put_meta(const CeParams& p, const CePack& q, int n, bool bad) {   // warp 0
+__device__ __forceinline__ void ce_put_meta(const CeParams& p, const CePack& q, int n, bool bad, float gain) {   // warp 0
   const int units = (n + q.dx_tile - 1) / q.dx_tile * ((p.H + q.dx_tile - 1) / q.dx_tile);
   const int splits = ce_splits(units, p.piece_steps, q.dx_workers, q.dx_most);
   if (threadIdx.x == 0) {
     p.meta->n = n;
     p.meta->error = bad ? ERR_TARGET_RANGE : 0u;
     p.meta->splits = splits;
+    p.meta->gain = gain;
   }
 }
 // The rows that take part, packed in order: row_map[i] and xp[i] = x[row_map[i]] for i < n, zeros up to t_pad; dx of the
@@ -1063,15 +1128,18 @@ __device__ __forceinline__ void ce_put_meta(const CeParams& p, const CePack& q, 
 constexpr int CE_PREP_THREADS = 1024;
 __global__ void __launch_bounds__(CE_PREP_THREADS) k_ce_prep(const CeParams p, const CePack q) {
   __shared__ int s_warp[3][32];
+  __shared__ uint32_t s_gain[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ce_dependents();
   const int per = (q.T + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int r0 = min(q.T, static_cast<int>(blockIdx.x) * per), r1 = min(q.T, r0 + per);
   int all = 0, ahead = 0, bad = 0;
+  CeGain gain;
 #pragma unroll 4
   for (int t = threadIdx.x; t < q.T; t += CE_PREP_THREADS) {
     const int64_t y = ce_target(p, t);
     const int in = y >= 0 && y < p.V;
+    if (in && blockIdx.x == 0) gain.add(p, t);
     all += in;
     ahead += t < r0 ? in : 0;
     bad |= y >= p.V;
@@ -1079,7 +1147,10 @@ __global__ void __launch_bounds__(CE_PREP_THREADS) k_ce_prep(const CeParams p, c
   all = __reduce_add_sync(0xFFFFFFFFu, all);
   ahead = __reduce_add_sync(0xFFFFFFFFu, ahead);
   bad = __any_sync(0xFFFFFFFFu, bad);
+  gain.join_warp();
   if (lane == 0) {
+    s_gain[0][warp] = gain.loss;
+    s_gain[1][warp] = gain.lse;
     s_warp[0][warp] = all;
     s_warp[1][warp] = ahead;
     s_warp[2][warp] = bad;
@@ -1088,7 +1159,12 @@ __global__ void __launch_bounds__(CE_PREP_THREADS) k_ce_prep(const CeParams p, c
   const int n = __reduce_add_sync(0xFFFFFFFFu, s_warp[0][lane]);
   int at = __reduce_add_sync(0xFFFFFFFFu, s_warp[1][lane]);
   bad = __any_sync(0xFFFFFFFFu, s_warp[2][lane]);
-  if (blockIdx.x == 0 && warp == 0) ce_put_meta(p, q, n, bad != 0);
+  if (blockIdx.x == 0 && warp == 0) {
+    gain.loss = s_gain[0][lane];
+    gain.lse = s_gain[1][lane];
+    gain.join_warp();
+    ce_put_meta(p, q, n, bad != 0, gain.value());
+  }
   const int64_t per_row = p.H / 8;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   // 32 rows at a time: every warp knows which of them take part, and copies its own
@@ -1120,6 +1196,7 @@ __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int s
   ce_wait_before();
   const bool few = p.rows > 0;                // rows as they are, those that take no part among them
   const int most = few ? p.few_splits : p.meta->splits;
+  const float gain = p.meta->gain;
   const int split_steps = (p.piece_steps + most - 1) / most;
   const int splits = (steps + split_steps - 1) / split_steps;   // of the first piece; a shorter last one has no more
   const int slices = splits >= 8 ? 8 : 1, width = CE_DX_THREADS / slices;
@@ -1150,7 +1227,7 @@ __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int s
         for (int q = 1; q < slices; ++q) add(s_sum[q * width + lane]);
     }
     if (slice == 0 && e < total) {
-      uint2 o = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      uint2 o = make_uint2(pack_bf16x2(v.x * gain, v.y * gain), pack_bf16x2(v.z * gain, v.w * gain));
       if (few) {
         const int64_t target = ce_target(p, i);
         if (target < 0 || target >= p.V) o = make_uint2(0u, 0u);
@@ -1165,6 +1242,7 @@ __global__ void __launch_bounds__(256) k_ce_dw(const CeParams p, uint16_t* dw) {
   ce_wait_before();
   const int64_t total = static_cast<int64_t>(p.vcols) * (p.H / 4);
   const float4* a = reinterpret_cast<const float4*>(p.acc_w);
+  const float gain = p.meta->gain;
   for (int64_t e = blockIdx.x * int64_t(256) + threadIdx.x; e < total; e += gridDim.x * int64_t(256)) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
@@ -1175,7 +1253,8 @@ __global__ void __launch_bounds__(256) k_ce_dw(const CeParams p, uint16_t* dw) {
       v.z += o.z;
       v.w += o.w;
     }
-    reinterpret_cast<uint2*>(dw)[e] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    reinterpret_cast<uint2*>(dw)[e] =
+        make_uint2(pack_bf16x2(v.x * gain, v.y * gain), pack_bf16x2(v.z * gain, v.w * gain));
   }
 }
 
@@ -1255,8 +1334,8 @@ bool ce_prepare_few() {
   auto set = [](auto kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
-  return set(k_ce_few<MODE, 16>, FewShape<16>::SMEM_BYTES) && set(k_ce_few<MODE, 32>, FewShape<32>::SMEM_BYTES) &&
-         set(k_ce_few<MODE, 64>, FewShape<64>::SMEM_BYTES);
+  return set(k_ce_few<MODE, 16>, FewShape<MODE, 16>::SMEM_BYTES) &&
+         set(k_ce_few<MODE, 32>, FewShape<MODE, 32>::SMEM_BYTES) && set(k_ce_few<MODE, 64>, FewShape<MODE, 64>::SMEM_BYTES);
 }
 bool ce_device(CeDevice* out) {
   static CeDevice info[64];
@@ -1310,7 +1389,7 @@ template <int MODE>
 cudaError_t ce_launch_few(int64_t T, int64_t units, const CeDevice& dev, const CUtensorMap& a, const CUtensorMap& b,
                           const CeParams& p, cudaStream_t stream, bool first, int* ctas = nullptr) {
   auto go = [&](auto nt, auto kernel) {
-    using S = FewShape<decltype(nt)::value>;
+    using S = FewShape<MODE, decltype(nt)::value>;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, S::PER_SM * dev.sms));
     if (ctas != nullptr) *ctas = static_cast<int>(grid);
     return ce_go(kernel, grid, S::THREADS, S::SMEM_BYTES, stream, first, false, a, b, p);
@@ -1381,14 +1460,14 @@ constexpr int CE_MAX_SPLITS = 16;
 CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   CeBwdWs w{};
   w.few = T <= CE_FEW;
-  w.t_pad = w.few ? few_rows(T) : up(T, 256) * 256;
+  w.t_pad = w.few ? 2 * few_rows(T) : up(T, 256) * 256;   // few: dz and x twice
   const int64_t most = std::max(CE_MIN_PIECE, CE_DZ_ELEMS / std::max<int64_t>(w.t_pad, 256) / 256 * 256);
   w.pieces = up(V, most);
   w.piece = up(up(V, w.pieces), 256) * 256;
   w.pieces = up(V, w.piece);
   // dx has few tiles where there are few rows: its K is shared out
   const int64_t tiles = up(T, 128) * up(H, 128);
-  const int64_t wanted = w.few ? (w.t_pad < 64 ? 304 : 152) / tiles : tiles >= 8 * 152 ? 1 : CE_MAX_SPLITS;
+  const int64_t wanted = w.few ? (T <= 32 ? 304 : 152) / tiles : tiles >= 8 * 152 ? 1 : CE_MAX_SPLITS;
   w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(wanted, up(w.piece, 16 * CE_BK))));
   w.status = sizeof(CeMeta);
   w.row_map = w.status + CE_MAX_CTAS * sizeof(uint32_t);
@@ -1521,6 +1600,7 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.few_splits = ws.splits;
   if (ws.few) {
     p.rows = static_cast<int>(T);
+    p.dw_rows = static_cast<int>(ws.t_pad);
   } else {
     CePack q{};
     q.x = static_cast<const uint4*>(x);
@@ -1535,11 +1615,10 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
       return MXFP8_ERR_CUDA;
   }
   CUtensorMap x_k, x_mn, w_k, w_mn, dz_k, dz_mn, dz_st;
-  const int box = ws.few ? static_cast<int>(ws.t_pad) : CE_HALF;
   p.dz = dz;
   p.dz_pitch = ws.piece;
-  if (!ce_kmajor(&x_k, ws.few ? x : xp, ws.few ? T : ws.t_pad, H, H, box) || !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) ||
-      !ce_mnmajor(&w_mn, w, V, H, H) || !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece, box) ||
+  if (!ce_kmajor(&x_k, ws.few ? x : xp, ws.few ? T : ws.t_pad, H, H, ws.few ? few_rows(T) : CE_HALF) || !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) ||
+      !ce_mnmajor(&w_mn, w, V, H, H) || !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece, ws.few ? 2 * few_rows(T) : CE_HALF) ||
       !ce_mnmajor(&dz_mn, dz, ws.t_pad, ws.piece, ws.piece) || !ce_store(&dz_st, dz, ws.t_pad, ws.piece, ws.piece))
     return MXFP8_ERR_CUDA;
   for (int64_t i = 0; i < ws.pieces; ++i) {
