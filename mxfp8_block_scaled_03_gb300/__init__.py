@@ -74,6 +74,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load the CUDA library (raises if it has not been built: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(build_ext.LIB):

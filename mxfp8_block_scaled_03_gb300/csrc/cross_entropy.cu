@@ -1095,15 +1095,19 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
 }
 
 // Shares of the vocabulary in dx, from the rows that take part: as many as deal the K steps out evenly to `workers` CTAs
-// (or pairs), a share's fixed cost counted as CE_SHARE_STEPS steps.
+// (or pairs).  Counted in K steps (about 0.27 us): a share's start and end, and its part of dx, written and read back
+// (1072 x 2048 values in 15 parts took 48 us to add up; 3 parts leave 10, and the product 10 us longer).
 constexpr int CE_SHARE_STEPS = 8;
-__device__ __forceinline__ int ce_splits(int units, int steps, int workers, int most) {   // a whole warp; most <= 32
+constexpr float CE_PART_STEPS = 4.4e-6f;   // per value of dx: 8 bytes at 6.8 TB/s
+__device__ __forceinline__ int ce_splits(int n, int H, int tile, int steps, int workers, int most) {   // a warp; most <= 32
   const int s = 1 + (threadIdx.x & 31);
-  const int64_t waves = (static_cast<int64_t>(units) * s + workers - 1) / workers;
-  const int64_t c = waves * ((steps + s - 1) / s + CE_SHARE_STEPS);
-  const uint32_t cost = s <= most && s <= steps && c < INT_MAX ? static_cast<uint32_t>(c) : INT_MAX;
+  const int64_t units = static_cast<int64_t>((n + tile - 1) / tile) * ((H + tile - 1) / tile);
+  const int64_t waves = (units * s + workers - 1) / workers;
+  const float c = static_cast<float>(waves * ((steps + s - 1) / s + CE_SHARE_STEPS)) +
+                  (s > 1 ? static_cast<float>(s) * CE_PART_STEPS * static_cast<float>(n) * static_cast<float>(H) : 0.0f);
+  const uint32_t cost = s <= most && s <= steps ? __float_as_uint(c) : 0x7F800000u;   // in the order of the floats
   const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, cost);
-  return __ffs(__ballot_sync(0xFFFFFFFFu, cost == least));
+  return max(1, __ffs(__ballot_sync(0xFFFFFFFFu, cost == least)));
 }
 struct CePack {
   const uint4* x;
@@ -1113,8 +1117,7 @@ struct CePack {
   int dx_tile, dx_workers, dx_most;   // ce_splits
 };
 __device__ __forceinline__ void ce_put_meta(const CeParams& p, const CePack& q, int n, bool bad, float gain) {   // warp 0
-  const int units = (n + q.dx_tile - 1) / q.dx_tile * ((p.H + q.dx_tile - 1) / q.dx_tile);
-  const int splits = ce_splits(units, p.piece_steps, q.dx_workers, q.dx_most);
+  const int splits = ce_splits(n, p.H, q.dx_tile, p.piece_steps, q.dx_workers, q.dx_most);
   if (threadIdx.x == 0) {
     p.meta->n = n;
     p.meta->error = bad ? ERR_TARGET_RANGE : 0u;
@@ -1165,27 +1168,30 @@ __global__ void __launch_bounds__(CE_PREP_THREADS) k_ce_prep(const CeParams p, c
     gain.join_warp();
     ce_put_meta(p, q, n, bad != 0, gain.value());
   }
-  const int64_t per_row = p.H / 8;
+  const int per_row = p.H / 8;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  // 32 rows at a time: every warp knows which of them take part, and copies its own
+  // 32 rows at a time: every warp knows which of them take part; the threads share out their pieces
   for (int t0 = r0; t0 < r1; t0 += 32) {
     const int t = t0 + lane;
     const int64_t y = t < r1 ? ce_target(p, t) : -1;
     const uint32_t in = __ballot_sync(0xFFFFFFFFu, y >= 0 && y < p.V);
-    const int rows = min(32, r1 - t0);
-    if (warp < rows) {
-      const bool mine = (in >> warp) & 1u;
-      const int i = at + __popc(in & ((1u << warp) - 1u)), src = t0 + warp;
-      uint4* to = mine ? q.xp + i * per_row : reinterpret_cast<uint4*>(p.dx) + src * per_row;
-      const uint4* from = q.x + src * per_row;
+    const int64_t pieces = static_cast<int64_t>(min(32, r1 - t0)) * per_row;
 #pragma unroll 4
-      for (int64_t c = lane; c < per_row; c += 32) to[c] = mine ? __ldcs(from + c) : zero;
-      if (mine && lane == 0) q.row_map[i] = src;
+    for (int64_t e = threadIdx.x; e < pieces; e += CE_PREP_THREADS) {
+      const int r = static_cast<int>(e / per_row);
+      const int64_t src = t0 + r, c = e - static_cast<int64_t>(r) * per_row;
+      if ((in >> r) & 1u) {
+        const int64_t i = at + __popc(in & ((1u << r) - 1u));
+        q.xp[i * per_row + c] = __ldcs(q.x + src * per_row + c);
+      } else {
+        reinterpret_cast<uint4*>(p.dx)[src * per_row + c] = zero;
+      }
     }
+    if (warp == 0 && (in >> lane) & 1u) q.row_map[at + __popc(in & ((1u << lane) - 1u))] = t;
     at += __popc(in);
   }
   for (int64_t i = n + blockIdx.x * int64_t(32) + warp; i < q.t_pad; i += gridDim.x * int64_t(32))
-    for (int64_t c = lane; c < per_row; c += 32) q.xp[i * per_row + c] = zero;
+    for (int c = lane; c < per_row; c += 32) q.xp[i * per_row + c] = zero;
 }
 
 // dx of the packed rows from their fp32 parts, added in a fixed order: a thread has four columns, of eight or more shares
@@ -1611,14 +1617,15 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     q.dx_tile = dx_pair ? 256 : 128;
     q.dx_workers = dx_pair ? dev.pairs : dev.sms;
     q.dx_most = ws.splits;
-    if (ce_go(k_ce_prep, std::min<int64_t>(up(T, 32), dev.sms), CE_PREP_THREADS, 0, st, true, false, p, q) != cudaSuccess)
+    if (ce_go(k_ce_prep, std::min<int64_t>(up(T, 8), 2 * dev.sms), CE_PREP_THREADS, 0, st, true, false, p, q) != cudaSuccess)
       return MXFP8_ERR_CUDA;
   }
   CUtensorMap x_k, x_mn, w_k, w_mn, dz_k, dz_mn, dz_st;
   p.dz = dz;
   p.dz_pitch = ws.piece;
-  if (!ce_kmajor(&x_k, ws.few ? x : xp, ws.few ? T : ws.t_pad, H, H, ws.few ? few_rows(T) : CE_HALF) || !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) ||
-      !ce_mnmajor(&w_mn, w, V, H, H) || !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece, ws.few ? 2 * few_rows(T) : CE_HALF) ||
+  if (!ce_kmajor(&x_k, ws.few ? x : xp, ws.few ? T : ws.t_pad, H, H, ws.few ? few_rows(T) : CE_HALF) ||
+      !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) || !ce_mnmajor(&w_mn, w, V, H, H) ||
+      !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece, ws.few ? 2 * few_rows(T) : CE_HALF) ||
       !ce_mnmajor(&dz_mn, dz, ws.t_pad, ws.piece, ws.piece) || !ce_store(&dz_st, dz, ws.t_pad, ws.piece, ws.piece))
     return MXFP8_ERR_CUDA;
   for (int64_t i = 0; i < ws.pieces; ++i) {
@@ -1653,8 +1660,12 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     if (!ce_store(&dw_st, static_cast<uint16_t*>(dw) + v0 * H, cols, H, H)) return MXFP8_ERR_CUDA;
     p.d_rows = static_cast<int>(cols);
     p.d_cols = static_cast<int>(H);
+    // few K steps: a tile is mostly its epilogue, so two CTAs per SM; of more rows only where these are done in two turns
+    // (256 x 2048 x 50257: 183 us with them, 162 without; 100 x 1448 x 3600: 33 and 37)
+    const bool dw_short =
+        ws.few || (T <= 4 * CE_BK && ws.dw_splits == 1 && up(cols, 128) * up(H, 128) <= 4 * dev.sms);
     const cudaError_t e =
-        ws.few ? ce_go(k_ce_gemm<CE_DW, 1, CE_SHORT>, std::min<int64_t>(up(cols, 128) * up(H, 128), 2 * dev.sms),
+        dw_short ? ce_go(k_ce_gemm<CE_DW, 1, CE_SHORT>, std::min<int64_t>(up(cols, 128) * up(H, 128), 2 * dev.sms),
                        CE_THREADS, ce_smem_bytes(CE_SHORT), st, false, false, dz_mn, x_mn, dw_st, p)
                : ce_launch<CE_DW>(dw_pair, up(cols, wt) * up(H, wt) * ws.dw_splits, dev, dz_mn, x_mn, dw_st, p, st);
     if (e != cudaSuccess) return MXFP8_ERR_CUDA;
