@@ -125,8 +125,8 @@ __device__ __forceinline__ void ce_join(const CeParams& p, int thread, int threa
   for (int i = thread; i < p.joins; i += threads) bits |= p.join[i];
   if (bits != 0) atomicOr(&p.meta->error, bits);
 }
-// dz is held divided by the largest |dloss| (of the finite ones of rows that take part; without any, by the largest
-// |dlse|): where all rows weigh the same, the target's entry is then p - 1, which bf16 holds exactly for p near 0, and not
+// dz is held divided by the largest |dloss| (of the finite ones of rows that take part; by the largest |dlse| where that is
+// 2^64 times as large): where all rows weigh the same, the target's entry is then p - 1, which bf16 holds exactly for p near 0, and not
 // the same weight rounded in every row (by up to 2^-8 and always the same way: 1 / n for a mean).
 struct CeGain {
   uint32_t loss, lse;   // bits of the largest magnitudes
@@ -144,7 +144,8 @@ struct CeGain {
     lse = __reduce_max_sync(0xFFFFFFFFu, lse);
   }
   __device__ __forceinline__ float value() const {
-    return loss != 0 ? __uint_as_float(loss) : lse != 0 ? __uint_as_float(lse) : 1.0f;
+    const bool small = (lse >> 23) > (loss >> 23) + 64;
+    return loss != 0 && !small ? __uint_as_float(loss) : lse != 0 ? __uint_as_float(lse) : 1.0f;
   }
 };
 __device__ __forceinline__ int ce_rows(const CeParams& p) { return p.rows > 0 ? p.rows : p.meta->n; }

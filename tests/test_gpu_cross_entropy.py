@@ -289,3 +289,78 @@ def test_neighbours_of_the_outputs_are_left_alone(mx):
     mx.linear_cross_entropy_bwd(torch.ones(T, device="cuda"), x, w, y, lse, out=(dx, dw))
     for b, n in zip(bufs, (T, T, T * H, V * H)):
         assert (b[:32] == 9).all() and (b[32 + n:] == 9).all()
+
+
+@pytest.mark.parametrize("T", [30, 300])
+@pytest.mark.parametrize("loss_scale,lse_scale", [(0.0, 1.0), (1.0, 0.0), (0.0, 0.0), (1e-30, 1e10), (1e10, 1e-30), (1e-38, 1e-39)])
+def test_weights_of_any_size(mx, T, loss_scale, lse_scale):
+    """dloss alone, dlse alone, neither, and each far above the other: dx and dw scale with them."""
+    import torch
+    H, V = 128, 700
+    x, w, y = make(T, H, V, seed=31)
+    _, lse = mx.linear_cross_entropy_fwd(x, w, y)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    dloss = loss_scale * (0.5 + torch.rand(T, generator=gen, device="cuda"))
+    dlse = lse_scale * (0.5 + torch.rand(T, generator=gen, device="cuda"))
+    dx, dw = mx.linear_cross_entropy_bwd(dloss, x, w, y, lse, dlse=dlse)
+    if loss_scale == lse_scale == 0.0:
+        assert not dx.any() and not dw.any()
+        return
+    scale = max(loss_scale, lse_scale)
+    rows = torch.nonzero(y >= 0)[:, 0]
+    X, W = x[rows].double(), w.double()
+    dz = (dloss + dlse.double())[rows][:, None] * torch.exp(X @ W.t() - lse[rows].double()[:, None])
+    dz.scatter_add_(1, y[rows].long()[:, None], -dloss[rows].double()[:, None])
+    for got, want in ((dx[rows], dz @ W), (dw, dz.t() @ X)):
+        # by the norms (see above), and below 2^-126 by the results' own steps of 2^-133
+        assert got.isfinite().all()
+        err = float((got.double() - want).norm())
+        assert err <= 2.0 ** -7 * float(want.norm()) + 2.0 ** -134 * want.numel() ** 0.5, (scale, err)
+
+
+def test_one_row_with_a_weight_of_nan_stays_its_own(mx):
+    """NaN in dloss of a row that takes part: NaN in its dx and in dw, nothing in the other rows of dx."""
+    import torch
+    for T in (20, 200):
+        x, w, y = make(T, 64, 300, seed=4, ignored=0.0)
+        _, lse = mx.linear_cross_entropy_fwd(x, w, y)
+        dloss = torch.ones(T, device="cuda")
+        clean, _ = mx.linear_cross_entropy_bwd(dloss, x, w, y, lse)
+        dloss[3] = math.nan
+        dx, dw = mx.linear_cross_entropy_bwd(dloss, x, w, y, lse)
+        keep = torch.arange(T, device="cuda") != 3
+        assert dx[3].isnan().all() and dw.isnan().all() and torch.equal(dx[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T", [20, 200])
+def test_more_than_four_gigabytes_of_weights(mx, T):
+    """V * H past 2^31 elements: rows of dw and logits beyond that offset."""
+    import torch
+    H, V = 2056, (1 << 20) + 77
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    w = torch.empty((V, H), dtype=torch.bfloat16, device="cuda")
+    for r in range(0, V, 65536):
+        w[r:r + 65536] = torch.randn((min(65536, V - r), H), generator=gen, device="cuda") / math.sqrt(H)
+    y = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    y[:4] = torch.tensor([V - 1, V - 77, 1 << 20, 0], device="cuda")
+    x = (torch.randn((T, H), generator=gen, device="cuda") + 8.0 * w[y].float()).bfloat16()
+    loss, lse = mx.linear_cross_entropy_fwd(x, w, y)
+    m = torch.full((T,), -math.inf, dtype=torch.float64, device="cuda")
+    for r in range(0, V, 131072):
+        m = torch.logaddexp(m, torch.logsumexp(x.double() @ w[r:r + 131072].double().t(), 1))
+    zy = (x.double() * w[y].double()).sum(1)
+    bar = 2.0 ** -15 + (H / 16 + 8) * 2.0 ** -22 * 4 * math.sqrt(H)   # sum of |x w|: below 4 sqrt(H) here
+    assert (lse.double() - m).abs().max() <= bar and (loss.double() - (m - zy)).abs().max() <= 2 * bar
+    dloss = torch.full((T,), 1.0 / T, device="cuda")
+    dx, dw = mx.linear_cross_entropy_bwd(dloss, x, w, y, lse)
+    want = torch.zeros((T, H), dtype=torch.float64, device="cuda")
+    for r in range(0, V, 131072):
+        W = w[r:r + 131072].double()
+        dz = torch.exp(x.double() @ W.t() - lse.double()[:, None]) / T
+        hit = torch.nonzero((y >= r) & (y < r + len(W)))[:, 0]
+        dz[hit, y[hit] - r] -= 1.0 / T
+        want += dz @ W
+        if r in (0, 1 << 20) or r + len(W) == V:
+            ref = dz.t() @ x.double()
+            assert (dw[r:r + len(W)].double() - ref).norm() <= 2.0 ** -7 * ref.norm()
+    assert (dx.double() - want).norm() <= 2.0 ** -7 * want.norm()
