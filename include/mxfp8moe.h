@@ -498,7 +498,8 @@ int residual_norm_bwd(const void* dn, const void* dres_out, const void* y, const
  *   lse        (device, out) float [T]; -inf where the token takes no part.
  *   counts     (device, out) int32 [E + 1]: choices per expert, then N.
  *   prob_sum   (device, out) float [E].   losses (device, out) float [2].
- *   workspace  moe_route_workspace_size(T, E, k) bytes, 16-byte aligned (unused for few tokens).
+ *   workspace  moe_route_workspace_size(T, E, k) bytes, 16-byte aligned (unused for few tokens).  Nothing in it needs
+ *              to be initialised or kept.  Not shared by two calls in flight.
  * moe_route_bwd -- the logits' gradient (counts are constants):
  *   logits, experts, gates, lse, counts, normalize   as the forward had or wrote them; counts may be sums
  *              over several batches (all E + 1 of them: the losses' gradient is then that of the whole).
@@ -535,15 +536,18 @@ int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
  *            are the error word.  Nothing in it needs to be initialised or kept.  Not shared by two
  *            calls in flight.
  * linear_cross_entropy_bwd -- gradients of x and w from those of loss and lse:
- *     dz_tv = (dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = targets_t]  (rounded to bf16)
+ *     dz_tv = (dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = targets_t]
  *     dx_t = sum_v dz_tv w_v,  dw_v = sum_t dz_tv x_t
+ *   dz enters the products as bf16, off by at most 2^-8 of its value (2^-16 up to 64 rows), held relative to the
+ *   largest |dloss|; sums are fp32, rounded once.
  *   dloss    (device) float [T].       dlse (device) float [T], or NULL for 0 (a loss on the logits' scale).
  *   x, w, targets, lse                 as the forward had or wrote them.
- *   dx       (device, out) bf16 [T, H].   dw (device, out) bf16 [V, H].  Both are fully overwritten.  A row
+ *   dx       (device, out) bf16 [T, H].   dw (device, out) bf16 [V, H].  Both are fully overwritten and must
+ *            not overlap the inputs.  A row
  *            without a target (negative or >= V) passes nothing on, whatever its x, lse, dloss and dlse hold;
  *            its dx is 0.
  *   workspace linear_cross_entropy_bwd_workspace_size(T, H, V) bytes, as above (packed rows, one piece of
- *            dz of at most 2^27 elements where T is up to 65536, parts of dx).
+ *            dz of at most 2^27 elements where T is up to 65536, parts of dx and dw).
  * Results do not depend on timing.  Requirements: T >= 0, H > 0, V > 0 (otherwise
  * MXFP8_ERR_INVALID_ARG); H % 8 == 0, H <= 2^20, T <= 2^24, V <= 2^28, fewer than 2^30 tiles of 128 x 128
  * logits (otherwise MXFP8_ERR_UNSUPPORTED); x, w, dx, dw 16-byte aligned, the others to their elements.

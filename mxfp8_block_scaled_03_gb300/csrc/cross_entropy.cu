@@ -18,6 +18,15 @@
 // The backward first packs the rows that take part, so that padding costs nothing and nothing it holds can reach
 // dw (0 * NaN).  dz is rounded to bf16 (by at most 2^-8 of its value): it is the operand of two products whose results
 // are rounded to bf16 as well.  It lives for one piece of the vocabulary only, of at most CE_DZ_ELEMS elements.
+// Up to CE_FEW rows the same modes run in a kernel of their own, k_ce_few, which is bound by the bytes of w.
+//
+// Measured (replayed, GB300; rows x H x vocabulary):
+//   forward   8192 x 4096 x 32000   1.11-1.27 ms = 1.69-1.94 PFLOP/s (cool and under sustained power; cuBLAS in bf16 1.72-1.88)
+//             1 x 4096 x 32000      48 us = 5.4 TB/s
+//   backward  8192 x 4096 x 32000   3.55-3.97 ms = 1.62-1.81 PFLOP/s (6 T H V operations)
+//             1531 x 2048 x 50257, 30% padding: 452 us = 1.46 PFLOP/s (1072 rows fill five tiles of 256)
+//             5 x 1024 x 32000      43 us; reads w twice and writes dw, 197 MB: 4.5 TB/s
+// The tensor pipe is active 78% of the time in the logits' and dw's products and 72% in dx's (2048 x 4096 x 16384).
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -696,12 +705,13 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
 // The tensor cores have time to spare here, so dz is held in two bf16 pieces, the second of what the first one leaves (to
 // 2^-16 of it): NT rows of first pieces and NT of second ones, in dx's product as 2 NT columns, in dw's as 2 NT rows of K
 // beside two copies of x.
-constexpr int CE_FEW = 64;
+constexpr int CE_FEW = 64;                         // rows; in the forward CE_FEW_FWD: 64 rows' maxima and sums leave room for
+constexpr int CE_FEW_FWD = 32;                     // one CTA per SM (64 x 4096 x 32000: 57 us, as 128 rows of k_ce_gemm 53)
 constexpr int CE_FEW_BUFS = 4;                     // accumulators of NT columns (dx: 2 NT)
-constexpr int CE_FEW_CHUNK = 2;                    // as CE_CHUNK: the epilogue has nothing else to do
+constexpr int CE_FEW_CHUNK = 4;                    // as CE_CHUNK: the epilogue has time (2 and 8 steps measure the same)
 template <int MODE, int NT>
 struct FewShape {
-  static constexpr int EPI_WARPS = NT == 64 ? 8 : 4;        // 64 rows' maxima and sums need two threads per entry
+  static constexpr int EPI_WARPS = NT == 64 ? 8 : 4;        // 64 rows are two threads' work per entry
   static constexpr int COLS = NT / (EPI_WARPS / 4);
   static constexpr int PER_SM = NT == 64 ? 1 : 2;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
@@ -735,6 +745,28 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  // units: 128 vocabulary entries each, or (share of the piece, 128 columns of dx)
+  const int tiles = MODE == CE_DX ? (p.H + 127) / 128 : (p.vcols + 127) / 128;
+  const int k_steps = MODE == CE_DX ? (p.vcols + CE_BK - 1) / CE_BK : (p.H + CE_BK - 1) / CE_BK;
+  const int split_steps = MODE == CE_DX ? (p.piece_steps + p.few_splits - 1) / p.few_splits : k_steps;
+  const int total = MODE == CE_DX ? tiles * ((k_steps + split_steps - 1) / split_steps) : tiles;
+  auto k_begin = [&](int u) { return MODE == CE_DX ? u / tiles * split_steps : 0; };
+  auto k_end = [&](int u) { return MODE == CE_DX ? min(k_steps, (u / tiles + 1) * split_steps) : k_steps; };
+
+  // The copies of the first stages need nothing of the kernel before (row packing, dz) but for the rows' half: the weights
+  // are on their way while that one ends and while this one sets itself up.
+  const int k_first = k_begin(blockIdx.x);
+  const int early = min(S::STAGES, k_end(blockIdx.x) - k_first);
+  auto load_w = [&](int stage, int m0, int ks) {
+    uint8_t* sA = smem + stage * S::STAGE_BYTES;
+    mbar_arrive_expect_tx(&full[stage], S::STAGE_BYTES);
+    if (A_MN) {
+      tma_load_2d(sA, &tmA, &full[stage], m0, p.v0 + ks * CE_BK);
+      tma_load_2d(sA + CE_OP_BYTES / 2, &tmA, &full[stage], m0 + 64, p.v0 + ks * CE_BK);
+    } else {
+      tma_load_2d(sA, &tmA, &full[stage], ks * CE_BK, p.v0 + m0);
+    }
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -752,6 +784,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
     }
     fence_barrier_init();
     fence_proxy_async_smem();
+    for (int s = 0; s < early; ++s) load_w(s, (MODE == CE_DX ? blockIdx.x % tiles : blockIdx.x) * 128, k_first + s);
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, CE_FEW_BUFS * S::NB);
@@ -763,32 +796,9 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
   const uint32_t tmem = *tmem_holder;
   // (the copying thread waits later, see there)
   if (threadIdx.x != 0) ce_start<MODE>();
-  // units: 128 vocabulary entries each, or (share of the piece, 128 columns of dx)
-  const int tiles = MODE == CE_DX ? (p.H + 127) / 128 : (p.vcols + 127) / 128;
-  const int k_steps = MODE == CE_DX ? (p.vcols + CE_BK - 1) / CE_BK : (p.H + CE_BK - 1) / CE_BK;
-  const int split_steps = MODE == CE_DX ? (p.piece_steps + p.few_splits - 1) / p.few_splits : k_steps;
-  const int total = MODE == CE_DX ? tiles * ((k_steps + split_steps - 1) / split_steps) : tiles;
-  auto k_begin = [&](int u) { return MODE == CE_DX ? u / tiles * split_steps : 0; };
-  auto k_end = [&](int u) { return MODE == CE_DX ? min(k_steps, (u / tiles + 1) * split_steps) : k_steps; };
-
   if (warp == 0) {
     // ---------------- tile copies (one lane) ----------------
     if (lane == 0) {
-      // The weights' copies of the first stages need nothing of the kernel before (row packing, dz): they are on their
-      // way while it ends.
-      const int k_first = k_begin(blockIdx.x);
-      const int early = MODE == CE_LSE ? 0 : min(S::STAGES, k_end(blockIdx.x) - k_first);
-      auto load_w = [&](int stage, int m0, int ks) {
-        uint8_t* sA = smem + stage * S::STAGE_BYTES;
-        mbar_arrive_expect_tx(&full[stage], S::STAGE_BYTES);
-        if (A_MN) {
-          tma_load_2d(sA, &tmA, &full[stage], m0, p.v0 + ks * CE_BK);
-          tma_load_2d(sA + CE_OP_BYTES / 2, &tmA, &full[stage], m0 + 64, p.v0 + ks * CE_BK);
-        } else {
-          tma_load_2d(sA, &tmA, &full[stage], ks * CE_BK, p.v0 + m0);
-        }
-      };
-      for (int s = 0; s < early; ++s) load_w(s, (MODE == CE_DX ? blockIdx.x % tiles : blockIdx.x) * 128, k_first + s);
       ce_start<MODE>();
       uint32_t issued = 0, issued_parity = 0;
       int stage = 0, ahead = early;
@@ -1341,8 +1351,10 @@ bool ce_prepare_few() {
   auto set = [](auto kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
-  return set(k_ce_few<MODE, 16>, FewShape<MODE, 16>::SMEM_BYTES) &&
-         set(k_ce_few<MODE, 32>, FewShape<MODE, 32>::SMEM_BYTES) && set(k_ce_few<MODE, 64>, FewShape<MODE, 64>::SMEM_BYTES);
+  bool ok = set(k_ce_few<MODE, 16>, FewShape<MODE, 16>::SMEM_BYTES) &&
+            set(k_ce_few<MODE, 32>, FewShape<MODE, 32>::SMEM_BYTES);
+  if constexpr (MODE != CE_LSE) ok = ok && set(k_ce_few<MODE, 64>, FewShape<MODE, 64>::SMEM_BYTES);
+  return ok;
 }
 bool ce_device(CeDevice* out) {
   static CeDevice info[64];
@@ -1404,7 +1416,8 @@ cudaError_t ce_launch_few(int64_t T, int64_t units, const CeDevice& dev, const C
   const int nt = few_rows(T);
   if (nt == 16) return go(std::integral_constant<int, 16>{}, k_ce_few<MODE, 16>);
   if (nt == 32) return go(std::integral_constant<int, 32>{}, k_ce_few<MODE, 32>);
-  return go(std::integral_constant<int, 64>{}, k_ce_few<MODE, 64>);
+  if constexpr (MODE == CE_LSE) return cudaErrorInvalidValue;   // (not called: CE_FEW_FWD)
+  else return go(std::integral_constant<int, 64>{}, k_ce_few<MODE, 64>);
 }
 
 constexpr int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1522,7 +1535,7 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   if (T == 0) return cudaMemsetAsync(workspace, 0, sizeof(CeMeta), st) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
   CeDevice dev;
   if (!ce_device(&dev)) return MXFP8_ERR_CUDA;
-  const bool few = T <= CE_FEW;
+  const bool few = T <= CE_FEW_FWD;
   const bool pair = !few && use_pair(dev, T, V);
   const int64_t tile = pair ? 256 : 128;
   CeParams p{};

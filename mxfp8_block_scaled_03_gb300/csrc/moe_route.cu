@@ -14,12 +14,17 @@
 //     otherwise:  p_te (dg_e [e chosen] - sum_i gate_i dg_i)
 // All of it in 32 bits.
 //
-// What bounds it: latency.  The logits of 32768 tokens and 64 experts are 4 to 8 MB, about a microsecond of
-// the memory's time.  A group of L lanes (a power of two, at least E up to 32) holds a token, E / L logits
-// per lane: the selection is k rounds of an argmax over the group, on integer keys in the order of the floats.
-// The column sums stay in registers (a lane sees the same experts of every token); each CTA writes its
-// own and a second kernel adds them in a fixed order, so that results do not depend on timing.  A call of few
-// tokens is one CTA, which finishes by itself.
+// What bounds it: latency.  The logits of 32768 tokens and 64 experts are 4 to 8 MB, about a microsecond of the memory's
+// time.  A token has L lanes with eight logits each (four up to eight experts), up to 16 tokens share a warp, and many
+// experts take two or four warps.  Every lane sorts its logits once, on integer keys that hold the float's order and the
+// expert; each of the k rounds is then a maximum over the lanes' first keys.  The column sums stay in registers (a lane
+// sees the same experts of every token) and are joined in a fixed order, so that results do not depend on timing: in the
+// CTA where one is enough, over a cluster of 16 up to 64 passes, and by a second kernel, a cluster of eight, beyond.
+//
+// Measured (replayed; 32768 tokens, 64 experts, 8 choices, bf16): forward 13 us, 10 and 6 for the two kernels alone;
+// backward 7.6 us.  16384 tokens, 8 experts, 2 choices, fp32: 7.3 and 3.4 us.  4 tokens, 128 experts: 4.0 us.  As calls
+// from Python, on this machine's cores, 22 to 26 and 14 to 15 us: the allocation of the six outputs and the launches.
+// With one warp per token, two logits per lane and selection by 32-lane reductions: 28 us forward; 10.2 us backward.
 #include <cuda_runtime.h>
 
 #include <algorithm>

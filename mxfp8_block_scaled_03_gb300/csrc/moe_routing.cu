@@ -4,8 +4,7 @@
 // Page "Efficient MoE training for biological foundation models", Key technical approaches,
 // item 1: GroupedLinear works on tokens gathered per expert with per-expert counts
 // (split_sizes); section "Dense vs. MoE scaling": each token activates a small subset of the
-// experts.  The router itself (a small GEMM + top-k) is outside this library: its choices come
-// in as expert ids [T, k].
+// experts.  The router's choices (moe_route.cu) come in as expert ids [T, k].
 //
 // Dispatch is a stable counting sort on the device, so split_sizes never visit the host:
 //   k_permute_count    per chunk of 1024 (token, slot) pairs: per-expert counts (shared atomics)
