@@ -547,7 +547,7 @@ int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
  *            without a target (negative or >= V) passes nothing on, whatever its x, lse, dloss and dlse hold;
  *            its dx is 0.
  *   workspace linear_cross_entropy_bwd_workspace_size(T, H, V) bytes, as above (packed rows, one piece of
- *            dz of at most 2^27 elements where T is up to 65536, parts of dx and dw).
+ *            dz of at most 2^28 elements where T is up to 131072, parts of dx and dw).
  * Results do not depend on timing.  Requirements: T >= 0, H > 0, V > 0 (otherwise
  * MXFP8_ERR_INVALID_ARG); H % 8 == 0, H <= 2^20, T <= 2^24, V <= 2^28, fewer than 2^30 tiles of 128 x 128
  * logits (otherwise MXFP8_ERR_UNSUPPORTED); x, w, dx, dw 16-byte aligned, the others to their elements.

@@ -65,7 +65,8 @@ static_assert(ce_smem_bytes(CE_STAGES) <= 232448 && ce_smem_bytes(CE_SHORT) <= 1
 constexpr int CE_CHUNK = 16;                       // CE_LSE: K steps that the tensor core sums before fp32 adds take over
 constexpr uint32_t CE_REGS_LOW = 56, CE_REGS_HIGH = 224;   // CE_LSE: warps 0-3, epilogue warps
 static_assert(128 * CE_REGS_LOW + 256 * CE_REGS_HIGH == CE_THREADS * 168, "register split must equal the launch pool");
-constexpr int64_t CE_DZ_ELEMS = int64_t(1) << 27;  // most elements of dz at a time (256 MB)
+constexpr int64_t CE_DZ_ELEMS = int64_t(1) << 28;  // most elements of dz at a time (512 MB; with half, 8192 x 4096 x 32000
+                                                   // takes two pieces, adds dx up in fp32 and 2.5% longer)
 constexpr int64_t CE_MIN_PIECE = 2048;             // vocabulary entries of a piece, whatever the rows
 constexpr uint64_t CE_WAIT_NS = 2000000000ull;     // 2 s per individual wait
 constexpr float LOG2E = 1.4426950408889634f;

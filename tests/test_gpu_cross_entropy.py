@@ -126,9 +126,9 @@ def test_forward_and_backward(mx, T, H, V):
 
 
 def test_several_pieces_of_the_vocabulary(mx):
-    """8200 rows: the vocabulary of 20001 takes two pieces; dx is the sum over them."""
+    """16400 rows: the vocabulary of 20001 takes two pieces; dx is the sum over them."""
     import torch
-    T, H, V = 8200, 72, 20001
+    T, H, V = 16400, 72, 20001
     x, w, y = make(T, H, V, seed=2, ignored=0.0)
     loss, lse = mx.linear_cross_entropy_fwd(x, w, y)
     check_forward(loss, lse, x, w, y)
