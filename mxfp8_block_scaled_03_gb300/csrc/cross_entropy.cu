@@ -169,31 +169,46 @@ __host__ __device__ constexpr uint32_t ce_idesc(uint32_t M, uint32_t N, bool a_m
   return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) |
          ((M >> 4) << 24);
 }
-// Shared memory descriptor of an M- or N-major operand in 128-byte swizzle: boxes of 64 elements x 64 rows of K
-// (8 KB apart: leading byte offset), groups of 8 rows of K 1024 bytes apart (stride byte offset).
-__device__ __forceinline__ uint64_t ce_sdesc_mn(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(8192 >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// Shared memory descriptors in 128-byte swizzle, lower word (address, leading byte offset) and upper word (stride byte
+// offset 1024, version 1, swizzle): K-major, rows of 128 bytes; or M- / N-major, boxes of 64 elements x 64 rows of K, 8 KB
+// apart (leading byte offset).  A step of 16 along K is 32 bytes of every row, or 16 rows of 128 bytes.
+template <bool MN>
+__device__ __forceinline__ uint32_t ce_desc_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((MN ? 8192u >> 4 : 1u) << 16);
 }
-template <int CG>
-__device__ __forceinline__ void ce_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+constexpr uint32_t CE_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <bool MN>
+constexpr uint32_t CE_DESC_K16 = (MN ? 2048u : 32u) >> 4;
+template <int CG, bool ALWAYS>
+__device__ __forceinline__ void ce_mma(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   if constexpr (CG == 2)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
-        "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc),
+        "r"(ALWAYS ? 1u : accumulate), "r"(CE_DESC_HI)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
-        "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc),
+        "r"(ALWAYS ? 1u : accumulate), "r"(CE_DESC_HI)
         : "memory");
+}
+// The products of one stage (K = 64); the first one overwrites the accumulator where `first`.
+template <int CG, bool A_MN, bool B_MN>
+__device__ __forceinline__ void ce_mma_stage(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool first) {
+  ce_mma<CG, false>(d_tmem, a_lo, b_lo, idesc, first ? 0u : 1u);
+#pragma unroll
+  for (int k = 1; k < CE_BK / 16; ++k)
+    ce_mma<CG, true>(d_tmem, a_lo + k * CE_DESC_K16<A_MN>, b_lo + k * CE_DESC_K16<B_MN>, idesc, 1u);
+}
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool ce_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 template <uint32_t N>
@@ -300,6 +315,13 @@ __device__ __forceinline__ bool ce_wait(uint64_t* bar, uint32_t parity, bool clu
   *abort = 1;
   if (CG == 2) st_remote_u32(peer_abort, 1u);
   return false;
+}
+
+// The same by a whole warp, which agrees on the outcome.
+template <int CG>
+__device__ __forceinline__ bool ce_wait_warp(uint64_t* bar, uint32_t parity, bool cluster_scope, volatile int* abort,
+                                             uint32_t peer_abort, const CeParams& p, uint32_t err_bit) {
+  return __all_sync(0xFFFFFFFFu, ce_wait<CG>(bar, parity, cluster_scope, abort, peer_abort, p, err_bit)) != 0;
 }
 
 // CG = 1: a CTA computes tiles of 128 x 128.  CG = 2: a CTA pair computes tiles of 256 x 256, each CTA with 128 rows
@@ -430,55 +452,48 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
       }
       __syncwarp();
     } else if (warp == CE_WARP_MMA && leader) {
-      // ---------------- MMA issuer (one lane of the leader) ----------------
-      if (lane == 0) {
-        constexpr uint32_t idesc = ce_idesc(TILE, TILE, A_MN, B_MN);
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        bool issued = false, ok = true;
-        for (int u = first; ok && u < units.total; u += stride) {
-          const CeTile t = ce_tile<MODE>(u, units, p);
-          if (t.steps == 0) continue;                 // no rows: the epilogue writes zeros without the accumulator
-          for (int s = 0; s < t.steps; ++s) {
-            if (s % CHUNK == 0) {
-              if (!ce_wait<CG>(&acc_empty[buf], acc_phase ^ 1u, true, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-            }
-            if (!ce_wait<CG>(&full[stage], phase, false, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t a0 = smem_u32(smem + stage * CE_STAGE_BYTES), b0 = a0 + CE_OP_BYTES;
-#pragma unroll
-            for (int k = 0; k < CE_BK / 16; ++k) {
-              const uint64_t da = A_MN ? ce_sdesc_mn(a0 + 2048 * k) : sdesc_kmajor_sw128(a0 + 32 * k);
-              const uint64_t db = B_MN ? ce_sdesc_mn(b0 + 2048 * k) : sdesc_kmajor_sw128(b0 + 32 * k);
-              ce_mma<CG>(tmem + buf * TILE, da, db, idesc, (s % CHUNK | k) != 0 ? 1u : 0u);
-            }
+      // ---------------- MMA issuer (leader) ----------------
+      // The warp runs the loop together, so that addresses stay in uniform registers, and one lane issues.
+      constexpr uint32_t idesc = ce_idesc(TILE, TILE, A_MN, B_MN);
+      const uint32_t a_lo = ce_desc_lo<A_MN>(smem_u32(smem)), b_lo = ce_desc_lo<B_MN>(smem_u32(smem) + CE_OP_BYTES);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool issued = false, ok = true;
+      for (int u = first; ok && u < units.total; u += stride) {
+        const CeTile t = ce_tile<MODE>(u, units, p);
+        if (t.steps == 0) continue;                 // no rows: the epilogue writes zeros without the accumulator
+        for (int s = 0; s < t.steps; ++s) {
+          const bool opens = s % CHUNK == 0, closes = (s + 1) % CHUNK == 0 || s + 1 == t.steps;
+          if (opens) ok = ce_wait_warp<CG>(&acc_empty[buf], acc_phase ^ 1u, true, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA);
+          ok = ok && ce_wait_warp<CG>(&full[stage], phase, false, abort_flag, peer_abort, p, ERR_TIMEOUT_MMA);
+          if (!ok) break;
+          tc_fence_after();
+          if (ce_elect()) {
+            const uint32_t at = stage * (CE_STAGE_BYTES >> 4);
+            ce_mma_stage<CG, A_MN, B_MN>(tmem + buf * TILE, a_lo + at, b_lo + at, idesc, opens);
             if constexpr (CG == 2) tc_commit_pair_both(&empty[stage]);
             else tc_commit(&empty[stage]);
-            issued = true;
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
-            if ((s + 1) % CHUNK == 0 || s + 1 == t.steps) {
+            if (closes) {
               if constexpr (CG == 2) tc_commit_pair_both(&acc_full[buf]);
               else tc_commit(&acc_full[buf]);
-              buf ^= 1;
-              if (buf == 0) acc_phase ^= 1u;
             }
           }
+          __syncwarp();
+          issued = true;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (closes) {
+            buf ^= 1;
+            if (buf == 0) acc_phase ^= 1u;
+          }
         }
-        if (issued) {
-          if constexpr (CG == 2) tc_commit_pair_local(drained);
-          else tc_commit(drained);
-          if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
-        }
+      }
+      if (issued && ce_elect()) {
+        if constexpr (CG == 2) tc_commit_pair_local(drained);
+        else tc_commit(drained);
+        if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
       }
       __syncwarp();
     }
@@ -835,51 +850,41 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMA issuer (one lane) ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc = ce_idesc(128, S::NB, A_MN, false);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool issued = false, ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const int steps = k_end(u) - k_begin(u);
-        for (int s = 0; s < steps; ++s) {
-          if (s % CHUNK == 0) {
-            if (!ce_wait<1>(&acc_empty[buf], acc_phase ^ 1u, false, abort_flag, 0u, p, ERR_TIMEOUT_MMA)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-          }
-          if (!ce_wait<1>(&full[stage], phase, false, abort_flag, 0u, p, ERR_TIMEOUT_MMA)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + stage * S::STAGE_BYTES), b0 = a0 + CE_OP_BYTES;
-#pragma unroll
-          for (int k = 0; k < CE_BK / 16; ++k)
-            ce_mma<1>(tmem + buf * S::NB, A_MN ? ce_sdesc_mn(a0 + 2048 * k) : sdesc_kmajor_sw128(a0 + 32 * k),
-                      sdesc_kmajor_sw128(b0 + 32 * k), idesc, (s % CHUNK | k) != 0 ? 1u : 0u);
+    // ---------------- MMA issuer (as in k_ce_gemm) ----------------
+    constexpr uint32_t idesc = ce_idesc(128, S::NB, A_MN, false);
+    const uint32_t a_lo = ce_desc_lo<A_MN>(smem_u32(smem)), b_lo = ce_desc_lo<false>(smem_u32(smem) + CE_OP_BYTES);
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool issued = false, ok = true;
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+      const int steps = k_end(u) - k_begin(u);
+      for (int s = 0; s < steps; ++s) {
+        const bool opens = s % CHUNK == 0, closes = (s + 1) % CHUNK == 0 || s + 1 == steps;
+        if (opens) ok = ce_wait_warp<1>(&acc_empty[buf], acc_phase ^ 1u, false, abort_flag, 0u, p, ERR_TIMEOUT_MMA);
+        ok = ok && ce_wait_warp<1>(&full[stage], phase, false, abort_flag, 0u, p, ERR_TIMEOUT_MMA);
+        if (!ok) break;
+        tc_fence_after();
+        if (ce_elect()) {
+          const uint32_t at = stage * (S::STAGE_BYTES >> 4);
+          ce_mma_stage<1, A_MN, false>(tmem + buf * S::NB, a_lo + at, b_lo + at, idesc, opens);
           tc_commit(&empty[stage]);
-          issued = true;
-          if (++stage == S::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if ((s + 1) % CHUNK == 0 || s + 1 == steps) {
-            tc_commit(&acc_full[buf]);
-            if (++buf == CE_FEW_BUFS) {
-              buf = 0;
-              acc_phase ^= 1u;
-            }
-          }
+          if (closes) tc_commit(&acc_full[buf]);
+        }
+        __syncwarp();
+        issued = true;
+        if (++stage == S::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (closes && ++buf == CE_FEW_BUFS) {
+          buf = 0;
+          acc_phase ^= 1u;
         }
       }
-      if (issued) {
-        tc_commit(drained);
-        if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
-      }
+    }
+    if (issued && ce_elect()) {
+      tc_commit(drained);
+      if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
     }
     __syncwarp();
   } else {
