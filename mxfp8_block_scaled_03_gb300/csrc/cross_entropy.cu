@@ -304,10 +304,23 @@ __device__ __forceinline__ CeTile ce_tile(int u, const CeUnits& c, const CeParam
   return t;
 }
 
+// A phase that is complete already, without the cost of a wait.
+__device__ __forceinline__ bool ce_ready(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait of one thread; a wait that runs out is reported and raises the abort flag of this CTA (and of its peer).
 template <int CG>
 __device__ __forceinline__ bool ce_wait(uint64_t* bar, uint32_t parity, bool cluster_scope, volatile int* abort,
                                         uint32_t peer_abort, const CeParams& p, uint32_t err_bit) {
+  if (!(CG == 2 && cluster_scope) && ce_ready(bar, parity)) return true;
   if (CG == 2 && cluster_scope ? mbar_wait_cluster_bounded(bar, parity, abort, p.timeout_ns)
                                : mbar_wait_bounded(bar, parity, abort, p.timeout_ns))
     return true;
@@ -393,22 +406,21 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
   if (warp < CE_EPI_WARP0) {
     if constexpr (MODE == CE_LSE) ce_regs_dec<CE_REGS_LOW>();
     if (warp == CE_WARP_PRODUCER) {
-      // ---------------- tile copies (every CTA its own; one lane) ----------------
-      if (lane == 0) {
-        const uint32_t leader_full = CG == 2 ? map_to_cta(full, 0) : 0u;
-        uint32_t issued_parity = 0;
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int u = first; ok && u < units.total; u += stride) {
-          const CeTile t = ce_tile<MODE>(u, units, p);
-          const int a0 = t.m * TILE + CE_HALF * static_cast<int>(rank);
-          const int b0 = t.n * TILE + CE_HALF * static_cast<int>(rank);
-          for (int s = 0; s < t.steps; ++s) {
-            if (!ce_wait<CG>(&empty[stage], phase ^ 1u, false, abort_flag, peer_abort, p, ERR_TIMEOUT_PRODUCER)) {
-              ok = false;
-              break;
-            }
+      // ---------------- tile copies (every CTA its own) ----------------
+      // The warp runs the loop together, so that addresses stay in uniform registers, and one lane issues.
+      const uint32_t leader_full = CG == 2 ? map_to_cta(full, 0) : 0u;
+      uint32_t issued_parity = 0;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = first; ok && u < units.total; u += stride) {
+        const CeTile t = ce_tile<MODE>(u, units, p);
+        const int a0 = t.m * TILE + CE_HALF * static_cast<int>(rank);
+        const int b0 = t.n * TILE + CE_HALF * static_cast<int>(rank);
+        for (int s = 0; s < t.steps; ++s) {
+          ok = ce_wait_warp<CG>(&empty[stage], phase ^ 1u, false, abort_flag, peer_abort, p, ERR_TIMEOUT_PRODUCER);
+          if (!ok) break;
+          if (ce_elect()) {
             uint8_t* sA = smem + stage * CE_STAGE_BYTES;
             uint8_t* sB = sA + CE_OP_BYTES;
             const int k = (t.k0 + s) * CE_BK;
@@ -431,25 +443,26 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
               load(sB, &tmB, k, p.v0 + b0);
             }
             if (leader) mbar_arrive_expect_tx(&full[stage], CG * CE_STAGE_BYTES);
-            prod_issued |= 1u << stage;
-            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
+          }
+          __syncwarp();
+          prod_issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
-        // Copies land before the CTA exits: the leader waits for its stages (their barriers count both CTAs' copies);
-        // the second CTA's wait for the leader is the pair's closing barriers below.
-        // (After an abort the second CTA may never have copied its half: then one wait is enough for this CTA's.)
-        if (leader)
-          for (int s = 0; s < STAGES; ++s)
-            if (((prod_issued >> s) & 1u) &&
-                !mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS)) {
-              ce_report(p, ERR_TIMEOUT_DRAIN);
-              break;
-            }
       }
+      // Copies land before the CTA exits: the leader waits for its stages (their barriers count both CTAs' copies);
+      // the second CTA's wait for the leader is the pair's closing barriers below.
+      // (After an abort the second CTA may never have copied its half: then one wait is enough for this CTA's.)
+      if (leader && lane == 0)
+        for (int s = 0; s < STAGES; ++s)
+          if (((prod_issued >> s) & 1u) &&
+              !mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS)) {
+            ce_report(p, ERR_TIMEOUT_DRAIN);
+            break;
+          }
       __syncwarp();
     } else if (warp == CE_WARP_MMA && leader) {
       // ---------------- MMA issuer (leader) ----------------
@@ -813,32 +826,34 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
   // (the copying thread waits later, see there)
   if (threadIdx.x != 0) ce_start<MODE>();
   if (warp == 0) {
-    // ---------------- tile copies (one lane) ----------------
-    if (lane == 0) {
-      ce_start<MODE>();
-      uint32_t issued = 0, issued_parity = 0;
-      int stage = 0, ahead = early;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const int m0 = (MODE == CE_DX ? u % tiles : u) * 128;
-        const int k1 = k_end(u);
-        for (int ks = k_begin(u); ks < k1; ++ks) {
-          if (!ce_wait<1>(&empty[stage], phase ^ 1u, false, abort_flag, 0u, p, ERR_TIMEOUT_PRODUCER)) {
-            ok = false;
-            break;
-          }
-          if (ahead > 0) --ahead;
-          else load_w(stage, m0, ks);
+    // ---------------- tile copies (as in k_ce_gemm) ----------------
+    if (lane == 0) ce_start<MODE>();
+    __syncwarp();
+    uint32_t issued = 0, issued_parity = 0;
+    int stage = 0, ahead = early;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+      const int m0 = (MODE == CE_DX ? u % tiles : u) * 128;
+      const int k1 = k_end(u);
+      for (int ks = k_begin(u); ks < k1; ++ks) {
+        ok = ce_wait_warp<1>(&empty[stage], phase ^ 1u, false, abort_flag, 0u, p, ERR_TIMEOUT_PRODUCER);
+        if (!ok) break;
+        if (ce_elect()) {
+          if (ahead <= 0) load_w(stage, m0, ks);
           tma_load_2d(smem + stage * S::STAGE_BYTES + CE_OP_BYTES, &tmB, &full[stage], ks * CE_BK, 0);
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == S::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        --ahead;
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == S::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
+    }
+    if (lane == 0) {
       for (; ahead > 0; --ahead) {                  // (after an abort) the early stages get their other half
         tma_load_2d(smem + (early - ahead) * S::STAGE_BYTES + CE_OP_BYTES, &tmB, &full[early - ahead], 0, 0);
         issued |= 1u << (early - ahead);
