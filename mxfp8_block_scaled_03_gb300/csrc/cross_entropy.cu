@@ -101,6 +101,7 @@ struct CeParams {
   float* zy;                   // CE_LSE: the target's logit
   int64_t pitch;
   float* acc;                  // CE_DX: [splits][pitch][H] fp32, or NULL: dx is written directly
+  int one_piece;               // (and also where one share of a single piece is all there is)
   float* acc_w;                // CE_DW: [dw_splits][vcols][H] fp32, or NULL: dw is written directly
   int dw_splits;
   int dw_rows;                 // few rows, CE_DW: rows of dz (and of the copies of x)
@@ -519,6 +520,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
     uint8_t* wbuf = smem + STAGES * CE_STAGE_BYTES + (warp - CE_EPI_WARP0) * 2 * CE_BUF_BYTES;
     const int n_rows = MODE == CE_LSE ? p.rows : MODE == CE_DW ? 0 : p.meta->n;
     const float gain = MODE == CE_LSE ? 1.0f : p.meta->gain;
+    const bool dx_direct = MODE == CE_DX && (p.acc == nullptr || (p.one_piece && p.meta->splits == 1));
     int buf = 0;
     uint32_t acc_phase = 0;
     for (int u = first; u < units.total; u += stride) {
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
             bulk_commit_group();
           }
         } else if (row < n_rows) {                  // CE_DX
-          if (p.acc == nullptr) {
+          if (dx_direct) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * gain);
             uint16_t* dst = p.dx + static_cast<int64_t>(src) * p.H + col;
@@ -1233,6 +1235,7 @@ __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int s
   __shared__ float4 s_sum[CE_DX_THREADS];
   ce_wait_before();
   const bool few = p.rows > 0;                // rows as they are, those that take no part among them
+  if (!few && p.one_piece && p.meta->splits == 1) return;   // dx has been written
   const int most = few ? p.few_splits : p.meta->splits;
   const float gain = p.meta->gain;
   const int split_steps = (p.piece_steps + most - 1) / most;
@@ -1632,6 +1635,7 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.dlse = dlse;
   p.pitch = ws.t_pad;
   p.acc = ws.pieces > 1 || ws.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
+  p.one_piece = ws.pieces == 1;
   p.acc_w = ws.dw_splits > 1 ? reinterpret_cast<float*>(base + ws.acc_w) : nullptr;
   p.dw_splits = ws.dw_splits;
   p.dx = static_cast<uint16_t*>(dx);
