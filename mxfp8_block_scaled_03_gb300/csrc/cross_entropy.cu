@@ -21,12 +21,14 @@
 // Up to CE_FEW rows the same modes run in a kernel of their own, k_ce_few, which is bound by the bytes of w.
 //
 // Measured (replayed, GB300; rows x H x vocabulary):
-//   forward   8192 x 4096 x 32000   1.11-1.27 ms = 1.69-1.94 PFLOP/s (cool and under sustained power; cuBLAS in bf16 1.72-1.88)
-//             1 x 4096 x 32000      48 us = 5.4 TB/s
-//   backward  8192 x 4096 x 32000   3.55-3.97 ms = 1.62-1.81 PFLOP/s (6 T H V operations)
-//             1531 x 2048 x 50257, 30% padding: 452 us = 1.46 PFLOP/s (1072 rows fill five tiles of 256)
-//             5 x 1024 x 32000      43 us; reads w twice and writes dw, 197 MB: 4.5 TB/s
-// The tensor pipe is active 78% of the time in the logits' and dw's products and 72% in dx's (2048 x 4096 x 16384).
+//   forward   8192 x 4096 x 32000   1.08-1.19 ms = 1.80-2.00 PFLOP/s (under sustained power and cool; cuBLAS in bf16 1.72-1.88)
+//             1 x 4096 x 32000      48 us = 5.5 TB/s
+//   backward  8192 x 4096 x 32000   3.31-3.79 ms = 1.70-1.95 PFLOP/s (6 T H V operations)
+//             1531 x 2048 x 50257, 30% padding: 427 us = 1.55 PFLOP/s (1072 rows fill five tiles of 256)
+//             5 x 1024 x 32000      42 us; reads w twice and writes dw, 197 MB: 4.7 TB/s
+// The tensor pipe is active 86-88% of the time in the logits' and dw's products and 76% in dx's (2048 x 4096 x 16384, 512 and
+// 128 tiles for 76 pairs).  Loops of one lane instead of whole warps around the copies and the products left it at 78%: a
+// step's 512 cycles of products took the issuing lane nearly as long.
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -60,7 +62,7 @@ constexpr int CE_EPI_BYTES = CE_EPI_WARPS * 2 * CE_BUF_BYTES;
 constexpr int ce_smem_bytes(int stages) {
   return stages * CE_STAGE_BYTES + CE_EPI_BYTES + (2 * stages + 5) * 8 + 8 + 1024;
 }
-constexpr int CE_SHORT = 2;                        // stages where K is one step (dw of few rows): two CTAs per SM
+constexpr int CE_SHORT = 2;                        // stages where K is few steps (dw of few rows): two CTAs per SM
 static_assert(ce_smem_bytes(CE_STAGES) <= 232448 && ce_smem_bytes(CE_SHORT) <= 115712, "shared memory budget");
 constexpr int CE_CHUNK = 16;                       // CE_LSE: K steps that the tensor core sums before fp32 adds take over
 constexpr uint32_t CE_REGS_LOW = 56, CE_REGS_HIGH = 224;   // CE_LSE: warps 0-3, epilogue warps
