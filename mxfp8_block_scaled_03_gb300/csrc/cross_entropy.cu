@@ -16,13 +16,14 @@
 //   CE_DW   dz^T x     -> dw of the piece            (both operands contract over their rows: M- and N-major tiles)
 //   CE_DX   dz w       -> dx, in fp32 parts where the vocabulary has several pieces or is split over CTAs
 // The backward first packs the rows that take part, so that padding costs nothing and nothing it holds can reach
-// dw (0 * NaN).  dz is rounded to bf16 (by at most 2^-8 of its value): it is the operand of two products whose results
-// are rounded to bf16 as well.  It lives for one piece of the vocabulary only, of at most CE_DZ_ELEMS elements.
+// dw (0 * NaN); where that takes longer than it could save, dz's kernel writes zeros for the other rows instead, to dz and to
+// a copy of x (rows as they are).  dz is rounded to bf16 (by at most 2^-8 of its value): it is the operand of two products
+// whose results are rounded to bf16 as well.  It lives for one piece of the vocabulary only, of at most CE_DZ_ELEMS elements.
 // Up to CE_FEW rows the same modes run in a kernel of their own, k_ce_few, which is bound by the bytes of w.
 //
 // Measured (replayed, GB300; rows x H x vocabulary):
 //   forward   8192 x 4096 x 32000   1.08-1.19 ms = 1.80-2.00 PFLOP/s (under sustained power and cool; cuBLAS in bf16 1.72-1.88)
-//             1 x 4096 x 32000      48 us = 5.5 TB/s
+//             1 x 4096 x 32000      47 us = 5.6 TB/s
 //   backward  8192 x 4096 x 32000   3.31-3.79 ms = 1.70-1.95 PFLOP/s (6 T H V operations)
 //             1531 x 2048 x 50257, 30% padding: 427 us = 1.55 PFLOP/s (1072 rows fill five tiles of 256)
 //             5 x 1024 x 32000      42 us; reads w twice and writes dw, 197 MB: 4.7 TB/s
@@ -60,7 +61,7 @@ constexpr uint32_t CE_BAR_EPI = 1;                 // hardware barrier of the ep
 constexpr int CE_BUF_BYTES = 2048;                 // a warp's staging tile: 32 rows x 32 bf16; two per warp
 constexpr int CE_EPI_BYTES = CE_EPI_WARPS * 2 * CE_BUF_BYTES;
 constexpr int ce_smem_bytes(int stages) {
-  return stages * CE_STAGE_BYTES + CE_EPI_BYTES + (2 * stages + 5) * 8 + 8 + 1024;
+  return stages * CE_STAGE_BYTES + CE_EPI_BYTES + (2 * stages + 5) * 8 + 16 + 1024;
 }
 constexpr int CE_SHORT = 2;                        // stages where K is few steps (dw of few rows): two CTAs per SM
 static_assert(ce_smem_bytes(CE_STAGES) <= 232448 && ce_smem_bytes(CE_SHORT) <= 115712, "shared memory budget");
@@ -88,12 +89,12 @@ static_assert(sizeof(CeMeta) == 256, "header");
 struct CeParams {
   CeMeta* meta;
   const int32_t* row_map;      // backward: row of packed row i
-  int rows;                    // forward, and backward of few rows: T; otherwise 0: meta->n packed rows
+  int rows;                    // forward, and backward with rows as they are: T; otherwise 0: meta->n packed rows
   int V, v0, vcols;            // vocabulary; first entry and entries of this piece
   int H;
   int group_m;                 // row tiles that share a column tile before the next one is taken
-  int few_splits;              // few rows, CE_DX: shares of the piece
-  int piece_steps;             // CE_DX: K steps of a whole piece, dealt out to meta->splits shares
+  int splits;                  // rows as they are, CE_DX: shares of the piece; otherwise meta->splits
+  int piece_steps;             // CE_DX: K steps of a whole piece, dealt out to the shares
   const void* targets;
   int wide_targets;
   const float* lse;
@@ -106,14 +107,15 @@ struct CeParams {
   int one_piece;               // (and also where one share of a single piece is all there is)
   float* acc_w;                // CE_DW: [dw_splits][vcols][H] fp32, or NULL: dw is written directly
   int dw_splits;
-  int dw_rows;                 // few rows, CE_DW: rows of dz (and of the copies of x)
+  int dw_rows;                 // rows as they are, CE_DW: rows of dz (few rows: of both its pieces)
   int acc_add;
   uint16_t* dz;                // few rows, CE_DZ: [NT][dz_pitch]
   int64_t dz_pitch;
   int d_rows, d_cols;          // CE_DZ, CE_DW: extent of the map that is stored to
   uint16_t* dx;
-  const uint4* x;              // few rows, CE_DZ of the first piece: x, and a copy with zeros for rows that take no part
-  uint4* xp;
+  const uint4* x;              // rows as they are, CE_DZ of the first piece: x, and a copy with zeros for rows that take no
+  uint4* xp;                   // part ([t_pad], few rows: twice)
+  int t_pad;
   uint32_t* status;            // a call's first kernel: an error word per CTA; otherwise NULL, meta->error
   const uint32_t* join;        // the kernel after it: those words, to be added to meta->error
   int joins;
@@ -162,9 +164,27 @@ struct CeGain {
   }
 };
 __device__ __forceinline__ int ce_rows(const CeParams& p) { return p.rows > 0 ? p.rows : p.meta->n; }
+__device__ __forceinline__ int ce_shares(const CeParams& p) { return p.rows > 0 ? p.splits : p.meta->splits; }
 __device__ __forceinline__ int64_t ce_target(const CeParams& p, int64_t row) {
   return p.wide_targets ? __ldg(static_cast<const long long*>(p.targets) + row)
                         : static_cast<int64_t>(__ldg(static_cast<const int32_t*>(p.targets) + row));
+}
+__device__ __forceinline__ bool ce_takes_part(const CeParams& p, int64_t row) {
+  const int64_t y = ce_target(p, row);
+  return y >= 0 && y < p.V;
+}
+// Rows as they are: the gain of this warp's rows i, i + n, ...; the first CTA reports targets that are too large.
+__device__ __forceinline__ CeGain ce_find_gain(const CeParams& p, int i, int n) {
+  CeGain g;
+  bool bad = false;
+  for (int t = i; t < p.rows; t += n) {
+    const int64_t y = ce_target(p, t);
+    if (y >= 0 && y < p.V) g.add(p, t);
+    bad |= y >= p.V;
+  }
+  if (bad && blockIdx.x == 0) ce_report(p, ERR_TARGET_RANGE);
+  g.join_warp();
+  return g;
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B, K-major unless the M / N major bits are set.
@@ -262,7 +282,7 @@ __device__ __forceinline__ CeUnits ce_units(const CeParams& p) {
     c.nn = up(p.V, TILE);
     c.steps = up(p.H, CE_BK);
   } else if (MODE == CE_DZ) {
-    c.nm = up(p.meta->n, TILE);
+    c.nm = up(ce_rows(p), TILE);
     c.nn = up(p.vcols, TILE);
     c.steps = up(p.H, CE_BK);
   } else if (MODE == CE_DW) {
@@ -270,13 +290,13 @@ __device__ __forceinline__ CeUnits ce_units(const CeParams& p) {
     c.nn = up(p.H, TILE);
     c.steps = up(p.rows > 0 ? p.dw_rows : p.meta->n, CE_BK);
   } else {
-    c.nm = up(p.meta->n, TILE);
+    c.nm = up(ce_rows(p), TILE);
     c.nn = up(p.H, TILE);
     c.steps = up(p.vcols, CE_BK);
   }
   c.split_steps = c.steps;
   if (MODE == CE_DX) {
-    c.split_steps = up(p.piece_steps, p.meta->splits);
+    c.split_steps = up(p.piece_steps, ce_shares(p));
     splits = up(c.steps, c.split_steps);
   }
   if (MODE == CE_DW && p.dw_splits > 1) {           // every share writes its part, one without rows zeros
@@ -361,6 +381,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
   uint64_t* drained = acc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  uint32_t* gain_bits = tmem_holder + 2;            // [2]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -378,7 +399,8 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
-    if (p.status != nullptr) {                      // (the forward's first kernel: nothing else writes these yet)
+    gain_bits[0] = gain_bits[1] = 0u;
+    if (p.status != nullptr) {                      // (the call's first kernel: nothing else writes these yet)
       p.status[blockIdx.x] = 0u;
       if (blockIdx.x == 0) p.meta->error = 0u;
     }
@@ -512,6 +534,19 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
       }
       __syncwarp();
+    } else if (MODE == CE_DZ && warp >= 2 && p.xp != nullptr) {
+      // ---------------- rows as they are: the copy of x for dw, with zeros for rows that take no part ----------------
+      const uint32_t per_row = static_cast<uint32_t>(p.H) / 8, total = static_cast<uint32_t>(p.t_pad) * per_row;
+#pragma unroll 8
+      for (uint32_t e = blockIdx.x * 64 + (threadIdx.x - 64); e < total; e += gridDim.x * 64) {
+        const uint32_t r = e / per_row;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < static_cast<uint32_t>(p.rows)) {
+          v = __ldg(p.x + e);
+          if (!ce_takes_part(p, r)) v = make_uint4(0u, 0u, 0u, 0u);
+        }
+        p.xp[e] = v;
+      }
     }
   } else {
     if constexpr (MODE == CE_LSE) ce_regs_inc<CE_REGS_HIGH>();
@@ -520,9 +555,28 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
     const int half = (warp - CE_EPI_WARP0) >> 2;
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + NH * half;
     uint8_t* wbuf = smem + STAGES * CE_STAGE_BYTES + (warp - CE_EPI_WARP0) * 2 * CE_BUF_BYTES;
-    const int n_rows = MODE == CE_LSE ? p.rows : MODE == CE_DW ? 0 : p.meta->n;
-    const float gain = MODE == CE_LSE ? 1.0f : p.meta->gain;
-    const bool dx_direct = MODE == CE_DX && (p.acc == nullptr || (p.one_piece && p.meta->splits == 1));
+    const int n_rows = MODE == CE_DW ? 0 : ce_rows(p);
+    const bool as_is = MODE != CE_LSE && p.rows > 0;
+    float gain = 1.0f;
+    if (MODE == CE_DZ && as_is) {
+      const int i = static_cast<int>(threadIdx.x) - 32 * CE_EPI_WARP0;
+      CeGain g = ce_find_gain(p, i, CE_EPI_WARPS * 32);
+      if (lane == 0) {
+        atomicMax(gain_bits, g.loss);
+        atomicMax(gain_bits + 1, g.lse);
+      }
+      __syncwarp();
+      group_and(CE_BAR_EPI, CE_EPI_WARPS * 32, true);
+      g.loss = *static_cast<volatile uint32_t*>(gain_bits);
+      g.lse = *static_cast<volatile uint32_t*>(gain_bits + 1);
+      gain = g.value();
+      if (blockIdx.x == 0 && i == 0) p.meta->gain = gain;
+    } else if (MODE != CE_LSE) {
+      gain = p.meta->gain;
+    }
+    if (MODE == CE_DX && p.join != nullptr && blockIdx.x == 0)
+      ce_join(p, static_cast<int>(threadIdx.x) - 32 * CE_EPI_WARP0, CE_EPI_WARPS * 32);
+    const bool dx_direct = MODE == CE_DX && (p.acc == nullptr || (!as_is && p.one_piece && p.meta->splits == 1));
     int buf = 0;
     uint32_t acc_phase = 0;
     for (int u = first; u < units.total; u += stride) {
@@ -538,8 +592,12 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         const int64_t target = ce_target(p, row);
         y = target < p.V ? static_cast<int>(max(target, int64_t(-1))) : -1;
       }
-      if ((MODE == CE_DZ || MODE == CE_DX) && row < n_rows) src = __ldg(p.row_map + row);
-      if (MODE == CE_DZ && row < n_rows) {
+      bool in = row < n_rows;                       // the row takes part
+      if ((MODE == CE_DZ || MODE == CE_DX) && in) {
+        src = as_is ? row : __ldg(p.row_map + row);
+        if (as_is) in = ce_takes_part(p, row);
+      }
+      if (MODE == CE_DZ && in) {
         y = static_cast<int>(ce_target(p, src)) - p.v0;
         hot = __ldg(p.dloss + src) / gain;
         rate = hot + (p.dlse != nullptr ? __ldg(p.dlse + src) / gain : 0.0f);
@@ -631,7 +689,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
             for (int i = 0; i < 32; ++i) {
               float d = rate * ex2(fmaf(__uint_as_float(v[i]), LOG2E, -lse2));
               if (y == col + i) d -= hot;
-              v[i] = row < n_rows && col + i < p.vcols ? __float_as_uint(d) : 0u;
+              v[i] = in && col + i < p.vcols ? __float_as_uint(d) : 0u;
             }
           }
           if (MODE == CE_DW && p.acc_w != nullptr) {
@@ -670,7 +728,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         } else if (row < n_rows) {                  // CE_DX
           if (dx_direct) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * gain);
+            for (int i = 0; i < 32; ++i) v[i] = in ? __float_as_uint(__uint_as_float(v[i]) * gain) : 0u;
             uint16_t* dst = p.dx + static_cast<int64_t>(src) * p.H + col;
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
@@ -781,7 +839,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
   // units: 128 vocabulary entries each, or (share of the piece, 128 columns of dx)
   const int tiles = MODE == CE_DX ? (p.H + 127) / 128 : (p.vcols + 127) / 128;
   const int k_steps = MODE == CE_DX ? (p.vcols + CE_BK - 1) / CE_BK : (p.H + CE_BK - 1) / CE_BK;
-  const int split_steps = MODE == CE_DX ? (p.piece_steps + p.few_splits - 1) / p.few_splits : k_steps;
+  const int split_steps = MODE == CE_DX ? (p.piece_steps + p.splits - 1) / p.splits : k_steps;
   const int total = MODE == CE_DX ? tiles * ((k_steps + split_steps - 1) / split_steps) : tiles;
   auto k_begin = [&](int u) { return MODE == CE_DX ? u / tiles * split_steps : 0; };
   auto k_end = [&](int u) { return MODE == CE_DX ? min(k_steps, (u / tiles + 1) * split_steps) : k_steps; };
@@ -811,7 +869,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
-    if (p.status != nullptr) {                      // (the forward's first kernel: nothing else writes these yet)
+    if (p.status != nullptr) {                      // (the call's first kernel: nothing else writes these yet)
       p.status[blockIdx.x] = 0u;
       if (blockIdx.x == 0) p.meta->error = 0u;
     }
@@ -918,14 +976,8 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
     if (MODE == CE_DX) gain = p.meta->gain;
     if (MODE != CE_DX) {
       const int i = static_cast<int>(threadIdx.x) - 64;
-      if (MODE == CE_DZ) {                          // every warp for itself
-        CeGain g;
-        for (int t = lane; t < n_rows; t += 32) {
-          const int64_t target = ce_target(p, t);
-          if (target >= 0 && target < p.V) g.add(p, t);
-        }
-        g.join_warp();
-        gain = g.value();
+      if (MODE == CE_DZ) {
+        gain = ce_find_gain(p, lane, 32).value();
         if (blockIdx.x == 0 && i == 0) p.meta->gain = gain;
       }
       if (i < NT) {
@@ -940,7 +992,6 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
               r.y = __ldg(p.lse + i) * LOG2E;
             }
           }
-          if (MODE == CE_DZ && target >= p.V && blockIdx.x == 0) ce_report(p, ERR_TARGET_RANGE);
         }
         s_row[i] = r;
       }
@@ -1032,11 +1083,9 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
           if (h < p.H)
 #pragma unroll
             for (int j = 0; j < S::COLS; ++j)
-              if (c0 + j < n_rows) {
-                const int64_t target = ce_target(p, c0 + j);
+              if (c0 + j < n_rows)
                 p.dx[static_cast<int64_t>(c0 + j) * p.H + h] =
-                    target >= 0 && target < p.V ? __bfloat16_as_ushort(__float2bfloat16_rn(z[j] * gain)) : 0;
-              }
+                    ce_takes_part(p, c0 + j) ? __bfloat16_as_ushort(__float2bfloat16_rn(z[j] * gain)) : 0;
           continue;
         }
         float* dst = p.acc + (static_cast<int64_t>(u / tiles) * p.pitch + c0) * p.H + h;
@@ -1137,12 +1186,15 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
 // (1072 x 2048 values in 15 parts took 48 us to add up; 3 parts leave 10, and the product 10 us longer).
 constexpr int CE_SHARE_STEPS = 8;
 constexpr float CE_PART_STEPS = 4.4e-6f;   // per value of dx: 8 bytes at 6.8 TB/s
-__device__ __forceinline__ int ce_splits(int n, int H, int tile, int steps, int workers, int most) {   // a warp; most <= 32
-  const int s = 1 + (threadIdx.x & 31);
+__host__ __device__ __forceinline__ float ce_share_cost(int s, int n, int H, int tile, int steps, int workers) {
   const int64_t units = static_cast<int64_t>((n + tile - 1) / tile) * ((H + tile - 1) / tile);
   const int64_t waves = (units * s + workers - 1) / workers;
-  const float c = static_cast<float>(waves * ((steps + s - 1) / s + CE_SHARE_STEPS)) +
-                  (s > 1 ? static_cast<float>(s) * CE_PART_STEPS * static_cast<float>(n) * static_cast<float>(H) : 0.0f);
+  return static_cast<float>(waves * ((steps + s - 1) / s + CE_SHARE_STEPS)) +
+         (s > 1 ? static_cast<float>(s) * CE_PART_STEPS * static_cast<float>(n) * static_cast<float>(H) : 0.0f);
+}
+__device__ __forceinline__ int ce_splits(int n, int H, int tile, int steps, int workers, int most) {   // a warp; most <= 32
+  const int s = 1 + (threadIdx.x & 31);
+  const float c = ce_share_cost(s, n, H, tile, steps, workers);
   const uint32_t cost = s <= most && s <= steps ? __float_as_uint(c) : 0x7F800000u;   // in the order of the floats
   const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, cost);
   return max(1, __ffs(__ballot_sync(0xFFFFFFFFu, cost == least)));
@@ -1238,9 +1290,9 @@ constexpr int CE_DX_THREADS = 256;
 __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int steps) {
   __shared__ float4 s_sum[CE_DX_THREADS];
   ce_wait_before();
-  const bool few = p.rows > 0;                // rows as they are, those that take no part among them
-  if (!few && p.one_piece && p.meta->splits == 1) return;   // dx has been written
-  const int most = few ? p.few_splits : p.meta->splits;
+  const bool as_is = p.rows > 0;              // rows that take no part are among them
+  if (!as_is && p.one_piece && p.meta->splits == 1) return;   // dx has been written
+  const int most = ce_shares(p);
   const float gain = p.meta->gain;
   const int split_steps = (p.piece_steps + most - 1) / most;
   const int splits = (steps + split_steps - 1) / split_steps;   // of the first piece; a shorter last one has no more
@@ -1273,11 +1325,8 @@ __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int s
     }
     if (slice == 0 && e < total) {
       uint2 o = make_uint2(pack_bf16x2(v.x * gain, v.y * gain), pack_bf16x2(v.z * gain, v.w * gain));
-      if (few) {
-        const int64_t target = ce_target(p, i);
-        if (target < 0 || target >= p.V) o = make_uint2(0u, 0u);
-      }
-      reinterpret_cast<uint2*>(p.dx)[(few ? i : static_cast<int64_t>(p.row_map[i])) * per_row + c] = o;
+      if (as_is && !ce_takes_part(p, i)) o = make_uint2(0u, 0u);
+      reinterpret_cast<uint2*>(p.dx)[(as_is ? i : static_cast<int64_t>(p.row_map[i])) * per_row + c] = o;
     }
   }
 }
@@ -1424,11 +1473,11 @@ bool ce_device(CeDevice* out) {
 
 template <int MODE>
 cudaError_t ce_launch(bool pair, int64_t units, const CeDevice& dev, const CUtensorMap& a, const CUtensorMap& b,
-                      const CUtensorMap& d, const CeParams& p, cudaStream_t stream, int* ctas = nullptr) {
+                      const CUtensorMap& d, const CeParams& p, cudaStream_t stream, bool first, int* ctas = nullptr) {
   const int64_t grid = pair ? 2 * std::min<int64_t>(units, dev.pairs) : std::min<int64_t>(units, dev.sms);
   if (ctas != nullptr) *ctas = static_cast<int>(grid);
   return ce_go(pair ? k_ce_gemm<MODE, 2, CE_STAGES> : k_ce_gemm<MODE, 1, CE_STAGES>, grid, CE_THREADS,
-               ce_smem_bytes(CE_STAGES), stream, MODE == CE_LSE, pair, a, b, d, p);
+               ce_smem_bytes(CE_STAGES), stream, first, pair, a, b, d, p);
 }
 
 int few_rows(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }   // NT of up to CE_FEW rows
@@ -1498,17 +1547,24 @@ CeFwdWs ce_fwd_ws(int64_t T, int64_t V) {
   return w;
 }
 
-// Backward workspace: header, row map, packed x [t_pad, H], dz of one piece [t_pad, piece], fp32 parts of dx.
+// Backward workspace: header, row map, packed (or cleared) x [t_pad, H], dz of one piece [t_pad, piece], fp32 parts of dx.
 struct CeBwdWs {
   size_t status, row_map, xp, dz, acc, acc_w, total;
   int64_t t_pad, piece, pieces;
   int splits, dw_splits;
-  bool few;
+  bool few, as_is;             // as_is: rows are not packed (few rows never are)
 };
 constexpr int CE_MAX_SPLITS = 16;
+// Rows as they are: packing is a launch of its own, 4 to 9 us with the choice of dx's shares, and below these sizes saves no
+// more than that in products.  dz's kernel copies x beside its products, which takes longer than these where H is large
+// beside V.  Packed and as they are: 100 x 1448 x 3600 32.8 and 28.1 us, 1000 rows of it 53.4 and 49.0; 1024 x 1024 x 8192
+// 57.9 and 54.4; 100 x 2048 x 32000 97.7 and 91.0; 65 x 64 x 128 12.4 and 10.8; but 400 x 512 x 256 16.2 and 21.9.
+constexpr int64_t CE_AS_IS_ROWS = 1024, CE_AS_IS_PRODUCTS = int64_t(1) << 33, CE_AS_IS_V = 1024;   // T, T * H * V, V
 CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   CeBwdWs w{};
   w.few = T <= CE_FEW;
+  w.as_is = w.few || (T <= CE_AS_IS_ROWS && T * H <= CE_AS_IS_PRODUCTS / V &&
+                       (V >= CE_AS_IS_V || 2 * H <= V));
   w.t_pad = w.few ? 2 * few_rows(T) : up(T, 256) * 256;   // few: dz and x twice
   const int64_t most = std::max(CE_MIN_PIECE, CE_DZ_ELEMS / std::max<int64_t>(w.t_pad, 256) / 256 * 256);
   w.pieces = up(V, most);
@@ -1584,7 +1640,7 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   if (!ce_kmajor(&a, x, T, H, H, few ? few_rows(T) : CE_HALF) || !ce_kmajor(&b, w, V, H, H)) return MXFP8_ERR_CUDA;
   int ctas = 0;
   const cudaError_t e = few ? ce_launch_few<CE_LSE>(T, up(V, 128), dev, b, a, p, st, true, &ctas)
-                            : ce_launch<CE_LSE>(pair, up(T, tile) * up(V, tile), dev, a, b, a, p, st, &ctas);
+                            : ce_launch<CE_LSE>(pair, up(T, tile) * up(V, tile), dev, a, b, a, p, st, true, &ctas);
   if (e != cudaSuccess) return MXFP8_ERR_CUDA;
   p.join = p.status;
   p.joins = ctas;
@@ -1639,7 +1695,6 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.dloss = dloss;
   p.dlse = dlse;
   p.pitch = ws.t_pad;
-  p.acc = ws.pieces > 1 || ws.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
   p.one_piece = ws.pieces == 1;
   p.acc_w = ws.dw_splits > 1 ? reinterpret_cast<float*>(base + ws.acc_w) : nullptr;
   p.dw_splits = ws.dw_splits;
@@ -1647,10 +1702,21 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.timeout_ns = ce_wait_ns();
   const bool dx_pair = !ws.few && use_pair(dev, T, H, ws.splits);
   p.piece_steps = static_cast<int>(up(ws.piece, CE_BK));
-  p.few_splits = ws.splits;
-  if (ws.few) {
+  p.splits = ws.splits;
+  if (ws.as_is) {
     p.rows = static_cast<int>(T);
-    p.dw_rows = static_cast<int>(ws.t_pad);
+    p.t_pad = static_cast<int>(ws.t_pad);
+    p.dw_rows = static_cast<int>(ws.few ? ws.t_pad : T);
+    if (!ws.few) {
+      float least = INFINITY;
+      for (int s = 1; s <= std::min(ws.splits, p.piece_steps); ++s) {
+        const float c = ce_share_cost(s, p.rows, p.H, dx_pair ? 256 : 128, p.piece_steps, dx_pair ? dev.pairs : dev.sms);
+        if (c < least) {
+          least = c;
+          p.splits = s;
+        }
+      }
+    }
   } else {
     CePack q{};
     q.x = static_cast<const uint4*>(x);
@@ -1664,10 +1730,11 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     if (ce_go(k_ce_prep, std::min<int64_t>(up(T, 8), 2 * dev.sms), CE_PREP_THREADS, 0, st, true, false, p, q) != cudaSuccess)
       return MXFP8_ERR_CUDA;
   }
+  p.acc = ws.pieces > 1 || p.splits > 1 ? reinterpret_cast<float*>(base + ws.acc) : nullptr;
   CUtensorMap x_k, x_mn, w_k, w_mn, dz_k, dz_mn, dz_st;
   p.dz = dz;
   p.dz_pitch = ws.piece;
-  if (!ce_kmajor(&x_k, ws.few ? x : xp, ws.few ? T : ws.t_pad, H, H, ws.few ? few_rows(T) : CE_HALF) ||
+  if (!ce_kmajor(&x_k, ws.as_is ? x : xp, ws.as_is ? T : ws.t_pad, H, H, ws.few ? few_rows(T) : CE_HALF) ||
       !ce_mnmajor(&x_mn, xp, ws.t_pad, H, H) || !ce_kmajor(&w_k, w, V, H, H) || !ce_mnmajor(&w_mn, w, V, H, H) ||
       !ce_kmajor(&dz_k, dz, ws.t_pad, ws.piece, ws.piece, ws.few ? 2 * few_rows(T) : CE_HALF) ||
       !ce_mnmajor(&dz_mn, dz, ws.t_pad, ws.piece, ws.piece) || !ce_store(&dz_st, dz, ws.t_pad, ws.piece, ws.piece))
@@ -1682,22 +1749,22 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     p.group_m = group_of(H * 2, dz_pair, up(T, zt));
     p.d_rows = static_cast<int>(ws.t_pad);
     p.d_cols = static_cast<int>(ws.piece);
-    if (ws.few) {
-      const bool first = i == 0;
-      CeParams z = p;
+    const bool first = ws.as_is && i == 0;         // of the call's kernels
+    CeParams z = p;
+    if (first) {
       z.x = static_cast<const uint4*>(x);
-      z.xp = first ? reinterpret_cast<uint4*>(xp) : nullptr;
-      z.status = first ? reinterpret_cast<uint32_t*>(base + ws.status) : nullptr;
-      if (ce_launch_few<CE_DZ>(T, up(cols, 128), dev, w_k, x_k, z, st, first, &p.joins) != cudaSuccess)
-        return MXFP8_ERR_CUDA;
-      p.join = z.status;
-    } else if (ce_launch<CE_DZ>(dz_pair, up(T, zt) * up(cols, zt), dev, x_k, w_k, dz_st, p, st) != cudaSuccess) {
-      return MXFP8_ERR_CUDA;
+      z.xp = reinterpret_cast<uint4*>(xp);
+      z.status = reinterpret_cast<uint32_t*>(base + ws.status);
     }
+    if ((ws.few ? ce_launch_few<CE_DZ>(T, up(cols, 128), dev, w_k, x_k, z, st, first, &p.joins)
+                : ce_launch<CE_DZ>(dz_pair, up(T, zt) * up(cols, zt), dev, x_k, w_k, dz_st, z, st, first, &p.joins)) !=
+        cudaSuccess)
+      return MXFP8_ERR_CUDA;
+    p.join = z.status;
     p.group_m = 1;
     // dx first: few rows leave w in the L2 for it, which dw overwrites
-    if ((ws.few ? ce_launch_few<CE_DX>(T, up(H, 128) * ws.splits, dev, w_mn, dz_k, p, st, false)
-                : ce_launch<CE_DX>(dx_pair, up(T, xt) * up(H, xt) * ws.splits, dev, dz_k, w_mn, dz_st, p, st)) !=
+    if ((ws.few ? ce_launch_few<CE_DX>(T, up(H, 128) * p.splits, dev, w_mn, dz_k, p, st, false)
+                : ce_launch<CE_DX>(dx_pair, up(T, xt) * up(H, xt) * p.splits, dev, dz_k, w_mn, dz_st, p, st, false)) !=
         cudaSuccess)
       return MXFP8_ERR_CUDA;
     CUtensorMap dw_st;
@@ -1711,7 +1778,8 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     const cudaError_t e =
         dw_short ? ce_go(k_ce_gemm<CE_DW, 1, CE_SHORT>, std::min<int64_t>(up(cols, 128) * up(H, 128), 2 * dev.sms),
                        CE_THREADS, ce_smem_bytes(CE_SHORT), st, false, false, dz_mn, x_mn, dw_st, p)
-               : ce_launch<CE_DW>(dw_pair, up(cols, wt) * up(H, wt) * ws.dw_splits, dev, dz_mn, x_mn, dw_st, p, st);
+               : ce_launch<CE_DW>(dw_pair, up(cols, wt) * up(H, wt) * ws.dw_splits, dev, dz_mn, x_mn, dw_st, p, st,
+                                   false);
     if (e != cudaSuccess) return MXFP8_ERR_CUDA;
     if (p.acc_w != nullptr && ce_go(k_ce_dw, std::min<int64_t>(up(cols * (H / 4), 256), 8 * dev.sms), 256, 0, st, false,
                                     false, p, static_cast<uint16_t*>(dw) + v0 * H) != cudaSuccess)
