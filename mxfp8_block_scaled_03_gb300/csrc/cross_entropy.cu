@@ -1571,7 +1571,7 @@ CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   w.piece = up(up(V, w.pieces), 256) * 256;
   w.pieces = up(V, w.piece);
   // dx has few tiles where there are few rows: its K is shared out
-  const int64_t tiles = up(T, 128) * up(H, 128);
+  const int64_t tiles = std::max<int64_t>(1, up(T, 128)) * up(H, 128);   // (no rows: no tiles)
   const int64_t wanted = w.few ? (T <= 32 ? 304 : 152) / tiles : tiles >= 8 * 152 ? 1 : CE_MAX_SPLITS;
   w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(wanted, up(w.piece, 16 * CE_BK))));
   w.status = sizeof(CeMeta);
