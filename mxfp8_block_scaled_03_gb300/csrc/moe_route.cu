@@ -470,6 +470,9 @@ __global__ void __launch_bounds__(RT_FINAL_THREADS) k_route_final(const RoutePar
   const int own = threadIdx.x % width, slice = threadIdx.x / width;
   const int e = static_cast<int>(rank) * share + own;
   const bool in = own < share && e < p.E;
+  // The first CTA's shared memory is written below, by the soonest (one without experts) at once: it has to run by then.
+  // While the kernel before this one is still at work the barrier costs nothing.
+  cluster_sync_all();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float2 zn = make_float2(0.0f, 0.0f);
   for (int i = threadIdx.x; rank == 0 && i < ctas; i += RT_FINAL_THREADS) {
