@@ -73,7 +73,6 @@ constexpr int64_t CE_DZ_ELEMS = int64_t(1) << 28;  // most elements of dz at a t
 constexpr int64_t CE_MIN_PIECE = 2048;             // vocabulary entries of a piece, whatever the rows
 constexpr uint64_t CE_WAIT_NS = 2000000000ull;     // 2 s per individual wait
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
 
 enum { CE_LSE = 0, CE_DZ = 1, CE_DW = 2, CE_DX = 3 };
 
@@ -100,7 +99,7 @@ struct CeParams {
   const float* lse;
   const float* dloss;
   const float* dlse;
-  float2* part;                // CE_LSE: [2 * column tiles][pitch] (largest logit, sum) in base 2
+  float2* part;                // CE_LSE: [2 * column tiles][pitch] (largest logit, sum of exponentials relative to it)
   float* zy;                   // CE_LSE: the target's logit
   int64_t pitch;
   float* acc;                  // CE_DX: [splits][pitch][H] fp32, or NULL: dx is written directly
@@ -127,6 +126,8 @@ __device__ __forceinline__ float ex2(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// exp(v - top): the difference first, so that the largest logit's own term is 1 exactly, whatever its size.
+__device__ __forceinline__ float exp_below(float v, float top) { return ex2((v - top) * LOG2E); }
 __device__ __forceinline__ void ce_report(const CeParams& p, uint32_t bits) {
   atomicOr(p.status != nullptr ? p.status + blockIdx.x : &p.meta->error, bits);
 }
@@ -662,12 +663,11 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         float top = z[0];
 #pragma unroll
         for (int i = 1; i < NH; ++i) top = fmaxf(top, z[i]);
-        const float m = top * LOG2E;                // in base 2
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NH; ++i) sum += ex2(fmaf(z[i], LOG2E, -base));
-        if (row < n_rows) p.part[(2 * t.n + half) * p.pitch + row] = make_float2(m, sum);
+        for (int i = 0; i < NH; ++i) sum += exp_below(z[i], base);
+        if (row < n_rows) p.part[(2 * t.n + half) * p.pitch + row] = make_float2(top, sum);
         continue;
       }
       if (t.steps > 0 && !wait_acc()) break;
@@ -1010,7 +1010,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
     } else if (p.join != nullptr && blockIdx.x == 0) {
       ce_join(p, static_cast<int>(threadIdx.x) - 64, S::EPI_WARPS * 32);
     }
-    // CE_LSE, base 2: below every logit, and finite, so that a first logit replaces it without a case of its own
+    // CE_LSE: below every logit, and finite, so that a first logit replaces it without a case of its own
     float m[S::COLS], sum[S::COLS];
     if (MODE == CE_LSE) {
 #pragma unroll
@@ -1058,10 +1058,10 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
           for (int j = 0; j < S::COLS; ++j) {
             if (j % 8 == 0 && c0 + j >= n_rows) break;
             if (__float_as_int(s_row[c0 + j].w) == v) p.zy[c0 + j] = z[j];
-            const float d = fmaf(z[j], LOG2E, -m[j]);
-            const float e = ex2(-fabsf(d));
+            const float d = z[j] - m[j];
+            const float e = ex2(-fabsf(d) * LOG2E);
             sum[j] = d > 0.0f ? fmaf(sum[j], e, 1.0f) : sum[j] + e;
-            m[j] = fmaxf(m[j], z[j] * LOG2E);
+            m[j] = fmaxf(m[j], z[j]);
           }
         }
       } else if constexpr (MODE == CE_DZ) {
@@ -1110,7 +1110,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
         float top = m[j];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        float t = sum[j] * ex2(m[j] - top);
+        float t = sum[j] * exp_below(m[j], top);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
         if (lane == 0) s_part[quarter * NT + c0 + j] = make_float2(top, t);
@@ -1123,7 +1123,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
         for (int q = 1; q < 4; ++q) {
           const float2 b = s_part[q * NT + i];
           const float top = fmaxf(a.x, b.x);
-          a = make_float2(top, a.y * ex2(a.x - top) + b.y * ex2(b.x - top));
+          a = make_float2(top, a.y * exp_below(a.x, top) + b.y * exp_below(b.x, top));
         }
         p.part[blockIdx.x * p.pitch + i] = a;
       }
@@ -1139,7 +1139,8 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
 }
 
 // Joins the parts of each row: the CTA takes `width` rows (a power of two up to 32), its threads equal shares of the
-// parts.
+// parts.  The loss is (largest logit - target's) + log(sum), both at least 0, and not lse - target: that difference has lse's
+// rounding, and left rows whose target is nearly certain with losses of some 1e-6 of either sign.
 constexpr int CE_MERGE_THREADS = 512;
 __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p, int parts, int width, float* loss, float* lse) {
   __shared__ float2 s[CE_MERGE_THREADS];
@@ -1149,7 +1150,7 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
   auto join = [&](float2 o) {
     const float m_new = fmaxf(m, o.x);
     const float base = m_new == -INFINITY ? 0.0f : m_new;
-    sum = sum * ex2(m - base) + o.y * ex2(o.x - base);
+    sum = sum * exp_below(m, base) + o.y * exp_below(o.x, base);
     m = m_new;
   };
   ce_wait_before();
@@ -1167,15 +1168,15 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
     }
   }
   if (share == 0 && row < p.rows) {
-    const float total = (m + log2f(sum)) * LN2;
-    lse[row] = total;
+    const float rest = logf(sum);
+    lse[row] = m + rest;
     const int64_t y = ce_target(p, row);
     float l = 0.0f;
     if (y >= p.V) {
       l = NAN;
       atomicOr(&p.meta->error, ERR_TARGET_RANGE);
     } else if (y >= 0) {
-      l = total - p.zy[row];
+      l = (m - p.zy[row]) + rest;
     }
     loss[row] = l;
   }
