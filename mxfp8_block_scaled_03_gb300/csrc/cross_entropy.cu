@@ -65,8 +65,8 @@ constexpr int ce_smem_bytes(int stages) {
 }
 constexpr int CE_SHORT = 2;                        // stages where K is few steps (dw of few rows): two CTAs per SM
 static_assert(ce_smem_bytes(CE_STAGES) <= 232448 && ce_smem_bytes(CE_SHORT) <= 115712, "shared memory budget");
-constexpr int CE_CHUNK = 16;                       // CE_LSE: K steps that the tensor core sums before fp32 adds take over
-constexpr uint32_t CE_REGS_LOW = 56, CE_REGS_HIGH = 224;   // CE_LSE: warps 0-3, epilogue warps
+constexpr int CE_CHUNK = 16;                       // logits: K steps that the tensor core sums before fp32 adds take over
+constexpr uint32_t CE_REGS_LOW = 56, CE_REGS_HIGH = 224;   // logits: warps 0-3, epilogue warps
 static_assert(128 * CE_REGS_LOW + 256 * CE_REGS_HIGH == CE_THREADS * 168, "register split must equal the launch pool");
 constexpr int64_t CE_DZ_ELEMS = int64_t(1) << 28;  // most elements of dz at a time (512 MB; with half, 8192 x 4096 x 32000
                                                    // takes two pieces, adds dx up in fp32 and 2.5% longer)
@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
   constexpr int TILE = CE_HALF * CG;
   constexpr int NH = TILE / 2;                      // columns of an epilogue warp
   constexpr uint32_t TMEM_COLS = 2 * TILE;
-  constexpr int CHUNK = MODE == CE_LSE ? CE_CHUNK : 1 << 30;
+  constexpr bool LOGITS = MODE == CE_LSE || MODE == CE_DZ;
+  constexpr int CHUNK = LOGITS ? CE_CHUNK : 1 << 30;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * CE_STAGE_BYTES + CE_EPI_BYTES);
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
   uint32_t prod_issued = 0;
 
   if (warp < CE_EPI_WARP0) {
-    if constexpr (MODE == CE_LSE) ce_regs_dec<CE_REGS_LOW>();
+    if constexpr (LOGITS) ce_regs_dec<CE_REGS_LOW>();
     if (warp == CE_WARP_PRODUCER) {
       // ---------------- tile copies (every CTA its own) ----------------
       // The warp runs the loop together, so that addresses stay in uniform registers, and one lane issues.
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
       }
     }
   } else {
-    if constexpr (MODE == CE_LSE) ce_regs_inc<CE_REGS_HIGH>();
+    if constexpr (LOGITS) ce_regs_inc<CE_REGS_HIGH>();
     // ---------------- epilogue (every CTA its 128 rows) ----------------
     const int quarter = warp & 3;
     const int half = (warp - CE_EPI_WARP0) >> 2;
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
       const int col0 = t.n * TILE + NH * half;
       // what the row needs besides its logits, before the wait
       int y = -1;                                   // the target's column; outside every tile without one
-      float rate = 0.0f, hot = 0.0f, lse2 = 0.0f;
+      float rate = 0.0f, hot = 0.0f, lse = 0.0f;
       int src = 0;
       if (MODE == CE_LSE && row < n_rows) {
         const int64_t target = ce_target(p, row);
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         y = static_cast<int>(ce_target(p, src)) - p.v0;
         hot = __ldg(p.dloss + src) / gain;
         rate = hot + (p.dlse != nullptr ? __ldg(p.dlse + src) / gain : 0.0f);
-        lse2 = __ldg(p.lse + src) * LOG2E;
+        lse = __ldg(p.lse + src);
       }
       auto wait_acc = [&]() {
         bool got = true;
@@ -625,10 +626,33 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         buf ^= 1;
         if (buf == 0) acc_phase ^= 1u;
       };
-      if constexpr (MODE == CE_LSE) {
+      // 32 columns from `col` on, as bf16, through a staging tile to the map that is stored to.
+      auto put_bf16 = [&](int c, const uint32_t* v) {
+        uint8_t* out = wbuf + ((c >> 5) & 1) * CE_BUF_BYTES;
+        if (lane == 0) bulk_wait_read_le1();        // the store that last used this buffer has read it
+        __syncwarp();
+        // row `lane`: four 16-byte chunks, 64B swizzle (chunk j of row i at j ^ ((i >> 1) & 3))
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 o;
+          o.x = pack_bf16x2(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
+          o.y = pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
+          o.z = pack_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
+          o.w = pack_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
+          *reinterpret_cast<uint4*>(out + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (row0 < p.d_rows && col0 + c < p.d_cols) tma_store_2d(&tmD, out, col0 + c, row0);   // clipped at the edges
+          bulk_commit_group();
+        }
+      };
+      if constexpr (LOGITS) {
         // The tensor core cuts its sums off instead of rounding them, always towards zero: H = 4096 in one sum left loss
         // off by 2.8e-6 of its norm, an fp32 product by 0.6e-6.  So it sums CE_CHUNK steps at a time, and these are added
         // here, rounded: 0.6e-6 with 16 steps (1269 us for 8192 x 4096 x 32000), 1.4e-6 with 32 (1256), 0.3e-6 with 8 (1293).
+        // The backward's logits are the forward's, bit for bit, so that p is 1 and dz 0 where the target is certain.
         float z[NH];
         bool ok = true;
         for (int s = 0; ok && s < t.steps; s += CE_CHUNK) {
@@ -647,6 +671,21 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
           }
         }
         if (!ok) break;
+        if constexpr (MODE == CE_DZ) {
+#pragma unroll
+          for (int c = 0; c < NH; c += 32) {
+            uint32_t v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int col = col0 + c + i;
+              float d = rate * exp_below(z[c + i], lse);
+              if (y == col) d -= hot;
+              v[i] = in && col < p.vcols ? __float_as_uint(d) : 0u;
+            }
+            put_bf16(c, v);
+          }
+          continue;
+        }
         if (y >= col0 && y < col0 + NH) {
           const int at = y - col0;
           float zy = 0.0f;
@@ -683,16 +722,8 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
         }
         if (c + 32 >= NH && t.steps > 0) release_acc();
         const int col = col0 + c;
-        if constexpr (MODE == CE_DZ || MODE == CE_DW) {
-          if constexpr (MODE == CE_DZ) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float d = rate * ex2(fmaf(__uint_as_float(v[i]), LOG2E, -lse2));
-              if (y == col + i) d -= hot;
-              v[i] = in && col + i < p.vcols ? __float_as_uint(d) : 0u;
-            }
-          }
-          if (MODE == CE_DW && p.acc_w != nullptr) {
+        if constexpr (MODE == CE_DW) {
+          if (p.acc_w != nullptr) {
             float* dst = p.acc_w + (static_cast<int64_t>(t.split) * p.vcols + row) * p.H + col;
             if (row < p.vcols)
 #pragma unroll
@@ -702,29 +733,9 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
                                 make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]));
             continue;
           }
-          if (MODE == CE_DW) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * gain);
-          }
-          uint8_t* out = wbuf + ((c >> 5) & 1) * CE_BUF_BYTES;
-          if (lane == 0) bulk_wait_read_le1();      // the store that last used this buffer has read it
-          __syncwarp();
-          // row `lane`: four 16-byte chunks, 64B swizzle (chunk j of row i at j ^ ((i >> 1) & 3))
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 o;
-            o.x = pack_bf16x2(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
-            o.y = pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
-            o.z = pack_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
-            o.w = pack_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
-            *reinterpret_cast<uint4*>(out + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) = o;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (row0 < p.d_rows && col < p.d_cols) tma_store_2d(&tmD, out, col, row0);   // clipped at the edges
-            bulk_commit_group();
-          }
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * gain);
+          put_bf16(c, v);
         } else if (row < n_rows) {                  // CE_DX
           if (dx_direct) {
 #pragma unroll
@@ -822,7 +833,8 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
     k_ce_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const CeParams p) {
   using S = FewShape<MODE, NT>;
   constexpr bool A_MN = MODE == CE_DX;
-  constexpr int CHUNK = MODE == CE_LSE ? CE_FEW_CHUNK : 1 << 30;
+  // (33 to 64 rows: the forward's logits are k_ce_gemm's)
+  constexpr int CHUNK = MODE == CE_DX ? 1 << 30 : NT == 64 ? CE_CHUNK : CE_FEW_CHUNK;
   constexpr int NO_TARGET = INT_MIN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -989,7 +1001,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
             if (MODE == CE_DZ) {
               r.z = __ldg(p.dloss + i) / gain;
               r.x = r.z + (p.dlse != nullptr ? __ldg(p.dlse + i) / gain : 0.0f);
-              r.y = __ldg(p.lse + i) * LOG2E;
+              r.y = __ldg(p.lse + i);
             }
           }
         }
@@ -1070,7 +1082,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
 #pragma unroll
         for (int j = 0; j < S::COLS; ++j) {
           const float4 r = s_row[c0 + j];
-          float d = r.x * ex2(fmaf(z[j], LOG2E, -r.y));
+          float d = r.x * exp_below(z[j], r.y);
           if (__float_as_int(r.w) == v) d -= r.z;
           const bool in = __float_as_int(r.w) != NO_TARGET && v < p.vcols;
           const __nv_bfloat16 hi = __float2bfloat16_rn(d), lo = __float2bfloat16_rn(d - __bfloat162float(hi));

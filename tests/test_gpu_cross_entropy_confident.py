@@ -60,3 +60,23 @@ def test_no_loss_is_negative(mx, T):
         y = (x.double() @ w.double().t()).argmax(1)
         loss, _ = mx.linear_cross_entropy_fwd(x, w, y)
         assert (loss >= 0).all()
+
+
+@pytest.mark.parametrize("T,H,V", [(1, 2048, 1000), (20, 4096, 1000), (32, 2048, 300), (50, 4096, 3000), (64, 2048, 300),
+                                   (300, 2048, 3000), (1000, 4096, 2000), (1100, 4096, 2000), (3000, 2048, 4000)])
+@pytest.mark.parametrize("margin", [50.0, 150.0, 900.0])
+def test_gradients_of_nearly_certain_targets(mx, T, H, V, margin):
+    """S is below 2^-40 here: lse is the target's logit to the bit, and the backward's logits are the forward's, so p is 1
+    and dz 0 at the target; at the others dz is p, in all S: dx is within S max|w| of 0 (S moved by exp(2 bz) and the
+    roundings of 2^-8), dw within the sum of S |x| over the rows."""
+    import torch
+    x, w, y = confident(T, H, V, margin, seed=T + V)
+    _, lse = mx.linear_cross_entropy_fwd(x, w, y)
+    z, bz = C.bars_of_logits(x, w)
+    d = z - z.gather(1, y[:, None])
+    d.scatter_(1, y[:, None], -math.inf)
+    S = torch.exp(d + 2 * bz.amax(1)[:, None]).sum(1)
+    assert S.max() < 2.0 ** -40
+    dx, dw = mx.linear_cross_entropy_bwd(torch.ones(T, device="cuda"), x, w, y, lse)
+    assert (dx.double().abs() <= 1.1 * S[:, None] * w.double().abs().max() + 1e-38).all()
+    assert (dw.double().abs() <= 1.1 * (S[:, None] * x.double().abs()).sum(0) + 1e-38).all()
