@@ -546,8 +546,11 @@ int moe_route_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
  *            not overlap the inputs.  A row
  *            without a target (negative or >= V) passes nothing on, whatever its x, lse, dloss and dlse hold;
  *            its dx is 0.
- *   workspace linear_cross_entropy_bwd_workspace_size(T, H, V) bytes, as above (packed rows, one piece of
- *            dz of at most 2^28 elements where T is up to 131072, parts of dx and dw).
+ *   workspace linear_cross_entropy_bwd_workspace_size(T, H, V) bytes, as above.  It holds the rows that take
+ *            part (2 T H bytes, T rounded up to 256), dz of a piece of the vocabulary (half of the logits' 2 T V
+ *            bytes at the most, but 64 MB where that is more and 256 MB where it is less; pieces have 2048 entries
+ *            or more; up to 64 rows 512 MB), and dx or parts of it in fp32 (4 T H bytes, or a quarter of the logits',
+ *            32 to 64 MB).
  * Results do not depend on timing.  Requirements: T >= 0, H > 0, V > 0 (otherwise
  * MXFP8_ERR_INVALID_ARG); H % 8 == 0, H <= 2^20, T <= 2^24, V <= 2^28, fewer than 2^30 tiles of 128 x 128
  * logits (otherwise MXFP8_ERR_UNSUPPORTED); x, w, dx, dw 16-byte aligned, the others to their elements.

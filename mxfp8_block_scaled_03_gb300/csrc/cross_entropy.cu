@@ -18,7 +18,7 @@
 // The backward first packs the rows that take part, so that padding costs nothing and nothing it holds can reach
 // dw (0 * NaN); where that takes longer than it could save, dz's kernel writes zeros for the other rows instead, to dz and to
 // a copy of x (rows as they are).  dz is rounded to bf16 (by at most 2^-8 of its value): it is the operand of two products
-// whose results are rounded to bf16 as well.  It lives for one piece of the vocabulary only, of at most CE_DZ_ELEMS elements.
+// whose results are rounded to bf16 as well.  It lives for one piece of the vocabulary only, at most half of a large one.
 // Up to CE_FEW rows the same modes run in a kernel of their own, k_ce_few, which is bound by the bytes of w.
 //
 // Measured (replayed, GB300; rows x H x vocabulary):
@@ -68,8 +68,13 @@ static_assert(ce_smem_bytes(CE_STAGES) <= 232448 && ce_smem_bytes(CE_SHORT) <= 1
 constexpr int CE_CHUNK = 16;                       // logits: K steps that the tensor core sums before fp32 adds take over
 constexpr uint32_t CE_REGS_LOW = 56, CE_REGS_HIGH = 224;   // logits: warps 0-3, epilogue warps
 static_assert(128 * CE_REGS_LOW + 256 * CE_REGS_HIGH == CE_THREADS * 168, "register split must equal the launch pool");
-constexpr int64_t CE_DZ_ELEMS = int64_t(1) << 28;  // most elements of dz at a time (512 MB; with half, 8192 x 4096 x 32000
-                                                   // takes two pieces, adds dx up in fp32 and 2.5% longer)
+// Most elements of dz at a time, in bf16: half of the logits', at least CE_DZ_LEAST (64 MB, below which it is not worth
+// another piece) and at most CE_DZ_MOST (256 MB; up to CE_FEW rows, whose dz is small beside w, CE_DZ_FEW).  With all of dz
+// in one piece the workspace was larger than the logits.
+constexpr int64_t CE_DZ_LEAST = int64_t(1) << 25, CE_DZ_MOST = int64_t(1) << 27, CE_DZ_FEW = int64_t(1) << 28;
+// Most elements of dx's fp32 parts: an eighth of the logits' (a quarter of their bytes in bf16), within these; where the
+// vocabulary has several pieces, dx once at the least.
+constexpr int64_t CE_PARTS_LEAST = int64_t(1) << 23, CE_PARTS_MOST = int64_t(1) << 24;
 constexpr int64_t CE_MIN_PIECE = 2048;             // vocabulary entries of a piece, whatever the rows
 constexpr uint64_t CE_WAIT_NS = 2000000000ull;     // 2 s per individual wait
 constexpr float LOG2E = 1.4426950408889634f;
@@ -102,8 +107,8 @@ struct CeParams {
   float2* part;                // CE_LSE: [2 * column tiles][pitch] (largest logit, sum of exponentials relative to it)
   float* zy;                   // CE_LSE: the target's logit
   int64_t pitch;
-  float* acc;                  // CE_DX: [splits][pitch][H] fp32, or NULL: dx is written directly
-  int one_piece;               // (and also where one share of a single piece is all there is)
+  float* acc;                  // CE_DX: [splits][rows][H] fp32, or NULL: dx is written directly
+  int last;                    // the vocabulary's last piece (where it is one share, dx is written with it)
   float* acc_w;                // CE_DW: [dw_splits][vcols][H] fp32, or NULL: dw is written directly
   int dw_splits;
   int dw_rows;                 // rows as they are, CE_DW: rows of dz (few rows: of both its pieces)
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
     }
     if (MODE == CE_DX && p.join != nullptr && blockIdx.x == 0)
       ce_join(p, static_cast<int>(threadIdx.x) - 32 * CE_EPI_WARP0, CE_EPI_WARPS * 32);
-    const bool dx_direct = MODE == CE_DX && (p.acc == nullptr || (!as_is && p.one_piece && p.meta->splits == 1));
+    const bool dx_direct = MODE == CE_DX && (p.acc == nullptr || (p.last && ce_shares(p) == 1));
     int buf = 0;
     uint32_t acc_phase = 0;
     for (int u = first; u < units.total; u += stride) {
@@ -737,6 +742,21 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
           for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * gain);
           put_bf16(c, v);
         } else if (row < n_rows) {                  // CE_DX
+          float* part = p.acc + (static_cast<int64_t>(t.split) * n_rows + row) * p.H + col;
+          if (p.acc_add) {                          // the pieces before this one; all loads first
+            float4 old[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (col + 4 * j < p.H) old[j] = *reinterpret_cast<const float4*>(part + 4 * j);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (col + 4 * j < p.H) {
+                v[4 * j + 0] = __float_as_uint(__uint_as_float(v[4 * j + 0]) + old[j].x);
+                v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + old[j].y);
+                v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + old[j].z);
+                v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + old[j].w);
+              }
+          }
           if (dx_direct) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = in ? __float_as_uint(__uint_as_float(v[i]) * gain) : 0u;
@@ -752,20 +772,11 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
                 *reinterpret_cast<uint4*>(dst + j) = o;
               }
           } else {
-            float* dst = p.acc + (t.split * p.pitch + row) * p.H + col;
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
-              if (col + j < p.H) {
-                if (p.acc_add) {
-                  const float4 a = *reinterpret_cast<const float4*>(dst + j);
-                  const float4 b = *reinterpret_cast<const float4*>(dst + j + 4);
-                  const float old[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) v[j + i] = __float_as_uint(__uint_as_float(v[j + i]) + old[i]);
-                }
-                st_global_32B(dst + j, make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]),
+              if (col + j < p.H)
+                st_global_32B(part + j, make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]),
                               make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]));
-              }
           }
         }
       }
@@ -1100,7 +1111,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
                     ce_takes_part(p, c0 + j) ? __bfloat16_as_ushort(__float2bfloat16_rn(z[j] * gain)) : 0;
           continue;
         }
-        float* dst = p.acc + (static_cast<int64_t>(u / tiles) * p.pitch + c0) * p.H + h;
+        float* dst = p.acc + (static_cast<int64_t>(u / tiles) * n_rows + c0) * p.H + h;
         if (h < p.H) {
 #pragma unroll
           for (int j = 0; j < S::COLS; ++j)
@@ -1194,7 +1205,7 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
   }
 }
 
-// Shares of the vocabulary in dx, from the rows that take part: as many as deal the K steps out evenly to `workers` CTAs
+// Shares of the vocabulary in dx, from the rows that take part: as many of those whose parts there is room for as deal the K steps out evenly to `workers` CTAs
 // (or pairs).  Counted in K steps (about 0.27 us): a share's start and end, and its part of dx, written and read back
 // (1072 x 2048 values in 15 parts took 48 us to add up; 3 parts leave 10, and the product 10 us longer).
 constexpr int CE_SHARE_STEPS = 8;
@@ -1204,6 +1215,11 @@ __host__ __device__ __forceinline__ float ce_share_cost(int s, int n, int H, int
   const int64_t waves = (units * s + workers - 1) / workers;
   return static_cast<float>(waves * ((steps + s - 1) / s + CE_SHARE_STEPS)) +
          (s > 1 ? static_cast<float>(s) * CE_PART_STEPS * static_cast<float>(n) * static_cast<float>(H) : 0.0f);
+}
+// What there is room for; one share needs none, or (several pieces) has it.
+__host__ __device__ __forceinline__ int ce_most_shares(int most, int n, int H, int64_t room) {
+  const int64_t fit = room / (static_cast<int64_t>(n > 0 ? n : 1) * H);
+  return fit < 1 ? 1 : fit < most ? static_cast<int>(fit) : most;
 }
 __device__ __forceinline__ int ce_splits(int n, int H, int tile, int steps, int workers, int most) {   // a warp; most <= 32
   const int s = 1 + (threadIdx.x & 31);
@@ -1218,9 +1234,10 @@ struct CePack {
   int32_t* row_map;
   int T, t_pad;
   int dx_tile, dx_workers, dx_most;   // ce_splits
+  int64_t dx_room;                    // elements of dx's parts
 };
 __device__ __forceinline__ void ce_put_meta(const CeParams& p, const CePack& q, int n, bool bad, float gain) {   // warp 0
-  const int splits = ce_splits(n, p.H, q.dx_tile, p.piece_steps, q.dx_workers, q.dx_most);
+  const int splits = ce_splits(n, p.H, q.dx_tile, p.piece_steps, q.dx_workers, ce_most_shares(q.dx_most, n, p.H, q.dx_room));
   if (threadIdx.x == 0) {
     p.meta->n = n;
     p.meta->error = bad ? ERR_TARGET_RANGE : 0u;
@@ -1304,8 +1321,8 @@ __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int s
   __shared__ float4 s_sum[CE_DX_THREADS];
   ce_wait_before();
   const bool as_is = p.rows > 0;              // rows that take no part are among them
-  if (!as_is && p.one_piece && p.meta->splits == 1) return;   // dx has been written
   const int most = ce_shares(p);
+  if (!as_is && most == 1) return;            // dx has been written
   const float gain = p.meta->gain;
   const int split_steps = (p.piece_steps + most - 1) / most;
   const int splits = (steps + split_steps - 1) / split_steps;   // of the first piece; a shorter last one has no more
@@ -1327,7 +1344,7 @@ __global__ void __launch_bounds__(CE_DX_THREADS) k_ce_dx(const CeParams p, int s
     if (e < total) {
       const float4* a = reinterpret_cast<const float4*>(p.acc) + i * per_row + c;
 #pragma unroll 8
-      for (int s = slice; s < splits; s += slices) add(__ldcs(a + s * p.pitch * per_row));
+      for (int s = slice; s < splits; s += slices) add(__ldcs(a + s * total));
     }
     if (slices > 1) {
       __syncthreads();
@@ -1563,7 +1580,7 @@ CeFwdWs ce_fwd_ws(int64_t T, int64_t V) {
 // Backward workspace: header, row map, packed (or cleared) x [t_pad, H], dz of one piece [t_pad, piece], fp32 parts of dx.
 struct CeBwdWs {
   size_t status, row_map, xp, dz, acc, acc_w, total;
-  int64_t t_pad, piece, pieces;
+  int64_t t_pad, piece, pieces, room;   // room: elements of dx's parts
   int splits, dw_splits;
   bool few, as_is;             // as_is: rows are not packed (few rows never are)
 };
@@ -1579,7 +1596,9 @@ CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   w.as_is = w.few || (T <= CE_AS_IS_ROWS && T * H <= CE_AS_IS_PRODUCTS / V &&
                        (V >= CE_AS_IS_V || 2 * H <= V));
   w.t_pad = w.few ? 2 * few_rows(T) : up(T, 256) * 256;   // few: dz and x twice
-  const int64_t most = std::max(CE_MIN_PIECE, CE_DZ_ELEMS / std::max<int64_t>(w.t_pad, 256) / 256 * 256);
+  auto entries = [&](int64_t elems) { return std::max(CE_MIN_PIECE, elems / std::max<int64_t>(w.t_pad, 256) / 256 * 256); };
+  const int64_t most = w.few ? entries(CE_DZ_FEW)
+                             : std::clamp(up(up(V, 2), 256) * 256, entries(CE_DZ_LEAST), entries(CE_DZ_MOST));
   w.pieces = up(V, most);
   w.piece = up(up(V, w.pieces), 256) * 256;
   w.pieces = up(V, w.piece);
@@ -1596,7 +1615,11 @@ CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   const int64_t dw_tiles = up(w.piece, 128) * up(H, 128);
   w.dw_splits = w.few ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({CE_MAX_SPLITS, 152 / dw_tiles,
                                                                                      up(T, 8 * CE_BK)})));
-  w.acc_w = up256(w.acc + (w.pieces > 1 || w.splits > 1 ? static_cast<size_t>(w.splits) * w.t_pad * H * 4 : 0));
+  w.room = w.splits * T * H;
+  if (!w.few) w.room = std::min(w.room, std::clamp(T * V / 8, CE_PARTS_LEAST, CE_PARTS_MOST));
+  if (w.pieces > 1) w.room = std::max(w.room, T * H);
+  else if (w.splits == 1) w.room = 0;
+  w.acc_w = up256(w.acc + static_cast<size_t>(w.room) * 4);
   w.total = up256(w.acc_w + (w.dw_splits > 1 ? static_cast<size_t>(w.dw_splits) * w.piece * H * 4 : 0));
   return w;
 }
@@ -1707,8 +1730,6 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.lse = lse;
   p.dloss = dloss;
   p.dlse = dlse;
-  p.pitch = ws.t_pad;
-  p.one_piece = ws.pieces == 1;
   p.acc_w = ws.dw_splits > 1 ? reinterpret_cast<float*>(base + ws.acc_w) : nullptr;
   p.dw_splits = ws.dw_splits;
   p.dx = static_cast<uint16_t*>(dx);
@@ -1722,7 +1743,8 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     p.dw_rows = static_cast<int>(ws.few ? ws.t_pad : T);
     if (!ws.few) {
       float least = INFINITY;
-      for (int s = 1; s <= std::min(ws.splits, p.piece_steps); ++s) {
+      const int most = std::min(p.piece_steps, ce_most_shares(ws.splits, p.rows, p.H, ws.room));
+      for (int s = 1; s <= most; ++s) {
         const float c = ce_share_cost(s, p.rows, p.H, dx_pair ? 256 : 128, p.piece_steps, dx_pair ? dev.pairs : dev.sms);
         if (c < least) {
           least = c;
@@ -1740,6 +1762,7 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     q.dx_tile = dx_pair ? 256 : 128;
     q.dx_workers = dx_pair ? dev.pairs : dev.sms;
     q.dx_most = ws.splits;
+    q.dx_room = ws.room;
     if (ce_go(k_ce_prep, std::min<int64_t>(up(T, 8), 2 * dev.sms), CE_PREP_THREADS, 0, st, true, false, p, q) != cudaSuccess)
       return MXFP8_ERR_CUDA;
   }
@@ -1757,6 +1780,7 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
     p.v0 = static_cast<int>(v0);
     p.vcols = static_cast<int>(cols);
     p.acc_add = i > 0;
+    p.last = i + 1 == ws.pieces;
     const bool dz_pair = use_pair(dev, T, cols), dw_pair = use_pair(dev, cols, H, ws.dw_splits);
     const int64_t zt = dz_pair ? 256 : 128, wt = dw_pair ? 256 : 128, xt = dx_pair ? 256 : 128;
     p.group_m = group_of(H * 2, dz_pair, up(T, zt));
@@ -1798,7 +1822,7 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
                                     false, p, static_cast<uint16_t*>(dw) + v0 * H) != cudaSuccess)
       return MXFP8_ERR_CUDA;
   }
-  if (p.acc != nullptr &&
+  if (p.acc != nullptr && (ws.few || !ws.as_is || p.splits > 1) &&   // (otherwise dx has been written)
       ce_go(k_ce_dx, std::min<int64_t>(up(T * (H / 4), CE_DX_THREADS / 8), 8 * dev.sms), CE_DX_THREADS, 0, st, false, false, p,
             static_cast<int>(up(std::min(ws.piece, V), CE_BK))) != cudaSuccess)
     return MXFP8_ERR_CUDA;
