@@ -1585,11 +1585,16 @@ struct CeBwdWs {
   bool few, as_is;             // as_is: rows are not packed (few rows never are)
 };
 constexpr int CE_MAX_SPLITS = 16;
-// Rows as they are: packing is a launch of its own, 4 to 9 us with the choice of dx's shares, and below these sizes saves no
-// more than that in products.  dz's kernel copies x beside its products, which takes longer than these where H is large
-// beside V.  Packed and as they are: 100 x 1448 x 3600 32.8 and 28.1 us, 1000 rows of it 53.4 and 49.0; 1024 x 1024 x 8192
-// 57.9 and 54.4; 100 x 2048 x 32000 97.7 and 91.0; 65 x 64 x 128 12.4 and 10.8; but 400 x 512 x 256 16.2 and 21.9.
-constexpr int64_t CE_AS_IS_ROWS = 1024, CE_AS_IS_PRODUCTS = int64_t(1) << 33, CE_AS_IS_V = 1024;   // T, T * H * V, V
+// Rows as they are: packing is a launch of its own, 4 to 9 us with the choice of dx's shares, and saves products where rows
+// take no part, which the host does not know; up to 512 rows and 2^33 products it is left out, where it saves hardly more than
+// that with half of the rows masked.  dz's kernel copies x beside its products, which takes longer than these where H is
+// large beside V.  As they are and packed, us with no rows masked, half of them, 80%:
+//   100 x 1448 x 3600    28.4 33.5   28.4 32.4   28.4 32.0        512 x 1024 x 8192    44.1 47.7   43.8 43.0   43.7 38.7
+//   400 x 1448 x 3600    35.7 41.1   35.5 38.3   35.4 36.4       1000 x 1448 x 3600    49.4 54.1   49.2 43.5   49.0 41.1
+//   256 x 2048 x 16384   71.2 75.5   70.5 68.7   69.4 63.4       1024 x 1024 x 8192    54.8 58.8   54.3 50.0   53.8 41.1
+//   100 x 2048 x 32000   92.3 99.8   92.4 96.1   91.9 94.5       1024 x 64 x 50257      110  111    110   77    110   61
+// and 400 x 512 x 256, none masked, 21.9 and 16.2.
+constexpr int64_t CE_AS_IS_ROWS = 512, CE_AS_IS_PRODUCTS = int64_t(1) << 33, CE_AS_IS_V = 1024;   // T, T * H * V, V
 CeBwdWs ce_bwd_ws(int64_t T, int64_t H, int64_t V) {
   CeBwdWs w{};
   w.few = T <= CE_FEW;

@@ -9,11 +9,12 @@ pytestmark = pytest.mark.gpu
 mx = C.mx
 
 
-# rows as they are, several shares; one share and packed rows; packed rows, several shares; with hardly a row left; a last
-# piece of few entries; 65536 rows of the smallest pieces
+# packed rows in several shares or one, with hardly a row left, a last piece of few entries; rows as they are; more than
+# 65536 rows, whose pieces are the smallest
 @pytest.mark.parametrize("T,H,V,ignored", [(600, 64, 120000, 0.3), (1000, 72, 100001, 0.0), (2048, 4096, 17000, 0.1),
                                            (1100, 264, 60000, 0.3), (1500, 520, 50257, 0.9), (2000, 136, 40000, 0.999),
-                                           (1024, 128, 131329, 0.2), (66000, 16, 4100, 0.5), (3000, 1024, 30001, 0.0)])
+                                           (1024, 128, 131329, 0.2), (500, 64, 200000, 0.3), (300, 72, 270001, 0.0),
+                                           (66000, 16, 4100, 0.5), (3000, 1024, 30001, 0.0)])
 def test_pieces(mx, T, H, V, ignored):
     import torch
     x, w, y = C.make(T, H, V, seed=T + V, ignored=ignored)
@@ -33,7 +34,7 @@ def test_pieces(mx, T, H, V, ignored):
     assert all(torch.equal(a, b) for a, b in zip((dx, dw), again))
 
 
-@pytest.mark.parametrize("T,H,V", [(600, 64, 120000), (2048, 4096, 17000), (1100, 264, 60000)])
+@pytest.mark.parametrize("T,H,V", [(600, 64, 120000), (500, 64, 200000), (2048, 4096, 17000), (1100, 264, 60000)])
 def test_rows_without_a_target_hold_anything(mx, T, H, V):
     import torch
     x, w, y = C.make(T, H, V, seed=5)
