@@ -19,7 +19,8 @@
 // dw (0 * NaN); where that takes longer than it could save, dz's kernel writes zeros for the other rows instead, to dz and to
 // a copy of x (rows as they are).  dz is rounded to bf16 (by at most 2^-8 of its value): it is the operand of two products
 // whose results are rounded to bf16 as well.  It lives for one piece of the vocabulary only, at most half of a large one.
-// Up to CE_FEW rows the same modes run in a kernel of their own, k_ce_few, which is bound by the bytes of w.
+// Few rows have a kernel of their own, k_ce_few, which is bound by the bytes of w: CE_LSE up to CE_FEW_FWD rows, CE_DZ and
+// CE_DX up to CE_FEW.  dw is k_ce_gemm's for any number of rows.
 //
 // Measured (replayed, GB300; rows x H x vocabulary):
 //   forward   8192 x 4096 x 32000   1.08-1.19 ms = 1.80-2.00 PFLOP/s (under sustained power and cool; cuBLAS in bf16 1.72-1.88)
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
 // Up to CE_FEW rows: the weights are the M operand (128 rows of w, or 128 columns for dx), the rows the N operand
 // (NT of them), so that nothing is spent on rows that are not there and a CTA's stages hold little but weights.  Bound:
 // the bytes of w.  Two CTAs per SM keep twice the copies in flight.
-//   CE_LSE  z^T = w x^T: a thread has one vocabulary entry and all rows; it carries every row's running maximum and sum
+//   CE_LSE  (up to 32 rows) z^T = w x^T: a thread has one vocabulary entry and all rows; it carries every row's running maximum and sum
 //           over all its tiles, and lanes are joined once, at the end
 //   CE_DZ   the same product and dz; rows that take no part are zeros in dz and in a copy of x for dw (no packing)
 //   CE_DX   dx^T = w^T dz^T over a share of the vocabulary: fp32 parts
@@ -835,6 +836,7 @@ struct FewShape {
   static constexpr int PARAM_OFFSET = STAGES * STAGE_BYTES;             // [NT] float4 (CE_DZ), [EPI_WARPS][COLS] float2 (CE_LSE)
   static constexpr int BAR_OFFSET = PARAM_OFFSET + EPI_WARPS * COLS * 16;
   static constexpr int SMEM_BYTES = BAR_OFFSET + (2 * STAGES + 2 * CE_FEW_BUFS + 1) * 8 + 8 + 1024;
+  static_assert(MODE == CE_DZ || MODE == CE_DX || (MODE == CE_LSE && NT <= CE_FEW_FWD), "forms of the few rows' kernel");
   static_assert(SMEM_BYTES <= (PER_SM == 2 ? 115712 : 232448), "shared memory budget");
   static_assert(PER_SM * CE_FEW_BUFS * NB <= 512, "TMEM budget");
 };
@@ -1522,9 +1524,10 @@ cudaError_t ce_launch_few(int64_t T, int64_t units, const CeDevice& dev, const C
   };
   const int nt = few_rows(T);
   if (nt == 16) return go(std::integral_constant<int, 16>{}, k_ce_few<MODE, 16>);
-  if (nt == 32) return go(std::integral_constant<int, 32>{}, k_ce_few<MODE, 32>);
-  if constexpr (MODE == CE_LSE) return cudaErrorInvalidValue;   // (not called: CE_FEW_FWD)
-  else return go(std::integral_constant<int, 64>{}, k_ce_few<MODE, 64>);
+  if constexpr (MODE != CE_LSE) {               // (CE_LSE: up to CE_FEW_FWD rows)
+    if (nt == 64) return go(std::integral_constant<int, 64>{}, k_ce_few<MODE, 64>);
+  }
+  return go(std::integral_constant<int, 32>{}, k_ce_few<MODE, 32>);
 }
 
 constexpr int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
