@@ -812,8 +812,8 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
 // Up to CE_FEW rows: the weights are the M operand (128 rows of w, or 128 columns for dx), the rows the N operand
 // (NT of them), so that nothing is spent on rows that are not there and a CTA's stages hold little but weights.  Bound:
 // the bytes of w.  Two CTAs per SM keep twice the copies in flight.
-//   CE_LSE  (up to 32 rows) z^T = w x^T: a thread has one vocabulary entry and all rows; it carries every row's running maximum and sum
-//           over all its tiles, and lanes are joined once, at the end
+//   CE_LSE  (up to 32 rows) z^T = w x^T: a thread has one vocabulary entry and all rows; it carries every row's running
+//           maximum and sum over all its tiles, and lanes are joined once, at the end
 //   CE_DZ   the same product and dz; rows that take no part are zeros in dz and in a copy of x for dw (no packing)
 //   CE_DX   dx^T = w^T dz^T over a share of the vocabulary: fp32 parts
 // The tensor cores have time to spare here, so dz is held in two bf16 pieces, the second of what the first one leaves (to
