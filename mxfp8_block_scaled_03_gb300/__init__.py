@@ -865,7 +865,7 @@ def moe_route_bwd(logits, experts, gates, lse, counts, dgates=None, dlosses=None
     f32, i32 = torch.float32, torch.int32
     dev, current = _place(logits, "logits")
     T, E, code, pl = _logits(logits, "logits", dev)
-    k = experts.shape[1]
+    _, k = experts.shape
     if row_of_slot is not None and dgates is None:
         raise ValueError("row_of_slot without dgates")
     args = (_need(experts, i32, (T, k), "experts", dev), _need(gates, f32, (T, k), "gates", dev),
@@ -897,8 +897,7 @@ def _lce_args(x, w, targets):
     """(device, stream, T, H, V, x pointer, w pointer, targets pointer, 1 for int64 targets)."""
     import torch
     dev, current = _place(x, "x")
-    T, H = x.shape
-    V = w.shape[0]
+    (T, H), (V, _) = x.shape, w.shape
     if targets.dtype is not torch.int32 and targets.dtype is not torch.int64:
         raise ValueError(f"targets: expected int32 or int64, got {targets.dtype}")
     return (dev, current, T, H, V, _need(x, torch.bfloat16, (T, H), "x", dev),
@@ -920,17 +919,18 @@ def linear_cross_entropy_fwd(x, w, targets, out=None, workspace=None, stream=Non
     f32, u8 = torch.float32, torch.uint8
     dev, current, T, H, V, px, pw, pt, wide = _lce_args(x, w, targets)
     if out is None:
-        out = (torch.empty(T, dtype=f32, device=x.device), torch.empty(T, dtype=f32, device=x.device))
-        ptrs = [t.data_ptr() for t in out]
+        loss, lse = (torch.empty(T, dtype=f32, device=x.device), torch.empty(T, dtype=f32, device=x.device))
+        ptrs = loss.data_ptr(), lse.data_ptr()
     else:
-        ptrs = [_need(t, f32, (T,), name, dev) for t, name in zip(out, ("loss", "lse"))]
+        loss, lse = out
+        ptrs = _need(loss, f32, (T,), "loss", dev), _need(lse, f32, (T,), "lse", dev)
     if workspace is None:
         workspace = torch.empty(max(256, linear_cross_entropy_workspace_size(T, H, V)), dtype=u8, device=x.device)
     st = lib().linear_cross_entropy_fwd(px, pw, pt, wide, T, H, V, *ptrs, _need(workspace, u8, 256, "workspace", dev),
                                         workspace.numel(), current)
     if st != OK:
         raise MXFP8Error(st, "linear_cross_entropy_fwd")
-    return tuple(out)
+    return loss, lse
 
 
 def linear_cross_entropy_bwd(dloss, x, w, targets, lse, dlse=None, out=None, workspace=None, stream=None):
@@ -947,17 +947,18 @@ def linear_cross_entropy_bwd(dloss, x, w, targets, lse, dlse=None, out=None, wor
     pd, ps = _need(dloss, f32, (T,), "dloss", dev), _need(lse, f32, (T,), "lse", dev)
     pe = None if dlse is None else _need(dlse, f32, (T,), "dlse", dev)
     if out is None:
-        out = torch.empty_like(x), torch.empty_like(w)
-        ptrs = [t.data_ptr() for t in out]
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        ptrs = dx.data_ptr(), dw.data_ptr()
     else:
-        ptrs = [_need(out[0], torch.bfloat16, (T, H), "dx", dev), _need(out[1], torch.bfloat16, (V, H), "dw", dev)]
+        dx, dw = out
+        ptrs = _need(dx, torch.bfloat16, (T, H), "dx", dev), _need(dw, torch.bfloat16, (V, H), "dw", dev)
     if workspace is None:
         workspace = torch.empty(max(256, linear_cross_entropy_bwd_workspace_size(T, H, V)), dtype=u8, device=x.device)
     st = lib().linear_cross_entropy_bwd(pd, pe, px, pw, pt, wide, ps, T, H, V, *ptrs,
                                         _need(workspace, u8, 256, "workspace", dev), workspace.numel(), current)
     if st != OK:
         raise MXFP8Error(st, "linear_cross_entropy_bwd")
-    return tuple(out)
+    return dx, dw
 
 
 def mxfp8_mma_peak(iters: int, workspace, fmt: int = 0, stream=None) -> int:
