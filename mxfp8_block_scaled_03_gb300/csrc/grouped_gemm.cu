@@ -46,12 +46,12 @@
 // drain and exit.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cstdlib>
 #include <mutex>
 
-#include "launch_host.h"
 #include "mx_device.cuh"
 #include "mx_internal.h"
 #include "mxfp8moe.h"
@@ -92,6 +92,7 @@ constexpr uint32_t ACC_COL = 0;            // accumulator: up to 256 fp32 column
 constexpr uint32_t SFA_COL = 256;          // 4 columns per stage
 constexpr uint32_t SFB_COL = 272;          // 8 columns per stage
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 256 + 1024;
+constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // 2 s per individual wait
 static_assert(A_BYTES + B_BYTES_MAX + 3 * SF_ATOM <= STAGE_BYTES, "stage layout");
 static_assert(STAGE_BYTES % 1024 == 0, "stages keep 1024-byte alignment for the 128B swizzle");
 static_assert(SFB_COL + 8 * STAGES <= TMEM_COLS, "TMEM budget");
@@ -262,6 +263,15 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+template <uint32_t N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Saved pre-activations [G | U] ([r_pad, 2F] bf16) are stored in blocks of 32 rows x 8 columns
@@ -1538,6 +1548,32 @@ __global__ void __launch_bounds__(1024) k_schedule(const int32_t* split, int E, 
 }
 
 // ---- host side -------------------------------------------------------------------------------
+
+// Limit of every pipeline wait: 2 s, or the value in ns of the environment variable
+// MXFP8MOE_WAIT_LIMIT_NS when it holds a positive integer (read at each call; failure-path tests
+// use it to make waits run out without any change to the kernels).  Teardown waits for copies and
+// MMAs in flight always keep the full 2 s.
+uint64_t pipeline_wait_ns() {
+  const char* v = getenv("MXFP8MOE_WAIT_LIMIT_NS");
+  if (v == nullptr || *v == 0) return kWaitTimeoutNs;
+  char* end = nullptr;
+  const unsigned long long n = strtoull(v, &end, 10);
+  return (end != nullptr && *end == 0 && n > 0) ? static_cast<uint64_t>(n) : kWaitTimeoutNs;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
 
 // 2-D byte matrix [rows, cols] (row pitch = cols), 128 x 128 boxes, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
