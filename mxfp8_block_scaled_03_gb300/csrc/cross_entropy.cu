@@ -32,7 +32,6 @@
 // 128 tiles for 76 pairs).  Loops of one lane instead of whole warps around the copies and the products left it at 78%: a
 // step's 512 cycles of products took the issuing lane nearly as long.
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <climits>
@@ -41,6 +40,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "launch_host.h"
 #include "mx_device.cuh"
 #include "mx_internal.h"
 #include "mxfp8moe.h"
@@ -77,7 +77,6 @@ constexpr int64_t CE_DZ_LEAST = int64_t(1) << 25, CE_DZ_MOST = int64_t(1) << 27,
 // vocabulary has several pieces, dx once at the least.
 constexpr int64_t CE_PARTS_LEAST = int64_t(1) << 23, CE_PARTS_MOST = int64_t(1) << 24;
 constexpr int64_t CE_MIN_PIECE = 2048;             // vocabulary entries of a piece, whatever the rows
-constexpr uint64_t CE_WAIT_NS = 2000000000ull;     // 2 s per individual wait
 constexpr float LOG2E = 1.4426950408889634f;
 
 enum { CE_LSE = 0, CE_DZ = 1, CE_DW = 2, CE_DX = 3 };
@@ -492,7 +491,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
       if (leader && lane == 0)
         for (int s = 0; s < STAGES; ++s)
           if (((prod_issued >> s) & 1u) &&
-              !mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS)) {
+              !mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, kWaitTimeoutNs)) {
             ce_report(p, ERR_TIMEOUT_DRAIN);
             break;
           }
@@ -539,7 +538,7 @@ __global__ void __launch_bounds__(CE_THREADS, STAGES == CE_SHORT ? 2 : 1)
       if (issued && ce_elect()) {
         if constexpr (CG == 2) tc_commit_pair_local(drained);
         else tc_commit(drained);
-        if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
+        if (!mbar_wait_bounded(drained, 0, nullptr, kWaitTimeoutNs)) ce_report(p, ERR_TIMEOUT_DRAIN);
       }
       __syncwarp();
     } else if (MODE == CE_DZ && warp >= 2 && p.xp != nullptr) {
@@ -947,7 +946,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
       }
       for (int s = 0; s < S::STAGES; ++s)           // copies land before the CTA exits
         if ((issued >> s) & 1u)
-          if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, CE_WAIT_NS))
+          if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, kWaitTimeoutNs))
             ce_report(p, ERR_TIMEOUT_DRAIN);
     }
     __syncwarp();
@@ -986,7 +985,7 @@ __global__ void __launch_bounds__(FewShape<MODE, NT>::THREADS, FewShape<MODE, NT
     }
     if (issued && ce_elect()) {
       tc_commit(drained);
-      if (!mbar_wait_bounded(drained, 0, nullptr, CE_WAIT_NS)) ce_report(p, ERR_TIMEOUT_DRAIN);
+      if (!mbar_wait_bounded(drained, 0, nullptr, kWaitTimeoutNs)) ce_report(p, ERR_TIMEOUT_DRAIN);
     }
     __syncwarp();
   } else {
@@ -1386,21 +1385,9 @@ __global__ void __launch_bounds__(256) k_ce_dw(const CeParams p, uint16_t* dw) {
 
 // ---- host side -------------------------------------------------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 ce_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* q = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) == cudaSuccess &&
-        r == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(q);
-  });
-  return fn;
-}
 // bf16 [rows, cols] with `pitch` elements per row, boxes of box_cols x box_rows.
 bool ce_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch, int box_cols, int box_rows) {
-  auto enc = ce_encoder();
+  auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
@@ -1549,14 +1536,6 @@ int group_of(int64_t row_bytes, bool pair, int64_t most) {
   return static_cast<int>(std::max<int64_t>(1, std::min(g, most)));
 }
 
-uint64_t ce_wait_ns() {
-  const char* v = getenv("MXFP8MOE_WAIT_LIMIT_NS");
-  if (v == nullptr || *v == 0) return CE_WAIT_NS;
-  char* end = nullptr;
-  const unsigned long long n = strtoull(v, &end, 10);
-  return (end != nullptr && *end == 0 && n > 0) ? static_cast<uint64_t>(n) : CE_WAIT_NS;
-}
-
 bool ce_sizes_ok(int64_t T, int64_t H, int64_t V) { return T >= 0 && H > 0 && V > 0; }
 bool ce_sizes_supported(int64_t T, int64_t H, int64_t V) {
   return H % 8 == 0 && T <= (int64_t(1) << 24) && H <= (int64_t(1) << 20) && V <= (int64_t(1) << 28) &&
@@ -1679,7 +1658,7 @@ int linear_cross_entropy_fwd(const void* x, const void* w, const void* targets, 
   p.part = reinterpret_cast<float2*>(base + ws.part);
   p.zy = reinterpret_cast<float*>(base + ws.zy);
   p.pitch = ws.pitch;
-  p.timeout_ns = ce_wait_ns();
+  p.timeout_ns = pipeline_wait_ns();
   CUtensorMap a, b;
   if (!ce_kmajor(&a, x, T, H, H, few ? few_rows(T) : CE_HALF) || !ce_kmajor(&b, w, V, H, H)) return MXFP8_ERR_CUDA;
   int ctas = 0;
@@ -1741,7 +1720,7 @@ int linear_cross_entropy_bwd(const float* dloss, const float* dlse, const void* 
   p.acc_w = ws.dw_splits > 1 ? reinterpret_cast<float*>(base + ws.acc_w) : nullptr;
   p.dw_splits = ws.dw_splits;
   p.dx = static_cast<uint16_t*>(dx);
-  p.timeout_ns = ce_wait_ns();
+  p.timeout_ns = pipeline_wait_ns();
   const bool dx_pair = !ws.few && use_pair(dev, T, H, ws.splits);
   p.piece_steps = static_cast<int>(up(ws.piece, CE_BK));
   p.splits = ws.splits;

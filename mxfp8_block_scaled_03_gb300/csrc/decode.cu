@@ -50,13 +50,13 @@
 //   linear 1x4096->4096              MXFP8  8.5 us, NVFP4 7.5: launch, columns, first weights, parts, in a row
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cstdlib>
 
+#include "launch_host.h"
 #include "mx_device.cuh"
 #include "mx_internal.h"
 #include "mxfp8moe.h"
@@ -1116,33 +1116,14 @@ __global__ void __launch_bounds__(256) k_sum_rows(const float* y, const int* row
 
 // ---- host side -------------------------------------------------------------------------------
 
-constexpr uint64_t kDecWaitNs = 2000000000ull;   // 2 s per wait; teardown waits always keep it
-
-// Limit of every pipeline wait: kDecWaitNs, or MXFP8MOE_WAIT_LIMIT_NS as for the grouped GEMMs.
-uint64_t dec_wait_ns() {
-  const char* v = getenv("MXFP8MOE_WAIT_LIMIT_NS");
-  if (v == nullptr || *v == 0) return kDecWaitNs;
-  char* end = nullptr;
-  const unsigned long long n = strtoull(v, &end, 10);
-  return (end != nullptr && *end == 0 && n > 0) ? static_cast<uint64_t>(n) : kDecWaitNs;
-}
-
 // 2-D byte matrix [rows, cols] (row pitch = cols) in boxes of box_rows rows x 128 bytes, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  static std::atomic<void*> entry{nullptr};
-  void* fn = entry.load(std::memory_order_acquire);
-  if (fn == nullptr) {
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || fn == nullptr)
-      return false;
-    entry.store(fn, std::memory_order_release);
-  }
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols};
   const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
-  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
-             m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1372,8 +1353,8 @@ int moe_decode(const void* x, int64_t T, int64_t H, int64_t F, int E, int k, con
   up.max_active = ws.max_active;
   up.chunks = 1;
   up.box_rows = group;
-  up.timeout_ns = dec_wait_ns();
-  up.drain_ns = kDecWaitNs;
+  up.timeout_ns = pipeline_wait_ns();
+  up.drain_ns = kWaitTimeoutNs;
   DecParams down = up;
   up.w_sf = w1_sf;
   up.w_amax = w1_amax;
@@ -1467,8 +1448,8 @@ int matvec(const void* x, int64_t T, int64_t K, int64_t N, const uint8_t* w_q, c
   p.steps = static_cast<int>(ws.x.steps);
   p.kt = p.steps * dec_atoms(FMT);
   p.tiles = static_cast<int>(N / 128);
-  p.timeout_ns = dec_wait_ns();
-  p.drain_ns = kDecWaitNs;
+  p.timeout_ns = pipeline_wait_ns();
+  p.drain_ns = kWaitTimeoutNs;
   if (!dec_layout(FMT, DEC_LINEAR, p.per_chunk, 0, 0, false, &p.L)) return MXFP8_ERR_UNSUPPORTED;
   SplitParams q{};
   q.x = static_cast<const uint16_t*>(x);
