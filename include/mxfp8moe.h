@@ -509,7 +509,7 @@ int residual_norm_bwd(const void* dn, const void* dres_out, const void* y, const
  *   dprob_sum  (device) float [E] gradient of prob_sum, or NULL for 0.
  *   dlosses    (device) float [2] gradient of losses, or NULL for 0.
  *   dlogits    (device, out) [T, E] in the logits' type; 0 where the token takes no part.
- * Sums are fp32 in an order that depends on T, E and the device only.  Requirements: T >= 0,
+ * Sums are fp32 in an order that depends on T, E, k and the device only.  Requirements: T >= 0,
  * 1 <= E <= 1024, 1 <= k <= E, T*k < 2^31 (otherwise MXFP8_ERR_INVALID_ARG); k <= 32 (otherwise
  * MXFP8_ERR_UNSUPPORTED); pointers aligned to their elements.  No device-side errors.
  */

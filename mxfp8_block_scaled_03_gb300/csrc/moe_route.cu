@@ -19,7 +19,7 @@
 // experts take two or four warps.  Every lane sorts its logits once, on integer keys that hold the float's order and the
 // expert; each of the k rounds is then a maximum over the lanes' first keys.  The column sums stay in registers (a lane
 // sees the same experts of every token) and are joined in a fixed order, so that results do not depend on timing: in the
-// CTA where one is enough, over a cluster of 16 up to 64 passes, and by a second kernel, a cluster of eight, beyond.
+// CTA where one is enough, over a cluster of 16 up to 32 or 64 passes, and by a second kernel, a cluster of eight, beyond.
 //
 // Measured (replayed; 32768 tokens, 64 experts, 8 choices, bf16): forward 13 us, 10 and 6 for the two kernels alone;
 // backward 7.6 us.  16384 tokens, 8 experts, 2 choices, fp32: 7.3 and 3.4 us.  4 tokens, 128 experts: 4.0 us.  As calls
@@ -700,17 +700,27 @@ int groups_of(int E) {
   return with_shape(E, [](auto l, auto v) { return RouteShape<decltype(l)::value, decltype(v)::value>::GROUPS; });
 }
 
-// One CTA up to two passes (a token per group each), a cluster of 16 up to 64 passes; beyond, as many CTAs as give all of
-// them equal passes, and a second kernel for their sums.
-constexpr int RT_CLUSTER_PASSES = 4 * RT_CLUSTER;
+// One CTA up to two passes (a token per group each); then a cluster of 16, which leaves most of the GPU idle but needs no
+// second kernel; then as many CTAs as give all of them equal passes, and a second kernel for their sums.  The second launch
+// costs the call from Python 2.4 to 4.5 us; the cluster's passes cost the GPU more and more.  Replayed, us, the cluster and the
+// second kernel, by passes:
+//                  16            32            48            64
+//   E 8, k 2     4.1  5.7      5.3  5.9      5.8  5.6      6.6  5.7
+//   E 8, k 8     5.3  6.6      7.0  6.7      9.2  6.9     10.9  6.7
+//   E 64, k 2    5.0  6.0      6.2  6.1      7.4  6.2      8.5  6.0
+//   E 64, k 8    5.3  6.4      7.2  6.6      8.7  6.5     10.5  6.6
+//   E 256, k 8   5.8  6.8      8.0  7.2      9.8  7.4     11.8  7.6
+// So 32 passes, where the cluster costs a replay at most a third of what it saves the call, and 64 for tokens whose passes
+// are short: up to eight experts and two rounds.
+int cluster_passes(int E, int k) { return (E <= 8 && k <= 2 ? 4 : 2) * RT_CLUSTER; }
 struct FwdGrid {
   int ctas;
   bool cluster;
 };
-FwdGrid fwd_grid(int64_t T, int E, bool clusters) {
+FwdGrid fwd_grid(int64_t T, int E, int k, bool clusters) {
   const int64_t passes = (T + groups_of(E) - 1) / groups_of(E);
   if (passes <= 2) return {1, false};
-  if (clusters && passes <= RT_CLUSTER_PASSES) return {RT_CLUSTER, true};
+  if (clusters && passes <= cluster_passes(E, k)) return {RT_CLUSTER, true};
   const int64_t most = RT_MAX_CTAS;
   const int64_t per = (passes + most - 1) / most;
   return {static_cast<int>((passes + per - 1) / per), false};
@@ -777,9 +787,9 @@ int launch_route(const RouteParams& p, unsigned grid, cudaStream_t st) {
       } else {
         constexpr auto kernel = k_route_fwd<S, L, V, MANY>;
         const size_t smem = (R::ROWS + 1) * static_cast<size_t>(p.E) * 4;
-        FwdGrid g = fwd_grid(p.T, p.E, true);
+        FwdGrid g = fwd_grid(p.T, p.E, p.k, true);
         if (g.cluster && !clusters_run<kernel>((R::ROWS + 1) * static_cast<size_t>(L * V) * 4, R::THREADS))
-          g = fwd_grid(p.T, p.E, false);
+          g = fwd_grid(p.T, p.E, p.k, false);
         if (g.cluster) {
           q.cluster = 1;
           cudaLaunchAttribute attr[1];
@@ -807,7 +817,7 @@ extern "C" {
 
 size_t moe_route_workspace_size(int64_t T, int E, int k) {
   if (!sizes_ok(T, E, k, MOE_LOGITS_F32) || k > RT_MAX_K) return 0;
-  return static_cast<size_t>(fwd_grid(T, E, false).ctas) * (E + 1) * sizeof(float2);
+  return static_cast<size_t>(fwd_grid(T, E, k, false).ctas) * (E + 1) * sizeof(float2);
 }
 
 int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k, const uint8_t* token_mask,
@@ -823,7 +833,7 @@ int moe_route_fwd(const void* logits, int logits_dtype, int64_t T, int E, int k,
   for (const void* q : {static_cast<const void*>(counts), static_cast<const void*>(prob_sum),
                         static_cast<const void*>(losses)})
     if (q == nullptr || !aligned4(q)) return MXFP8_ERR_INVALID_ARG;
-  if (fwd_grid(T, E, false).ctas > 1) {
+  if (fwd_grid(T, E, k, false).ctas > 1) {
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return MXFP8_ERR_INVALID_ARG;
     if (workspace_bytes < moe_route_workspace_size(T, E, k)) return MXFP8_ERR_WORKSPACE;
   }
