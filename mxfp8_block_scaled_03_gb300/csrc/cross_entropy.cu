@@ -15,20 +15,20 @@
 //   CE_DZ   x w^T      -> dz of one piece of the vocabulary, bf16, in the workspace
 //   CE_DW   dz^T x     -> dw of the piece            (both operands contract over their rows: M- and N-major tiles)
 //   CE_DX   dz w       -> dx, in fp32 parts where the vocabulary has several pieces or is split over CTAs
-// The backward first packs the rows that take part, so that padding costs nothing and nothing it holds can reach
-// dw (0 * NaN); where that takes longer than it could save, dz's kernel writes zeros for the other rows instead, to dz and to
-// a copy of x (rows as they are).  dz is rounded to bf16 (by at most 2^-8 of its value): it is the operand of two products
+// The forward computes every row, since lse is written for all.  The backward first packs the rows that take part, so that
+// padding costs its products nothing and nothing it holds can reach dw (0 * NaN); for fewer rows dz's kernel writes zeros
+// for the others instead, to dz and to a copy of x (rows as they are).  dz is rounded to bf16 (by at most 2^-8 of its value): it is the operand of two products
 // whose results are rounded to bf16 as well.  It lives for one piece of the vocabulary only, at most half of a large one.
 // Few rows have a kernel of their own, k_ce_few, which is bound by the bytes of w: CE_LSE up to CE_FEW_FWD rows, CE_DZ and
 // CE_DX up to CE_FEW.  dw is k_ce_gemm's for any number of rows.
 //
-// Measured (replayed, GB300; rows x H x vocabulary):
-//   forward   8192 x 4096 x 32000   1.08-1.19 ms = 1.80-2.00 PFLOP/s (under sustained power and cool; cuBLAS in bf16 1.72-1.88)
+// Measured (GB300; rows x H x vocabulary):
+//   forward   8192 x 4096 x 32000   1.03-1.21 ms = 1.78-2.09 PFLOP/s (cool and under sustained power; cuBLAS in bf16 1.72-1.88)
 //             1 x 4096 x 32000      47 us = 5.6 TB/s
-//   backward  8192 x 4096 x 32000   3.31-3.79 ms = 1.70-1.95 PFLOP/s (6 T H V operations)
-//             1531 x 2048 x 50257, 30% padding: 427 us = 1.55 PFLOP/s (1072 rows fill five tiles of 256)
+//   backward  8192 x 4096 x 32000   3.31-3.86 ms = 1.67-1.95 PFLOP/s (6 T H V operations)
+//             1531 x 2048 x 50257, 30% padding: 461 us = 1.44 PFLOP/s (1072 rows fill five tiles of 256; two pieces)
 //             5 x 1024 x 32000      42 us; reads w twice and writes dw, 197 MB: 4.7 TB/s
-// The tensor pipe is active 86-88% of the time in the logits' and dw's products and 76% in dx's (2048 x 4096 x 16384, 512 and
+// The tensor pipe is active 85-88% of the time in the logits' and dw's products and 76% in dx's (2048 x 4096 x 16384, 512 and
 // 128 tiles for 76 pairs).  Loops of one lane instead of whole warps around the copies and the products left it at 78%: a
 // step's 512 cycles of products took the issuing lane nearly as long.
 #include <cuda_runtime.h>
@@ -1206,8 +1206,8 @@ __global__ void __launch_bounds__(CE_MERGE_THREADS) k_ce_merge(const CeParams p,
   }
 }
 
-// Shares of the vocabulary in dx, from the rows that take part: as many of those whose parts there is room for as deal the K steps out evenly to `workers` CTAs
-// (or pairs).  Counted in K steps (about 0.27 us): a share's start and end, and its part of dx, written and read back
+// Shares of the vocabulary in dx, from the rows that take part: of the numbers whose parts there is room for, the one that
+// deals the K steps out best to `workers` CTAs (or pairs).  Counted in K steps (about 0.27 us): a share's start and end, and its part of dx, written and read back
 // (1072 x 2048 values in 15 parts took 48 us to add up; 3 parts leave 10, and the product 10 us longer).
 constexpr int CE_SHARE_STEPS = 8;
 constexpr float CE_PART_STEPS = 4.4e-6f;   // per value of dx: 8 bytes at 6.8 TB/s

@@ -22,8 +22,8 @@
 // CTA where one is enough, over a cluster of 16 up to 32 or 64 passes, and by a second kernel, a cluster of eight, beyond.
 //
 // Measured (replayed; 32768 tokens, 64 experts, 8 choices, bf16): forward 13 us, 10 and 6 for the two kernels alone;
-// backward 7.6 us.  16384 tokens, 8 experts, 2 choices, fp32: 7.3 and 3.4 us.  4 tokens, 128 experts: 4.0 us.  As calls
-// from Python, on this machine's cores, 22 to 26 and 14 to 15 us: the allocation of the six outputs and the launches.
+// backward 7.6 us.  16384 tokens, 8 experts, 2 choices, fp32: 6.9 and 3.4 us.  4 tokens, 128 experts: 4.0 us.  As calls
+// from Python, on this machine's cores, 20 to 26 and 13 to 16 us: the allocation of the six outputs and the launches.
 // With one warp per token, two logits per lane and selection by 32-lane reductions: 28 us forward; 10.2 us backward.
 #include <cuda_runtime.h>
 
@@ -702,8 +702,8 @@ int groups_of(int E) {
 
 // One CTA up to two passes (a token per group each); then a cluster of 16, which leaves most of the GPU idle but needs no
 // second kernel; then as many CTAs as give all of them equal passes, and a second kernel for their sums.  The second launch
-// costs the call from Python 2.4 to 4.5 us; the cluster's passes cost the GPU more and more.  Replayed, us, the cluster and the
-// second kernel, by passes:
+// costs the call from Python 2.4 to 4.5 us; the cluster's passes cost the GPU more and more.  Replayed, us, the cluster and
+// the second kernel, by passes:
 //                  16            32            48            64
 //   E 8, k 2     4.1  5.7      5.3  5.9      5.8  5.6      6.6  5.7
 //   E 8, k 8     5.3  6.6      7.0  6.7      9.2  6.9     10.9  6.7
